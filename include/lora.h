@@ -82,7 +82,12 @@ enum { LORA_F32 = 0, LORA_BF16 = 1 };
 enum {
     LORA_DEV_BAD_ADAPTER = 1,    /* an id >= max_adapters, or an unloaded adapter */
     LORA_DEV_BAD_SEGMENTS = 2,   /* a segment table that breaks the rules above */
-    LORA_DEV_WAIT_TIMEOUT = 4    /* a pipeline wait inside a kernel gave up */
+    LORA_DEV_WAIT_TIMEOUT = 4,   /* a pipeline wait inside a kernel gave up */
+    /* decode-step operators (lora_kv_pages.status): */
+    LORA_DEV_BAD_SLOT = 8,       /* an append slot beyond the cache (the token is not stored) */
+    LORA_DEV_BAD_POSITION = 16,  /* a rotation position outside the table (clamped) */
+    LORA_DEV_BAD_LENGTH = 32,    /* a cached length below the drafted count or beyond the page table (clamped) */
+    LORA_DEV_BAD_PAGE = 64       /* a page id outside the cache (clamped) */
 };
 
 /*
@@ -303,6 +308,111 @@ size_t lora_layer_forward_fp8_workspace_size(const lora_pool *pool, int matrix, 
 int lora_layer_forward_fp8(lora_pool *pool, int matrix, const void *x, const void *W8, float w_scale, void *y,
                            const int *seg_starts, const int *seg_adapter, int S, int T,
                            void *workspace, size_t ws_bytes, lora_stream stream);
+
+/*
+ * Decode step of an attention block: the operators around the adapted
+ * projections when every request adds one token, or a few drafted ones.
+ *
+ *   lora_w4_matvec        base product of a projection from 4-bit weights
+ *                         (lora_bgmv then adds each token's adapter term)
+ *   lora_kv_append        norm and rotation of queries and keys, append of
+ *                         keys and values to a paged cache
+ *   lora_tree_attention   attention of the drafted tokens over that cache
+ *
+ * They take no pool: element types are arguments (LORA_F32 or LORA_BF16) and
+ * all memory is the caller's.  Arithmetic is fp32 (products of bf16 operands
+ * are exact in it); outputs are rounded once on store.
+ */
+
+/*
+ * Matrix products with 4-bit weights:
+ *   y[t][n] = sum_k x[t][k] * scales[n][k / group] * (code(n, k) - zero(n, k / group))
+ * y (T x h_out) is OVERWRITTEN; x is T x h_in; both of type dtype, row-major, dense.
+ *   codes   h_out x h_in/2 bytes: element k of row n is the low half of byte
+ *           k/2 when k is even, the high half when it is odd; 0..15.
+ *   scales  h_out x h_in/group, bf16.
+ *   zeros   h_out x h_in/group bytes (0..15), or NULL: 8 everywhere.
+ *   group   32, 64 or 128; h_in is a multiple of it.  h_out is any size.
+ * Meant for the few tokens of a decode step: the weights are read once for
+ * every 64 tokens.
+ * Errors: LORA_ERR_ARG, LORA_ERR_SHAPE (group, or h_in no multiple of it).
+ */
+int lora_w4_matvec(int dtype, const void *x, int T, int h_in, const void *codes, const void *scales,
+                   const void *zeros, int group, int h_out, void *y, lora_stream stream);
+
+/*
+ * One layer's paged key/value cache, in caller-owned device memory.
+ *   k, v    n_pages x n_kv_heads x page_size x head_dim elements of dtype, 16-byte
+ *           aligned.  A cache slot is page * page_size + offset in the page.
+ *   page_size  a power of two, 1..1024.   head_dim  a multiple of 8, 8..256.
+ *   status  one device int32 that collects LORA_DEV_* bits of the calls on
+ *           this cache (never cleared by them), or NULL.
+ * The struct is read during the call only.
+ */
+typedef struct lora_kv_pages {
+    int dtype, n_pages, page_size, n_kv_heads, head_dim;
+    void *k, *v;
+    int *status;
+} lora_kv_pages;
+
+/*
+ * Norm, rotation and append, for T new tokens of any requests:
+ *   per query head and key head h of token t, r = 1 / sqrt(mean_i h[i]^2 + eps):
+ *     h[i] <- h[i] * r * norm[i]                 (q_norm for queries, k_norm for keys; NULL: no norm)
+ *     (a, b) <- (a c_i - b s_i, a s_i + b c_i)   over the rot_dim/2 pairs i,
+ *   where (a, b) are elements i and i + rot_dim/2, or 2i and 2i+1 when
+ *   interleaved is non-zero, and c_i, s_i are entries i and rot_dim/2 + i of
+ *   row positions[t] of cos_sin; elements from rot_dim on are not rotated.
+ *   q_out[t] gets the queries; slot slots[t] of the cache gets the keys (as
+ *   above) and the values (as they are).  slots[t] < 0: not stored.
+ *   q, k, v    T rows of n_q_heads (n_kv_heads) x head_dim elements, ld_* elements
+ *              apart (a column range of one fused projection is fine); 16-byte
+ *              aligned, ld_* a multiple of 16 bytes.  q may be NULL with
+ *              n_q_heads 0 (nothing but the append).
+ *   cos_sin    n_pos x rot_dim fp32; rot_dim even, 0..head_dim (0: no
+ *              rotation; cos_sin and positions may then be NULL).
+ *   q_out      T x n_q_heads x head_dim, dense; may be q itself when q is dense.
+ *   q_norm, k_norm   head_dim elements, 16-byte aligned.
+ * Two tokens with one slot in one call leave either's values in it.
+ * Errors: LORA_ERR_ARG, LORA_ERR_SHAPE (head counts, head_dim, page_size, rot_dim, ld_*).
+ * Device-detected: LORA_DEV_BAD_SLOT, LORA_DEV_BAD_POSITION.
+ */
+int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, const void *k, int ld_k, const void *v, int ld_v,
+                   int T, int n_q_heads, const int *positions, const long long *slots, const float *cos_sin,
+                   int n_pos, int rot_dim, int interleaved, const void *q_norm, const void *k_norm, float eps,
+                   void *q_out, lora_stream stream);
+
+/* Bytes of device workspace lora_tree_attention needs for T drafted tokens of
+ * S requests (0 on a bad argument). */
+size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T);
+
+/*
+ * Attention of drafted tokens over the paged cache.  Request s has the tokens
+ * seg_starts[s] .. seg_starts[s+1]-1 (n_s of them, n_s >= 0) and kv_lens[s]
+ * cached tokens, the last n_s of which are its drafted ones, in order (append
+ * them first).  Cached token c of request s is at offset c % page_size of page
+ * page_table[s * max_pages + c / page_size].
+ *   out[t][h] = sum_c p_c v_c,   p = softmax over the visible c of scale * q[t][h] . k_c,
+ * k and v of kv head h / (n_q_heads / n_kv_heads).  Visible to drafted token i
+ * of a request: every c < kv_lens[s] - n_s; and drafted token j (c = kv_lens[s]
+ * - n_s + j) when bit j % 64 of word j / 64 of row t of tree_mask is set
+ * (mask_words words a row; j beyond them is not visible), or, with tree_mask
+ * NULL, when j <= i.  With n_s = 1 and no mask this is plain decoding.  A token
+ * that sees nothing gets zeros.  What a masked or unused slot holds (NaN
+ * included) reaches no output.
+ *   q, out     T x n_q_heads x head_dim of the cache's dtype, dense, 16-byte aligned;
+ *              out may be q.
+ *   workspace  lora_tree_attention_workspace_size() bytes, contents undefined
+ *              on entry and exit.
+ * Softmax statistics and sums are fp32; for a bf16 cache the probabilities
+ * enter the second product as bf16.
+ * Errors: LORA_ERR_ARG (includes ws_bytes too small), LORA_ERR_SHAPE.
+ * Device-detected: LORA_DEV_BAD_SEGMENTS, LORA_DEV_BAD_LENGTH,
+ * LORA_DEV_BAD_PAGE, LORA_DEV_WAIT_TIMEOUT; no access leaves the arrays.
+ */
+int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, const int *seg_starts, int S, int T,
+                        const int *kv_lens, const int *page_table, int max_pages, const long long *tree_mask,
+                        int mask_words, float scale, void *out, void *workspace, size_t ws_bytes, lora_stream stream);
 
 /*
  * Synchronise the device, read the pool's device status word into

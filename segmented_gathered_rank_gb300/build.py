@@ -1,7 +1,7 @@
 """Build the CUDA library in-tree for sm_103a.
 
 ``python -m segmented_gathered_rank_gb300.build`` compiles every ``csrc/*.cu``
-with nvcc (one ``-gencode arch=compute_103a,code=sm_103a``, in parallel) and
+and ``csrc/decode/*.cu`` with nvcc (one ``-gencode arch=compute_103a,code=sm_103a``, in parallel) and
 links ``liblora_gb300.so`` next to this file.  The CUDA runtime is linked
 statically, so the library loads on a machine without a GPU (calls that need
 one then return LORA_ERR_CUDA).
@@ -35,11 +35,12 @@ def _nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "decode", "*.cu")))
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "decode", "*.cuh")) +
+            glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def up_to_date() -> bool:

@@ -1,0 +1,42 @@
+// Shared by the decode-step operators: host-side checks of the paged cache and
+// the device view of one request's cached tokens.
+#pragma once
+
+#include "internal.cuh"
+
+namespace lora {
+namespace decode {
+
+constexpr int kMaxHeadDim = 256;
+constexpr int kMaxPageSize = 1024;
+
+// Host checks shared by the calls on a paged cache.
+inline int check_kv(const lora_kv_pages *kv, int n_q_heads) {
+    if (!kv || !kv->k || !kv->v || (kv->dtype != LORA_F32 && kv->dtype != LORA_BF16)) return LORA_ERR_ARG;
+    if (!aligned16(kv->k) || !aligned16(kv->v) || ((uintptr_t)kv->status & 3u)) return LORA_ERR_ARG;
+    if (kv->n_pages < 1 || kv->n_kv_heads < 1 || n_q_heads < 0) return LORA_ERR_ARG;
+    if (kv->page_size < 1 || kv->page_size > kMaxPageSize || (kv->page_size & (kv->page_size - 1))) return LORA_ERR_SHAPE;
+    if (kv->head_dim < 8 || kv->head_dim > kMaxHeadDim || kv->head_dim % 8) return LORA_ERR_SHAPE;
+    if (n_q_heads % kv->n_kv_heads) return LORA_ERR_SHAPE;
+    return LORA_OK;
+}
+
+inline int log2_of(int power_of_two) {
+    int n = 0;
+    while ((1 << n) < power_of_two) ++n;
+    return n;
+}
+
+__device__ __forceinline__ void flag_status(int *status, int bits) {
+    if (status) atomicOr(status, bits);
+}
+
+// Checks a device segment table (every thread of the block calls it).
+__device__ __forceinline__ void check_starts(const int *starts, int S, int T, int *status) {
+    bool bad = threadIdx.x == 0 && (starts[0] != 0 || starts[S] != T);
+    for (int s = threadIdx.x; s < S; s += blockDim.x) bad |= starts[s + 1] < starts[s];
+    if (__syncthreads_or(bad) && threadIdx.x == 0) flag_status(status, LORA_DEV_BAD_SEGMENTS);
+}
+
+}  // namespace decode
+}  // namespace lora

@@ -31,6 +31,10 @@ LORA_BF16 = 1
 LORA_DEV_BAD_ADAPTER = 1
 LORA_DEV_BAD_SEGMENTS = 2
 LORA_DEV_WAIT_TIMEOUT = 4
+LORA_DEV_BAD_SLOT = 8
+LORA_DEV_BAD_POSITION = 16
+LORA_DEV_BAD_LENGTH = 32
+LORA_DEV_BAD_PAGE = 64
 
 LORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -44,7 +48,8 @@ EXPORTS = ["lora_pool_create", "lora_pool_destroy", "lora_pool_load", "lora_pool
            "lora_launch_count", "lora_layer_forward_noalloc", "lora_tier_cache_create", "lora_tier_cache_destroy",
            "lora_tier_cache_touch", "lora_tier_cache_resident", "lora_tier_sim", "lora_pool_load_async",
            "lora_pool_unload_async", "lora_pool_prefetch", "lora_quantize_e4m3",
-           "lora_layer_forward_fp8_workspace_size", "lora_layer_forward_fp8"]
+           "lora_layer_forward_fp8_workspace_size", "lora_layer_forward_fp8", "lora_w4_matvec", "lora_kv_append",
+           "lora_tree_attention_workspace_size", "lora_tree_attention"]
 
 if not os.path.exists(_build.LIB):
     raise ImportError(f"CUDA library {_build.LIB} is not built: run segmented_gathered_rank_gb300.build.build()")
@@ -98,6 +103,31 @@ _sig("lora_tier_cache_resident", _I, _P, _I)
 _sig("lora_tier_sim", _I, _P, ctypes.c_longlong, _I, _I, _I, ctypes.POINTER(ctypes.c_longlong))
 
 
+class KvPages(ctypes.Structure):
+    """``lora_kv_pages``: one layer's paged key/value cache in two CUDA tensors
+    of shape [n_pages, n_kv_heads, page_size, head_dim] (kept alive by this
+    object), with an optional int32 status tensor."""
+    _fields_ = [("dtype", _I), ("n_pages", _I), ("page_size", _I), ("n_kv_heads", _I), ("head_dim", _I), ("k", _P),
+                ("v", _P), ("status", _P)]
+
+    def __init__(self, dtype, k_pages, v_pages, n_pages, page_size, n_kv_heads, head_dim, status=None):
+        for t in (k_pages, v_pages):
+            if t.numel() != n_pages * n_kv_heads * page_size * head_dim:
+                raise ValueError("a cache tensor does not hold n_pages x n_kv_heads x page_size x head_dim elements")
+        super().__init__(dtype, n_pages, page_size, n_kv_heads, head_dim, _dptr(k_pages), _dptr(v_pages),
+                         _dptr(status))
+        self.tensors = (k_pages, v_pages, status)
+        self.ref = ctypes.byref(self)
+
+
+_sig("lora_w4_matvec", _I, _I, _P, _I, _I, _P, _P, _P, _I, _I, _P, _P)
+_sig("lora_kv_append", _I, ctypes.POINTER(KvPages), _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P,
+     ctypes.c_float, _P, _P)
+_sig("lora_tree_attention_workspace_size", ctypes.c_size_t, ctypes.POINTER(KvPages), _I, _I, _I)
+_sig("lora_tree_attention", _I, ctypes.POINTER(KvPages), _P, _I, _P, _I, _I, _P, _P, _I, _P, _I, ctypes.c_float, _P, _P,
+     ctypes.c_size_t, _P)
+
+
 class LoraError(RuntimeError):
     def __init__(self, status: int, where: str, device_status: int = 0):
         self.status = status
@@ -120,6 +150,24 @@ def _dptr(t):
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError("expected a contiguous CUDA tensor")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _ptr(t):
+    """_dptr as a plain integer (cheaper to pass; decode calls are short)."""
+    if t is None:
+        return None
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("expected a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _rows(t):
+    """(pointer, elements between rows) of a CUDA matrix whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("expected a CUDA matrix with contiguous rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _hptr(a):
@@ -299,3 +347,38 @@ def lora_layer_forward_fp8(pool, matrix, x, W8, w_scale, y, seg_starts, seg_adap
     _check(_lib.lora_layer_forward_fp8(pool, matrix, _dptr(x), _dptr(W8), float(w_scale), _dptr(y),
                                        _dptr(seg_starts), _dptr(seg_adapter), S, T, _dptr(workspace), ws_bytes,
                                        _stream(stream)), "lora_layer_forward_fp8")
+
+
+def lora_w4_matvec(dtype, x, T, h_in, codes, scales, zeros, group, h_out, y, stream=None) -> None:
+    """Products with 4-bit weights (uint8 codes, bf16 scales, uint8 zeros or None); y is overwritten."""
+    rc = _lib.lora_w4_matvec(dtype, _ptr(x), T, h_in, _ptr(codes), _ptr(scales), _ptr(zeros), group, h_out, _ptr(y),
+                             _stream(stream))
+    if rc:
+        _check(rc, "lora_w4_matvec")
+
+
+def lora_kv_append(kv, q, k, v, T, n_q_heads, positions, slots, cos_sin, n_pos, rot_dim, interleaved, q_out,
+                   q_norm=None, k_norm=None, eps=1e-6, stream=None) -> None:
+    """Norm, rotation and append of T tokens; q, k and v are matrices of T rows (any row stride), slots int64."""
+    (pq, ld_q), (pk, ld_k), (pv, ld_v) = _rows(q), _rows(k), _rows(v)
+    rc = _lib.lora_kv_append(kv.ref, pq, ld_q, pk, ld_k, pv, ld_v, T, n_q_heads, _ptr(positions), _ptr(slots),
+                             _ptr(cos_sin), n_pos, rot_dim, 1 if interleaved else 0, _ptr(q_norm), _ptr(k_norm), eps,
+                             _ptr(q_out), _stream(stream))
+    if rc:
+        _check(rc, "lora_kv_append")
+
+
+def lora_tree_attention_workspace_size(kv, n_q_heads, S, T) -> int:
+    return int(_lib.lora_tree_attention_workspace_size(kv.ref, n_q_heads, S, T))
+
+
+def lora_tree_attention(kv, q, n_q_heads, seg_starts, S, T, kv_lens, page_table, max_pages, tree_mask, mask_words, scale,
+                        out, workspace, ws_bytes=None, stream=None) -> None:
+    """Attention of drafted tokens over the cache; tree_mask is int64 [T, mask_words], or None for causal chains."""
+    if ws_bytes is None:
+        ws_bytes = workspace.nbytes
+    rc = _lib.lora_tree_attention(kv.ref, _ptr(q), n_q_heads, _ptr(seg_starts), S, T, _ptr(kv_lens), _ptr(page_table),
+                                  max_pages, _ptr(tree_mask), mask_words, scale, _ptr(out), _ptr(workspace), ws_bytes,
+                                  _stream(stream))
+    if rc:
+        _check(rc, "lora_tree_attention")
