@@ -402,6 +402,7 @@ size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, int n_q_heads
  * included) reaches no output.
  *   q, out     T x n_q_heads x head_dim of the cache's dtype, dense, 16-byte aligned;
  *              out may be q.
+ *   scale      greater than 0.
  *   workspace  lora_tree_attention_workspace_size() bytes, contents undefined
  *              on entry and exit.
  * Softmax statistics and sums are fp32; for a bf16 cache the probabilities

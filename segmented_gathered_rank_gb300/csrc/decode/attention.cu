@@ -1,83 +1,645 @@
 // Attention of drafted tokens over a paged cache (lora_tree_attention).
 //
 // For drafted token i of a request with prefix P = kv_len - n:
-//   o = sum_c p_c v_c / sum_c p_c,  p_c = exp(scale q . k_c - m),  m the running maximum,
+//   o = sum_c p_c v_c / sum_c p_c,  p_c = 2^(scale log2(e) q . k_c - m),  m the running maximum,
 // over the visible c: every c < P, and drafted j (c = P + j) that the token's
-// mask row names (or j <= i without a mask).
-#include "decode.cuh"
+// mask row names (or j <= i without a mask).  K and V are read once, which is
+// the bound while few query rows share them (2 flops a byte and row).
+//
+// attention_mma_kernel (bf16): warp MMAs on units of 16 or 32 rows.
+// attention_simt_kernel (fp32): the same list, fp32 multiply-adds.
+// attention_join_kernel: joins the units that were cut between blocks.
+#include "attention.cuh"
 
 namespace lora {
 namespace {
 
 using namespace decode;
 
-struct AttnParams {
-    const void *q;
-    const void *k, *v;
-    int n_q, n_kv, d, page_shift, n_pages;
-    const int *starts, *lens, *table;
-    int S, T, max_pages;
-    const long long *mask;
-    int words;
-    float scale;
-    void *out;
-    int *status;
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool real) {
+    const int bytes = real ? 16 : 0;        // 0: the 16 bytes become zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+constexpr int kThreads = 128;
+constexpr int kStages = 3;
+
+// D: head width padded to 64, 128 or 256; MT: 16-row tiles a unit.
+template <int D, int MT>
+struct MmaShape {
+    static constexpr int kTile = D == 64 ? 128 : 64;       // cached tokens a stage
+    static constexpr int kWarpKeys = kTile / 4;
+    static constexpr int kRowBytes = D * 2;
+    static constexpr int kHalf = kTile * kRowBytes;        // K, then V
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kLanes = D / 8;                   // threads that copy one row
+    static constexpr int kRowsPerPass = kThreads / kLanes;
+    static constexpr int kPasses = kTile / kRowsPerPass;
+    static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
 };
 
-// One warp per (token, query head); each lane holds 8 elements of the head.
-template <typename E>
-__global__ void __launch_bounds__(128) attention_rows_kernel(const AttnParams p) {
-    const int lane = threadIdx.x & 31, at = lane * 8;
-    const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (blockIdx.x == 0) check_starts(p.starts, p.S, p.T, p.status);
-    if (w >= (long long)p.T * p.n_q) return;
-    const int t = (int)(w / p.n_q), h = (int)(w % p.n_q);
-    const int s = segment_of(p.starts, p.S, t);
-    const int begin = p.starts[s], n = p.starts[s + 1] - begin, i = t - begin;
-    int len = p.lens[s], bad = 0;
-    if (i < 0 || i >= n) bad |= LORA_DEV_BAD_SEGMENTS;
-    if (len < n || len > ((long long)p.max_pages << p.page_shift)) {
-        bad |= LORA_DEV_BAD_LENGTH;
-        len = len < n ? n : p.max_pages << p.page_shift;
-    }
-    const int prefix = max(0, len - n);
-    float q[8] = {}, o[8] = {}, m = -INFINITY, l = 0.f;
-    if (at < p.d) load8(static_cast<const E *>(p.q) + w * p.d + at, q);
-    const int page_mask = (1 << p.page_shift) - 1, kv_head = h / (p.n_q / p.n_kv);
-    for (int c = 0; c < len && !(bad & LORA_DEV_BAD_SEGMENTS); ++c) {
-        const int j = c - prefix;
-        if (j >= 0) {
-            if (!p.mask) {
-                if (j > i) break;
-            } else if (j >= 64 * p.words || !((p.mask[(long long)t * p.words + (j >> 6)] >> (j & 63)) & 1)) {
-                continue;
+// Byte offset of 16-byte chunk `chunk` of row `row`: the low three chunk bits
+// are XORed with the row, so that eight rows' chunks lie in different banks.
+template <int D>
+__device__ __forceinline__ uint32_t swz(int row, int chunk) {
+    return (uint32_t)(row * (D * 2) + ((chunk ^ (row & 7)) << 4));
+}
+
+// Four warps; each takes kWarpKeys of a stage's tokens for all rows of the
+// unit, with a maximum, sum and output of its own, joined in shared memory when
+// the block leaves the unit.  Copies run kStages - 1 tiles ahead, across units.
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) attention_mma_kernel(const AttnParams p) {
+    using Sh = MmaShape<D, MT>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ ScanShared scan;
+    __shared__ float row_max[4][16], row_sum[4][16];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g4 = lane >> 2, t4 = lane & 3;
+    const uint32_t base = smem_addr(smem);
+
+    Cursor cur;
+    long long first = 0;
+    const long long total = scan_list(p, scan, cur, blockIdx.x == 0, [&](long long n) {
+        first = block_begin(n, blockIdx.x, p.grid);
+        return first < block_begin(n, blockIdx.x + 1, p.grid) ? first : -1;
+    });
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (cur.s < 0) return;
+    int count = (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);     // tiles of this block
+    Cursor ahead = cur;
+    int to_load = count;
+
+    // copies: this thread's chunk of rows copy_row + i * kRowsPerPass
+    const int chunk = tid % Sh::kLanes, copy_row = tid / Sh::kLanes;
+    const bool copies = chunk * 8 < p.d, pads = chunk * 8 == p.d && (p.d & 8);
+    int pages[Sh::kPasses];
+    auto fetch_pages = [&]() {
+#pragma unroll
+        for (int i = 0; i < Sh::kPasses; ++i)
+            pages[i] = page_of(p, ahead.s, ahead.r, ahead.tile * Sh::kTile + copy_row + i * Sh::kRowsPerPass);
+    };
+    auto load = [&](int stage) {
+        if (to_load > 0) {
+            const int page_mask = (1 << p.page_shift) - 1;
+            const uint32_t dst = base + stage * Sh::kStage;
+#pragma unroll
+            for (int i = 0; i < Sh::kPasses; ++i) {
+                const int row = copy_row + i * Sh::kRowsPerPass, c = ahead.tile * Sh::kTile + row;
+                const bool real = c < ahead.r.len && copies;
+                long long off = 0;
+                if (real) {
+                    const int page = checked_page(p, pages[i]);
+                    off = ((((long long)page * p.n_kv + ahead.head) << p.page_shift) + (c & page_mask)) * p.d + chunk * 8;
+                }
+                if (copies || pads) {
+                    cp_async16(dst + swz<D>(row, chunk), static_cast<const __nv_bfloat16 *>(p.k) + off, real);
+                    cp_async16(dst + Sh::kHalf + swz<D>(row, chunk), static_cast<const __nv_bfloat16 *>(p.v) + off, real);
+                }
+            }
+            if (--to_load > 0) {
+                if (++ahead.tile == ahead.r.tiles) ahead.next_unit(p);
+                fetch_pages();
             }
         }
-        int page = p.table[(long long)s * p.max_pages + (c >> p.page_shift)];
-        if (page < 0 || page >= p.n_pages) {
-            bad |= LORA_DEV_BAD_PAGE;
-            page = 0;
-        }
-        const long long off = ((((long long)page * p.n_kv + kv_head) << p.page_shift) + (c & page_mask)) * p.d + at;
-        float kk[8] = {}, vv[8] = {}, dot = 0.f;
-        if (at < p.d) {
-            load8(static_cast<const E *>(p.k) + off, kk);
-            load8(static_cast<const E *>(p.v) + off, vv);
-        }
+        cp_commit();
+    };
+    fetch_pages();
+    for (int s = 0; s < kStages - 1; ++s) load(s);
+
+    uint32_t qf[MT][D / 16][4];
+    float o[MT][D / 8][4], m[MT][2], l[MT][2];
+    bool fresh = true;
+    int start_tile = cur.tile;
+    for (int it = 0; it < count; ++it) {
+        if (fresh) {        // a new unit: its queries, straight into MMA fragments
+            fresh = false;
+            start_tile = cur.tile;
+            const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dot += q[e] * kk[e];
-        dot = warp_sum(dot) * p.scale;
-        const float m2 = fmaxf(m, dot), a = __expf(m - m2), b = __expf(dot - m2);
-        m = m2;
-        l = l * a + b;
+            for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = o[e] * a + b * vv[e];
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int row = mt * 16 + hh * 8 + g4;
+                    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
+                                               (row < rows ? row_offset(p, cur, cur.row_tile * p.rt + row) : 0);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk) {
+                            const int col = ks * 16 + kk * 8 + t4 * 2;
+                            qf[mt][ks][kk * 2 + hh] =
+                                row < rows && col < p.d ? *reinterpret_cast<const uint32_t *>(src + col) : 0u;
+                        }
+                    m[mt][hh] = -INFINITY;
+                    l[mt][hh] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
+            }
+        }
+        cp_wait<kStages - 2>();
+        __syncthreads();
+        load((it + kStages - 1) % kStages);
+        const uint32_t ks_base = base + (it % kStages) * Sh::kStage, vs_base = ks_base + Sh::kHalf;
+        const int key0 = warp * Sh::kWarpKeys;
+        const int c0 = cur.tile * Sh::kTile + key0;         // first cached token of this warp's keys
+        const bool masked = c0 + Sh::kWarpKeys > cur.r.len - cur.r.n;
+
+        if (c0 < cur.r.len) {
+            // scores
+            float s[MT][Sh::kWarpKeys / 8][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[mt][j][e] = 0.f;
+            const int mi = lane >> 3, r8 = lane & 7;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                if (ks * 16 >= p.d) break;
+#pragma unroll
+                for (int kg = 0; kg < Sh::kWarpKeys / 16; ++kg) {
+                    uint32_t b[4];
+                    ldm4(b, ks_base + swz<D>(key0 + kg * 16 + (mi >> 1) * 8 + r8, ks * 2 + (mi & 1)));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma16816(s[mt][kg * 2], qf[mt][ks], b[0], b[1]);
+                        mma16816(s[mt][kg * 2 + 1], qf[mt][ks], b[2], b[3]);
+                    }
+                }
+            }
+            uint32_t see[MT][2] = {};       // bit x: row hh * 8 + g4 sees the warp's token x
+            if (masked) {
+                // scores that are not visible leave the softmax here, whatever they hold
+                const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        const int row = mt * 16 + hh * 8 + g4;
+                        if (row >= rows) continue;
+                        const int i = (cur.row_tile * p.rt + row) / p.group;
+                        for (int x = 0; x < Sh::kWarpKeys; ++x)
+                            if (sees(p, cur.r, i, c0 + x)) see[mt][hh] |= 1u << x;
+                    }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int x = j * 8 + t4 * 2 + (e & 1);
+                            if (!((see[mt][e >> 1] >> x) & 1)) s[mt][j][e] = -INFINITY;
+                        }
+            }
+            // softmax of the warp's keys, then its share of the output
+            uint32_t pf[MT][Sh::kWarpKeys / 16][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < Sh::kWarpKeys / 8; ++j) top = fmaxf(top, fmaxf(s[mt][j][hh * 2], s[mt][j][hh * 2 + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const float m2 = fmaxf(m[mt][hh], top * p.scale_log2);
+                    const float ref = m2 == -INFINITY ? 0.f : m2;        // nothing visible so far
+                    const float a = exp2_fast(m[mt][hh] - ref);
+                    m[mt][hh] = m2;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float &x = s[mt][j][hh * 2 + e];
+                            x = exp2_fast(fmaf(x, p.scale_log2, -ref));
+                            sum += x;
+                        }
+                    l[mt][hh] = l[mt][hh] * a + sum;      // this thread's columns only, joined at the end
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j) {
+                        o[mt][j][hh * 2] *= a;
+                        o[mt][j][hh * 2 + 1] *= a;
+                    }
+                }
+#pragma unroll
+                for (int kg = 0; kg < Sh::kWarpKeys / 16; ++kg) {
+                    pf[mt][kg][0] = pack_bf16(s[mt][kg * 2][0], s[mt][kg * 2][1]);
+                    pf[mt][kg][1] = pack_bf16(s[mt][kg * 2][2], s[mt][kg * 2][3]);
+                    pf[mt][kg][2] = pack_bf16(s[mt][kg * 2 + 1][0], s[mt][kg * 2 + 1][1]);
+                    pf[mt][kg][3] = pack_bf16(s[mt][kg * 2 + 1][2], s[mt][kg * 2 + 1][3]);
+                }
+            }
+            if (masked) {
+                // values that are not finite would enter the product times zero where they are masked: they are
+                // added to the rows that see them and taken out of the tile (its rows are this warp's own)
+                bool bad = false;
+                for (int x = lane; x < Sh::kWarpKeys * (D / 8); x += 32) {
+                    const int key = key0 + x / (D / 8), ch = x % (D / 8);
+                    if (ch * 8 >= p.d) continue;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(smem + (it % kStages) * Sh::kStage + Sh::kHalf + swz<D>(key, ch));
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        bad |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+                }
+                if (__any_sync(0xffffffffu, bad)) {
+                    for (int x = 0; x < Sh::kWarpKeys; ++x)
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) {
+                            if (j * 8 >= p.d) break;
+                            const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                                smem + (it % kStages) * Sh::kStage + Sh::kHalf + swz<D>(key0 + x, j) + t4 * 4);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t bits = e ? w & 0xffff0000u : w << 16;
+                                if ((bits & 0x7f800000u) != 0x7f800000u) continue;
+#pragma unroll
+                                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                                    for (int hh = 0; hh < 2; ++hh)
+                                        if ((see[mt][hh] >> x) & 1) o[mt][j][hh * 2 + e] += __uint_as_float(bits);
+                            }
+                        }
+                    __syncwarp();
+                    for (int x = lane; x < Sh::kWarpKeys * D; x += 32) {
+                        const int key = key0 + x / D, col = x % D;
+                        uint16_t *v16 = reinterpret_cast<uint16_t *>(smem + (it % kStages) * Sh::kStage + Sh::kHalf +
+                                                                     swz<D>(key, col >> 3)) + (col & 7);
+                        if ((*v16 & 0x7f80) == 0x7f80) *v16 = 0;
+                    }
+                    __syncwarp();
+                }
+            }
+#pragma unroll
+            for (int kg = 0; kg < Sh::kWarpKeys / 16; ++kg)
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    if (j * 16 >= p.d) break;
+                    uint32_t b[4];
+                    ldm4t(b, vs_base + swz<D>(key0 + kg * 16 + (mi & 1) * 8 + r8, j * 2 + (mi >> 1)));
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma16816(o[mt][j * 2], pf[mt][kg], b[0], b[1]);
+                        mma16816(o[mt][j * 2 + 1], pf[mt][kg], b[2], b[3]);
+                    }
+                }
+        }
+
+        const bool unit_ends = cur.tile + 1 == cur.r.tiles;
+        if (unit_ends || it + 1 == count) {
+            // join the four warps; the stage just used is free until the next iteration's barrier
+            const bool whole = unit_ends && start_tile == 0;
+            const int rows = min(p.rt, cur.r.n * p.group - cur.row_tile * p.rt);
+            float *dst = partial_of(p, blockIdx.x, start_tile > 0 ? 0 : 1);
+            float *scratch = reinterpret_cast<float *>(smem + (it % kStages) * Sh::kStage);     // [4][16][D]
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                __syncthreads();
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    const int row = hh * 8 + g4;
+                    float sum = l[mt][hh];
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    if (t4 == 0) {
+                        row_max[warp][row] = m[mt][hh];
+                        row_sum[warp][row] = sum;
+                    }
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j)
+                        *reinterpret_cast<float2 *>(scratch + (warp * 16 + row) * D + ((j ^ g4) * 8 + t4 * 2)) =
+                            make_float2(o[mt][j][hh * 2], o[mt][j][hh * 2 + 1]);
+                }
+                __syncthreads();
+                for (int x = tid; x < 16 * (D / 4); x += kThreads) {
+                    const int row = x / (D / 4), col = (x % (D / 4)) * 4, ur = mt * 16 + row;
+                    if (ur >= rows || col >= p.d) continue;
+                    float top = row_max[0][row];
+#pragma unroll
+                    for (int w = 1; w < 4; ++w) top = fmaxf(top, row_max[w][row]);
+                    const float ref = top == -INFINITY ? 0.f : top;
+                    float sum = 0.f;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const float a = exp2_fast(row_max[w][row] - ref);
+                        const float4 u =
+                            *reinterpret_cast<const float4 *>(scratch + (w * 16 + row) * D + (col ^ ((row & 7) * 8)));
+                        sum += a * row_sum[w][row];
+                        acc.x += a * u.x;
+                        acc.y += a * u.y;
+                        acc.z += a * u.z;
+                        acc.w += a * u.w;
+                    }
+                    if (whole) {
+                        const float r = sum == 0.f ? 0.f : 1.f / sum;      // a row that saw nothing: zeros
+                        uint2 w2;
+                        w2.x = pack_bf16(acc.x * r, acc.y * r);
+                        w2.y = pack_bf16(acc.z * r, acc.w * r);
+                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                                   row_offset(p, cur, cur.row_tile * p.rt + ur) + col) = w2;
+                    } else {
+                        *reinterpret_cast<float4 *>(dst + (long long)ur * p.d + col) = acc;
+                        if (col == 0) {
+                            dst[(long long)p.rt * p.d + ur * 2] = top;
+                            dst[(long long)p.rt * p.d + ur * 2 + 1] = sum;
+                        }
+                    }
+                }
+            }
+            fresh = true;
+        }
+        if (unit_ends) {
+            if (it + 1 < count) cur.next_unit(p);
+        } else {
+            ++cur.tile;
+        }
     }
-    if (bad && lane == 0) flag_status(p.status, bad);
-    const float r = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+    cp_wait<0>();
+}
+
+// fp32: four warps of four rows each, over 32 cached tokens a stage.  A lane
+// holds one token's score for its warp's rows, then four output columns.
+constexpr int kSimtTile = 32;
+constexpr int kSimtRows = 16;
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnParams p) {
+    constexpr int kLd = D + 4;            // row pitch: lanes a row apart read different banks
+    constexpr int kCols = D / 32;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ ScanShared scan;
+    float *qs = reinterpret_cast<float *>(smem);            // [16][D]
+    float *ps = qs + kSimtRows * D;                         // [4 warps][32 tokens][4 rows]
+    float *ring = ps + 4 * kSimtTile * 4;                   // [2][K, V][32][kLd]
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    Cursor cur;
+    long long first = 0;
+    const long long total = scan_list(p, scan, cur, blockIdx.x == 0, [&](long long n) {
+        first = block_begin(n, blockIdx.x, p.grid);
+        return first < block_begin(n, blockIdx.x + 1, p.grid) ? first : -1;
+    });
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (cur.s < 0) return;
+    const int count = (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);
+    Cursor ahead = cur;
+    int to_load = count;
+    const int chunks = p.d / 4;
+    auto load = [&](int stage) {
+        if (to_load > 0) {
+            const int page_mask = (1 << p.page_shift) - 1;
+            float *dst = ring + stage * 2 * kSimtTile * kLd;
+            for (int x = tid; x < kSimtTile * chunks; x += kThreads) {
+                const int row = x / chunks, ch = x - row * chunks, c = ahead.tile * kSimtTile + row;
+                long long off = 0;
+                if (c < ahead.r.len) {
+                    const int page = checked_page(p, page_of(p, ahead.s, ahead.r, c));
+                    off = ((((long long)page * p.n_kv + ahead.head) << p.page_shift) + (c & page_mask)) * p.d + ch * 4;
+                }
+                cp_async16(smem_addr(dst + row * kLd + ch * 4), static_cast<const float *>(p.k) + off, c < ahead.r.len);
+                cp_async16(smem_addr(dst + (kSimtTile + row) * kLd + ch * 4), static_cast<const float *>(p.v) + off,
+                           c < ahead.r.len);
+            }
+            if (--to_load > 0 && ++ahead.tile == ahead.r.tiles) ahead.next_unit(p);
+        }
+        cp_commit();
+    };
+    load(0);
+    float o[4][kCols], m[4], l[4];
+    bool fresh = true;
+    int start_tile = cur.tile;
+    for (int it = 0; it < count; ++it) {
+        const int row0 = warp * 4, rows = min(p.rt, cur.r.n * p.group - cur.row_tile * p.rt);
+        if (fresh) {
+            fresh = false;
+            start_tile = cur.tile;
+            __syncthreads();
+            for (int x = tid; x < kSimtRows * D; x += kThreads) {
+                const int row = x / D, col = x % D;
+                qs[x] = row < rows && col < p.d
+                            ? static_cast<const float *>(p.q)[row_offset(p, cur, cur.row_tile * p.rt + row) + col]
+                            : 0.f;
+            }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] *= r;
-    if (at < p.d) store8(static_cast<E *>(p.out) + w * p.d + at, o);
+            for (int a = 0; a < 4; ++a) {
+                m[a] = -INFINITY;
+                l[a] = 0.f;
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) o[a][j] = 0.f;
+            }
+        }
+        load((it + 1) & 1);
+        cp_wait<1>();
+        __syncthreads();
+        const float *ks = ring + (it & 1) * 2 * kSimtTile * kLd, *vs = ks + kSimtTile * kLd;
+        const int c = cur.tile * kSimtTile + lane;
+        if (row0 < rows) {
+            float s[4] = {};
+            for (int k = 0; k < p.d; k += 4) {
+                const float4 kk = *reinterpret_cast<const float4 *>(ks + lane * kLd + k);
+#pragma unroll
+                for (int a = 0; a < 4; ++a) {
+                    const float4 qq = *reinterpret_cast<const float4 *>(qs + (row0 + a) * D + k);
+                    s[a] = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, s[a]))));
+                }
+            }
+            uint32_t see[4];
+            float w[4];
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const bool on = row0 + a < rows && c < cur.r.len && sees(p, cur.r, (cur.row_tile * p.rt + row0 + a) / p.group, c);
+                see[a] = __ballot_sync(0xffffffffu, on);
+                const float x = on ? s[a] * p.scale_log2 : -INFINITY;
+                float top = x;
+#pragma unroll
+                for (int b = 16; b > 0; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
+                const float m2 = fmaxf(m[a], top), ref = m2 == -INFINITY ? 0.f : m2;
+                const float scale = exp2f(m[a] - ref);
+                w[a] = on ? exp2f(x - ref) : 0.f;
+                m[a] = m2;
+                l[a] = l[a] * scale + warp_sum(w[a]);
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) o[a][j] *= scale;
+            }
+            *reinterpret_cast<float4 *>(ps + (warp * kSimtTile + lane) * 4) = make_float4(w[0], w[1], w[2], w[3]);
+            __syncwarp();
+            const bool part = cur.tile * kSimtTile + kSimtTile > cur.r.len - cur.r.n;
+            for (int x = 0; x < kSimtTile; ++x) {
+                const float4 pp = *reinterpret_cast<const float4 *>(ps + (warp * kSimtTile + x) * 4);
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) {
+                    const float v = vs[x * kLd + j * 32 + lane];
+                    if (part) {      // what a masked slot holds must not be multiplied
+                        if ((see[0] >> x) & 1) o[0][j] = fmaf(pp.x, v, o[0][j]);
+                        if ((see[1] >> x) & 1) o[1][j] = fmaf(pp.y, v, o[1][j]);
+                        if ((see[2] >> x) & 1) o[2][j] = fmaf(pp.z, v, o[2][j]);
+                        if ((see[3] >> x) & 1) o[3][j] = fmaf(pp.w, v, o[3][j]);
+                    } else {
+                        o[0][j] = fmaf(pp.x, v, o[0][j]);
+                        o[1][j] = fmaf(pp.y, v, o[1][j]);
+                        o[2][j] = fmaf(pp.z, v, o[2][j]);
+                        o[3][j] = fmaf(pp.w, v, o[3][j]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const bool unit_ends = cur.tile + 1 == cur.r.tiles;
+        if (unit_ends || it + 1 == count) {
+            const bool whole = unit_ends && start_tile == 0;
+            float *dst = partial_of(p, blockIdx.x, start_tile > 0 ? 0 : 1);
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const int ur = row0 + a;
+                if (ur >= rows) continue;
+                const float r = l[a] == 0.f ? 0.f : 1.f / l[a];
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) {
+                    const int col = j * 32 + lane;
+                    if (col >= p.d) continue;
+                    if (whole)
+                        static_cast<float *>(p.out)[row_offset(p, cur, cur.row_tile * p.rt + ur) + col] = o[a][j] * r;
+                    else
+                        dst[(long long)ur * p.d + col] = o[a][j];
+                }
+                if (!whole && lane == 0) {
+                    dst[(long long)p.rt * p.d + ur * 2] = m[a];
+                    dst[(long long)p.rt * p.d + ur * 2 + 1] = l[a];
+                }
+            }
+            fresh = true;
+        }
+        if (unit_ends) {
+            if (it + 1 < count) cur.next_unit(p);
+        } else {
+            ++cur.tile;
+        }
+    }
+    cp_wait<0>();
+}
+
+// Block (c, part): if a unit starts in block c's part of the list and goes on
+// after it, adds up the parts: c's slot 1, then slot 0 of each block after it
+// until the unit ends.  One warp a row.
+template <typename E>
+__global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnParams p) {
+    __shared__ ScanShared scan;
+    Cursor cur;
+    const int c = blockIdx.x;
+    const long long total = scan_list(p, scan, cur, false, [&](long long n) {
+        const long long b = block_begin(n, c, p.grid), e = block_begin(n, c + 1, p.grid);
+        return b < e ? e - 1 : -1;
+    });
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (cur.s < 0 || cur.tile + 1 == cur.r.tiles) return;              // ends with this block
+    const long long begin = block_begin(total, c, p.grid), end = block_begin(total, c + 1, p.grid);
+    if (end - begin < cur.tile + 1) return;                            // started before this block
+    const long long last = end - 1 + (cur.r.tiles - 1 - cur.tile);     // the unit's last tile
+    int c_last = c;
+    while (block_begin(total, c_last + 1, p.grid) <= last) ++c_last;
+    const int lane = threadIdx.x & 31;
+    const int rows = min(p.rt, cur.r.n * p.group - cur.row_tile * p.rt);
+    for (int row = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); row < rows; row += gridDim.y * (kThreads / 32)) {
+        float m = -INFINITY, l = 0.f, o[8] = {};
+        const int at = lane * 8;
+        for (int b = c; b <= c_last; ++b) {
+            if (b > c && block_begin(total, b, p.grid) == block_begin(total, b + 1, p.grid)) continue;
+            const float *src = partial_of(p, b, b == c ? 1 : 0);
+            const float mb = src[(long long)p.rt * p.d + row * 2], lb = src[(long long)p.rt * p.d + row * 2 + 1];
+            const float m2 = fmaxf(m, mb), ref = m2 == -INFINITY ? 0.f : m2;
+            const float a = exp2f(m - ref), w = exp2f(mb - ref);
+            m = m2;
+            l = l * a + lb * w;
+            if (at < p.d) {
+                float u[8];
+                load8(src + (long long)row * p.d + at, u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = o[e] * a + u[e] * w;
+            }
+        }
+        const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= r;
+        if (at < p.d) store8(static_cast<E *>(p.out) + row_offset(p, cur, cur.row_tile * p.rt + row) + at, o);
+    }
+}
+
+template <typename K>
+int launch_list(K kernel, size_t smem, AttnParams &p, float *partial, cudaStream_t st, int *grid) {
+    int occ = 0;
+    if (smem_optin(reinterpret_cast<const void *>(kernel), smem, kThreads, &occ) || occ < 1) return LORA_ERR_CUDA;
+    p.grid = *grid = num_sms() * (occ < 2 ? occ : 2);
+    p.partial = partial;
+    kernel<<<p.grid, kThreads, smem, st>>>(p);
+    count_launch();
+    return cuda_status(cudaGetLastError());
+}
+
+constexpr int kMaxBlocksPerSm = 2;
+constexpr int kMaxRows = 32;
+
+template <int D, int MT>
+int launch_mma(AttnParams &p, float *partial, cudaStream_t st) {
+    int grid;
+    p.rt = 16 * MT;
+    p.tk = MmaShape<D, MT>::kTile;
+    return launch_list(attention_mma_kernel<D, MT>, MmaShape<D, MT>::kSmem, p, partial, st, &grid);
+}
+
+template <int D>
+int launch_simt(AttnParams &p, float *partial, cudaStream_t st) {
+    int grid;
+    p.rt = kSimtRows;
+    p.tk = kSimtTile;
+    const size_t smem = (size_t)(kSimtRows * D + 4 * kSimtTile * 4 + 4 * kSimtTile * (D + 4)) * 4;
+    return launch_list(attention_simt_kernel<D>, smem, p, partial, st, &grid);
+}
+
+int launch_attention(AttnParams &p, int dtype, float *partial, cudaStream_t st) {
+    if (dtype == LORA_F32)
+        return p.d <= 64 ? launch_simt<64>(p, partial, st) : p.d <= 128 ? launch_simt<128>(p, partial, st) : launch_simt<256>(p, partial, st);
+    // rows a request and kv head, on average: more than 16 share a tile of 32
+    const bool wide = (long long)p.T * p.group > 16LL * p.S;
+    if (p.d <= 64) return wide ? launch_mma<64, 2>(p, partial, st) : launch_mma<64, 1>(p, partial, st);
+    if (p.d <= 128) return wide ? launch_mma<128, 2>(p, partial, st) : launch_mma<128, 1>(p, partial, st);
+    return launch_mma<256, 1>(p, partial, st);
 }
 
 }  // namespace
@@ -87,7 +649,7 @@ using namespace lora;
 
 extern "C" size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T) {
     if (decode::check_kv(kv, n_q_heads) || n_q_heads < 1 || S < 0 || T < 0) return 0;
-    return 256;
+    return (size_t)num_sms() * kMaxBlocksPerSm * 2 * kMaxRows * (kv->head_dim + 2) * sizeof(float) + 256;
 }
 
 extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, const int *seg_starts, int S,
@@ -97,20 +659,24 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     int rc = decode::check_kv(kv, n_q_heads);
     if (rc) return rc;
     if (n_q_heads < 1) return LORA_ERR_SHAPE;
+    if (!(scale > 0.f) || scale > 1.0e30f) return LORA_ERR_ARG;
     if (S < 0 || T < 0 || (S == 0 && T > 0) || max_pages < 0 || (tree_mask && mask_words < 1)) return LORA_ERR_ARG;
-    if ((long long)max_pages * kv->page_size > 0x7fffffffLL) return LORA_ERR_SHAPE;
+    if ((long long)max_pages * kv->page_size > 0x7fffffffLL - 1024) return LORA_ERR_SHAPE;
+    if ((long long)T * n_q_heads > 0x7fffffffLL) return LORA_ERR_SHAPE;
     if (T == 0) return LORA_OK;
     if (!q || !out || !seg_starts || !kv_lens || !page_table || !workspace || max_pages < 1) return LORA_ERR_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || ((uintptr_t)tree_mask & 7u) ||
         (((uintptr_t)seg_starts | (uintptr_t)kv_lens | (uintptr_t)page_table) & 3u))
         return LORA_ERR_ARG;
+    if (num_sms() < 1) return LORA_ERR_CUDA;
     if (ws_bytes < lora_tree_attention_workspace_size(kv, n_q_heads, S, T)) return LORA_ERR_ARG;
-    AttnParams p;
+    decode::AttnParams p;
     p.q = q;
     p.k = kv->k;
     p.v = kv->v;
     p.n_q = n_q_heads;
     p.n_kv = kv->n_kv_heads;
+    p.group = n_q_heads / kv->n_kv_heads;
     p.d = kv->head_dim;
     p.page_shift = decode::log2_of(kv->page_size);
     p.n_pages = kv->n_pages;
@@ -122,14 +688,23 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     p.max_pages = max_pages;
     p.mask = tree_mask;
     p.words = mask_words;
-    p.scale = scale;
+    p.scale_log2 = scale * 1.44269504088896340736f;
     p.out = out;
     p.status = kv->status;
-    const long long warps = (long long)T * n_q_heads;
-    if (warps > 4LL * 0x7fffffff) return LORA_ERR_SHAPE;
-    const unsigned grid = (unsigned)((warps + 3) / 4);
-    if (kv->dtype == LORA_BF16) attention_rows_kernel<__nv_bfloat16><<<grid, 128, 0, (cudaStream_t)stream>>>(p);
-    else attention_rows_kernel<float><<<grid, 128, 0, (cudaStream_t)stream>>>(p);
+    cudaStream_t st = (cudaStream_t)stream;
+    if ((rc = launch_attention(p, kv->dtype, static_cast<float *>(workspace), st))) return rc;
+    // the join starts while the last blocks run; it waits for them before it reads their sums
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid, p.rt / (kThreads / 32));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = kv->dtype == LORA_BF16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<__nv_bfloat16>, p)
+                                                 : cudaLaunchKernelEx(&cfg, attention_join_kernel<float>, p);
     count_launch();
-    return cuda_status(cudaGetLastError());
+    return cuda_status(e);
 }

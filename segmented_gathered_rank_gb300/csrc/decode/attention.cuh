@@ -1,0 +1,172 @@
+// The work list of lora_tree_attention, shared by its kernels.
+//
+// The rows of a unit are up to `rt` of the n * (n_q / n_kv) query rows that
+// share one kv head of one request (row r: drafted token r / group, head r %
+// group), so a cached key and value are loaded once for the whole group.  A unit
+// is cut into tiles of `tk` cached tokens, and all tiles of all units, in
+// order (request, kv head, row tile, key tile), form one list.  Block c of
+// `grid` takes the tiles [c total / grid, (c + 1) total / grid): every block
+// gets the same number whatever the lengths are, and a unit cut between blocks
+// is joined afterwards from the blocks' partial sums.
+#pragma once
+
+#include "decode.cuh"
+
+namespace lora {
+namespace decode {
+
+struct AttnParams {
+    const void *q, *k, *v;
+    int n_q, n_kv, group, d, page_shift, n_pages;
+    const int *starts, *lens, *table;
+    int S, T, max_pages;
+    const long long *mask;
+    int words;
+    float scale_log2;        // scale * log2(e): the softmax works in powers of two
+    void *out;
+    int *status;
+    float *partial;          // [grid][2][rt][d + 2]: sums, then the rows' maximum and sum
+    int rt, tk, grid;        // rows a unit, tokens a tile (a power of two), blocks
+};
+
+struct Request {
+    int begin, n, len, tiles, row_tiles;   // tokens; drafted; cached; key tiles; row tiles
+    __device__ __forceinline__ long long work(int n_kv) const { return (long long)tiles * row_tiles * n_kv; }
+};
+
+// Request s with everything clamped into the arrays.  bad: LORA_DEV_* bits.
+__device__ __forceinline__ Request request_of(const AttnParams &p, int s, int *bad = nullptr) {
+    Request r;
+    const int b = p.starts[s], e = p.starts[s + 1], len = p.lens[s];
+    const long long cap = (long long)p.max_pages << p.page_shift;
+    r.begin = min(max(b, 0), p.T);
+    r.n = min(max(e, r.begin), p.T) - r.begin;
+    r.len = (int)min((long long)max(len, r.n), cap);
+    if (bad && (len < r.n || len > cap)) *bad |= LORA_DEV_BAD_LENGTH;
+    r.tiles = (r.len + p.tk - 1) / p.tk;
+    r.row_tiles = (int)(((long long)r.n * p.group + p.rt - 1) / p.rt);
+    return r;
+}
+
+// One block's place in the list.  tile/tiles: key tile of the unit.
+struct Cursor {
+    Request r;
+    int s, head, row_tile, tile;
+
+    __device__ __forceinline__ void next_unit(const AttnParams &p) {
+        tile = 0;
+        if (++row_tile < r.row_tiles) return;
+        row_tile = 0;
+        if (++head < p.n_kv) return;
+        head = 0;
+        do {
+            if (++s >= p.S) return;        // only past the end of the list
+            r = request_of(p, s);
+        } while (r.work(p.n_kv) == 0);
+    }
+};
+
+constexpr int kScanThreads = 128;
+
+struct ScanShared {
+    long long sums[kScanThreads / 32];
+    long long residual;
+    int request;
+};
+
+// Called by all of the block's first kScanThreads threads (others only join the
+// barriers): the length of the list, and the cursor at its tile `at(total)`
+// (s = -1 when that is negative).  flags: report bad tables.
+template <typename At>
+__device__ __forceinline__ long long scan_list(const AttnParams &p, ScanShared &sh, Cursor &c, bool flags, At at) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.S + kScanThreads - 1) / kScanThreads;
+    const int s0 = tid < kScanThreads ? min(p.S, tid * per) : p.S, s1 = min(p.S, s0 + per);
+    long long mine = 0;
+    int bad = 0;
+    for (int s = s0; s < s1; ++s) {
+        mine += request_of(p, s, &bad).work(p.n_kv);
+        if (flags && (p.starts[s + 1] < p.starts[s] || (s == 0 && p.starts[0] != 0) || (s + 1 == p.S && p.starts[p.S] != p.T)))
+            bad |= LORA_DEV_BAD_SEGMENTS;
+    }
+    if (flags && bad) flag_status(p.status, bad);
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long other = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += other;
+    }
+    if (lane == 31 && warp < kScanThreads / 32) sh.sums[warp] = upto;
+    if (tid == 0) sh.request = -1;
+    __syncthreads();
+    long long total = 0, before = upto - mine;
+#pragma unroll
+    for (int w = 0; w < kScanThreads / 32; ++w) {
+        if (w < warp) before += sh.sums[w];
+        total += sh.sums[w];
+    }
+    const long long pos = at(total);
+    if (pos >= before && pos < before + mine) {
+        long long left = pos - before;
+        for (int s = s0; s < s1; ++s) {
+            const long long w = request_of(p, s).work(p.n_kv);
+            if (left < w) {
+                sh.request = s;
+                sh.residual = left;
+                break;
+            }
+            left -= w;
+        }
+    }
+    __syncthreads();
+    c.s = sh.request;
+    if (c.s >= 0) {
+        c.r = request_of(p, c.s);
+        const long long unit = sh.residual / c.r.tiles;
+        c.tile = (int)(sh.residual % c.r.tiles);
+        c.row_tile = (int)(unit % c.r.row_tiles);
+        c.head = (int)(unit / c.r.row_tiles);
+    }
+    return total;
+}
+
+__device__ __forceinline__ long long block_begin(long long total, int c, int grid) { return total * c / grid; }
+
+// Whether drafted token i (row t of the mask) sees cached token c.
+__device__ __forceinline__ bool sees(const AttnParams &p, const Request &r, int i, int c) {
+    const int j = c - (r.len - r.n);
+    if (j < 0) return true;
+    if (c >= r.len) return false;
+    if (!p.mask) return j <= i;
+    return j < 64 * p.words && ((p.mask[(long long)(r.begin + i) * p.words + (j >> 6)] >> (j & 63)) & 1);
+}
+
+// Page of cached token c, clamped into the cache (flagged); -1 beyond the request.
+__device__ __forceinline__ int page_of(const AttnParams &p, int s, const Request &r, int c) {
+    return c < r.len ? __ldg(p.table + (long long)s * p.max_pages + (c >> p.page_shift)) : -1;
+}
+__device__ __forceinline__ int checked_page(const AttnParams &p, int page) {
+    if (page >= 0 && page < p.n_pages) return page;
+    flag_status(p.status, LORA_DEV_BAD_PAGE);
+    return 0;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Element offset of row `row` of the unit at cursor c in q and out.
+__device__ __forceinline__ long long row_offset(const AttnParams &p, const Cursor &c, int row) {
+    const int i = row / p.group, g = row - i * p.group;
+    return ((long long)(c.r.begin + i) * p.n_q + c.head * p.group + g) * p.d;
+}
+
+// Sums of block `block`: slot 0 when its part of the unit does not start it, else 1.
+__device__ __forceinline__ float *partial_of(const AttnParams &p, int block, int slot) {
+    return p.partial + ((long long)block * 2 + slot) * p.rt * (p.d + 2);
+}
+
+}  // namespace decode
+}  // namespace lora

@@ -445,12 +445,12 @@ def test_attention_refusals():
     mask = torch.zeros((3, 1), dtype=torch.int64, device="cuda")
 
     def status(dtype=L.LORA_BF16, page=8, d=16, q=q, n_q=4, starts=i32, S=2, T=3, lens=i32, table=i32, max_pages=4, mask=mask, words=1,
-               out=q, ws=ws, ws_bytes=None):
+               out=q, ws=ws, ws_bytes=None, scale=1.0):
         kv = L.KvPages(dtype, kd, kd, 4, 8, 2, 16)
         kv.page_size, kv.head_dim = page, d
         n = L.lora_launch_count()
         try:
-            L.lora_tree_attention(kv, q, n_q, starts, S, T, lens, table, max_pages, mask, words, 1.0, out, ws, ws_bytes=ws_bytes or ws.numel())
+            L.lora_tree_attention(kv, q, n_q, starts, S, T, lens, table, max_pages, mask, words, scale, out, ws, ws_bytes=ws_bytes or ws.numel())
         except L.LoraError as e:
             assert L.lora_launch_count() == n
             return e.status
@@ -470,6 +470,8 @@ def test_attention_refusals():
     assert status(table=None) == L.LORA_ERR_ARG
     assert status(max_pages=0) == L.LORA_ERR_ARG
     assert status(words=0) == L.LORA_ERR_ARG
+    assert status(scale=0.0) == L.LORA_ERR_ARG
+    assert status(scale=float("nan")) == L.LORA_ERR_ARG
     assert status(out=None) == L.LORA_ERR_ARG
     assert status(ws_bytes=16) == L.LORA_ERR_ARG
     assert status(max_pages=1 << 30) == L.LORA_ERR_SHAPE
