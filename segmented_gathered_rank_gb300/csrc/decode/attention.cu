@@ -572,15 +572,13 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnPara
     const long long begin = block_begin(total, c, p.grid), end = block_begin(total, c + 1, p.grid);
     if (end - begin < cur.tile + 1) return;                            // started before this block
     const long long last = end - 1 + (cur.r.tiles - 1 - cur.tile);     // the unit's last tile
-    int c_last = c;
-    while (block_begin(total, c_last + 1, p.grid) <= last) ++c_last;
+    const int c_last = block_of(total, last, p.grid);
     const int lane = threadIdx.x & 31;
     const int rows = min(p.rt, cur.r.n * p.group - cur.row_tile * p.rt);
     for (int row = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); row < rows; row += gridDim.y * (kThreads / 32)) {
         float m = -INFINITY, l = 0.f, o[8] = {};
         const int at = lane * 8;
         for (int b = c; b <= c_last; ++b) {
-            if (b > c && block_begin(total, b, p.grid) == block_begin(total, b + 1, p.grid)) continue;
             const float *src = partial_of(p, b, b == c ? 1 : 0);
             const float mb = src[(long long)p.rt * p.d + row * 2], lb = src[(long long)p.rt * p.d + row * 2 + 1];
             const float m2 = fmaxf(m, mb), ref = m2 == -INFINITY ? 0.f : m2;
@@ -601,46 +599,56 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnPara
     }
 }
 
+// What a call runs: rows and cached tokens a unit tile, blocks a SM.
+struct Variant {
+    bool tc;
+    int rt, tk, per_sm;
+};
+
+template <int D, int MT>
+Variant mma_variant() {
+    return {false, 16 * MT, MmaShape<D, MT>::kTile, D <= 128 ? 2 : 1};
+}
+
+Variant variant_of(int dtype, int d, int group, int S, int T) {
+    if (dtype == LORA_F32) return {false, kSimtRows, kSimtTile, d <= 128 ? 2 : 1};
+    const long long rows = (long long)T * group;       // against S: rows a request and kv head, on average
+    if ((d == 64 || d == 128) && rows > 32LL * S) return {true, rows > 128LL * S ? 256 : 128, 128, 1};
+    const bool wide = rows > 16LL * S;
+    if (d <= 64) return wide ? mma_variant<64, 2>() : mma_variant<64, 1>();
+    if (d <= 128) return wide ? mma_variant<128, 2>() : mma_variant<128, 1>();
+    return mma_variant<256, 1>();
+}
+
 template <typename K>
-int launch_list(K kernel, size_t smem, AttnParams &p, float *partial, cudaStream_t st, int *grid) {
-    int occ = 0;
-    if (smem_optin(reinterpret_cast<const void *>(kernel), smem, kThreads, &occ) || occ < 1) return LORA_ERR_CUDA;
-    p.grid = *grid = num_sms() * (occ < 2 ? occ : 2);
-    p.partial = partial;
+int launch_list(K kernel, size_t smem, const AttnParams &p, cudaStream_t st) {
+    if (smem_optin(reinterpret_cast<const void *>(kernel), smem)) return LORA_ERR_CUDA;
     kernel<<<p.grid, kThreads, smem, st>>>(p);
     count_launch();
     return cuda_status(cudaGetLastError());
 }
 
-constexpr int kMaxBlocksPerSm = 2;
-constexpr int kMaxRows = 32;
-
 template <int D, int MT>
-int launch_mma(AttnParams &p, float *partial, cudaStream_t st) {
-    int grid;
-    p.rt = 16 * MT;
-    p.tk = MmaShape<D, MT>::kTile;
-    return launch_list(attention_mma_kernel<D, MT>, MmaShape<D, MT>::kSmem, p, partial, st, &grid);
+int launch_mma(const AttnParams &p, cudaStream_t st) {
+    return launch_list(attention_mma_kernel<D, MT>, MmaShape<D, MT>::kSmem, p, st);
 }
 
 template <int D>
-int launch_simt(AttnParams &p, float *partial, cudaStream_t st) {
-    int grid;
-    p.rt = kSimtRows;
-    p.tk = kSimtTile;
+int launch_simt(const AttnParams &p, cudaStream_t st) {
     const size_t smem = (size_t)(kSimtRows * D + 4 * kSimtTile * 4 + 4 * kSimtTile * (D + 4)) * 4;
-    return launch_list(attention_simt_kernel<D>, smem, p, partial, st, &grid);
+    return launch_list(attention_simt_kernel<D>, smem, p, st);
 }
 
-int launch_attention(AttnParams &p, int dtype, float *partial, cudaStream_t st) {
+int launch_attention(AttnParams &p, const Variant &v, int dtype, cudaStream_t st) {
+    if (v.tc) return launch_attention_tc(p, st);
     if (dtype == LORA_F32)
-        return p.d <= 64 ? launch_simt<64>(p, partial, st) : p.d <= 128 ? launch_simt<128>(p, partial, st) : launch_simt<256>(p, partial, st);
-    // rows a request and kv head, on average: more than 16 share a tile of 32
-    const bool wide = (long long)p.T * p.group > 16LL * p.S;
-    if (p.d <= 64) return wide ? launch_mma<64, 2>(p, partial, st) : launch_mma<64, 1>(p, partial, st);
-    if (p.d <= 128) return wide ? launch_mma<128, 2>(p, partial, st) : launch_mma<128, 1>(p, partial, st);
-    return launch_mma<256, 1>(p, partial, st);
+        return p.d <= 64 ? launch_simt<64>(p, st) : p.d <= 128 ? launch_simt<128>(p, st) : launch_simt<256>(p, st);
+    if (p.d <= 64) return v.rt == 32 ? launch_mma<64, 2>(p, st) : launch_mma<64, 1>(p, st);
+    if (p.d <= 128) return v.rt == 32 ? launch_mma<128, 2>(p, st) : launch_mma<128, 1>(p, st);
+    return launch_mma<256, 1>(p, st);
 }
+
+size_t partial_bytes(const Variant &v, int d) { return (size_t)num_sms() * v.per_sm * 2 * v.rt * (d + 2) * sizeof(float); }
 
 }  // namespace
 }  // namespace lora
@@ -649,7 +657,8 @@ using namespace lora;
 
 extern "C" size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T) {
     if (decode::check_kv(kv, n_q_heads) || n_q_heads < 1 || S < 0 || T < 0) return 0;
-    return (size_t)num_sms() * kMaxBlocksPerSm * 2 * kMaxRows * (kv->head_dim + 2) * sizeof(float) + 256;
+    if (S == 0) return 16;
+    return partial_bytes(variant_of(kv->dtype, kv->head_dim, n_q_heads / kv->n_kv_heads, S, T), kv->head_dim) + 16;
 }
 
 extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, const int *seg_starts, int S,
@@ -692,10 +701,15 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     p.out = out;
     p.status = kv->status;
     cudaStream_t st = (cudaStream_t)stream;
-    if ((rc = launch_attention(p, kv->dtype, static_cast<float *>(workspace), st))) return rc;
+    const Variant variant = variant_of(kv->dtype, p.d, p.group, S, T);
+    p.rt = variant.rt;
+    p.tk = variant.tk;
+    p.grid = num_sms() * variant.per_sm;
+    p.partial = static_cast<float *>(workspace);
+    if ((rc = launch_attention(p, variant, kv->dtype, st))) return rc;
     // the join starts while the last blocks run; it waits for them before it reads their sums
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.grid, p.rt / (kThreads / 32));
+    cfg.gridDim = dim3(p.grid, p.rt <= 32 ? p.rt / 4 : 8);
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

@@ -4,9 +4,8 @@
 // share one kv head of one request (row r: drafted token r / group, head r %
 // group), so a cached key and value are loaded once for the whole group.  A unit
 // is cut into tiles of `tk` cached tokens, and all tiles of all units, in
-// order (request, kv head, row tile, key tile), form one list.  Block c of
-// `grid` takes the tiles [c total / grid, (c + 1) total / grid): every block
-// gets the same number whatever the lengths are, and a unit cut between blocks
+// order (request, kv head, row tile, key tile), form one list that is cut into
+// `grid` equal parts: every block gets the same number whatever the lengths are, and a unit cut between blocks
 // is joined afterwards from the blocks' partial sums.
 #pragma once
 
@@ -130,7 +129,16 @@ __device__ __forceinline__ long long scan_list(const AttnParams &p, ScanShared &
     return total;
 }
 
-__device__ __forceinline__ long long block_begin(long long total, int c, int grid) { return total * c / grid; }
+// The first tile of block c: total / grid tiles each, one more for the first total % grid blocks.
+__device__ __forceinline__ long long block_begin(long long total, int c, int grid) {
+    const long long each = total / grid;
+    return each * c + min((long long)c, total - each * grid);
+}
+// The block that has tile x.
+__device__ __forceinline__ int block_of(long long total, long long x, int grid) {
+    const long long each = total / grid, more = total - each * grid, edge = more * (each + 1);
+    return (int)(x < edge ? x / (each + 1) : more + (x - edge) / each);
+}
 
 // Whether drafted token i (row t of the mask) sees cached token c.
 __device__ __forceinline__ bool sees(const AttnParams &p, const Request &r, int i, int c) {
@@ -167,6 +175,9 @@ __device__ __forceinline__ long long row_offset(const AttnParams &p, const Curso
 __device__ __forceinline__ float *partial_of(const AttnParams &p, int block, int slot) {
     return p.partial + ((long long)block * 2 + slot) * p.rt * (p.d + 2);
 }
+
+// attention_tc.cu: p.rt (128 or 256 rows), p.tk (128), p.grid and p.partial set; p.d is 64 or 128.
+int launch_attention_tc(AttnParams &p, cudaStream_t st);
 
 }  // namespace decode
 }  // namespace lora

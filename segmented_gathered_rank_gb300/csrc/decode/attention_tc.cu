@@ -1,0 +1,611 @@
+// Tree attention on the tensor cores (tcgen05) for units of many query rows.
+//
+// With R rows a kv head the products cost 4 R flops for every 2 bytes of K and
+// V: from R = 64 on, warp MMAs (about a quarter of the tcgen05 rate) bound the
+// kernel instead of memory.  Here S = Q K^T and O += P V are tcgen05 products
+// of 128 rows x 128 cached tokens with S, P and O in tensor memory.
+//
+// Two softmax streams of four warps each (one thread a row) share the tensor
+// cores, so that one's products run under the other's exponentials:
+//   NQ = 2   units of up to 256 rows; stream w has rows w * 128 .. + 127 and both
+//            take every key tile, so a tile in shared memory serves 256 rows;
+//   NQ = 1   units of up to 128 rows; stream w takes every other key tile, with
+//            a maximum, sum and output of its own, joined when the unit ends.
+// Four producer warps copy K and V tiles with cp.async (any page size; rows past
+// the request become zeros) into a ring of swizzled slots; one thread issues all
+// MMAs.  P overwrites the columns of S that it was computed from.
+//
+// A row keeps the maximum it last scaled by until a score passes it by 2^8
+// (sums stay far inside fp32), so the output is rescaled in a few tiles only.
+#include "attention.cuh"
+#include "tc_common.cuh"
+
+namespace lora {
+namespace {
+
+using namespace decode;
+using namespace tc;
+
+constexpr int kTile = 128;                 // cached tokens a tile, rows a stream
+constexpr int kThreadsTc = 13 * 32;        // streams 0 and 1, producers, MMA
+constexpr int kProducer0 = 8, kMmaWarp = 12;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.f;
+
+template <int D>
+struct TcShape {
+    static constexpr int kSlot = kTile * D * 2;              // a K or V tile (or a stream's queries)
+    static constexpr int kSlots = D == 128 ? 5 : 10;
+    static constexpr int kControl = 1536;
+    static constexpr size_t kSmem = (size_t)(2 + kSlots) * kSlot + kControl + 1024;
+};
+
+struct Control {
+    uint64_t full[10], empty[10], s_full[2], p_ready[2], o_full[2], q_ready[2], pair, drain;
+    int bad[10];              // sequence number + 1 of a V tile that held values that are not finite
+    int accumulate[2];        // the stream wrote its output itself before the unit's first product
+    volatile int abort;
+    uint32_t tmem;
+    float row_max[kTile], row_sum[kTile];       // stream 1's, for the join
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Control *ctl) {
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    if (wait_phase(bar, parity, &ctl->abort)) return true;
+    ctl->abort = 1;
+    return false;
+}
+
+// wait_bar for a whole warp: all lanes go on, or none.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Control *ctl) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, ctl));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool real) {
+    const int bytes = real ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// Arrives on `bar` once this thread's copies so far are complete.
+__device__ __forceinline__ void cp_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// D[tmem] (+)= A[tmem] . B[smem], A bf16 pairs in columns.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+        "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+        "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// V as the B operand of O += P V: rows of 64 head elements (128 bytes, swizzled),
+// one row a cached token, so the token (K) axis runs along the rows.  lbo: bytes
+// between the two halves of the head; 1024 bytes between groups of 8 tokens.
+__device__ __forceinline__ uint64_t desc_rows_sw128(uint32_t smem_addr, uint32_t lbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(lbo >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+constexpr uint32_t kTransposeB = 1u << 16;
+
+// Byte offset of 16-byte chunk `chunk` of row `row` in a tile: halves of 64
+// elements, rows of 128 bytes, chunks XORed with the row.
+__device__ __forceinline__ uint32_t tile_off(int row, int chunk) {
+    return (uint32_t)((chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ bool has_non_finite(uint4 u) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bad |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
+    return bad;
+}
+
+// The part of the list that a block works through, one unit after another.
+struct Segment {
+    int first, tiles;        // key tiles of the unit
+    bool whole;              // the block has the unit to itself
+};
+__device__ __forceinline__ Segment segment_at(const Cursor &c, int left) {
+    Segment s;
+    s.first = c.tile;
+    s.tiles = min(left, c.r.tiles - c.tile);
+    s.whole = c.tile == 0 && s.tiles == c.r.tiles;
+    return s;
+}
+__device__ __forceinline__ void advance(const AttnParams &p, Cursor &c, const Segment &s, int &left) {
+    left -= s.tiles;
+    c.tile += s.tiles;
+    if (left > 0 && c.tile == c.r.tiles) c.next_unit(p);
+}
+
+template <int D, int NQ>
+__device__ void produce(const AttnParams &p, Cursor cur, int left, uint8_t *ring, Control *ctl) {
+    using Sh = TcShape<D>;
+    constexpr int kLanes = D / 8, kRowsPerPass = 128 / kLanes, kPasses = kTile / kRowsPerPass;
+    const int tid = threadIdx.x - kProducer0 * 32;
+    const int chunk = tid % kLanes, row0 = tid / kLanes;
+    const int page_mask = (1 << p.page_shift) - 1;
+    const uint32_t base = smem_u32(ring);
+    uint32_t seq = 0;
+    while (left > 0) {
+        const Segment seg = segment_at(cur, left);
+        for (int tile = seg.first; tile < seg.first + seg.tiles; ++tile) {
+            int pages[kPasses];
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) pages[i] = page_of(p, cur.s, cur.r, tile * kTile + row0 + i * kRowsPerPass);
+            const bool masked = (tile + 1) * kTile > cur.r.len - cur.r.n;
+            for (int which = 0; which < 2; ++which, ++seq) {
+                const uint32_t slot = seq % Sh::kSlots, use = seq / Sh::kSlots;
+                if (!wait_bar(&ctl->empty[slot], (use & 1) ^ 1, ctl)) return;
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(which ? p.v : p.k);
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const int row = row0 + i * kRowsPerPass, c = tile * kTile + row;
+                    const bool real = c < cur.r.len;
+                    long long off = 0;
+                    if (real) {
+                        const int page = checked_page(p, pages[i]);
+                        off = ((((long long)page * p.n_kv + cur.head) << p.page_shift) + (c & page_mask)) * D + chunk * 8;
+                    }
+                    cp_async16(base + slot * Sh::kSlot + tile_off(row, chunk), src + off, real);
+                }
+                if (!(which && masked)) {
+                    cp_arrive(&ctl->full[slot]);
+                    continue;
+                }
+                // a V tile with drafted tokens: a masked value that is not finite would enter the product times
+                // zero, so each thread takes such values out of the chunks it copied and says that it did
+                asm volatile("cp.async.wait_all;\n" ::: "memory");
+                for (int i = 0; i < kPasses; ++i) {
+                    uint4 *at = reinterpret_cast<uint4 *>(ring + slot * Sh::kSlot + tile_off(row0 + i * kRowsPerPass, chunk));
+                    const uint4 u = *at;
+                    if (!has_non_finite(u)) continue;
+                    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+                        if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
+                    }
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                    ctl->bad[slot] = (int)seq + 1;
+                }
+                fence_proxy_async();
+                mbar_arrive(&ctl->full[slot]);
+            }
+        }
+        advance(p, cur, seg, left);
+    }
+}
+
+template <int D, int NQ>
+__device__ void issue(const AttnParams &p, Cursor cur, int left, uint8_t *queries, uint8_t *ring, Control *ctl) {
+    using Sh = TcShape<D>;
+    const uint32_t tmem = ctl->tmem;
+    const uint32_t q_base = smem_u32(queries), r_base = smem_u32(ring);
+    constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
+    constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, D) | kTransposeB;
+    uint32_t seq0 = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
+    // tile t of the segment: K in ring position seq0 + 2 t, V right after it
+    auto slot_full = [&](uint32_t seq) {
+        if (!wait_bar(&ctl->full[seq % Sh::kSlots], (seq / Sh::kSlots) & 1, ctl)) return false;
+        fence_proxy_async();          // the copies were ordinary writes; the MMAs read through the async proxy
+        fence_after_sync();
+        return true;
+    };
+    auto scores = [&](int w, uint32_t seq) {      // S_w = Q_w K^T
+        const uint32_t k = r_base + (seq % Sh::kSlots) * Sh::kSlot, q = q_base + w * Sh::kSlot;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * (kTile * 128) + (ks & 3) * 32;
+            mma_bf16(tmem + w * kTile, desc_kmajor_sw128(q + off), desc_kmajor_sw128(k + off), idesc_s, ks > 0);
+        }
+        mma_commit(&ctl->s_full[w]);
+    };
+    auto output = [&](int w, uint32_t seq, bool accumulate) {      // O_w += P_w V
+        const uint32_t v = r_base + (seq % Sh::kSlots) * Sh::kSlot;
+#pragma unroll
+        for (int ks = 0; ks < kTile / 16; ++ks)
+            mma_bf16_ts(tmem + 2 * kTile + w * D, tmem + w * kTile + ks * 8,
+                        desc_rows_sw128(v + ks * 2048, kTile * 128), idesc_o, accumulate || ks > 0);
+    };
+    auto release = [&](uint32_t seq) { mma_commit(&ctl->empty[seq % Sh::kSlots]); };
+    auto probabilities = [&](int w) {
+        if (!wait_bar(&ctl->p_ready[w], p_phase[w] & 1, ctl)) return false;
+        ++p_phase[w];
+        fence_after_sync();
+        return true;
+    };
+    while (left > 0) {
+        const Segment seg = segment_at(cur, left);
+        const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
+        const int streams = NQ == 2 ? (rows > kTile ? 2 : 1) : (seg.tiles > 1 ? 2 : 1);
+        for (int w = 0; w < streams; ++w) {
+            if (!wait_bar(&ctl->q_ready[w], q_phase[w] & 1, ctl)) return;
+            ++q_phase[w];
+        }
+        fence_after_sync();
+        if (NQ == 2) {
+            if (!slot_full(seq0)) return;
+            for (int w = 0; w < streams; ++w) scores(w, seq0);
+            release(seq0);
+            for (int t = 0; t < seg.tiles; ++t) {
+                const uint32_t v = seq0 + 2 * t + 1;
+                const bool more = t + 1 < seg.tiles;
+                for (int w = 0; w < streams; ++w) {
+                    if (!probabilities(w)) return;
+                    if (w == 0 && !slot_full(v)) return;
+                    output(w, v, t > 0 || ctl->accumulate[w]);
+                    if (!more) mma_commit(&ctl->o_full[w]);
+                    if (w == streams - 1) release(v);
+                    if (more) {
+                        if (w == 0 && !slot_full(v + 1)) return;
+                        scores(w, v + 1);
+                    }
+                }
+                if (more) release(v + 1);
+            }
+        } else {
+            for (int w = 0; w < streams; ++w) {
+                if (!slot_full(seq0 + 2 * w)) return;
+                scores(w, seq0 + 2 * w);
+                release(seq0 + 2 * w);
+            }
+            for (int t = 0; t < seg.tiles; ++t) {
+                const int w = t & 1;
+                const uint32_t v = seq0 + 2 * t + 1;
+                if (!probabilities(w) || !slot_full(v)) return;
+                output(w, v, t > 1 || ctl->accumulate[w]);
+                release(v);
+                if (t + 2 < seg.tiles) {
+                    if (!slot_full(v + 3)) return;
+                    scores(w, v + 3);
+                    release(v + 3);
+                } else {
+                    mma_commit(&ctl->o_full[w]);
+                }
+            }
+        }
+        seq0 += 2 * seg.tiles;
+        advance(p, cur, seg, left);
+    }
+}
+
+// One thread a row: its queries into shared memory, the softmax of its scores,
+// and at the end of the segment its output.
+template <int D, int NQ>
+__device__ void attend(const AttnParams &p, Cursor cur, int left, uint8_t *queries, Control *ctl) {
+    using Sh = TcShape<D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = warp >> 2;                                  // stream
+    const int row = (warp & 3) * 32 + lane;                   // of the stream, and its lane of tensor memory
+    const uint32_t quad = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_tmem = ctl->tmem + quad + w * kTile, o_tmem = ctl->tmem + quad + 2 * kTile + w * D;
+    uint8_t *my_q = queries + w * Sh::kSlot;
+    uint32_t s_phase = 0, o_phase = 0, pair_phase = 0, seq0 = 0;
+    auto both_streams = [&]() {                               // a barrier of the eight softmax warps
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->pair);
+        return wait_warp(&ctl->pair, pair_phase++ & 1, ctl);
+    };
+    while (left > 0) {
+        const Segment seg = segment_at(cur, left);
+        const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
+        const int ur = row + (NQ == 2 ? w * kTile : 0);       // row of the unit
+        const bool live = ur < rows, warp_live = ur - lane < rows;
+        const bool active = NQ == 2 ? (w == 0 || rows > kTile) : (w == 0 || seg.tiles > 1);
+        float m = -INFINITY, l = 0.f;
+        if (active) {
+            const long long q_off = live ? row_offset(p, cur, cur.row_tile * p.rt + ur) : 0;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + q_off);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint4 *>(my_q + tile_off(row, c)) = live ? src[c] : make_uint4(0, 0, 0, 0);
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) {
+                if ((warp & 3) == 0) ctl->accumulate[w] = 0;
+                mbar_arrive(&ctl->q_ready[w]);
+            }
+            const int token = (cur.row_tile * p.rt + ur) / p.group;
+            for (int t = NQ == 2 ? 0 : w; t < seg.tiles; t += NQ == 2 ? 1 : 2) {
+                const int tile = seg.first + t;
+                const bool first = t < (NQ == 2 ? 1 : 2);
+                if (!wait_warp(&ctl->s_full[w], s_phase & 1, ctl)) return;
+                ++s_phase;
+                fence_after_sync();
+                const int c0 = tile * kTile;
+                const bool masked = c0 + kTile > cur.r.len - cur.r.n;
+                uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+                if (warp_live) {
+                    if (masked) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            see[b] = 0;
+                            if (live)
+                                for (int x = 0; x < 32; ++x)
+                                    if (sees(p, cur.r, token, c0 + b * 32 + x)) see[b] |= 1u << x;
+                        }
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float s[32];
+                        tmem_ld32(s_tmem + b * 32, s);
+                        if (masked) {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                if ((see[b] >> x) & 1) top = fmaxf(top, s[x]);
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) top = fmaxf(top, s[x]);
+                        }
+                    }
+                    top *= p.scale_log2;
+                    if (__any_sync(0xffffffffu, top > m + kRescaleLog2 || (m == -INFINITY && top > m))) {
+                        const float m2 = fmaxf(m, top);
+                        const float a = m2 == -INFINITY ? 1.f : exp2_fast(m - m2);
+                        m = m2;
+                        l *= a;
+                        if (!first) {
+#pragma unroll
+                            for (int b = 0; b < D / 32; ++b) {
+                                float o[32];
+                                tmem_ld32(o_tmem + b * 32, o);
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) o[x] *= a;
+                                tmem_st32(o_tmem + b * 32, o);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        float s[32];
+                        uint32_t pk[16];
+                        tmem_ld32(s_tmem + b * 32, s);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            float e = exp2_fast(fmaf(s[x], p.scale_log2, -ref));
+                            if (masked && !((see[b] >> x) & 1)) e = 0.f;
+                            s[x] = e;
+                            sum += e;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(s[2 * x], s[2 * x + 1]);
+                            pk[x] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        tmem_st16(s_tmem + b * 16, pk);
+                    }
+                    l += sum;
+                    tmem_wait_st();
+                }
+                if (masked) {
+                    // values that the producers took out of the tile, for the rows that see them
+                    const uint32_t v = seq0 + 2 * t + 1, slot = v % Sh::kSlots;
+                    if (!wait_warp(&ctl->full[slot], (v / Sh::kSlots) & 1, ctl)) return;
+                    if (*(volatile int *)&ctl->bad[slot] == (int)v + 1) {
+                        if ((warp & 3) == 0 && lane == 0) ctl->accumulate[w] = 1;
+                        for (int b = 0; b < D / 32; ++b) {
+                            float o[32];
+                            tmem_ld32(o_tmem + b * 32, o);
+                            if (first) {
+#pragma unroll
+                                for (int x = 0; x < 32; ++x) o[x] = 0.f;
+                            }
+                            for (int x = 0; x < kTile; ++x) {
+                                if (!live || !((see[x >> 5] >> (x & 31)) & 1)) continue;
+                                const int c = c0 + x;
+                                const int page = checked_page(p, page_of(p, cur.s, cur.r, c));
+                                const __nv_bfloat16 *vr =
+                                    static_cast<const __nv_bfloat16 *>(p.v) +
+                                    ((((long long)page * p.n_kv + cur.head) << p.page_shift) + (c & ((1 << p.page_shift) - 1))) * D + b * 32;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) {
+                                    const float f = __bfloat162float(vr[e]);
+                                    if ((__float_as_uint(f) & 0x7f800000u) == 0x7f800000u) o[e] += f;
+                                }
+                            }
+                            tmem_st32(o_tmem + b * 32, o);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->p_ready[w]);
+            }
+            if (!wait_warp(&ctl->o_full[w], o_phase & 1, ctl)) return;
+            ++o_phase;
+            fence_after_sync();
+        }
+        // the end of the segment: join the streams (NQ == 1), then write
+        float other = 0.f;                       // weight of stream 1's sums
+        const bool joined = NQ == 1 && seg.tiles > 1;
+        float scale = 1.f;
+        if (joined) {
+            if (w == 1) {
+                ctl->row_max[row] = m;
+                ctl->row_sum[row] = l;
+            }
+            if (!both_streams()) return;
+            if (w == 0) {
+                const float m1 = ctl->row_max[row], top = fmaxf(m, m1), ref = top == -INFINITY ? 0.f : top;
+                scale = exp2_fast(m - ref);
+                other = exp2_fast(m1 - ref);
+                m = top;
+                l = l * scale + ctl->row_sum[row] * other;
+            }
+        }
+        const bool writes = active && live && (NQ == 2 || w == 0);
+        float *dst = partial_of(p, blockIdx.x, seg.first > 0 ? 0 : 1);
+        const float r = l == 0.f ? 0.f : 1.f / l;            // a row that saw nothing: zeros
+        if (writes && !seg.whole) {
+            dst[(long long)p.rt * D + ur * 2] = m;
+            dst[(long long)p.rt * D + ur * 2 + 1] = l;
+        }
+        // stream 1 hands its output over through its queries' space, 64 columns at a time
+        float *hand = reinterpret_cast<float *>(queries + Sh::kSlot);
+        constexpr int kHandCols = D == 128 ? 64 : 32;
+        for (int h = 0; h < D / kHandCols; ++h) {
+            if (joined && w == 1) {
+#pragma unroll
+                for (int b = 0; b < kHandCols / 32; ++b) {
+                    float o[32];
+                    tmem_ld32(o_tmem + h * kHandCols + b * 32, o);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) hand[(b * 32 + x) * kTile + row] = o[x];
+                }
+            }
+            if (joined && !both_streams()) return;
+            if (active && warp_live && (NQ == 2 || w == 0)) {
+#pragma unroll
+                for (int b = 0; b < kHandCols / 32; ++b) {
+                    float o[32];
+                    tmem_ld32(o_tmem + h * kHandCols + b * 32, o);
+                    if (joined) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) o[x] = o[x] * scale + hand[(b * 32 + x) * kTile + row] * other;
+                    }
+                    if (writes) {
+                        const int col = h * kHandCols + b * 32;
+                        if (seg.whole) {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] *= r;
+                            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row_offset(p, cur, cur.row_tile * p.rt + ur) + col;
+#pragma unroll
+                            for (int x = 0; x < 32; x += 8) store8(out + x, o + x);
+                        } else {
+                            float *to = dst + (long long)ur * D + col;
+#pragma unroll
+                            for (int x = 0; x < 32; x += 8) store8(to + x, o + x);
+                        }
+                    }
+                }
+            }
+            if (joined && !both_streams()) return;
+        }
+        fence_before_sync();       // the reads of O come before the next unit's first product
+        seq0 += 2 * seg.tiles;
+        advance(p, cur, seg, left);
+    }
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(kThreadsTc, 1) attention_tc_kernel(const AttnParams p) {
+    using Sh = TcShape<D>;
+    extern __shared__ uint8_t raw[];
+    __shared__ ScanShared scan;
+    uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint8_t *queries = smem, *ring = smem + 2 * Sh::kSlot;
+    Control *ctl = reinterpret_cast<Control *>(ring + Sh::kSlots * Sh::kSlot);
+    const int warp = threadIdx.x >> 5;
+    static_assert(sizeof(Control) <= Sh::kControl, "control block");
+
+    Cursor cur;
+    long long first = 0;
+    const long long total = scan_list(p, scan, cur, blockIdx.x == 0, [&](long long n) {
+        first = block_begin(n, blockIdx.x, p.grid);
+        return first < block_begin(n, blockIdx.x + 1, p.grid) ? first : -1;
+    });
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (cur.s < 0) return;
+    const int count = (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Sh::kSlots; ++i) {
+            mbar_init(&ctl->full[i], 128);
+            mbar_init(&ctl->empty[i], 1);
+            ctl->bad[i] = 0;
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&ctl->s_full[w], 1);
+            mbar_init(&ctl->p_ready[w], 4);
+            mbar_init(&ctl->o_full[w], 1);
+            mbar_init(&ctl->q_ready[w], 4);
+            ctl->accumulate[w] = 0;
+        }
+        mbar_init(&ctl->pair, 8);
+        mbar_init(&ctl->drain, 1);
+        ctl->abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ctl->tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp < kProducer0) {
+        attend<D, NQ>(p, cur, count, queries, ctl);
+    } else if (warp < kMmaWarp) {
+        produce<D, NQ>(p, cur, count, ring, ctl);
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+    } else {
+        if ((threadIdx.x & 31) == 0) {
+            issue<D, NQ>(p, cur, count, queries, ring, ctl);
+            mma_commit(&ctl->drain);
+            wait_phase(&ctl->drain, 0, nullptr);
+        }
+        __syncwarp();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (threadIdx.x == 0 && ctl->abort) flag_status(p.status, LORA_DEV_WAIT_TIMEOUT);
+    if (warp == kMmaWarp) tmem_dealloc(ctl->tmem, kTmemCols);
+}
+
+template <int D, int NQ>
+int launch(AttnParams &p, cudaStream_t st) {
+    if (smem_optin(reinterpret_cast<const void *>(attention_tc_kernel<D, NQ>), TcShape<D>::kSmem)) return LORA_ERR_CUDA;
+    attention_tc_kernel<D, NQ><<<p.grid, kThreadsTc, TcShape<D>::kSmem, st>>>(p);
+    count_launch();
+    return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+
+namespace decode {
+
+int launch_attention_tc(AttnParams &p, cudaStream_t st) {
+    if (p.d == 128) return p.rt == 256 ? launch<128, 2>(p, st) : launch<128, 1>(p, st);
+    return p.rt == 256 ? launch<64, 2>(p, st) : launch<64, 1>(p, st);
+}
+
+}  // namespace decode
+}  // namespace lora
