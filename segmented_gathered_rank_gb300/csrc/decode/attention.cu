@@ -214,8 +214,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) attention_mma_kern
                         const int row = mt * 16 + hh * 8 + g4;
                         if (row >= rows) continue;
                         const int i = (cur.row_tile * p.rt + row) / p.group;
-                        for (int x = 0; x < Sh::kWarpKeys; ++x)
-                            if (sees(p, cur.r, i, c0 + x)) see[mt][hh] |= 1u << x;
+                        see[mt][hh] = seen_word(p, cur.r, i, c0);
                     }
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
@@ -469,7 +468,6 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
         cp_wait<1>();
         __syncthreads();
         const float *ks = ring + (it & 1) * 2 * kSimtTile * kLd, *vs = ks + kSimtTile * kLd;
-        const int c = cur.tile * kSimtTile + lane;
         if (row0 < rows) {
             float s[4] = {};
             for (int k = 0; k < p.d; k += 4) {
@@ -484,8 +482,9 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
             float w[4];
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
-                const bool on = row0 + a < rows && c < cur.r.len && sees(p, cur.r, (cur.row_tile * p.rt + row0 + a) / p.group, c);
-                see[a] = __ballot_sync(0xffffffffu, on);
+                see[a] = 0;
+                if (row0 + a < rows) see[a] = seen_word(p, cur.r, (cur.row_tile * p.rt + row0 + a) / p.group, cur.tile * kSimtTile);
+                const bool on = (see[a] >> lane) & 1;
                 const float x = on ? s[a] * p.scale_log2 : -INFINITY;
                 float top = x;
 #pragma unroll
@@ -575,28 +574,43 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnPara
     const int c_last = block_of(total, last, p.grid);
     const int lane = threadIdx.x & 31;
     const int rows = min(p.rt, cur.r.n * p.group - cur.row_tile * p.rt);
-    for (int row = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); row < rows; row += gridDim.y * (kThreads / 32)) {
-        float m = -INFINITY, l = 0.f, o[8] = {};
-        const int at = lane * 8;
-        for (int b = c; b <= c_last; ++b) {
-            const float *src = partial_of(p, b, b == c ? 1 : 0);
-            const float mb = src[(long long)p.rt * p.d + row * 2], lb = src[(long long)p.rt * p.d + row * 2 + 1];
-            const float m2 = fmaxf(m, mb), ref = m2 == -INFINITY ? 0.f : m2;
-            const float a = exp2f(m - ref), w = exp2f(mb - ref);
-            m = m2;
-            l = l * a + lb * w;
+    const int row = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5), at = lane * 8, parts = c_last - c + 1;
+    if (row >= rows) return;
+    auto part = [&](int b) { return partial_of(p, c + b, b == 0 ? 1 : 0); };
+    // each part's maximum and sum, a lane a part, then the parts' shares
+    float m = -INFINITY, l = 0.f, o[8] = {};
+    for (int b0 = 0; b0 < parts; b0 += 32) {
+        float mb = -INFINITY, lb = 0.f;
+        if (b0 + lane < parts) {
+            const float *ml = part(b0 + lane) + (long long)p.rt * p.d + row * 2;
+            mb = ml[0];
+            lb = ml[1];
+        }
+        float top = mb;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        top = fmaxf(m, top);
+        const float ref = top == -INFINITY ? 0.f : top, a = exp2f(m - ref), share = exp2f(mb - ref);
+        m = top;
+        l = l * a + warp_sum(lb * share);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= a;
+        const int n = min(32, parts - b0);
+#pragma unroll 4
+        for (int b = 0; b < n; ++b) {
+            const float w = __shfl_sync(0xffffffffu, share, b);
             if (at < p.d) {
                 float u[8];
-                load8(src + (long long)row * p.d + at, u);
+                load8(part(b0 + b) + (long long)row * p.d + at, u);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = o[e] * a + u[e] * w;
+                for (int e = 0; e < 8; ++e) o[e] = fmaf(u[e], w, o[e]);
             }
         }
-        const float r = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= r;
-        if (at < p.d) store8(static_cast<E *>(p.out) + row_offset(p, cur, cur.row_tile * p.rt + row) + at, o);
     }
+    const float r = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= r;
+    if (at < p.d) store8(static_cast<E *>(p.out) + row_offset(p, cur, cur.row_tile * p.rt + row) + at, o);
 }
 
 // What a call runs: rows and cached tokens a unit tile, blocks a SM.
@@ -709,7 +723,7 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     if ((rc = launch_attention(p, variant, kv->dtype, st))) return rc;
     // the join starts while the last blocks run; it waits for them before it reads their sums
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.grid, p.rt <= 32 ? p.rt / 4 : 8);
+    cfg.gridDim = dim3(p.grid, p.rt / (kThreads / 32));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

@@ -140,13 +140,25 @@ __device__ __forceinline__ int block_of(long long total, long long x, int grid) 
     return (int)(x < edge ? x / (each + 1) : more + (x - edge) / each);
 }
 
-// Whether drafted token i (row t of the mask) sees cached token c.
-__device__ __forceinline__ bool sees(const AttnParams &p, const Request &r, int i, int c) {
-    const int j = c - (r.len - r.n);
-    if (j < 0) return true;
-    if (c >= r.len) return false;
-    if (!p.mask) return j <= i;
-    return j < 64 * p.words && ((p.mask[(long long)(r.begin + i) * p.words + (j >> 6)] >> (j & 63)) & 1);
+// Which of the 32 cached tokens from c0 on drafted token i sees, one bit each.
+__device__ __forceinline__ uint32_t seen_word(const AttnParams &p, const Request &r, int i, int c0) {
+    const int j0 = c0 - (r.len - r.n);       // drafted index of bit 0
+    if (j0 <= -32) return ~0u;
+    if (j0 >= r.n) return 0u;
+    uint32_t bits;
+    if (!p.mask) {
+        const int count = i + 1 - j0;        // tokens up to i itself
+        bits = count >= 32 ? ~0u : count <= 0 ? 0u : (1u << count) - 1;
+    } else {
+        const unsigned long long *row = reinterpret_cast<const unsigned long long *>(p.mask) + (long long)(r.begin + i) * p.words;
+        const int at = max(j0, 0), q = at >> 6, sh = at & 63;
+        unsigned long long w = q < p.words ? __ldg(row + q) >> sh : 0ull;
+        if (sh > 32 && q + 1 < p.words) w |= __ldg(row + q + 1) << (64 - sh);
+        bits = (uint32_t)w;
+        if (j0 < 0) bits = (bits << -j0) | ((1u << -j0) - 1);      // the prefix
+    }
+    const int valid = r.n - j0;              // tokens up to the request's end
+    return valid < 32 ? bits & ((1u << valid) - 1) : bits;
 }
 
 // Page of cached token c, clamped into the cache (flagged); -1 beyond the request.

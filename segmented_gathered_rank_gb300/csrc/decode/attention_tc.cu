@@ -27,7 +27,7 @@ using namespace decode;
 using namespace tc;
 
 constexpr int kTile = 128;                 // cached tokens a tile, rows a stream
-constexpr int kThreadsTc = 13 * 32;        // streams 0 and 1, producers, MMA
+constexpr int kThreadsTc = 16 * 32;        // four warps each: streams 0 and 1, producers, MMA (one of them)
 constexpr int kProducer0 = 8, kMmaWarp = 12;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
@@ -162,10 +162,13 @@ __device__ void produce(const AttnParams &p, Cursor cur, int left, uint8_t *ring
     uint32_t seq = 0;
     while (left > 0) {
         const Segment seg = segment_at(cur, left);
-        for (int tile = seg.first; tile < seg.first + seg.tiles; ++tile) {
-            int pages[kPasses];
+        int pages[kPasses];
+        auto fetch = [&](int tile) {
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) pages[i] = page_of(p, cur.s, cur.r, tile * kTile + row0 + i * kRowsPerPass);
+        };
+        fetch(seg.first);
+        for (int tile = seg.first; tile < seg.first + seg.tiles; ++tile) {
             const bool masked = (tile + 1) * kTile > cur.r.len - cur.r.n;
             for (int which = 0; which < 2; ++which, ++seq) {
                 const uint32_t slot = seq % Sh::kSlots, use = seq / Sh::kSlots;
@@ -182,6 +185,7 @@ __device__ void produce(const AttnParams &p, Cursor cur, int left, uint8_t *ring
                     }
                     cp_async16(base + slot * Sh::kSlot + tile_off(row, chunk), src + off, real);
                 }
+                if (which && tile + 1 < seg.first + seg.tiles) fetch(tile + 1);
                 if (!(which && masked)) {
                     cp_arrive(&ctl->full[slot]);
                     continue;
@@ -352,12 +356,7 @@ __device__ void attend(const AttnParams &p, Cursor cur, int left, uint8_t *queri
                 if (warp_live) {
                     if (masked) {
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            see[b] = 0;
-                            if (live)
-                                for (int x = 0; x < 32; ++x)
-                                    if (sees(p, cur.r, token, c0 + b * 32 + x)) see[b] |= 1u << x;
-                        }
+                        for (int b = 0; b < 4; ++b) see[b] = live ? seen_word(p, cur.r, token, c0 + b * 32) : 0u;
                     }
                     float top = -INFINITY;
 #pragma unroll
@@ -570,13 +569,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attention_tc_kernel(const AttnP
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
+    // registers: 512 threads start with 128 each; 2 x 192 + 2 x 64 a warpgroup is the same sum
     if (warp < kProducer0) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n");
         attend<D, NQ>(p, cur, count, queries, ctl);
     } else if (warp < kMmaWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         produce<D, NQ>(p, cur, count, ring, ctl);
         asm volatile("cp.async.wait_all;\n" ::: "memory");
     } else {
-        if ((threadIdx.x & 31) == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+        if (threadIdx.x == kMmaWarp * 32) {
             issue<D, NQ>(p, cur, count, queries, ring, ctl);
             mma_commit(&ctl->drain);
             wait_phase(&ctl->drain, 0, nullptr);
