@@ -344,6 +344,7 @@ int lora_w4_matvec(int dtype, const void *x, int T, int h_in, const void *codes,
  * One layer's paged key/value cache, in caller-owned device memory.
  *   k, v    n_pages x n_kv_heads x page_size x head_dim elements of dtype, 16-byte
  *           aligned.  A cache slot is page * page_size + offset in the page.
+ *           n_pages * n_kv_heads * page_size is below 2^31.
  *   page_size  a power of two, 1..1024.   head_dim  a multiple of 8, 8..256.
  *   status  one device int32 that collects LORA_DEV_* bits of the calls on
  *           this cache (never cleared by them), or NULL.

@@ -6,10 +6,15 @@
 // mask row names (or j <= i without a mask).  K and V are read once, which is
 // the bound while few query rows share them (2 flops a byte and row).
 //
-// attention_mma_kernel (bf16): warp MMAs on units of 16 or 32 rows.
+// attention_mma_kernel (bf16): warp MMAs on units of 16 rows.
+// attention_tc_kernel (bf16, attention_tc.cu): tcgen05 on units of 128 or 256 rows.
 // attention_simt_kernel (fp32): the same list, fp32 multiply-adds.
 // attention_join_kernel: joins the units that were cut between blocks.
-#include "attention.cuh"
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+#include "kv_copy.cuh"
 
 namespace lora {
 namespace {
@@ -18,10 +23,6 @@ using namespace decode;
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool real) {
-    const int bytes = real ? 16 : 0;        // 0: the 16 bytes become zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
@@ -52,43 +53,295 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-constexpr int kThreads = 128;
-constexpr int kStages = 3;
+constexpr int kThreads = 128;      // the join kernel's, the fp32 kernel's, the consumers of the MMA kernel
+constexpr int kRows = 16;          // query rows a unit
 
-// D: head width padded to 64, 128 or 256; MT: 16-row tiles a unit.
-template <int D, int MT>
+// This thread's writes to a stage come before the copies that fill it next.
+__device__ __forceinline__ void fence_own_writes() { tc::fence_proxy_async(); }
+
+// D: head width padded to 64, 128 or 256.
+template <int D, bool TMA>
 struct MmaShape {
     static constexpr int kTile = D == 64 ? 128 : 64;       // cached tokens a stage
     static constexpr int kWarpKeys = kTile / 4;
-    static constexpr int kRowBytes = D * 2;
-    static constexpr int kHalf = kTile * kRowBytes;        // K, then V
+    static constexpr int kHalf = kTile * D * 2;            // K, then V
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kLanes = D / 8;                   // threads that copy one row
-    static constexpr int kRowsPerPass = kThreads / kLanes;
-    static constexpr int kPasses = kTile / kRowsPerPass;
+    static constexpr int kPerSm = TMA && D <= 128 ? 2 : 1;
+    static constexpr int kStages = D <= 128 && !TMA ? 6 : 3;
+    static constexpr int kThreadsAll = kThreads + (TMA ? 32 : 128);
     static constexpr size_t kSmem = (size_t)kStages * kStage + 1024;
 };
 
-// Byte offset of 16-byte chunk `chunk` of row `row`: the low three chunk bits
-// are XORed with the row, so that eight rows' chunks lie in different banks.
-template <int D>
-__device__ __forceinline__ uint32_t swz(int row, int chunk) {
-    return (uint32_t)(row * (D * 2) + ((chunk ^ (row & 7)) << 4));
+struct MmaControl {
+    uint64_t full[6], empty[6], join;
+    volatile int abort;
+    float row_max[4][16], row_sum[4][16];
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, MmaControl &ctl) {
+    for (int i = 0; i < 64; ++i)
+        if (tc::mbar_try_wait(bar, parity)) return true;
+    if (tc::wait_phase(bar, parity, &ctl.abort)) return true;
+    ctl.abort = 1;
+    return false;
+}
+// wait_bar for a whole warp: all lanes go on, or none.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, MmaControl &ctl) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, ctl));
 }
 
-// Four warps; each takes kWarpKeys of a stage's tokens for all rows of the
-// unit, with a maximum, sum and output of its own, joined in shared memory when
-// the block leaves the unit.  Copies run kStages - 1 tiles ahead, across units.
-template <int D, int MT>
-__global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) attention_mma_kernel(const AttnParams p) {
-    using Sh = MmaShape<D, MT>;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ ScanShared scan;
-    __shared__ float row_max[4][16], row_sum[4][16];
+// Four consumer warps; each takes kWarpKeys of a stage's tokens for all rows of
+// the unit, with a maximum, sum and output of its own (so a tile needs no exchange
+// between warps), joined in shared memory when the block leaves the unit.
+template <int D, bool TMA>
+__device__ void consume(const AttnParams &p, Cursor cur, int count, uint8_t *smem, MmaControl &ctl) {
+    using Sh = MmaShape<D, TMA>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g4 = lane >> 2, t4 = lane & 3;
+    const int g4 = lane >> 2, t4 = lane & 3, mi = lane >> 3, r8 = lane & 7;
     const uint32_t base = smem_addr(smem);
+    const int key0 = warp * Sh::kWarpKeys;
+    uint32_t qf[D / 16][4], join_phase = 0;
+    float o[D / 8][4], m[2], l[2];
+    bool fresh = true;
+    int start_tile = cur.tile;
+    auto all_warps = [&]() {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl.join);
+        return wait_warp(&ctl.join, join_phase++ & 1, ctl);
+    };
+    for (int it = 0; it < count; ++it) {
+        const int stage = it % Sh::kStages;
+        uint8_t *vs = smem + stage * Sh::kStage + Sh::kHalf;
+        const uint32_t ks_base = base + stage * Sh::kStage, vs_base = ks_base + Sh::kHalf;
+        const int rows = min(kRows, cur.r.n * p.group - cur.row_tile * kRows);
+        if (fresh) {        // a new unit: its queries, straight into MMA fragments
+            fresh = false;
+            start_tile = cur.tile;
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int row = hh * 8 + g4;
+                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
+                                           (row < rows ? row_offset(p, cur, cur.row_tile * kRows + row) : 0);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                    for (int kk = 0; kk < 2; ++kk) {
+                        const int col = ks * 16 + kk * 8 + t4 * 2;
+                        qf[ks][kk * 2 + hh] = row < rows && col < p.d ? *reinterpret_cast<const uint32_t *>(src + col) : 0u;
+                    }
+                m[hh] = -INFINITY;
+                l[hh] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+        }
+        if (!wait_warp(&ctl.full[stage], (it / Sh::kStages) & 1, ctl)) return;
+        const int c0 = cur.tile * Sh::kTile + key0;         // first cached token of this warp's keys
+        const int drafted = cur.r.len - cur.r.n - c0;       // the first of them that a mask rules
 
+        if (c0 < cur.r.len) {
+            float s[Sh::kWarpKeys / 8][4];
+#pragma unroll
+            for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                if (ks * 16 >= p.d) break;
+#pragma unroll
+                for (int kg = 0; kg < Sh::kWarpKeys / 16; ++kg) {
+                    uint32_t b[4];
+                    ldm4(b, ks_base + panel_off(Sh::kTile, key0 + kg * 16 + (mi >> 1) * 8 + r8, ks * 2 + (mi & 1)));
+                    mma16816(s[kg * 2], qf[ks], b[0], b[1]);
+                    mma16816(s[kg * 2 + 1], qf[ks], b[2], b[3]);
+                }
+            }
+            uint32_t see[2] = {0u, 0u};       // bit x: row hh * 8 + g4 sees the warp's token x
+            if (drafted < Sh::kWarpKeys) {
+                // scores that are not visible leave the softmax here, whatever they hold
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh)
+                    if (hh * 8 + g4 < rows) see[hh] = seen_word(p, cur.r, (cur.row_tile * kRows + hh * 8 + g4) / p.group, c0);
+#pragma unroll
+                for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!((see[e >> 1] >> (j * 8 + t4 * 2 + (e & 1))) & 1)) s[j][e] = -INFINITY;
+            }
+            // softmax of the warp's keys
+            float a[2];
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < Sh::kWarpKeys / 8; ++j) top = fmaxf(top, fmaxf(s[j][hh * 2], s[j][hh * 2 + 1]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float m2 = fmaxf(m[hh], top * p.scale_log2);
+                const float ref = m2 == -INFINITY ? 0.f : m2;        // nothing visible so far
+                a[hh] = exp2_fast(m[hh] - ref);
+                m[hh] = m2;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &x = s[j][hh * 2 + e];
+                        x = exp2_fast(fmaf(x, p.scale_log2, -ref));
+                        sum += x;
+                    }
+                l[hh] = l[hh] * a[hh] + sum;      // this thread's columns only, joined at the end
+            }
+            if (__any_sync(0xffffffffu, a[0] != 1.f || a[1] != 1.f)) {
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    o[j][0] *= a[0];
+                    o[j][1] *= a[0];
+                    o[j][2] *= a[1];
+                    o[j][3] *= a[1];
+                }
+            }
+            if (drafted < Sh::kWarpKeys) {
+                // values past the request, and drafted ones that are not finite, would enter the product times
+                // zero: the latter are added to the rows that see them, and both leave the tile (its rows are
+                // this warp's own)
+                const int first = max(0, drafted), end = cur.r.len - c0;
+                bool bad = false;
+                for (int x = lane; x < (Sh::kWarpKeys - first) * (D / 8); x += 32) {
+                    const int key = first + x / (D / 8), ch = x % (D / 8);
+                    uint4 *at = reinterpret_cast<uint4 *>(vs + panel_off(Sh::kTile, key0 + key, ch));
+                    const uint4 u = *at;
+                    if (key >= end) *at = make_uint4(0, 0, 0, 0);
+                    else bad |= ch * 8 < p.d && (non_finite2(u.x) || non_finite2(u.y) || non_finite2(u.z) || non_finite2(u.w));
+                }
+                __syncwarp();
+                if (__any_sync(0xffffffffu, bad)) {
+                    for (int x = first; x < min(end, Sh::kWarpKeys); ++x)
+#pragma unroll
+                        for (int j = 0; j < D / 8; ++j) {
+                            if (j * 8 >= p.d) break;
+                            const uint32_t w = *reinterpret_cast<const uint32_t *>(vs + panel_off(Sh::kTile, key0 + x, j) + t4 * 4);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t bits = e ? w & 0xffff0000u : w << 16;
+                                if ((bits & 0x7f800000u) != 0x7f800000u) continue;
+#pragma unroll
+                                for (int hh = 0; hh < 2; ++hh)
+                                    if ((see[hh] >> x) & 1) o[j][hh * 2 + e] += __uint_as_float(bits);
+                            }
+                        }
+                    __syncwarp();
+                    for (int x = lane; x < (Sh::kWarpKeys - first) * (D / 8); x += 32)
+                        make_finite(reinterpret_cast<uint4 *>(vs + panel_off(Sh::kTile, key0 + first + x / (D / 8), x % (D / 8))));
+                    __syncwarp();
+                }
+                fence_own_writes();
+            }
+#pragma unroll
+            for (int kg = 0; kg < Sh::kWarpKeys / 16; ++kg) {
+                const uint32_t pf[4] = {pack_bf16(s[kg * 2][0], s[kg * 2][1]), pack_bf16(s[kg * 2][2], s[kg * 2][3]),
+                                        pack_bf16(s[kg * 2 + 1][0], s[kg * 2 + 1][1]),
+                                        pack_bf16(s[kg * 2 + 1][2], s[kg * 2 + 1][3])};
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j) {
+                    if (j * 16 >= p.d) break;
+                    uint32_t b[4];
+                    ldm4t(b, vs_base + panel_off(Sh::kTile, key0 + kg * 16 + (mi & 1) * 8 + r8, j * 2 + (mi >> 1)));
+                    mma16816(o[j * 2], pf, b[0], b[1]);
+                    mma16816(o[j * 2 + 1], pf, b[2], b[3]);
+                }
+            }
+        }
+
+        const bool unit_ends = cur.tile + 1 == cur.r.tiles;
+        if (unit_ends || it + 1 == count) {
+            // join the four warps through the stage just used
+            const bool whole = unit_ends && start_tile == 0;
+            float *dst = partial_of(p, blockIdx.x, start_tile > 0 ? 0 : 1);
+            float *scratch = reinterpret_cast<float *>(smem + stage * Sh::kStage);     // [4][16][D]
+            if (!all_warps()) return;
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                const int row = hh * 8 + g4;
+                float sum = l[hh];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                if (t4 == 0) {
+                    ctl.row_max[warp][row] = m[hh];
+                    ctl.row_sum[warp][row] = sum;
+                }
+                if (row < rows) {
+#pragma unroll
+                    for (int j = 0; j < D / 8; ++j)
+                        *reinterpret_cast<float2 *>(scratch + (warp * 16 + row) * D + ((j ^ g4) * 8 + t4 * 2)) =
+                            make_float2(o[j][hh * 2], o[j][hh * 2 + 1]);
+                }
+            }
+            if (!all_warps()) return;
+            for (int x = tid; x < rows * (D / 4); x += kThreads) {
+                const int row = x / (D / 4), col = (x % (D / 4)) * 4;
+                if (col >= p.d) continue;
+                float top = ctl.row_max[0][row];
+#pragma unroll
+                for (int w = 1; w < 4; ++w) top = fmaxf(top, ctl.row_max[w][row]);
+                const float ref = top == -INFINITY ? 0.f : top;
+                float sum = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float share = exp2_fast(ctl.row_max[w][row] - ref);
+                    const float4 u = *reinterpret_cast<const float4 *>(scratch + (w * 16 + row) * D + (col ^ ((row & 7) * 8)));
+                    sum += share * ctl.row_sum[w][row];
+                    acc.x += share * u.x;
+                    acc.y += share * u.y;
+                    acc.z += share * u.z;
+                    acc.w += share * u.w;
+                }
+                if (whole) {
+                    const float r = sum == 0.f ? 0.f : 1.f / sum;      // a row that saw nothing: zeros
+                    uint2 w2;
+                    w2.x = pack_bf16(acc.x * r, acc.y * r);
+                    w2.y = pack_bf16(acc.z * r, acc.w * r);
+                    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
+                                               row_offset(p, cur, cur.row_tile * kRows + row) + col) = w2;
+                } else {
+                    *reinterpret_cast<float4 *>(dst + (long long)row * p.d + col) = acc;
+                    if (col == 0) {
+                        dst[(long long)kRows * p.d + row * 2] = top;
+                        dst[(long long)kRows * p.d + row * 2 + 1] = sum;
+                    }
+                }
+            }
+            fence_own_writes();
+            fresh = true;
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&ctl.empty[stage]);
+        if (!unit_ends) ++cur.tile;
+        else if (it + 1 < count) cur.next_unit(p);
+    }
+}
+
+template <int D, bool TMA>
+__global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, TMA>::kPerSm))
+    attention_mma_kernel(const __grid_constant__ KvMaps maps, const AttnParams p) {
+    using Sh = MmaShape<D, TMA>;
+    using Copy = std::conditional_t<TMA, TmaCopy<D, Sh::kTile>, ChunkCopy<D, Sh::kTile>>;
+    extern __shared__ uint8_t raw[];
+    __shared__ ScanShared scan;
+    __shared__ MmaControl ctl;
+    uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Sh::kStages; ++i) {
+            tc::mbar_init(&ctl.full[i], 2 * Copy::kArrivals);       // K, then V
+            tc::mbar_init(&ctl.empty[i], 4);
+        }
+        tc::mbar_init(&ctl.join, 4);
+        ctl.abort = 0;
+        tc::mbar_fence_init();
+    }
     Cursor cur;
     long long first = 0;
     const long long total = scan_list(p, scan, cur, blockIdx.x == 0, [&](long long n) {
@@ -97,301 +350,31 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 2 : 1) attention_mma_kern
     });
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (cur.s < 0) return;
-    int count = (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);     // tiles of this block
-    Cursor ahead = cur;
-    int to_load = count;
-
-    // copies: this thread's chunk of rows copy_row + i * kRowsPerPass
-    const int chunk = tid % Sh::kLanes, copy_row = tid / Sh::kLanes;
-    const bool copies = chunk * 8 < p.d, pads = chunk * 8 == p.d && (p.d & 8);
-    int pages[Sh::kPasses];
-    auto fetch_pages = [&]() {
-#pragma unroll
-        for (int i = 0; i < Sh::kPasses; ++i)
-            pages[i] = page_of(p, ahead.s, ahead.r, ahead.tile * Sh::kTile + copy_row + i * Sh::kRowsPerPass);
-    };
-    auto load = [&](int stage) {
-        if (to_load > 0) {
-            const int page_mask = (1 << p.page_shift) - 1;
-            const uint32_t dst = base + stage * Sh::kStage;
-#pragma unroll
-            for (int i = 0; i < Sh::kPasses; ++i) {
-                const int row = copy_row + i * Sh::kRowsPerPass, c = ahead.tile * Sh::kTile + row;
-                const bool real = c < ahead.r.len && copies;
-                long long off = 0;
-                if (real) {
-                    const int page = checked_page(p, pages[i]);
-                    off = ((((long long)page * p.n_kv + ahead.head) << p.page_shift) + (c & page_mask)) * p.d + chunk * 8;
-                }
-                if (copies || pads) {
-                    cp_async16(dst + swz<D>(row, chunk), static_cast<const __nv_bfloat16 *>(p.k) + off, real);
-                    cp_async16(dst + Sh::kHalf + swz<D>(row, chunk), static_cast<const __nv_bfloat16 *>(p.v) + off, real);
-                }
+    const int count = (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);
+    if (threadIdx.x < kThreads) {
+        consume<D, TMA>(p, cur, count, smem, ctl);
+    } else {
+        const int tid = threadIdx.x - kThreads;
+        const uint32_t base = smem_addr(smem);
+        Copy copy;
+        copy.fetch(p, cur, cur.tile, tid);
+        for (int it = 0; it < count; ++it) {
+            const int stage = it % Sh::kStages;
+            if (!wait_warp(&ctl.empty[stage], ((it / Sh::kStages) & 1) ^ 1, ctl)) break;
+            for (int which = 0; which < 2; ++which) {
+                copy.copy(p, which ? &maps.v : &maps.k, which ? p.v : p.k, base + stage * Sh::kStage + which * Sh::kHalf,
+                          &ctl.full[stage], tid);
+                if (!TMA) cp_arrive(&ctl.full[stage]);
             }
-            if (--to_load > 0) {
-                if (++ahead.tile == ahead.r.tiles) ahead.next_unit(p);
-                fetch_pages();
+            if (it + 1 < count) {
+                if (++cur.tile == cur.r.tiles) cur.next_unit(p);
+                copy.fetch(p, cur, cur.tile, tid);
             }
         }
-        cp_commit();
-    };
-    fetch_pages();
-    for (int s = 0; s < kStages - 1; ++s) load(s);
-
-    uint32_t qf[MT][D / 16][4];
-    float o[MT][D / 8][4], m[MT][2], l[MT][2];
-    bool fresh = true;
-    int start_tile = cur.tile;
-    for (int it = 0; it < count; ++it) {
-        if (fresh) {        // a new unit: its queries, straight into MMA fragments
-            fresh = false;
-            start_tile = cur.tile;
-            const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int row = mt * 16 + hh * 8 + g4;
-                    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
-                                               (row < rows ? row_offset(p, cur, cur.row_tile * p.rt + row) : 0);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk) {
-                            const int col = ks * 16 + kk * 8 + t4 * 2;
-                            qf[mt][ks][kk * 2 + hh] =
-                                row < rows && col < p.d ? *reinterpret_cast<const uint32_t *>(src + col) : 0u;
-                        }
-                    m[mt][hh] = -INFINITY;
-                    l[mt][hh] = 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
-            }
-        }
-        cp_wait<kStages - 2>();
-        __syncthreads();
-        load((it + kStages - 1) % kStages);
-        const uint32_t ks_base = base + (it % kStages) * Sh::kStage, vs_base = ks_base + Sh::kHalf;
-        const int key0 = warp * Sh::kWarpKeys;
-        const int c0 = cur.tile * Sh::kTile + key0;         // first cached token of this warp's keys
-        const bool masked = c0 + Sh::kWarpKeys > cur.r.len - cur.r.n;
-
-        if (c0 < cur.r.len) {
-            // scores
-            float s[MT][Sh::kWarpKeys / 8][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[mt][j][e] = 0.f;
-            const int mi = lane >> 3, r8 = lane & 7;
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                if (ks * 16 >= p.d) break;
-#pragma unroll
-                for (int kg = 0; kg < Sh::kWarpKeys / 16; ++kg) {
-                    uint32_t b[4];
-                    ldm4(b, ks_base + swz<D>(key0 + kg * 16 + (mi >> 1) * 8 + r8, ks * 2 + (mi & 1)));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma16816(s[mt][kg * 2], qf[mt][ks], b[0], b[1]);
-                        mma16816(s[mt][kg * 2 + 1], qf[mt][ks], b[2], b[3]);
-                    }
-                }
-            }
-            uint32_t see[MT][2] = {};       // bit x: row hh * 8 + g4 sees the warp's token x
-            if (masked) {
-                // scores that are not visible leave the softmax here, whatever they hold
-                const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const int row = mt * 16 + hh * 8 + g4;
-                        if (row >= rows) continue;
-                        const int i = (cur.row_tile * p.rt + row) / p.group;
-                        see[mt][hh] = seen_word(p, cur.r, i, c0);
-                    }
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int x = j * 8 + t4 * 2 + (e & 1);
-                            if (!((see[mt][e >> 1] >> x) & 1)) s[mt][j][e] = -INFINITY;
-                        }
-            }
-            // softmax of the warp's keys, then its share of the output
-            uint32_t pf[MT][Sh::kWarpKeys / 16][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < Sh::kWarpKeys / 8; ++j) top = fmaxf(top, fmaxf(s[mt][j][hh * 2], s[mt][j][hh * 2 + 1]));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const float m2 = fmaxf(m[mt][hh], top * p.scale_log2);
-                    const float ref = m2 == -INFINITY ? 0.f : m2;        // nothing visible so far
-                    const float a = exp2_fast(m[mt][hh] - ref);
-                    m[mt][hh] = m2;
-                    float sum = 0.f;
-#pragma unroll
-                    for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float &x = s[mt][j][hh * 2 + e];
-                            x = exp2_fast(fmaf(x, p.scale_log2, -ref));
-                            sum += x;
-                        }
-                    l[mt][hh] = l[mt][hh] * a + sum;      // this thread's columns only, joined at the end
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        o[mt][j][hh * 2] *= a;
-                        o[mt][j][hh * 2 + 1] *= a;
-                    }
-                }
-#pragma unroll
-                for (int kg = 0; kg < Sh::kWarpKeys / 16; ++kg) {
-                    pf[mt][kg][0] = pack_bf16(s[mt][kg * 2][0], s[mt][kg * 2][1]);
-                    pf[mt][kg][1] = pack_bf16(s[mt][kg * 2][2], s[mt][kg * 2][3]);
-                    pf[mt][kg][2] = pack_bf16(s[mt][kg * 2 + 1][0], s[mt][kg * 2 + 1][1]);
-                    pf[mt][kg][3] = pack_bf16(s[mt][kg * 2 + 1][2], s[mt][kg * 2 + 1][3]);
-                }
-            }
-            if (masked) {
-                // values that are not finite would enter the product times zero where they are masked: they are
-                // added to the rows that see them and taken out of the tile (its rows are this warp's own)
-                bool bad = false;
-                for (int x = lane; x < Sh::kWarpKeys * (D / 8); x += 32) {
-                    const int key = key0 + x / (D / 8), ch = x % (D / 8);
-                    if (ch * 8 >= p.d) continue;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(smem + (it % kStages) * Sh::kStage + Sh::kHalf + swz<D>(key, ch));
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        bad |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-                }
-                if (__any_sync(0xffffffffu, bad)) {
-                    for (int x = 0; x < Sh::kWarpKeys; ++x)
-#pragma unroll
-                        for (int j = 0; j < D / 8; ++j) {
-                            if (j * 8 >= p.d) break;
-                            const uint32_t w = *reinterpret_cast<const uint32_t *>(
-                                smem + (it % kStages) * Sh::kStage + Sh::kHalf + swz<D>(key0 + x, j) + t4 * 4);
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t bits = e ? w & 0xffff0000u : w << 16;
-                                if ((bits & 0x7f800000u) != 0x7f800000u) continue;
-#pragma unroll
-                                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                                    for (int hh = 0; hh < 2; ++hh)
-                                        if ((see[mt][hh] >> x) & 1) o[mt][j][hh * 2 + e] += __uint_as_float(bits);
-                            }
-                        }
-                    __syncwarp();
-                    for (int x = lane; x < Sh::kWarpKeys * D; x += 32) {
-                        const int key = key0 + x / D, col = x % D;
-                        uint16_t *v16 = reinterpret_cast<uint16_t *>(smem + (it % kStages) * Sh::kStage + Sh::kHalf +
-                                                                     swz<D>(key, col >> 3)) + (col & 7);
-                        if ((*v16 & 0x7f80) == 0x7f80) *v16 = 0;
-                    }
-                    __syncwarp();
-                }
-            }
-#pragma unroll
-            for (int kg = 0; kg < Sh::kWarpKeys / 16; ++kg)
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j) {
-                    if (j * 16 >= p.d) break;
-                    uint32_t b[4];
-                    ldm4t(b, vs_base + swz<D>(key0 + kg * 16 + (mi & 1) * 8 + r8, j * 2 + (mi >> 1)));
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma16816(o[mt][j * 2], pf[mt][kg], b[0], b[1]);
-                        mma16816(o[mt][j * 2 + 1], pf[mt][kg], b[2], b[3]);
-                    }
-                }
-        }
-
-        const bool unit_ends = cur.tile + 1 == cur.r.tiles;
-        if (unit_ends || it + 1 == count) {
-            // join the four warps; the stage just used is free until the next iteration's barrier
-            const bool whole = unit_ends && start_tile == 0;
-            const int rows = min(p.rt, cur.r.n * p.group - cur.row_tile * p.rt);
-            float *dst = partial_of(p, blockIdx.x, start_tile > 0 ? 0 : 1);
-            float *scratch = reinterpret_cast<float *>(smem + (it % kStages) * Sh::kStage);     // [4][16][D]
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                __syncthreads();
-#pragma unroll
-                for (int hh = 0; hh < 2; ++hh) {
-                    const int row = hh * 8 + g4;
-                    float sum = l[mt][hh];
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    if (t4 == 0) {
-                        row_max[warp][row] = m[mt][hh];
-                        row_sum[warp][row] = sum;
-                    }
-#pragma unroll
-                    for (int j = 0; j < D / 8; ++j)
-                        *reinterpret_cast<float2 *>(scratch + (warp * 16 + row) * D + ((j ^ g4) * 8 + t4 * 2)) =
-                            make_float2(o[mt][j][hh * 2], o[mt][j][hh * 2 + 1]);
-                }
-                __syncthreads();
-                for (int x = tid; x < 16 * (D / 4); x += kThreads) {
-                    const int row = x / (D / 4), col = (x % (D / 4)) * 4, ur = mt * 16 + row;
-                    if (ur >= rows || col >= p.d) continue;
-                    float top = row_max[0][row];
-#pragma unroll
-                    for (int w = 1; w < 4; ++w) top = fmaxf(top, row_max[w][row]);
-                    const float ref = top == -INFINITY ? 0.f : top;
-                    float sum = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const float a = exp2_fast(row_max[w][row] - ref);
-                        const float4 u =
-                            *reinterpret_cast<const float4 *>(scratch + (w * 16 + row) * D + (col ^ ((row & 7) * 8)));
-                        sum += a * row_sum[w][row];
-                        acc.x += a * u.x;
-                        acc.y += a * u.y;
-                        acc.z += a * u.z;
-                        acc.w += a * u.w;
-                    }
-                    if (whole) {
-                        const float r = sum == 0.f ? 0.f : 1.f / sum;      // a row that saw nothing: zeros
-                        uint2 w2;
-                        w2.x = pack_bf16(acc.x * r, acc.y * r);
-                        w2.y = pack_bf16(acc.z * r, acc.w * r);
-                        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
-                                                   row_offset(p, cur, cur.row_tile * p.rt + ur) + col) = w2;
-                    } else {
-                        *reinterpret_cast<float4 *>(dst + (long long)ur * p.d + col) = acc;
-                        if (col == 0) {
-                            dst[(long long)p.rt * p.d + ur * 2] = top;
-                            dst[(long long)p.rt * p.d + ur * 2 + 1] = sum;
-                        }
-                    }
-                }
-            }
-            fresh = true;
-        }
-        if (unit_ends) {
-            if (it + 1 < count) cur.next_unit(p);
-        } else {
-            ++cur.tile;
-        }
+        if (!TMA) cp_wait_all();
     }
-    cp_wait<0>();
+    __syncthreads();
+    if (threadIdx.x == 0 && ctl.abort) flag_status(p.status, LORA_DEV_WAIT_TIMEOUT);
 }
 
 // fp32: four warps of four rows each, over 32 cached tokens a stage.  A lane
@@ -619,47 +602,75 @@ struct Variant {
     int rt, tk, per_sm;
 };
 
-template <int D, int MT>
-Variant mma_variant() {
-    return {false, 16 * MT, MmaShape<D, MT>::kTile, D <= 128 ? 2 : 1};
-}
+constexpr int kTmaMinPage = 8;
 
-Variant variant_of(int dtype, int d, int group, int S, int T) {
-    if (dtype == LORA_F32) return {false, kSimtRows, kSimtTile, d <= 128 ? 2 : 1};
+Variant variant_of(const lora_kv_pages *kv, int group, int S, int T) {
+    const int d = kv->head_dim;
+    if (kv->dtype == LORA_F32) return {false, kSimtRows, kSimtTile, d <= 128 ? 2 : 1};
     const long long rows = (long long)T * group;       // against S: rows a request and kv head, on average
-    if ((d == 64 || d == 128) && rows > 32LL * S) return {true, rows > 128LL * S ? 256 : 128, 128, 1};
-    const bool wide = rows > 16LL * S;
-    if (d <= 64) return wide ? mma_variant<64, 2>() : mma_variant<64, 1>();
-    if (d <= 128) return wide ? mma_variant<128, 2>() : mma_variant<128, 1>();
-    return mma_variant<256, 1>();
+    if ((d == 64 || d == 128) && rows > (long long)kRows * S) return {true, rows > 128LL * S ? 256 : 128, 128, 1};
+    const bool tma = kv->page_size >= kTmaMinPage;
+    return {false, kRows, d <= 64 ? 128 : 64, tma && d <= 128 ? 2 : 1};
 }
 
-template <typename K>
-int launch_list(K kernel, size_t smem, const AttnParams &p, cudaStream_t st) {
-    if (smem_optin(reinterpret_cast<const void *>(kernel), smem)) return LORA_ERR_CUDA;
-    kernel<<<p.grid, kThreads, smem, st>>>(p);
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            ptr = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+// Boxes of 64 head elements (columns from head_dim on read as zeros) x `rows` cache rows.
+bool make_map(CUtensorMap *map, void *pages, const lora_kv_pages *kv, int rows) {
+    if (!encode_fn()) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)kv->head_dim, (cuuint64_t)kv->n_pages * kv->n_kv_heads * kv->page_size};
+    const cuuint64_t strides[1] = {(cuuint64_t)kv->head_dim * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)rows}, step[2] = {1, 1};
+    return encode_fn()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, pages, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool TMA>
+int launch_mma(const KvMaps &maps, const AttnParams &p, cudaStream_t st) {
+    using Sh = MmaShape<D, TMA>;
+    if (smem_optin(reinterpret_cast<const void *>(attention_mma_kernel<D, TMA>), Sh::kSmem)) return LORA_ERR_CUDA;
+    attention_mma_kernel<D, TMA><<<p.grid, Sh::kThreadsAll, Sh::kSmem, st>>>(maps, p);
     count_launch();
     return cuda_status(cudaGetLastError());
-}
-
-template <int D, int MT>
-int launch_mma(const AttnParams &p, cudaStream_t st) {
-    return launch_list(attention_mma_kernel<D, MT>, MmaShape<D, MT>::kSmem, p, st);
 }
 
 template <int D>
 int launch_simt(const AttnParams &p, cudaStream_t st) {
     const size_t smem = (size_t)(kSimtRows * D + 4 * kSimtTile * 4 + 4 * kSimtTile * (D + 4)) * 4;
-    return launch_list(attention_simt_kernel<D>, smem, p, st);
+    if (smem_optin(reinterpret_cast<const void *>(attention_simt_kernel<D>), smem)) return LORA_ERR_CUDA;
+    attention_simt_kernel<D><<<p.grid, kThreads, smem, st>>>(p);
+    count_launch();
+    return cuda_status(cudaGetLastError());
 }
 
-int launch_attention(AttnParams &p, const Variant &v, int dtype, cudaStream_t st) {
-    if (v.tc) return launch_attention_tc(p, st);
-    if (dtype == LORA_F32)
+int launch_attention(const lora_kv_pages *kv, const AttnParams &p, const Variant &v, cudaStream_t st) {
+    if (kv->dtype == LORA_F32)
         return p.d <= 64 ? launch_simt<64>(p, st) : p.d <= 128 ? launch_simt<128>(p, st) : launch_simt<256>(p, st);
-    if (p.d <= 64) return v.rt == 32 ? launch_mma<64, 2>(p, st) : launch_mma<64, 1>(p, st);
-    if (p.d <= 128) return v.rt == 32 ? launch_mma<128, 2>(p, st) : launch_mma<128, 1>(p, st);
-    return launch_mma<256, 1>(p, st);
+    KvMaps maps = {};
+    const bool tma = kv->page_size >= kTmaMinPage;
+    if (tma) {
+        const int rows = kv->page_size < v.tk ? kv->page_size : v.tk;
+        if (!make_map(&maps.k, kv->k, kv, rows) || !make_map(&maps.v, kv->v, kv, rows)) return LORA_ERR_CUDA;
+    }
+    if (v.tc) return launch_attention_tc(tma ? &maps : nullptr, p, st);
+    if (tma)
+        return p.d <= 64 ? launch_mma<64, true>(maps, p, st)
+               : p.d <= 128 ? launch_mma<128, true>(maps, p, st) : launch_mma<256, true>(maps, p, st);
+    return p.d <= 64 ? launch_mma<64, false>(maps, p, st)
+           : p.d <= 128 ? launch_mma<128, false>(maps, p, st) : launch_mma<256, false>(maps, p, st);
 }
 
 size_t partial_bytes(const Variant &v, int d) { return (size_t)num_sms() * v.per_sm * 2 * v.rt * (d + 2) * sizeof(float); }
@@ -672,7 +683,7 @@ using namespace lora;
 extern "C" size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T) {
     if (decode::check_kv(kv, n_q_heads) || n_q_heads < 1 || S < 0 || T < 0) return 0;
     if (S == 0) return 16;
-    return partial_bytes(variant_of(kv->dtype, kv->head_dim, n_q_heads / kv->n_kv_heads, S, T), kv->head_dim) + 16;
+    return partial_bytes(variant_of(kv, n_q_heads / kv->n_kv_heads, S, T), kv->head_dim) + 16;
 }
 
 extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, const int *seg_starts, int S,
@@ -715,12 +726,12 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     p.out = out;
     p.status = kv->status;
     cudaStream_t st = (cudaStream_t)stream;
-    const Variant variant = variant_of(kv->dtype, p.d, p.group, S, T);
+    const Variant variant = variant_of(kv, p.group, S, T);
     p.rt = variant.rt;
     p.tk = variant.tk;
     p.grid = num_sms() * variant.per_sm;
     p.partial = static_cast<float *>(workspace);
-    if ((rc = launch_attention(p, variant, kv->dtype, st))) return rc;
+    if ((rc = launch_attention(kv, p, variant, st))) return rc;
     // the join starts while the last blocks run; it waits for them before it reads their sums
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid, p.rt / (kThreads / 32));

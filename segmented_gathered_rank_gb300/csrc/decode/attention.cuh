@@ -188,8 +188,11 @@ __device__ __forceinline__ float *partial_of(const AttnParams &p, int block, int
     return p.partial + ((long long)block * 2 + slot) * p.rt * (p.d + 2);
 }
 
-// attention_tc.cu: p.rt (128 or 256 rows), p.tk (128), p.grid and p.partial set; p.d is 64 or 128.
-int launch_attention_tc(AttnParams &p, cudaStream_t st);
+struct KvMaps;
+
+// attention_tc.cu: p.rt (128 or 256 rows), p.tk (128), p.grid and p.partial set; p.d is 64
+// or 128.  maps: tensor maps with boxes of min(page, 128) rows, or NULL (pages below 8 tokens).
+int launch_attention_tc(const KvMaps *maps, const AttnParams &p, cudaStream_t st);
 
 }  // namespace decode
 }  // namespace lora

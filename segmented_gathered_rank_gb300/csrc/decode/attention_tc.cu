@@ -11,14 +11,15 @@
 //            take every key tile, so a tile in shared memory serves 256 rows;
 //   NQ = 1   units of up to 128 rows; stream w takes every other key tile, with
 //            a maximum, sum and output of its own, joined when the unit ends.
-// Four producer warps copy K and V tiles with cp.async (any page size; rows past
-// the request become zeros) into a ring of swizzled slots; one thread issues all
-// MMAs.  P overwrites the columns of S that it was computed from.
+// A producer warp (four for pages below 8 tokens) keeps a ring of K and V tiles
+// filled; one thread issues all MMAs.  P overwrites the columns of S that it was
+// computed from.
 //
 // A row keeps the maximum it last scaled by until a score passes it by 2^8
 // (sums stay far inside fp32), so the output is rescaled in a few tiles only.
-#include "attention.cuh"
-#include "tc_common.cuh"
+#include <type_traits>
+
+#include "kv_copy.cuh"
 
 namespace lora {
 namespace {
@@ -41,7 +42,7 @@ struct TcShape {
 };
 
 struct Control {
-    uint64_t full[10], empty[10], s_full[2], p_ready[2], o_full[2], q_ready[2], pair, drain;
+    uint64_t full[10], empty[10], s_full[2], p_ready[2], o_full[2], q_ready[2], landed, pair, drain;
     int bad[10];              // sequence number + 1 of a V tile that held values that are not finite
     int accumulate[2];        // the stream wrote its output itself before the unit's first product
     volatile int abort;
@@ -60,15 +61,6 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Control
 // wait_bar for a whole warp: all lanes go on, or none.
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Control *ctl) {
     return __all_sync(0xffffffffu, wait_bar(bar, parity, ctl));
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool real) {
-    const int bytes = real ? 16 : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// Arrives on `bar` once this thread's copies so far are complete.
-__device__ __forceinline__ void cp_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // D[tmem] (+)= A[tmem] . B[smem], A bf16 pairs in columns.
@@ -119,20 +111,6 @@ __device__ __forceinline__ uint64_t desc_rows_sw128(uint32_t smem_addr, uint32_t
 }
 constexpr uint32_t kTransposeB = 1u << 16;
 
-// Byte offset of 16-byte chunk `chunk` of row `row` in a tile: halves of 64
-// elements, rows of 128 bytes, chunks XORed with the row.
-__device__ __forceinline__ uint32_t tile_off(int row, int chunk) {
-    return (uint32_t)((chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
-}
-
-__device__ __forceinline__ bool has_non_finite(uint4 u) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    bool bad = false;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) bad |= (w[e] & 0x7f80u) == 0x7f80u || (w[e] & 0x7f800000u) == 0x7f800000u;
-    return bad;
-}
-
 // The part of the list that a block works through, one unit after another.
 struct Segment {
     int first, tiles;        // key tiles of the unit
@@ -151,63 +129,45 @@ __device__ __forceinline__ void advance(const AttnParams &p, Cursor &c, const Se
     if (left > 0 && c.tile == c.r.tiles) c.next_unit(p);
 }
 
-template <int D, int NQ>
-__device__ void produce(const AttnParams &p, Cursor cur, int left, uint8_t *ring, Control *ctl) {
+template <int D, bool TMA>
+__device__ void produce(const AttnParams &p, const KvMaps &maps, Cursor cur, int left, uint8_t *ring, Control *ctl) {
     using Sh = TcShape<D>;
-    constexpr int kLanes = D / 8, kRowsPerPass = 128 / kLanes, kPasses = kTile / kRowsPerPass;
+    using Copy = std::conditional_t<TMA, TmaCopy<D, kTile>, ChunkCopy<D, kTile>>;
     const int tid = threadIdx.x - kProducer0 * 32;
-    const int chunk = tid % kLanes, row0 = tid / kLanes;
-    const int page_mask = (1 << p.page_shift) - 1;
+    if (tid >= Copy::kThreads) return;
     const uint32_t base = smem_u32(ring);
-    uint32_t seq = 0;
+    Copy copy;
+    uint32_t seq = 0, landed = 0;
     while (left > 0) {
         const Segment seg = segment_at(cur, left);
-        int pages[kPasses];
-        auto fetch = [&](int tile) {
-#pragma unroll
-            for (int i = 0; i < kPasses; ++i) pages[i] = page_of(p, cur.s, cur.r, tile * kTile + row0 + i * kRowsPerPass);
-        };
-        fetch(seg.first);
+        copy.fetch(p, cur, seg.first, tid);
         for (int tile = seg.first; tile < seg.first + seg.tiles; ++tile) {
-            const bool masked = (tile + 1) * kTile > cur.r.len - cur.r.n;
+            const int drafted = max(0, cur.r.len - cur.r.n - tile * kTile);      // first row that a mask rules
             for (int which = 0; which < 2; ++which, ++seq) {
                 const uint32_t slot = seq % Sh::kSlots, use = seq / Sh::kSlots;
-                if (!wait_bar(&ctl->empty[slot], (use & 1) ^ 1, ctl)) return;
-                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(which ? p.v : p.k);
-#pragma unroll
-                for (int i = 0; i < kPasses; ++i) {
-                    const int row = row0 + i * kRowsPerPass, c = tile * kTile + row;
-                    const bool real = c < cur.r.len;
-                    long long off = 0;
-                    if (real) {
-                        const int page = checked_page(p, pages[i]);
-                        off = ((((long long)page * p.n_kv + cur.head) << p.page_shift) + (c & page_mask)) * D + chunk * 8;
-                    }
-                    cp_async16(base + slot * Sh::kSlot + tile_off(row, chunk), src + off, real);
-                }
-                if (which && tile + 1 < seg.first + seg.tiles) fetch(tile + 1);
-                if (!(which && masked)) {
-                    cp_arrive(&ctl->full[slot]);
+                if (TMA ? !wait_warp(&ctl->empty[slot], (use & 1) ^ 1, ctl) : !wait_bar(&ctl->empty[slot], (use & 1) ^ 1, ctl)) return;
+                const bool clean = which && drafted < kTile;     // before the products see the tile
+                copy.copy(p, which ? &maps.v : &maps.k, which ? p.v : p.k, base + slot * Sh::kSlot,
+                          TMA && clean ? &ctl->landed : &ctl->full[slot], tid);
+                if (which && tile + 1 < seg.first + seg.tiles) copy.fetch(p, cur, tile + 1, tid);
+                if (!clean) {
+                    if (!TMA) cp_arrive(&ctl->full[slot]);
                     continue;
                 }
-                // a V tile with drafted tokens: a masked value that is not finite would enter the product times
-                // zero, so each thread takes such values out of the chunks it copied and says that it did
-                asm volatile("cp.async.wait_all;\n" ::: "memory");
-                for (int i = 0; i < kPasses; ++i) {
-                    uint4 *at = reinterpret_cast<uint4 *>(ring + slot * Sh::kSlot + tile_off(row0 + i * kRowsPerPass, chunk));
-                    const uint4 u = *at;
-                    if (!has_non_finite(u)) continue;
-                    uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
-                        if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
-                    }
-                    *at = make_uint4(w[0], w[1], w[2], w[3]);
-                    ctl->bad[slot] = (int)seq + 1;
+                uint8_t *at = ring + slot * Sh::kSlot;
+                if (TMA) {
+                    if (!wait_warp(&ctl->landed, landed++ & 1, ctl)) return;
+                } else {
+                    cp_wait_all();
                 }
+                if (copy.clean(p, at, drafted, cur.r.len - tile * kTile, tid)) ctl->bad[slot] = (int)seq + 1;
                 fence_proxy_async();
-                mbar_arrive(&ctl->full[slot]);
+                if (TMA) {
+                    __syncwarp();
+                    if (tid == 0) mbar_arrive(&ctl->full[slot]);
+                } else {
+                    mbar_arrive(&ctl->full[slot]);
+                }
             }
         }
         advance(p, cur, seg, left);
@@ -336,7 +296,7 @@ __device__ void attend(const AttnParams &p, Cursor cur, int left, uint8_t *queri
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + q_off);
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4 *>(my_q + tile_off(row, c)) = live ? src[c] : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(my_q + panel_off(kTile, row, c)) = live ? src[c] : make_uint4(0, 0, 0, 0);
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
@@ -426,7 +386,7 @@ __device__ void attend(const AttnParams &p, Cursor cur, int left, uint8_t *queri
 #pragma unroll
                                 for (int x = 0; x < 32; ++x) o[x] = 0.f;
                             }
-                            for (int x = 0; x < kTile; ++x) {
+                            for (int x = max(0, cur.r.len - cur.r.n - c0); x < kTile; ++x) {
                                 if (!live || !((see[x >> 5] >> (x & 31)) & 1)) continue;
                                 const int c = c0 + x;
                                 const int page = checked_page(p, page_of(p, cur.s, cur.r, c));
@@ -524,8 +484,9 @@ __device__ void attend(const AttnParams &p, Cursor cur, int left, uint8_t *queri
     }
 }
 
-template <int D, int NQ>
-__global__ void __launch_bounds__(kThreadsTc, 1) attention_tc_kernel(const AttnParams p) {
+template <int D, int NQ, bool TMA>
+__global__ void __launch_bounds__(kThreadsTc, 1)
+    attention_tc_kernel(const __grid_constant__ KvMaps maps, const AttnParams p) {
     using Sh = TcShape<D>;
     extern __shared__ uint8_t raw[];
     __shared__ ScanShared scan;
@@ -546,7 +507,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attention_tc_kernel(const AttnP
     const int count = (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kSlots; ++i) {
-            mbar_init(&ctl->full[i], 128);
+            mbar_init(&ctl->full[i], TMA ? 1 : 128);
             mbar_init(&ctl->empty[i], 1);
             ctl->bad[i] = 0;
         }
@@ -557,6 +518,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attention_tc_kernel(const AttnP
             mbar_init(&ctl->q_ready[w], 4);
             ctl->accumulate[w] = 0;
         }
+        mbar_init(&ctl->landed, 1);
         mbar_init(&ctl->pair, 8);
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
@@ -575,8 +537,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attention_tc_kernel(const AttnP
         attend<D, NQ>(p, cur, count, queries, ctl);
     } else if (warp < kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-        produce<D, NQ>(p, cur, count, ring, ctl);
-        asm volatile("cp.async.wait_all;\n" ::: "memory");
+        produce<D, TMA>(p, maps, cur, count, ring, ctl);
+        if (!TMA) cp_wait_all();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         if (threadIdx.x == kMmaWarp * 32) {
@@ -593,21 +555,28 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attention_tc_kernel(const AttnP
     if (warp == kMmaWarp) tmem_dealloc(ctl->tmem, kTmemCols);
 }
 
-template <int D, int NQ>
-int launch(AttnParams &p, cudaStream_t st) {
-    if (smem_optin(reinterpret_cast<const void *>(attention_tc_kernel<D, NQ>), TcShape<D>::kSmem)) return LORA_ERR_CUDA;
-    attention_tc_kernel<D, NQ><<<p.grid, kThreadsTc, TcShape<D>::kSmem, st>>>(p);
+template <int D, int NQ, bool TMA>
+int launch(const KvMaps &maps, const AttnParams &p, cudaStream_t st) {
+    if (smem_optin(reinterpret_cast<const void *>(attention_tc_kernel<D, NQ, TMA>), TcShape<D>::kSmem)) return LORA_ERR_CUDA;
+    attention_tc_kernel<D, NQ, TMA><<<p.grid, kThreadsTc, TcShape<D>::kSmem, st>>>(maps, p);
     count_launch();
     return cuda_status(cudaGetLastError());
+}
+
+template <int D>
+int launch(const KvMaps *maps, const AttnParams &p, cudaStream_t st) {
+    const bool two = p.rt == 256;
+    if (maps) return two ? launch<D, 2, true>(*maps, p, st) : launch<D, 1, true>(*maps, p, st);
+    const KvMaps none = {};
+    return two ? launch<D, 2, false>(none, p, st) : launch<D, 1, false>(none, p, st);
 }
 
 }  // namespace
 
 namespace decode {
 
-int launch_attention_tc(AttnParams &p, cudaStream_t st) {
-    if (p.d == 128) return p.rt == 256 ? launch<128, 2>(p, st) : launch<128, 1>(p, st);
-    return p.rt == 256 ? launch<64, 2>(p, st) : launch<64, 1>(p, st);
+int launch_attention_tc(const KvMaps *maps, const AttnParams &p, cudaStream_t st) {
+    return p.d == 128 ? launch<128>(maps, p, st) : launch<64>(maps, p, st);
 }
 
 }  // namespace decode

@@ -18,6 +18,7 @@ inline int check_kv(const lora_kv_pages *kv, int n_q_heads) {
     if (kv->page_size < 1 || kv->page_size > kMaxPageSize || (kv->page_size & (kv->page_size - 1))) return LORA_ERR_SHAPE;
     if (kv->head_dim < 8 || kv->head_dim > kMaxHeadDim || kv->head_dim % 8) return LORA_ERR_SHAPE;
     if (n_q_heads % kv->n_kv_heads) return LORA_ERR_SHAPE;
+    if ((long long)kv->n_pages * kv->page_size > 0x7fffffffLL / kv->n_kv_heads) return LORA_ERR_SHAPE;   // rows are ints
     return LORA_OK;
 }
 
