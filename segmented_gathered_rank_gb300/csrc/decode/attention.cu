@@ -54,6 +54,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 constexpr int kThreads = 128;      // the join kernel's, the fp32 kernel's, the consumers of the MMA kernel
+constexpr int kJoinThreads = 256;
 constexpr int kRows = 16;          // query rows a unit
 
 // This thread's writes to a stage come before the copies that fill it next.
@@ -94,7 +95,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, MmaCon
 // the unit, with a maximum, sum and output of its own (so a tile needs no exchange
 // between warps), joined in shared memory when the block leaves the unit.
 template <int D, bool TMA>
-__device__ void consume(const AttnParams &p, Cursor cur, int count, uint8_t *smem, MmaControl &ctl) {
+__device__ void consume(const AttnParams &p, Cursor cur, int count, long long total, uint8_t *smem, MmaControl &ctl) {
     using Sh = MmaShape<D, TMA>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g4 = lane >> 2, t4 = lane & 3, mi = lane >> 3, r8 = lane & 7;
@@ -259,6 +260,7 @@ __device__ void consume(const AttnParams &p, Cursor cur, int count, uint8_t *sme
         if (unit_ends || it + 1 == count) {
             // join the four warps through the stage just used
             const bool whole = unit_ends && start_tile == 0;
+            if (tid == 0 && start_tile == 0 && !unit_ends) record_unit(p, cur, total);
             float *dst = partial_of(p, blockIdx.x, start_tile > 0 ? 0 : 1);
             float *scratch = reinterpret_cast<float *>(smem + stage * Sh::kStage);     // [4][16][D]
             if (!all_warps()) return;
@@ -328,7 +330,7 @@ template <int D, bool TMA>
 __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, TMA>::kPerSm))
     attention_mma_kernel(const __grid_constant__ KvMaps maps, const AttnParams p) {
     using Sh = MmaShape<D, TMA>;
-    using Copy = std::conditional_t<TMA, TmaCopy<D, Sh::kTile>, ChunkCopy<D, Sh::kTile>>;
+    using Copy = std::conditional_t<TMA, TmaCopy<D, Sh::kTile>, ChunkCopy<D, Sh::kTile, 128>>;
     extern __shared__ uint8_t raw[];
     __shared__ ScanShared scan;
     __shared__ MmaControl ctl;
@@ -348,11 +350,10 @@ __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, 
         first = block_begin(n, blockIdx.x, p.grid);
         return first < block_begin(n, blockIdx.x + 1, p.grid) ? first : -1;
     });
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    if (cur.s < 0) return;
-    const int count = (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);
+    const int count = start_block(p, cur, total, first);
+    if (count == 0) return;
     if (threadIdx.x < kThreads) {
-        consume<D, TMA>(p, cur, count, smem, ctl);
+        consume<D, TMA>(p, cur, count, total, smem, ctl);
     } else {
         const int tid = threadIdx.x - kThreads;
         const uint32_t base = smem_addr(smem);
@@ -398,9 +399,8 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
         first = block_begin(n, blockIdx.x, p.grid);
         return first < block_begin(n, blockIdx.x + 1, p.grid) ? first : -1;
     });
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    if (cur.s < 0) return;
-    const int count = (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);
+    const int count = start_block(p, cur, total, first);
+    if (count == 0) return;
     Cursor ahead = cur;
     int to_load = count;
     const int chunks = p.d / 4;
@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
         const bool unit_ends = cur.tile + 1 == cur.r.tiles;
         if (unit_ends || it + 1 == count) {
             const bool whole = unit_ends && start_tile == 0;
+            if (tid == 0 && start_tile == 0 && !unit_ends) record_unit(p, cur, total);
             float *dst = partial_of(p, blockIdx.x, start_tile > 0 ? 0 : 1);
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
@@ -538,62 +539,52 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
 }
 
 // Block (c, part): if a unit starts in block c's part of the list and goes on
-// after it, adds up the parts: c's slot 1, then slot 0 of each block after it
-// until the unit ends.  One warp a row.
+// after it (its record says so), adds up the parts: c's slot 1, then slot 0 of each
+// block after it until the unit ends.  One warp a row, a lane 8 columns.
 template <typename E>
-__global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttnParams p) {
-    __shared__ ScanShared scan;
-    Cursor cur;
-    const int c = blockIdx.x;
-    const long long total = scan_list(p, scan, cur, false, [&](long long n) {
-        const long long b = block_begin(n, c, p.grid), e = block_begin(n, c + 1, p.grid);
-        return b < e ? e - 1 : -1;
-    });
+__global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p) {
+    const int c = blockIdx.x, lane = threadIdx.x & 31, at = lane * 8;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    if (cur.s < 0 || cur.tile + 1 == cur.r.tiles) return;              // ends with this block
-    const long long begin = block_begin(total, c, p.grid), end = block_begin(total, c + 1, p.grid);
-    if (end - begin < cur.tile + 1) return;                            // started before this block
-    const long long last = end - 1 + (cur.r.tiles - 1 - cur.tile);     // the unit's last tile
-    const int c_last = block_of(total, last, p.grid);
-    const int lane = threadIdx.x & 31;
-    const int rows = min(p.rt, cur.r.n * p.group - cur.row_tile * p.rt);
-    const int row = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5), at = lane * 8, parts = c_last - c + 1;
-    if (row >= rows) return;
-    auto part = [&](int b) { return partial_of(p, c + b, b == 0 ? 1 : 0); };
-    // each part's maximum and sum, a lane a part, then the parts' shares
-    float m = -INFINITY, l = 0.f, o[8] = {};
-    for (int b0 = 0; b0 < parts; b0 += 32) {
-        float mb = -INFINITY, lb = 0.f;
-        if (b0 + lane < parts) {
-            const float *ml = part(b0 + lane) + (long long)p.rt * p.d + row * 2;
-            mb = ml[0];
-            lb = ml[1];
-        }
-        float top = mb;
+    const JoinRecord rec = p.records[c];
+    for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < rec.rows; row += gridDim.y * (kJoinThreads / 32)) {
+        auto part = [&](int b) { return partial_of(p, c + b, b == 0 ? 1 : 0); };
+        // each part's maximum and sum, a lane a part, then the parts' shares
+        float m = -INFINITY, l = 0.f, o[8] = {};
+        for (int b0 = 0; b0 < rec.parts; b0 += 32) {
+            float mb = -INFINITY, lb = 0.f;
+            if (b0 + lane < rec.parts) {
+                const float *ml = part(b0 + lane) + (long long)p.rt * p.d + row * 2;
+                mb = ml[0];
+                lb = ml[1];
+            }
+            float top = mb;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        top = fmaxf(m, top);
-        const float ref = top == -INFINITY ? 0.f : top, a = exp2f(m - ref), share = exp2f(mb - ref);
-        m = top;
-        l = l * a + warp_sum(lb * share);
+            for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            top = fmaxf(m, top);
+            const float ref = top == -INFINITY ? 0.f : top, a = exp2f(m - ref), share = exp2f(mb - ref);
+            m = top;
+            l = l * a + warp_sum(lb * share);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= a;
-        const int n = min(32, parts - b0);
+            for (int e = 0; e < 8; ++e) o[e] *= a;
+            const int n = min(32, rec.parts - b0);
 #pragma unroll 4
-        for (int b = 0; b < n; ++b) {
-            const float w = __shfl_sync(0xffffffffu, share, b);
-            if (at < p.d) {
-                float u[8];
-                load8(part(b0 + b) + (long long)row * p.d + at, u);
+            for (int b = 0; b < n; ++b) {
+                const float w = __shfl_sync(0xffffffffu, share, b);
+                if (at < p.d) {
+                    float u[8];
+                    load8(part(b0 + b) + (long long)row * p.d + at, u);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = fmaf(u[e], w, o[e]);
+                    for (int e = 0; e < 8; ++e) o[e] = fmaf(u[e], w, o[e]);
+                }
             }
         }
-    }
-    const float r = l == 0.f ? 0.f : 1.f / l;
+        const float r = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] *= r;
-    if (at < p.d) store8(static_cast<E *>(p.out) + row_offset(p, cur, cur.row_tile * p.rt + row) + at, o);
+        for (int e = 0; e < 8; ++e) o[e] *= r;
+        const int unit_row = rec.first_row + row, i = unit_row / p.group;
+        if (at < p.d)
+            store8(static_cast<E *>(p.out) + ((long long)(rec.begin + i) * p.n_q + rec.head * p.group + unit_row - i * p.group) * p.d + at, o);
+    }
 }
 
 // What a call runs: rows and cached tokens a unit tile, blocks a SM.
@@ -673,7 +664,9 @@ int launch_attention(const lora_kv_pages *kv, const AttnParams &p, const Variant
            : p.d <= 128 ? launch_mma<128, false>(maps, p, st) : launch_mma<256, false>(maps, p, st);
 }
 
-size_t partial_bytes(const Variant &v, int d) { return (size_t)num_sms() * v.per_sm * 2 * v.rt * (d + 2) * sizeof(float); }
+size_t partial_bytes(const Variant &v, int d) {
+    return (size_t)num_sms() * v.per_sm * (2 * v.rt * (d + 2) * sizeof(float) + sizeof(JoinRecord));
+}
 
 }  // namespace
 }  // namespace lora
@@ -730,12 +723,13 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     p.rt = variant.rt;
     p.tk = variant.tk;
     p.grid = num_sms() * variant.per_sm;
-    p.partial = static_cast<float *>(workspace);
+    p.records = static_cast<JoinRecord *>(workspace);
+    p.partial = reinterpret_cast<float *>(p.records + p.grid);
     if ((rc = launch_attention(kv, p, variant, st))) return rc;
     // the join starts while the last blocks run; it waits for them before it reads their sums
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.grid, p.rt / (kThreads / 32));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(p.grid, p.rt <= 16 ? 1 : p.rt / 16);       // two rows a warp
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -14,6 +14,11 @@
 namespace lora {
 namespace decode {
 
+// What the join reads of a block: the unit that starts in its part and goes on after it.
+struct __align__(16) JoinRecord {
+    int parts, rows, begin, head, first_row, unused[3];      // rows 0: nothing to join
+};
+
 struct AttnParams {
     const void *q, *k, *v;
     int n_q, n_kv, group, d, page_shift, n_pages;
@@ -24,6 +29,7 @@ struct AttnParams {
     float scale_log2;        // scale * log2(e): the softmax works in powers of two
     void *out;
     int *status;
+    JoinRecord *records;     // [grid]
     float *partial;          // [grid][2][rt][d + 2]: sums, then the rows' maximum and sum
     int rt, tk, grid;        // rows a unit, tokens a tile (a power of two), blocks
 };
@@ -138,6 +144,25 @@ __device__ __forceinline__ long long block_begin(long long total, int c, int gri
 __device__ __forceinline__ int block_of(long long total, long long x, int grid) {
     const long long each = total / grid, more = total - each * grid, edge = more * (each + 1);
     return (int)(x < edge ? x / (each + 1) : more + (x - edge) / each);
+}
+
+// Lets the join launch and returns the number of the block's tiles; `first`: its
+// first one in the list.
+__device__ __forceinline__ int start_block(const AttnParams &p, const Cursor &cur, long long total, long long first) {
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (threadIdx.x == 0) p.records[blockIdx.x] = JoinRecord{};
+    return cur.s < 0 ? 0 : (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);
+}
+// Thread 0, at the block's last tile, when its unit started in the block and goes on after it.
+__device__ __forceinline__ void record_unit(const AttnParams &p, const Cursor &cur, long long total) {
+    JoinRecord rec = {};
+    const long long last = block_begin(total, blockIdx.x + 1, p.grid) - 1 + (cur.r.tiles - 1 - cur.tile);
+    rec.parts = block_of(total, last, p.grid) - (int)blockIdx.x + 1;
+    rec.begin = cur.r.begin;
+    rec.head = cur.head;
+    rec.first_row = cur.row_tile * p.rt;
+    rec.rows = min(p.rt, cur.r.n * p.group - rec.first_row);
+    p.records[blockIdx.x] = rec;
 }
 
 // Which of the 32 cached tokens from c0 on drafted token i sees, one bit each.

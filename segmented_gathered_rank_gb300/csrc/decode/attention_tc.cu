@@ -28,8 +28,8 @@ using namespace decode;
 using namespace tc;
 
 constexpr int kTile = 128;                 // cached tokens a tile, rows a stream
-constexpr int kThreadsTc = 16 * 32;        // four warps each: streams 0 and 1, producers, MMA (one of them)
-constexpr int kProducer0 = 8, kMmaWarp = 12;
+constexpr int kThreadsTc = 12 * 32;        // four warps each: streams 0 and 1; copies and MMAs
+constexpr int kProducer0 = 8, kMmaWarp = 11;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
 
@@ -87,6 +87,51 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *v) {
         "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
         : "memory");
 }
+// 32 columns without a wait; tmem_arrived() below orders the reads of `r` after it.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, float *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]),
+          "=f"(r[17]), "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]), "=f"(r[24]),
+          "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_arrived(float *r) {
+    asm volatile(""
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15]),
+                   "+f"(r[16]), "+f"(r[17]), "+f"(r[18]), "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]),
+                   "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]), "+f"(r[28]), "+f"(r[29]),
+                   "+f"(r[30]), "+f"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+        "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 d, a, b;\nmov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -132,7 +177,7 @@ __device__ __forceinline__ void advance(const AttnParams &p, Cursor &c, const Se
 template <int D, bool TMA>
 __device__ void produce(const AttnParams &p, const KvMaps &maps, Cursor cur, int left, uint8_t *ring, Control *ctl) {
     using Sh = TcShape<D>;
-    using Copy = std::conditional_t<TMA, TmaCopy<D, kTile>, ChunkCopy<D, kTile>>;
+    using Copy = std::conditional_t<TMA, TmaCopy<D, kTile>, ChunkCopy<D, kTile, 64>>;
     const int tid = threadIdx.x - kProducer0 * 32;
     if (tid >= Copy::kThreads) return;
     const uint32_t base = smem_u32(ring);
@@ -270,7 +315,7 @@ __device__ void issue(const AttnParams &p, Cursor cur, int left, uint8_t *querie
 // One thread a row: its queries into shared memory, the softmax of its scores,
 // and at the end of the segment its output.
 template <int D, int NQ>
-__device__ void attend(const AttnParams &p, Cursor cur, int left, uint8_t *queries, Control *ctl) {
+__device__ void attend(const AttnParams &p, Cursor cur, int left, long long total, uint8_t *queries, Control *ctl) {
     using Sh = TcShape<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = warp >> 2;                                  // stream
@@ -318,20 +363,23 @@ __device__ void attend(const AttnParams &p, Cursor cur, int left, uint8_t *queri
 #pragma unroll
                         for (int b = 0; b < 4; ++b) see[b] = live ? seen_word(p, cur.r, token, c0 + b * 32) : 0u;
                     }
-                    float top = -INFINITY;
+                    float s[kTile];
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        float s[32];
-                        tmem_ld32(s_tmem + b * 32, s);
-                        if (masked) {
+                    for (int b = 0; b < 4; ++b) tmem_ld32_start(s_tmem + b * 32, s + b * 32);
+                    tmem_wait_ld();
 #pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if ((see[b] >> x) & 1) top = fmaxf(top, s[x]);
-                        } else {
+                    for (int b = 0; b < 4; ++b) tmem_arrived(s + b * 32);
+                    if (masked) {        // what is not visible leaves here, whatever it is
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) top = fmaxf(top, s[x]);
-                        }
+                        for (int x = 0; x < kTile; ++x)
+                            if (!((see[x >> 5] >> (x & 31)) & 1)) s[x] = -INFINITY;
                     }
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int x = 0; x < kTile; x += 8)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) tops[b] = max3(tops[b], s[x + 2 * b], s[x + 2 * b + 1]);
+                    float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     top *= p.scale_log2;
                     if (__any_sync(0xffffffffu, top > m + kRescaleLog2 || (m == -INFINITY && top > m))) {
                         const float m2 = fmaxf(m, top);
@@ -350,26 +398,22 @@ __device__ void attend(const AttnParams &p, Cursor cur, int left, uint8_t *queri
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m;
-                    float sum = 0.f;
+                    const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), ref2 = make_float2(-ref, -ref);
+                    float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
-                        float s[32];
                         uint32_t pk[16];
-                        tmem_ld32(s_tmem + b * 32, s);
-#pragma unroll
-                        for (int x = 0; x < 32; ++x) {
-                            float e = exp2_fast(fmaf(s[x], p.scale_log2, -ref));
-                            if (masked && !((see[b] >> x) & 1)) e = 0.f;
-                            s[x] = e;
-                            sum += e;
-                        }
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(s[2 * x], s[2 * x + 1]);
+                            float2 e = fma2(make_float2(s[b * 32 + 2 * x], s[b * 32 + 2 * x + 1]), scale2, ref2);
+                            e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+                            sums[x & 1] = add2(sums[x & 1], e);
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
                             pk[x] = *reinterpret_cast<const uint32_t *>(&h);
                         }
                         tmem_st16(s_tmem + b * 16, pk);
                     }
+                    const float sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
                     l += sum;
                     tmem_wait_st();
                 }
@@ -479,6 +523,11 @@ __device__ void attend(const AttnParams &p, Cursor cur, int left, uint8_t *queri
             if (joined && !both_streams()) return;
         }
         fence_before_sync();       // the reads of O come before the next unit's first product
+        if (threadIdx.x == 0 && seg.tiles == left && seg.first == 0 && !seg.whole) {
+            Cursor end = cur;
+            end.tile = seg.tiles - 1;
+            record_unit(p, end, total);
+        }
         seq0 += 2 * seg.tiles;
         advance(p, cur, seg, left);
     }
@@ -502,12 +551,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         first = block_begin(n, blockIdx.x, p.grid);
         return first < block_begin(n, blockIdx.x + 1, p.grid) ? first : -1;
     });
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    if (cur.s < 0) return;
-    const int count = (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);
+    const int count = start_block(p, cur, total, first);
+    if (count == 0) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kSlots; ++i) {
-            mbar_init(&ctl->full[i], TMA ? 1 : 128);
+            mbar_init(&ctl->full[i], TMA ? 1 : 64);
             mbar_init(&ctl->empty[i], 1);
             ctl->bad[i] = 0;
         }
@@ -531,16 +579,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    // registers: 512 threads start with 128 each; 2 x 192 + 2 x 64 a warpgroup is the same sum
+    // registers: three warpgroups start with 168 a thread; 2 x 208 + 88 is the same sum
     if (warp < kProducer0) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n");
-        attend<D, NQ>(p, cur, count, queries, ctl);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
+        attend<D, NQ>(p, cur, count, total, queries, ctl);
     } else if (warp < kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
         produce<D, TMA>(p, maps, cur, count, ring, ctl);
         if (!TMA) cp_wait_all();
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
         if (threadIdx.x == kMmaWarp * 32) {
             issue<D, NQ>(p, cur, count, queries, ring, ctl);
             mma_commit(&ctl->drain);

@@ -8,7 +8,7 @@
 //   tma = true   pages of 8 tokens or more (8 rows are one swizzle atom): one
 //                copy a page and panel, by one warp, a lane a page.  Rows past
 //                the request hold whatever the page holds.
-//   tma = false  smaller pages: 16-byte copies by 128 threads; rows past the
+//   tma = false  smaller pages: 16-byte copies by several warps; rows past the
 //                request become zeros.
 #pragma once
 
@@ -99,12 +99,12 @@ struct TmaCopy {
     }
 };
 
-// 128 threads' 16-byte copies.
-template <int D, int TILE>
+// 16-byte copies by THREADS threads.
+template <int D, int TILE, int THREADS>
 struct ChunkCopy {
-    static constexpr int kThreads = 128;
-    static constexpr int kArrivals = 128;
-    static constexpr int kLanes = D / 8, kRows = 128 / kLanes, kPasses = TILE / kRows;
+    static constexpr int kThreads = THREADS;
+    static constexpr int kArrivals = THREADS;
+    static constexpr int kLanes = D / 8, kRows = THREADS / kLanes, kPasses = TILE / kRows;
     int row[kPasses];                       // cache rows, -1 past the request
 
     __device__ __forceinline__ void fetch(const AttnParams &p, const Cursor &c, int tile, int tid) {
