@@ -95,7 +95,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, MmaCon
 // the unit, with a maximum, sum and output of its own (so a tile needs no exchange
 // between warps), joined in shared memory when the block leaves the unit.
 template <int D, bool TMA>
-__device__ void consume(const AttnParams &p, Cursor cur, int count, long long total, uint8_t *smem, MmaControl &ctl) {
+__device__ void consume(const AttnParams &p, Cursor cur, long long total, uint8_t *smem, MmaControl &ctl) {
     using Sh = MmaShape<D, TMA>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g4 = lane >> 2, t4 = lane & 3, mi = lane >> 3, r8 = lane & 7;
@@ -110,7 +110,7 @@ __device__ void consume(const AttnParams &p, Cursor cur, int count, long long to
         if (lane == 0) tc::mbar_arrive(&ctl.join);
         return wait_warp(&ctl.join, join_phase++ & 1, ctl);
     };
-    for (int it = 0; it < count; ++it) {
+    for (int it = 0; cur.left > 0; ++it) {
         const int stage = it % Sh::kStages;
         uint8_t *vs = smem + stage * Sh::kStage + Sh::kHalf;
         const uint32_t ks_base = base + stage * Sh::kStage, vs_base = ks_base + Sh::kHalf;
@@ -257,10 +257,10 @@ __device__ void consume(const AttnParams &p, Cursor cur, int count, long long to
         }
 
         const bool unit_ends = cur.tile + 1 == cur.r.tiles;
-        if (unit_ends || it + 1 == count) {
+        if (unit_ends || cur.left == 1) {
             // join the four warps through the stage just used
             const bool whole = unit_ends && start_tile == 0;
-            if (tid == 0 && start_tile == 0 && !unit_ends) record_unit(p, cur, total);
+            if (tid == 0 && start_tile == 0 && !unit_ends) record_unit(p, cur, cur.tile, total);
             float *dst = partial_of(p, blockIdx.x, start_tile > 0 ? 0 : 1);
             float *scratch = reinterpret_cast<float *>(smem + stage * Sh::kStage);     // [4][16][D]
             if (!all_warps()) return;
@@ -282,9 +282,9 @@ __device__ void consume(const AttnParams &p, Cursor cur, int count, long long to
                 }
             }
             if (!all_warps()) return;
-            for (int x = tid; x < rows * (D / 4); x += kThreads) {
-                const int row = x / (D / 4), col = (x % (D / 4)) * 4;
-                if (col >= p.d) continue;
+            for (int x = tid; x < 16 * (D / 4); x += kThreads) {
+                const int row = x & 15, col = (x >> 4) * 4;
+                if (row >= rows || col >= p.d) continue;
                 float top = ctl.row_max[0][row];
 #pragma unroll
                 for (int w = 1; w < 4; ++w) top = fmaxf(top, ctl.row_max[w][row]);
@@ -309,10 +309,10 @@ __device__ void consume(const AttnParams &p, Cursor cur, int count, long long to
                     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
                                                row_offset(p, cur, cur.row_tile * kRows + row) + col) = w2;
                 } else {
-                    *reinterpret_cast<float4 *>(dst + (long long)row * p.d + col) = acc;
+                    *reinterpret_cast<float4 *>(dst + partial_at(p, row, col)) = acc;
                     if (col == 0) {
-                        dst[(long long)kRows * p.d + row * 2] = top;
-                        dst[(long long)kRows * p.d + row * 2 + 1] = sum;
+                        dst[kRows * p.d + row * 2] = top;
+                        dst[kRows * p.d + row * 2 + 1] = sum;
                     }
                 }
             }
@@ -321,8 +321,7 @@ __device__ void consume(const AttnParams &p, Cursor cur, int count, long long to
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.empty[stage]);
-        if (!unit_ends) ++cur.tile;
-        else if (it + 1 < count) cur.next_unit(p);
+        cur.advance(p, 1);
     }
 }
 
@@ -345,21 +344,16 @@ __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, 
         tc::mbar_fence_init();
     }
     Cursor cur;
-    long long first = 0;
-    const long long total = scan_list(p, scan, cur, blockIdx.x == 0, [&](long long n) {
-        first = block_begin(n, blockIdx.x, p.grid);
-        return first < block_begin(n, blockIdx.x + 1, p.grid) ? first : -1;
-    });
-    const int count = start_block(p, cur, total, first);
-    if (count == 0) return;
+    const long long total = start_block(p, scan, cur);
+    if (cur.left <= 0) return;
     if (threadIdx.x < kThreads) {
-        consume<D, TMA>(p, cur, count, total, smem, ctl);
+        consume<D, TMA>(p, cur, total, smem, ctl);
     } else {
         const int tid = threadIdx.x - kThreads;
         const uint32_t base = smem_addr(smem);
         Copy copy;
         copy.fetch(p, cur, cur.tile, tid);
-        for (int it = 0; it < count; ++it) {
+        for (int it = 0; cur.left > 0; ++it) {
             const int stage = it % Sh::kStages;
             if (!wait_warp(&ctl.empty[stage], ((it / Sh::kStages) & 1) ^ 1, ctl)) break;
             for (int which = 0; which < 2; ++which) {
@@ -367,10 +361,8 @@ __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, 
                           &ctl.full[stage], tid);
                 if (!TMA) cp_arrive(&ctl.full[stage]);
             }
-            if (it + 1 < count) {
-                if (++cur.tile == cur.r.tiles) cur.next_unit(p);
-                copy.fetch(p, cur, cur.tile, tid);
-            }
+            cur.advance(p, 1);
+            if (cur.left > 0) copy.fetch(p, cur, cur.tile, tid);
         }
         if (!TMA) cp_wait_all();
     }
@@ -394,18 +386,12 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
     float *ring = ps + 4 * kSimtTile * 4;                   // [2][K, V][32][kLd]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Cursor cur;
-    long long first = 0;
-    const long long total = scan_list(p, scan, cur, blockIdx.x == 0, [&](long long n) {
-        first = block_begin(n, blockIdx.x, p.grid);
-        return first < block_begin(n, blockIdx.x + 1, p.grid) ? first : -1;
-    });
-    const int count = start_block(p, cur, total, first);
-    if (count == 0) return;
+    const long long total = start_block(p, scan, cur);
+    if (cur.left <= 0) return;
     Cursor ahead = cur;
-    int to_load = count;
     const int chunks = p.d / 4;
     auto load = [&](int stage) {
-        if (to_load > 0) {
+        if (ahead.left > 0) {
             const int page_mask = (1 << p.page_shift) - 1;
             float *dst = ring + stage * 2 * kSimtTile * kLd;
             for (int x = tid; x < kSimtTile * chunks; x += kThreads) {
@@ -419,7 +405,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                 cp_async16(smem_addr(dst + (kSimtTile + row) * kLd + ch * 4), static_cast<const float *>(p.v) + off,
                            c < ahead.r.len);
             }
-            if (--to_load > 0 && ++ahead.tile == ahead.r.tiles) ahead.next_unit(p);
+            ahead.advance(p, 1);
         }
         cp_commit();
     };
@@ -427,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
     float o[4][kCols], m[4], l[4];
     bool fresh = true;
     int start_tile = cur.tile;
-    for (int it = 0; it < count; ++it) {
+    for (int it = 0; cur.left > 0; ++it) {
         const int row0 = warp * 4, rows = min(p.rt, cur.r.n * p.group - cur.row_tile * p.rt);
         if (fresh) {
             fresh = false;
@@ -504,9 +490,9 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
         }
         __syncthreads();
         const bool unit_ends = cur.tile + 1 == cur.r.tiles;
-        if (unit_ends || it + 1 == count) {
+        if (unit_ends || cur.left == 1) {
             const bool whole = unit_ends && start_tile == 0;
-            if (tid == 0 && start_tile == 0 && !unit_ends) record_unit(p, cur, total);
+            if (tid == 0 && start_tile == 0 && !unit_ends) record_unit(p, cur, cur.tile, total);
             float *dst = partial_of(p, blockIdx.x, start_tile > 0 ? 0 : 1);
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
@@ -520,88 +506,74 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                     if (whole)
                         static_cast<float *>(p.out)[row_offset(p, cur, cur.row_tile * p.rt + ur) + col] = o[a][j] * r;
                     else
-                        dst[(long long)ur * p.d + col] = o[a][j];
+                        dst[partial_at(p, ur, col)] = o[a][j];
                 }
                 if (!whole && lane == 0) {
-                    dst[(long long)p.rt * p.d + ur * 2] = m[a];
-                    dst[(long long)p.rt * p.d + ur * 2 + 1] = l[a];
+                    dst[p.rt * p.d + ur * 2] = m[a];
+                    dst[p.rt * p.d + ur * 2 + 1] = l[a];
                 }
             }
             fresh = true;
         }
-        if (unit_ends) {
-            if (it + 1 < count) cur.next_unit(p);
-        } else {
-            ++cur.tile;
-        }
+        cur.advance(p, 1);
     }
     cp_wait<0>();
 }
 
-// Block (c, part): if a unit starts in block c's part of the list and goes on
-// after it (its record says so), adds up the parts: c's slot 1, then slot 0 of each
-// block after it until the unit ends.  One warp a row, a lane 8 columns.
+// Block (c, y): if a unit starts in block c's part of the list and goes on after it
+// (its record says so), adds up the parts: c's slot 1, then slot 0 of each block
+// after it until the unit ends.  A warp has 8 rows x 16 columns at a time: 128-byte
+// reads, 32-byte writes.
 template <typename E>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p) {
-    const int c = blockIdx.x, lane = threadIdx.x & 31, at = lane * 8;
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const JoinRecord rec = p.records[c];
-    for (int row = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); row < rec.rows; row += gridDim.y * (kJoinThreads / 32)) {
-        auto part = [&](int b) { return partial_of(p, c + b, b == 0 ? 1 : 0); };
-        // each part's maximum and sum, a lane a part, then the parts' shares
-        float m = -INFINITY, l = 0.f, o[8] = {};
-        for (int b0 = 0; b0 < rec.parts; b0 += 32) {
-            float mb = -INFINITY, lb = 0.f;
-            if (b0 + lane < rec.parts) {
-                const float *ml = part(b0 + lane) + (long long)p.rt * p.d + row * 2;
-                mb = ml[0];
-                lb = ml[1];
-            }
-            float top = mb;
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            top = fmaxf(m, top);
-            const float ref = top == -INFINITY ? 0.f : top, a = exp2f(m - ref), share = exp2f(mb - ref);
-            m = top;
-            l = l * a + warp_sum(lb * share);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] *= a;
-            const int n = min(32, rec.parts - b0);
+    const int across = (p.d + 15) >> 4, items = ((rec.rows + 7) >> 3) * across;
+    for (int x = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); x < items; x += gridDim.y * (kJoinThreads / 32)) {
+        const int row = (x / across) * 8 + (lane & 7), col = (x % across) * 16 + (lane >> 3) * 4;
+        if (row >= rec.rows || col >= p.d) continue;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-            for (int b = 0; b < n; ++b) {
-                const float w = __shfl_sync(0xffffffffu, share, b);
-                if (at < p.d) {
-                    float u[8];
-                    load8(part(b0 + b) + (long long)row * p.d + at, u);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[e] = fmaf(u[e], w, o[e]);
-                }
-            }
+        for (int b = 0; b < rec.parts; ++b) {
+            const float *src = partial_of(p, c + b, b == 0 ? 1 : 0);
+            const float2 ml = *reinterpret_cast<const float2 *>(src + p.rt * p.d + row * 2);
+            const float4 u = *reinterpret_cast<const float4 *>(src + partial_at(p, row, col));
+            const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
+            const float a = exp2f(m - ref), w = exp2f(ml.x - ref);
+            m = top;
+            l = l * a + ml.y * w;
+            o.x = o.x * a + u.x * w;
+            o.y = o.y * a + u.y * w;
+            o.z = o.z * a + u.z * w;
+            o.w = o.w * a + u.w * w;
         }
         const float r = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] *= r;
         const int unit_row = rec.first_row + row, i = unit_row / p.group;
-        if (at < p.d)
-            store8(static_cast<E *>(p.out) + ((long long)(rec.begin + i) * p.n_q + rec.head * p.group + unit_row - i * p.group) * p.d + at, o);
+        E *out = static_cast<E *>(p.out) + ((long long)(rec.begin + i) * p.n_q + rec.head * p.group + unit_row - i * p.group) * p.d + col;
+        if constexpr (sizeof(E) == 2)
+            *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16(o.x * r, o.y * r), pack_bf16(o.z * r, o.w * r));
+        else
+            *reinterpret_cast<float4 *>(out) = make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
     }
 }
 
 // What a call runs: rows and cached tokens a unit tile, blocks a SM.
 struct Variant {
     bool tc;
-    int rt, tk, per_sm;
+    int rt, tk, per_sm, unit_cost;
 };
 
 constexpr int kTmaMinPage = 8;
 
 Variant variant_of(const lora_kv_pages *kv, int group, int S, int T) {
     const int d = kv->head_dim;
-    if (kv->dtype == LORA_F32) return {false, kSimtRows, kSimtTile, d <= 128 ? 2 : 1};
+    if (kv->dtype == LORA_F32) return {false, kSimtRows, kSimtTile, d <= 128 ? 2 : 1, 1};
     const long long rows = (long long)T * group;       // against S: rows a request and kv head, on average
-    if ((d == 64 || d == 128) && rows > (long long)kRows * S) return {true, rows > 128LL * S ? 256 : 128, 128, 1};
+    if ((d == 64 || d == 128) && rows > (long long)kRows * S) return {true, rows > 128LL * S ? 256 : 128, 128, 1, 8};
     const bool tma = kv->page_size >= kTmaMinPage;
-    return {false, kRows, d <= 64 ? 128 : 64, tma && d <= 128 ? 2 : 1};
+    return {false, kRows, d <= 64 ? 128 : 64, tma && d <= 128 ? 2 : 1, 5};
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -722,6 +694,7 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     const Variant variant = variant_of(kv, p.group, S, T);
     p.rt = variant.rt;
     p.tk = variant.tk;
+    p.unit_cost = variant.unit_cost;
     p.grid = num_sms() * variant.per_sm;
     p.records = static_cast<JoinRecord *>(workspace);
     p.partial = reinterpret_cast<float *>(p.records + p.grid);

@@ -5,7 +5,9 @@
 // group), so a cached key and value are loaded once for the whole group.  A unit
 // is cut into tiles of `tk` cached tokens, and all tiles of all units, in
 // order (request, kv head, row tile, key tile), form one list that is cut into
-// `grid` equal parts: every block gets the same number whatever the lengths are, and a unit cut between blocks
+// `grid` equal parts.  A unit's first tile has `unit_cost` empty places before it,
+// for what starting and ending a unit takes (measured, in tiles): every block gets
+// the same work whatever the lengths are, and a unit cut between blocks
 // is joined afterwards from the blocks' partial sums.
 #pragma once
 
@@ -30,13 +32,16 @@ struct AttnParams {
     void *out;
     int *status;
     JoinRecord *records;     // [grid]
-    float *partial;          // [grid][2][rt][d + 2]: sums, then the rows' maximum and sum
+    float *partial;          // [grid][2]: sums [d / 4][rt][4], then the rows' maximum and sum [rt][2]
     int rt, tk, grid;        // rows a unit, tokens a tile (a power of two), blocks
+    int unit_cost;
 };
 
 struct Request {
     int begin, n, len, tiles, row_tiles;   // tokens; drafted; cached; key tiles; row tiles
-    __device__ __forceinline__ long long work(int n_kv) const { return (long long)tiles * row_tiles * n_kv; }
+    __device__ __forceinline__ long long places(const AttnParams &p) const {
+        return (long long)(tiles + p.unit_cost) * row_tiles * p.n_kv;
+    }
 };
 
 // Request s with everything clamped into the arrays.  bad: LORA_DEV_* bits.
@@ -53,21 +58,30 @@ __device__ __forceinline__ Request request_of(const AttnParams &p, int s, int *b
     return r;
 }
 
-// One block's place in the list.  tile/tiles: key tile of the unit.
+// One block's place in the list: at key tile `tile` of a unit, with `left` places
+// to go (none or fewer: done).
 struct Cursor {
     Request r;
-    int s, head, row_tile, tile;
+    int s, head, row_tile, tile, left;
 
-    __device__ __forceinline__ void next_unit(const AttnParams &p) {
+    // Past `count` tiles of the unit.
+    __device__ __forceinline__ void advance(const AttnParams &p, int count) {
+        left -= count;
+        tile += count;
+        if (tile < r.tiles || left <= 0) return;
         tile = 0;
+        left -= p.unit_cost;
         if (++row_tile < r.row_tiles) return;
         row_tile = 0;
         if (++head < p.n_kv) return;
         head = 0;
         do {
-            if (++s >= p.S) return;        // only past the end of the list
+            if (++s >= p.S) {
+                left = 0;
+                return;
+            }
             r = request_of(p, s);
-        } while (r.work(p.n_kv) == 0);
+        } while (r.row_tiles == 0);
     }
 };
 
@@ -79,18 +93,28 @@ struct ScanShared {
     int request;
 };
 
-// Called by all of the block's first kScanThreads threads (others only join the
-// barriers): the length of the list, and the cursor at its tile `at(total)`
-// (s = -1 when that is negative).  flags: report bad tables.
-template <typename At>
-__device__ __forceinline__ long long scan_list(const AttnParams &p, ScanShared &sh, Cursor &c, bool flags, At at) {
+// The first place of block c: total / grid places each, one more for the first total % grid.
+__device__ __forceinline__ long long block_begin(long long total, int c, int grid) {
+    const long long each = total / grid;
+    return each * c + min((long long)c, total - each * grid);
+}
+// The block that has place x.
+__device__ __forceinline__ int block_of(long long total, long long x, int grid) {
+    const long long each = total / grid, more = total - each * grid, edge = more * (each + 1);
+    return (int)(x < edge ? x / (each + 1) : more + (x - edge) / each);
+}
+
+// Called by every thread of the block: the block's first tile, and the length of
+// the list.  Lets the join launch; block 0 reports bad tables.
+__device__ __forceinline__ long long start_block(const AttnParams &p, ScanShared &sh, Cursor &c) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.S + kScanThreads - 1) / kScanThreads;
     const int s0 = tid < kScanThreads ? min(p.S, tid * per) : p.S, s1 = min(p.S, s0 + per);
+    const bool flags = blockIdx.x == 0;
     long long mine = 0;
     int bad = 0;
     for (int s = s0; s < s1; ++s) {
-        mine += request_of(p, s, &bad).work(p.n_kv);
+        mine += request_of(p, s, &bad).places(p);
         if (flags && (p.starts[s + 1] < p.starts[s] || (s == 0 && p.starts[0] != 0) || (s + 1 == p.S && p.starts[p.S] != p.T)))
             bad |= LORA_DEV_BAD_SEGMENTS;
     }
@@ -102,7 +126,10 @@ __device__ __forceinline__ long long scan_list(const AttnParams &p, ScanShared &
         if (lane >= o) upto += other;
     }
     if (lane == 31 && warp < kScanThreads / 32) sh.sums[warp] = upto;
-    if (tid == 0) sh.request = -1;
+    if (tid == 0) {
+        sh.request = -1;
+        p.records[blockIdx.x] = JoinRecord{};
+    }
     __syncthreads();
     long long total = 0, before = upto - mine;
 #pragma unroll
@@ -110,53 +137,41 @@ __device__ __forceinline__ long long scan_list(const AttnParams &p, ScanShared &
         if (w < warp) before += sh.sums[w];
         total += sh.sums[w];
     }
-    const long long pos = at(total);
+    const long long pos = block_begin(total, blockIdx.x, p.grid);
     if (pos >= before && pos < before + mine) {
-        long long left = pos - before;
+        long long rest = pos - before;
         for (int s = s0; s < s1; ++s) {
-            const long long w = request_of(p, s).work(p.n_kv);
-            if (left < w) {
+            const long long w = request_of(p, s).places(p);
+            if (rest < w) {
                 sh.request = s;
-                sh.residual = left;
+                sh.residual = rest;
                 break;
             }
-            left -= w;
+            rest -= w;
         }
     }
     __syncthreads();
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     c.s = sh.request;
+    c.left = 0;
     if (c.s >= 0) {
         c.r = request_of(p, c.s);
-        const long long unit = sh.residual / c.r.tiles;
-        c.tile = (int)(sh.residual % c.r.tiles);
-        c.row_tile = (int)(unit % c.r.row_tiles);
+        const int each = c.r.tiles + p.unit_cost;
+        const long long unit = sh.residual / each;
+        const int place = (int)(sh.residual - unit * each) - p.unit_cost;       // below 0: before the first tile
         c.head = (int)(unit / c.r.row_tiles);
+        c.row_tile = (int)(unit - (long long)c.head * c.r.row_tiles);
+        c.tile = max(place, 0);
+        c.left = (int)(block_begin(total, blockIdx.x + 1, p.grid) - pos) + min(place, 0);
     }
     return total;
 }
 
-// The first tile of block c: total / grid tiles each, one more for the first total % grid blocks.
-__device__ __forceinline__ long long block_begin(long long total, int c, int grid) {
-    const long long each = total / grid;
-    return each * c + min((long long)c, total - each * grid);
-}
-// The block that has tile x.
-__device__ __forceinline__ int block_of(long long total, long long x, int grid) {
-    const long long each = total / grid, more = total - each * grid, edge = more * (each + 1);
-    return (int)(x < edge ? x / (each + 1) : more + (x - edge) / each);
-}
-
-// Lets the join launch and returns the number of the block's tiles; `first`: its
-// first one in the list.
-__device__ __forceinline__ int start_block(const AttnParams &p, const Cursor &cur, long long total, long long first) {
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    if (threadIdx.x == 0) p.records[blockIdx.x] = JoinRecord{};
-    return cur.s < 0 ? 0 : (int)(block_begin(total, blockIdx.x + 1, p.grid) - first);
-}
-// Thread 0, at the block's last tile, when its unit started in the block and goes on after it.
-__device__ __forceinline__ void record_unit(const AttnParams &p, const Cursor &cur, long long total) {
+// Thread 0, where a unit started in the block and goes on after the block's last
+// tile, at which the cursor is.
+__device__ __forceinline__ void record_unit(const AttnParams &p, const Cursor &cur, int tile, long long total) {
     JoinRecord rec = {};
-    const long long last = block_begin(total, blockIdx.x + 1, p.grid) - 1 + (cur.r.tiles - 1 - cur.tile);
+    const long long last = block_begin(total, blockIdx.x + 1, p.grid) - 1 + (cur.r.tiles - 1 - tile);
     rec.parts = block_of(total, last, p.grid) - (int)blockIdx.x + 1;
     rec.begin = cur.r.begin;
     rec.head = cur.head;
@@ -207,6 +222,9 @@ __device__ __forceinline__ long long row_offset(const AttnParams &p, const Curso
     const int i = row / p.group, g = row - i * p.group;
     return ((long long)(c.r.begin + i) * p.n_q + c.head * p.group + g) * p.d;
 }
+
+// Place of element (row, col) in a block's sums: neighbouring rows' groups of four columns lie side by side.
+__device__ __forceinline__ int partial_at(const AttnParams &p, int row, int col) { return ((col >> 2) * p.rt + row) * 4 + (col & 3); }
 
 // Sums of block `block`: slot 0 when its part of the unit does not start it, else 1.
 __device__ __forceinline__ float *partial_of(const AttnParams &p, int block, int slot) {

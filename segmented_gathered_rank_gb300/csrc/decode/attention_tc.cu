@@ -63,19 +63,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Contro
     return __all_sync(0xffffffffu, wait_bar(bar, parity, ctl));
 }
 
-// D[tmem] (+)= A[tmem] . B[smem], A bf16 pairs in columns.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-    asm volatile(
-        "{\n"
-        ".reg .pred p;\n"
-        "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-        "}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -156,56 +143,61 @@ __device__ __forceinline__ uint64_t desc_rows_sw128(uint32_t smem_addr, uint32_t
 }
 constexpr uint32_t kTransposeB = 1u << 16;
 
-// The part of the list that a block works through, one unit after another.
+// The tiles of one unit that a block takes.
 struct Segment {
-    int first, tiles;        // key tiles of the unit
+    int first, tiles;
     bool whole;              // the block has the unit to itself
 };
-__device__ __forceinline__ Segment segment_at(const Cursor &c, int left) {
+__device__ __forceinline__ Segment segment_at(const Cursor &c) {
     Segment s;
     s.first = c.tile;
-    s.tiles = min(left, c.r.tiles - c.tile);
+    s.tiles = min(c.left, c.r.tiles - c.tile);
     s.whole = c.tile == 0 && s.tiles == c.r.tiles;
     return s;
 }
-__device__ __forceinline__ void advance(const AttnParams &p, Cursor &c, const Segment &s, int &left) {
-    left -= s.tiles;
-    c.tile += s.tiles;
-    if (left > 0 && c.tile == c.r.tiles) c.next_unit(p);
-}
 
+// Ring positions 2 t (keys) and 2 t + 1 (values) of the block's tile t.  Tensor
+// copies: one warp the keys, one the values; else both warps copy both.
 template <int D, bool TMA>
-__device__ void produce(const AttnParams &p, const KvMaps &maps, Cursor cur, int left, uint8_t *ring, Control *ctl) {
+__device__ void produce(const AttnParams &p, const KvMaps &maps, Cursor cur, uint8_t *ring, Control *ctl) {
     using Sh = TcShape<D>;
     using Copy = std::conditional_t<TMA, TmaCopy<D, kTile>, ChunkCopy<D, kTile, 64>>;
-    const int tid = threadIdx.x - kProducer0 * 32;
-    if (tid >= Copy::kThreads) return;
+    const int warp = (threadIdx.x >> 5) - kProducer0;
+    const int tid = TMA ? threadIdx.x & 31 : threadIdx.x - kProducer0 * 32;
+    if (warp >= 2) return;
     const uint32_t base = smem_u32(ring);
     Copy copy;
-    uint32_t seq = 0, landed = 0;
-    while (left > 0) {
-        const Segment seg = segment_at(cur, left);
-        copy.fetch(p, cur, seg.first, tid);
-        for (int tile = seg.first; tile < seg.first + seg.tiles; ++tile) {
+    uint32_t seq0 = 0, landed = 0;
+    copy.fetch(p, cur, cur.tile, tid);
+    while (cur.left > 0) {
+        const Segment seg = segment_at(cur);
+        Cursor after = cur;
+        after.advance(p, seg.tiles);
+        for (int t = 0; t < seg.tiles; ++t, seq0 += 2) {
+            const int tile = seg.first + t;
             const int drafted = max(0, cur.r.len - cur.r.n - tile * kTile);      // first row that a mask rules
-            for (int which = 0; which < 2; ++which, ++seq) {
-                const uint32_t slot = seq % Sh::kSlots, use = seq / Sh::kSlots;
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                if (TMA && which != warp) continue;
+                const uint32_t seq = seq0 + which, slot = seq % Sh::kSlots, use = seq / Sh::kSlots;
                 if (TMA ? !wait_warp(&ctl->empty[slot], (use & 1) ^ 1, ctl) : !wait_bar(&ctl->empty[slot], (use & 1) ^ 1, ctl)) return;
                 const bool clean = which && drafted < kTile;     // before the products see the tile
                 copy.copy(p, which ? &maps.v : &maps.k, which ? p.v : p.k, base + slot * Sh::kSlot,
                           TMA && clean ? &ctl->landed : &ctl->full[slot], tid);
-                if (which && tile + 1 < seg.first + seg.tiles) copy.fetch(p, cur, tile + 1, tid);
+                if (which || TMA) {
+                    if (t + 1 < seg.tiles) copy.fetch(p, cur, tile + 1, tid);
+                    else if (after.left > 0) copy.fetch(p, after, after.tile, tid);
+                }
                 if (!clean) {
                     if (!TMA) cp_arrive(&ctl->full[slot]);
                     continue;
                 }
-                uint8_t *at = ring + slot * Sh::kSlot;
                 if (TMA) {
                     if (!wait_warp(&ctl->landed, landed++ & 1, ctl)) return;
                 } else {
                     cp_wait_all();
                 }
-                if (copy.clean(p, at, drafted, cur.r.len - tile * kTile, tid)) ctl->bad[slot] = (int)seq + 1;
+                if (copy.clean(p, ring + slot * Sh::kSlot, drafted, cur.r.len - tile * kTile, tid)) ctl->bad[slot] = (int)seq + 1;
                 fence_proxy_async();
                 if (TMA) {
                     __syncwarp();
@@ -215,72 +207,89 @@ __device__ void produce(const AttnParams &p, const KvMaps &maps, Cursor cur, int
                 }
             }
         }
-        advance(p, cur, seg, left);
+        cur = after;
     }
 }
 
-template <int D, int NQ>
-__device__ void issue(const AttnParams &p, Cursor cur, int left, uint8_t *queries, uint8_t *ring, Control *ctl) {
+// One thread issues every MMA.  At 64 cycles a product of 128 x 128 x 16 its own
+// instructions are what can starve the tensor cores, so the loop over a segment
+// is a function of its own with little state: descriptors are 32-bit additions
+// (16-byte units) to a constant upper half.
+template <int D, int NQ, bool TMA>
+struct Issuer {
     using Sh = TcShape<D>;
-    const uint32_t tmem = ctl->tmem;
-    const uint32_t q_base = smem_u32(queries), r_base = smem_u32(ring);
-    constexpr uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
-    constexpr uint32_t idesc_o = idesc_bf16_f32(kTile, D) | kTransposeB;
-    uint32_t seq0 = 0, p_phase[2] = {0, 0}, q_phase[2] = {0, 0};
-    // tile t of the segment: K in ring position seq0 + 2 t, V right after it
-    auto slot_full = [&](uint32_t seq) {
+    static constexpr uint32_t kSwizzled = (1024u >> 4) | (1u << 14) | (2u << 29);      // descriptor bits 32..63
+    static constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kTile);
+    static constexpr uint32_t kIdescO = idesc_bf16_f32(kTile, D) | kTransposeB;
+
+    Control *ctl;
+    uint32_t tmem, q_lo, k_lo, v_lo;             // descriptors' lower halves of stream 0's queries and slot 0
+    uint32_t seq0, p_phase0, p_phase1;
+
+    __device__ __forceinline__ bool slot_full(uint32_t seq) {
         if (!wait_bar(&ctl->full[seq % Sh::kSlots], (seq / Sh::kSlots) & 1, ctl)) return false;
-        fence_proxy_async();          // the copies were ordinary writes; the MMAs read through the async proxy
+        if (!TMA) fence_proxy_async();          // ordinary writes; the MMAs read through the async proxy
         fence_after_sync();
         return true;
-    };
-    auto scores = [&](int w, uint32_t seq) {      // S_w = Q_w K^T
-        const uint32_t k = r_base + (seq % Sh::kSlots) * Sh::kSlot, q = q_base + w * Sh::kSlot;
+    }
+    __device__ __forceinline__ void release(uint32_t seq) { mma_commit(&ctl->empty[seq % Sh::kSlots]); }
+    __device__ __forceinline__ bool probabilities(int w) {
+        uint32_t &phase = w ? p_phase1 : p_phase0;
+        if (!wait_bar(&ctl->p_ready[w], phase & 1, ctl)) return false;
+        ++phase;
+        fence_after_sync();
+        return true;
+    }
+    __device__ __forceinline__ void scores(int w, uint32_t seq) {      // S_w = Q_w K^T
+        uint32_t q = q_lo + w * (Sh::kSlot / 16), k = k_lo + (seq % Sh::kSlots) * (Sh::kSlot / 16);
+        const uint32_t d = tmem + w * kTile;
+#pragma unroll 1
+        for (int panel = 0; panel < D / 64; ++panel, q += kTile * 128 / 16, k += kTile * 128 / 16) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * (kTile * 128) + (ks & 3) * 32;
-            mma_bf16(tmem + w * kTile, desc_kmajor_sw128(q + off), desc_kmajor_sw128(k + off), idesc_s, ks > 0);
+            for (int ks = 0; ks < 4; ++ks) {
+                asm volatile(
+                    "{\n.reg .pred p;\n.reg .b64 a, b;\nsetp.ne.b32 p, %5, 0;\nmov.b64 a, {%1, %3};\nmov.b64 b, {%2, %3};\n"
+                    "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+                    "r"(q + ks * 2), "r"(k + ks * 2), "n"(kSwizzled), "n"(kIdescS), "r"(ks > 0 || panel > 0 ? 1u : 0u)
+                    : "memory");
+            }
         }
         mma_commit(&ctl->s_full[w]);
-    };
-    auto output = [&](int w, uint32_t seq, bool accumulate) {      // O_w += P_w V
-        const uint32_t v = r_base + (seq % Sh::kSlots) * Sh::kSlot;
+    }
+    __device__ __forceinline__ void output(int w, uint32_t seq, bool accumulate) {      // O_w += P_w V
+        uint32_t v = v_lo + (seq % Sh::kSlots) * (Sh::kSlot / 16), pr = tmem + w * kTile, acc = accumulate ? 1u : 0u;
+        const uint32_t d = tmem + 2 * kTile + w * D;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half, v += 4 * 2048 / 16, pr += 32) {
 #pragma unroll
-        for (int ks = 0; ks < kTile / 16; ++ks)
-            mma_bf16_ts(tmem + 2 * kTile + w * D, tmem + w * kTile + ks * 8,
-                        desc_rows_sw128(v + ks * 2048, kTile * 128), idesc_o, accumulate || ks > 0);
-    };
-    auto release = [&](uint32_t seq) { mma_commit(&ctl->empty[seq % Sh::kSlots]); };
-    auto probabilities = [&](int w) {
-        if (!wait_bar(&ctl->p_ready[w], p_phase[w] & 1, ctl)) return false;
-        ++p_phase[w];
-        fence_after_sync();
-        return true;
-    };
-    while (left > 0) {
-        const Segment seg = segment_at(cur, left);
-        const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
-        const int streams = NQ == 2 ? (rows > kTile ? 2 : 1) : (seg.tiles > 1 ? 2 : 1);
-        for (int w = 0; w < streams; ++w) {
-            if (!wait_bar(&ctl->q_ready[w], q_phase[w] & 1, ctl)) return;
-            ++q_phase[w];
+            for (int ks = 0; ks < 4; ++ks) {
+                asm volatile(
+                    "{\n.reg .pred p;\n.reg .b64 b;\nsetp.ne.b32 p, %5, 0;\nmov.b64 b, {%2, %3};\n"
+                    "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+                    "r"(pr + ks * 8), "r"(v + ks * (2048 / 16)), "n"(kSwizzled), "n"(kIdescO), "r"(acc)
+                    : "memory");
+                acc = 1u;
+            }
         }
-        fence_after_sync();
+    }
+    // The tiles of a segment; tile t has its keys at ring position seq0 + 2 t, its values right after them.
+    __device__ __noinline__ bool segment(int tiles, int streams) {
         if (NQ == 2) {
-            if (!slot_full(seq0)) return;
+            if (!slot_full(seq0)) return false;
             for (int w = 0; w < streams; ++w) scores(w, seq0);
             release(seq0);
-            for (int t = 0; t < seg.tiles; ++t) {
+            for (int t = 0; t < tiles; ++t) {
                 const uint32_t v = seq0 + 2 * t + 1;
-                const bool more = t + 1 < seg.tiles;
+                const bool more = t + 1 < tiles;
+#pragma unroll 1
                 for (int w = 0; w < streams; ++w) {
-                    if (!probabilities(w)) return;
-                    if (w == 0 && !slot_full(v)) return;
+                    if (!probabilities(w)) return false;
+                    if (w == 0 && !slot_full(v)) return false;
                     output(w, v, t > 0 || ctl->accumulate[w]);
                     if (!more) mma_commit(&ctl->o_full[w]);
                     if (w == streams - 1) release(v);
                     if (more) {
-                        if (w == 0 && !slot_full(v + 1)) return;
+                        if (w == 0 && !slot_full(v + 1)) return false;
                         scores(w, v + 1);
                     }
                 }
@@ -288,18 +297,19 @@ __device__ void issue(const AttnParams &p, Cursor cur, int left, uint8_t *querie
             }
         } else {
             for (int w = 0; w < streams; ++w) {
-                if (!slot_full(seq0 + 2 * w)) return;
+                if (!slot_full(seq0 + 2 * w)) return false;
                 scores(w, seq0 + 2 * w);
                 release(seq0 + 2 * w);
             }
-            for (int t = 0; t < seg.tiles; ++t) {
+#pragma unroll 1
+            for (int t = 0; t < tiles; ++t) {
                 const int w = t & 1;
                 const uint32_t v = seq0 + 2 * t + 1;
-                if (!probabilities(w) || !slot_full(v)) return;
+                if (!probabilities(w) || !slot_full(v)) return false;
                 output(w, v, t > 1 || ctl->accumulate[w]);
                 release(v);
-                if (t + 2 < seg.tiles) {
-                    if (!slot_full(v + 3)) return;
+                if (t + 2 < tiles) {
+                    if (!slot_full(v + 3)) return false;
                     scores(w, v + 3);
                     release(v + 3);
                 } else {
@@ -307,15 +317,39 @@ __device__ void issue(const AttnParams &p, Cursor cur, int left, uint8_t *querie
                 }
             }
         }
-        seq0 += 2 * seg.tiles;
-        advance(p, cur, seg, left);
+        seq0 += 2 * tiles;
+        return true;
+    }
+};
+
+template <int D, int NQ, bool TMA>
+__device__ void issue(const AttnParams &p, Cursor cur, uint8_t *queries, uint8_t *ring, Control *ctl) {
+    Issuer<D, NQ, TMA> is;
+    is.ctl = ctl;
+    is.tmem = ctl->tmem;
+    is.q_lo = (uint32_t)desc_kmajor_sw128(smem_u32(queries));
+    is.k_lo = (uint32_t)desc_kmajor_sw128(smem_u32(ring));
+    is.v_lo = (uint32_t)desc_rows_sw128(smem_u32(ring), kTile * 128);
+    is.seq0 = is.p_phase0 = is.p_phase1 = 0;
+    uint32_t q_phase[2] = {0, 0};
+    while (cur.left > 0) {
+        const Segment seg = segment_at(cur);
+        const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
+        const int streams = NQ == 2 ? (rows > kTile ? 2 : 1) : (seg.tiles > 1 ? 2 : 1);
+        for (int w = 0; w < streams; ++w) {
+            if (!wait_bar(&ctl->q_ready[w], q_phase[w] & 1, ctl)) return;
+            ++q_phase[w];
+        }
+        fence_after_sync();
+        if (!is.segment(seg.tiles, streams)) return;
+        cur.advance(p, seg.tiles);
     }
 }
 
 // One thread a row: its queries into shared memory, the softmax of its scores,
 // and at the end of the segment its output.
 template <int D, int NQ>
-__device__ void attend(const AttnParams &p, Cursor cur, int left, long long total, uint8_t *queries, Control *ctl) {
+__device__ void attend(const AttnParams &p, Cursor cur, long long total, uint8_t *queries, Control *ctl) {
     using Sh = TcShape<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = warp >> 2;                                  // stream
@@ -329,19 +363,24 @@ __device__ void attend(const AttnParams &p, Cursor cur, int left, long long tota
         if (lane == 0) mbar_arrive(&ctl->pair);
         return wait_warp(&ctl->pair, pair_phase++ & 1, ctl);
     };
-    while (left > 0) {
-        const Segment seg = segment_at(cur, left);
+    while (cur.left > 0) {
+        const Segment seg = segment_at(cur);
         const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
         const int ur = row + (NQ == 2 ? w * kTile : 0);       // row of the unit
         const bool live = ur < rows, warp_live = ur - lane < rows;
         const bool active = NQ == 2 ? (w == 0 || rows > kTile) : (w == 0 || seg.tiles > 1);
         float m = -INFINITY, l = 0.f;
+        const long long my_off = live ? row_offset(p, cur, cur.row_tile * p.rt + ur) : -1;     // in q and out
         if (active) {
-            const long long q_off = live ? row_offset(p, cur, cur.row_tile * p.rt + ur) : 0;
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + q_off);
+            // the warp's 32 rows, D / 8 lanes a row
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4 *>(my_q + panel_off(kTile, row, c)) = live ? src[c] : make_uint4(0, 0, 0, 0);
+            for (int x = 0; x < D / 8; ++x) {
+                const int rr = x * (256 / D) + lane / (D / 8), c = lane % (D / 8);
+                const long long off = __shfl_sync(0xffffffffu, my_off, rr);
+                uint4 u = make_uint4(0, 0, 0, 0);
+                if (off >= 0) u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + off + c * 8);
+                *reinterpret_cast<uint4 *>(my_q + panel_off(kTile, (warp & 3) * 32 + rr, c)) = u;
+            }
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
@@ -478,8 +517,7 @@ __device__ void attend(const AttnParams &p, Cursor cur, int left, long long tota
         float *dst = partial_of(p, blockIdx.x, seg.first > 0 ? 0 : 1);
         const float r = l == 0.f ? 0.f : 1.f / l;            // a row that saw nothing: zeros
         if (writes && !seg.whole) {
-            dst[(long long)p.rt * D + ur * 2] = m;
-            dst[(long long)p.rt * D + ur * 2 + 1] = l;
+            *reinterpret_cast<float2 *>(dst + p.rt * D + ur * 2) = make_float2(m, l);
         }
         // stream 1 hands its output over through its queries' space, 64 columns at a time
         float *hand = reinterpret_cast<float *>(queries + Sh::kSlot);
@@ -504,32 +542,37 @@ __device__ void attend(const AttnParams &p, Cursor cur, int left, long long tota
 #pragma unroll
                         for (int x = 0; x < 32; ++x) o[x] = o[x] * scale + hand[(b * 32 + x) * kTile + row] * other;
                     }
-                    if (writes) {
-                        const int col = h * kHandCols + b * 32;
-                        if (seg.whole) {
+                    const int col = h * kHandCols + b * 32;
+                    if (seg.whole) {        // into the queries' place, as they lay
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) o[x] *= r;
-                            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row_offset(p, cur, cur.row_tile * p.rt + ur) + col;
+                        for (int x = 0; x < 32; ++x) o[x] *= r;
 #pragma unroll
-                            for (int x = 0; x < 32; x += 8) store8(out + x, o + x);
-                        } else {
-                            float *to = dst + (long long)ur * D + col;
+                        for (int x = 0; x < 32; x += 8)
+                            store8(reinterpret_cast<__nv_bfloat16 *>(my_q + panel_off(kTile, row, (col + x) >> 3)), o + x);
+                    } else if (writes) {
 #pragma unroll
-                            for (int x = 0; x < 32; x += 8) store8(to + x, o + x);
-                        }
+                        for (int x = 0; x < 32; x += 4)
+                            *reinterpret_cast<float4 *>(dst + partial_at(p, ur, col + x)) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
                     }
                 }
             }
             if (joined && !both_streams()) return;
         }
-        fence_before_sync();       // the reads of O come before the next unit's first product
-        if (threadIdx.x == 0 && seg.tiles == left && seg.first == 0 && !seg.whole) {
-            Cursor end = cur;
-            end.tile = seg.tiles - 1;
-            record_unit(p, end, total);
+        if (seg.whole && active && warp_live && (NQ == 2 || w == 0)) {
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x) {
+                const int rr = x * (256 / D) + lane / (D / 8), c = lane % (D / 8);
+                const long long off = __shfl_sync(0xffffffffu, my_off, rr);
+                const uint4 u = *reinterpret_cast<const uint4 *>(my_q + panel_off(kTile, (warp & 3) * 32 + rr, c));
+                if (off >= 0) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + off + c * 8) = u;
+            }
+            __syncwarp();
         }
+        fence_before_sync();       // the reads of O come before the next unit's first product
+        if (threadIdx.x == 0 && seg.first == 0 && !seg.whole) record_unit(p, cur, seg.tiles - 1, total);
         seq0 += 2 * seg.tiles;
-        advance(p, cur, seg, left);
+        cur.advance(p, seg.tiles);
     }
 }
 
@@ -546,13 +589,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     static_assert(sizeof(Control) <= Sh::kControl, "control block");
 
     Cursor cur;
-    long long first = 0;
-    const long long total = scan_list(p, scan, cur, blockIdx.x == 0, [&](long long n) {
-        first = block_begin(n, blockIdx.x, p.grid);
-        return first < block_begin(n, blockIdx.x + 1, p.grid) ? first : -1;
-    });
-    const int count = start_block(p, cur, total, first);
-    if (count == 0) return;
+    const long long total = start_block(p, scan, cur);
+    if (cur.left <= 0) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kSlots; ++i) {
             mbar_init(&ctl->full[i], TMA ? 1 : 64);
@@ -582,15 +620,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     // registers: three warpgroups start with 168 a thread; 2 x 208 + 88 is the same sum
     if (warp < kProducer0) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
-        attend<D, NQ>(p, cur, count, total, queries, ctl);
+        attend<D, NQ>(p, cur, total, queries, ctl);
     } else if (warp < kMmaWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-        produce<D, TMA>(p, maps, cur, count, ring, ctl);
+        produce<D, TMA>(p, maps, cur, ring, ctl);
         if (!TMA) cp_wait_all();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
         if (threadIdx.x == kMmaWarp * 32) {
-            issue<D, NQ>(p, cur, count, queries, ring, ctl);
+            issue<D, NQ, TMA>(p, cur, queries, ring, ctl);
             mma_commit(&ctl->drain);
             wait_phase(&ctl->drain, 0, nullptr);
         }

@@ -56,28 +56,29 @@ __device__ __forceinline__ bool make_finite(uint4 *at) {
     return true;
 }
 
-// One warp's tensor copies.  rows[]: first cache row of this lane's page of the next tile.
+// One warp's tensor copies.  fetch() starts the load of this lane's page id of a
+// tile, copy() uses it: fetched a tile ahead, its latency is hidden.
 template <int D, int TILE>
 struct TmaCopy {
     static constexpr int kThreads = 32;
     static constexpr int kArrivals = 1;     // on the tile's barrier
-    int row = -1;                           // -1: no page for this lane
+    int page, offset, head;                 // offset: in the page, -1 without a page
 
     __device__ __forceinline__ void fetch(const AttnParams &p, const Cursor &c, int tile, int lane) {
         const int per = min(1 << p.page_shift, TILE), at = tile * TILE + lane * per;
-        row = -1;
-        if (lane * per < TILE && at < c.r.len) {
-            const int page = checked_page(p, page_of(p, c.s, c.r, at));
-            row = ((page * p.n_kv + c.head) << p.page_shift) + (at & ((1 << p.page_shift) - 1));
-        }
+        const bool has = lane * per < TILE && at < c.r.len;
+        offset = has ? at & ((1 << p.page_shift) - 1) : -1;
+        page = has ? page_of(p, c.s, c.r, at) : 0;
+        head = c.head;
     }
     __device__ __forceinline__ void copy(const AttnParams &p, const CUtensorMap *map, const void *, uint32_t dst,
                                          uint64_t *bar, int lane) const {
         const int per = min(1 << p.page_shift, TILE), panels = (p.d + 63) >> 6;
-        const int pages = __popc(__ballot_sync(0xffffffffu, row >= 0));
+        const int pages = __popc(__ballot_sync(0xffffffffu, offset >= 0));
         if (lane == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)(pages * per * panels * 128));
         __syncwarp();
-        if (row < 0) return;
+        if (offset < 0) return;
+        const int row = ((checked_page(p, page) * p.n_kv + head) << p.page_shift) + offset;
         for (int h = 0; h < panels; ++h)
             asm volatile(
                 "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::
