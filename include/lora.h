@@ -408,7 +408,8 @@ size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, int n_q_heads
  *              on entry and exit.
  * Softmax statistics and sums are fp32; for a bf16 cache the probabilities
  * enter the second product as bf16.
- * Errors: LORA_ERR_ARG (includes ws_bytes too small), LORA_ERR_SHAPE.
+ * Errors: LORA_ERR_ARG (includes ws_bytes too small), LORA_ERR_SHAPE (also for
+ * tables so wide that the list of key tiles could pass 2^31).
  * Device-detected: LORA_DEV_BAD_SEGMENTS, LORA_DEV_BAD_LENGTH,
  * LORA_DEV_BAD_PAGE, LORA_DEV_WAIT_TIMEOUT; no access leaves the arrays.
  */

@@ -95,7 +95,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, MmaCon
 // the unit, with a maximum, sum and output of its own (so a tile needs no exchange
 // between warps), joined in shared memory when the block leaves the unit.
 template <int D, bool TMA>
-__device__ void consume(const AttnParams &p, Cursor cur, long long total, uint8_t *smem, MmaControl &ctl) {
+__device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t *smem, MmaControl &ctl) {
     using Sh = MmaShape<D, TMA>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g4 = lane >> 2, t4 = lane & 3, mi = lane >> 3, r8 = lane & 7;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, 
         tc::mbar_fence_init();
     }
     Cursor cur;
-    const long long total = start_block(p, scan, cur);
+    const uint32_t total = start_block(p, scan, cur);
     if (cur.left <= 0) return;
     if (threadIdx.x < kThreads) {
         consume<D, TMA>(p, cur, total, smem, ctl);
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
     float *ring = ps + 4 * kSimtTile * 4;                   // [2][K, V][32][kLd]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Cursor cur;
-    const long long total = start_block(p, scan, cur);
+    const uint32_t total = start_block(p, scan, cur);
     if (cur.left <= 0) return;
     Cursor ahead = cur;
     const int chunks = p.d / 4;
@@ -573,7 +573,7 @@ Variant variant_of(const lora_kv_pages *kv, int group, int S, int T) {
     const long long rows = (long long)T * group;       // against S: rows a request and kv head, on average
     if ((d == 64 || d == 128) && rows > (long long)kRows * S) return {true, rows > 128LL * S ? 256 : 128, 128, 1, 8};
     const bool tma = kv->page_size >= kTmaMinPage;
-    return {false, kRows, d <= 64 ? 128 : 64, tma && d <= 128 ? 2 : 1, 5};
+    return {false, kRows, d <= 64 ? 128 : 64, tma && d <= 128 ? 2 : 1, 4};
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -694,7 +694,10 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     const Variant variant = variant_of(kv, p.group, S, T);
     p.rt = variant.rt;
     p.tk = variant.tk;
+    p.tk_shift = decode::log2_of(variant.tk);
     p.unit_cost = variant.unit_cost;
+    const long long tiles = (long long)max_pages * kv->page_size / variant.tk + 1 + variant.unit_cost;
+    if (tiles * ((long long)T * p.group / variant.rt + S) > 0x7fffffffLL / p.n_kv) return LORA_ERR_SHAPE;
     p.grid = num_sms() * variant.per_sm;
     p.records = static_cast<JoinRecord *>(workspace);
     p.partial = reinterpret_cast<float *>(p.records + p.grid);

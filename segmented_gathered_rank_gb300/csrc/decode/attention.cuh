@@ -34,13 +34,13 @@ struct AttnParams {
     JoinRecord *records;     // [grid]
     float *partial;          // [grid][2]: sums [d / 4][rt][4], then the rows' maximum and sum [rt][2]
     int rt, tk, grid;        // rows a unit, tokens a tile (a power of two), blocks
-    int unit_cost;
+    int tk_shift, unit_cost;
 };
 
 struct Request {
     int begin, n, len, tiles, row_tiles;   // tokens; drafted; cached; key tiles; row tiles
-    __device__ __forceinline__ long long places(const AttnParams &p) const {
-        return (long long)(tiles + p.unit_cost) * row_tiles * p.n_kv;
+    __device__ __forceinline__ uint32_t places(const AttnParams &p) const {
+        return (uint32_t)(tiles + p.unit_cost) * row_tiles * p.n_kv;
     }
 };
 
@@ -53,8 +53,8 @@ __device__ __forceinline__ Request request_of(const AttnParams &p, int s, int *b
     r.n = min(max(e, r.begin), p.T) - r.begin;
     r.len = (int)min((long long)max(len, r.n), cap);
     if (bad && (len < r.n || len > cap)) *bad |= LORA_DEV_BAD_LENGTH;
-    r.tiles = (r.len + p.tk - 1) / p.tk;
-    r.row_tiles = (int)(((long long)r.n * p.group + p.rt - 1) / p.rt);
+    r.tiles = (r.len + p.tk - 1) >> p.tk_shift;
+    r.row_tiles = (int)(((uint32_t)r.n * p.group + p.rt - 1) / (uint32_t)p.rt);
     return r;
 }
 
@@ -88,41 +88,45 @@ struct Cursor {
 constexpr int kScanThreads = 128;
 
 struct ScanShared {
-    long long sums[kScanThreads / 32];
-    long long residual;
+    uint32_t sums[kScanThreads / 32];
+    uint32_t residual;
     int request;
+    Request r;
 };
 
-// The first place of block c: total / grid places each, one more for the first total % grid.
-__device__ __forceinline__ long long block_begin(long long total, int c, int grid) {
-    const long long each = total / grid;
-    return each * c + min((long long)c, total - each * grid);
+// The list has below 2^31 places (checked on the host).  The first place of block c:
+// total / grid places each, one more for the first total % grid.
+__device__ __forceinline__ uint32_t block_begin(uint32_t total, uint32_t c, uint32_t grid) {
+    const uint32_t each = total / grid;
+    return each * c + min(c, total - each * grid);
 }
 // The block that has place x.
-__device__ __forceinline__ int block_of(long long total, long long x, int grid) {
-    const long long each = total / grid, more = total - each * grid, edge = more * (each + 1);
+__device__ __forceinline__ int block_of(uint32_t total, uint32_t x, uint32_t grid) {
+    const uint32_t each = total / grid, more = total - each * grid, edge = more * (each + 1);
     return (int)(x < edge ? x / (each + 1) : more + (x - edge) / each);
 }
 
 // Called by every thread of the block: the block's first tile, and the length of
 // the list.  Lets the join launch; block 0 reports bad tables.
-__device__ __forceinline__ long long start_block(const AttnParams &p, ScanShared &sh, Cursor &c) {
+__device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared &sh, Cursor &c) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.S + kScanThreads - 1) / kScanThreads;
     const int s0 = tid < kScanThreads ? min(p.S, tid * per) : p.S, s1 = min(p.S, s0 + per);
     const bool flags = blockIdx.x == 0;
-    long long mine = 0;
+    uint32_t mine = 0;
     int bad = 0;
+    Request r = {};
     for (int s = s0; s < s1; ++s) {
-        mine += request_of(p, s, &bad).places(p);
+        r = request_of(p, s, &bad);
+        mine += r.places(p);
         if (flags && (p.starts[s + 1] < p.starts[s] || (s == 0 && p.starts[0] != 0) || (s + 1 == p.S && p.starts[p.S] != p.T)))
             bad |= LORA_DEV_BAD_SEGMENTS;
     }
     if (flags && bad) flag_status(p.status, bad);
-    long long upto = mine;
+    uint32_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long other = __shfl_up_sync(0xffffffffu, upto, o);
+        const uint32_t other = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += other;
     }
     if (lane == 31 && warp < kScanThreads / 32) sh.sums[warp] = upto;
@@ -131,20 +135,22 @@ __device__ __forceinline__ long long start_block(const AttnParams &p, ScanShared
         p.records[blockIdx.x] = JoinRecord{};
     }
     __syncthreads();
-    long long total = 0, before = upto - mine;
+    uint32_t total = 0, before = upto - mine;
 #pragma unroll
     for (int w = 0; w < kScanThreads / 32; ++w) {
         if (w < warp) before += sh.sums[w];
         total += sh.sums[w];
     }
-    const long long pos = block_begin(total, blockIdx.x, p.grid);
+    const uint32_t pos = block_begin(total, blockIdx.x, p.grid);
     if (pos >= before && pos < before + mine) {
-        long long rest = pos - before;
+        uint32_t rest = pos - before;
         for (int s = s0; s < s1; ++s) {
-            const long long w = request_of(p, s).places(p);
+            if (s1 - s0 > 1) r = request_of(p, s);
+            const uint32_t w = r.places(p);
             if (rest < w) {
                 sh.request = s;
                 sh.residual = rest;
+                sh.r = r;
                 break;
             }
             rest -= w;
@@ -155,12 +161,11 @@ __device__ __forceinline__ long long start_block(const AttnParams &p, ScanShared
     c.s = sh.request;
     c.left = 0;
     if (c.s >= 0) {
-        c.r = request_of(p, c.s);
-        const int each = c.r.tiles + p.unit_cost;
-        const long long unit = sh.residual / each;
+        c.r = sh.r;
+        const uint32_t each = c.r.tiles + p.unit_cost, unit = sh.residual / each;
         const int place = (int)(sh.residual - unit * each) - p.unit_cost;       // below 0: before the first tile
-        c.head = (int)(unit / c.r.row_tiles);
-        c.row_tile = (int)(unit - (long long)c.head * c.r.row_tiles);
+        c.head = unit / (uint32_t)c.r.row_tiles;
+        c.row_tile = unit - c.head * c.r.row_tiles;
         c.tile = max(place, 0);
         c.left = (int)(block_begin(total, blockIdx.x + 1, p.grid) - pos) + min(place, 0);
     }
@@ -169,9 +174,9 @@ __device__ __forceinline__ long long start_block(const AttnParams &p, ScanShared
 
 // Thread 0, where a unit started in the block and goes on after the block's last
 // tile, at which the cursor is.
-__device__ __forceinline__ void record_unit(const AttnParams &p, const Cursor &cur, int tile, long long total) {
+__device__ __forceinline__ void record_unit(const AttnParams &p, const Cursor &cur, int tile, uint32_t total) {
     JoinRecord rec = {};
-    const long long last = block_begin(total, blockIdx.x + 1, p.grid) - 1 + (cur.r.tiles - 1 - tile);
+    const uint32_t last = block_begin(total, blockIdx.x + 1, p.grid) - 1 + (cur.r.tiles - 1 - tile);
     rec.parts = block_of(total, last, p.grid) - (int)blockIdx.x + 1;
     rec.begin = cur.r.begin;
     rec.head = cur.head;

@@ -346,10 +346,24 @@ __device__ void issue(const AttnParams &p, Cursor cur, uint8_t *queries, uint8_t
     }
 }
 
+// 64 scores of the thread's row; those that it does not see become -infinity, whatever they are.
+__device__ __forceinline__ void load_scores(float *s, uint32_t taddr, bool masked, const uint32_t *see) {
+    tmem_ld32_start(taddr, s);
+    tmem_ld32_start(taddr + 32, s + 32);
+    tmem_wait_ld();
+    tmem_arrived(s);
+    tmem_arrived(s + 32);
+    if (masked) {
+#pragma unroll
+        for (int x = 0; x < 64; ++x)
+            if (!((see[x >> 5] >> (x & 31)) & 1)) s[x] = -INFINITY;
+    }
+}
+
 // One thread a row: its queries into shared memory, the softmax of its scores,
 // and at the end of the segment its output.
 template <int D, int NQ>
-__device__ void attend(const AttnParams &p, Cursor cur, long long total, uint8_t *queries, Control *ctl) {
+__device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t *queries, Control *ctl) {
     using Sh = TcShape<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = warp >> 2;                                  // stream
@@ -402,22 +416,17 @@ __device__ void attend(const AttnParams &p, Cursor cur, long long total, uint8_t
 #pragma unroll
                         for (int b = 0; b < 4; ++b) see[b] = live ? seen_word(p, cur.r, token, c0 + b * 32) : 0u;
                     }
-                    float s[kTile];
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) tmem_ld32_start(s_tmem + b * 32, s + b * 32);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) tmem_arrived(s + b * 32);
-                    if (masked) {        // what is not visible leaves here, whatever it is
-#pragma unroll
-                        for (int x = 0; x < kTile; ++x)
-                            if (!((see[x >> 5] >> (x & 31)) & 1)) s[x] = -INFINITY;
-                    }
+                    // the scores are read twice, 64 columns at a time: all of them would take most registers
                     float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int x = 0; x < kTile; x += 8)
+                    for (int h = 0; h < 2; ++h) {
+                        float s[64];
+                        load_scores(s, s_tmem + h * 64, masked, see + 2 * h);
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) tops[b] = max3(tops[b], s[x + 2 * b], s[x + 2 * b + 1]);
+                        for (int x = 0; x < 64; x += 8)
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) tops[b] = max3(tops[b], s[x + 2 * b], s[x + 2 * b + 1]);
+                    }
                     float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                     top *= p.scale_log2;
                     if (__any_sync(0xffffffffu, top > m + kRescaleLog2 || (m == -INFINITY && top > m))) {
@@ -440,17 +449,22 @@ __device__ void attend(const AttnParams &p, Cursor cur, long long total, uint8_t
                     const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), ref2 = make_float2(-ref, -ref);
                     float2 sums[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        uint32_t pk[16];
+                    for (int h = 0; h < 2; ++h) {
+                        float s[64];
+                        load_scores(s, s_tmem + h * 64, masked, see + 2 * h);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            float2 e = fma2(make_float2(s[b * 32 + 2 * x], s[b * 32 + 2 * x + 1]), scale2, ref2);
-                            e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
-                            sums[x & 1] = add2(sums[x & 1], e);
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(e.x, e.y);
-                            pk[x] = *reinterpret_cast<const uint32_t *>(&h);
+                        for (int b = 0; b < 2; ++b) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) {
+                                float2 e = fma2(make_float2(s[b * 32 + 2 * x], s[b * 32 + 2 * x + 1]), scale2, ref2);
+                                e = make_float2(exp2_fast(e.x), exp2_fast(e.y));
+                                sums[x & 1] = add2(sums[x & 1], e);
+                                const __nv_bfloat162 v = __floats2bfloat162_rn(e.x, e.y);
+                                pk[x] = *reinterpret_cast<const uint32_t *>(&v);
+                            }
+                            tmem_st16(s_tmem + h * 32 + b * 16, pk);
                         }
-                        tmem_st16(s_tmem + b * 16, pk);
                     }
                     const float sum = (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
                     l += sum;
@@ -588,9 +602,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const int warp = threadIdx.x >> 5;
     static_assert(sizeof(Control) <= Sh::kControl, "control block");
 
-    Cursor cur;
-    const long long total = start_block(p, scan, cur);
-    if (cur.left <= 0) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kSlots; ++i) {
             mbar_init(&ctl->full[i], TMA ? 1 : 64);
@@ -614,19 +625,21 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         tmem_alloc(&ctl->tmem, kTmemCols);
         tmem_relinquish();
     }
+    Cursor cur;
+    const uint32_t total = start_block(p, scan, cur);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
-    // registers: three warpgroups start with 168 a thread; 2 x 208 + 88 is the same sum
+    if (cur.left <= 0) {
+        if (warp == kMmaWarp) tmem_dealloc(ctl->tmem, kTmemCols);
+        return;
+    }
     if (warp < kProducer0) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
         attend<D, NQ>(p, cur, total, queries, ctl);
     } else if (warp < kMmaWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
         produce<D, TMA>(p, maps, cur, ring, ctl);
         if (!TMA) cp_wait_all();
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
         if (threadIdx.x == kMmaWarp * 32) {
             issue<D, NQ, TMA>(p, cur, queries, ring, ctl);
             mma_commit(&ctl->drain);
