@@ -1,0 +1,63 @@
+// Shared by the kernels for products with 4-bit weights.
+#pragma once
+
+#include "decode.cuh"
+
+namespace lora {
+namespace decode {
+
+struct W4Params {
+    const void *x;
+    const uint8_t *codes;
+    const __nv_bfloat16 *scales;
+    const uint8_t *zeros;        // NULL: 8 everywhere
+    void *y;
+    int T, h_in, h_out, groups;  // groups: h_in / group
+};
+
+// Eight codes of one word as four bf16 pairs (k, k + 4), k = 0..3, less the zero:
+// 0x4300 | code is 128 + code in bf16, and 128 + code - (128 + zero) is exact.  The
+// order of k inside a word is free as long as x follows it (pair_x below).
+__device__ __forceinline__ void code_pairs(uint32_t w, __nv_bfloat162 offset, uint32_t (&out)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t v = ((w >> (4 * k)) & 0x000f000fu) | 0x43004300u;
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), offset);
+        out[k] = *reinterpret_cast<const uint32_t *>(&d);
+    }
+}
+// 128 + zero, twice.
+__device__ __forceinline__ __nv_bfloat162 code_offset(uint32_t zero) {
+    const uint32_t v = (0x4300u | zero) * 0x10001u;
+    return *reinterpret_cast<const __nv_bfloat162 *>(&v);
+}
+// Eight bf16 of x (four words) in the order of code_pairs.
+__device__ __forceinline__ void pair_x(uint4 x, uint32_t (&out)[4]) {
+    out[0] = __byte_perm(x.x, x.z, 0x5410);
+    out[1] = __byte_perm(x.x, x.z, 0x7632);
+    out[2] = __byte_perm(x.y, x.w, 0x5410);
+    out[3] = __byte_perm(x.y, x.w, 0x7632);
+}
+// fp32 x as three bf16 parts, 24 bits in all, in the order of code_pairs.  A part that
+// is not finite has no remainder (infinity less itself would be NaN).
+__device__ __forceinline__ void split_x(const float (&x)[8], uint32_t (&hi)[4], uint32_t (&mid)[4], uint32_t (&lo)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float a = x[k], b = x[k + 4];
+        uint32_t *parts[3] = {&hi[k], &mid[k], &lo[k]};
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            *parts[i] = *reinterpret_cast<const uint32_t *>(&h);
+            const float2 f = __bfloat1622float2(h);
+            a = isfinite(f.x) ? a - f.x : 0.f;
+            b = isfinite(f.y) ? b - f.y : 0.f;
+        }
+    }
+}
+
+// w4_tc.cu: T of more than a few tokens.
+int launch_w4_tc(int dtype, const W4Params &p, int group, cudaStream_t st);
+
+}  // namespace decode
+}  // namespace lora
