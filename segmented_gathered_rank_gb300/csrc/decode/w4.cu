@@ -15,9 +15,10 @@ namespace {
 
 using namespace decode;
 
-constexpr int kWarps = 8;
+constexpr int kMaxWarps = 16;
 constexpr int kBlock = 128;        // weights of a row that a warp takes at a time
 constexpr int kDepth = 4;          // such blocks on their way from memory
+constexpr int kXBytes = 192 * 1024;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -28,11 +29,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// A block of 16 rows of W: warp w takes blocks w, w + 8, ... of kBlock columns for
-// all rows (rows lane/4 and lane/4 + 8 a thread), so a row's 64 bytes are one
-// request, x is read once a warp, and the warps' sums meet in shared memory.
-// Word j of a thread's four holds columns column(j) .. + 7 of the block: a word's
-// four threads (lane % 4) are in one group, whatever its size.
+// A thread block has `tiles` tiles of 16 rows of W, so that about one block a SM
+// covers all rows, and `slices` warps a tile: warp s of them takes the blocks of
+// kBlock columns s, s + slices, ...  Codes go from memory straight into registers,
+// kDepth blocks ahead; x lies in shared memory in the order of the MMA operands.
+// Word j of a thread's four (rows lane/4 and lane/4 + 8) holds columns column(j) ..
+// + 7 of the block: a word's four threads (lane % 4) are in one group, whatever its
+// size.
 template <int GROUP>
 __device__ __forceinline__ int column(int j, int t4) {
     return GROUP == 128 ? t4 * 32 + j * 8 : GROUP == 64 ? (j >> 1) * 64 + t4 * 16 + (j & 1) * 8 : j * 32 + t4 * 8;
@@ -79,128 +82,156 @@ __device__ __forceinline__ void load_block(const W4Params &p, const uint8_t *(&r
     }
 }
 
-template <typename E, int NT>
-struct BlockX {
-    uint4 v[NT][4][sizeof(E) / 2];
-};
-
-template <typename E, int GROUP, int NT>
-__device__ __forceinline__ void load_x(const W4Params &p, int block, int g4, int t4, BlockX<E, NT> &b) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int t = nt * 8 + g4;
-        const E *src = static_cast<const E *>(p.x) + (long long)t * p.h_in + block * kBlock;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int col = column<GROUP>(j, t4);
-            const bool in = t < p.T && block * kBlock + col < p.h_in;
-#pragma unroll
-            for (int h = 0; h < (int)sizeof(E) / 2; ++h)
-                b.v[nt][j][h] = in ? __ldg(reinterpret_cast<const uint4 *>(src + col) + h) : make_uint4(0, 0, 0, 0);
-        }
-    }
+// One thread's operand of 16 bytes: x of one token in one word's columns.  Place of
+// (block, word j, part, token tile nt, lane) in shared memory, 16-byte units.
+template <int NT, int PARTS>
+__device__ __forceinline__ int x_place(int block, int j, int part, int nt, int lane) {
+    return (((block * 4 + j) * PARTS + part) * NT + nt) * 32 + lane;
 }
 
+// x of the columns of blocks [first, first + blocks) into shared memory.
 template <typename E, int GROUP, int NT>
-__global__ void __launch_bounds__(kWarps * 32) w4_rows_kernel(const W4Params p) {
-    constexpr int kGroups = kBlock / GROUP;
-    __shared__ float sums[kWarps][NT * 8][17];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g4 = lane >> 2, t4 = lane & 3;
-    const int n0 = blockIdx.x * 16, blocks = (p.h_in + kBlock - 1) / kBlock;
-    const int n[2] = {min(n0 + g4, p.h_out - 1), min(n0 + g4 + 8, p.h_out - 1)};
-    const uint8_t *rows[2] = {p.codes + (long long)n[0] * (p.h_in / 2), p.codes + (long long)n[1] * (p.h_in / 2)};
-    float acc[NT][4] = {};
-    BlockWords ring[kDepth];
-    BlockX<E, NT> xs;
+__device__ __forceinline__ void stage_x(const W4Params &p, int first, int blocks, uint4 *xs) {
+    constexpr int kParts = sizeof(E) == 2 ? 1 : 3;
+    for (int i = threadIdx.x; i < blocks * 16 * p.T; i += blockDim.x) {
+        const int t = i / (blocks * 16), x = i - t * (blocks * 16), block = x >> 4, j = (x >> 2) & 3, t4 = x & 3;
+        const int k = (first + block) * kBlock + column<GROUP>(j, t4), lane = (t & 7) * 4 + t4;
+        const E *src = static_cast<const E *>(p.x) + (long long)t * p.h_in + k;
+        uint4 part[kParts];
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i)
-        if (warp + i * kWarps < blocks) load_block<GROUP>(p, rows, n, warp + i * kWarps, t4, ring[i]);
-    for (int base = warp; base < blocks; base += kDepth * kWarps) {
+        for (int q = 0; q < kParts; ++q) part[q] = make_uint4(0, 0, 0, 0);
+        if (k < p.h_in) {
+            if constexpr (sizeof(E) == 2) {
+                uint32_t o[4];
+                pair_x(__ldg(reinterpret_cast<const uint4 *>(src)), o);
+                part[0] = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                float f[8];
+                load8(src, f);
+                uint32_t o[3][4];
+                split_x(f, o[0], o[1], o[2]);
 #pragma unroll
-        for (int i = 0; i < kDepth; ++i) {
-            const int block = base + i * kWarps;
-            if (block >= blocks) break;
-            load_x<E, GROUP, NT>(p, block, g4, t4, xs);
-            const BlockWords cur = ring[i];
-            if (block + kDepth * kWarps < blocks) load_block<GROUP>(p, rows, n, block + kDepth * kWarps, t4, ring[i]);
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g) {
-                float c[NT][4] = {};
-                float scale[2];
-                __nv_bfloat162 offset[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    uint32_t z = cur.zero[r];
-                    scale[r] = cur.scale[r];
-                    if (kGroups > 1) {
-                        z = __shfl_sync(0xffffffffu, z, (lane & ~3) | g);
-                        scale[r] = __shfl_sync(0xffffffffu, scale[r], (lane & ~3) | g);
-                    }
-                    offset[r] = code_offset(z);
-                }
-#pragma unroll
-                for (int j = g * (4 / kGroups); j < (g + 1) * (4 / kGroups); ++j) {
-                    uint32_t a[2][4];
-                    code_pairs(cur.w[0][j], offset[0], a[0]);
-                    code_pairs(cur.w[1][j], offset[1], a[1]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (sizeof(E) == 2) {
-                            uint32_t b[4];
-                            pair_x(xs.v[nt][j][0], b);
-                            mma16816(c[nt], a[0][0], a[1][0], a[0][1], a[1][1], b[0], b[1]);
-                            mma16816(c[nt], a[0][2], a[1][2], a[0][3], a[1][3], b[2], b[3]);
-                        } else {
-                            const float f[8] = {__uint_as_float(xs.v[nt][j][0].x), __uint_as_float(xs.v[nt][j][0].y),
-                                                __uint_as_float(xs.v[nt][j][0].z), __uint_as_float(xs.v[nt][j][0].w),
-                                                __uint_as_float(xs.v[nt][j][1].x), __uint_as_float(xs.v[nt][j][1].y),
-                                                __uint_as_float(xs.v[nt][j][1].z), __uint_as_float(xs.v[nt][j][1].w)};
-                            uint32_t b[3][4];
-                            split_x(f, b[0], b[1], b[2]);
-#pragma unroll
-                            for (int part = 2; part >= 0; --part) {
-                                mma16816(c[nt], a[0][0], a[1][0], a[0][1], a[1][1], b[part][0], b[part][1]);
-                                mma16816(c[nt], a[0][2], a[1][2], a[0][3], a[1][3], b[part][2], b[part][3]);
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[nt][e] = fmaf(scale[e >> 1], c[nt][e], acc[nt][e]);
+                for (int q = 0; q < kParts; ++q) part[q] = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
             }
         }
-    }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sums[warp][nt * 8 + t4 * 2 + (e & 1)][g4 + (e >> 1) * 8] = acc[nt][e];
-    __syncthreads();
-    for (int x = threadIdx.x; x < NT * 8 * 16; x += kWarps * 32) {
-        const int t = x >> 4, r = x & 15;
-        if (t >= p.T || n0 + r >= p.h_out) continue;
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += sums[w][t][r];
-        E *dst = static_cast<E *>(p.y) + (long long)t * p.h_out + n0 + r;
-        if constexpr (sizeof(E) == 2) *dst = __float2bfloat16_rn(s);
-        else *dst = s;
+        for (int q = 0; q < kParts; ++q) xs[x_place<NT, kParts>(block, j, q, t >> 3, lane)] = part[q];
     }
 }
 
-template <typename E, int GROUP>
-void launch(const W4Params &p, cudaStream_t st) {
-    const unsigned grid = (p.h_out + 15) / 16;
-    if (p.T <= 8) w4_rows_kernel<E, GROUP, 1><<<grid, kWarps * 32, 0, st>>>(p);
-    else w4_rows_kernel<E, GROUP, 2><<<grid, kWarps * 32, 0, st>>>(p);
+// span: blocks of columns whose x fits in shared memory.
+template <typename E, int GROUP, int NT>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Params p, int tiles, int slices, int span) {
+    constexpr int kGroups = kBlock / GROUP, kParts = sizeof(E) == 2 ? 1 : 3;
+    extern __shared__ uint4 xs[];
+    float *sums = reinterpret_cast<float *>(xs);        // [warp][token][17], at the end
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g4 = lane >> 2, t4 = lane & 3;
+    const int slice = warp % slices, blocks = (p.h_in + kBlock - 1) / kBlock;
+    for (int n_first = blockIdx.x * tiles * 16; n_first < p.h_out; n_first += gridDim.x * tiles * 16) {
+        const int n0 = n_first + (warp / slices) * 16;
+        const int n[2] = {min(n0 + g4, p.h_out - 1), min(n0 + g4 + 8, p.h_out - 1)};
+        const uint8_t *rows[2] = {p.codes + (long long)n[0] * (p.h_in / 2), p.codes + (long long)n[1] * (p.h_in / 2)};
+        float acc[NT][4] = {};
+        BlockWords ring[kDepth];
+#pragma unroll
+        for (int i = 0; i < kDepth; ++i)
+            if (slice + i * slices < blocks) load_block<GROUP>(p, rows, n, slice + i * slices, t4, ring[i]);
+        for (int first = 0; first < blocks; first += span) {
+            const int end = min(blocks, first + span);
+            if (first > 0 || n_first > (int)blockIdx.x * tiles * 16) __syncthreads();
+            stage_x<E, GROUP, NT>(p, first, end - first, xs);
+            __syncthreads();
+            // span is a multiple of slices * kDepth: the ring keeps its places from one span to the next
+            for (int base = first + slice; base < end; base += kDepth * slices) {
+#pragma unroll
+                for (int i = 0; i < kDepth; ++i) {
+                    const int block = base + i * slices;
+                    if (block >= end) break;
+                    const BlockWords cur = ring[i];
+                    if (block + kDepth * slices < blocks) load_block<GROUP>(p, rows, n, block + kDepth * slices, t4, ring[i]);
+#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) {
+                        float c[NT][4] = {};
+                        float scale[2];
+                        __nv_bfloat162 offset[2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            uint32_t z = cur.zero[r];
+                            scale[r] = cur.scale[r];
+                            if (kGroups > 1) {
+                                z = __shfl_sync(0xffffffffu, z, (lane & ~3) | g);
+                                scale[r] = __shfl_sync(0xffffffffu, scale[r], (lane & ~3) | g);
+                            }
+                            offset[r] = code_offset(z);
+                        }
+#pragma unroll
+                        for (int j = g * (4 / kGroups); j < (g + 1) * (4 / kGroups); ++j) {
+                            uint32_t a[2][4];
+                            code_pairs(cur.w[0][j], offset[0], a[0]);
+                            code_pairs(cur.w[1][j], offset[1], a[1]);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int q = kParts - 1; q >= 0; --q) {        // the smallest part first
+                                    uint4 b = make_uint4(0, 0, 0, 0);
+                                    if (nt * 8 + g4 < p.T) b = xs[x_place<NT, kParts>(block - first, j, q, nt, lane)];
+                                    mma16816(c[nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+                                    mma16816(c[nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+                                }
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) acc[nt][e] = fmaf(scale[e >> 1], c[nt][e], acc[nt][e]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                sums[(warp * NT * 8 + nt * 8 + t4 * 2 + (e & 1)) * 17 + g4 + (e >> 1) * 8] = acc[nt][e];
+        __syncthreads();
+        for (int x = threadIdx.x; x < p.T * tiles * 16; x += blockDim.x) {
+            const int t = x / (tiles * 16), r = x - t * (tiles * 16), tile = r >> 4;
+            if (n_first + r >= p.h_out) continue;
+            float s = 0.f;
+            for (int w = 0; w < slices; ++w) s += sums[((tile * slices + w) * NT * 8 + t) * 17 + (r & 15)];
+            E *dst = static_cast<E *>(p.y) + (long long)t * p.h_out + n_first + r;
+            if constexpr (sizeof(E) == 2) *dst = __float2bfloat16_rn(s);
+            else *dst = s;
+        }
+    }
+}
+
+template <typename E, int GROUP, int NT>
+int launch(const W4Params &p, cudaStream_t st) {
+    const int sms = num_sms();
+    if (sms < 1) return LORA_ERR_CUDA;
+    // tiles of 16 rows a block: as few as let one block a SM cover all rows, at most 8
+    const int row_tiles = (p.h_out + 15) / 16, each = (row_tiles + sms - 1) / sms, tiles = each < 8 ? each : 8;
+    const int blocks = (p.h_in + kBlock - 1) / kBlock;
+    constexpr int kBlockBytes = 4 * (sizeof(E) == 2 ? 1 : 3) * NT * 512, kFit = kXBytes / kBlockBytes;
+    // all of x in shared memory at once, or spans of whole rounds of the ring
+    const int most = blocks <= kFit ? kMaxWarps : kFit / kDepth, slices = kMaxWarps / tiles < most ? kMaxWarps / tiles : most;
+    const int span = blocks <= kFit ? blocks : kFit / (slices * kDepth) * (slices * kDepth);
+    const size_t sums = (size_t)tiles * slices * NT * 8 * 17 * sizeof(float);
+    const size_t smem = (size_t)span * kBlockBytes > sums ? (size_t)span * kBlockBytes : sums;
+    const int need = (row_tiles + tiles - 1) / tiles, grid = need < sms ? need : sms;
+    if (smem_optin(reinterpret_cast<const void *>(w4_rows_kernel<E, GROUP, NT>), smem)) return LORA_ERR_CUDA;
+    w4_rows_kernel<E, GROUP, NT><<<grid, tiles * slices * 32, smem, st>>>(p, tiles, slices, span);
+    count_launch();
+    return cuda_status(cudaGetLastError());
 }
 
 template <typename E>
-void launch(const W4Params &p, int group, cudaStream_t st) {
-    if (group == 128) launch<E, 128>(p, st);
-    else if (group == 64) launch<E, 64>(p, st);
-    else launch<E, 32>(p, st);
+int launch(const W4Params &p, int group, cudaStream_t st) {
+    const bool two = p.T > 8;
+    if (group == 128) return two ? launch<E, 128, 2>(p, st) : launch<E, 128, 1>(p, st);
+    if (group == 64) return two ? launch<E, 64, 2>(p, st) : launch<E, 64, 1>(p, st);
+    return two ? launch<E, 32, 2>(p, st) : launch<E, 32, 1>(p, st);
 }
 
 constexpr int kRowsTokens = 16;
@@ -233,9 +264,9 @@ extern "C" int lora_w4_matvec(int dtype, const void *x, int T, int h_in, const v
         p.x = static_cast<const char *>(x) + (size_t)t * h_in * e;
         p.y = static_cast<char *>(y) + (size_t)t * h_out * e;
         p.T = T - t < kRowsTokens ? T - t : kRowsTokens;
-        if (dtype == LORA_BF16) launch<__nv_bfloat16>(p, group, (cudaStream_t)stream);
-        else launch<float>(p, group, (cudaStream_t)stream);
-        count_launch();
+        const int rc = dtype == LORA_BF16 ? launch<__nv_bfloat16>(p, group, (cudaStream_t)stream)
+                                          : launch<float>(p, group, (cudaStream_t)stream);
+        if (rc) return rc;
     }
-    return cuda_status(cudaGetLastError());
+    return LORA_OK;
 }
