@@ -260,12 +260,14 @@ extern "C" int lora_w4_matvec(int dtype, const void *x, int T, int h_in, const v
     p.h_out = h_out;
     p.groups = h_in / group;
     const size_t e = dtype == LORA_BF16 ? 2 : 4;
-    for (int t = 0; t < T; t += kRowsTokens) {
+    constexpr int kTcTokens = 64;
+    for (int t = 0; t < T; t += kTcTokens) {
         p.x = static_cast<const char *>(x) + (size_t)t * h_in * e;
         p.y = static_cast<char *>(y) + (size_t)t * h_out * e;
-        p.T = T - t < kRowsTokens ? T - t : kRowsTokens;
-        const int rc = dtype == LORA_BF16 ? launch<__nv_bfloat16>(p, group, (cudaStream_t)stream)
-                                          : launch<float>(p, group, (cudaStream_t)stream);
+        p.T = T - t < kTcTokens ? T - t : kTcTokens;
+        const int rc = p.T > kRowsTokens      ? decode::launch_w4_tc(dtype, p, group, (cudaStream_t)stream)
+                       : dtype == LORA_BF16 ? launch<__nv_bfloat16>(p, group, (cudaStream_t)stream)
+                                            : launch<float>(p, group, (cudaStream_t)stream);
         if (rc) return rc;
     }
     return LORA_OK;

@@ -1,0 +1,394 @@
+// Products with 4-bit weights for more than a few tokens, on the tensor cores (tcgen05).
+//
+// At 64 tokens the flops (128 a weight) need more than the warp-MMA rate while the
+// codes still come at half a byte a weight.  A thread block has 128 rows of W:
+//   one warp     copies code tiles (128 rows x 128 columns) by tensor copies;
+//   eight warps  turn codes less zeros into bf16 (exact) in shared memory, the A
+//                operand; two more warps do the same for x, the B operand (fp32 x:
+//                three bf16 parts, multiplied one after another);
+//   one thread   issues the MMAs, one accumulator in tensor memory a group of columns;
+//   four warps   scale each group's accumulator and add it up in fp32, a thread a row.
+// When the rows give too few blocks the columns are split over a cluster, whose
+// blocks each add up a share of the tokens, in rank order.
+#include <cudaTypedefs.h>
+
+#include "tc_common.cuh"
+#include "w4.cuh"
+
+namespace lora {
+namespace {
+
+using namespace decode;
+using namespace tc;
+
+constexpr int kRows = 128, kCols = 128;          // of W, a tile
+constexpr int kThreads = 16 * 32;
+constexpr int kScaleWarp0 = 8, kCopyWarp = 12, kMmaWarp = 13, kXWarp0 = 14;
+constexpr int kCodeBytes = kRows * kCols / 2, kABytes = kRows * kCols * 2;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kAccumulators = 8;
+
+template <typename E, int NTOK>
+struct W4Shape {
+    static constexpr int kParts = sizeof(E) == 2 ? 1 : 3;
+    static constexpr int kBPart = NTOK * kCols * 2;
+    static constexpr int kStage = kABytes + kParts * kBPart;
+    static constexpr int kStages = kParts == 1 ? 3 : 2;
+    static constexpr int kCodes = kParts == 1 ? 8 : 7;
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + (size_t)kCodes * kCodeBytes;
+};
+
+struct W4Control {
+    uint64_t codes_full[8], codes_free[8], ab_full[3], ab_free[3], d_full[kAccumulators], d_free[kAccumulators], drain;
+    volatile int abort;
+    uint32_t tmem;
+};
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, W4Control &ctl) {
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    if (wait_phase(bar, parity, &ctl.abort)) return true;
+    ctl.abort = 1;
+    return false;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, W4Control &ctl) {
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, ctl));
+}
+// A place in a ring of N and its parity.
+template <int N>
+struct Ring {
+    int at = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++at == N) {
+            at = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+// Byte offset of 16-byte chunk `chunk` (0..15) of row `row` in a tile of `rows` x 128 bf16.
+__device__ __forceinline__ uint32_t tile_off(int rows, int row, int chunk) {
+    return (uint32_t)((chunk >> 3) * (rows * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+template <typename E, int GROUP, int NTOK>
+__global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constant__ CUtensorMap map, const W4Params p, int splits) {
+    using Sh = W4Shape<E, NTOK>;
+    constexpr int kGroups = kCols / GROUP;               // a tile
+    extern __shared__ uint8_t raw[];
+    __shared__ W4Control ctl;
+    uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    uint8_t *codes = smem + Sh::kStages * Sh::kStage;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % splits, n0 = (blockIdx.x / splits) * kRows;
+    const int tiles = (p.h_in + kCols - 1) / kCols;
+    const int first = tiles * rank / splits, end = tiles * (rank + 1) / splits;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Sh::kCodes; ++i) {
+            mbar_init(&ctl.codes_full[i], 1);
+            mbar_init(&ctl.codes_free[i], 8);
+        }
+        for (int i = 0; i < Sh::kStages; ++i) {
+            mbar_init(&ctl.ab_full[i], 10);
+            mbar_init(&ctl.ab_free[i], 1);
+        }
+        for (int i = 0; i < kAccumulators; ++i) {
+            mbar_init(&ctl.d_full[i], 1);
+            mbar_init(&ctl.d_free[i], 4);
+        }
+        mbar_init(&ctl.drain, 1);
+        ctl.abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(&ctl.tmem, kTmemCols);
+        tmem_relinquish();
+    }
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+
+    E *y = static_cast<E *>(p.y);
+    auto store = [&](int t, int row, float v) {
+        if (t >= p.T || n0 + row >= p.h_out) return;
+        if (ctl.abort) v = __uint_as_float(0x7fffffffu);       // a wait gave up: no numbers rather than wrong ones
+        if constexpr (sizeof(E) == 2) y[(long long)t * p.h_out + n0 + row] = __float2bfloat16_rn(v);
+        else y[(long long)t * p.h_out + n0 + row] = v;
+    };
+    if (warp < kScaleWarp0) {
+        // codes of half a row of the tile, eight words, a thread
+        const int row = threadIdx.x & 127, half = threadIdx.x >> 7;
+        const long long n = min(n0 + row, p.h_out - 1);
+        constexpr int kZeros = GROUP == 32 ? 2 : 1;
+        uint32_t zero[kZeros], next[kZeros];
+        auto fetch = [&](int tile, uint32_t (&z)[kZeros]) {
+#pragma unroll
+            for (int i = 0; i < kZeros; ++i) {
+                const int g = min((tile * kCols + half * 64 + i * 32) / GROUP, p.groups - 1);
+                z[i] = p.zeros ? __ldg(p.zeros + n * p.groups + g) : 8u;
+            }
+        };
+        fetch(first, zero);
+        Ring<Sh::kCodes> c;
+        Ring<Sh::kStages> ab;
+        for (int tile = first; tile < end; ++tile, c.next(), ab.next()) {
+            if (tile + 1 < end) fetch(tile + 1, next);
+            if (!wait_warp(&ctl.codes_full[c.at], c.parity, ctl)) break;
+            const uint8_t *src = codes + c.at * kCodeBytes + row * 64;
+            uint4 w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)      // tensor copies with 64-byte swizzling: chunks XORed with bits 1 and 2 of the row
+                w[i] = *reinterpret_cast<const uint4 *>(src + ((((half * 2 + i) ^ (row >> 1)) & 3) << 4));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.codes_free[c.at]);
+            if (!wait_warp(&ctl.ab_free[ab.at], ab.parity ^ 1, ctl)) break;
+            uint8_t *a = smem + ab.at * Sh::kStage;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const __nv_bfloat162 offset = code_offset(zero[kZeros == 2 ? i : 0]);
+                const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t o[4];
+                    code_pairs(words[j], offset, o);
+                    *reinterpret_cast<uint4 *>(a + tile_off(kRows, row, half * 8 + i * 4 + j)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.ab_full[ab.at]);
+#pragma unroll
+            for (int i = 0; i < kZeros; ++i) zero[i] = next[i];
+        }
+    } else if (warp < kCopyWarp) {
+        // this thread's row: each group's sums, scaled
+        float acc[NTOK];
+#pragma unroll
+        for (int t = 0; t < NTOK; ++t) acc[t] = 0.f;
+        const int row = (warp - kScaleWarp0) * 32 + lane;
+        const __nv_bfloat16 *scales = p.scales + (long long)min(n0 + row, p.h_out - 1) * p.groups;
+        const uint32_t quad = (uint32_t)((warp - kScaleWarp0) * 32) << 16;
+        const int g0 = first * kGroups, g1 = end * kGroups;        // past p.groups: columns past h_in, zeros
+        float scale[kAccumulators];
+#pragma unroll
+        for (int i = 0; i < kAccumulators; ++i) scale[i] = __bfloat162float(scales[min(g0 + i, p.groups - 1)]);
+        uint32_t parity = 0;
+        bool ok = true;
+        for (int g = g0; ok && g < g1; g += kAccumulators, parity ^= 1) {
+            float after[kAccumulators];
+#pragma unroll
+            for (int i = 0; i < kAccumulators; ++i)
+                after[i] = __bfloat162float(scales[min(g + kAccumulators + i, p.groups - 1)]);
+#pragma unroll
+            for (int i = 0; i < kAccumulators; ++i) {
+                if (g + i >= g1) break;
+                if (!(ok = wait_warp(&ctl.d_full[i], parity, ctl))) break;
+                fence_after_sync();
+#pragma unroll
+                for (int b = 0; b < NTOK / 32; ++b) {
+                    float d[32];
+                    tmem_ld32(ctl.tmem + quad + i * NTOK + b * 32, d);
+#pragma unroll
+                    for (int t = 0; t < 32; ++t) acc[b * 32 + t] = fmaf(scale[i], d[t], acc[b * 32 + t]);
+                }
+                fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.d_free[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kAccumulators; ++i) scale[i] = after[i];
+        }
+        if (splits == 1) {
+#pragma unroll
+            for (int t = 0; t < NTOK; ++t) store(t, row, acc[t]);
+        } else {
+            // every block's sums of token t go to block t % splits: [from][t / splits][row]
+            cluster_barrier();                 // all of the cluster's blocks are past their tiles
+            const uint32_t local = smem_u32(smem) + (uint32_t)(rank * (NTOK / splits) * kRows + row) * 4;
+#pragma unroll
+            for (int t = 0; t < NTOK; ++t) {
+                uint32_t remote;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n"
+                             : "=r"(remote)
+                             : "r"(local + (uint32_t)(t / splits) * kRows * 4), "r"((uint32_t)(t % splits)));
+                asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(remote), "f"(ctl.abort ? __uint_as_float(0x7fffffffu) : acc[t])
+                             : "memory");
+            }
+        }
+    } else if (warp == kCopyWarp) {
+        if (lane == 0) {
+            Ring<Sh::kCodes> c;
+            for (int tile = first; tile < end; ++tile, c.next()) {
+                if (!wait_bar(&ctl.codes_free[c.at], c.parity ^ 1, ctl)) break;
+                mbar_arrive_expect_tx(&ctl.codes_full[c.at], kCodeBytes);
+                tma_load_2d(codes + c.at * kCodeBytes, &map, tile * (kCols / 2), n0, &ctl.codes_full[c.at]);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16_f32(kRows, NTOK);
+            const uint64_t a0 = desc_kmajor_sw128(smem_u32(smem)), b0 = desc_kmajor_sw128(smem_u32(smem) + kABytes);
+            Ring<Sh::kStages> ab;
+            Ring<kAccumulators> d;
+            for (int tile = first; tile < end; ++tile, ab.next()) {
+                if (!wait_bar(&ctl.ab_full[ab.at], ab.parity, ctl)) break;
+                fence_after_sync();
+                const uint64_t a = a0 + ab.at * (Sh::kStage / 16), b = b0 + ab.at * (Sh::kStage / 16);
+                bool ok = true;
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g, d.next()) {
+                    if (!(ok = wait_bar(&ctl.d_free[d.at], d.parity ^ 1, ctl))) break;
+                    fence_after_sync();
+#pragma unroll
+                    for (int q = Sh::kParts - 1; q >= 0; --q)      // the smallest part first
+#pragma unroll
+                        for (int ks = g * (8 / kGroups); ks < (g + 1) * (8 / kGroups); ++ks)
+                            mma_bf16(ctl.tmem + d.at * NTOK, a + ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) / 16,
+                                     b + (q * Sh::kBPart + (ks >> 2) * (NTOK * 128) + (ks & 3) * 32) / 16, idesc,
+                                     q < Sh::kParts - 1 || ks > g * (8 / kGroups));
+                    mma_commit(&ctl.d_full[d.at]);
+                }
+                if (!ok) break;
+                mma_commit(&ctl.ab_free[ab.at]);
+            }
+            mma_commit(&ctl.drain);
+            wait_phase(&ctl.drain, 0, nullptr);
+        }
+        __syncwarp();
+    } else {
+        // x of the tile's columns, in the order of code_pairs; tokens past T are zeros
+        const int tid = threadIdx.x - kXWarp0 * 32;
+        constexpr int kPieces = NTOK * 16 / 64;
+        Ring<Sh::kStages> ab;
+        for (int tile = first; tile < end; ++tile, ab.next()) {
+            uint4 v[sizeof(E) == 2 ? kPieces : 1];
+            auto piece = [&](int i, int *t, int *k) {
+                const int x = i * 64 + tid;
+                *t = x >> 4;
+                *k = tile * kCols + (x & 15) * 8;
+                return *t < p.T && *k < p.h_in;
+            };
+            if constexpr (sizeof(E) == 2) {
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    int t, k;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (piece(i, &t, &k))
+                        v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(p.x) + (long long)t * p.h_in + k));
+                }
+            }
+            if (!wait_warp(&ctl.ab_free[ab.at], ab.parity ^ 1, ctl)) break;
+            uint8_t *b = smem + ab.at * Sh::kStage + kABytes;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                int t, k;
+                const bool in = piece(i, &t, &k);
+                const uint32_t at = tile_off(NTOK, t, (i * 64 + tid) & 15);
+                if constexpr (sizeof(E) == 2) {
+                    uint32_t o[4];
+                    pair_x(v[i], o);
+                    *reinterpret_cast<uint4 *>(b + at) = make_uint4(o[0], o[1], o[2], o[3]);
+                } else {
+                    float f[8] = {};
+                    if (in) load8(static_cast<const E *>(p.x) + (long long)t * p.h_in + k, f);
+                    uint32_t o[3][4];
+                    split_x(f, o[0], o[1], o[2]);
+#pragma unroll
+                    for (int q = 0; q < 3; ++q)
+                        *reinterpret_cast<uint4 *>(b + q * Sh::kBPart + at) = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+                }
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.ab_full[ab.at]);
+        }
+    }
+    if (splits > 1 && (warp < kScaleWarp0 || warp >= kCopyWarp)) cluster_barrier();      // the scaling warps' first one
+    fence_before_sync();
+    __syncthreads();
+    fence_after_sync();
+    if (warp == kMmaWarp) tmem_dealloc(ctl.tmem, kTmemCols);
+    if (splits > 1) {
+        cluster_barrier();
+        const float *in = reinterpret_cast<const float *>(smem);
+        for (int x = threadIdx.x; x < NTOK / splits * kRows; x += kThreads) {
+            const int t = x / kRows, r = x % kRows;
+            float s = 0.f;
+            for (int from = 0; from < splits; ++from) s += in[(from * (NTOK / splits) + t) * kRows + r];
+            store(t * splits + rank, r, s);
+        }
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            ptr = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }();
+    return fn;
+}
+
+template <typename E, int GROUP, int NTOK>
+int launch(const W4Params &p, const CUtensorMap &map, cudaStream_t st) {
+    using Sh = W4Shape<E, NTOK>;
+    const int rows = (p.h_out + kRows - 1) / kRows, tiles = (p.h_in + kCols - 1) / kCols, sms = num_sms();
+    int splits = 1;        // blocks that share the columns: as many as leave one block a SM, two tiles of columns each
+    while (splits < 8 && rows * splits * 2 <= sms && tiles >= 4 * splits) splits *= 2;
+    const void *func = reinterpret_cast<const void *>(w4_tc_kernel<E, GROUP, NTOK>);
+    if (smem_optin(func, Sh::kSmem)) return LORA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * splits));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Sh::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_tc_kernel<E, GROUP, NTOK>, map, p, splits);
+    count_launch();
+    return cuda_status(e);
+}
+
+template <typename E, int NTOK>
+int launch(const W4Params &p, int group, const CUtensorMap &map, cudaStream_t st) {
+    if (group == 128) return launch<E, 128, NTOK>(p, map, st);
+    return group == 64 ? launch<E, 64, NTOK>(p, map, st) : launch<E, 32, NTOK>(p, map, st);
+}
+
+}  // namespace
+
+namespace decode {
+
+int launch_w4_tc(int dtype, const W4Params &p, int group, cudaStream_t st) {
+    if (!encode_fn() || num_sms() < 1) return LORA_ERR_CUDA;
+    // codes as bytes [h_out][h_in / 2]; what lies outside reads as zeros
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {(cuuint64_t)p.h_in / 2, (cuuint64_t)p.h_out}, strides[1] = {(cuuint64_t)p.h_in / 2};
+    const cuuint32_t box[2] = {kCols / 2, kRows}, step[2] = {1, 1};
+    if (encode_fn()(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(p.codes), dims, strides, box, step,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return LORA_ERR_CUDA;
+    if (dtype == LORA_BF16)
+        return p.T <= 32 ? launch<__nv_bfloat16, 32>(p, group, map, st) : launch<__nv_bfloat16, 64>(p, group, map, st);
+    return p.T <= 32 ? launch<float, 32>(p, group, map, st) : launch<float, 64>(p, group, map, st);
+}
+
+}  // namespace decode
+}  // namespace lora
