@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         produce<D, TMA>(p, maps, cur, ring, ctl);
         if (!TMA) cp_wait_all();
     } else {
-        if (threadIdx.x == kMmaWarp * 32) {
+        if (warp == kMmaWarp && elect_lane()) {
             issue<D, NQ, TMA>(p, cur, queries, ring, ctl);
             mma_commit(&ctl->drain);
             wait_phase(&ctl->drain, 0, nullptr);

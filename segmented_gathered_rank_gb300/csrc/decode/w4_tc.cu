@@ -3,9 +3,11 @@
 // At 64 tokens the flops (128 a weight) need more than the warp-MMA rate while the
 // codes still come at half a byte a weight.  A thread block has 128 rows of W:
 //   one warp     copies code tiles (128 rows x 128 columns) by tensor copies;
-//   eight warps  turn codes less zeros into bf16 (exact) in shared memory, the A
-//                operand; two more warps do the same for x, the B operand (fp32 x:
-//                three bf16 parts, multiplied one after another);
+//   eight warps  turn codes less zeros into bf16 (exact) in tensor memory, the A
+//                operand (through shared memory its 32 KB a tile, written and read
+//                again, would bound the kernel: 47 against 36 us at 64 x 4096 -> 16384);
+//   two warps    put x into shared memory, the B operand (fp32 x: three bf16 parts,
+//                multiplied one after another);
 //   one thread   issues the MMAs, one accumulator in tensor memory a group of columns;
 //   four warps   scale each group's accumulator and add it up in fp32, a thread a row.
 // When the rows give too few blocks the columns are split over a cluster, whose
@@ -24,22 +26,21 @@ using namespace tc;
 constexpr int kRows = 128, kCols = 128;          // of W, a tile
 constexpr int kThreads = 16 * 32;
 constexpr int kScaleWarp0 = 8, kCopyWarp = 12, kMmaWarp = 13, kXWarp0 = 14;
-constexpr int kCodeBytes = kRows * kCols / 2, kABytes = kRows * kCols * 2;
+constexpr int kCodeBytes = kRows * kCols / 2, kACols = kCols / 2;      // tensor memory columns of an A tile
 constexpr uint32_t kTmemCols = 512;
-constexpr int kAccumulators = 8;
+constexpr int kAccumulators = 4, kStages = 3, kACol0 = 256;
 
 template <typename E, int NTOK>
 struct W4Shape {
     static constexpr int kParts = sizeof(E) == 2 ? 1 : 3;
     static constexpr int kBPart = NTOK * kCols * 2;
-    static constexpr int kStage = kABytes + kParts * kBPart;
-    static constexpr int kStages = kParts == 1 ? 3 : 2;
-    static constexpr int kCodes = kParts == 1 ? 8 : 7;
+    static constexpr int kStage = kParts * kBPart;
+    static constexpr int kCodes = 8;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + (size_t)kCodes * kCodeBytes;
 };
 
 struct W4Control {
-    uint64_t codes_full[8], codes_free[8], ab_full[3], ab_free[3], d_full[kAccumulators], d_free[kAccumulators], drain;
+    uint64_t codes_full[8], codes_free[8], ab_full[kStages], ab_free[kStages], d_full[kAccumulators], d_free[kAccumulators], drain;
     volatile int abort;
     uint32_t tmem;
 };
@@ -67,9 +68,31 @@ struct Ring {
     }
 };
 
-// Byte offset of 16-byte chunk `chunk` (0..15) of row `row` in a tile of `rows` x 128 bf16.
+// Byte offset of 16-byte chunk `chunk` (0..15) of row `row` in a tile of `rows` x 128 bf16 (128-byte swizzling).
 __device__ __forceinline__ uint32_t tile_off(int rows, int row, int chunk) {
     return (uint32_t)((chunk >> 3) * (rows * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+// D[tmem] (+)= A[tmem] . B[smem]^T, A as bf16 pairs in columns.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
 }
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
@@ -82,7 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
     extern __shared__ uint8_t raw[];
     __shared__ W4Control ctl;
     uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    uint8_t *codes = smem + Sh::kStages * Sh::kStage;
+    uint8_t *codes = smem + kStages * Sh::kStage;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % splits, n0 = (blockIdx.x / splits) * kRows;
     const int tiles = (p.h_in + kCols - 1) / kCols;
@@ -93,7 +116,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             mbar_init(&ctl.codes_full[i], 1);
             mbar_init(&ctl.codes_free[i], 8);
         }
-        for (int i = 0; i < Sh::kStages; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(&ctl.ab_full[i], 10);
             mbar_init(&ctl.ab_free[i], 1);
         }
@@ -135,19 +158,24 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
         };
         fetch(first, zero);
         Ring<Sh::kCodes> c;
-        Ring<Sh::kStages> ab;
-        for (int tile = first; tile < end; ++tile, c.next(), ab.next()) {
-            if (tile + 1 < end) fetch(tile + 1, next);
-            if (!wait_warp(&ctl.codes_full[c.at], c.parity, ctl)) break;
+        Ring<kStages> ab;
+        uint4 w[2];
+        auto take = [&]() {                  // the thread's codes of the next tile
+            if (!wait_warp(&ctl.codes_full[c.at], c.parity, ctl)) return false;
             const uint8_t *src = codes + c.at * kCodeBytes + row * 64;
-            uint4 w[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i)      // tensor copies with 64-byte swizzling: chunks XORed with bits 1 and 2 of the row
                 w[i] = *reinterpret_cast<const uint4 *>(src + ((((half * 2 + i) ^ (row >> 1)) & 3) << 4));
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.codes_free[c.at]);
+            c.next();
+            return true;
+        };
+        bool ok = take();
+        for (int tile = first; ok && tile < end; ++tile, ab.next()) {
+            if (tile + 1 < end) fetch(tile + 1, next);
             if (!wait_warp(&ctl.ab_free[ab.at], ab.parity ^ 1, ctl)) break;
-            uint8_t *a = smem + ab.at * Sh::kStage;
+            uint32_t a[32];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const __nv_bfloat162 offset = code_offset(zero[kZeros == 2 ? i : 0]);
@@ -156,10 +184,14 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                 for (int j = 0; j < 4; ++j) {
                     uint32_t o[4];
                     code_pairs(words[j], offset, o);
-                    *reinterpret_cast<uint4 *>(a + tile_off(kRows, row, half * 8 + i * 4 + j)) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[(i * 4 + j) * 4 + e] = o[e];
                 }
             }
-            fence_proxy_async();
+            tmem_st32(ctl.tmem + ((uint32_t)((warp & 3) * 32) << 16) + kACol0 + ab.at * kACols + half * 32, a);
+            if (tile + 1 < end) ok = take();
+            asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+            fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.ab_full[ab.at]);
 #pragma unroll
@@ -221,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             }
         }
     } else if (warp == kCopyWarp) {
-        if (lane == 0) {
+        if (elect_lane()) {
             Ring<Sh::kCodes> c;
             for (int tile = first; tile < end; ++tile, c.next()) {
                 if (!wait_bar(&ctl.codes_free[c.at], c.parity ^ 1, ctl)) break;
@@ -231,15 +263,16 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
+        if (elect_lane()) {
             constexpr uint32_t idesc = idesc_bf16_f32(kRows, NTOK);
-            const uint64_t a0 = desc_kmajor_sw128(smem_u32(smem)), b0 = desc_kmajor_sw128(smem_u32(smem) + kABytes);
-            Ring<Sh::kStages> ab;
+            const uint64_t b0 = desc_kmajor_sw128(smem_u32(smem));
+            Ring<kStages> ab;
             Ring<kAccumulators> d;
             for (int tile = first; tile < end; ++tile, ab.next()) {
                 if (!wait_bar(&ctl.ab_full[ab.at], ab.parity, ctl)) break;
                 fence_after_sync();
-                const uint64_t a = a0 + ab.at * (Sh::kStage / 16), b = b0 + ab.at * (Sh::kStage / 16);
+                const uint32_t a = ctl.tmem + kACol0 + ab.at * kACols;
+                const uint64_t b = b0 + ab.at * (Sh::kStage / 16);
                 bool ok = true;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g, d.next()) {
@@ -249,9 +282,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                     for (int q = Sh::kParts - 1; q >= 0; --q)      // the smallest part first
 #pragma unroll
                         for (int ks = g * (8 / kGroups); ks < (g + 1) * (8 / kGroups); ++ks)
-                            mma_bf16(ctl.tmem + d.at * NTOK, a + ((ks >> 2) * (kRows * 128) + (ks & 3) * 32) / 16,
-                                     b + (q * Sh::kBPart + (ks >> 2) * (NTOK * 128) + (ks & 3) * 32) / 16, idesc,
-                                     q < Sh::kParts - 1 || ks > g * (8 / kGroups));
+                            mma_ts(ctl.tmem + d.at * NTOK, a + ks * 8,
+                                   b + (q * Sh::kBPart + (ks >> 2) * (NTOK * 128) + (ks & 3) * 32) / 16, idesc,
+                                   q < Sh::kParts - 1 || ks > g * (8 / kGroups));
                     mma_commit(&ctl.d_full[d.at]);
                 }
                 if (!ok) break;
@@ -262,47 +295,50 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
         }
         __syncwarp();
     } else {
-        // x of the tile's columns, in the order of code_pairs; tokens past T are zeros
+        // x of the tile's columns, in the order of code_pairs; tokens past T are zeros.  Each thread's pieces
+        // of the next tile are on their way while this one's are written.
         const int tid = threadIdx.x - kXWarp0 * 32;
-        constexpr int kPieces = NTOK * 16 / 64;
-        Ring<Sh::kStages> ab;
-        for (int tile = first; tile < end; ++tile, ab.next()) {
-            uint4 v[sizeof(E) == 2 ? kPieces : 1];
-            auto piece = [&](int i, int *t, int *k) {
-                const int x = i * 64 + tid;
-                *t = x >> 4;
-                *k = tile * kCols + (x & 15) * 8;
-                return *t < p.T && *k < p.h_in;
-            };
-            if constexpr (sizeof(E) == 2) {
+        constexpr int kPieces = NTOK * 16 / 64, kWords = sizeof(E) / 2, kHeld = sizeof(E) == 2 ? kPieces : kPieces / 2;
+        const int t0 = tid >> 4, k0 = (tid & 15) * 8;          // piece i: token t0 + 4 i
+        const E *src = static_cast<const E *>(p.x) + (long long)t0 * p.h_in + k0;
+        uint4 v[kHeld][kWords];
+        auto load = [&](int tile, int i0) {
 #pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    int t, k;
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (piece(i, &t, &k))
-                        v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(p.x) + (long long)t * p.h_in + k));
-                }
+            for (int i = 0; i < kHeld; ++i) {
+                const bool in = t0 + 4 * (i0 + i) < p.T && tile * kCols + k0 < p.h_in;
+#pragma unroll
+                for (int h = 0; h < kWords; ++h)
+                    v[i][h] = in ? __ldg(reinterpret_cast<const uint4 *>(src + 4LL * (i0 + i) * p.h_in + tile * kCols) + h)
+                                 : make_uint4(0, 0, 0, 0);
             }
+        };
+        Ring<kStages> ab;
+        load(first, 0);
+        for (int tile = first; tile < end; ++tile, ab.next()) {
             if (!wait_warp(&ctl.ab_free[ab.at], ab.parity ^ 1, ctl)) break;
-            uint8_t *b = smem + ab.at * Sh::kStage + kABytes;
+            uint8_t *b = smem + ab.at * Sh::kStage;
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) {
-                int t, k;
-                const bool in = piece(i, &t, &k);
-                const uint32_t at = tile_off(NTOK, t, (i * 64 + tid) & 15);
-                if constexpr (sizeof(E) == 2) {
-                    uint32_t o[4];
-                    pair_x(v[i], o);
-                    *reinterpret_cast<uint4 *>(b + at) = make_uint4(o[0], o[1], o[2], o[3]);
-                } else {
-                    float f[8] = {};
-                    if (in) load8(static_cast<const E *>(p.x) + (long long)t * p.h_in + k, f);
-                    uint32_t o[3][4];
-                    split_x(f, o[0], o[1], o[2]);
+            for (int i0 = 0; i0 < kPieces; i0 += kHeld) {
 #pragma unroll
-                    for (int q = 0; q < 3; ++q)
-                        *reinterpret_cast<uint4 *>(b + q * Sh::kBPart + at) = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+                for (int i = 0; i < kHeld; ++i) {
+                    const uint32_t at = tile_off(NTOK, t0 + 4 * (i0 + i), tid & 15);
+                    if constexpr (sizeof(E) == 2) {
+                        uint32_t o[4];
+                        pair_x(v[i][0], o);
+                        *reinterpret_cast<uint4 *>(b + at) = make_uint4(o[0], o[1], o[2], o[3]);
+                    } else {
+                        const float f[8] = {__uint_as_float(v[i][0].x), __uint_as_float(v[i][0].y), __uint_as_float(v[i][0].z),
+                                            __uint_as_float(v[i][0].w), __uint_as_float(v[i][1].x), __uint_as_float(v[i][1].y),
+                                            __uint_as_float(v[i][1].z), __uint_as_float(v[i][1].w)};
+                        uint32_t o[3][4];
+                        split_x(f, o[0], o[1], o[2]);
+#pragma unroll
+                        for (int q = 0; q < 3; ++q)
+                            *reinterpret_cast<uint4 *>(b + q * Sh::kBPart + at) = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+                    }
                 }
+                if (i0 + kHeld < kPieces) load(tile, i0 + kHeld);
+                else if (tile + 1 < end) load(tile + 1, 0);
             }
             fence_proxy_async();
             __syncwarp();
