@@ -6,7 +6,7 @@
 //   eight warps  turn codes less zeros into bf16 (exact) in tensor memory, the A
 //                operand (through shared memory its 32 KB a tile, written and read
 //                again, would bound the kernel: 47 against 36 us at 64 x 4096 -> 16384);
-//   two warps    put x into shared memory, the B operand (fp32 x: three bf16 parts,
+//   four warps   put x into shared memory, the B operand (fp32 x: three bf16 parts,
 //                multiplied one after another);
 //   one thread   issues the MMAs, one accumulator in tensor memory a group of columns;
 //   four warps   scale each group's accumulator and add it up in fp32, a thread a row.
@@ -24,8 +24,8 @@ using namespace decode;
 using namespace tc;
 
 constexpr int kRows = 128, kCols = 128;          // of W, a tile
-constexpr int kThreads = 16 * 32;
-constexpr int kScaleWarp0 = 8, kCopyWarp = 12, kMmaWarp = 13, kXWarp0 = 14;
+constexpr int kThreads = 20 * 32;
+constexpr int kScaleWarp0 = 8, kXWarp0 = 12, kCopyWarp = 16, kMmaWarp = 17;     // warpgroups of one kind
 constexpr int kCodeBytes = kRows * kCols / 2, kACols = kCols / 2;      // tensor memory columns of an A tile
 constexpr uint32_t kTmemCols = 512;
 constexpr int kAccumulators = 4, kStages = 3, kACol0 = 256;
@@ -94,6 +94,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+        "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
 __device__ __forceinline__ void cluster_barrier() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
@@ -114,10 +123,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kCodes; ++i) {
             mbar_init(&ctl.codes_full[i], 1);
-            mbar_init(&ctl.codes_free[i], 8);
+            mbar_init(&ctl.codes_free[i], 4);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&ctl.ab_full[i], 10);
+            mbar_init(&ctl.ab_full[i], 8);
             mbar_init(&ctl.ab_free[i], 1);
         }
         for (int i = 0; i < kAccumulators; ++i) {
@@ -137,71 +146,79 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
     fence_after_sync();
 
     E *y = static_cast<E *>(p.y);
-    auto store = [&](int t, int row, float v) {
-        if (t >= p.T || n0 + row >= p.h_out) return;
-        if (ctl.abort) v = __uint_as_float(0x7fffffffu);       // a wait gave up: no numbers rather than wrong ones
-        if constexpr (sizeof(E) == 2) y[(long long)t * p.h_out + n0 + row] = __float2bfloat16_rn(v);
-        else y[(long long)t * p.h_out + n0 + row] = v;
+    auto store = [](E *dst, float v) {
+        if constexpr (sizeof(E) == 2) *dst = __float2bfloat16_rn(v);
+        else *dst = v;
     };
+    // registers: five warpgroups start with 96 a thread; 2 x 96 + 152 + 88 + 40 is less than five times that
     if (warp < kScaleWarp0) {
-        // codes of half a row of the tile, eight words, a thread
-        const int row = threadIdx.x & 127, half = threadIdx.x >> 7;
+        // the codes of a row of the tile a thread; the two warpgroups take turns, so that one's waits
+        // lie under the other's work
+        const int row = threadIdx.x & 127;
         const long long n = min(n0 + row, p.h_out - 1);
-        constexpr int kZeros = GROUP == 32 ? 2 : 1;
-        uint32_t zero[kZeros], next[kZeros];
-        auto fetch = [&](int tile, uint32_t (&z)[kZeros]) {
+        const uint8_t *zeros = p.zeros ? p.zeros + n * p.groups : nullptr;
+        const uint32_t a_tmem = ctl.tmem + ((uint32_t)((warp & 3) * 32) << 16) + kACol0;
+        uint32_t zero[kGroups], next[kGroups];
+        auto fetch = [&](int tile, uint32_t (&z)[kGroups]) {
 #pragma unroll
-            for (int i = 0; i < kZeros; ++i) {
-                const int g = min((tile * kCols + half * 64 + i * 32) / GROUP, p.groups - 1);
-                z[i] = p.zeros ? __ldg(p.zeros + n * p.groups + g) : 8u;
-            }
+            for (int i = 0; i < kGroups; ++i) z[i] = zeros ? __ldg(zeros + min(tile * kGroups + i, p.groups - 1)) : 8u;
         };
-        fetch(first, zero);
         Ring<Sh::kCodes> c;
         Ring<kStages> ab;
-        uint4 w[2];
-        auto take = [&]() {                  // the thread's codes of the next tile
-            if (!wait_warp(&ctl.codes_full[c.at], c.parity, ctl)) return false;
+        int tile = first + (warp >> 2);
+        if (warp >> 2) {
+            c.next();
+            ab.next();
+        }
+        fetch(tile, zero);
+        for (; tile < end; tile += 2) {
+            fetch(tile + 2, next);
+            if (!wait_warp(&ctl.codes_full[c.at], c.parity, ctl)) break;
             const uint8_t *src = codes + c.at * kCodeBytes + row * 64;
+            uint4 w[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)      // tensor copies with 64-byte swizzling: chunks XORed with bits 1 and 2 of the row
-                w[i] = *reinterpret_cast<const uint4 *>(src + ((((half * 2 + i) ^ (row >> 1)) & 3) << 4));
+            for (int i = 0; i < 4; ++i)      // tensor copies with 64-byte swizzling: chunks XORed with bits 1 and 2 of the row
+                w[i] = *reinterpret_cast<const uint4 *>(src + (((i ^ (row >> 1)) & 3) << 4));
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.codes_free[c.at]);
-            c.next();
-            return true;
-        };
-        bool ok = take();
-        for (int tile = first; ok && tile < end; ++tile, ab.next()) {
-            if (tile + 1 < end) fetch(tile + 1, next);
-            if (!wait_warp(&ctl.ab_free[ab.at], ab.parity ^ 1, ctl)) break;
-            uint32_t a[32];
+            bool ok = true;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const __nv_bfloat162 offset = code_offset(zero[kZeros == 2 ? i : 0]);
-                const uint32_t words[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            for (int h = 0; h < 2; ++h) {
+                uint32_t a[32];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t o[4];
-                    code_pairs(words[j], offset, o);
+                for (int i = 0; i < 2; ++i) {
+                    const int q = h * 2 + i;               // 32 columns
+                    const __nv_bfloat162 offset = code_offset(zero[q * kGroups / 4]);
+                    const uint32_t words[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) a[(i * 4 + j) * 4 + e] = o[e];
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t o[4];
+                        code_pairs(words[j], offset, o);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) a[(i * 4 + j) * 4 + e] = o[e];
+                    }
                 }
+                if (h == 0 && !(ok = wait_warp(&ctl.ab_free[ab.at], ab.parity ^ 1, ctl))) break;
+                tmem_st32(a_tmem + ab.at * kACols + h * 32, a);
             }
-            tmem_st32(ctl.tmem + ((uint32_t)((warp & 3) * 32) << 16) + kACol0 + ab.at * kACols + half * 32, a);
-            if (tile + 1 < end) ok = take();
+            if (!ok) break;
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.ab_full[ab.at]);
+            c.next();
+            c.next();
+            ab.next();
+            ab.next();
 #pragma unroll
-            for (int i = 0; i < kZeros; ++i) zero[i] = next[i];
+            for (int i = 0; i < kGroups; ++i) zero[i] = next[i];
         }
-    } else if (warp < kCopyWarp) {
+    } else if (warp < kXWarp0) {
         // this thread's row: each group's sums, scaled
-        float acc[NTOK];
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;\n");
+        float2 acc[NTOK / 2];
 #pragma unroll
-        for (int t = 0; t < NTOK; ++t) acc[t] = 0.f;
+        for (int t = 0; t < NTOK / 2; ++t) acc[t] = make_float2(0.f, 0.f);
         const int row = (warp - kScaleWarp0) * 32 + lane;
         const __nv_bfloat16 *scales = p.scales + (long long)min(n0 + row, p.h_out - 1) * p.groups;
         const uint32_t quad = (uint32_t)((warp - kScaleWarp0) * 32) << 16;
@@ -226,7 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                     float d[32];
                     tmem_ld32(ctl.tmem + quad + i * NTOK + b * 32, d);
 #pragma unroll
-                    for (int t = 0; t < 32; ++t) acc[b * 32 + t] = fmaf(scale[i], d[t], acc[b * 32 + t]);
+                    for (int t = 0; t < 16; ++t)
+                        acc[b * 16 + t] = fma2(make_float2(scale[i], scale[i]), make_float2(d[2 * t], d[2 * t + 1]), acc[b * 16 + t]);
                 }
                 fence_before_sync();
                 __syncwarp();
@@ -235,9 +253,14 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < kAccumulators; ++i) scale[i] = after[i];
         }
+        const float lost = ctl.abort ? __uint_as_float(0x7fffffffu) : 0.f;       // a wait gave up: no numbers rather than wrong ones
         if (splits == 1) {
+            if (n0 + row < p.h_out) {
+                E *dst = y + n0 + row;
 #pragma unroll
-            for (int t = 0; t < NTOK; ++t) store(t, row, acc[t]);
+                for (int t = 0; t < NTOK; ++t, dst += p.h_out)
+                    if (t < p.T) store(dst, (t & 1 ? acc[t / 2].y : acc[t / 2].x) + lost);
+            }
         } else {
             // every block's sums of token t go to block t % splits: [from][t / splits][row]
             cluster_barrier();                 // all of the cluster's blocks are past their tiles
@@ -248,11 +271,67 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n"
                              : "=r"(remote)
                              : "r"(local + (uint32_t)(t / splits) * kRows * 4), "r"((uint32_t)(t % splits)));
-                asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(remote), "f"(ctl.abort ? __uint_as_float(0x7fffffffu) : acc[t])
+                asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(remote), "f"((t & 1 ? acc[t / 2].y : acc[t / 2].x) + lost)
                              : "memory");
             }
         }
-    } else if (warp == kCopyWarp) {
+    } else if (warp < kCopyWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        // x of the tile's columns, in the order of code_pairs; tokens past T are zeros.  Each thread's pieces
+        // of the next tile are on their way while this one's are written.
+        const int tid = threadIdx.x - kXWarp0 * 32;
+        constexpr int kPieces = NTOK * 16 / 128, kWords = sizeof(E) / 2, kHeld = sizeof(E) == 2 ? kPieces : kPieces / 2;
+        const int t0 = tid >> 4, k0 = (tid & 15) * 8;          // piece i: token t0 + 8 i
+        const E *src = static_cast<const E *>(p.x) + (long long)t0 * p.h_in + k0;
+        const long long step = 8LL * p.h_in;
+        const uint32_t place = tile_off(NTOK, t0, tid & 15);   // 8 tokens are one swizzle atom: piece i is i KB further
+        const int pieces = (p.T - t0 + 7) / 8;                 // that exist
+        uint4 v[kHeld][kWords];
+        auto load = [&](int tile, int i0) {
+            const E *at = src + tile * kCols;
+            const int n = tile * kCols + k0 < p.h_in ? pieces - i0 : 0;
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+#pragma unroll
+                for (int h = 0; h < kWords; ++h)
+                    v[i][h] = i < n ? __ldg(reinterpret_cast<const uint4 *>(at + (i0 + i) * step) + h) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        Ring<kStages> ab;
+        load(first, 0);
+        for (int tile = first; tile < end; ++tile, ab.next()) {
+            if (!wait_warp(&ctl.ab_free[ab.at], ab.parity ^ 1, ctl)) break;
+            uint8_t *b = smem + ab.at * Sh::kStage;
+#pragma unroll
+            for (int i0 = 0; i0 < kPieces; i0 += kHeld) {
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) {
+                    const uint32_t at = place + (i0 + i) * 1024;
+                    if constexpr (sizeof(E) == 2) {
+                        uint32_t o[4];
+                        pair_x(v[i][0], o);
+                        *reinterpret_cast<uint4 *>(b + at) = make_uint4(o[0], o[1], o[2], o[3]);
+                    } else {
+                        const float f[8] = {__uint_as_float(v[i][0].x), __uint_as_float(v[i][0].y), __uint_as_float(v[i][0].z),
+                                            __uint_as_float(v[i][0].w), __uint_as_float(v[i][1].x), __uint_as_float(v[i][1].y),
+                                            __uint_as_float(v[i][1].z), __uint_as_float(v[i][1].w)};
+                        uint32_t o[3][4];
+                        split_x(f, o[0], o[1], o[2]);
+#pragma unroll
+                        for (int q = 0; q < 3; ++q)
+                            *reinterpret_cast<uint4 *>(b + q * Sh::kBPart + at) = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+                    }
+                }
+                if (i0 + kHeld < kPieces) load(tile, i0 + kHeld);
+                else if (tile + 1 < end) load(tile + 1, 0);
+            }
+            fence_proxy_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.ab_full[ab.at]);
+        }
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+      if (warp == kCopyWarp) {
         if (elect_lane()) {
             Ring<Sh::kCodes> c;
             for (int tile = first; tile < end; ++tile, c.next()) {
@@ -262,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+      } else if (warp == kMmaWarp) {
         if (elect_lane()) {
             constexpr uint32_t idesc = idesc_bf16_f32(kRows, NTOK);
             const uint64_t b0 = desc_kmajor_sw128(smem_u32(smem));
@@ -294,58 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             wait_phase(&ctl.drain, 0, nullptr);
         }
         __syncwarp();
-    } else {
-        // x of the tile's columns, in the order of code_pairs; tokens past T are zeros.  Each thread's pieces
-        // of the next tile are on their way while this one's are written.
-        const int tid = threadIdx.x - kXWarp0 * 32;
-        constexpr int kPieces = NTOK * 16 / 64, kWords = sizeof(E) / 2, kHeld = sizeof(E) == 2 ? kPieces : kPieces / 2;
-        const int t0 = tid >> 4, k0 = (tid & 15) * 8;          // piece i: token t0 + 4 i
-        const E *src = static_cast<const E *>(p.x) + (long long)t0 * p.h_in + k0;
-        uint4 v[kHeld][kWords];
-        auto load = [&](int tile, int i0) {
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                const bool in = t0 + 4 * (i0 + i) < p.T && tile * kCols + k0 < p.h_in;
-#pragma unroll
-                for (int h = 0; h < kWords; ++h)
-                    v[i][h] = in ? __ldg(reinterpret_cast<const uint4 *>(src + 4LL * (i0 + i) * p.h_in + tile * kCols) + h)
-                                 : make_uint4(0, 0, 0, 0);
-            }
-        };
-        Ring<kStages> ab;
-        load(first, 0);
-        for (int tile = first; tile < end; ++tile, ab.next()) {
-            if (!wait_warp(&ctl.ab_free[ab.at], ab.parity ^ 1, ctl)) break;
-            uint8_t *b = smem + ab.at * Sh::kStage;
-#pragma unroll
-            for (int i0 = 0; i0 < kPieces; i0 += kHeld) {
-#pragma unroll
-                for (int i = 0; i < kHeld; ++i) {
-                    const uint32_t at = tile_off(NTOK, t0 + 4 * (i0 + i), tid & 15);
-                    if constexpr (sizeof(E) == 2) {
-                        uint32_t o[4];
-                        pair_x(v[i][0], o);
-                        *reinterpret_cast<uint4 *>(b + at) = make_uint4(o[0], o[1], o[2], o[3]);
-                    } else {
-                        const float f[8] = {__uint_as_float(v[i][0].x), __uint_as_float(v[i][0].y), __uint_as_float(v[i][0].z),
-                                            __uint_as_float(v[i][0].w), __uint_as_float(v[i][1].x), __uint_as_float(v[i][1].y),
-                                            __uint_as_float(v[i][1].z), __uint_as_float(v[i][1].w)};
-                        uint32_t o[3][4];
-                        split_x(f, o[0], o[1], o[2]);
-#pragma unroll
-                        for (int q = 0; q < 3; ++q)
-                            *reinterpret_cast<uint4 *>(b + q * Sh::kBPart + at) = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
-                    }
-                }
-                if (i0 + kHeld < kPieces) load(tile, i0 + kHeld);
-                else if (tile + 1 < end) load(tile + 1, 0);
-            }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.ab_full[ab.at]);
-        }
+      }
     }
-    if (splits > 1 && (warp < kScaleWarp0 || warp >= kCopyWarp)) cluster_barrier();      // the scaling warps' first one
+    if (splits > 1 && (warp < kScaleWarp0 || warp >= kXWarp0)) cluster_barrier();      // the scaling warps' first one
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
@@ -357,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             const int t = x / kRows, r = x % kRows;
             float s = 0.f;
             for (int from = 0; from < splits; ++from) s += in[(from * (NTOK / splits) + t) * kRows + r];
-            store(t * splits + rank, r, s);
+            const int token = t * splits + rank;
+            if (token < p.T && n0 + r < p.h_out) store(y + (long long)token * p.h_out + n0 + r, s);
         }
     }
 }
