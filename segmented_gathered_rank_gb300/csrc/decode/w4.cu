@@ -45,19 +45,22 @@ __device__ __forceinline__ int column(int j, int t4) {
 // of group lane % 4 (they are passed around the four threads), or of the one group.
 struct BlockWords {
     uint32_t w[2][4];
-    uint32_t zero[2];
-    float scale[2];
+    uint32_t zero[2], scale[2];
+};
+// A thread's two rows.
+struct Rows {
+    const uint8_t *codes[2], *zeros[2];
+    const __nv_bfloat16 *scales[2];
 };
 
 template <int GROUP>
-__device__ __forceinline__ void load_block(const W4Params &p, const uint8_t *(&rows)[2], const int (&n)[2], int block, int t4,
-                                           BlockWords &b) {
+__device__ __forceinline__ void load_block(const W4Params &p, const Rows &rows, int block, int t4, BlockWords &b) {
     constexpr int kGroups = kBlock / GROUP;
-    const int g = min(block * kGroups + (kGroups > 1 ? t4 % kGroups : 0), p.groups - 1);
+    const int g = kGroups == 1 ? block : min(block * kGroups + t4 % kGroups, p.groups - 1);
+    const int left = p.h_in - block * kBlock;      // h_in ends inside the last block at a group's end
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const uint8_t *src = rows[r] + block * (kBlock / 2);
-        const int left = p.h_in - block * kBlock;      // h_in ends inside the last block at a group's end
+        const uint8_t *src = rows.codes[r] + block * (kBlock / 2);
         if (GROUP == 128) {
             const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src + column<128>(0, t4) / 2));
             b.w[r][0] = u.x;
@@ -76,9 +79,8 @@ __device__ __forceinline__ void load_block(const W4Params &p, const uint8_t *(&r
             for (int j = 0; j < 4; ++j)
                 b.w[r][j] = j * 32 < left ? __ldg(reinterpret_cast<const uint32_t *>(src + column<32>(j, t4) / 2)) : 0u;
         }
-        const long long at = (long long)n[r] * p.groups + g;
-        b.scale[r] = __bfloat162float(p.scales[at]);
-        b.zero[r] = p.zeros ? __ldg(p.zeros + at) : 8u;
+        b.scale[r] = __ldg(reinterpret_cast<const unsigned short *>(rows.scales[r] + g));
+        b.zero[r] = rows.zeros[r] ? __ldg(rows.zeros[r] + g) : 8u;
     }
 }
 
@@ -119,71 +121,90 @@ __device__ __forceinline__ void stage_x(const W4Params &p, int first, int blocks
     }
 }
 
-// span: blocks of columns whose x fits in shared memory.
+// 16 bytes of shared memory, where `mine`; else `b` stays as it is.
+__device__ __forceinline__ void lds_if(uint4 &b, uint32_t addr, uint32_t mine) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %5, 0;\n@p ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n}\n"
+                 : "+r"(b.x), "+r"(b.y), "+r"(b.z), "+r"(b.w)
+                 : "r"(addr), "r"(mine)
+                 : "memory");
+}
+
+// span: blocks of columns whose x fits in shared memory.  run: consecutive blocks that a
+// warp takes at a time (256 bytes of a row: memory is read in longer pieces).
 template <typename E, int GROUP, int NT>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Params p, int tiles, int slices, int span) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Params p, int tiles, int slices, int span, int run) {
     constexpr int kGroups = kBlock / GROUP, kParts = sizeof(E) == 2 ? 1 : 3;
     extern __shared__ uint4 xs[];
     float *sums = reinterpret_cast<float *>(xs);        // [warp][token][17], at the end
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g4 = lane >> 2, t4 = lane & 3;
-    const int slice = warp % slices, blocks = (p.h_in + kBlock - 1) / kBlock;
+    const int slice = warp % slices, blocks = (p.h_in + kBlock - 1) / kBlock, run_shift = run == 4 ? 2 : run == 2 ? 1 : 0;
+    const uint32_t x_addr = (uint32_t)__cvta_generic_to_shared(xs) + lane * 16;
+    auto block_at = [&](int q) { return ((((q >> run_shift) * slices) + slice) << run_shift) + (q & (run - 1)); };      // a warp's q-th
     for (int n_first = blockIdx.x * tiles * 16; n_first < p.h_out; n_first += gridDim.x * tiles * 16) {
-        const int n0 = n_first + (warp / slices) * 16;
-        const int n[2] = {min(n0 + g4, p.h_out - 1), min(n0 + g4 + 8, p.h_out - 1)};
-        const uint8_t *rows[2] = {p.codes + (long long)n[0] * (p.h_in / 2), p.codes + (long long)n[1] * (p.h_in / 2)};
+        Rows rows;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const long long n = min(n_first + (warp / slices) * 16 + g4 + r * 8, p.h_out - 1);
+            rows.codes[r] = p.codes + n * (p.h_in / 2);
+            rows.scales[r] = p.scales + n * p.groups;
+            rows.zeros[r] = p.zeros ? p.zeros + n * p.groups : nullptr;
+        }
         float acc[NT][4] = {};
+        uint4 b[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) b[nt] = make_uint4(0, 0, 0, 0);        // of tokens past T for good
         BlockWords ring[kDepth];
 #pragma unroll
         for (int i = 0; i < kDepth; ++i)
-            if (slice + i * slices < blocks) load_block<GROUP>(p, rows, n, slice + i * slices, t4, ring[i]);
+            if (block_at(i) < blocks) load_block<GROUP>(p, rows, block_at(i), t4, ring[i]);
+        int q = 0;          // the warp's blocks so far: a multiple of kDepth where a span begins
         for (int first = 0; first < blocks; first += span) {
             const int end = min(blocks, first + span);
             if (first > 0 || n_first > (int)blockIdx.x * tiles * 16) __syncthreads();
             stage_x<E, GROUP, NT>(p, first, end - first, xs);
             __syncthreads();
-            // span is a multiple of slices * kDepth: the ring keeps its places from one span to the next
-            for (int base = first + slice; base < end; base += kDepth * slices) {
+            for (; block_at(q) < end; q += kDepth) {
 #pragma unroll
                 for (int i = 0; i < kDepth; ++i) {
-                    const int block = base + i * slices;
+                    const int block = block_at(q + i);
                     if (block >= end) break;
-                    const BlockWords cur = ring[i];
-                    if (block + kDepth * slices < blocks) load_block<GROUP>(p, rows, n, block + kDepth * slices, t4, ring[i]);
+                    const uint32_t xb = x_addr + (block - first) * (4 * kParts * NT * 512);
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
-                        float c[NT][4] = {};
+                        float c[2][NT][4] = {};        // two chains of sums
                         float scale[2];
                         __nv_bfloat162 offset[2];
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            uint32_t z = cur.zero[r];
-                            scale[r] = cur.scale[r];
+                            uint32_t z = ring[i].zero[r], sc = ring[i].scale[r];
                             if (kGroups > 1) {
                                 z = __shfl_sync(0xffffffffu, z, (lane & ~3) | g);
-                                scale[r] = __shfl_sync(0xffffffffu, scale[r], (lane & ~3) | g);
+                                sc = __shfl_sync(0xffffffffu, sc, (lane & ~3) | g);
                             }
+                            scale[r] = __uint_as_float(sc << 16);
                             offset[r] = code_offset(z);
                         }
 #pragma unroll
                         for (int j = g * (4 / kGroups); j < (g + 1) * (4 / kGroups); ++j) {
                             uint32_t a[2][4];
-                            code_pairs(cur.w[0][j], offset[0], a[0]);
-                            code_pairs(cur.w[1][j], offset[1], a[1]);
+                            code_pairs(ring[i].w[0][j], offset[0], a[0]);
+                            code_pairs(ring[i].w[1][j], offset[1], a[1]);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int q = kParts - 1; q >= 0; --q) {        // the smallest part first
-                                    uint4 b = make_uint4(0, 0, 0, 0);
-                                    if (nt * 8 + g4 < p.T) b = xs[x_place<NT, kParts>(block - first, j, q, nt, lane)];
-                                    mma16816(c[nt], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
-                                    mma16816(c[nt], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+                                for (int part = kParts - 1; part >= 0; --part) {        // the smallest part first
+                                    lds_if(b[nt], xb + ((j * kParts + part) * NT + nt) * 512, nt * 8 + g4 < p.T);
+                                    mma16816(c[0][nt], a[0][0], a[1][0], a[0][1], a[1][1], b[nt].x, b[nt].y);
+                                    mma16816(c[1][nt], a[0][2], a[1][2], a[0][3], a[1][3], b[nt].z, b[nt].w);
                                 }
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[nt][e] = fmaf(scale[e >> 1], c[nt][e], acc[nt][e]);
+                            for (int e = 0; e < 4; ++e)
+                                acc[nt][e] = fmaf(scale[e >> 1], c[0][nt][e] + c[1][nt][e], acc[nt][e]);
                     }
+                    if (block_at(q + i + kDepth) < blocks) load_block<GROUP>(p, rows, block_at(q + i + kDepth), t4, ring[i]);
                 }
             }
         }
@@ -217,11 +238,12 @@ int launch(const W4Params &p, cudaStream_t st) {
     // all of x in shared memory at once, or spans of whole rounds of the ring
     const int most = blocks <= kFit ? kMaxWarps : kFit / kDepth, slices = kMaxWarps / tiles < most ? kMaxWarps / tiles : most;
     const int span = blocks <= kFit ? blocks : kFit / (slices * kDepth) * (slices * kDepth);
+    const int run = blocks >= 4 * slices ? 4 : blocks >= 2 * slices ? 2 : 1;
     const size_t sums = (size_t)tiles * slices * NT * 8 * 17 * sizeof(float);
     const size_t smem = (size_t)span * kBlockBytes > sums ? (size_t)span * kBlockBytes : sums;
     const int need = (row_tiles + tiles - 1) / tiles, grid = need < sms ? need : sms;
     if (smem_optin(reinterpret_cast<const void *>(w4_rows_kernel<E, GROUP, NT>), smem)) return LORA_ERR_CUDA;
-    w4_rows_kernel<E, GROUP, NT><<<grid, tiles * slices * 32, smem, st>>>(p, tiles, slices, span);
+    w4_rows_kernel<E, GROUP, NT><<<grid, tiles * slices * 32, smem, st>>>(p, tiles, slices, span, run);
     count_launch();
     return cuda_status(cudaGetLastError());
 }

@@ -2,7 +2,7 @@
 //
 // At 64 tokens the flops (128 a weight) need more than the warp-MMA rate while the
 // codes still come at half a byte a weight.  A thread block has 128 rows of W:
-//   one warp     copies code tiles (128 rows x 128 columns) by tensor copies;
+//   one warp     copies code tiles (128 rows x 256 columns) by tensor copies;
 //   eight warps  turn codes less zeros into bf16 (exact) in tensor memory, the A
 //                operand (through shared memory its 32 KB a tile, written and read
 //                again, would bound the kernel: 47 against 36 us at 64 x 4096 -> 16384);
@@ -26,7 +26,7 @@ using namespace tc;
 constexpr int kRows = 128, kCols = 128;          // of W, a tile
 constexpr int kThreads = 20 * 32;
 constexpr int kScaleWarp0 = 8, kXWarp0 = 12, kCopyWarp = 16, kMmaWarp = 17;     // warpgroups of one kind
-constexpr int kCodeBytes = kRows * kCols / 2, kACols = kCols / 2;      // tensor memory columns of an A tile
+constexpr int kCodeBytes = kRows * kCols, kACols = kCols / 2;      // codes of two tiles; tensor memory columns of an A tile
 constexpr uint32_t kTmemCols = 512;
 constexpr int kAccumulators = 4, kStages = 3, kACol0 = 256;
 
@@ -35,12 +35,12 @@ struct W4Shape {
     static constexpr int kParts = sizeof(E) == 2 ? 1 : 3;
     static constexpr int kBPart = NTOK * kCols * 2;
     static constexpr int kStage = kParts * kBPart;
-    static constexpr int kCodes = 8;
+    static constexpr int kCodes = 4;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + (size_t)kCodes * kCodeBytes;
 };
 
 struct W4Control {
-    uint64_t codes_full[8], codes_free[8], ab_full[kStages], ab_free[kStages], d_full[kAccumulators], d_free[kAccumulators], drain;
+    uint64_t codes_full[4], codes_free[4], ab_full[kStages], ab_free[kStages], d_full[kAccumulators], d_free[kAccumulators], drain;
     volatile int abort;
     uint32_t tmem;
 };
@@ -118,12 +118,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % splits, n0 = (blockIdx.x / splits) * kRows;
     const int tiles = (p.h_in + kCols - 1) / kCols;
-    const int first = tiles * rank / splits, end = tiles * (rank + 1) / splits;
+    const int pairs = (tiles + 1) / 2;                   // of tiles, whose codes are copied together
+    const int first = 2 * (pairs * rank / splits), end = min(tiles, 2 * (pairs * (rank + 1) / splits));
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kCodes; ++i) {
             mbar_init(&ctl.codes_full[i], 1);
-            mbar_init(&ctl.codes_free[i], 4);
+            mbar_init(&ctl.codes_free[i], 8);
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&ctl.ab_full[i], 8);
@@ -166,19 +167,16 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
         Ring<Sh::kCodes> c;
         Ring<kStages> ab;
         int tile = first + (warp >> 2);
-        if (warp >> 2) {
-            c.next();
-            ab.next();
-        }
+        if (warp >> 2) ab.next();
         fetch(tile, zero);
         for (; tile < end; tile += 2) {
             fetch(tile + 2, next);
             if (!wait_warp(&ctl.codes_full[c.at], c.parity, ctl)) break;
-            const uint8_t *src = codes + c.at * kCodeBytes + row * 64;
+            const uint8_t *src = codes + c.at * kCodeBytes + row * 128;
             uint4 w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)      // tensor copies with 64-byte swizzling: chunks XORed with bits 1 and 2 of the row
-                w[i] = *reinterpret_cast<const uint4 *>(src + (((i ^ (row >> 1)) & 3) << 4));
+            for (int i = 0; i < 4; ++i)      // tensor copies with 128-byte swizzling: 16-byte chunks XORed with the row
+                w[i] = *reinterpret_cast<const uint4 *>(src + ((((warp >> 2) * 4 + i) ^ (row & 7)) << 4));
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.codes_free[c.at]);
             bool ok = true;
@@ -206,7 +204,6 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl.ab_full[ab.at]);
-            c.next();
             c.next();
             ab.next();
             ab.next();
@@ -334,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
       if (warp == kCopyWarp) {
         if (elect_lane()) {
             Ring<Sh::kCodes> c;
-            for (int tile = first; tile < end; ++tile, c.next()) {
+            for (int tile = first; tile < end; tile += 2, c.next()) {
                 if (!wait_bar(&ctl.codes_free[c.at], c.parity ^ 1, ctl)) break;
                 mbar_arrive_expect_tx(&ctl.codes_full[c.at], kCodeBytes);
                 tma_load_2d(codes + c.at * kCodeBytes, &map, tile * (kCols / 2), n0, &ctl.codes_full[c.at]);
@@ -426,7 +423,7 @@ int launch(const W4Params &p, const CUtensorMap &map, cudaStream_t st) {
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_tc_kernel<E, GROUP, NTOK>, map, p, splits);
     count_launch();
     return cuda_status(e);
@@ -447,9 +444,9 @@ int launch_w4_tc(int dtype, const W4Params &p, int group, cudaStream_t st) {
     // codes as bytes [h_out][h_in / 2]; what lies outside reads as zeros
     CUtensorMap map;
     const cuuint64_t dims[2] = {(cuuint64_t)p.h_in / 2, (cuuint64_t)p.h_out}, strides[1] = {(cuuint64_t)p.h_in / 2};
-    const cuuint32_t box[2] = {kCols / 2, kRows}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {kCols, kRows}, step[2] = {1, 1};
     if (encode_fn()(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(p.codes), dims, strides, box, step,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return LORA_ERR_CUDA;
     if (dtype == LORA_BF16)
