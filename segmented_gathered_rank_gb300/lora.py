@@ -165,9 +165,9 @@ def _rows(t):
     """(pointer, elements between rows) of a CUDA matrix whose rows are contiguous."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or not t.is_cuda or (t.shape[1] > 1 and t.stride(1) != 1):
+    if not (t.is_cuda and t.dim() == 2 and t.stride(1) == 1):
         raise ValueError("expected a CUDA matrix with contiguous rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.data_ptr(), t.stride(0)
 
 
 def _hptr(a):
@@ -183,13 +183,25 @@ def _hptr(a):
     return ctypes.c_void_p(a.data_ptr())
 
 
-def _stream(stream):
+_raw_stream = None      # torch's current stream as an address: the Stream object around it takes longer to make than a launch
+
+
+def _stream_ptr(stream):
+    """Address of a stream (None: torch's current one)."""
+    global _raw_stream
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-    if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        if _raw_stream is None:
+            import torch
+            get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+            torch.cuda.current_stream()      # initialises CUDA, or says why not
+            _raw_stream = ((lambda: get(device())) if get and device else
+                           (lambda: torch.cuda.current_stream().cuda_stream))
+        return _raw_stream()
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _stream(stream):
+    return ctypes.c_void_p(_stream_ptr(stream))
 
 
 def lora_strerror(status: int) -> str:
@@ -352,7 +364,7 @@ def lora_layer_forward_fp8(pool, matrix, x, W8, w_scale, y, seg_starts, seg_adap
 def lora_w4_matvec(dtype, x, T, h_in, codes, scales, zeros, group, h_out, y, stream=None) -> None:
     """Products with 4-bit weights (uint8 codes, bf16 scales, uint8 zeros or None); y is overwritten."""
     rc = _lib.lora_w4_matvec(dtype, _ptr(x), T, h_in, _ptr(codes), _ptr(scales), _ptr(zeros), group, h_out, _ptr(y),
-                             _stream(stream))
+                             _stream_ptr(stream))
     if rc:
         _check(rc, "lora_w4_matvec")
 
@@ -363,7 +375,7 @@ def lora_kv_append(kv, q, k, v, T, n_q_heads, positions, slots, cos_sin, n_pos, 
     (pq, ld_q), (pk, ld_k), (pv, ld_v) = _rows(q), _rows(k), _rows(v)
     rc = _lib.lora_kv_append(kv.ref, pq, ld_q, pk, ld_k, pv, ld_v, T, n_q_heads, _ptr(positions), _ptr(slots),
                              _ptr(cos_sin), n_pos, rot_dim, 1 if interleaved else 0, _ptr(q_norm), _ptr(k_norm), eps,
-                             _ptr(q_out), _stream(stream))
+                             _ptr(q_out), _stream_ptr(stream))
     if rc:
         _check(rc, "lora_kv_append")
 
@@ -379,6 +391,6 @@ def lora_tree_attention(kv, q, n_q_heads, seg_starts, S, T, kv_lens, page_table,
         ws_bytes = workspace.nbytes
     rc = _lib.lora_tree_attention(kv.ref, _ptr(q), n_q_heads, _ptr(seg_starts), S, T, _ptr(kv_lens), _ptr(page_table),
                                   max_pages, _ptr(tree_mask), mask_words, scale, _ptr(out), _ptr(workspace), ws_bytes,
-                                  _stream(stream))
+                                  _stream_ptr(stream))
     if rc:
         _check(rc, "lora_tree_attention")
