@@ -6,10 +6,11 @@
 // each head read once and written once: memory is the bound for large T, the
 // chain of dependent loads (position -> table row; slot -> address) for small.
 //
-// Layout: `lanes` threads (the power of two >= d/8) hold one head, 8 elements
-// each, so the sum of squares is a few shuffles and the partner of a
-// half-split pair is a shuffle away (or, when rot/2 is no multiple of 8, in a
-// row of shared memory).
+// Layout: LANES threads (the power of two >= d/8) hold one head, 8 elements each,
+// so the sum of squares is a few shuffles and the partner of a half-split pair is a
+// shuffle away (or, when rot/2 is no multiple of 8, in a row of shared memory).  A
+// block takes the heads of one token, kHeads a thread at a time with their loads in
+// flight together; its lanes keep their elements' cosines and sines for all heads.
 #include "decode.cuh"
 
 namespace lora {
@@ -18,6 +19,7 @@ namespace {
 using namespace decode;
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 3, kManyBlocks = 4096;
 
 struct AppendParams {
     const void *q, *k, *v;
@@ -34,95 +36,161 @@ struct AppendParams {
     int *status;
 };
 
-// One block: `heads_per_block` consecutive heads (queries, keys, values in that
-// order) of token blockIdx.x; LANES threads a head.
-template <typename E, int LANES, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
-    __shared__ float row[kThreads * 8];
-    const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-    const int head = blockIdx.y * (kThreads / LANES) + group;
-    const int heads = p.n_q + 2 * p.n_kv;
-    const long long t = blockIdx.x;
-    const int at = lane * 8;
-    const bool live = head < heads && at < p.d;
-    const bool is_q = head < p.n_q, is_k = !is_q && head < p.n_q + p.n_kv;
+// The lanes of this thread's head within its warp.
+template <int LANES>
+__device__ __forceinline__ unsigned group_mask() {
+    return LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << ((threadIdx.x & 31) / LANES * LANES);
+}
 
-    float x[8] = {};
-    if (live) {
-        const E *src = is_q   ? static_cast<const E *>(p.q) + t * p.ld_q + (long long)head * p.d
-                       : is_k ? static_cast<const E *>(p.k) + t * p.ld_k + (long long)(head - p.n_q) * p.d
-                              : static_cast<const E *>(p.v) + t * p.ld_v + (long long)(head - p.n_q - p.n_kv) * p.d;
-        load8(src + at, x);
+// Eight elements as loaded, and as floats.
+template <typename E>
+struct Held {
+    uint4 v[sizeof(E) / 2];
+    __device__ __forceinline__ void load(const E *p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(E) / 2; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
     }
-    const E *norm = static_cast<const E *>(is_q ? p.q_norm : is_k ? p.k_norm : nullptr);
-    float sum = 0.f;
+    __device__ __forceinline__ void get(float (&f)[8]) const { load8(reinterpret_cast<const E *>(v), f); }
+};
+
+// PAIRS: how elements pair up.  kNear: neighbours; kFar: i and i + rot/2 with rot/2 a
+// multiple of 8; both with an aligned table (kNear: rot a multiple of 8).  kAnyNear, kAnyFar:
+// without those conditions.  HEADS: heads a thread.
+enum { kNear, kFar, kAnyNear, kAnyFar };
+
+template <typename E, int LANES, int PAIRS, int HEADS>
+__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+    constexpr int kGroups = kThreads / LANES;
+    constexpr bool kFarPairs = PAIRS == kFar || PAIRS == kAnyFar;
+    __shared__ float rows[PAIRS == kAnyFar ? kThreads * 8 : 1];
+    const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, at = lane * 8;
+    const int heads = p.n_q + 2 * p.n_kv, half = p.rot >> 1;
+    const int head_first = blockIdx.y * kGroups * HEADS + group;
+    const long long t = blockIdx.x;
+    const bool inside = at < p.d;
+
+    Held<E> held[HEADS];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum += x[e] * x[e];
-#pragma unroll
-    for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (norm && live) {
-        float w[8];
-        load8(norm + at, w);
-        const float r = rsqrtf(sum / (float)p.d + p.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+    for (int u = 0; u < HEADS; ++u) {
+        const int head = head_first + u * kGroups;
+        const E *src = head < p.n_q ? static_cast<const E *>(p.q) + t * p.ld_q + head * p.d
+                       : head < p.n_q + p.n_kv ? static_cast<const E *>(p.k) + t * p.ld_k + (head - p.n_q) * p.d
+                                               : static_cast<const E *>(p.v) + t * p.ld_v + (head - p.n_q - p.n_kv) * p.d;
+        if (head < heads && inside) held[u].load(src + at);
     }
-    const int half = p.rot >> 1;
+    const long long slot = p.slots[t];
+    float c[kFarPairs ? 8 : 4], s[kFarPairs ? 8 : 4];
     if (half) {
         int pos = p.positions[t];
         if (pos < 0 || pos >= p.n_pos) {
             if (threadIdx.x == 0) flag_status(p.status, LORA_DEV_BAD_POSITION);
             pos = pos < 0 ? 0 : p.n_pos - 1;
         }
-        const float *c = p.cos_sin + (long long)pos * p.rot, *s = c + half;
-        const bool turn = live && (is_q || is_k);
-        if (INTERLEAVED) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 2)
-                if (turn && at + e < p.rot) {
-                    const int i = (at + e) >> 1;
-                    const float a = x[e], b = x[e + 1];
-                    x[e] = a * c[i] - b * s[i];
-                    x[e + 1] = a * s[i] + b * c[i];
-                }
+        const float *row = p.cos_sin + (long long)pos * p.rot;
+        if (PAIRS == kFar) {
+            if (at < p.rot) {
+                const int i = at < half ? at : at - half;
+                load8(row + i, c);
+                load8(row + half + i, s);
+            }
+        } else if (PAIRS == kNear) {
+            if (at < p.rot) {
+                *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(row + (at >> 1));
+                *reinterpret_cast<float4 *>(s) = *reinterpret_cast<const float4 *>(row + half + (at >> 1));
+            }
         } else {
-            float *mine = row + group * (LANES * 8);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mine[at + e] = x[e];
-            __syncwarp();
-            if (turn) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int i = at + e;
-                    if (i < half) x[e] = x[e] * c[i] - mine[i + half] * s[i];
-                    else if (i < p.rot) x[e] = mine[i - half] * s[i - half] + x[e] * c[i - half];
+            for (int e = 0; e < (kFarPairs ? 8 : 4); ++e) {
+                const int x = kFarPairs ? at + e : at + 2 * e, i = !kFarPairs ? x >> 1 : x < half ? x : x - half;
+                if (x < p.rot) {
+                    c[e] = row[i];
+                    s[e] = row[half + i];
                 }
             }
         }
     }
-    if (!live) return;
-    if (is_q) {
-        store8(static_cast<E *>(p.q_out) + (t * p.n_q + head) * p.d + at, x);
-        return;
-    }
-    const long long slot = p.slots[t];
-    if (slot < 0) return;
-    if (slot >= p.n_slots) {
-        flag_status(p.status, LORA_DEV_BAD_SLOT);
-        return;
-    }
-    const int kv_head = head - p.n_q - (is_k ? 0 : p.n_kv);
     const long long page = slot >> p.page_shift, off = slot & ((1 << p.page_shift) - 1);
-    E *dst = static_cast<E *>(is_k ? p.k_pages : p.v_pages);
-    store8(dst + (((page * p.n_kv + kv_head) << p.page_shift) + off) * p.d + at, x);
+    const bool stored = slot >= 0 && slot < p.n_slots;
+    if (slot >= p.n_slots && threadIdx.x == 0) flag_status(p.status, LORA_DEV_BAD_SLOT);
+
+#pragma unroll
+    for (int u = 0; u < HEADS; ++u) {
+        const int head = head_first + u * kGroups;
+        if (head >= heads) return;
+        const bool is_q = head < p.n_q, is_v = head >= p.n_q + p.n_kv;
+        float h[8] = {};
+        if (inside) held[u].get(h);
+        const E *norm = static_cast<const E *>(is_q ? p.q_norm : p.k_norm);
+        if (!is_v && norm) {
+            float sum = 0.f, w[8] = {};
+            if (inside) load8(norm + at, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += h[e] * h[e];
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(group_mask<LANES>(), sum, o);
+            const float r = rsqrtf(sum / (float)p.d + p.eps);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = h[e] * r * w[e];
+        }
+        if (!is_v && half) {
+            if (!kFarPairs) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (at + 2 * e < p.rot) {
+                        const float a = h[2 * e], b = h[2 * e + 1];
+                        h[2 * e] = a * c[e] - b * s[e];
+                        h[2 * e + 1] = a * s[e] + b * c[e];
+                    }
+            } else {
+                float other[8];
+                if (PAIRS == kFar) {
+                    const int partner = (at < half ? lane + half / 8 : lane - half / 8) & (LANES - 1);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) other[e] = __shfl_sync(group_mask<LANES>(), h[e], partner, LANES);
+                } else {
+                    float *mine = rows + group * (LANES * 8);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mine[at + e] = h[e];
+                    __syncwarp(group_mask<LANES>());
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) other[e] = at + e < p.rot ? mine[at + e < half ? at + e + half : at + e - half] : 0.f;
+                    __syncwarp(group_mask<LANES>());
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (at + e < p.rot) h[e] = at + e < half ? h[e] * c[e] - other[e] * s[e] : other[e] * s[e] + h[e] * c[e];
+            }
+        }
+        if (!inside) continue;
+        if (is_q) {
+            store8(static_cast<E *>(p.q_out) + (t * p.n_q + head) * p.d + at, h);
+        } else if (stored) {
+            E *dst = static_cast<E *>(is_v ? p.v_pages : p.k_pages);
+            const int kv_head = head - p.n_q - (is_v ? p.n_kv : 0);
+            store8(dst + (((page * p.n_kv + kv_head) << p.page_shift) + off) * p.d + at, h);
+        }
+    }
+}
+
+template <typename E, int LANES, int PAIRS>
+void launch(const AppendParams &p, int T, cudaStream_t st) {
+    constexpr int kGroups = kThreads / LANES;
+    const int heads = p.n_q + 2 * p.n_kv;
+    const dim3 one(T, (heads + kGroups - 1) / kGroups), more(T, (heads + kGroups * kHeads - 1) / (kGroups * kHeads));
+    if ((long long)one.x * one.y > kManyBlocks) append_kernel<E, LANES, PAIRS, kHeads><<<more, kThreads, 0, st>>>(p);
+    else append_kernel<E, LANES, PAIRS, 1><<<one, kThreads, 0, st>>>(p);
 }
 
 template <typename E, int LANES>
 void launch(const AppendParams &p, int T, bool interleaved, cudaStream_t st) {
-    const int per = kThreads / LANES, heads = p.n_q + 2 * p.n_kv;
-    const dim3 grid(T, (heads + per - 1) / per);
-    if (interleaved) append_kernel<E, LANES, true><<<grid, kThreads, 0, st>>>(p);
-    else append_kernel<E, LANES, false><<<grid, kThreads, 0, st>>>(p);
+    const bool table = aligned16(p.cos_sin);
+    if (interleaved) {
+        if (table && p.rot % 8 == 0) launch<E, LANES, kNear>(p, T, st);
+        else launch<E, LANES, kAnyNear>(p, T, st);
+    } else {
+        if (table && p.rot % 16 == 0) launch<E, LANES, kFar>(p, T, st);
+        else launch<E, LANES, kAnyFar>(p, T, st);
+    }
 }
 
 template <typename E>
