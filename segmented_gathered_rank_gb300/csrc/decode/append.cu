@@ -59,7 +59,7 @@ struct Held {
 enum { kNear, kFar, kAnyNear, kAnyFar };
 
 template <typename E, int LANES, int PAIRS, int HEADS>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 5) append_kernel(const AppendParams p) {
     constexpr int kGroups = kThreads / LANES;
     constexpr bool kFarPairs = PAIRS == kFar || PAIRS == kAnyFar;
     __shared__ float rows[PAIRS == kAnyFar ? kThreads * 8 : 1];

@@ -389,26 +389,35 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
     const uint32_t total = start_block(p, scan, cur);
     if (cur.left <= 0) return;
     Cursor ahead = cur;
-    const int chunks = p.d / 4;
+    // copies: this thread's 16 bytes of rows copy_row + i * kRowsPerPass, whose pages are fetched a tile ahead
+    constexpr int kLanes = D / 4, kRowsPerPass = kThreads / kLanes, kPasses = kSimtTile / kRowsPerPass;
+    const int chunk = tid % kLanes, copy_row = tid / kLanes, page_mask = (1 << p.page_shift) - 1;
+    int pages[kPasses];
+    auto fetch = [&]() {
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i)
+            pages[i] = page_of(p, ahead.s, ahead.r, ahead.tile * kSimtTile + copy_row + i * kRowsPerPass);
+    };
     auto load = [&](int stage) {
         if (ahead.left > 0) {
-            const int page_mask = (1 << p.page_shift) - 1;
-            float *dst = ring + stage * 2 * kSimtTile * kLd;
-            for (int x = tid; x < kSimtTile * chunks; x += kThreads) {
-                const int row = x / chunks, ch = x - row * chunks, c = ahead.tile * kSimtTile + row;
-                long long off = 0;
-                if (c < ahead.r.len) {
-                    const int page = checked_page(p, page_of(p, ahead.s, ahead.r, c));
-                    off = ((((long long)page * p.n_kv + ahead.head) << p.page_shift) + (c & page_mask)) * p.d + ch * 4;
+            float *dst = ring + stage * 2 * kSimtTile * kLd + copy_row * kLd + chunk * 4;
+            if (chunk * 4 < p.d) {
+#pragma unroll
+                for (int i = 0; i < kPasses; ++i) {
+                    const int c = ahead.tile * kSimtTile + copy_row + i * kRowsPerPass;
+                    const bool real = c < ahead.r.len;
+                    const int row = real ? ((checked_page(p, pages[i]) * p.n_kv + ahead.head) << p.page_shift) + (c & page_mask) : 0;
+                    const long long off = (long long)row * p.d + chunk * 4;
+                    cp_async16(smem_addr(dst + i * kRowsPerPass * kLd), static_cast<const float *>(p.k) + off, real);
+                    cp_async16(smem_addr(dst + (kSimtTile + i * kRowsPerPass) * kLd), static_cast<const float *>(p.v) + off, real);
                 }
-                cp_async16(smem_addr(dst + row * kLd + ch * 4), static_cast<const float *>(p.k) + off, c < ahead.r.len);
-                cp_async16(smem_addr(dst + (kSimtTile + row) * kLd + ch * 4), static_cast<const float *>(p.v) + off,
-                           c < ahead.r.len);
             }
             ahead.advance(p, 1);
+            if (ahead.left > 0) fetch();
         }
         cp_commit();
     };
+    fetch();
     load(0);
     float o[4][kCols], m[4], l[4];
     bool fresh = true;
