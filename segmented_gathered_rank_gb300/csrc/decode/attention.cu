@@ -260,7 +260,6 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
         if (unit_ends || cur.left == 1) {
             // join the four warps through the stage just used
             const bool whole = unit_ends && start_tile == 0;
-            if (tid == 0 && start_tile == 0 && !unit_ends) record_unit(p, cur, cur.tile, total);
             float *dst = partial_of(p, blockIdx.x, start_tile > 0 ? 0 : 1);
             float *scratch = reinterpret_cast<float *>(smem + stage * Sh::kStage);     // [4][16][D]
             if (!all_warps()) return;
@@ -316,6 +315,7 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
                     }
                 }
             }
+            if (tid == 0 && start_tile == 0 && !unit_ends) record_unit(p, cur, cur.tile, total);
             fence_own_writes();
             fresh = true;
         }
@@ -428,11 +428,14 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
             fresh = false;
             start_tile = cur.tile;
             __syncthreads();
-            for (int x = tid; x < kSimtRows * D; x += kThreads) {
-                const int row = x / D, col = x % D;
-                qs[x] = row < rows && col < p.d
-                            ? static_cast<const float *>(p.q)[row_offset(p, cur, cur.row_tile * p.rt + row) + col]
-                            : 0.f;
+#pragma unroll
+            for (int x = 0; x < kSimtRows / kRowsPerPass; ++x) {
+                const int row = copy_row + x * kRowsPerPass;
+                float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (row < rows && chunk * 4 < p.d)
+                    u = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) +
+                                                          row_offset(p, cur, cur.row_tile * p.rt + row) + chunk * 4);
+                *reinterpret_cast<float4 *>(qs + row * D + chunk * 4) = u;
             }
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
@@ -477,22 +480,35 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
             }
             *reinterpret_cast<float4 *>(ps + (warp * kSimtTile + lane) * 4) = make_float4(w[0], w[1], w[2], w[3]);
             __syncwarp();
-            const bool part = cur.tile * kSimtTile + kSimtTile > cur.r.len - cur.r.n;
+            // drafted values that are not finite must not meet the zero weights of rows that do not see them: they
+            // count as zeros here and are added to the rows that do see them after
+            bool bad = false;
+#pragma unroll 4
             for (int x = 0; x < kSimtTile; ++x) {
                 const float4 pp = *reinterpret_cast<const float4 *>(ps + (warp * kSimtTile + x) * 4);
 #pragma unroll
                 for (int j = 0; j < kCols; ++j) {
-                    const float v = vs[x * kLd + j * 32 + lane];
-                    if (part) {      // what a masked slot holds must not be multiplied
-                        if ((see[0] >> x) & 1) o[0][j] = fmaf(pp.x, v, o[0][j]);
-                        if ((see[1] >> x) & 1) o[1][j] = fmaf(pp.y, v, o[1][j]);
-                        if ((see[2] >> x) & 1) o[2][j] = fmaf(pp.z, v, o[2][j]);
-                        if ((see[3] >> x) & 1) o[3][j] = fmaf(pp.w, v, o[3][j]);
-                    } else {
-                        o[0][j] = fmaf(pp.x, v, o[0][j]);
-                        o[1][j] = fmaf(pp.y, v, o[1][j]);
-                        o[2][j] = fmaf(pp.z, v, o[2][j]);
-                        o[3][j] = fmaf(pp.w, v, o[3][j]);
+                    float v = vs[x * kLd + j * 32 + lane];
+                    if (!(fabsf(v) < INFINITY)) {
+                        bad |= j * 32 + lane < p.d;
+                        v = 0.f;
+                    }
+                    o[0][j] = fmaf(pp.x, v, o[0][j]);
+                    o[1][j] = fmaf(pp.y, v, o[1][j]);
+                    o[2][j] = fmaf(pp.z, v, o[2][j]);
+                    o[3][j] = fmaf(pp.w, v, o[3][j]);
+                }
+            }
+            if (__any_sync(0xffffffffu, bad)) {
+                for (int x = 0; x < kSimtTile; ++x) {
+                    const float4 pp = *reinterpret_cast<const float4 *>(ps + (warp * kSimtTile + x) * 4);
+                    const float w4[4] = {pp.x, pp.y, pp.z, pp.w};
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) {
+                        const float v = vs[x * kLd + j * 32 + lane];
+#pragma unroll
+                        for (int a = 0; a < 4; ++a)
+                            if (!(fabsf(v) < INFINITY) && ((see[a] >> x) & 1)) o[a][j] = fmaf(w4[a], v, o[a][j]);
                     }
                 }
             }
