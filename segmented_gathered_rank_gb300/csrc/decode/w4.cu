@@ -47,20 +47,21 @@ struct BlockWords {
     uint32_t w[2][4];
     uint32_t zero[2], scale[2];
 };
-// A thread's two rows.
-struct Rows {
+// Where a thread's two rows are for a round of blocks.
+struct Place {
     const uint8_t *codes[2], *zeros[2];
     const __nv_bfloat16 *scales[2];
 };
 
+// The block `step` blocks after the place, `left` columns before the row's end; at a row's
+// end the words past it are read from the row's start (x is zero there).
 template <int GROUP>
-__device__ __forceinline__ void load_block(const W4Params &p, const Rows &rows, int block, int t4, BlockWords &b) {
+__device__ __forceinline__ void load_block(const Place &at, bool has_zeros, int step, int left, int t4, BlockWords &b) {
     constexpr int kGroups = kBlock / GROUP;
-    const int g = kGroups == 1 ? block : min(block * kGroups + t4 % kGroups, p.groups - 1);
-    const int left = p.h_in - block * kBlock;      // h_in ends inside the last block at a group's end
+    const int g = step * kGroups + (kGroups > 1 ? min(t4 % kGroups, (left - 1) / GROUP) : 0);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const uint8_t *src = rows.codes[r] + block * (kBlock / 2);
+        const uint8_t *src = at.codes[r] + step * (kBlock / 2);
         if (GROUP == 128) {
             const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src + column<128>(0, t4) / 2));
             b.w[r][0] = u.x;
@@ -70,17 +71,17 @@ __device__ __forceinline__ void load_block(const W4Params &p, const Rows &rows, 
         } else if (GROUP == 64) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint2 u = h * 64 < left ? __ldg(reinterpret_cast<const uint2 *>(src + column<64>(2 * h, t4) / 2)) : make_uint2(0, 0);
+                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src + (h * 64 < left ? column<64>(2 * h, t4) / 2 : 0)));
                 b.w[r][2 * h] = u.x;
                 b.w[r][2 * h + 1] = u.y;
             }
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                b.w[r][j] = j * 32 < left ? __ldg(reinterpret_cast<const uint32_t *>(src + column<32>(j, t4) / 2)) : 0u;
+                b.w[r][j] = __ldg(reinterpret_cast<const uint32_t *>(src + (j * 32 < left ? column<32>(j, t4) / 2 : 0)));
         }
-        b.scale[r] = __ldg(reinterpret_cast<const unsigned short *>(rows.scales[r] + g));
-        b.zero[r] = rows.zeros[r] ? __ldg(rows.zeros[r] + g) : 8u;
+        b.scale[r] = __ldg(reinterpret_cast<const unsigned short *>(at.scales[r] + g));
+        b.zero[r] = has_zeros ? __ldg(at.zeros[r] + g) : 8u;
     }
 }
 
@@ -121,33 +122,27 @@ __device__ __forceinline__ void stage_x(const W4Params &p, int first, int blocks
     }
 }
 
-// 16 bytes of shared memory, where `mine`; else `b` stays as it is.
-__device__ __forceinline__ void lds_if(uint4 &b, uint32_t addr, uint32_t mine) {
-    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %5, 0;\n@p ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n}\n"
-                 : "+r"(b.x), "+r"(b.y), "+r"(b.z), "+r"(b.w)
-                 : "r"(addr), "r"(mine)
-                 : "memory");
-}
-
-// span: blocks of columns whose x fits in shared memory.  run: consecutive blocks that a
-// warp takes at a time (256 bytes of a row: memory is read in longer pieces).
-template <typename E, int GROUP, int NT>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Params p, int tiles, int slices, int span, int run) {
-    constexpr int kGroups = kBlock / GROUP, kParts = sizeof(E) == 2 ? 1 : 3;
+// A warp takes kDepth blocks a round.  LONG: consecutive ones (256 bytes of a row: memory
+// is read in longer pieces); else one of every `slices`, for rows too short for that.
+// span: blocks of columns whose x fits in shared memory, whole rounds of them.
+template <typename E, int GROUP, int NT, bool LONG>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Params p, int tiles, int slices, int span) {
+    constexpr int kGroups = kBlock / GROUP, kParts = sizeof(E) == 2 ? 1 : 3, kBlockX = 4 * kParts * NT * 512;
     extern __shared__ uint4 xs[];
     float *sums = reinterpret_cast<float *>(xs);        // [warp][token][17], at the end
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g4 = lane >> 2, t4 = lane & 3;
-    const int slice = warp % slices, blocks = (p.h_in + kBlock - 1) / kBlock, run_shift = run == 4 ? 2 : run == 2 ? 1 : 0;
+    const int slice = warp % slices, blocks = (p.h_in + kBlock - 1) / kBlock;
+    const int step = LONG ? 1 : slices, round = kDepth * slices, start = LONG ? slice * kDepth : slice;
     const uint32_t x_addr = (uint32_t)__cvta_generic_to_shared(xs) + lane * 16;
-    auto block_at = [&](int q) { return ((((q >> run_shift) * slices) + slice) << run_shift) + (q & (run - 1)); };      // a warp's q-th
+    const bool has_zeros = p.zeros != nullptr;
     for (int n_first = blockIdx.x * tiles * 16; n_first < p.h_out; n_first += gridDim.x * tiles * 16) {
-        Rows rows;
+        Place next;                 // of the round that is being fetched
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const long long n = min(n_first + (warp / slices) * 16 + g4 + r * 8, p.h_out - 1);
-            rows.codes[r] = p.codes + n * (p.h_in / 2);
-            rows.scales[r] = p.scales + n * p.groups;
-            rows.zeros[r] = p.zeros ? p.zeros + n * p.groups : nullptr;
+            next.codes[r] = p.codes + n * (p.h_in / 2) + start * (kBlock / 2);
+            next.scales[r] = p.scales + n * p.groups + start * kGroups;
+            next.zeros[r] = p.zeros + n * p.groups + start * kGroups;
         }
         float acc[NT][4] = {};
         uint4 b[NT];
@@ -156,19 +151,25 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
         BlockWords ring[kDepth];
 #pragma unroll
         for (int i = 0; i < kDepth; ++i)
-            if (block_at(i) < blocks) load_block<GROUP>(p, rows, block_at(i), t4, ring[i]);
-        int q = 0;          // the warp's blocks so far: a multiple of kDepth where a span begins
+            if (start + i * step < blocks)
+                load_block<GROUP>(next, has_zeros, i * step, p.h_in - (start + i * step) * kBlock, t4, ring[i]);
+        int base = start;           // the round's first block
         for (int first = 0; first < blocks; first += span) {
             const int end = min(blocks, first + span);
             if (first > 0 || n_first > (int)blockIdx.x * tiles * 16) __syncthreads();
             stage_x<E, GROUP, NT>(p, first, end - first, xs);
             __syncthreads();
-            for (; block_at(q) < end; q += kDepth) {
+            for (; base < end; base += round) {
 #pragma unroll
-                for (int i = 0; i < kDepth; ++i) {
-                    const int block = block_at(q + i);
-                    if (block >= end) break;
-                    const uint32_t xb = x_addr + (block - first) * (4 * kParts * NT * 512);
+                for (int r = 0; r < 2; ++r) {
+                    next.codes[r] += round * (kBlock / 2);
+                    next.scales[r] += round * kGroups;
+                    next.zeros[r] += round * kGroups;
+                }
+                uint32_t xb = x_addr + (base - first) * kBlockX;
+#pragma unroll
+                for (int i = 0; i < kDepth; ++i, xb += step * kBlockX) {
+                    if (base + i * step >= end) break;
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
                         float c[2][NT][4] = {};        // two chains of sums
@@ -193,7 +194,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int part = kParts - 1; part >= 0; --part) {        // the smallest part first
-                                    lds_if(b[nt], xb + ((j * kParts + part) * NT + nt) * 512, nt * 8 + g4 < p.T);
+                                    if (nt * 8 + g4 < p.T)
+                                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                                                     : "=r"(b[nt].x), "=r"(b[nt].y), "=r"(b[nt].z), "=r"(b[nt].w)
+                                                     : "r"(xb + ((j * kParts + part) * NT + nt) * 512));
                                     mma16816(c[0][nt], a[0][0], a[1][0], a[0][1], a[1][1], b[nt].x, b[nt].y);
                                     mma16816(c[1][nt], a[0][2], a[1][2], a[0][3], a[1][3], b[nt].z, b[nt].w);
                                 }
@@ -204,7 +208,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
                             for (int e = 0; e < 4; ++e)
                                 acc[nt][e] = fmaf(scale[e >> 1], c[0][nt][e] + c[1][nt][e], acc[nt][e]);
                     }
-                    if (block_at(q + i + kDepth) < blocks) load_block<GROUP>(p, rows, block_at(q + i + kDepth), t4, ring[i]);
+                    const int ahead = base + round + i * step;
+                    if (ahead < blocks) load_block<GROUP>(next, has_zeros, i * step, p.h_in - ahead * kBlock, t4, ring[i]);
                 }
             }
         }
@@ -238,12 +243,12 @@ int launch(const W4Params &p, cudaStream_t st) {
     // all of x in shared memory at once, or spans of whole rounds of the ring
     const int most = blocks <= kFit ? kMaxWarps : kFit / kDepth, slices = kMaxWarps / tiles < most ? kMaxWarps / tiles : most;
     const int span = blocks <= kFit ? blocks : kFit / (slices * kDepth) * (slices * kDepth);
-    const int run = blocks >= 4 * slices ? 4 : blocks >= 2 * slices ? 2 : 1;
     const size_t sums = (size_t)tiles * slices * NT * 8 * 17 * sizeof(float);
     const size_t smem = (size_t)span * kBlockBytes > sums ? (size_t)span * kBlockBytes : sums;
     const int need = (row_tiles + tiles - 1) / tiles, grid = need < sms ? need : sms;
-    if (smem_optin(reinterpret_cast<const void *>(w4_rows_kernel<E, GROUP, NT>), smem)) return LORA_ERR_CUDA;
-    w4_rows_kernel<E, GROUP, NT><<<grid, tiles * slices * 32, smem, st>>>(p, tiles, slices, span, run);
+    const auto kernel = blocks >= kDepth * slices ? w4_rows_kernel<E, GROUP, NT, true> : w4_rows_kernel<E, GROUP, NT, false>;
+    if (smem_optin(reinterpret_cast<const void *>(kernel), smem)) return LORA_ERR_CUDA;
+    kernel<<<grid, tiles * slices * 32, smem, st>>>(p, tiles, slices, span);
     count_launch();
     return cuda_status(cudaGetLastError());
 }
