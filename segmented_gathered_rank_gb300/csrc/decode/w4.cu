@@ -6,8 +6,10 @@
 // bf16, so the inner sums run on the tensor cores without rounding the weights, and
 // each group's sum is scaled in fp32.
 //
-// Up to 16 tokens: w4_rows_kernel below, warp MMAs on registers filled straight from
-// memory.  More: w4_tc.cu, whose tcgen05 rate the flops then need.
+// Up to 8 tokens: w4_rows_kernel below, warp MMAs on registers filled straight from
+// memory.  More: w4_tc.cu, whose tcgen05 rate the flops then need (8 tokens, 4096 ->
+// 16384: 17.6 us here, 23.1 there; 16 tokens in two tiles of columns: 23.9, 24.3;
+// 16 in fp32, 4096 -> 4096: 22.2, 13.6).
 #include "w4.cuh"
 
 namespace lora {
@@ -86,19 +88,19 @@ __device__ __forceinline__ void load_block(const Place &at, bool has_zeros, int 
 }
 
 // One thread's operand of 16 bytes: x of one token in one word's columns.  Place of
-// (block, word j, part, token tile nt, lane) in shared memory, 16-byte units.
-template <int NT, int PARTS>
-__device__ __forceinline__ int x_place(int block, int j, int part, int nt, int lane) {
-    return (((block * 4 + j) * PARTS + part) * NT + nt) * 32 + lane;
+// (block, word j, part, lane) in shared memory, 16-byte units.
+template <int PARTS>
+__device__ __forceinline__ int x_place(int block, int j, int part, int lane) {
+    return ((block * 4 + j) * PARTS + part) * 32 + lane;
 }
 
 // x of the columns of blocks [first, first + blocks) into shared memory.
-template <typename E, int GROUP, int NT>
+template <typename E, int GROUP>
 __device__ __forceinline__ void stage_x(const W4Params &p, int first, int blocks, uint4 *xs) {
     constexpr int kParts = sizeof(E) == 2 ? 1 : 3;
     for (int i = threadIdx.x; i < blocks * 16 * p.T; i += blockDim.x) {
         const int t = i / (blocks * 16), x = i - t * (blocks * 16), block = x >> 4, j = (x >> 2) & 3, t4 = x & 3;
-        const int k = (first + block) * kBlock + column<GROUP>(j, t4), lane = (t & 7) * 4 + t4;
+        const int k = (first + block) * kBlock + column<GROUP>(j, t4), lane = t * 4 + t4;
         const E *src = static_cast<const E *>(p.x) + (long long)t * p.h_in + k;
         uint4 part[kParts];
 #pragma unroll
@@ -118,16 +120,16 @@ __device__ __forceinline__ void stage_x(const W4Params &p, int first, int blocks
             }
         }
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) xs[x_place<NT, kParts>(block, j, q, t >> 3, lane)] = part[q];
+        for (int q = 0; q < kParts; ++q) xs[x_place<kParts>(block, j, q, lane)] = part[q];
     }
 }
 
 // A warp takes kDepth blocks a round.  LONG: consecutive ones (256 bytes of a row: memory
 // is read in longer pieces); else one of every `slices`, for rows too short for that.
 // span: blocks of columns whose x fits in shared memory, whole rounds of them.
-template <typename E, int GROUP, int NT, bool LONG>
+template <typename E, int GROUP, bool LONG>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Params p, int tiles, int slices, int span) {
-    constexpr int kGroups = kBlock / GROUP, kParts = sizeof(E) == 2 ? 1 : 3, kBlockX = 4 * kParts * NT * 512;
+    constexpr int kGroups = kBlock / GROUP, kParts = sizeof(E) == 2 ? 1 : 3, kBlockX = 4 * kParts * 512;
     extern __shared__ uint4 xs[];
     float *sums = reinterpret_cast<float *>(xs);        // [warp][token][17], at the end
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g4 = lane >> 2, t4 = lane & 3;
@@ -144,10 +146,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
             next.scales[r] = p.scales + n * p.groups + start * kGroups;
             next.zeros[r] = p.zeros + n * p.groups + start * kGroups;
         }
-        float acc[NT][4] = {};
-        uint4 b[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) b[nt] = make_uint4(0, 0, 0, 0);        // of tokens past T for good
+        float acc[4] = {};
+        uint4 b = make_uint4(0, 0, 0, 0);       // of tokens past T for good
         BlockWords ring[kDepth];
 #pragma unroll
         for (int i = 0; i < kDepth; ++i)
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
         for (int first = 0; first < blocks; first += span) {
             const int end = min(blocks, first + span);
             if (first > 0 || n_first > (int)blockIdx.x * tiles * 16) __syncthreads();
-            stage_x<E, GROUP, NT>(p, first, end - first, xs);
+            stage_x<E, GROUP>(p, first, end - first, xs);
             __syncthreads();
             for (; base < end; base += round) {
 #pragma unroll
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
                     if (base + i * step >= end) break;
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
-                        float c[2][NT][4] = {};        // two chains of sums
+                        float c[2][4] = {};        // two chains of sums
                         float scale[2];
                         __nv_bfloat162 offset[2];
 #pragma unroll
@@ -191,22 +191,17 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
                             code_pairs(ring[i].w[0][j], offset[0], a[0]);
                             code_pairs(ring[i].w[1][j], offset[1], a[1]);
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int part = kParts - 1; part >= 0; --part) {        // the smallest part first
-                                    if (nt * 8 + g4 < p.T)
-                                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-                                                     : "=r"(b[nt].x), "=r"(b[nt].y), "=r"(b[nt].z), "=r"(b[nt].w)
-                                                     : "r"(xb + ((j * kParts + part) * NT + nt) * 512));
-                                    mma16816(c[0][nt], a[0][0], a[1][0], a[0][1], a[1][1], b[nt].x, b[nt].y);
-                                    mma16816(c[1][nt], a[0][2], a[1][2], a[0][3], a[1][3], b[nt].z, b[nt].w);
-                                }
+                            for (int part = kParts - 1; part >= 0; --part) {        // the smallest part first
+                                if (g4 < p.T)
+                                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                                                 : "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                                                 : "r"(xb + (j * kParts + part) * 512));
+                                mma16816(c[0], a[0][0], a[1][0], a[0][1], a[1][1], b.x, b.y);
+                                mma16816(c[1], a[0][2], a[1][2], a[0][3], a[1][3], b.z, b.w);
+                            }
                         }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc[nt][e] = fmaf(scale[e >> 1], c[0][nt][e] + c[1][nt][e], acc[nt][e]);
+                        for (int e = 0; e < 4; ++e) acc[e] = fmaf(scale[e >> 1], c[0][e] + c[1][e], acc[e]);
                     }
                     const int ahead = base + round + i * step;
                     if (ahead < blocks) load_block<GROUP>(next, has_zeros, i * step, p.h_in - ahead * kBlock, t4, ring[i]);
@@ -215,16 +210,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
         }
         __syncthreads();
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sums[(warp * NT * 8 + nt * 8 + t4 * 2 + (e & 1)) * 17 + g4 + (e >> 1) * 8] = acc[nt][e];
+        for (int e = 0; e < 4; ++e) sums[(warp * 8 + t4 * 2 + (e & 1)) * 17 + g4 + (e >> 1) * 8] = acc[e];
         __syncthreads();
         for (int x = threadIdx.x; x < p.T * tiles * 16; x += blockDim.x) {
             const int t = x / (tiles * 16), r = x - t * (tiles * 16), tile = r >> 4;
             if (n_first + r >= p.h_out) continue;
             float s = 0.f;
-            for (int w = 0; w < slices; ++w) s += sums[((tile * slices + w) * NT * 8 + t) * 17 + (r & 15)];
+            for (int w = 0; w < slices; ++w) s += sums[((tile * slices + w) * 8 + t) * 17 + (r & 15)];
             E *dst = static_cast<E *>(p.y) + (long long)t * p.h_out + n_first + r;
             if constexpr (sizeof(E) == 2) *dst = __float2bfloat16_rn(s);
             else *dst = s;
@@ -232,21 +224,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
     }
 }
 
-template <typename E, int GROUP, int NT>
+template <typename E, int GROUP>
 int launch(const W4Params &p, cudaStream_t st) {
     const int sms = num_sms();
     if (sms < 1) return LORA_ERR_CUDA;
     // tiles of 16 rows a block: as few as let one block a SM cover all rows, at most 8
     const int row_tiles = (p.h_out + 15) / 16, each = (row_tiles + sms - 1) / sms, tiles = each < 8 ? each : 8;
     const int blocks = (p.h_in + kBlock - 1) / kBlock;
-    constexpr int kBlockBytes = 4 * (sizeof(E) == 2 ? 1 : 3) * NT * 512, kFit = kXBytes / kBlockBytes;
+    constexpr int kBlockBytes = 4 * (sizeof(E) == 2 ? 1 : 3) * 512, kFit = kXBytes / kBlockBytes;
     // all of x in shared memory at once, or spans of whole rounds of the ring
     const int most = blocks <= kFit ? kMaxWarps : kFit / kDepth, slices = kMaxWarps / tiles < most ? kMaxWarps / tiles : most;
     const int span = blocks <= kFit ? blocks : kFit / (slices * kDepth) * (slices * kDepth);
-    const size_t sums = (size_t)tiles * slices * NT * 8 * 17 * sizeof(float);
+    const size_t sums = (size_t)tiles * slices * 8 * 17 * sizeof(float);
     const size_t smem = (size_t)span * kBlockBytes > sums ? (size_t)span * kBlockBytes : sums;
     const int need = (row_tiles + tiles - 1) / tiles, grid = need < sms ? need : sms;
-    const auto kernel = blocks >= kDepth * slices ? w4_rows_kernel<E, GROUP, NT, true> : w4_rows_kernel<E, GROUP, NT, false>;
+    const auto kernel = blocks >= kDepth * slices ? w4_rows_kernel<E, GROUP, true> : w4_rows_kernel<E, GROUP, false>;
     if (smem_optin(reinterpret_cast<const void *>(kernel), smem)) return LORA_ERR_CUDA;
     kernel<<<grid, tiles * slices * 32, smem, st>>>(p, tiles, slices, span);
     count_launch();
@@ -255,13 +247,10 @@ int launch(const W4Params &p, cudaStream_t st) {
 
 template <typename E>
 int launch(const W4Params &p, int group, cudaStream_t st) {
-    const bool two = p.T > 8;
-    if (group == 128) return two ? launch<E, 128, 2>(p, st) : launch<E, 128, 1>(p, st);
-    if (group == 64) return two ? launch<E, 64, 2>(p, st) : launch<E, 64, 1>(p, st);
-    return two ? launch<E, 32, 2>(p, st) : launch<E, 32, 1>(p, st);
+    return group == 128 ? launch<E, 128>(p, st) : group == 64 ? launch<E, 64>(p, st) : launch<E, 32>(p, st);
 }
 
-constexpr int kRowsTokens = 16;
+constexpr int kRowsTokens = 8;       // one MMA's columns
 
 }  // namespace
 }  // namespace lora

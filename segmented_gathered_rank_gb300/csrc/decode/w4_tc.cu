@@ -294,6 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                     v[i][h] = i < n ? __ldg(reinterpret_cast<const uint4 *>(at + (i0 + i) * step) + h) : make_uint4(0, 0, 0, 0);
             }
         };
+        // every block will want all of x at about the same time: each brings a share of it into L2
+        const size_t bytes = (size_t)p.T * p.h_in * sizeof(E);
+        for (size_t i = ((size_t)blockIdx.x * 128 + tid) * 128; i < bytes; i += (size_t)gridDim.x * 128 * 128)
+            asm volatile("prefetch.global.L2 [%0];\n" ::"l"(static_cast<const char *>(p.x) + i));
         Ring<kStages> ab;
         load(first, 0);
         for (int tile = first; tile < end; ++tile, ab.next()) {
