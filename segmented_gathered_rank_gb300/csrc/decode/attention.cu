@@ -54,7 +54,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 constexpr int kThreads = 128;      // the join kernel's, the fp32 kernel's, the consumers of the MMA kernel
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinRows = 8;
 constexpr int kRows = 16;          // query rows a unit
 
 // This thread's writes to a stage come before the copies that fill it next.
@@ -103,8 +103,37 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
     const int key0 = warp * Sh::kWarpKeys;
     uint32_t qf[D / 16][4], join_phase = 0;
     float o[D / 8][4], m[2], l[2];
-    bool fresh = true;
     int start_tile = cur.tile;
+    // a new unit: its queries, straight into MMA fragments, and nothing seen yet
+    auto load_queries = [&](const Cursor &c) {
+        const int rows = min(kRows, c.r.n * p.group - c.row_tile * kRows);
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const int row = hh * 8 + g4;
+            const __nv_bfloat16 *src =
+                static_cast<const __nv_bfloat16 *>(p.q) + (row < rows ? row_offset(p, c, c.row_tile * kRows + row) : 0);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const int col = ks * 16 + kk * 8 + t4 * 2;
+                    qf[ks][kk * 2 + hh] = row < rows && col < p.d ? *reinterpret_cast<const uint32_t *>(src + col) : 0u;
+                }
+        }
+    };
+    auto clear = [&]() {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            m[hh] = -INFINITY;
+            l[hh] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+    };
+    load_queries(cur);
+    clear();
     auto all_warps = [&]() {
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.join);
@@ -115,29 +144,6 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
         uint8_t *vs = smem + stage * Sh::kStage + Sh::kHalf;
         const uint32_t ks_base = base + stage * Sh::kStage, vs_base = ks_base + Sh::kHalf;
         const int rows = min(kRows, cur.r.n * p.group - cur.row_tile * kRows);
-        if (fresh) {        // a new unit: its queries, straight into MMA fragments
-            fresh = false;
-            start_tile = cur.tile;
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-                const int row = hh * 8 + g4;
-                const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) +
-                                           (row < rows ? row_offset(p, cur, cur.row_tile * kRows + row) : 0);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        const int col = ks * 16 + kk * 8 + t4 * 2;
-                        qf[ks][kk * 2 + hh] = row < rows && col < p.d ? *reinterpret_cast<const uint32_t *>(src + col) : 0u;
-                    }
-                m[hh] = -INFINITY;
-                l[hh] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-        }
         if (!wait_warp(&ctl.full[stage], (it / Sh::kStages) & 1, ctl)) return;
         const int c0 = cur.tile * Sh::kTile + key0;         // first cached token of this warp's keys
         const int drafted = cur.r.len - cur.r.n - c0;       // the first of them that a mask rules
@@ -262,6 +268,9 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
             const bool whole = unit_ends && start_tile == 0;
             float *dst = partial_of(p, blockIdx.x, start_tile > 0 ? 0 : 1);
             float *scratch = reinterpret_cast<float *>(smem + stage * Sh::kStage);     // [4][16][D]
+            Cursor after = cur;
+            after.advance(p, 1);
+            if (after.left > 0) load_queries(after);      // on their way while this unit is joined
             if (!all_warps()) return;
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
@@ -281,8 +290,9 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
                 }
             }
             if (!all_warps()) return;
-            for (int x = tid; x < 16 * (D / 4); x += kThreads) {
-                const int row = x & 15, col = (x >> 4) * 4;
+            const int shift = rows <= 4 ? 2 : rows <= 8 ? 3 : 4;
+            for (int x = tid; x < (D / 4) << shift; x += kThreads) {
+                const int row = x & ((1 << shift) - 1), col = (x >> shift) * 4;
                 if (row >= rows || col >= p.d) continue;
                 float top = ctl.row_max[0][row];
 #pragma unroll
@@ -317,7 +327,12 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
             }
             if (tid == 0 && start_tile == 0 && !unit_ends) record_unit(p, cur, cur.tile, total);
             fence_own_writes();
-            fresh = true;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&ctl.empty[stage]);
+            clear();
+            cur = after;
+            start_tile = cur.tile;
+            continue;
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&ctl.empty[stage]);
@@ -554,25 +569,25 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const JoinRecord rec = p.records[c];
-    const int across = (p.d + 15) >> 4, items = ((rec.rows + 7) >> 3) * across;
-    for (int x = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); x < items; x += gridDim.y * (kJoinThreads / 32)) {
+    const int across = (p.d + 15) >> 4, pieces = ((rec.rows + 7) >> 3) * across;
+    for (int x = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); x < pieces; x += gridDim.y * (kJoinThreads / 32)) {
         const int row = (x / across) * 8 + (lane & 7), col = (x % across) * 16 + (lane >> 3) * 4;
         if (row >= rec.rows || col >= p.d) continue;
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int b = 0; b < rec.parts; ++b) {
-            const float *src = partial_of(p, c + b, b == 0 ? 1 : 0);
+#pragma unroll 8
+        for (int i = 0; i < rec.parts; ++i) {
+            const float *src = partial_of(p, c + i, i == 0 ? 1 : 0);
             const float2 ml = *reinterpret_cast<const float2 *>(src + p.rt * p.d + row * 2);
             const float4 u = *reinterpret_cast<const float4 *>(src + partial_at(p, row, col));
             const float top = fmaxf(m, ml.x), ref = top == -INFINITY ? 0.f : top;
-            const float a = exp2f(m - ref), w = exp2f(ml.x - ref);
+            const float old = exp2f(m - ref), w = exp2f(ml.x - ref);
             m = top;
-            l = l * a + ml.y * w;
-            o.x = o.x * a + u.x * w;
-            o.y = o.y * a + u.y * w;
-            o.z = o.z * a + u.z * w;
-            o.w = o.w * a + u.w * w;
+            l = l * old + ml.y * w;
+            o.x = o.x * old + u.x * w;
+            o.y = o.y * old + u.y * w;
+            o.z = o.z * old + u.z * w;
+            o.w = o.w * old + u.w * w;
         }
         const float r = l == 0.f ? 0.f : 1.f / l;
         const int unit_row = rec.first_row + row, i = unit_row / p.group;
@@ -598,7 +613,7 @@ Variant variant_of(const lora_kv_pages *kv, int group, int S, int T) {
     const long long rows = (long long)T * group;       // against S: rows a request and kv head, on average
     if ((d == 64 || d == 128) && rows > (long long)kRows * S) return {true, rows > 128LL * S ? 256 : 128, 128, 1, 8};
     const bool tma = kv->page_size >= kTmaMinPage;
-    return {false, kRows, d <= 64 ? 128 : 64, tma && d <= 128 ? 2 : 1, 4};
+    return {false, kRows, d <= 64 ? 128 : 64, tma && d <= 128 ? 2 : 1, 2};
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -729,7 +744,7 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     if ((rc = launch_attention(kv, p, variant, st))) return rc;
     // the join starts while the last blocks run; it waits for them before it reads their sums
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.grid, p.rt <= 16 ? 1 : p.rt / 16);       // two rows a warp
+    cfg.gridDim = dim3(p.grid, p.rt / kJoinRows);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

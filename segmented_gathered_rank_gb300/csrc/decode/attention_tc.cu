@@ -386,15 +386,18 @@ __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t 
         float m = -INFINITY, l = 0.f;
         const long long my_off = live ? row_offset(p, cur, cur.row_tile * p.rt + ur) : -1;     // in q and out
         if (active) {
-            // the warp's 32 rows, D / 8 lanes a row
+            // the warp's 32 rows, D / 8 lanes a row; all loads before the first store (which might alias them)
+            uint4 u[D / 8];
 #pragma unroll
             for (int x = 0; x < D / 8; ++x) {
-                const int rr = x * (256 / D) + lane / (D / 8), c = lane % (D / 8);
-                const long long off = __shfl_sync(0xffffffffu, my_off, rr);
-                uint4 u = make_uint4(0, 0, 0, 0);
-                if (off >= 0) u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + off + c * 8);
-                *reinterpret_cast<uint4 *>(my_q + panel_off(kTile, (warp & 3) * 32 + rr, c)) = u;
+                const long long off = __shfl_sync(0xffffffffu, my_off, x * (256 / D) + lane / (D / 8));
+                u[x] = make_uint4(0, 0, 0, 0);
+                if (off >= 0)
+                    u[x] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + off) + lane % (D / 8));
             }
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x)
+                *reinterpret_cast<uint4 *>(my_q + panel_off(kTile, (warp & 3) * 32 + x * (256 / D) + lane / (D / 8), lane % (D / 8))) = u[x];
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
@@ -574,12 +577,14 @@ __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t 
         }
         if (seg.whole && active && warp_live && (NQ == 2 || w == 0)) {
             __syncwarp();
+            uint4 u[D / 8];
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x)
+                u[x] = *reinterpret_cast<const uint4 *>(my_q + panel_off(kTile, (warp & 3) * 32 + x * (256 / D) + lane / (D / 8), lane % (D / 8)));
 #pragma unroll
             for (int x = 0; x < D / 8; ++x) {
-                const int rr = x * (256 / D) + lane / (D / 8), c = lane % (D / 8);
-                const long long off = __shfl_sync(0xffffffffu, my_off, rr);
-                const uint4 u = *reinterpret_cast<const uint4 *>(my_q + panel_off(kTile, (warp & 3) * 32 + rr, c));
-                if (off >= 0) *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + off + c * 8) = u;
+                const long long off = __shfl_sync(0xffffffffu, my_off, x * (256 / D) + lane / (D / 8));
+                if (off >= 0) *(reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + off) + lane % (D / 8)) = u[x];
             }
             __syncwarp();
         }

@@ -89,13 +89,18 @@ struct TmaCopy {
     // Rows `first` on of a landed V tile: rows from `end` on become zeros, values that are not finite
     // too; returns whether there were any such (masked, they would enter the product times zero).
     __device__ __forceinline__ bool clean(const AttnParams &p, uint8_t *tile, int first, int end, int lane) const {
+        for (int x = lane; x < (TILE - end) * (D / 8); x += 32)
+            *reinterpret_cast<uint4 *>(tile + panel_off(TILE, end + x / (D / 8), x % (D / 8))) = make_uint4(0, 0, 0, 0);
+        const int last = min(end, TILE), count = (last - first) * (D / 8);
         bool found = false;
-        for (int x = lane; x < (TILE - first) * (D / 8); x += 32) {
-            const int r = first + x / (D / 8);
-            uint4 *at = reinterpret_cast<uint4 *>(tile + panel_off(TILE, r, x % (D / 8)));
-            if (r >= end) *at = make_uint4(0, 0, 0, 0);
-            else found |= make_finite(at);
+#pragma unroll 4
+        for (int x = lane; x < count; x += 32) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(tile + panel_off(TILE, first + x / (D / 8), x % (D / 8)));
+            found |= non_finite2(u.x) || non_finite2(u.y) || non_finite2(u.z) || non_finite2(u.w);
         }
+        if (found)
+            for (int x = lane; x < count; x += 32)
+                make_finite(reinterpret_cast<uint4 *>(tile + panel_off(TILE, first + x / (D / 8), x % (D / 8))));
         return found;
     }
 };
