@@ -362,6 +362,27 @@ __device__ __forceinline__ void load_scores(float *s, uint32_t taddr, bool maske
 
 // One thread a row: its queries into shared memory, the softmax of its scores,
 // and at the end of the segment its output.
+// A softmax thread's row of its stream, and where the unit's row lies in q and out (-1: none).
+template <int NQ>
+__device__ __forceinline__ long long row_at(const AttnParams &p, const Cursor &cur) {
+    const int warp = threadIdx.x >> 5, row = (warp & 3) * 32 + (threadIdx.x & 31) + (NQ == 2 ? (warp >> 2) * kTile : 0);
+    return row < cur.r.n * p.group - cur.row_tile * p.rt ? row_offset(p, cur, cur.row_tile * p.rt + row) : -1;
+}
+// Starts the copies of the queries of a warp's 32 rows, D / 8 lanes a row (no row: zeros).
+template <int D>
+__device__ __forceinline__ void load_queries(const AttnParams &p, long long my_off, uint8_t *queries) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t dst = smem_u32(queries) + (warp >> 2) * TcShape<D>::kSlot;
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x) {
+        const int rr = x * (256 / D) + lane / (D / 8), c = lane % (D / 8);
+        const long long off = __shfl_sync(0xffffffffu, my_off, rr);
+        cp_async16(dst + panel_off(kTile, (warp & 3) * 32 + rr, c), static_cast<const __nv_bfloat16 *>(p.q) + (off >= 0 ? off + c * 8 : 0),
+                   off >= 0);
+    }
+}
+
+// The first unit's queries are on their way.
 template <int D, int NQ>
 __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t *queries, Control *ctl) {
     using Sh = TcShape<D>;
@@ -384,20 +405,9 @@ __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t 
         const bool live = ur < rows, warp_live = ur - lane < rows;
         const bool active = NQ == 2 ? (w == 0 || rows > kTile) : (w == 0 || seg.tiles > 1);
         float m = -INFINITY, l = 0.f;
-        const long long my_off = live ? row_offset(p, cur, cur.row_tile * p.rt + ur) : -1;     // in q and out
+        const long long my_off = row_at<NQ>(p, cur);
         if (active) {
-            // the warp's 32 rows, D / 8 lanes a row; all loads before the first store (which might alias them)
-            uint4 u[D / 8];
-#pragma unroll
-            for (int x = 0; x < D / 8; ++x) {
-                const long long off = __shfl_sync(0xffffffffu, my_off, x * (256 / D) + lane / (D / 8));
-                u[x] = make_uint4(0, 0, 0, 0);
-                if (off >= 0)
-                    u[x] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.q) + off) + lane % (D / 8));
-            }
-#pragma unroll
-            for (int x = 0; x < D / 8; ++x)
-                *reinterpret_cast<uint4 *>(my_q + panel_off(kTile, (warp & 3) * 32 + x * (256 / D) + lane / (D / 8), lane % (D / 8))) = u[x];
+            cp_wait_all();
             fence_proxy_async();
             __syncwarp();
             if (lane == 0) {
@@ -592,7 +602,9 @@ __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t 
         if (threadIdx.x == 0 && seg.first == 0 && !seg.whole) record_unit(p, cur, seg.tiles - 1, total);
         seq0 += 2 * seg.tiles;
         cur.advance(p, seg.tiles);
+        if (cur.left > 0) load_queries<D>(p, row_at<NQ>(p, cur), queries);
     }
+    cp_wait_all();
 }
 
 template <int D, int NQ, bool TMA>
@@ -632,6 +644,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
     Cursor cur;
     const uint32_t total = start_block(p, scan, cur);
+    // the first queries are requested before the ring's tiles, which would keep them waiting
+    if (warp < kProducer0 && cur.left > 0) load_queries<D>(p, row_at<NQ>(p, cur), queries);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
