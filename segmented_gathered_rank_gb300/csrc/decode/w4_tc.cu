@@ -3,7 +3,7 @@
 // At 64 tokens the flops (128 a weight) need more than the warp-MMA rate while the
 // codes still come at half a byte a weight.  A thread block has 128 rows of W:
 //   one warp     copies code tiles (128 rows x 256 columns) by tensor copies;
-//   eight warps  turn codes less zeros into bf16 (exact) in tensor memory, the A
+//   twelve warps turn codes less zeros into bf16 (exact) in tensor memory, the A
 //                operand (through shared memory its 32 KB a tile, written and read
 //                again, would bound the kernel: 47 against 36 us at 64 x 4096 -> 16384);
 //   four warps   put x into shared memory, the B operand (fp32 x: three bf16 parts,
@@ -24,23 +24,23 @@ using namespace decode;
 using namespace tc;
 
 constexpr int kRows = 128, kCols = 128;          // of W, a tile
-constexpr int kThreads = 20 * 32;
-constexpr int kScaleWarp0 = 8, kXWarp0 = 12, kCopyWarp = 16, kMmaWarp = 17;     // warpgroups of one kind
+constexpr int kThreads = 24 * 32, kTurns = 3;
+constexpr int kScaleWarp0 = 4 * kTurns, kXWarp0 = kScaleWarp0 + 4, kCopyWarp = kXWarp0 + 4, kMmaWarp = kCopyWarp + 1;      // warpgroups of one kind
 constexpr int kCodeBytes = kRows * kCols, kACols = kCols / 2;      // codes of two tiles; tensor memory columns of an A tile
 constexpr uint32_t kTmemCols = 512;
-constexpr int kAccumulators = 4, kStages = 3, kACol0 = 256;
+constexpr int kAccumulators = 4, kStages = kTurns, kACol0 = 256;
 
 template <typename E, int NTOK>
 struct W4Shape {
     static constexpr int kParts = sizeof(E) == 2 ? 1 : 3;
     static constexpr int kBPart = NTOK * kCols * 2;
     static constexpr int kStage = kParts * kBPart;
-    static constexpr int kCodes = 4;
+    static constexpr int kCodes = kParts == 1 ? 8 : 4;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + (size_t)kCodes * kCodeBytes;
 };
 
 struct W4Control {
-    uint64_t codes_full[4], codes_free[4], ab_full[kStages], ab_free[kStages], d_full[kAccumulators], d_free[kAccumulators], drain;
+    uint64_t codes_full[8], codes_free[8], ab_full[kStages], ab_free[kStages], d_full[kAccumulators], d_free[kAccumulators], drain;
     volatile int abort;
     uint32_t tmem;
 };
@@ -72,15 +72,20 @@ struct Ring {
 __device__ __forceinline__ uint32_t tile_off(int rows, int row, int chunk) {
     return (uint32_t)((chunk >> 3) * (rows * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
-// D[tmem] (+)= A[tmem] . B[smem]^T, A as bf16 pairs in columns.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] . B[smem]^T, A as bf16 pairs in columns; b_lo: the lower half of
+// B's descriptor (128-byte swizzling, K-major), whose upper half is constant.
+template <uint32_t IDESC>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t accumulate) {
+    constexpr uint32_t kSwizzled = (1024u >> 4) | (1u << 14) | (2u << 29);
     asm volatile(
         "{\n"
         ".reg .pred p;\n"
-        "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+        ".reg .b64 b;\n"
+        "setp.ne.b32 p, %5, 0;\n"
+        "mov.b64 b, {%2, %3};\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n"
         "}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "r"(a_tmem), "r"(b_lo), "n"(kSwizzled), "n"(IDESC), "r"(accumulate)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
@@ -151,10 +156,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
         if constexpr (sizeof(E) == 2) *dst = __float2bfloat16_rn(v);
         else *dst = v;
     };
-    // registers: five warpgroups start with 96 a thread; 2 x 96 + 152 + 88 + 40 is less than five times that
+    // registers: six warpgroups start with 80 a thread; 3 x 80 + 136 + 64 + 40 is the same sum
     if (warp < kScaleWarp0) {
-        // the codes of a row of the tile a thread; the two warpgroups take turns, so that one's waits
-        // lie under the other's work
+        // the codes of a row of the tile a thread; the warpgroups take turns (and have a stage each), so
+        // that one's waits lie under the others' work
         const int row = threadIdx.x & 127;
         const long long n = min(n0 + row, p.h_out - 1);
         const uint8_t *zeros = p.zeros ? p.zeros + n * p.groups : nullptr;
@@ -164,21 +169,20 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) z[i] = zeros ? __ldg(zeros + min(tile * kGroups + i, p.groups - 1)) : 8u;
         };
-        Ring<Sh::kCodes> c;
-        Ring<kStages> ab;
-        int tile = first + (warp >> 2);
-        if (warp >> 2) ab.next();
-        fetch(tile, zero);
-        for (; tile < end; tile += 2) {
-            fetch(tile + 2, next);
-            if (!wait_warp(&ctl.codes_full[c.at], c.parity, ctl)) break;
-            const uint8_t *src = codes + c.at * kCodeBytes + row * 128;
+        const int turn = warp >> 2;
+        uint32_t parity = 0;
+        fetch(first + turn, zero);
+        for (int rel = turn; first + rel < end; rel += kTurns, parity ^= 1) {
+            fetch(first + rel + kTurns, next);
+            const int slot = (rel >> 1) % Sh::kCodes;
+            if (!wait_warp(&ctl.codes_full[slot], (rel >> 1) / Sh::kCodes & 1, ctl)) break;
+            const uint8_t *src = codes + slot * kCodeBytes + row * 128;
             uint4 w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)      // tensor copies with 128-byte swizzling: 16-byte chunks XORed with the row
-                w[i] = *reinterpret_cast<const uint4 *>(src + ((((warp >> 2) * 4 + i) ^ (row & 7)) << 4));
+                w[i] = *reinterpret_cast<const uint4 *>(src + ((((rel & 1) * 4 + i) ^ (row & 7)) << 4));
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.codes_free[c.at]);
+            if (lane == 0) mbar_arrive(&ctl.codes_free[slot]);
             bool ok = true;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -196,23 +200,20 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                         for (int e = 0; e < 4; ++e) a[(i * 4 + j) * 4 + e] = o[e];
                     }
                 }
-                if (h == 0 && !(ok = wait_warp(&ctl.ab_free[ab.at], ab.parity ^ 1, ctl))) break;
-                tmem_st32(a_tmem + ab.at * kACols + h * 32, a);
+                if (h == 0 && !(ok = wait_warp(&ctl.ab_free[turn], parity ^ 1, ctl))) break;
+                tmem_st32(a_tmem + turn * kACols + h * 32, a);
             }
             if (!ok) break;
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.ab_full[ab.at]);
-            c.next();
-            ab.next();
-            ab.next();
+            if (lane == 0) mbar_arrive(&ctl.ab_full[turn]);
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) zero[i] = next[i];
         }
     } else if (warp < kXWarp0) {
         // this thread's row: each group's sums, scaled
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;\n");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 136;\n");
         float2 acc[NTOK / 2];
 #pragma unroll
         for (int t = 0; t < NTOK / 2; ++t) acc[t] = make_float2(0.f, 0.f);
@@ -273,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             }
         }
     } else if (warp < kCopyWarp) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
         // x of the tile's columns, in the order of code_pairs; tokens past T are zeros.  Each thread's pieces
         // of the next tile are on their way while this one's are written.
         const int tid = threadIdx.x - kXWarp0 * 32;
@@ -345,14 +346,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
       } else if (warp == kMmaWarp) {
         if (elect_lane()) {
             constexpr uint32_t idesc = idesc_bf16_f32(kRows, NTOK);
-            const uint64_t b0 = desc_kmajor_sw128(smem_u32(smem));
+            const uint32_t b0 = (uint32_t)desc_kmajor_sw128(smem_u32(smem)), tmem = ctl.tmem;
             Ring<kStages> ab;
             Ring<kAccumulators> d;
             for (int tile = first; tile < end; ++tile, ab.next()) {
                 if (!wait_bar(&ctl.ab_full[ab.at], ab.parity, ctl)) break;
                 fence_after_sync();
-                const uint32_t a = ctl.tmem + kACol0 + ab.at * kACols;
-                const uint64_t b = b0 + ab.at * (Sh::kStage / 16);
+                const uint32_t a = tmem + kACol0 + ab.at * kACols, b = b0 + ab.at * (Sh::kStage / 16);
                 bool ok = true;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g, d.next()) {
@@ -362,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                     for (int q = Sh::kParts - 1; q >= 0; --q)      // the smallest part first
 #pragma unroll
                         for (int ks = g * (8 / kGroups); ks < (g + 1) * (8 / kGroups); ++ks)
-                            mma_ts(ctl.tmem + d.at * NTOK, a + ks * 8,
-                                   b + (q * Sh::kBPart + (ks >> 2) * (NTOK * 128) + (ks & 3) * 32) / 16, idesc,
-                                   q < Sh::kParts - 1 || ks > g * (8 / kGroups));
+                            mma_ts<idesc>(tmem + d.at * NTOK, a + ks * 8,
+                                          b + (q * Sh::kBPart + (ks >> 2) * (NTOK * 128) + (ks & 3) * 32) / 16,
+                                          q < Sh::kParts - 1 || ks > g * (8 / kGroups));
                     mma_commit(&ctl.d_full[d.at]);
                 }
                 if (!ok) break;
