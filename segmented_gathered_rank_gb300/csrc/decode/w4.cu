@@ -55,17 +55,42 @@ struct Place {
     const __nv_bfloat16 *scales[2];
 };
 
+// Codes are read once a call: they leave L2 first.
+__device__ __forceinline__ uint64_t once_policy() {
+    uint64_t policy;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(policy));
+    return policy;
+}
+__device__ __forceinline__ uint4 ld_once(const uint4 *p, uint64_t policy) {
+    uint4 u;
+    asm volatile("ld.global.nc.L2::cache_hint.v4.b32 {%0, %1, %2, %3}, [%4], %5;\n"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "l"(p), "l"(policy));
+    return u;
+}
+__device__ __forceinline__ uint2 ld_once(const uint2 *p, uint64_t policy) {
+    uint2 u;
+    asm volatile("ld.global.nc.L2::cache_hint.v2.b32 {%0, %1}, [%2], %3;\n" : "=r"(u.x), "=r"(u.y) : "l"(p), "l"(policy));
+    return u;
+}
+__device__ __forceinline__ uint32_t ld_once(const uint32_t *p, uint64_t policy) {
+    uint32_t u;
+    asm volatile("ld.global.nc.L2::cache_hint.b32 %0, [%1], %2;\n" : "=r"(u) : "l"(p), "l"(policy));
+    return u;
+}
+
 // The block `step` blocks after the place, `left` columns before the row's end; at a row's
 // end the words past it are read from the row's start (x is zero there).
 template <int GROUP>
-__device__ __forceinline__ void load_block(const Place &at, bool has_zeros, int step, int left, int t4, BlockWords &b) {
+__device__ __forceinline__ void load_block(const Place &at, bool has_zeros, int step, int left, int t4, uint64_t policy,
+                                           BlockWords &b) {
     constexpr int kGroups = kBlock / GROUP;
     const int g = step * kGroups + (kGroups > 1 ? min(t4 % kGroups, (left - 1) / GROUP) : 0);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const uint8_t *src = at.codes[r] + step * (kBlock / 2);
         if (GROUP == 128) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src + column<128>(0, t4) / 2));
+            const uint4 u = ld_once(reinterpret_cast<const uint4 *>(src + column<128>(0, t4) / 2), policy);
             b.w[r][0] = u.x;
             b.w[r][1] = u.y;
             b.w[r][2] = u.z;
@@ -73,14 +98,14 @@ __device__ __forceinline__ void load_block(const Place &at, bool has_zeros, int 
         } else if (GROUP == 64) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(src + (h * 64 < left ? column<64>(2 * h, t4) / 2 : 0)));
+                const uint2 u = ld_once(reinterpret_cast<const uint2 *>(src + (h * 64 < left ? column<64>(2 * h, t4) / 2 : 0)), policy);
                 b.w[r][2 * h] = u.x;
                 b.w[r][2 * h + 1] = u.y;
             }
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                b.w[r][j] = __ldg(reinterpret_cast<const uint32_t *>(src + (j * 32 < left ? column<32>(j, t4) / 2 : 0)));
+                b.w[r][j] = ld_once(reinterpret_cast<const uint32_t *>(src + (j * 32 < left ? column<32>(j, t4) / 2 : 0)), policy);
         }
         b.scale[r] = __ldg(reinterpret_cast<const unsigned short *>(at.scales[r] + g));
         b.zero[r] = has_zeros ? __ldg(at.zeros[r] + g) : 8u;
@@ -137,6 +162,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
     const int step = LONG ? 1 : slices, round = kDepth * slices, start = LONG ? slice * kDepth : slice;
     const uint32_t x_addr = (uint32_t)__cvta_generic_to_shared(xs) + lane * 16;
     const bool has_zeros = p.zeros != nullptr;
+    const uint64_t policy = once_policy();
     for (int n_first = blockIdx.x * tiles * 16; n_first < p.h_out; n_first += gridDim.x * tiles * 16) {
         Place next;                 // of the round that is being fetched
 #pragma unroll
@@ -152,7 +178,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
 #pragma unroll
         for (int i = 0; i < kDepth; ++i)
             if (start + i * step < blocks)
-                load_block<GROUP>(next, has_zeros, i * step, p.h_in - (start + i * step) * kBlock, t4, ring[i]);
+                load_block<GROUP>(next, has_zeros, i * step, p.h_in - (start + i * step) * kBlock, t4, policy, ring[i]);
         int base = start;           // the round's first block
         for (int first = 0; first < blocks; first += span) {
             const int end = min(blocks, first + span);
@@ -204,7 +230,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
                         for (int e = 0; e < 4; ++e) acc[e] = fmaf(scale[e >> 1], c[0][e] + c[1][e], acc[e]);
                     }
                     const int ahead = base + round + i * step;
-                    if (ahead < blocks) load_block<GROUP>(next, has_zeros, i * step, p.h_in - ahead * kBlock, t4, ring[i]);
+                    if (ahead < blocks) load_block<GROUP>(next, has_zeros, i * step, p.h_in - ahead * kBlock, t4, policy, ring[i]);
                 }
             }
         }

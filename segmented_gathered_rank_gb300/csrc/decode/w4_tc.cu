@@ -335,11 +335,18 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
       asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
       if (warp == kCopyWarp) {
         if (elect_lane()) {
+            // codes are read once a call: they leave L2 first
+            uint64_t policy;
+            asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(policy));
             Ring<Sh::kCodes> c;
             for (int tile = first; tile < end; tile += 2, c.next()) {
                 if (!wait_bar(&ctl.codes_free[c.at], c.parity ^ 1, ctl)) break;
                 mbar_arrive_expect_tx(&ctl.codes_full[c.at], kCodeBytes);
-                tma_load_2d(codes + c.at * kCodeBytes, &map, tile * (kCols / 2), n0, &ctl.codes_full[c.at]);
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint "
+                    "[%0], [%1, {%2, %3}], [%4], %5;\n" ::"r"(smem_u32(codes + c.at * kCodeBytes)),
+                    "l"(&map), "r"(tile * (kCols / 2)), "r"(n0), "r"(smem_u32(&ctl.codes_full[c.at])), "l"(policy)
+                    : "memory");
             }
         }
         __syncwarp();
