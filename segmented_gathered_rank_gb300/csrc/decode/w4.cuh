@@ -38,21 +38,27 @@ __device__ __forceinline__ void pair_x(uint4 x, uint32_t (&out)[4]) {
     out[2] = __byte_perm(x.y, x.w, 0x5410);
     out[3] = __byte_perm(x.y, x.w, 0x7632);
 }
-// fp32 x as three bf16 parts, 24 bits in all, in the order of code_pairs.  A part that
-// is not finite has no remainder (infinity less itself would be NaN).
+// fp32 x as three bf16 parts in the order of code_pairs: the leading 8 bits, the next
+// 8 and the rest, which is exact.  What is not finite has no rest (infinity less
+// itself would be NaN), and a NaN stays one without its lower bits.
 __device__ __forceinline__ void split_x(const float (&x)[8], uint32_t (&hi)[4], uint32_t (&mid)[4], uint32_t (&lo)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        float a = x[k], b = x[k + 4];
-        uint32_t *parts[3] = {&hi[k], &mid[k], &lo[k]};
+        uint32_t first[2], second[2];
+        float rest[2];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-            *parts[i] = *reinterpret_cast<const uint32_t *>(&h);
-            const float2 f = __bfloat1622float2(h);
-            a = isfinite(f.x) ? a - f.x : 0.f;
-            b = isfinite(f.y) ? b - f.y : 0.f;
+        for (int i = 0; i < 2; ++i) {
+            const float f = x[k + 4 * i];
+            const bool finite = fabsf(f) < INFINITY;
+            first[i] = __float_as_uint(f) | (f != f ? 0x00400000u : 0u);
+            const float r = finite ? f - __uint_as_float(first[i] & 0xffff0000u) : 0.f;
+            second[i] = __float_as_uint(r);
+            rest[i] = r - __uint_as_float(second[i] & 0xffff0000u);
         }
+        hi[k] = __byte_perm(first[0], first[1], 0x7632);
+        mid[k] = __byte_perm(second[0], second[1], 0x7632);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(rest[0], rest[1]);
+        lo[k] = *reinterpret_cast<const uint32_t *>(&h);
     }
 }
 
