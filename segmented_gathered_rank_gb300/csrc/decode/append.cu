@@ -5,12 +5,14 @@
 // over the pairs of the first rot elements; values are copied.  The bytes are
 // each head read once and written once: memory is the bound for large T, the
 // chain of dependent loads (position -> table row; slot -> address) for small.
+// Measured, bf16, heads of 128: 1 token 2.0 us, 256 tokens of 48 heads with norms
+// 3.0 us, 8192 tokens 39.8 us (5.2 TB/s).
 //
-// Layout: LANES threads (the power of two >= d/8) hold one head, 8 elements each,
-// so the sum of squares is a few shuffles and the partner of a half-split pair is a
-// shuffle away (or, when rot/2 is no multiple of 8, in a row of shared memory).  A
-// block takes the heads of one token, kHeads a thread at a time with their loads in
-// flight together; its lanes keep their elements' cosines and sines for all heads.
+// Layout: LANES threads (the power of two >= d/8) hold one head, 8 elements each in two
+// quads that are each other's partners in the rotation, so a pair meets in a thread (or,
+// when rot is no multiple of 8, in a row of shared memory).  A block takes heads of one
+// token, several a thread for long batches; its lanes keep their pairs' cosines and
+// sines for all of them.
 #include "decode.cuh"
 
 namespace lora {
@@ -19,7 +21,15 @@ namespace {
 using namespace decode;
 
 constexpr int kThreads = 256;
-constexpr int kHeads = 3, kManyBlocks = 4096;
+// Heads a thread when neighbours pair up and one head a thread would make more than
+// kManyBlocks blocks: the loads of three heads are in flight at once, and position, slot
+// and table row are read once for them.  bf16, 48 heads of 128, one against three:
+// 256 tokens (768 blocks) 2.8 and 2.9 us, 512 tokens 3.9 and 3.6, 4096 tokens 26.7 and
+// 22.6; 8192 tokens: 1, 2, 3, 4, 6 heads took 55.0, 48.9, 43.9, 44.9, 47.0 at
+// four blocks an SM, and 39.8 with three at five blocks an SM.  Halves that pair up are read in 8-byte
+// pieces, and there one head a thread is as fast or faster throughout (4096 tokens 27.3
+// against 30.2 us, 512 tokens 3.9 against 4.9), so they always take it.
+constexpr int kHeads = 3, kManyBlocks = 1500;
 
 struct AppendParams {
     const void *q, *k, *v;
@@ -30,7 +40,7 @@ struct AppendParams {
     const float *cos_sin;
     int n_pos, rot;
     const void *q_norm, *k_norm;
-    float eps;
+    float eps, inv_d;
     void *q_out, *k_pages, *v_pages;
     long long n_slots;
     int *status;
@@ -42,44 +52,95 @@ __device__ __forceinline__ unsigned group_mask() {
     return LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << ((threadIdx.x & 31) / LANES * LANES);
 }
 
-// Eight elements as loaded, and as floats.
+// Four elements, as loaded and as floats.
 template <typename E>
-struct Held {
-    uint4 v[sizeof(E) / 2];
-    __device__ __forceinline__ void load(const E *p) {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(E) / 2; ++i) v[i] = reinterpret_cast<const uint4 *>(p)[i];
+struct Quad;
+template <>
+struct Quad<__nv_bfloat16> {
+    uint2 v;
+    __device__ __forceinline__ void get(float *f) const {
+        const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v.x));
+        const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v.y));
+        f[0] = a.x;
+        f[1] = a.y;
+        f[2] = b.x;
+        f[3] = b.y;
     }
-    __device__ __forceinline__ void get(float (&f)[8]) const { load8(reinterpret_cast<const E *>(v), f); }
+    __device__ __forceinline__ void set(const float *f) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+        v = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+};
+template <>
+struct Quad<float> {
+    float4 v;
+    __device__ __forceinline__ void get(float *f) const {
+        f[0] = v.x;
+        f[1] = v.y;
+        f[2] = v.z;
+        f[3] = v.w;
+    }
+    __device__ __forceinline__ void set(const float *f) { v = make_float4(f[0], f[1], f[2], f[3]); }
 };
 
-// PAIRS: how elements pair up.  kNear: neighbours; kFar: i and i + rot/2 with rot/2 a
-// multiple of 8; both with an aligned table (kNear: rot a multiple of 8).  kAnyNear, kAnyFar:
-// without those conditions.  HEADS: heads a thread.
+// Two quads of a head: places o0 and o1, or side by side (not APART).
+template <typename E>
+struct Quads {
+    Quad<E> a, b;
+};
+template <typename E, bool APART>
+__device__ __forceinline__ void load_quads(Quads<E> &h, const E *head, int o0, int o1) {
+    if constexpr (!APART && sizeof(E) == 2) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(head + o0);
+        h.a.v = make_uint2(v.x, v.y);
+        h.b.v = make_uint2(v.z, v.w);
+    } else {
+        h.a = *reinterpret_cast<const Quad<E> *>(head + o0);
+        h.b = *reinterpret_cast<const Quad<E> *>(head + o1);
+    }
+}
+template <typename E, bool APART>
+__device__ __forceinline__ void store_quads(const Quads<E> &h, E *head, int o0, int o1) {
+    if constexpr (!APART && sizeof(E) == 2) {
+        *reinterpret_cast<uint4 *>(head + o0) = make_uint4(h.a.v.x, h.a.v.y, h.b.v.x, h.b.v.y);
+    } else {
+        *reinterpret_cast<Quad<E> *>(head + o0) = h.a;
+        *reinterpret_cast<Quad<E> *>(head + o1) = h.b;
+    }
+}
+
+// PAIRS: how elements pair up.  kNear: neighbours (a thread's quads are neighbours too);
+// kFar: i and i + rot/2 (its quads are rot/2 apart); both with rot a multiple of 8 and an
+// aligned table.  kAnyNear, kAnyFar: without those conditions, quads side by side.
+// HEADS: heads a thread.
 enum { kNear, kFar, kAnyNear, kAnyFar };
 
 template <typename E, int LANES, int PAIRS, int HEADS>
 __global__ void __launch_bounds__(kThreads, 5) append_kernel(const AppendParams p) {
     constexpr int kGroups = kThreads / LANES;
-    constexpr bool kFarPairs = PAIRS == kFar || PAIRS == kAnyFar;
+    constexpr int kTable = PAIRS == kAnyFar ? 8 : 4;
     __shared__ float rows[PAIRS == kAnyFar ? kThreads * 8 : 1];
-    const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, at = lane * 8;
+    const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
     const int heads = p.n_q + 2 * p.n_kv, half = p.rot >> 1;
     const int head_first = blockIdx.y * kGroups * HEADS + group;
     const long long t = blockIdx.x;
-    const bool inside = at < p.d;
+    const int at = lane * 8;
+    const bool inside = at < p.d, turns = at < p.rot;
+    // places of the thread's two quads in a head
+    const int o0 = PAIRS == kFar && turns ? lane * 4 : at, o1 = PAIRS == kFar && turns ? half + lane * 4 : at + 4;
 
-    Held<E> held[HEADS];
+    constexpr bool kApart = PAIRS == kFar;
+    Quads<E> held[HEADS];
 #pragma unroll
     for (int u = 0; u < HEADS; ++u) {
         const int head = head_first + u * kGroups;
         const E *src = head < p.n_q ? static_cast<const E *>(p.q) + t * p.ld_q + head * p.d
                        : head < p.n_q + p.n_kv ? static_cast<const E *>(p.k) + t * p.ld_k + (head - p.n_q) * p.d
                                                : static_cast<const E *>(p.v) + t * p.ld_v + (head - p.n_q - p.n_kv) * p.d;
-        if (head < heads && inside) held[u].load(src + at);
+        if (head < heads && inside) load_quads<E, kApart>(held[u], src, o0, o1);
     }
     const long long slot = p.slots[t];
-    float c[kFarPairs ? 8 : 4], s[kFarPairs ? 8 : 4];
+    float c[kTable], s[kTable];
     if (half) {
         int pos = p.positions[t];
         if (pos < 0 || pos >= p.n_pos) {
@@ -87,21 +148,15 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const AppendParams 
             pos = pos < 0 ? 0 : p.n_pos - 1;
         }
         const float *row = p.cos_sin + (long long)pos * p.rot;
-        if (PAIRS == kFar) {
-            if (at < p.rot) {
-                const int i = at < half ? at : at - half;
-                load8(row + i, c);
-                load8(row + half + i, s);
-            }
-        } else if (PAIRS == kNear) {
-            if (at < p.rot) {
-                *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(row + (at >> 1));
-                *reinterpret_cast<float4 *>(s) = *reinterpret_cast<const float4 *>(row + half + (at >> 1));
+        if (PAIRS == kNear || PAIRS == kFar) {
+            if (turns) {
+                *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(row + lane * 4);
+                *reinterpret_cast<float4 *>(s) = *reinterpret_cast<const float4 *>(row + half + lane * 4);
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < (kFarPairs ? 8 : 4); ++e) {
-                const int x = kFarPairs ? at + e : at + 2 * e, i = !kFarPairs ? x >> 1 : x < half ? x : x - half;
+            for (int e = 0; e < kTable; ++e) {
+                const int x = PAIRS == kAnyFar ? at + e : at + 2 * e, i = PAIRS == kAnyNear ? x >> 1 : x < half ? x : x - half;
                 if (x < p.rot) {
                     c[e] = row[i];
                     s[e] = row[half + i];
@@ -119,21 +174,48 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const AppendParams 
         if (head >= heads) return;
         const bool is_q = head < p.n_q, is_v = head >= p.n_q + p.n_kv;
         float h[8] = {};
-        if (inside) held[u].get(h);
+        if (inside) {
+            held[u].a.get(h);
+            held[u].b.get(h + 4);
+        }
         const E *norm = static_cast<const E *>(is_q ? p.q_norm : p.k_norm);
         if (!is_v && norm) {
             float sum = 0.f, w[8] = {};
-            if (inside) load8(norm + at, w);
+            if (inside) {
+                Quads<E> n;
+                load_quads<E, kApart>(n, norm, o0, o1);
+                n.a.get(w);
+                n.b.get(w + 4);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum += h[e] * h[e];
 #pragma unroll
             for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(group_mask<LANES>(), sum, o);
-            const float r = rsqrtf(sum / (float)p.d + p.eps);
+            const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps));
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[e] = h[e] * r * w[e];
         }
         if (!is_v && half) {
-            if (!kFarPairs) {
+            if (PAIRS == kFar) {
+                if (turns) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float a = h[e], b = h[4 + e];
+                        h[e] = a * c[e] - b * s[e];
+                        h[4 + e] = a * s[e] + b * c[e];
+                    }
+                }
+            } else if (PAIRS == kAnyFar) {
+                float *mine = rows + group * (LANES * 8);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mine[at + e] = h[e];
+                __syncwarp(group_mask<LANES>());
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (at + e < half) h[e] = h[e] * c[e] - mine[at + e + half] * s[e];
+                    else if (at + e < p.rot) h[e] = mine[at + e - half] * s[e] + h[e] * c[e];
+                __syncwarp(group_mask<LANES>());
+            } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     if (at + 2 * e < p.rot) {
@@ -141,34 +223,20 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const AppendParams 
                         h[2 * e] = a * c[e] - b * s[e];
                         h[2 * e + 1] = a * s[e] + b * c[e];
                     }
-            } else {
-                float other[8];
-                if (PAIRS == kFar) {
-                    const int partner = (at < half ? lane + half / 8 : lane - half / 8) & (LANES - 1);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) other[e] = __shfl_sync(group_mask<LANES>(), h[e], partner, LANES);
-                } else {
-                    float *mine = rows + group * (LANES * 8);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) mine[at + e] = h[e];
-                    __syncwarp(group_mask<LANES>());
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) other[e] = at + e < p.rot ? mine[at + e < half ? at + e + half : at + e - half] : 0.f;
-                    __syncwarp(group_mask<LANES>());
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (at + e < p.rot) h[e] = at + e < half ? h[e] * c[e] - other[e] * s[e] : other[e] * s[e] + h[e] * c[e];
             }
         }
         if (!inside) continue;
+        E *dst;
         if (is_q) {
-            store8(static_cast<E *>(p.q_out) + (t * p.n_q + head) * p.d + at, h);
-        } else if (stored) {
-            E *dst = static_cast<E *>(is_v ? p.v_pages : p.k_pages);
+            dst = static_cast<E *>(p.q_out) + (t * p.n_q + head) * p.d;
+        } else {
+            if (!stored) continue;
             const int kv_head = head - p.n_q - (is_v ? p.n_kv : 0);
-            store8(dst + (((page * p.n_kv + kv_head) << p.page_shift) + off) * p.d + at, h);
+            dst = static_cast<E *>(is_v ? p.v_pages : p.k_pages) + (((page * p.n_kv + kv_head) << p.page_shift) + off) * p.d;
         }
+        held[u].a.set(h);
+        held[u].b.set(h + 4);
+        store_quads<E, kApart>(held[u], dst, o0, o1);
     }
 }
 
@@ -177,8 +245,13 @@ void launch(const AppendParams &p, int T, cudaStream_t st) {
     constexpr int kGroups = kThreads / LANES;
     const int heads = p.n_q + 2 * p.n_kv;
     const dim3 one(T, (heads + kGroups - 1) / kGroups), more(T, (heads + kGroups * kHeads - 1) / (kGroups * kHeads));
-    if ((long long)one.x * one.y > kManyBlocks) append_kernel<E, LANES, PAIRS, kHeads><<<more, kThreads, 0, st>>>(p);
-    else append_kernel<E, LANES, PAIRS, 1><<<one, kThreads, 0, st>>>(p);
+    if constexpr (PAIRS == kNear) {
+        if ((long long)one.x * one.y > kManyBlocks) {
+            append_kernel<E, LANES, PAIRS, kHeads><<<more, kThreads, 0, st>>>(p);
+            return;
+        }
+    }
+    append_kernel<E, LANES, PAIRS, 1><<<one, kThreads, 0, st>>>(p);
 }
 
 template <typename E, int LANES>
@@ -188,7 +261,7 @@ void launch(const AppendParams &p, int T, bool interleaved, cudaStream_t st) {
         if (table && p.rot % 8 == 0) launch<E, LANES, kNear>(p, T, st);
         else launch<E, LANES, kAnyNear>(p, T, st);
     } else {
-        if (table && p.rot % 16 == 0) launch<E, LANES, kFar>(p, T, st);
+        if (table && p.rot % 8 == 0) launch<E, LANES, kFar>(p, T, st);
         else launch<E, LANES, kAnyFar>(p, T, st);
     }
 }
@@ -243,6 +316,7 @@ extern "C" int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, 
     p.q_norm = q_norm;
     p.k_norm = k_norm;
     p.eps = eps;
+    p.inv_d = 1.f / (float)d;
     p.q_out = q_out;
     p.k_pages = kv->k;
     p.v_pages = kv->v;
