@@ -6,10 +6,23 @@
 // mask row names (or j <= i without a mask).  K and V are read once, which is
 // the bound while few query rows share them (2 flops a byte and row).
 //
-// attention_mma_kernel (bf16): warp MMAs on units of 16 rows.
+// attention_mma_kernel (bf16): warp MMAs on units of 16 rows.  Few rows share a key,
+//   so memory is the bound: one producer warp keeps two to six tiles of K and V on
+//   their way, four warps take a quarter of each tile's keys and add up at the unit's
+//   end.  128 requests of one token over <= 8192 cached, 32 query and 8 kv heads of
+//   128: 240 us, 6.64 TB/s.  One request over 777: 10.6 us, of which the bytes take
+//   0.5; the rest is the chain launch -> page ids -> tile -> products -> sums in
+//   memory -> join.
 // attention_tc_kernel (bf16, attention_tc.cu): tcgen05 on units of 128 or 256 rows.
-// attention_simt_kernel (fp32): the same list, fp32 multiply-adds.
-// attention_join_kernel: joins the units that were cut between blocks.
+// attention_simt_kernel (fp32): the same list, fp32 multiply-adds, which bound it
+//   (5 requests of up to 7 tokens over <= 300, 6 query heads of 80: 13.2 us, mostly
+//   the same chain).
+// attention_join_kernel: joins the units that were cut between blocks.  It is
+//   launched while the attention still runs, and waits for it.
+//
+// Probabilities are rounded to bf16 for their product with V, as the tensor cores
+// take them (2^-9 relative each, no more than V's own rounding); maximum, sum and
+// output stay in fp32.  fp32 caches are not rounded anywhere.
 #include <cudaTypedefs.h>
 
 #include <type_traits>
@@ -370,7 +383,12 @@ __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, 
         copy.fetch(p, cur, cur.tile, tid);
         for (int it = 0; cur.left > 0; ++it) {
             const int stage = it % Sh::kStages;
-            if (!wait_warp(&ctl.empty[stage], ((it / Sh::kStages) & 1) ^ 1, ctl)) break;
+            if (!wait_warp(&ctl.empty[stage], ((it / Sh::kStages) & 1) ^ 1, ctl)) {
+                // tensor copies on their way land before the block leaves
+                for (int x = max(0, it - Sh::kStages); TMA && x < it; ++x)
+                    tc::wait_phase(&ctl.full[x % Sh::kStages], (x / Sh::kStages) & 1, nullptr);
+                break;
+            }
             for (int which = 0; which < 2; ++which) {
                 copy.copy(p, which ? &maps.v : &maps.k, which ? p.v : p.k, base + stage * Sh::kStage + which * Sh::kHalf,
                           &ctl.full[stage], tid);
@@ -563,7 +581,9 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
 // Block (c, y): if a unit starts in block c's part of the list and goes on after it
 // (its record says so), adds up the parts: c's slot 1, then slot 0 of each block
 // after it until the unit ends.  A warp has 8 rows x 16 columns at a time: 128-byte
-// reads, 32-byte writes.
+// reads, 32-byte writes.  gridDim.y is a unit's rows / kJoinRows: 16 rows a block made
+// 8 trees of 64 take 58.4 us for 56.6 and the small fp32 case 15.9 for 13.2, 4 rows
+// gained nothing.
 template <typename E>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p) {
     const int c = blockIdx.x, lane = threadIdx.x & 31;
@@ -605,8 +625,24 @@ struct Variant {
     int rt, tk, per_sm, unit_cost;
 };
 
+// Pages of whole swizzle atoms (8 rows) come by tensor copies, a page a copy, smaller
+// ones by 16-byte copies, whose address arithmetic costs more than the transfer: pages
+// of 8, 16, 64 by tensor copies 83, 75, 75 us for 32 requests over <= 8192 and 54 us
+// for 8 trees of 64; by 16-byte copies 127, 109, 101 us and 131 us.
 constexpr int kTmaMinPage = 8;
 
+// The kernel goes by the rows that share a kv head of a request, on average (lengths
+// are on the device).  More than 16 go to tcgen05: with warp MMAs a unit of 16 rows
+// reads K and V again for each 16.  Page 16, 4 query heads a kv head, tcgen05 against
+// warp MMAs: 8 requests over <= 20000, 16 rows 63 and 57 us, 24 rows 60 and 76, 32 rows
+// 56 and 73, 64 rows 66 and 147; 64 requests over <= 900, 16 rows 58 and 32, 32 rows
+// 62 and 47, 64 rows 65 and 92; one request over 4000, 32 rows 17.0 and 17.1.
+// Units of 256 rows when that is more than 128: 8 x 256 rows 53 us against 67 with
+// units of 128, 8 x 160 rows 55 against 58, 1 x 256 rows over <= 65536 72 against 99,
+// 32 x 160 over <= 2000 the same.
+// unit_cost, in tiles: 128 requests of one token take 305, 240, 242, 248 us with 0, 2,
+// 4, 8; 8 trees of 64 take 81, 62.5, 60.1, 60.2 with 2, 4, 6, 8 (the others' shares
+// grow with the cost of a unit's start and end against that of its tiles).
 Variant variant_of(const lora_kv_pages *kv, int group, int S, int T) {
     const int d = kv->head_dim;
     if (kv->dtype == LORA_F32) return {false, kSimtRows, kSimtTile, d <= 128 ? 2 : 1, 1};

@@ -32,13 +32,6 @@ __device__ __forceinline__ void flag_status(int *status, int bits) {
     if (status) atomicOr(status, bits);
 }
 
-// Checks a device segment table (every thread of the block calls it).
-__device__ __forceinline__ void check_starts(const int *starts, int S, int T, int *status) {
-    bool bad = threadIdx.x == 0 && (starts[0] != 0 || starts[S] != T);
-    for (int s = threadIdx.x; s < S; s += blockDim.x) bad |= starts[s + 1] < starts[s];
-    if (__syncthreads_or(bad) && threadIdx.x == 0) flag_status(status, LORA_DEV_BAD_SEGMENTS);
-}
-
 // One lane of a converged warp.  The compiler knows that a branch on it has one
 // thread, so that the operands of tcgen05 instructions inside, which the hardware
 // wants uniform, need no loop over lanes (32 against 57 cycles a 128 x 64 x 16

@@ -2,14 +2,22 @@
 //   y[t][n] = sum_g s[n][g] * sum_{k in g} x[t][k] * (c[n][k] - z[n][g])
 //
 // The codes are read once: half a byte a weight against 2 T flops, so memory is the
-// bound up to T of about 70.  Codes less zeros are whole numbers of 5 bits, exact in
+// bound up to T of about 140 (at 1.9 PFLOP/s and 6.8 TB/s).  Codes less zeros are whole numbers of 5 bits, exact in
 // bf16, so the inner sums run on the tensor cores without rounding the weights, and
 // each group's sum is scaled in fp32.
 //
 // Up to 8 tokens: w4_rows_kernel below, warp MMAs on registers filled straight from
-// memory.  More: w4_tc.cu, whose tcgen05 rate the flops then need (8 tokens, 4096 ->
-// 16384: 17.6 us here, 23.1 there; 16 tokens in two tiles of columns: 23.9, 24.3;
-// 16 in fp32, 4096 -> 4096: 22.2, 13.6).
+// memory.  More: w4_tc.cu, whose tcgen05 rate the flops then need.  4096 -> 16384, here
+// and there: 4 tokens 13.3 and 16.9 us, 8 tokens 14.7 and 16.9; in fp32 17.5 and 29.0,
+// 20.6 and 29.3; 4096 -> 4096: 8 tokens 7.2 and 9.4.  16 tokens would be two columns of
+// MMAs here and were slower (two calls of 8: 29.4 against 17.1).
+//
+// w4_rows_kernel reaches 2.9 TB/s (1 x 4096 -> 16384 12.3 us): the instructions that turn
+// codes into bf16 pairs and feed the MMAs, and for small matrices a few round trips to
+// memory (1 x 4096 -> 1024 3.7 us), take longer than the bytes.
+//
+// fp32 x enters as three bf16 parts, whose sum is x to 2^-24: the products with whole
+// numbers are exact and the sums are fp32, so nothing is lost against fp32 arithmetic.
 #include "w4.cuh"
 
 namespace lora {
