@@ -226,37 +226,51 @@ __device__ void produce(const AttnParams &p, const KvMaps &maps, Cursor cur, uin
     }
 }
 
+// A position of the ring, without divisions on the way.
+template <int SLOTS>
+struct Place {
+    uint32_t slot, parity;
+    __device__ __forceinline__ explicit Place(uint32_t seq) : slot(seq % SLOTS), parity((seq / SLOTS) & 1) {}
+    __device__ __forceinline__ Place next(int n) const {        // n <= SLOTS
+        Place to = *this;
+        to.slot += n;
+        if (to.slot >= SLOTS) {
+            to.slot -= SLOTS;
+            to.parity ^= 1;
+        }
+        return to;
+    }
+};
+
 // One thread issues every MMA.  At 64 cycles a product of 128 x 128 x 16 its own
-// instructions are what can starve the tensor cores, so the loop over a segment
-// is a function of its own with little state: descriptors are 32-bit additions
-// (16-byte units) to a constant upper half.
+// instructions are what can starve the tensor cores (its warp shares scheduler and
+// instruction cache with softmax warps), so the loop over a segment is a function of
+// its own whose state is in registers: descriptors are 32-bit additions (16-byte
+// units) to a constant upper half.
 template <int D, int NQ, bool TMA>
 struct Issuer {
     using Sh = TcShape<D>;
+    using At = Place<Sh::kSlots>;
     static constexpr uint32_t kSwizzled = (1024u >> 4) | (1u << 14) | (2u << 29);      // descriptor bits 32..63
     static constexpr uint32_t kIdescS = idesc_bf16_f32(kTile, kTile);
     static constexpr uint32_t kIdescO = idesc_bf16_f32(kTile, D) | kTransposeB;
 
-    Control *ctl;
-    uint32_t tmem, q_lo, k_lo, v_lo;             // descriptors' lower halves of stream 0's queries and slot 0
-    uint32_t seq0, p_phase0, p_phase1;
-
-    __device__ __forceinline__ bool slot_full(uint32_t seq) {
-        if (!wait_bar(&ctl->full[seq % Sh::kSlots], (seq / Sh::kSlots) & 1, ctl)) return false;
+    static __device__ __forceinline__ bool slot_full(Control *ctl, const At &at) {
+        if (!wait_bar(&ctl->full[at.slot], at.parity, ctl)) return false;
         if (!TMA) fence_proxy_async();          // ordinary writes; the MMAs read through the async proxy
         fence_after_sync();
         return true;
     }
-    __device__ __forceinline__ void release(uint32_t seq) { mma_commit(&ctl->empty[seq % Sh::kSlots]); }
-    __device__ __forceinline__ bool probabilities(int w) {
-        uint32_t &phase = w ? p_phase1 : p_phase0;
-        if (!wait_bar(&ctl->p_ready[w], phase & 1, ctl)) return false;
-        ++phase;
+    static __device__ __forceinline__ void release(Control *ctl, const At &at) { mma_commit(&ctl->empty[at.slot]); }
+    static __device__ __forceinline__ bool probabilities(Control *ctl, int w, uint32_t &phases) {
+        if (!wait_bar(&ctl->p_ready[w], (phases >> w) & 1, ctl)) return false;
+        phases ^= 1u << w;
         fence_after_sync();
         return true;
     }
-    __device__ __forceinline__ void scores(int w, uint32_t seq) {      // S_w = Q_w K^T
-        uint32_t q = q_lo + w * (Sh::kSlot / 16), k = k_lo + (seq % Sh::kSlots) * (Sh::kSlot / 16);
+    // S_w = Q_w K^T
+    static __device__ __forceinline__ void scores(Control *ctl, uint32_t tmem, uint32_t q_lo, uint32_t k_lo, int w, const At &at) {
+        uint32_t q = q_lo + w * (Sh::kSlot / 16), k = k_lo + at.slot * (Sh::kSlot / 16);
         const uint32_t d = tmem + w * kTile;
 #pragma unroll 1
         for (int panel = 0; panel < D / 64; ++panel, q += kTile * 128 / 16, k += kTile * 128 / 16) {
@@ -271,8 +285,9 @@ struct Issuer {
         }
         mma_commit(&ctl->s_full[w]);
     }
-    __device__ __forceinline__ void output(int w, uint32_t seq, bool accumulate) {      // O_w += P_w V
-        uint32_t v = v_lo + (seq % Sh::kSlots) * (Sh::kSlot / 16), pr = tmem + w * kTile, acc = accumulate ? 1u : 0u;
+    // O_w += P_w V
+    static __device__ __forceinline__ void output(uint32_t tmem, uint32_t v_lo, int w, const At &at, bool accumulate) {
+        uint32_t v = v_lo + at.slot * (Sh::kSlot / 16), pr = tmem + w * kTile, acc = accumulate ? 1u : 0u;
         const uint32_t d = tmem + 2 * kTile + w * D;
 #pragma unroll 1
         for (int half = 0; half < 2; ++half, v += 4 * 2048 / 16, pr += 32) {
@@ -287,66 +302,71 @@ struct Issuer {
             }
         }
     }
-    // The tiles of a segment; tile t has its keys at ring position seq0 + 2 t, its values right after them.
-    __device__ __noinline__ bool segment(int tiles, int streams) {
+    // The tiles of a segment; tile t has its keys at ring position seq0 + 2 t, its values right
+    // after them.  phases: bit w, the parity of stream w's next probabilities; returns them, or
+    // kGaveUp.
+    static constexpr uint32_t kGaveUp = 4;
+    static __device__ __noinline__ uint32_t segment(Control *ctl, uint32_t tmem, uint32_t q_lo, uint32_t k_lo, uint32_t v_lo,
+                                                    uint32_t seq0, uint32_t phases, int tiles, int streams) {
+        At k(seq0);
         if (NQ == 2) {
-            if (!slot_full(seq0)) return false;
-            for (int w = 0; w < streams; ++w) scores(w, seq0);
-            release(seq0);
+            if (!slot_full(ctl, k)) return kGaveUp;
+            for (int w = 0; w < streams; ++w) scores(ctl, tmem, q_lo, k_lo, w, k);
+            release(ctl, k);
+#pragma unroll 1
             for (int t = 0; t < tiles; ++t) {
-                const uint32_t v = seq0 + 2 * t + 1;
+                const At v = k.next(1);
                 const bool more = t + 1 < tiles;
+                k = k.next(2);
 #pragma unroll 1
                 for (int w = 0; w < streams; ++w) {
-                    if (!probabilities(w)) return false;
-                    if (w == 0 && !slot_full(v)) return false;
-                    output(w, v, t > 0 || ctl->accumulate[w]);
+                    if (!probabilities(ctl, w, phases)) return kGaveUp;
+                    if (w == 0 && !slot_full(ctl, v)) return kGaveUp;
+                    output(tmem, v_lo, w, v, t > 0 || ctl->accumulate[w]);
                     if (!more) mma_commit(&ctl->o_full[w]);
-                    if (w == streams - 1) release(v);
+                    if (w == streams - 1) release(ctl, v);
                     if (more) {
-                        if (w == 0 && !slot_full(v + 1)) return false;
-                        scores(w, v + 1);
+                        if (w == 0 && !slot_full(ctl, k)) return kGaveUp;
+                        scores(ctl, tmem, q_lo, k_lo, w, k);
                     }
                 }
-                if (more) release(v + 1);
+                if (more) release(ctl, k);
             }
         } else {
-            for (int w = 0; w < streams; ++w) {
-                if (!slot_full(seq0 + 2 * w)) return false;
-                scores(w, seq0 + 2 * w);
-                release(seq0 + 2 * w);
-            }
 #pragma unroll 1
-            for (int t = 0; t < tiles; ++t) {
+            for (int w = 0; w < streams; ++w, k = k.next(2)) {
+                if (!slot_full(ctl, k)) return kGaveUp;
+                scores(ctl, tmem, q_lo, k_lo, w, k);
+                release(ctl, k);
+            }
+            At v(seq0 + 1);
+#pragma unroll 1
+            for (int t = 0; t < tiles; ++t, v = v.next(2), k = k.next(2)) {
                 const int w = t & 1;
-                const uint32_t v = seq0 + 2 * t + 1;
-                if (!probabilities(w) || !slot_full(v)) return false;
-                output(w, v, t > 1 || ctl->accumulate[w]);
-                release(v);
+                if (!probabilities(ctl, w, phases) || !slot_full(ctl, v)) return kGaveUp;
+                output(tmem, v_lo, w, v, t > 1 || ctl->accumulate[w]);
+                release(ctl, v);
                 if (t + 2 < tiles) {
-                    if (!slot_full(v + 3)) return false;
-                    scores(w, v + 3);
-                    release(v + 3);
+                    if (!slot_full(ctl, k)) return kGaveUp;
+                    scores(ctl, tmem, q_lo, k_lo, w, k);
+                    release(ctl, k);
                 } else {
                     mma_commit(&ctl->o_full[w]);
                 }
             }
         }
-        seq0 += 2 * tiles;
-        return true;
+        return phases;
     }
 };
 
 template <int D, int NQ, bool TMA>
 __device__ void issue(const AttnParams &p, Cursor cur, uint8_t *queries, uint8_t *ring, Control *ctl) {
-    Issuer<D, NQ, TMA> is;
-    is.ctl = ctl;
-    is.tmem = ctl->tmem;
-    is.q_lo = (uint32_t)desc_kmajor_sw128(smem_u32(queries));
-    is.k_lo = (uint32_t)desc_kmajor_sw128(smem_u32(ring));
-    is.v_lo = (uint32_t)desc_rows_sw128(smem_u32(ring), kTile * 128);
-    is.seq0 = is.p_phase0 = is.p_phase1 = 0;
-    uint32_t q_phase[2] = {0, 0};
+    using Is = Issuer<D, NQ, TMA>;
+    const uint32_t tmem = ctl->tmem;
+    const uint32_t q_lo = (uint32_t)desc_kmajor_sw128(smem_u32(queries));
+    const uint32_t k_lo = (uint32_t)desc_kmajor_sw128(smem_u32(ring));
+    const uint32_t v_lo = (uint32_t)desc_rows_sw128(smem_u32(ring), kTile * 128);
+    uint32_t seq0 = 0, phases = 0, q_phase[2] = {0, 0};
     while (cur.left > 0) {
         const Segment seg = segment_at(cur);
         const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
@@ -356,7 +376,9 @@ __device__ void issue(const AttnParams &p, Cursor cur, uint8_t *queries, uint8_t
             ++q_phase[w];
         }
         fence_after_sync();
-        if (!is.segment(seg.tiles, streams)) return;
+        phases = Is::segment(ctl, tmem, q_lo, k_lo, v_lo, seq0, phases, seg.tiles, streams);
+        if (phases == Is::kGaveUp) return;
+        seq0 += 2 * seg.tiles;
         cur.advance(p, seg.tiles);
     }
 }
