@@ -26,6 +26,17 @@ __device__ __forceinline__ void code_pairs(uint32_t w, __nv_bfloat162 offset, ui
         out[k] = *reinterpret_cast<const uint32_t *>(&d);
     }
 }
+// The same as pairs of neighbours (2 k, 2 k + 1), for x as it lies in memory: two
+// instructions a word more.
+__device__ __forceinline__ void code_neighbours(uint32_t w, __nv_bfloat162 offset, uint32_t (&out)[4]) {
+    const uint32_t odd = w >> 4;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t v = (__byte_perm(w, odd, 0x4400 + 0x1111 * k) & 0x000f000fu) | 0x43004300u;
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v), offset);
+        out[k] = *reinterpret_cast<const uint32_t *>(&d);
+    }
+}
 // 128 + zero, twice.
 __device__ __forceinline__ __nv_bfloat162 code_offset(uint32_t zero) {
     const uint32_t v = (0x4300u | zero) * 0x10001u;

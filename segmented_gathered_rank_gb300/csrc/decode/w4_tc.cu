@@ -40,12 +40,13 @@ struct W4Shape {
     static constexpr int kParts = sizeof(E) == 2 ? 1 : 3;
     static constexpr int kBPart = NTOK * kCols * 2;
     static constexpr int kStage = kParts * kBPart;
+    static constexpr int kX = kParts > 1 ? 3 : NTOK == 32 ? 8 : 5;      // tiles of x
     static constexpr int kCodes = kParts == 1 ? 8 : 4;
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + (size_t)kCodes * kCodeBytes;
+    static constexpr size_t kSmem = 1024 + (size_t)kX * kStage + (size_t)kCodes * kCodeBytes;
 };
 
 struct W4Control {
-    uint64_t codes_full[8], codes_free[8], ab_full[kStages], ab_free[kStages], d_full[kAccumulators], d_free[kAccumulators], drain;
+    uint64_t codes_full[8], codes_free[8], a_full[kStages], a_free[kStages], x_full[8], x_free[8], d_full[kAccumulators], d_free[kAccumulators], drain;
     volatile int abort;
     uint32_t tmem;
 };
@@ -118,13 +119,15 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 template <typename E, int GROUP, int NTOK>
-__global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constant__ CUtensorMap map, const W4Params p, int splits) {
+__global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap x_map, const W4Params p,
+                                                            int splits) {
     using Sh = W4Shape<E, NTOK>;
+    constexpr bool kCopiesX = Sh::kParts == 1;           // x needs no splitting: tensor copies
     constexpr int kGroups = kCols / GROUP;               // a tile
     extern __shared__ uint8_t raw[];
     __shared__ W4Control ctl;
     uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    uint8_t *codes = smem + kStages * Sh::kStage;
+    uint8_t *codes = smem + Sh::kX * Sh::kStage;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = blockIdx.x % splits, n0 = (blockIdx.x / splits) * kRows;
     const int tiles = (p.h_in + kCols - 1) / kCols;
@@ -137,8 +140,12 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             mbar_init(&ctl.codes_free[i], 8);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&ctl.ab_full[i], 8);
-            mbar_init(&ctl.ab_free[i], 1);
+            mbar_init(&ctl.a_full[i], 4);
+            mbar_init(&ctl.a_free[i], 1);
+        }
+        for (int i = 0; i < Sh::kX; ++i) {
+            mbar_init(&ctl.x_full[i], kCopiesX ? 1 : 4);
+            mbar_init(&ctl.x_free[i], 1);
         }
         for (int i = 0; i < kAccumulators; ++i) {
             mbar_init(&ctl.d_full[i], 1);
@@ -200,19 +207,20 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t o[4];
-                        code_pairs(words[j], offset, o);
+                        if constexpr (kCopiesX) code_neighbours(words[j], offset, o);
+                        else code_pairs(words[j], offset, o);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) a[(i * 4 + j) * 4 + e] = o[e];
                     }
                 }
-                if (h == 0 && !(ok = wait_warp(&ctl.ab_free[turn], parity ^ 1, ctl))) break;
+                if (h == 0 && !(ok = wait_warp(&ctl.a_free[turn], parity ^ 1, ctl))) break;
                 tmem_st32(a_tmem + turn * kACols + h * 32, a);
             }
             if (!ok) break;
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.ab_full[turn]);
+            if (lane == 0) mbar_arrive(&ctl.a_full[turn]);
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) zero[i] = next[i];
         }
@@ -280,45 +288,58 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
         }
     } else if (warp < kCopyWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-        // x of the tile's columns, in the order of code_pairs; tokens past T are zeros.  Each thread's pieces
-        // of the next tile are on their way while this one's are written.
         const int tid = threadIdx.x - kXWarp0 * 32;
-        constexpr int kPieces = NTOK * 16 / 128, kWords = sizeof(E) / 2, kHeld = sizeof(E) == 2 ? kPieces : kPieces / 2;
-        const int t0 = tid >> 4, k0 = (tid & 15) * 8;          // piece i: token t0 + 8 i
-        const E *src = static_cast<const E *>(p.x) + (long long)t0 * p.h_in + k0;
-        const long long step = 8LL * p.h_in;
-        const uint32_t place = tile_off(NTOK, t0, tid & 15);   // 8 tokens are one swizzle atom: piece i is i KB further
-        const int pieces = (p.T - t0 + 7) / 8;                 // that exist
-        uint4 v[kHeld][kWords];
-        auto load = [&](int tile, int i0) {
-            const E *at = src + tile * kCols;
-            const int n = tile * kCols + k0 < p.h_in ? pieces - i0 : 0;
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-#pragma unroll
-                for (int h = 0; h < kWords; ++h)
-                    v[i][h] = i < n ? __ldg(reinterpret_cast<const uint4 *>(at + (i0 + i) * step) + h) : make_uint4(0, 0, 0, 0);
-            }
-        };
         // every block will want all of x at about the same time: each brings a share of it into L2
         const size_t bytes = (size_t)p.T * p.h_in * sizeof(E);
         for (size_t i = ((size_t)blockIdx.x * 128 + tid) * 128; i < bytes; i += (size_t)gridDim.x * 128 * 128)
             asm volatile("prefetch.global.L2 [%0];\n" ::"l"(static_cast<const char *>(p.x) + i));
-        Ring<kStages> ab;
-        load(first, 0);
-        for (int tile = first; tile < end; ++tile, ab.next()) {
-            if (!wait_warp(&ctl.ab_free[ab.at], ab.parity ^ 1, ctl)) break;
-            uint8_t *b = smem + ab.at * Sh::kStage;
+        if constexpr (kCopiesX) {
+            // two panels of 64 columns a tile; what lies outside of x reads as zeros
+            if (warp == kXWarp0 && elect_lane()) {
+                Ring<Sh::kX> r;
+                for (int tile = first; tile < end; ++tile, r.next()) {
+                    if (!wait_bar(&ctl.x_free[r.at], r.parity ^ 1, ctl)) {
+                        for (int i = 0; i < Sh::kX && tile - (i + 1) >= first; ++i)      // as below, for the codes
+                            wait_phase(&ctl.x_full[(r.at + Sh::kX - 1 - i) % Sh::kX], i < r.at ? r.parity : r.parity ^ 1, nullptr);
+                        break;
+                    }
+                    mbar_arrive_expect_tx(&ctl.x_full[r.at], Sh::kStage);
 #pragma unroll
-            for (int i0 = 0; i0 < kPieces; i0 += kHeld) {
+                    for (int panel = 0; panel < 2; ++panel)
+                        tma_load_2d(smem + r.at * Sh::kStage + panel * (NTOK * 128), &x_map, tile * kCols + panel * 64, 0, &ctl.x_full[r.at]);
+                }
+            }
+            __syncwarp();
+        } else {
+            // the parts of x of the tile's columns, in the order of code_pairs; tokens past T are zeros.  Each
+            // thread's next pieces are on their way while these are written.
+            constexpr int kPieces = NTOK * 16 / 128, kHeld = kPieces / 2;
+            const int t0 = tid >> 4, k0 = (tid & 15) * 8;          // piece i: token t0 + 8 i
+            const E *src = static_cast<const E *>(p.x) + (long long)t0 * p.h_in + k0;
+            const long long step = 8LL * p.h_in;
+            const uint32_t place = tile_off(NTOK, t0, tid & 15);   // 8 tokens are one swizzle atom: piece i is i KB further
+            const int pieces = (p.T - t0 + 7) / 8;                 // that exist
+            uint4 v[kHeld][2];
+            auto load = [&](int tile, int i0) {
+                const E *at = src + tile * kCols;
+                const int n = tile * kCols + k0 < p.h_in ? pieces - i0 : 0;
 #pragma unroll
                 for (int i = 0; i < kHeld; ++i) {
-                    const uint32_t at = place + (i0 + i) * 1024;
-                    if constexpr (sizeof(E) == 2) {
-                        uint32_t o[4];
-                        pair_x(v[i][0], o);
-                        *reinterpret_cast<uint4 *>(b + at) = make_uint4(o[0], o[1], o[2], o[3]);
-                    } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        v[i][h] = i < n ? __ldg(reinterpret_cast<const uint4 *>(at + (i0 + i) * step) + h) : make_uint4(0, 0, 0, 0);
+                }
+            };
+            Ring<Sh::kX> xr;
+            load(first, 0);
+            for (int tile = first; tile < end; ++tile, xr.next()) {
+                if (!wait_warp(&ctl.x_free[xr.at], xr.parity ^ 1, ctl)) break;
+                uint8_t *b = smem + xr.at * Sh::kStage;
+#pragma unroll
+                for (int i0 = 0; i0 < kPieces; i0 += kHeld) {
+#pragma unroll
+                    for (int i = 0; i < kHeld; ++i) {
+                        const uint32_t at = place + (i0 + i) * 1024;
                         const float f[8] = {__uint_as_float(v[i][0].x), __uint_as_float(v[i][0].y), __uint_as_float(v[i][0].z),
                                             __uint_as_float(v[i][0].w), __uint_as_float(v[i][1].x), __uint_as_float(v[i][1].y),
                                             __uint_as_float(v[i][1].z), __uint_as_float(v[i][1].w)};
@@ -328,13 +349,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                         for (int q = 0; q < 3; ++q)
                             *reinterpret_cast<uint4 *>(b + q * Sh::kBPart + at) = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
                     }
+                    if (i0 + kHeld < kPieces) load(tile, i0 + kHeld);
+                    else if (tile + 1 < end) load(tile + 1, 0);
                 }
-                if (i0 + kHeld < kPieces) load(tile, i0 + kHeld);
-                else if (tile + 1 < end) load(tile + 1, 0);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.x_full[xr.at]);
             }
-            fence_proxy_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.ab_full[ab.at]);
         }
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
@@ -364,12 +385,13 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
         if (elect_lane()) {
             constexpr uint32_t idesc = idesc_bf16_f32(kRows, NTOK);
             const uint32_t b0 = (uint32_t)desc_kmajor_sw128(smem_u32(smem)), tmem = ctl.tmem;
-            Ring<kStages> ab;
+            Ring<kStages> ar;
+            Ring<Sh::kX> xr;
             Ring<kAccumulators> d;
-            for (int tile = first; tile < end; ++tile, ab.next()) {
-                if (!wait_bar(&ctl.ab_full[ab.at], ab.parity, ctl)) break;
+            for (int tile = first; tile < end; ++tile, ar.next(), xr.next()) {
+                if (!wait_bar(&ctl.x_full[xr.at], xr.parity, ctl) || !wait_bar(&ctl.a_full[ar.at], ar.parity, ctl)) break;
                 fence_after_sync();
-                const uint32_t a = tmem + kACol0 + ab.at * kACols, b = b0 + ab.at * (Sh::kStage / 16);
+                const uint32_t a = tmem + kACol0 + ar.at * kACols, b = b0 + xr.at * (Sh::kStage / 16);
                 bool ok = true;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g, d.next()) {
@@ -385,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                     mma_commit(&ctl.d_full[d.at]);
                 }
                 if (!ok) break;
-                mma_commit(&ctl.ab_free[ab.at]);
+                mma_commit(&ctl.a_free[ar.at]);
+                mma_commit(&ctl.x_free[xr.at]);
             }
             mma_commit(&ctl.drain);
             wait_phase(&ctl.drain, 0, nullptr);
@@ -425,8 +448,18 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
+// A matrix of `rows` rows of `cols` elements in boxes of 128 bytes x box_rows; what lies outside reads as zeros.
+bool make_map(CUtensorMap *map, CUtensorMapDataType type, void *base, int cols, int rows, cuuint64_t pitch, int box_cols,
+              int box_rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {pitch};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, step[2] = {1, 1};
+    return encode_fn()(map, type, 2, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename E, int GROUP, int NTOK>
-int launch(const W4Params &p, const CUtensorMap &map, cudaStream_t st) {
+int launch(const W4Params &p, const CUtensorMap &map, const CUtensorMap &x_map, cudaStream_t st) {
     using Sh = W4Shape<E, NTOK>;
     const int rows = (p.h_out + kRows - 1) / kRows, tiles = (p.h_in + kCols - 1) / kCols, sms = num_sms();
     // Blocks that share the columns: as many as leave one block a SM, with two tiles of
@@ -448,15 +481,19 @@ int launch(const W4Params &p, const CUtensorMap &map, cudaStream_t st) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = splits > 1 ? 1 : 0;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_tc_kernel<E, GROUP, NTOK>, map, p, splits);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_tc_kernel<E, GROUP, NTOK>, map, x_map, p, splits);
     count_launch();
     return cuda_status(e);
 }
 
 template <typename E, int NTOK>
 int launch(const W4Params &p, int group, const CUtensorMap &map, cudaStream_t st) {
-    if (group == 128) return launch<E, 128, NTOK>(p, map, st);
-    return group == 64 ? launch<E, 64, NTOK>(p, map, st) : launch<E, 32, NTOK>(p, map, st);
+    CUtensorMap x_map = {};
+    if (W4Shape<E, NTOK>::kParts == 1 &&
+        !make_map(&x_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, const_cast<void *>(p.x), p.h_in, p.T, (cuuint64_t)p.h_in * 2, 64, NTOK))
+        return LORA_ERR_CUDA;
+    if (group == 128) return launch<E, 128, NTOK>(p, map, x_map, st);
+    return group == 64 ? launch<E, 64, NTOK>(p, map, x_map, st) : launch<E, 32, NTOK>(p, map, x_map, st);
 }
 
 }  // namespace
@@ -465,13 +502,8 @@ namespace decode {
 
 int launch_w4_tc(int dtype, const W4Params &p, int group, cudaStream_t st) {
     if (!encode_fn() || num_sms() < 1) return LORA_ERR_CUDA;
-    // codes as bytes [h_out][h_in / 2]; what lies outside reads as zeros
-    CUtensorMap map;
-    const cuuint64_t dims[2] = {(cuuint64_t)p.h_in / 2, (cuuint64_t)p.h_out}, strides[1] = {(cuuint64_t)p.h_in / 2};
-    const cuuint32_t box[2] = {kCols, kRows}, step[2] = {1, 1};
-    if (encode_fn()(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(p.codes), dims, strides, box, step,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    CUtensorMap map;        // codes as bytes [h_out][h_in / 2]
+    if (!make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.codes), p.h_in / 2, p.h_out, p.h_in / 2, kCols, kRows))
         return LORA_ERR_CUDA;
     // Few tokens take the narrow tile of x: half the shared memory traffic, products and
     // scaling.  16 x 4096 -> 16384: 17.1 us for 19.9 with 64 columns, in fp32 29.9 for 43.5.
