@@ -33,20 +33,20 @@ constexpr int kThreads = 24 * 32, kTurns = 3;
 constexpr int kScaleWarp0 = 4 * kTurns, kXWarp0 = kScaleWarp0 + 4, kCopyWarp = kXWarp0 + 4, kMmaWarp = kCopyWarp + 1;      // warpgroups of one kind
 constexpr int kCodeBytes = kRows * kCols, kACols = kCols / 2;      // codes of two tiles; tensor memory columns of an A tile
 constexpr uint32_t kTmemCols = 512;
-constexpr int kAccumulators = 4, kStages = kTurns, kACol0 = 256;
+constexpr int kAccumulators = 4, kStages = 4, kACol0 = 256;      // kStages: A tiles
 
 template <typename E, int NTOK>
 struct W4Shape {
     static constexpr int kParts = sizeof(E) == 2 ? 1 : 3;
     static constexpr int kBPart = NTOK * kCols * 2;
     static constexpr int kStage = kParts * kBPart;
-    static constexpr int kX = kParts > 1 ? 3 : NTOK == 32 ? 8 : 5;      // tiles of x
+    static constexpr int kX = kParts > 1 ? 3 : kStages;      // tiles of x
     static constexpr int kCodes = kParts == 1 ? 8 : 4;
     static constexpr size_t kSmem = 1024 + (size_t)kX * kStage + (size_t)kCodes * kCodeBytes;
 };
 
 struct W4Control {
-    uint64_t codes_full[8], codes_free[8], a_full[kStages], a_free[kStages], x_full[8], x_free[8], d_full[kAccumulators], d_free[kAccumulators], drain;
+    uint64_t codes_full[8], codes_free[8], a_full[kStages], done[kStages], x_full[kStages], x_free[kStages], d_full[kAccumulators], d_free[kAccumulators], drain;
     volatile int abort;
     uint32_t tmem;
 };
@@ -122,8 +122,10 @@ template <typename E, int GROUP, int NTOK>
 __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap x_map, const W4Params p,
                                                             int splits) {
     using Sh = W4Shape<E, NTOK>;
-    constexpr bool kCopiesX = Sh::kParts == 1;           // x needs no splitting: tensor copies
     constexpr int kGroups = kCols / GROUP;               // a tile
+    constexpr bool kCopiesX = Sh::kParts == 1;           // x needs no splitting: tensor copies
+    // One commit a tile says that its A and x stages are free, and, with one group a tile, that its sums are there.
+    constexpr bool kOneX = Sh::kX == kStages, kOneD = kGroups == 1;
     extern __shared__ uint8_t raw[];
     __shared__ W4Control ctl;
     uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&ctl.a_full[i], 4);
-            mbar_init(&ctl.a_free[i], 1);
+            mbar_init(&ctl.done[i], 1);
         }
         for (int i = 0; i < Sh::kX; ++i) {
             mbar_init(&ctl.x_full[i], kCopiesX ? 1 : 4);
@@ -182,9 +184,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             for (int i = 0; i < kGroups; ++i) z[i] = zeros ? __ldg(zeros + min(tile * kGroups + i, p.groups - 1)) : 8u;
         };
         const int turn = warp >> 2;
-        uint32_t parity = 0;
         fetch(first + turn, zero);
-        for (int rel = turn; first + rel < end; rel += kTurns, parity ^= 1) {
+        for (int rel = turn; first + rel < end; rel += kTurns) {
             fetch(first + rel + kTurns, next);
             const int slot = (rel >> 1) % Sh::kCodes;
             if (!wait_warp(&ctl.codes_full[slot], (rel >> 1) / Sh::kCodes & 1, ctl)) break;
@@ -213,14 +214,14 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                         for (int e = 0; e < 4; ++e) a[(i * 4 + j) * 4 + e] = o[e];
                     }
                 }
-                if (h == 0 && !(ok = wait_warp(&ctl.a_free[turn], parity ^ 1, ctl))) break;
-                tmem_st32(a_tmem + turn * kACols + h * 32, a);
+                if (h == 0 && !(ok = wait_warp(&ctl.done[rel % kStages], (rel / kStages & 1) ^ 1, ctl))) break;
+                tmem_st32(a_tmem + rel % kStages * kACols + h * 32, a);
             }
             if (!ok) break;
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.a_full[turn]);
+            if (lane == 0) mbar_arrive(&ctl.a_full[rel % kStages]);
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) zero[i] = next[i];
         }
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < kAccumulators; ++i) {
                 if (g + i >= g1) break;
-                if (!(ok = wait_warp(&ctl.d_full[i], parity, ctl))) break;
+                if (!(ok = wait_warp(kOneD ? &ctl.done[i] : &ctl.d_full[i], parity, ctl))) break;
                 fence_after_sync();
 #pragma unroll
                 for (int b = 0; b < NTOK / 32; ++b) {
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             if (warp == kXWarp0 && elect_lane()) {
                 Ring<Sh::kX> r;
                 for (int tile = first; tile < end; ++tile, r.next()) {
-                    if (!wait_bar(&ctl.x_free[r.at], r.parity ^ 1, ctl)) {
+                    if (!wait_bar(&ctl.done[r.at], r.parity ^ 1, ctl)) {
                         for (int i = 0; i < Sh::kX && tile - (i + 1) >= first; ++i)      // as below, for the codes
                             wait_phase(&ctl.x_full[(r.at + Sh::kX - 1 - i) % Sh::kX], i < r.at ? r.parity : r.parity ^ 1, nullptr);
                         break;
@@ -389,14 +390,21 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             Ring<Sh::kX> xr;
             Ring<kAccumulators> d;
             for (int tile = first; tile < end; ++tile, ar.next(), xr.next()) {
-                if (!wait_bar(&ctl.x_full[xr.at], xr.parity, ctl) || !wait_bar(&ctl.a_full[ar.at], ar.parity, ctl)) break;
+                // asked for together, as each answer takes longer than the products of a few columns
+                const bool ready = mbar_try_wait(&ctl.x_full[xr.at], xr.parity) & mbar_try_wait(&ctl.a_full[ar.at], ar.parity) &
+                                   mbar_try_wait(&ctl.d_free[d.at], d.parity ^ 1);
+                if (!ready && !(wait_bar(&ctl.x_full[xr.at], xr.parity, ctl) && wait_bar(&ctl.a_full[ar.at], ar.parity, ctl) &&
+                                wait_bar(&ctl.d_free[d.at], d.parity ^ 1, ctl)))
+                    break;
                 fence_after_sync();
                 const uint32_t a = tmem + kACol0 + ar.at * kACols, b = b0 + xr.at * (Sh::kStage / 16);
                 bool ok = true;
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g, d.next()) {
-                    if (!(ok = wait_bar(&ctl.d_free[d.at], d.parity ^ 1, ctl))) break;
-                    fence_after_sync();
+                    if (g > 0) {
+                        if (!(ok = wait_bar(&ctl.d_free[d.at], d.parity ^ 1, ctl))) break;
+                        fence_after_sync();
+                    }
 #pragma unroll
                     for (int q = Sh::kParts - 1; q >= 0; --q)      // the smallest part first
 #pragma unroll
@@ -404,11 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                             mma_ts<idesc>(tmem + d.at * NTOK, a + ks * 8,
                                           b + (q * Sh::kBPart + (ks >> 2) * (NTOK * 128) + (ks & 3) * 32) / 16,
                                           q < Sh::kParts - 1 || ks > g * (8 / kGroups));
-                    mma_commit(&ctl.d_full[d.at]);
+                    if (!kOneD) mma_commit(&ctl.d_full[d.at]);
                 }
                 if (!ok) break;
-                mma_commit(&ctl.a_free[ar.at]);
-                mma_commit(&ctl.x_free[xr.at]);
+                mma_commit(&ctl.done[ar.at]);
+                if (!kOneX) mma_commit(&ctl.x_free[xr.at]);
             }
             mma_commit(&ctl.drain);
             wait_phase(&ctl.drain, 0, nullptr);
