@@ -15,11 +15,11 @@
 // thread issues all MMAs.  P overwrites the columns of S that it was
 // computed from.
 //
-// 8 trees of 64 tokens over <= 16384 (256 rows a kv head): 56.6 us, 576 TFLOP/s, 0.30 of
-// the measured rate.  A tile of keys takes about 4400 cycles, of which the products
-// are 2048: 1600 from a stream's scores to its probabilities, and the issuing thread's
-// own instructions between its products for most of the rest.  2 requests of 16
-// tokens over 131072 (64 rows): 155 us, 6.06 TB/s.
+// 8 trees of 64 tokens over <= 16384 (256 rows a kv head): 55.1 us, 591 TFLOP/s, 0.31 of
+// the measured rate.  A tile of keys takes about 3450 cycles, of which the products are
+// 2048: a stream goes from its scores to its probabilities in 1870 (650 of them the
+// exponentials) and waits 1580 for its two products of 512 and the hand-overs.
+// 2 requests of 16 tokens over 131072 (64 rows): 155 us, 6.1 TB/s, the bytes' bound.
 //
 // A row keeps the maximum it last scaled by until a score passes it by 2^8
 // (sums stay far inside fp32), so the output is rescaled in a few tiles only.

@@ -8,13 +8,15 @@
 //
 // Up to 8 tokens: w4_rows_kernel below, warp MMAs on registers filled straight from
 // memory.  More: w4_tc.cu, whose tcgen05 rate the flops then need.  4096 -> 16384, here
-// and there: 4 tokens 13.3 and 16.9 us, 8 tokens 14.7 and 16.9; in fp32 17.5 and 29.0,
-// 20.6 and 29.3; 4096 -> 4096: 8 tokens 7.2 and 9.4.  16 tokens would be two columns of
-// MMAs here and were slower (two calls of 8: 29.4 against 17.1).
+// and there: 4 tokens 13.3 and 16.6 us, 8 tokens 14.8 and 16.7; in fp32 17.7 and 30.6,
+// 20.6 and 30.7; 4096 -> 4096: 8 tokens 7.2 and 9.4; 16384 -> 4096: 4 tokens 17.4 and
+// 19.1, but 8 tokens 21.7 and 19.2 (x comes in two spans).  16 tokens would be two
+// columns of MMAs here (two calls of 8: 29.6 against 16.9).
 //
-// w4_rows_kernel reaches 2.9 TB/s (1 x 4096 -> 16384 12.3 us): the instructions that turn
-// codes into bf16 pairs and feed the MMAs, and for small matrices a few round trips to
-// memory (1 x 4096 -> 1024 3.7 us), take longer than the bytes.
+// w4_rows_kernel reads 3.4 TB/s of a large matrix (1 x 16384 -> 16384 40.9 us; 1 x 4096
+// -> 16384 12.3 us): the shifts and masks that turn codes into bf16 pairs fill 58 % of
+// the integer pipe, and starting, staging x and adding up take 3.5 us, which is all of
+// a small call (1 x 4096 -> 1024 3.7 us).
 //
 // fp32 x enters as three bf16 parts, whose sum is x to 2^-24: the products with whole
 // numbers are exact and the sums are fp32, so nothing is lost against fp32 arithmetic.

@@ -6,17 +6,20 @@
 //   twelve warps turn codes less zeros into bf16 (exact) in tensor memory, the A
 //                operand (through shared memory its 32 KB a tile, written and read
 //                again, bound an earlier form: 47 against 36 us at 64 x 4096 -> 16384);
-//   four warps   put x into shared memory, the B operand (fp32 x: three bf16 parts,
-//                multiplied one after another);
+//   x            is the B operand in shared memory: bf16 by tensor copies, whose order the
+//                codes follow (through registers, in the codes' order, four warps were
+//                what bound the kernel: 20.6 against 17.5 us); fp32 as three bf16 parts,
+//                multiplied one after another, that four warps make;
 //   one thread   issues the MMAs, one accumulator in tensor memory a group of columns;
 //   four warps   scale each group's accumulator and add it up in fp32, a thread a row.
 // When the rows give too few blocks the columns are split over a cluster, whose
 // blocks each add up a share of the tokens, in rank order.
 //
-// 64 x 4096 -> 16384: 20.6 us, 1.8 TB/s of codes, 416 TFLOP/s.  128 rows a block give 128
-// blocks, whose pipeline of five roles is what takes the time: neither memory (0.27 of
-// the measured rate), nor the tensor cores (17 % active), nor instruction issue (43 %)
-// is full, and the wait for the previous role is the largest stall of each.
+// 64 x 4096 -> 16384: 17.5 us (4.5 of them to start and end), 2.2 TB/s, 492 TFLOP/s.  128
+// rows a block make 128 blocks.  What bounds them is the integer pipe, 79 % busy there,
+// mostly with the shifts, byte moves and masks of the codes; a fourth warpgroup for
+// those, and a second one that scales, changed nothing (17.0 against 17.0 us with 32
+// tokens, 18.5 against 17.5 with 64).
 #include <cudaTypedefs.h>
 
 #include "tc_common.cuh"
@@ -471,8 +474,8 @@ int launch(const W4Params &p, const CUtensorMap &map, const CUtensorMap &x_map, 
     using Sh = W4Shape<E, NTOK>;
     const int rows = (p.h_out + kRows - 1) / kRows, tiles = (p.h_in + kCols - 1) / kCols, sms = num_sms();
     // Blocks that share the columns: as many as leave one block a SM, with two tiles of
-    // columns each.  Against one block: 16 x 4096 -> 4096 10.9 for 18.8 us, 64 x 16384 ->
-    // 4096 25.8 for 76.2.
+    // columns each.  Against one block, measured when all kernels were a fifth slower:
+    // 16 x 4096 -> 4096 10.9 for 18.8 us, 64 x 16384 -> 4096 25.8 for 76.2.
     int splits = 1;
     while (splits < 8 && rows * splits * 2 <= sms && tiles >= 4 * splits) splits *= 2;
     const void *func = reinterpret_cast<const void *>(w4_tc_kernel<E, GROUP, NTOK>);
@@ -514,7 +517,7 @@ int launch_w4_tc(int dtype, const W4Params &p, int group, cudaStream_t st) {
     if (!make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.codes), p.h_in / 2, p.h_out, p.h_in / 2, kCols, kRows))
         return LORA_ERR_CUDA;
     // Few tokens take the narrow tile of x: half the shared memory traffic, products and
-    // scaling.  16 x 4096 -> 16384: 17.1 us for 19.9 with 64 columns, in fp32 29.9 for 43.5.
+    // scaling.  16 x 4096 -> 16384: 16.9 us for 17.4 with 64 columns, in fp32 30.9 for 54.
     if (dtype == LORA_BF16)
         return p.T <= 32 ? launch<__nv_bfloat16, 32>(p, group, map, st) : launch<__nv_bfloat16, 64>(p, group, map, st);
     return p.T <= 32 ? launch<float, 32>(p, group, map, st) : launch<float, 64>(p, group, map, st);
