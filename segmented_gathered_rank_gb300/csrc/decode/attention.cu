@@ -14,9 +14,11 @@
 //   0.5; the rest is the chain launch -> page ids -> tile -> products -> sums in
 //   memory -> join.
 // attention_tc_kernel (bf16, attention_tc.cu): tcgen05 on units of 128 or 256 rows.
-// attention_simt_kernel (fp32): the same list, fp32 multiply-adds, which bound it
-//   (5 requests of up to 7 tokens over <= 300, 6 query heads of 80: 13.2 us, mostly
-//   the same chain).
+// attention_few_kernel, attention_simt_kernel (fp32): the same list, fp32
+//   multiply-adds.  Few rows: memory, as long as it comes in time (39 requests of one
+//   token over <= 6697, 4 heads of 112: 89 us, 4.4 TB/s).  More: instructions (4 trees
+//   of 22 over <= 13071, 28 query and 4 kv heads of 128: 430 us, 13.5 TFLOP/s), and for
+//   short contexts the chain above (5 requests of up to 7 tokens over <= 300: 13.3 us).
 // attention_join_kernel: joins the units that were cut between blocks.  It is
 //   launched while the attention still runs, and waits for it.
 //
@@ -578,6 +580,202 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
     cp_wait<0>();
 }
 
+constexpr int kFewTile = 64, kFewWarps = 8, kFewRows = 16;
+constexpr int kWarpRows = 4;       // query rows a warp
+
+__device__ __forceinline__ float2 mul_add2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+        "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// fp32 for few rows (16 a unit).  Keys and values go from memory straight into
+// registers: kLanes lanes have a token (16 bytes of every kLanes * 16), a warp kTokens
+// tokens at a time for 4 query rows, the next tokens on their way meanwhile and the page
+// ids of those after them.  A unit's rows are dealt to 1, 2 or 4 groups of warps, the
+// tokens to the warps of a group in turn, so that a single row has all eight warps.
+// Each group of lanes has a maximum, sum and output of its own per row until the block
+// leaves the unit; the maximum is raised only when a score passes it by 2^8.  In the
+// steps past the prefix, values that a row does not see are left out, whatever they are.
+// FULL: d is D.
+template <int D, bool FULL>
+__global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few_kernel(const AttnParams p) {
+    constexpr int kLanes = D == 256 ? 16 : 8, kTokens = 32 / kLanes, kVec = D / (4 * kLanes);
+    __shared__ ScanShared scan;
+    __shared__ float4 sums[kFewWarps][kWarpRows][D / 4];
+    __shared__ float2 tops[kFewWarps][kWarpRows];         // maximum, sum
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tok = lane / kLanes, first_chunk = lane % kLanes, chunks = p.d >> 2;
+    Cursor cur;
+    const uint32_t total = start_block(p, scan, cur);
+    while (cur.left > 0) {
+        const int tiles = min(cur.left, cur.r.tiles - cur.tile), rows = min(p.rt, cur.r.n * p.group - cur.row_tile * p.rt);
+        const int begin = cur.tile * kFewTile, end = min(begin + tiles * kFewTile, cur.r.len);
+        const int sure = min(cur.r.len - cur.r.n, end);        // tokens before it are seen by every row
+        const int groups = rows <= 4 ? 1 : rows <= 8 ? 2 : 4, parts = kFewWarps / groups;
+        const int row0 = (warp % groups) * kWarpRows, step = parts * kTokens;
+        float2 q[kWarpRows][2 * kVec], o[kWarpRows][2 * kVec];
+        float m[kWarpRows], l[kWarpRows];
+#pragma unroll
+        for (int a = 0; a < kWarpRows; ++a) {
+            const bool live = row0 + a < rows;
+            const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) +
+                                                                 (live ? row_offset(p, cur, cur.row_tile * p.rt + row0 + a) : 0));
+#pragma unroll
+            for (int x = 0; x < kVec; ++x) {
+                const int c = first_chunk + x * kLanes;
+                const float4 u = live && c < chunks ? src[c] : make_float4(0.f, 0.f, 0.f, 0.f);
+                q[a][2 * x] = make_float2(u.x, u.y);
+                q[a][2 * x + 1] = make_float2(u.z, u.w);
+                o[a][2 * x] = o[a][2 * x + 1] = make_float2(0.f, 0.f);
+            }
+            m[a] = -INFINITY;
+            l[a] = 0.f;
+        }
+        auto load = [&](float4 (&k)[kVec], float4 (&v)[kVec], int c, int page) {
+            const bool real = c < end;
+            const int row = real ? ((checked_page(p, page) * p.n_kv + cur.head) << p.page_shift) + (c & ((1 << p.page_shift) - 1)) : 0;
+            const long long at = (long long)row * chunks + first_chunk;
+#pragma unroll
+            for (int x = 0; x < kVec; ++x) {
+                const bool has = FULL || (real && first_chunk + x * kLanes < chunks);      // FULL: row 0, masked below
+                k[x] = has ? __ldg(static_cast<const float4 *>(p.k) + at + x * kLanes) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[x] = has ? __ldg(static_cast<const float4 *>(p.v) + at + x * kLanes) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        };
+        auto add = [&](const float4 (&k)[kVec], const float4 (&v)[kVec], int c) {
+            float s[kWarpRows];
+            bool on[kWarpRows];
+#pragma unroll
+            for (int a = 0; a < kWarpRows; ++a) {
+                float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int x = 0; x < kVec; ++x) {
+                    t = mul_add2(make_float2(k[x].x, k[x].y), q[a][2 * x], t);
+                    t = mul_add2(make_float2(k[x].z, k[x].w), q[a][2 * x + 1], t);
+                }
+                s[a] = t.x + t.y;
+                on[a] = true;
+            }
+#pragma unroll
+            for (int b = kLanes / 2; b > 0; b >>= 1)
+#pragma unroll
+                for (int a = 0; a < kWarpRows; ++a) s[a] += __shfl_xor_sync(0xffffffffu, s[a], b);
+            const bool masked = c - tok + kTokens > sure;
+            bool raise = false;
+#pragma unroll
+            for (int a = 0; a < kWarpRows; ++a) {
+                s[a] *= p.scale_log2;
+                if (masked) {
+                    const uint32_t see = row0 + a < rows ? seen_word(p, cur.r, (cur.row_tile * p.rt + row0 + a) / p.group, c & ~31) : 0u;
+                    on[a] = (see >> (c & 31)) & 1;
+                    if (!on[a]) s[a] = -INFINITY;
+                }
+                raise |= s[a] > m[a] + 8.f;        // from -infinity by any score
+            }
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int a = 0; a < kWarpRows; ++a) {
+                    const float top = fmaxf(m[a], s[a]), scale = top == -INFINITY ? 1.f : exp2f(m[a] - top);
+                    m[a] = top;
+                    l[a] *= scale;
+#pragma unroll
+                    for (int x = 0; x < 2 * kVec; ++x) o[a][x] = make_float2(o[a][x].x * scale, o[a][x].y * scale);
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < kWarpRows; ++a) {
+                const float w = on[a] ? exp2f(s[a] - (m[a] == -INFINITY ? 0.f : m[a])) : 0.f;
+                l[a] += w;
+                const float2 w2 = make_float2(w, w);
+                if (masked && !on[a]) continue;
+#pragma unroll
+                for (int x = 0; x < kVec; ++x) {
+                    o[a][2 * x] = mul_add2(w2, make_float2(v[x].x, v[x].y), o[a][2 * x]);
+                    o[a][2 * x + 1] = mul_add2(w2, make_float2(v[x].z, v[x].w), o[a][2 * x + 1]);
+                }
+            }
+        };
+        if (row0 < rows) {
+            float4 k0[kVec], v0[kVec], k1[kVec], v1[kVec];
+            int c = begin + (warp / groups) * kTokens + tok;
+            int page = page_of(p, cur.s, cur.r, c);
+            load(k0, v0, c, page);
+            page = page_of(p, cur.s, cur.r, c + step);
+            while (c - tok < end) {
+                load(k1, v1, c + step, page);
+                page = page_of(p, cur.s, cur.r, c + 2 * step);
+                add(k0, v0, c);
+                c += step;
+                if (c - tok >= end) break;
+                load(k0, v0, c + step, page);
+                page = page_of(p, cur.s, cur.r, c + 2 * step);
+                add(k1, v1, c);
+                c += step;
+            }
+        }
+        // the warp's groups of lanes join, then the warps of a group of rows
+#pragma unroll
+        for (int a = 0; a < kWarpRows; ++a) {
+            float top = m[a];
+#pragma unroll
+            for (int b = 16; b >= kLanes; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
+            const float scale = m[a] == -INFINITY ? 0.f : exp2f(m[a] - top);
+            l[a] *= scale;
+#pragma unroll
+            for (int x = 0; x < 2 * kVec; ++x) o[a][x] = make_float2(o[a][x].x * scale, o[a][x].y * scale);
+#pragma unroll
+            for (int b = 16; b >= kLanes; b >>= 1) {
+                l[a] += __shfl_xor_sync(0xffffffffu, l[a], b);
+#pragma unroll
+                for (int x = 0; x < 2 * kVec; ++x) {
+                    o[a][x].x += __shfl_xor_sync(0xffffffffu, o[a][x].x, b);
+                    o[a][x].y += __shfl_xor_sync(0xffffffffu, o[a][x].y, b);
+                }
+            }
+            if (tok == 0) {
+#pragma unroll
+                for (int x = 0; x < kVec; ++x)
+                    sums[warp][a][first_chunk + x * kLanes] = make_float4(o[a][2 * x].x, o[a][2 * x].y, o[a][2 * x + 1].x, o[a][2 * x + 1].y);
+                if (lane == 0) tops[warp][a] = make_float2(top, l[a]);
+            }
+        }
+        __syncthreads();
+        const bool whole = tiles == cur.r.tiles;
+        float *dst = partial_of(p, blockIdx.x, cur.tile > 0 ? 0 : 1);
+        for (int x = tid; x < rows * chunks; x += kFewWarps * 32) {
+            const int row = x / chunks, c = x - row * chunks, w0 = row / kWarpRows, a = row % kWarpRows;
+            float top = -INFINITY, sum = 0.f;
+            float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = w0; w < kFewWarps; w += groups) top = fmaxf(top, tops[w][a].x);
+            for (int w = w0; w < kFewWarps; w += groups) {
+                const float2 t = tops[w][a];
+                const float scale = t.x == -INFINITY ? 0.f : exp2f(t.x - top);
+                const float4 part = sums[w][a][c];
+                sum += t.y * scale;
+                u.x += part.x * scale;
+                u.y += part.y * scale;
+                u.z += part.z * scale;
+                u.w += part.w * scale;
+            }
+            if (whole) {
+                const float r = sum == 0.f ? 0.f : 1.f / sum;
+                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row_offset(p, cur, cur.row_tile * p.rt + row) + c * 4) =
+                    make_float4(u.x * r, u.y * r, u.z * r, u.w * r);
+            } else {
+                *reinterpret_cast<float4 *>(dst + partial_at(p, row, c * 4)) = u;
+                if (c == 0) *reinterpret_cast<float2 *>(dst + p.rt * p.d + row * 2) = make_float2(top, sum);
+            }
+        }
+        if (tid == 0 && cur.tile == 0 && !whole) record_unit(p, cur, tiles - 1, total);
+        __syncthreads();
+        cur.advance(p, tiles);
+    }
+}
+
 // Block (c, y): if a unit starts in block c's part of the list and goes on after it
 // (its record says so), adds up the parts: c's slot 1, then slot 0 of each block
 // after it until the unit ends.  A warp has 8 rows x 16 columns at a time: 128-byte
@@ -621,7 +819,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
 
 // What a call runs: rows and cached tokens a unit tile, blocks a SM.
 struct Variant {
-    bool tc;
+    bool tc, few;            // tcgen05; fp32 for few rows
     int rt, tk, per_sm, unit_cost;
 };
 
@@ -637,19 +835,26 @@ constexpr int kTmaMinPage = 8;
 // warp MMAs: 8 requests over <= 20000, 16 rows 63 and 57 us, 24 rows 60 and 76, 32 rows
 // 56 and 73, 64 rows 66 and 147; 64 requests over <= 900, 16 rows 58 and 32, 32 rows
 // 62 and 47, 64 rows 65 and 92; one request over 4000, 32 rows 17.0 and 17.1.
+// fp32: up to 8 rows go to the kernel without shared tiles.  It and the other: 39
+// requests of one token over <= 6697, 1 row of 112, 89 and 192 us; 48 over <= 25977, 1 row
+// of 64, 183 and 503; 48 over <= 421, 8 rows of 256, 77 and 145; 10 over <= 39506, 8 rows
+// of 112, 111 and 147; but 75 of 3 tokens over <= 16886, 12 rows of 80, 367 and 304.
 // Units of 256 rows when that is more than 128: 8 x 256 rows 53 us against 67 with
 // units of 128, 8 x 160 rows 55 against 58, 1 x 256 rows over <= 65536 72 against 99,
 // 32 x 160 over <= 2000 the same.
-// unit_cost, in tiles: 128 requests of one token take 305, 240, 242, 248 us with 0, 2,
-// 4, 8; 8 trees of 64 take 81, 62.5, 60.1, 60.2 with 2, 4, 6, 8 (the others' shares
-// grow with the cost of a unit's start and end against that of its tiles).
+// unit_cost, in tiles, stands for a unit's start and end: 128 requests of one token take
+// 305, 240, 242, 248 us with 0, 2, 4, 8; 8 trees of 64 take 81, 62.5, 60.1, 60.2 with 2, 4,
+// 6, 8; in fp32 39 requests of one token over <= 6697 take 103, 89, 91 with 1, 2, 4.
 Variant variant_of(const lora_kv_pages *kv, int group, int S, int T) {
     const int d = kv->head_dim;
-    if (kv->dtype == LORA_F32) return {false, kSimtRows, kSimtTile, d <= 128 ? 2 : 1, 1};
     const long long rows = (long long)T * group;       // against S: rows a request and kv head, on average
-    if ((d == 64 || d == 128) && rows > (long long)kRows * S) return {true, rows > 128LL * S ? 256 : 128, 128, 1, 8};
+    if (kv->dtype == LORA_F32) {
+        if (rows <= 8LL * S) return {false, true, kFewRows, kFewTile, d <= 64 ? 2 : 1, 2};
+        return {false, false, kSimtRows, kSimtTile, d <= 128 ? 2 : 1, 1};
+    }
+    if ((d == 64 || d == 128) && rows > (long long)kRows * S) return {true, false, rows > 128LL * S ? 256 : 128, 128, 1, 8};
     const bool tma = kv->page_size >= kTmaMinPage;
-    return {false, kRows, d <= 64 ? 128 : 64, tma && d <= 128 ? 2 : 1, 2};
+    return {false, false, kRows, d <= 64 ? 128 : 64, tma && d <= 128 ? 2 : 1, 2};
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -695,7 +900,16 @@ int launch_simt(const AttnParams &p, cudaStream_t st) {
     return cuda_status(cudaGetLastError());
 }
 
+template <int D>
+int launch_few(const AttnParams &p, cudaStream_t st) {
+    if (p.d == D) attention_few_kernel<D, true><<<p.grid, kFewWarps * 32, 0, st>>>(p);
+    else attention_few_kernel<D, false><<<p.grid, kFewWarps * 32, 0, st>>>(p);
+    count_launch();
+    return cuda_status(cudaGetLastError());
+}
+
 int launch_attention(const lora_kv_pages *kv, const AttnParams &p, const Variant &v, cudaStream_t st) {
+    if (v.few) return p.d <= 64 ? launch_few<64>(p, st) : p.d <= 128 ? launch_few<128>(p, st) : launch_few<256>(p, st);
     if (kv->dtype == LORA_F32)
         return p.d <= 64 ? launch_simt<64>(p, st) : p.d <= 128 ? launch_simt<128>(p, st) : launch_simt<256>(p, st);
     KvMaps maps = {};

@@ -475,3 +475,40 @@ def test_attention_refusals():
     assert status(out=None) == L.LORA_ERR_ARG
     assert status(ws_bytes=16) == L.LORA_ERR_ARG
     assert status(max_pages=1 << 30) == L.LORA_ERR_SHAPE
+
+
+# ----------------------------------------------------------------------------
+# fp32 attention of few rows a request on average (requests, n_q, n_kv, d, page, mask)
+# ----------------------------------------------------------------------------
+FEW_CASES = [
+    ([(1, 1)] * 3 + [(1, 64), (1, 65), (1, 4), (1, 3)], 3, 3, 8, 1, None),
+    ([(1, n) for n in (1, 31, 32, 33, 63, 64, 65, 127, 500)], 8, 1, 40, 8, None),
+    ([(40, 300)] + [(1, 20 + i) for i in range(30)], 2, 1, 72, 16, "tree"),       # one request of many row tiles
+    ([(17, 17), (0, 90)] + [(1, 1000 + i) for i in range(12)], 4, 4, 128, 1024, "random"),
+    ([(2, 700), (3, 64), (1, 1)], 6, 2, 136, 32, "tree"),
+    ([(5, 9), (1, 260), (1, 12)], 4, 2, 200, 4, "tree"),
+    ([(2, 3000)], 4, 1, 256, 64, "random"),
+    ([(1, 9000 - 37 * i) for i in range(40)], 2, 2, 64, 128, None)]
+
+
+@pytest.mark.parametrize("case", range(len(FEW_CASES)))
+def test_attention_few_rows(case):
+    requests, n_q, n_kv, d, page, mask = FEW_CASES[case]
+    check_attention(C.Attention(300 + case, I.F32, requests, n_q, n_kv, d, page, mask=mask))
+
+
+@pytest.mark.parametrize("d", [64, 80, 128, 256])
+def test_attention_few_rows_infinite_keys(d):
+    """Keys of the prefix that score -infinity drop out; of +infinity or NaN make their rows NaN."""
+    c = C.Attention(320, I.F32, [(1, 50), (1, 200), (1, 90)], 2, 2, d, 16)
+    c.q[...] = np.abs(c.q) + np.float32(0.5)
+    k = c.k.copy()
+    k[c.table[1, 0], :, 3, d - 1] = -np.inf             # request 1, token 3
+    got = run_attention(c, k=k)
+    without = c.k.copy()
+    without[c.table[1, 0], :, 3] = -1e30
+    assert np.array_equal(got, run_attention(c, k=without)) and np.isfinite(got).all()
+    k[c.table[1, 0], :, 3, d - 1] = np.inf
+    k[c.table[2, 0], :, 5, 0] = np.nan
+    got, clean = run_attention(c, k=k), run_attention(c)
+    assert np.array_equal(got[0], clean[0]) and np.isnan(got[1:]).all()
