@@ -108,6 +108,16 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *v) {
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;\n"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+          "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
 // Two fp32 operations an instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
@@ -253,12 +263,14 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                 if (g + i >= g1) break;
                 if (!(ok = wait_warp(kOneD ? &ctl.done[i] : &ctl.d_full[i], parity, ctl))) break;
                 fence_after_sync();
+                constexpr int kPart = NTOK < 32 ? NTOK : 32;
 #pragma unroll
-                for (int b = 0; b < NTOK / 32; ++b) {
-                    float d[32];
-                    tmem_ld32(ctl.tmem + quad + i * NTOK + b * 32, d);
+                for (int b = 0; b < NTOK / kPart; ++b) {
+                    float d[kPart];
+                    if constexpr (kPart == 32) tmem_ld32(ctl.tmem + quad + i * NTOK + b * 32, d);
+                    else tmem_ld16(ctl.tmem + quad + i * NTOK, d);
 #pragma unroll
-                    for (int t = 0; t < 16; ++t)
+                    for (int t = 0; t < kPart / 2; ++t)
                         acc[b * 16 + t] = fma2(make_float2(scale[i], scale[i]), make_float2(d[2 * t], d[2 * t + 1]), acc[b * 16 + t]);
                 }
                 fence_before_sync();
@@ -517,10 +529,12 @@ int launch_w4_tc(int dtype, const W4Params &p, int group, cudaStream_t st) {
     if (!make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.codes), p.h_in / 2, p.h_out, p.h_in / 2, kCols, kRows))
         return LORA_ERR_CUDA;
     // Few tokens take the narrow tile of x: half the shared memory traffic, products and
-    // scaling.  16 x 4096 -> 16384: 16.9 us for 17.4 with 64 columns, in fp32 30.9 for 54.
+    // scaling.  16 x 4096 -> 16384: 16.9 us with 32 columns for 17.4 with 64, in fp32 30.9 for
+    // 54; 12 x 4096 -> 16384: 16.3 us with 16 columns for 17.0 with 32, groups of 32 34.5 for
+    // 37.5, in fp32 25.5 for 30.9.
     if (dtype == LORA_BF16)
-        return p.T <= 32 ? launch<__nv_bfloat16, 32>(p, group, map, st) : launch<__nv_bfloat16, 64>(p, group, map, st);
-    return p.T <= 32 ? launch<float, 32>(p, group, map, st) : launch<float, 64>(p, group, map, st);
+        return p.T <= 16 ? launch<__nv_bfloat16, 16>(p, group, map, st) : p.T <= 32 ? launch<__nv_bfloat16, 32>(p, group, map, st) : launch<__nv_bfloat16, 64>(p, group, map, st);
+    return p.T <= 16 ? launch<float, 16>(p, group, map, st) : p.T <= 32 ? launch<float, 32>(p, group, map, st) : launch<float, 64>(p, group, map, st);
 }
 
 }  // namespace decode
