@@ -17,7 +17,7 @@
 // attention_few_kernel, attention_simt_kernel (fp32): the same list, fp32
 //   multiply-adds.  Few rows: memory, as long as it comes in time (39 requests of one
 //   token over <= 6697, 4 heads of 112: 89 us, 4.4 TB/s).  More: instructions (4 trees
-//   of 22 over <= 13071, 28 query and 4 kv heads of 128: 430 us, 13.5 TFLOP/s), and for
+//   of 22 over <= 13071, 28 query and 4 kv heads of 128: 362 us, 16.1 TFLOP/s), and for
 //   short contexts the chain above (5 requests of up to 7 tokens over <= 300: 13.3 us).
 // attention_join_kernel: joins the units that were cut between blocks.  It is
 //   launched while the attention still runs, and waits for it.
@@ -66,6 +66,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 mul_add2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+        "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
 
 constexpr int kThreads = 128;      // the join kernel's, the fp32 kernel's, the consumers of the MMA kernel
@@ -405,8 +415,10 @@ __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, 
     if (threadIdx.x == 0 && ctl.abort) flag_status(p.status, LORA_DEV_WAIT_TIMEOUT);
 }
 
-// fp32: four warps of four rows each, over 32 cached tokens a stage.  A lane
-// holds one token's score for its warp's rows, then four output columns.
+// fp32: four warps of four rows each, over 32 cached tokens a stage.  A lane holds one
+// token's score for its warp's rows, then every 32nd output column.  Two multiply-adds
+// an instruction; tiles that every row sees whole need neither masks nor a look at
+// the values (both steps: 430 -> 362 us for the 4 trees above).
 constexpr int kSimtTile = 32;
 constexpr int kSimtRows = 16;
 
@@ -454,7 +466,9 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
     };
     fetch();
     load(0);
-    float o[4][kCols], m[4], l[4];
+    float2 o2[2][kCols];                  // rows in pairs
+    float m[4], l[4];
+    auto o = [&](int a, int j) -> float & { return a & 1 ? o2[a >> 1][j].y : o2[a >> 1][j].x; };
     bool fresh = true;
     int start_tile = cur.tile;
     for (int it = 0; cur.left > 0; ++it) {
@@ -477,7 +491,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                 m[a] = -INFINITY;
                 l[a] = 0.f;
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) o[a][j] = 0.f;
+                for (int j = 0; j < kCols; ++j) o(a, j) = 0.f;
             }
         }
         load((it + 1) & 1);
@@ -485,23 +499,25 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
         __syncthreads();
         const float *ks = ring + (it & 1) * 2 * kSimtTile * kLd, *vs = ks + kSimtTile * kLd;
         if (row0 < rows) {
-            float s[4] = {};
+            const bool sure = (cur.tile + 1) * kSimtTile <= cur.r.len - cur.r.n;        // every row sees the whole tile
+            float2 s2[4] = {};
             for (int k = 0; k < p.d; k += 4) {
                 const float4 kk = *reinterpret_cast<const float4 *>(ks + lane * kLd + k);
 #pragma unroll
                 for (int a = 0; a < 4; ++a) {
                     const float4 qq = *reinterpret_cast<const float4 *>(qs + (row0 + a) * D + k);
-                    s[a] = fmaf(kk.x, qq.x, fmaf(kk.y, qq.y, fmaf(kk.z, qq.z, fmaf(kk.w, qq.w, s[a]))));
+                    s2[a] = mul_add2(make_float2(kk.x, kk.y), make_float2(qq.x, qq.y), s2[a]);
+                    s2[a] = mul_add2(make_float2(kk.z, kk.w), make_float2(qq.z, qq.w), s2[a]);
                 }
             }
             uint32_t see[4];
             float w[4];
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
-                see[a] = 0;
-                if (row0 + a < rows) see[a] = seen_word(p, cur.r, (cur.row_tile * p.rt + row0 + a) / p.group, cur.tile * kSimtTile);
+                see[a] = sure ? ~0u : 0u;
+                if (!sure && row0 + a < rows) see[a] = seen_word(p, cur.r, (cur.row_tile * p.rt + row0 + a) / p.group, cur.tile * kSimtTile);
                 const bool on = (see[a] >> lane) & 1;
-                const float x = on ? s[a] * p.scale_log2 : -INFINITY;
+                const float x = on ? (s2[a].x + s2[a].y) * p.scale_log2 : -INFINITY;
                 float top = x;
 #pragma unroll
                 for (int b = 16; b > 0; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
@@ -511,27 +527,38 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                 m[a] = m2;
                 l[a] = l[a] * scale + warp_sum(w[a]);
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) o[a][j] *= scale;
+                for (int j = 0; j < kCols; ++j) o(a, j) *= scale;
             }
             *reinterpret_cast<float4 *>(ps + (warp * kSimtTile + lane) * 4) = make_float4(w[0], w[1], w[2], w[3]);
             __syncwarp();
             // drafted values that are not finite must not meet the zero weights of rows that do not see them: they
             // count as zeros here and are added to the rows that do see them after
             bool bad = false;
+            if (sure) {
 #pragma unroll 4
-            for (int x = 0; x < kSimtTile; ++x) {
-                const float4 pp = *reinterpret_cast<const float4 *>(ps + (warp * kSimtTile + x) * 4);
+                for (int x = 0; x < kSimtTile; ++x) {
+                    const float4 pp = *reinterpret_cast<const float4 *>(ps + (warp * kSimtTile + x) * 4);
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) {
-                    float v = vs[x * kLd + j * 32 + lane];
-                    if (!(fabsf(v) < INFINITY)) {
-                        bad |= j * 32 + lane < p.d;
-                        v = 0.f;
+                    for (int j = 0; j < kCols; ++j) {
+                        const float v = vs[x * kLd + j * 32 + lane];
+                        o2[0][j] = mul_add2(make_float2(pp.x, pp.y), make_float2(v, v), o2[0][j]);
+                        o2[1][j] = mul_add2(make_float2(pp.z, pp.w), make_float2(v, v), o2[1][j]);
                     }
-                    o[0][j] = fmaf(pp.x, v, o[0][j]);
-                    o[1][j] = fmaf(pp.y, v, o[1][j]);
-                    o[2][j] = fmaf(pp.z, v, o[2][j]);
-                    o[3][j] = fmaf(pp.w, v, o[3][j]);
+                }
+            } else {
+#pragma unroll 4
+                for (int x = 0; x < kSimtTile; ++x) {
+                    const float4 pp = *reinterpret_cast<const float4 *>(ps + (warp * kSimtTile + x) * 4);
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) {
+                        float v = vs[x * kLd + j * 32 + lane];
+                        if (!(fabsf(v) < INFINITY)) {
+                            bad |= j * 32 + lane < p.d;
+                            v = 0.f;
+                        }
+                        o2[0][j] = mul_add2(make_float2(pp.x, pp.y), make_float2(v, v), o2[0][j]);
+                        o2[1][j] = mul_add2(make_float2(pp.z, pp.w), make_float2(v, v), o2[1][j]);
+                    }
                 }
             }
             if (__any_sync(0xffffffffu, bad)) {
@@ -543,7 +570,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                         const float v = vs[x * kLd + j * 32 + lane];
 #pragma unroll
                         for (int a = 0; a < 4; ++a)
-                            if (!(fabsf(v) < INFINITY) && ((see[a] >> x) & 1)) o[a][j] = fmaf(w4[a], v, o[a][j]);
+                            if (!(fabsf(v) < INFINITY) && ((see[a] >> x) & 1)) o(a, j) = fmaf(w4[a], v, o(a, j));
                     }
                 }
             }
@@ -564,9 +591,9 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                     const int col = j * 32 + lane;
                     if (col >= p.d) continue;
                     if (whole)
-                        static_cast<float *>(p.out)[row_offset(p, cur, cur.row_tile * p.rt + ur) + col] = o[a][j] * r;
+                        static_cast<float *>(p.out)[row_offset(p, cur, cur.row_tile * p.rt + ur) + col] = o(a, j) * r;
                     else
-                        dst[partial_at(p, ur, col)] = o[a][j];
+                        dst[partial_at(p, ur, col)] = o(a, j);
                 }
                 if (!whole && lane == 0) {
                     dst[p.rt * p.d + ur * 2] = m[a];
@@ -582,15 +609,6 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
 
 constexpr int kFewTile = 64, kFewWarps = 8, kFewRows = 16;
 constexpr int kWarpRows = 4;       // query rows a warp
-
-__device__ __forceinline__ float2 mul_add2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
-        "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
 
 // fp32 for few rows (16 a unit).  Keys and values go from memory straight into
 // registers: kLanes lanes have a token (16 bytes of every kLanes * 16), a warp kTokens
@@ -836,9 +854,9 @@ constexpr int kTmaMinPage = 8;
 // 56 and 73, 64 rows 66 and 147; 64 requests over <= 900, 16 rows 58 and 32, 32 rows
 // 62 and 47, 64 rows 65 and 92; one request over 4000, 32 rows 17.0 and 17.1.
 // fp32: up to 8 rows go to the kernel without shared tiles.  It and the other: 39
-// requests of one token over <= 6697, 1 row of 112, 89 and 192 us; 48 over <= 25977, 1 row
-// of 64, 183 and 503; 48 over <= 421, 8 rows of 256, 77 and 145; 10 over <= 39506, 8 rows
-// of 112, 111 and 147; but 75 of 3 tokens over <= 16886, 12 rows of 80, 367 and 304.
+// requests of one token over <= 6697, 1 row of 112, 89 and 166 us; 48 over <= 25977, 1 row
+// of 64, 183 and 491; 48 over <= 421, 8 rows of 256, 77 and 151; 10 over <= 39506, 8 rows
+// of 112, 110 and 122; but 75 of 3 tokens over <= 16886, 12 rows of 80, 367 and 247.
 // Units of 256 rows when that is more than 128: 8 x 256 rows 53 us against 67 with
 // units of 128, 8 x 160 rows 55 against 58, 1 x 256 rows over <= 65536 72 against 99,
 // 32 x 160 over <= 2000 the same.
