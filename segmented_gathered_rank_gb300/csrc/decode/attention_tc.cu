@@ -405,10 +405,19 @@ __device__ __forceinline__ long long row_at(const AttnParams &p, const Cursor &c
     const int warp = threadIdx.x >> 5, row = (warp & 3) * 32 + (threadIdx.x & 31) + (NQ == 2 ? (warp >> 2) * kTile : 0);
     return row < cur.r.n * p.group - cur.row_tile * p.rt ? row_offset(p, cur, cur.row_tile * p.rt + row) : -1;
 }
-// Starts the copies of the queries of a warp's 32 rows, D / 8 lanes a row (no row: zeros).
-template <int D>
-__device__ __forceinline__ void load_queries(const AttnParams &p, long long my_off, uint8_t *queries) {
+// Whether stream w has a part in the segment at the cursor: rows of its own, or key tiles.
+template <int NQ>
+__device__ __forceinline__ bool takes_part(const AttnParams &p, const Cursor &cur, int w) {
+    return w == 0 || (NQ == 2 ? cur.r.n * p.group - cur.row_tile * p.rt > kTile : segment_at(cur).tiles > 1);
+}
+// Starts the copies of the queries of a warp's 32 rows, D / 8 lanes a row (no row: zeros).  A stream
+// without a part in the segment copies nothing: it would not wait for its copies, which have no
+// order against those of the next segment to the same place.
+template <int D, int NQ>
+__device__ __forceinline__ void load_queries(const AttnParams &p, const Cursor &cur, uint8_t *queries) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (!takes_part<NQ>(p, cur, warp >> 2)) return;
+    const long long my_off = row_at<NQ>(p, cur);
     const uint32_t dst = smem_u32(queries) + (warp >> 2) * TcShape<D>::kSlot;
 #pragma unroll
     for (int x = 0; x < D / 8; ++x) {
@@ -440,7 +449,7 @@ __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t 
         const int rows = cur.r.n * p.group - cur.row_tile * p.rt;
         const int ur = row + (NQ == 2 ? w * kTile : 0);       // row of the unit
         const bool live = ur < rows, warp_live = ur - lane < rows;
-        const bool active = NQ == 2 ? (w == 0 || rows > kTile) : (w == 0 || seg.tiles > 1);
+        const bool active = takes_part<NQ>(p, cur, w);
         float m = -INFINITY, l = 0.f;
         const long long my_off = row_at<NQ>(p, cur);
         if (active) {
@@ -639,7 +648,7 @@ __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t 
         if (threadIdx.x == 0 && seg.first == 0 && !seg.whole) record_unit(p, cur, seg.tiles - 1, total);
         seq0 += 2 * seg.tiles;
         cur.advance(p, seg.tiles);
-        if (cur.left > 0) load_queries<D>(p, row_at<NQ>(p, cur), queries);
+        if (cur.left > 0) load_queries<D, NQ>(p, cur, queries);
     }
     cp_wait_all();
 }
@@ -682,7 +691,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     Cursor cur;
     const uint32_t total = start_block(p, scan, cur);
     // the first queries are requested before the ring's tiles, which would keep them waiting
-    if (warp < kProducer0 && cur.left > 0) load_queries<D>(p, row_at<NQ>(p, cur), queries);
+    if (warp < kProducer0 && cur.left > 0) load_queries<D, NQ>(p, cur, queries);
     fence_before_sync();
     __syncthreads();
     fence_after_sync();
