@@ -411,7 +411,9 @@ size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, int n_q_heads
  * Errors: LORA_ERR_ARG (includes ws_bytes too small), LORA_ERR_SHAPE (also for
  * tables so wide that the list of key tiles could pass 2^31).
  * Device-detected: LORA_DEV_BAD_SEGMENTS, LORA_DEV_BAD_LENGTH,
- * LORA_DEV_BAD_PAGE, LORA_DEV_WAIT_TIMEOUT; no access leaves the arrays.
+ * LORA_DEV_BAD_PAGE, LORA_DEV_WAIT_TIMEOUT; no access leaves the arrays.  Where
+ * segments overlap until they name more work than T tokens can have, nothing is
+ * computed and out stays as it was.
  */
 int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, const int *seg_starts, int S, int T,
                         const int *kv_lens, const int *page_table, int max_pages, const long long *tree_mask,

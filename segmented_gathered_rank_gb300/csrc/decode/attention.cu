@@ -1005,7 +1005,9 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     p.tk_shift = decode::log2_of(variant.tk);
     p.unit_cost = variant.unit_cost;
     const long long tiles = (long long)max_pages * kv->page_size / variant.tk + 1 + variant.unit_cost;
-    if (tiles * ((long long)T * p.group / variant.rt + S) > 0x7fffffffLL / p.n_kv) return LORA_ERR_SHAPE;
+    const long long units = (long long)T * p.group / variant.rt + S;       // a kv head
+    if (tiles * units > 0x7fffffffLL / p.n_kv) return LORA_ERR_SHAPE;
+    p.max_places = (uint32_t)(tiles * units * p.n_kv);
     p.grid = num_sms() * variant.per_sm;
     p.records = static_cast<JoinRecord *>(workspace);
     p.partial = reinterpret_cast<float *>(p.records + p.grid);

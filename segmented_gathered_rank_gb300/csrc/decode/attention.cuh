@@ -35,6 +35,7 @@ struct AttnParams {
     float *partial;          // [grid][2]: sums [d / 4][rt][4], then the rows' maximum and sum [rt][2]
     int rt, tk, grid;        // rows a unit, tokens a tile (a power of two), blocks
     int tk_shift, unit_cost;
+    uint32_t max_places;     // of the list of any table that keeps the rules; below 2^31
 };
 
 struct Request {
@@ -94,8 +95,11 @@ struct ScanShared {
     Request r;
 };
 
-// The list has below 2^31 places (checked on the host).  The first place of block c:
-// total / grid places each, one more for the first total % grid.
+// Sum of places, at most 2^31 - 1: segments that overlap can name any number of them.
+__device__ __forceinline__ uint32_t add_places(uint32_t a, uint32_t b) { return min(a + b, 0x7fffffffu); }
+
+// The list has up to max_places places.  The first place of block c: total / grid places
+// each, one more for the first total % grid.
 __device__ __forceinline__ uint32_t block_begin(uint32_t total, uint32_t c, uint32_t grid) {
     const uint32_t each = total / grid;
     return each * c + min(c, total - each * grid);
@@ -107,7 +111,8 @@ __device__ __forceinline__ int block_of(uint32_t total, uint32_t x, uint32_t gri
 }
 
 // Called by every thread of the block: the block's first tile, and the length of
-// the list.  Lets the join launch; block 0 reports bad tables.
+// the list.  Lets the join launch; block 0 reports bad tables.  A table whose segments
+// overlap until they name more places than the T tokens can have has an empty list.
 __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared &sh, Cursor &c) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.S + kScanThreads - 1) / kScanThreads;
@@ -118,7 +123,7 @@ __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared 
     Request r = {};
     for (int s = s0; s < s1; ++s) {
         r = request_of(p, s, &bad);
-        mine += r.places(p);
+        mine = add_places(mine, r.places(p));
         if (flags && (p.starts[s + 1] < p.starts[s] || (s == 0 && p.starts[0] != 0) || (s + 1 == p.S && p.starts[p.S] != p.T)))
             bad |= LORA_DEV_BAD_SEGMENTS;
     }
@@ -127,7 +132,7 @@ __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared 
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t other = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += other;
+        if (lane >= o) upto = add_places(upto, other);
     }
     if (lane == 31 && warp < kScanThreads / 32) sh.sums[warp] = upto;
     if (tid == 0) {
@@ -138,11 +143,12 @@ __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared 
     uint32_t total = 0, before = upto - mine;
 #pragma unroll
     for (int w = 0; w < kScanThreads / 32; ++w) {
-        if (w < warp) before += sh.sums[w];
-        total += sh.sums[w];
+        if (w < warp) before = add_places(before, sh.sums[w]);
+        total = add_places(total, sh.sums[w]);
     }
+    if (total > p.max_places) total = 0;
     const uint32_t pos = block_begin(total, blockIdx.x, p.grid);
-    if (pos >= before && pos < before + mine) {
+    if (total > 0 && pos >= before && pos < before + mine) {
         uint32_t rest = pos - before;
         for (int s = s0; s < s1; ++s) {
             if (s1 - s0 > 1) r = request_of(p, s);
@@ -173,11 +179,12 @@ __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared 
 }
 
 // Thread 0, where a unit started in the block and goes on after the block's last
-// tile, at which the cursor is.
+// tile, at which the cursor is.  Its parts stay inside the grid also when the lengths change
+// under the call, between one read and the next.
 __device__ __forceinline__ void record_unit(const AttnParams &p, const Cursor &cur, int tile, uint32_t total) {
     JoinRecord rec = {};
     const uint32_t last = block_begin(total, blockIdx.x + 1, p.grid) - 1 + (cur.r.tiles - 1 - tile);
-    rec.parts = block_of(total, last, p.grid) - (int)blockIdx.x + 1;
+    rec.parts = (int)min((uint32_t)block_of(total, last, p.grid), (uint32_t)p.grid - 1) - (int)blockIdx.x + 1;
     rec.begin = cur.r.begin;
     rec.head = cur.head;
     rec.first_row = cur.row_tile * p.rt;

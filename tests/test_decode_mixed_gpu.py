@@ -11,6 +11,7 @@ if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a GPU", allow_module_level=True)
 
 from segmented_gathered_rank_gb300 import inputs as I  # noqa: E402
+from segmented_gathered_rank_gb300 import lora as L  # noqa: E402
 from tests import decode_cases as C  # noqa: E402
 from tests.test_decode_gpu import check_attention, run_attention  # noqa: E402
 
@@ -29,3 +30,36 @@ def test_attention_streams_take_turns(requests, d):
     got = check_attention(c)
     for _ in range(10):
         assert np.array_equal(run_attention(c), got)
+
+
+# ----------------------------------------------------------------------------
+# Segments that overlap: T tokens counted again and again
+# ----------------------------------------------------------------------------
+def overlapping(dtype, T, S, n_q, n_kv, d, page, max_pages, guard=4096):
+    """seg_starts 0, T, 0, T, ..: (status word, whether out was written, whether the bytes after the workspace were)."""
+    dt = torch.bfloat16 if dtype == I.BF16 else torch.float32
+    k, v = (torch.randn(4, n_kv, page, d, device="cuda").to(dt) for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kv = L.KvPages(L.LORA_BF16 if dtype == I.BF16 else L.LORA_F32, k, v, 4, page, n_kv, d, status=status)
+    q = torch.randn(T, n_q * d, device="cuda").to(dt)
+    out = torch.full_like(q, float("nan"))
+    starts = torch.tensor([0, T] * (S // 2) + [0], dtype=torch.int32, device="cuda")
+    lens = torch.full((S,), max_pages * page, dtype=torch.int32, device="cuda")
+    table = torch.zeros((S, max_pages), dtype=torch.int32, device="cuda")
+    size = L.lora_tree_attention_workspace_size(kv, n_q, S, T)
+    ws = torch.full((size + guard,), 0xAB, dtype=torch.uint8, device="cuda")
+    L.lora_tree_attention(kv, q, n_q, starts, S, T, lens, table, max_pages, None, 0, 0.1, out, ws, ws_bytes=size)
+    torch.cuda.synchronize()
+    return int(status), not bool(torch.isnan(out).all()), not bool((ws[size:] == 0xAB).all())
+
+
+@pytest.mark.parametrize("dtype, T, S, d", [(I.BF16, 32, 64, 64), (I.BF16, 128, 16, 128), (I.BF16, 512, 16, 64), (I.F32, 32, 64, 128),
+                                            (I.F32, 512, 16, 64)])
+def test_attention_overlapping_segments_compute_nothing(dtype, T, S, d):
+    assert overlapping(dtype, T, S, 8, 1, d, 64, 8) == (L.LORA_DEV_BAD_SEGMENTS, False, False)
+
+
+@pytest.mark.parametrize("T, S", [(2048, 2048), (8192, 2048)])
+def test_attention_overlapping_segments_beyond_32_bits_of_places(T, S):
+    """The places that these tables name pass 2^32."""
+    assert overlapping(I.BF16, T, S, 32, 8, 64, 1024, 128) == (L.LORA_DEV_BAD_SEGMENTS, False, False)
