@@ -207,8 +207,6 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < 4; ++i)      // tensor copies with 128-byte swizzling: 16-byte chunks XORed with the row
                 w[i] = *reinterpret_cast<const uint4 *>(src + ((((rel & 1) * 4 + i) ^ (row & 7)) << 4));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.codes_free[slot]);
             bool ok = true;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -234,7 +232,12 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
             asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
             fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.a_full[rel % kStages]);
+            if (lane == 0) {
+                mbar_arrive(&ctl.a_full[rel % kStages]);
+                // The slot is given back here and not after the loads above: what the codes became is in tensor
+                // memory, so the loads are complete.  Right after them the next copy overtook some of them.
+                mbar_arrive(&ctl.codes_free[slot]);
+            }
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) zero[i] = next[i];
         }

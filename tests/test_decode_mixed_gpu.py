@@ -10,10 +10,11 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a GPU", allow_module_level=True)
 
+from oracle import decode as D  # noqa: E402
 from segmented_gathered_rank_gb300 import inputs as I  # noqa: E402
 from segmented_gathered_rank_gb300 import lora as L  # noqa: E402
 from tests import decode_cases as C  # noqa: E402
-from tests.test_decode_gpu import check_attention, run_attention  # noqa: E402
+from tests.test_decode_gpu import CODE, TORCH, assert_within, check_attention, cuda, host, run_attention  # noqa: E402
 
 
 # ----------------------------------------------------------------------------
@@ -63,3 +64,21 @@ def test_attention_overlapping_segments_compute_nothing(dtype, T, S, d):
 def test_attention_overlapping_segments_beyond_32_bits_of_places(T, S):
     """The places that these tables name pass 2^32."""
     assert overlapping(I.BF16, T, S, 32, 8, 64, 1024, 128) == (L.LORA_DEV_BAD_SEGMENTS, False, False)
+
+
+# ----------------------------------------------------------------------------
+# 4-bit products on tcgen05: many tiles of weights through the stages of tensor memory
+# ----------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [I.BF16, I.F32])
+@pytest.mark.parametrize("T, h_in, h_out, group", [(40, 8192, 1300, 128), (12, 16384, 300, 64), (24, 12320, 640, 32)])
+def test_w4_stages_of_long_rows(T, h_in, h_out, group, dtype):
+    x, codes, scales, z = C.w4_case(T + h_in, dtype, T, h_in, h_out, group, True)
+    ref, mag = D.w4_matvec(x, codes, scales, z, group)
+    args = (CODE[dtype], C.device(x, dtype), T, h_in, cuda(codes), cuda(scales).to(torch.bfloat16), cuda(z), group, h_out)
+    y = torch.full((T, h_out), float("nan"), dtype=TORCH[dtype], device="cuda")
+    L.lora_w4_matvec(*args, y)
+    assert_within(host(y), ref, C.w4_bound(ref, mag, h_in, group, dtype))
+    for _ in range(20):
+        again = torch.full_like(y, float("nan"))
+        L.lora_w4_matvec(*args, again)
+        assert torch.equal(again, y)
