@@ -225,7 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_tc_kernel(const __grid_constan
                         for (int e = 0; e < 4; ++e) a[(i * 4 + j) * 4 + e] = o[e];
                     }
                 }
-                if (h == 0 && !(ok = wait_warp(&ctl.done[rel % kStages], (rel / kStages & 1) ^ 1, ctl))) break;
+                if (h == 0) {
+                    if (!(ok = wait_warp(&ctl.done[rel % kStages], (rel / kStages & 1) ^ 1, ctl))) break;
+                    fence_after_sync();        // the products that read the stage come before these stores
+                }
                 tmem_st32(a_tmem + rel % kStages * kACols + h * 32, a);
             }
             if (!ok) break;
