@@ -1,0 +1,58 @@
+"""The Python side of the decode-step calls without a GPU: what their objects keep alive and what they pass on."""
+import ctypes
+import gc
+import weakref
+
+from segmented_gathered_rank_gb300 import lora as L
+
+BUF = ctypes.create_string_buffer(1 << 16)
+P = (ctypes.addressof(BUF) + 255) & ~255
+
+
+class Cuda:
+    """Stands in for a CUDA tensor: host memory that nothing reads."""
+    is_cuda = True
+
+    def __init__(self, *shape, stride=None):
+        self.shape, self._stride = shape, stride or tuple(self._dense(shape))
+
+    @staticmethod
+    def _dense(shape):
+        step = 1
+        for n in reversed(shape):
+            yield step
+            step *= n
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i):
+        return self._stride[i]
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return P
+
+
+def test_pages_let_their_tensors_go():
+    """No cycle: a cache of many GB is free as soon as the last reference to it is."""
+    k, v = Cuda(4, 2, 8, 16), Cuda(4, 2, 8, 16)
+    kv = L.KvPages(L.LORA_BF16, k, v, 4, 8, 2, 16)
+    assert L.lora_tree_attention_workspace_size(kv, 4, 0, 0) == 16       # the struct as the library reads it
+    alive = weakref.ref(k), weakref.ref(v)
+    del k, v
+    assert all(a() is not None for a in alive)
+    gc.disable()
+    try:
+        del kv
+        assert all(a() is None for a in alive)
+    finally:
+        gc.enable()
