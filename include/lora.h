@@ -383,8 +383,9 @@ int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, const void 
                    int n_pos, int rot_dim, int interleaved, const void *q_norm, const void *k_norm, float eps,
                    void *q_out, lora_stream stream);
 
-/* Bytes of device workspace lora_tree_attention needs for T drafted tokens of
- * S requests (0 on a bad argument). */
+/* Bytes of device workspace that lora_tree_attention needs at most for up to T
+ * drafted tokens of up to S requests (0 on a bad argument): a workspace of the
+ * largest batch serves every smaller one. */
 size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T);
 
 /*

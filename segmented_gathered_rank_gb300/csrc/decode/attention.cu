@@ -956,7 +956,8 @@ using namespace lora;
 extern "C" size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T) {
     if (decode::check_kv(kv, n_q_heads) || n_q_heads < 1 || S < 0 || T < 0) return 0;
     if (S == 0) return 16;
-    return partial_bytes(variant_of(kv, n_q_heads / kv->n_kv_heads, S, T), kv->head_dim) + 16;
+    // T tokens of one request have the most rows a kv head, and the kernel for more rows never needs less
+    return partial_bytes(variant_of(kv, n_q_heads / kv->n_kv_heads, 1, T), kv->head_dim) + 16;
 }
 
 extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, const int *seg_starts, int S,
@@ -976,7 +977,8 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
         (((uintptr_t)seg_starts | (uintptr_t)kv_lens | (uintptr_t)page_table) & 3u))
         return LORA_ERR_ARG;
     if (num_sms() < 1) return LORA_ERR_CUDA;
-    if (ws_bytes < lora_tree_attention_workspace_size(kv, n_q_heads, S, T)) return LORA_ERR_ARG;
+    const Variant variant = variant_of(kv, n_q_heads / kv->n_kv_heads, S, T);
+    if (ws_bytes < partial_bytes(variant, kv->head_dim) + 16) return LORA_ERR_ARG;
     decode::AttnParams p;
     p.q = q;
     p.k = kv->k;
@@ -999,7 +1001,6 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     p.out = out;
     p.status = kv->status;
     cudaStream_t st = (cudaStream_t)stream;
-    const Variant variant = variant_of(kv, p.group, S, T);
     p.rt = variant.rt;
     p.tk = variant.tk;
     p.tk_shift = decode::log2_of(variant.tk);

@@ -82,3 +82,32 @@ def test_w4_stages_of_long_rows(T, h_in, h_out, group, dtype):
         again = torch.full_like(y, float("nan"))
         L.lora_w4_matvec(*args, again)
         assert torch.equal(again, y)
+
+
+# ----------------------------------------------------------------------------
+# A workspace made once for the largest batch
+# ----------------------------------------------------------------------------
+def pages_of(dtype, n_kv, d, page=16, n_pages=40):
+    k, v = (torch.randn(n_pages, n_kv, page, d, device="cuda").to(TORCH[dtype]) for _ in range(2))
+    return L.KvPages(CODE[dtype], k, v, n_pages, page, n_kv, d)
+
+
+@pytest.mark.parametrize("dtype", [I.BF16, I.F32])
+@pytest.mark.parametrize("d", [64, 80, 128, 256])
+def test_workspace_of_the_largest_batch_serves_every_smaller_one(dtype, d):
+    for group in (1, 4, 16):
+        kv = pages_of(dtype, 2, d)
+        most = L.lora_tree_attention_workspace_size(kv, 2 * group, 128, 128)
+        ws = torch.empty(most, dtype=torch.uint8, device="cuda")
+        for T in (1, 2, 7, 16, 33, 64, 127, 128):
+            for S in {1, 2, (T + 15) // 16, (T + 1) // 2, T} - {t for t in (1, 2) if t > T}:
+                assert L.lora_tree_attention_workspace_size(kv, 2 * group, S, T) <= most
+                starts = torch.linspace(0, T, S + 1, device="cuda").round().int()
+                lens = (starts[1:] - starts[:-1] + 3).int()
+                table = torch.arange(9, device="cuda", dtype=torch.int32).repeat(S, 1)
+                q = torch.randn(T, 2 * group * d, device="cuda").to(TORCH[dtype])
+                out, own = torch.zeros_like(q), torch.zeros_like(q)
+                size = L.lora_tree_attention_workspace_size(kv, 2 * group, S, T)
+                for o, w in ((out, ws), (own, torch.empty(size, dtype=torch.uint8, device="cuda"))):
+                    L.lora_tree_attention(kv, q, 2 * group, starts, S, T, lens, table, 9, None, 0, 0.1, o, w)
+                assert torch.equal(out, own) and bool(torch.isfinite(out.float()).all())
