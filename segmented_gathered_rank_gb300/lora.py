@@ -166,7 +166,8 @@ def _rows(t):
         return None, 0
     if not (t.is_cuda and t.dim() == 2 and t.stride(1) == 1):
         raise ValueError("expected a CUDA matrix with contiguous rows")
-    return t.data_ptr(), t.stride(0)
+    # a single row's stride means nothing, and need not be the width (a transposed column's is 1)
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def _hptr(a):

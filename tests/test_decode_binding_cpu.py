@@ -56,3 +56,20 @@ def test_pages_let_their_tensors_go():
         assert all(a() is None for a in alive)
     finally:
         gc.enable()
+
+
+def append_status(monkeypatch, q, k, v, T, n_q=4, slots=None):
+    """What lora_kv_append returns without launching: n_pos 0 is refused last, once the row strides have passed."""
+    got = []
+    monkeypatch.setattr(L, "_check", lambda rc, where: got.append(rc))
+    kv = L.KvPages(L.LORA_BF16, Cuda(4, 2, 8, 16), Cuda(4, 2, 8, 16), 4, 8, 2, 16)
+    L.lora_kv_append(kv, q, k, v, T, n_q, Cuda(T), Cuda(T), Cuda(1, 16), 0, 16, False, Cuda(T, n_q * 16), stream=0)
+    return got[0]
+
+
+def test_append_takes_one_row_of_any_stride(monkeypatch):
+    """(W @ x.T).T of one token has the shape [1, width] and the strides (1, 1)."""
+    one = [Cuda(1, w, stride=(1, 1)) for w in (64, 32, 32)]
+    assert append_status(monkeypatch, *one, T=1) == L.LORA_ERR_ARG       # for n_pos, not LORA_ERR_SHAPE for the rows
+    two = [Cuda(2, w, stride=(8, 1)) for w in (64, 32, 32)]
+    assert append_status(monkeypatch, *two, T=2) == L.LORA_ERR_SHAPE     # rows that overlap
