@@ -167,7 +167,10 @@ def _rows(t):
     if not (t.is_cuda and t.dim() == 2 and t.stride(1) == 1):
         raise ValueError("expected a CUDA matrix with contiguous rows")
     # a single row's stride means nothing, and need not be the width (a transposed column's is 1)
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld > 0x7fffffff:
+        raise ValueError("rows are further apart than an int says")
+    return t.data_ptr(), ld
 
 
 def _hptr(a):

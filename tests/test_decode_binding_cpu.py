@@ -3,6 +3,8 @@ import ctypes
 import gc
 import weakref
 
+import pytest
+
 from segmented_gathered_rank_gb300 import lora as L
 
 BUF = ctypes.create_string_buffer(1 << 16)
@@ -73,3 +75,10 @@ def test_append_takes_one_row_of_any_stride(monkeypatch):
     assert append_status(monkeypatch, *one, T=1) == L.LORA_ERR_ARG       # for n_pos, not LORA_ERR_SHAPE for the rows
     two = [Cuda(2, w, stride=(8, 1)) for w in (64, 32, 32)]
     assert append_status(monkeypatch, *two, T=2) == L.LORA_ERR_SHAPE     # rows that overlap
+
+
+def test_append_refuses_rows_further_apart_than_an_int(monkeypatch):
+    k = Cuda(2, 32)
+    for far in (1 << 31, (1 << 32) + 64):           # the second would wrap to a valid distance
+        with pytest.raises(ValueError):
+            append_status(monkeypatch, Cuda(2, 64, stride=(far, 1)), k, k, T=2)
