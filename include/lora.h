@@ -332,7 +332,8 @@ int lora_layer_forward_fp8(lora_pool *pool, int matrix, const void *x, const voi
  *           k/2 when k is even, the high half when it is odd; 0..15.
  *   scales  h_out x h_in/group, bf16.
  *   zeros   h_out x h_in/group bytes (0..15), or NULL: 8 everywhere.
- *   group   32, 64 or 128; h_in is a multiple of it.  h_out is any size.
+ *   group   32, 64 or 128; h_in is a multiple of it.  h_out is any size.  Both are
+ *           at most 2^31 - 2^16.
  * Meant for the few tokens of a decode step: the weights are read once for
  * every 64 tokens.
  * Errors: LORA_ERR_ARG, LORA_ERR_SHAPE (group, or h_in no multiple of it).

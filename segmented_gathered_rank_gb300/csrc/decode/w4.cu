@@ -287,6 +287,7 @@ int launch(const W4Params &p, int group, cudaStream_t st) {
 }
 
 constexpr int kRowsTokens = 8;       // one MMA's columns
+constexpr int kMaxSize = 0x7fff0000;  // of h_in and h_out: loops step past the end by up to 8 tiles of 16 rows on every SM
 
 }  // namespace
 }  // namespace lora
@@ -297,6 +298,7 @@ extern "C" int lora_w4_matvec(int dtype, const void *x, int T, int h_in, const v
                               const void *zeros, int group, int h_out, void *y, lora_stream stream) {
     if ((dtype != LORA_F32 && dtype != LORA_BF16) || T < 0 || h_in <= 0 || h_out <= 0) return LORA_ERR_ARG;
     if ((group != 32 && group != 64 && group != 128) || h_in % group) return LORA_ERR_SHAPE;
+    if (h_in > kMaxSize || h_out > kMaxSize) return LORA_ERR_SHAPE;
     if (T == 0) return LORA_OK;
     if (!x || !codes || !scales || !y || !aligned16(x) || !aligned16(codes) || !aligned16(y) ||
         ((uintptr_t)scales & 1u))

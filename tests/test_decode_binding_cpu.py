@@ -1,6 +1,7 @@
 """The Python side of the decode-step calls without a GPU: what their objects keep alive and what they pass on."""
 import ctypes
 import gc
+import math
 import weakref
 
 import pytest
@@ -16,20 +17,10 @@ class Cuda:
     is_cuda = True
 
     def __init__(self, *shape, stride=None):
-        self.shape, self._stride = shape, stride or tuple(self._dense(shape))
-
-    @staticmethod
-    def _dense(shape):
-        step = 1
-        for n in reversed(shape):
-            yield step
-            step *= n
+        self.shape, self._stride = shape, stride or tuple(math.prod(shape[i + 1:]) for i in range(len(shape)))
 
     def numel(self):
-        n = 1
-        for s in self.shape:
-            n *= s
-        return n
+        return math.prod(self.shape)
 
     def dim(self):
         return len(self.shape)
@@ -80,5 +71,13 @@ def test_append_takes_one_row_of_any_stride(monkeypatch):
 def test_append_refuses_rows_further_apart_than_an_int(monkeypatch):
     k = Cuda(2, 32)
     for far in (1 << 31, (1 << 32) + 64):           # the second would wrap to a valid distance
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="an int"):
             append_status(monkeypatch, Cuda(2, 64, stride=(far, 1)), k, k, T=2)
+
+
+@pytest.mark.parametrize("T", [1, 8, 9, 64])
+@pytest.mark.parametrize("h_in, h_out", [(64, (1 << 31) - 1), (64, (1 << 31) - (1 << 16) + 1), ((1 << 31) - 64, 32)])
+def test_w4_refuses_sizes_that_indexes_would_pass(T, h_in, h_out):
+    before = L.lora_launch_count()
+    assert L._lib.lora_w4_matvec(L.LORA_BF16, P, T, h_in, P, P, None, 64, h_out, P, None) == L.LORA_ERR_SHAPE
+    assert L.lora_launch_count() == before
