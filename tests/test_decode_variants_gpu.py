@@ -79,11 +79,13 @@ def test_attention_small_pages_in_place_and_bad_pages(n_q, page):
 
 
 # ----------------------------------------------------------------------------
-# Append, neighbouring pairs, three heads a thread (more than 1500 blocks of one)
+# Append, neighbouring pairs: three heads a thread (more than 1000 blocks of one in bf16, 16000 in fp32, and more than one
+# block a token), and the sizes beside that
 # ----------------------------------------------------------------------------
 MANY_HEADS = [   # T, n_q, n_kv, d, rot, page, interleaved, norm, fused
     (800, 28, 4, 128, 128, 16, True, True, True), (1600, 5, 1, 64, 32, 64, True, False, False), (400, 33, 11, 256, 128, 8, True, True, False),
-    (1001, 16, 8, 80, 80, 1, True, True, True), (1501, 0, 3, 128, 8, 32, True, True, False)]
+    (1001, 16, 8, 80, 80, 1, True, True, True), (1501, 0, 3, 128, 8, 32, True, True, False),
+    (1000, 28, 4, 64, 64, 16, True, True, False), (801, 0, 9, 128, 8, 4, True, True, False), (8201, 14, 2, 128, 8, 16, True, True, False)]
 
 
 @pytest.mark.parametrize("dtype", [I.BF16, I.F32])
