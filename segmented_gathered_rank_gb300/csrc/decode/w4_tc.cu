@@ -22,6 +22,8 @@
 // tokens, 18.5 against 17.5 with 64).
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "tc_common.cuh"
 #include "w4.cuh"
 
@@ -487,28 +489,62 @@ bool make_map(CUtensorMap *map, CUtensorMapDataType type, void *base, int cols, 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+cudaLaunchAttribute cluster_of(int blocks) {
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = blocks;
+    a.val.clusterDim.y = 1;
+    a.val.clusterDim.z = 1;
+    return a;
+}
+
+// Clusters of 2^log2 blocks (1 to 3) that run at once on the current device, asked for once
+// a device: every form of the kernel has one block an SM.  The SMs that can share a
+// cluster come in groups that are no multiples of eight, so there are 76, 36 and 15 here.
+int clusters_at_once(const void *func, size_t smem, int log2) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][4];          // plus one; 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) dev = -1;
+    if (dev >= 0 && known[dev][log2].load(std::memory_order_relaxed)) return known[dev][log2].load(std::memory_order_relaxed) - 1;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr = cluster_of(1 << log2);
+    cfg.gridDim = dim3(1 << log2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, func, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev >= 0) known[dev][log2].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 template <typename E, int GROUP, int NTOK>
 int launch(const W4Params &p, const CUtensorMap &map, const CUtensorMap &x_map, cudaStream_t st) {
     using Sh = W4Shape<E, NTOK>;
-    const int rows = (p.h_out + kRows - 1) / kRows, tiles = (p.h_in + kCols - 1) / kCols, sms = num_sms();
-    // Blocks that share the columns: as many as leave one block a SM, with two tiles of
-    // columns each.  Against one block, measured when all kernels were a fifth slower:
-    // 16 x 4096 -> 4096 10.9 for 18.8 us, 64 x 16384 -> 4096 25.8 for 76.2.
-    int splits = 1;
-    while (splits < 8 && rows * splits * 2 <= sms && tiles >= 4 * splits) splits *= 2;
+    const int rows = (p.h_out + kRows - 1) / kRows, tiles = (p.h_in + kCols - 1) / kCols;
     const void *func = reinterpret_cast<const void *>(w4_tc_kernel<E, GROUP, NTOK>);
     if (smem_optin(func, Sh::kSmem)) return LORA_ERR_CUDA;
+    // Blocks that share the columns: as many as let all clusters run at once, with two tiles
+    // of columns each.  Against one block: 16 x 4096 -> 4096 8.4 for 15.4 us, 64 x 16384 ->
+    // 4096 20.8 for 53.6.  Clusters that wait for others cost more than smaller ones: 16 x
+    // 4096 -> 2048 (16 row blocks) 8.3 us in fours for 12.0 in eights, 64 x 4096 -> 4736 (37)
+    // 13.8 in twos for 18.3 in fours; up to the limit, 16 x 4096 -> 1920 (15) 7.0 in eights
+    // for 8.3 in fours, 64 x 4096 -> 4608 (36) 11.0 in fours for 13.7 in twos.
+    int log2 = 0;
+    while (log2 < 3 && tiles >= 4 << log2 && rows <= clusters_at_once(func, Sh::kSmem, log2 + 1)) ++log2;
+    const int splits = 1 << log2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * splits));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Sh::kSmem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
+    cudaLaunchAttribute attr = cluster_of(splits);
+    cfg.attrs = &attr;
     cfg.numAttrs = splits > 1 ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_tc_kernel<E, GROUP, NTOK>, map, x_map, p, splits);
     count_launch();

@@ -111,8 +111,10 @@ def test_kv_append_many_heads(case, dtype):
 # 4-bit products: more rows than one turn of the blocks, wide projections without a cluster, non-finite activations
 # ----------------------------------------------------------------------------
 W4_TALL = [   # T, h_in, h_out, group
+    (12, 2080, 1900, 32), (12, 2048, 2048, 128), (64, 2112, 2400, 64), (33, 2048, 4600, 128), (16, 2048, 4800, 64),   # clusters of 8, 4, 2
     (1, 512, 20001, 64), (8, 256, 39000, 128), (3, 288, 19600, 32), (5, 4224, 19500, 128),            # warp MMAs, more than one turn
-    (9, 1024, 9800, 128), (24, 1056, 9999, 32), (64, 1088, 9801, 64), (40, 640, 20000, 128)]          # tcgen05, no cluster
+    (9, 1024, 9800, 128), (24, 1056, 9999, 32), (64, 1088, 9801, 64), (40, 640, 20000, 128),          # tcgen05, no cluster
+    (1, 14336, 300, 64), (3, 14336, 300, 64), (6, 13312, 2500, 128), (7, 13312, 2500, 32)]            # x in parts; both kernels
 
 
 @pytest.mark.parametrize("dtype", [I.BF16, I.F32])
