@@ -25,16 +25,17 @@ constexpr int kThreads = 256;
 // and one head a thread would make more than kManyBlocks blocks: the loads of three heads
 // are in flight at once, and position, slot and table row are read once for them.  bf16,
 // one head a thread against three: 48 heads of 128, 256 tokens (768 blocks) 2.7 and 2.9
-// us, 512 tokens (1536) 3.9 and 3.6, 4096 tokens 26.3 and 22.5, 8192 tokens 50.6 and 40.0 (2, 4,
-// 6 heads were slower than 3); 80 heads of 128, 4096 tokens 40.4 and 34.5; 48 heads of 64
-// 17.4 and 15.7; 24 heads of 256 26.3 and 22.4; 18 heads of 128 16.5 and 14.5.  Where a
-// block holds all heads, threads would idle: 9 heads of 128, 4096 tokens 7.1 and 8.9, 16
-// heads 11.7 and 12.9.  20 heads, 512 tokens (1024 blocks) 3.2 and 2.8.  fp32 has twice the bytes in flight as it is, and gains from three
-// heads only where the call leaves L2 far behind: 48 heads of 128, 1024 tokens 11.3 and
-// 13.6 us, 4096 tokens (12288 blocks) 36.2 and 37.8, 8192 tokens 74.6 and 68.3; 20 heads,
-// 8192 tokens (16384 blocks) 40.6 and 36.4.  Halves that pair up are read in 8-byte
-// pieces, and there one head a thread is as fast or faster throughout (bf16, 48 heads of
-// 128, 4096 tokens 27.3 against 30.2 us, 512 tokens 3.9 against 4.9), so they always take it.
+// us, 512 tokens (1536) 3.9 and 3.6, 4096 tokens 26.3 and 22.5, 8192 tokens 50.6 and 40.0
+// (2, 4, 6 heads were slower than 3); 20 heads of 128, 512 tokens (1024 blocks) 3.2 and 2.8;
+// at 4096 tokens 80 heads of 128 40.4 and 34.5, 48 heads of 64 17.4 and 15.7, 24 heads of
+// 256 26.3 and 22.4, 18 heads of 128 16.5 and 14.5.  Where a block holds all heads, threads
+// would idle: 4096 tokens of 9 heads of 128 7.1 and 8.9, of 16 heads 11.7 and 12.9.  fp32
+// has twice the bytes on their way as it is, and gains only in the largest calls: 48 heads
+// of 128, 1024 tokens 11.3 and 13.6 us, 4096 tokens (12288 blocks) 36.2 and 37.8, 8192
+// tokens 74.6 and 68.3; 20 heads, 8192 tokens (16384 blocks) 40.6 and 36.4.  Halves that
+// pair up are read in 8-byte pieces, and there one head a thread is as fast or faster
+// throughout (bf16, 48 heads of 128, 4096 tokens 27.3 against 30.2 us, 512 tokens 3.9
+// against 4.9), so they always take it.
 constexpr int kHeads = 3;
 template <typename E>
 constexpr int kManyBlocks = sizeof(E) == 2 ? 1000 : 16000;

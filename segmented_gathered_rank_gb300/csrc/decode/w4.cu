@@ -1,22 +1,22 @@
 // Matrix products with 4-bit weights (lora_w4_matvec):
 //   y[t][n] = sum_g s[n][g] * sum_{k in g} x[t][k] * (c[n][k] - z[n][g])
 //
-// The codes are read once: half a byte a weight against 2 T flops, so memory is the
-// bound up to T of about 140 (at 1.9 PFLOP/s and 6.8 TB/s).  Codes less zeros are whole numbers of 5 bits, exact in
-// bf16, so the inner sums run on the tensor cores without rounding the weights, and
+// The codes are read once: half a byte a weight against 2 T flops (6 T with fp32
+// activations), so the bytes are the larger part of the floor up to T of about 70 (23 in
+// fp32) at 1.9 PFLOP/s and 6.8 TB/s.  Codes less zeros are whole numbers of 5 bits, exact
+// in bf16, so the inner sums run on the tensor cores without rounding the weights, and
 // each group's sum is scaled in fp32.
 //
 // Up to 8 tokens: w4_rows_kernel below, warp MMAs on registers filled straight from
-// memory.  More: w4_tc.cu, whose tcgen05 rate the flops then need.  4096 -> 16384, here
-// and there: 4 tokens 13.3 and 16.6 us, 8 tokens 14.8 and 16.7; in fp32 17.7 and 30.6,
-// 20.6 and 30.7; 4096 -> 4096: 8 tokens 7.2 and 9.4; 16384 -> 4096: 4 tokens 17.4 and
-// 19.1, but 8 tokens 21.7 and 19.2 (x comes in two spans).  16 tokens would be two
-// columns of MMAs here (two calls of 8: 29.6 against 16.9).
+// memory, unless its blocks would stage too much of x each (takes_rows).  More: w4_tc.cu,
+// whose tcgen05 rate the flops then need; 16 tokens would be two columns of MMAs here
+// (4096 -> 16384, two calls of 8: 29.6 against 16.6 us).
 //
-// w4_rows_kernel reads 3.4 TB/s of a large matrix (1 x 16384 -> 16384 40.9 us; 1 x 4096
-// -> 16384 12.3 us): the shifts and masks that turn codes into bf16 pairs fill 58 % of
-// the integer pipe, and starting, staging x and adding up take 3.5 us, which is all of
-// a small call (1 x 4096 -> 1024 3.7 us).
+// w4_rows_kernel reads 3.4 TB/s of a large matrix (1 x 16384 -> 16384 41.0 us; 1 x 4096 ->
+// 16384 12.3 us), half of what memory gives.  No unit is full either: the shifts and masks
+// that turn codes into bf16 pairs take 58 % of the integer pipe, and a warp stalls about
+// as long for that pipe as for its loads and for fixed latencies.  Starting, staging x
+// and adding up take 3.5 us, which is all of a small call (1 x 4096 -> 1024 3.7 us).
 //
 // fp32 x enters as three bf16 parts, whose sum is x to 2^-24: the products with whole
 // numbers are exact and the sums are fp32, so nothing is lost against fp32 arithmetic.
@@ -260,19 +260,28 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) w4_rows_kernel(const W4Para
     }
 }
 
+// x of a block of columns in shared memory, and blocks that fit there at once.
+template <typename E>
+constexpr int kBlockBytes = 4 * (sizeof(E) == 2 ? 1 : 3) * 512;
+template <typename E>
+constexpr int kFit = kXBytes / kBlockBytes<E>;
+
+// Tiles of 16 rows a thread block: as few as let one block a SM cover all rows, at most 8.
+int tiles_of(const W4Params &p, int sms) {
+    const int row_tiles = (p.h_out + 15) / 16, each = (row_tiles + sms - 1) / sms;
+    return each < 8 ? each : 8;
+}
+
 template <typename E, int GROUP>
 int launch(const W4Params &p, cudaStream_t st) {
     const int sms = num_sms();
-    if (sms < 1) return LORA_ERR_CUDA;
-    // tiles of 16 rows a block: as few as let one block a SM cover all rows, at most 8
-    const int row_tiles = (p.h_out + 15) / 16, each = (row_tiles + sms - 1) / sms, tiles = each < 8 ? each : 8;
+    const int row_tiles = (p.h_out + 15) / 16, tiles = tiles_of(p, sms);
     const int blocks = (p.h_in + kBlock - 1) / kBlock;
-    constexpr int kBlockBytes = 4 * (sizeof(E) == 2 ? 1 : 3) * 512, kFit = kXBytes / kBlockBytes;
     // all of x in shared memory at once, or spans of whole rounds of the ring
-    const int most = blocks <= kFit ? kMaxWarps : kFit / kDepth, slices = kMaxWarps / tiles < most ? kMaxWarps / tiles : most;
-    const int span = blocks <= kFit ? blocks : kFit / (slices * kDepth) * (slices * kDepth);
+    const int most = blocks <= kFit<E> ? kMaxWarps : kFit<E> / kDepth, slices = kMaxWarps / tiles < most ? kMaxWarps / tiles : most;
+    const int span = blocks <= kFit<E> ? blocks : kFit<E> / (slices * kDepth) * (slices * kDepth);
     const size_t sums = (size_t)tiles * slices * 8 * 17 * sizeof(float);
-    const size_t smem = (size_t)span * kBlockBytes > sums ? (size_t)span * kBlockBytes : sums;
+    const size_t smem = (size_t)span * kBlockBytes<E> > sums ? (size_t)span * kBlockBytes<E> : sums;
     const int need = (row_tiles + tiles - 1) / tiles, grid = need < sms ? need : sms;
     const auto kernel = blocks >= kDepth * slices ? w4_rows_kernel<E, GROUP, true> : w4_rows_kernel<E, GROUP, false>;
     if (smem_optin(reinterpret_cast<const void *>(kernel), smem)) return LORA_ERR_CUDA;
@@ -288,6 +297,26 @@ int launch(const W4Params &p, int group, cudaStream_t st) {
 
 constexpr int kRowsTokens = 8;       // one MMA's columns
 constexpr int kMaxSize = 0x7fff0000;  // of h_in and h_out: loops step past the end by up to 8 tiles of 16 rows on every SM
+
+// Whether w4_rows_kernel takes the tokens: up to 8 when x fits in shared memory at once.  When
+// it comes in parts, a block stages and awaits each of them, for as many row tiles as it
+// has (0.065 us a thousand elements in bf16, twice that in fp32), while the other kernel
+// is 3 to 4 us slower to start, so then only up to kStaged elements a row tile.  Here and
+// there, us, one part: 4096 -> 16384 4 tokens 13.3 and 16.5, 8 tokens 14.9 and 16.7, in fp32
+// 20.5 and 24.3; 4096 -> 4096 8 tokens 7.2 and 8.5, in fp32 10.3 and 9.9; 4096 -> 1024 8 tokens
+// 5.8 and 6.8, in fp32 8.6 and 7.3; 4096 -> 2048 in fp32 8.7 and 9.7.  Parts, up to the limit
+// and past it: 16384 -> 4096 (two row tiles) 4 tokens 17.4 and 18.7, 6 tokens 19.5 and 18.6, in
+// fp32 3 tokens 23.5 and 26.7, 8 tokens 34.9 and 27.1 (but 4 tokens 25.6 and 27.0); 4128 -> 4001
+// in fp32 5 tokens 11.3 and 12.8; 8192 -> 4096 in fp32 5 tokens 15.1 and 15.7, 7 tokens 17.4 and
+// 15.8; 13312 -> 1024 (one) 3 tokens 9.6 and 10.5, 5 tokens 11.3 and 10.5; 14336 -> 1024 in fp32
+// 1 token 12.4 and 12.9, 8 tokens 32.1 and 14.0; 16384 -> 16384 (seven) 8 tokens 50.1 and 52.7.
+constexpr long long kStaged = 40960;        // elements of x, an fp32 one as one and a half
+template <typename E>
+bool takes_rows(const W4Params &p, int sms) {
+    if (p.T > kRowsTokens) return false;
+    return (p.h_in + kBlock - 1) / kBlock <= kFit<E> ||
+           (long long)p.T * p.h_in * (sizeof(E) == 2 ? 2 : 3) <= 2 * kStaged * tiles_of(p, sms);
+}
 
 }  // namespace
 }  // namespace lora
@@ -314,12 +343,15 @@ extern "C" int lora_w4_matvec(int dtype, const void *x, int T, int h_in, const v
     p.h_out = h_out;
     p.groups = h_in / group;
     const size_t e = dtype == LORA_BF16 ? 2 : 4;
+    const int sms = num_sms();
+    if (sms < 1) return LORA_ERR_CUDA;
     constexpr int kTcTokens = 64;
     for (int t = 0; t < T; t += kTcTokens) {
         p.x = static_cast<const char *>(x) + (size_t)t * h_in * e;
         p.y = static_cast<char *>(y) + (size_t)t * h_out * e;
         p.T = T - t < kTcTokens ? T - t : kTcTokens;
-        const int rc = p.T > kRowsTokens      ? decode::launch_w4_tc(dtype, p, group, (cudaStream_t)stream)
+        const bool rows = dtype == LORA_BF16 ? takes_rows<__nv_bfloat16>(p, sms) : takes_rows<float>(p, sms);
+        const int rc = !rows                  ? decode::launch_w4_tc(dtype, p, group, (cudaStream_t)stream)
                        : dtype == LORA_BF16 ? launch<__nv_bfloat16>(p, group, (cudaStream_t)stream)
                                             : launch<float>(p, group, (cudaStream_t)stream);
         if (rc) return rc;
