@@ -650,7 +650,6 @@ __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t 
         cur.advance(p, seg.tiles);
         if (cur.left > 0) load_queries<D, NQ>(p, cur, queries);
     }
-    cp_wait_all();
 }
 
 template <int D, int NQ, bool TMA>
@@ -701,6 +700,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
     if (warp < kProducer0) {
         attend<D, NQ>(p, cur, total, queries, ctl);
+        cp_wait_all();             // also where it gave up: no copy outlives the block
     } else if (warp < kMmaWarp) {
         produce<D, TMA>(p, maps, cur, ring, ctl);
         if (!TMA) cp_wait_all();
