@@ -273,8 +273,7 @@ int tiles_of(const W4Params &p, int sms) {
 }
 
 template <typename E, int GROUP>
-int launch(const W4Params &p, cudaStream_t st) {
-    const int sms = num_sms();
+int launch(const W4Params &p, int sms, cudaStream_t st) {
     const int row_tiles = (p.h_out + 15) / 16, tiles = tiles_of(p, sms);
     const int blocks = (p.h_in + kBlock - 1) / kBlock;
     // all of x in shared memory at once, or spans of whole rounds of the ring
@@ -291,8 +290,8 @@ int launch(const W4Params &p, cudaStream_t st) {
 }
 
 template <typename E>
-int launch(const W4Params &p, int group, cudaStream_t st) {
-    return group == 128 ? launch<E, 128>(p, st) : group == 64 ? launch<E, 64>(p, st) : launch<E, 32>(p, st);
+int launch(const W4Params &p, int group, int sms, cudaStream_t st) {
+    return group == 128 ? launch<E, 128>(p, sms, st) : group == 64 ? launch<E, 64>(p, sms, st) : launch<E, 32>(p, sms, st);
 }
 
 constexpr int kRowsTokens = 8;       // one MMA's columns
@@ -352,8 +351,8 @@ extern "C" int lora_w4_matvec(int dtype, const void *x, int T, int h_in, const v
         p.T = T - t < kTcTokens ? T - t : kTcTokens;
         const bool rows = dtype == LORA_BF16 ? takes_rows<__nv_bfloat16>(p, sms) : takes_rows<float>(p, sms);
         const int rc = !rows                  ? decode::launch_w4_tc(dtype, p, group, (cudaStream_t)stream)
-                       : dtype == LORA_BF16 ? launch<__nv_bfloat16>(p, group, (cudaStream_t)stream)
-                                            : launch<float>(p, group, (cudaStream_t)stream);
+                       : dtype == LORA_BF16 ? launch<__nv_bfloat16>(p, group, sms, (cudaStream_t)stream)
+                                            : launch<float>(p, group, sms, (cudaStream_t)stream);
         if (rc) return rc;
     }
     return LORA_OK;

@@ -566,7 +566,7 @@ int launch(const W4Params &p, int group, const CUtensorMap &map, cudaStream_t st
 namespace decode {
 
 int launch_w4_tc(int dtype, const W4Params &p, int group, cudaStream_t st) {
-    if (!encode_fn() || num_sms() < 1) return LORA_ERR_CUDA;
+    if (!encode_fn()) return LORA_ERR_CUDA;
     CUtensorMap map;        // codes as bytes [h_out][h_in / 2]
     if (!make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.codes), p.h_in / 2, p.h_out, p.h_in / 2, kCols, kRows))
         return LORA_ERR_CUDA;

@@ -117,13 +117,14 @@ class KvPages(ctypes.Structure):
         super().__init__(dtype, n_pages, page_size, n_kv_heads, head_dim, _dptr(k_pages), _dptr(v_pages),
                          _dptr(status))
         self.tensors = (k_pages, v_pages, status)
+        self.address = ctypes.addressof(self)      # what calls pass: no reference, so no cycle, and quick
 
 
 _sig("lora_w4_matvec", _I, _I, _P, _I, _I, _P, _P, _P, _I, _I, _P, _P)
-_sig("lora_kv_append", _I, ctypes.POINTER(KvPages), _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P,
+_sig("lora_kv_append", _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P,
      ctypes.c_float, _P, _P)
-_sig("lora_tree_attention_workspace_size", ctypes.c_size_t, ctypes.POINTER(KvPages), _I, _I, _I)
-_sig("lora_tree_attention", _I, ctypes.POINTER(KvPages), _P, _I, _P, _I, _I, _P, _P, _I, _P, _I, ctypes.c_float, _P, _P,
+_sig("lora_tree_attention_workspace_size", ctypes.c_size_t, _P, _I, _I, _I)
+_sig("lora_tree_attention", _I, _P, _P, _I, _P, _I, _I, _P, _P, _I, _P, _I, ctypes.c_float, _P, _P,
      ctypes.c_size_t, _P)
 
 
@@ -376,7 +377,7 @@ def lora_kv_append(kv, q, k, v, T, n_q_heads, positions, slots, cos_sin, n_pos, 
                    q_norm=None, k_norm=None, eps=1e-6, stream=None) -> None:
     """Norm, rotation and append of T tokens; q, k and v are matrices of T rows (any row stride), slots int64."""
     (pq, ld_q), (pk, ld_k), (pv, ld_v) = _rows(q), _rows(k), _rows(v)
-    rc = _lib.lora_kv_append(kv, pq, ld_q, pk, ld_k, pv, ld_v, T, n_q_heads, _ptr(positions), _ptr(slots),
+    rc = _lib.lora_kv_append(kv.address, pq, ld_q, pk, ld_k, pv, ld_v, T, n_q_heads, _ptr(positions), _ptr(slots),
                              _ptr(cos_sin), n_pos, rot_dim, 1 if interleaved else 0, _ptr(q_norm), _ptr(k_norm), eps,
                              _ptr(q_out), _stream_ptr(stream))
     if rc:
@@ -384,7 +385,7 @@ def lora_kv_append(kv, q, k, v, T, n_q_heads, positions, slots, cos_sin, n_pos, 
 
 
 def lora_tree_attention_workspace_size(kv, n_q_heads, S, T) -> int:
-    return int(_lib.lora_tree_attention_workspace_size(kv, n_q_heads, S, T))
+    return int(_lib.lora_tree_attention_workspace_size(kv.address, n_q_heads, S, T))
 
 
 def lora_tree_attention(kv, q, n_q_heads, seg_starts, S, T, kv_lens, page_table, max_pages, tree_mask, mask_words, scale,
@@ -392,7 +393,7 @@ def lora_tree_attention(kv, q, n_q_heads, seg_starts, S, T, kv_lens, page_table,
     """Attention of drafted tokens over the cache; tree_mask is int64 [T, mask_words], or None for causal chains."""
     if ws_bytes is None:
         ws_bytes = workspace.nbytes
-    rc = _lib.lora_tree_attention(kv, _ptr(q), n_q_heads, _ptr(seg_starts), S, T, _ptr(kv_lens), _ptr(page_table),
+    rc = _lib.lora_tree_attention(kv.address, _ptr(q), n_q_heads, _ptr(seg_starts), S, T, _ptr(kv_lens), _ptr(page_table),
                                   max_pages, _ptr(tree_mask), mask_words, scale, _ptr(out), _ptr(workspace), ws_bytes,
                                   _stream_ptr(stream))
     if rc:
