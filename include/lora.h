@@ -336,7 +336,9 @@ int lora_layer_forward_fp8(lora_pool *pool, int matrix, const void *x, const voi
  *           at most 2^31 - 2^16.
  * Meant for the few tokens of a decode step: the weights are read once for
  * every 64 tokens.
- * Errors: LORA_ERR_ARG, LORA_ERR_SHAPE (group, or h_in no multiple of it).
+ * Errors: LORA_ERR_ARG, LORA_ERR_SHAPE (group, or h_in no multiple of it, or a
+ * size beyond the limit).  The call has no status word: a pipeline wait inside a
+ * kernel that gives up (after 2 s) leaves NaN in the outputs that it concerns.
  */
 int lora_w4_matvec(int dtype, const void *x, int T, int h_in, const void *codes, const void *scales,
                    const void *zeros, int group, int h_out, void *y, lora_stream stream);

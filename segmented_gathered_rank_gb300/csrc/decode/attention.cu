@@ -10,7 +10,7 @@
 //   so memory is the bound: one producer warp keeps two to six tiles of K and V on
 //   their way, four warps take a quarter of each tile's keys and add up at the unit's
 //   end.  128 requests of one token over <= 8192 cached, 32 query and 8 kv heads of
-//   128: 240 us, 6.64 TB/s.  One request over 777: 10.6 us, of which the bytes take
+//   128: 240 us, 6.64 TB/s.  One request over 777: 10.7 us, of which the bytes take
 //   0.5; the rest is the chain launch -> page ids -> tile -> products -> sums in
 //   memory -> join.
 // attention_tc_kernel (bf16, attention_tc.cu): tcgen05 on units of 128 or 256 rows.
@@ -18,13 +18,16 @@
 //   multiply-adds.  Few rows: memory, as long as it comes in time (39 requests of one
 //   token over <= 6697, 4 heads of 112: 89 us, 4.4 TB/s).  More: instructions (4 trees
 //   of 22 over <= 13071, 28 query and 4 kv heads of 128: 362 us, 16.1 TFLOP/s), and for
-//   short contexts the chain above (5 requests of up to 7 tokens over <= 300: 13.3 us).
+//   short contexts the chain above (5 requests of up to 7 tokens over <= 300: 13.5 us).
 // attention_join_kernel: joins the units that were cut between blocks.  It is
 //   launched while the attention still runs, and waits for it.
 //
 // Probabilities are rounded to bf16 for their product with V, as the tensor cores
 // take them (2^-9 relative each, no more than V's own rounding); maximum, sum and
-// output stay in fp32.  fp32 caches are not rounded anywhere.
+// output stay in fp32.  The error of a bf16 output, root mean square, is then 0.0018 to
+// 0.0023 of the outputs' size (long contexts most), of which storing them in bf16 makes
+// 0.00165.  A second bf16 part of each probability would take that away for half as many
+// products again, which are what bounds large trees.  fp32 caches are not rounded anywhere.
 #include <cudaTypedefs.h>
 
 #include <type_traits>

@@ -15,7 +15,7 @@
 // thread issues all MMAs.  P overwrites the columns of S that it was
 // computed from.
 //
-// 8 trees of 64 tokens over <= 16384 (256 rows a kv head): 55.1 us, 591 TFLOP/s, 0.31 of
+// 8 trees of 64 tokens over <= 16384 (256 rows a kv head): 55.6 us, 586 TFLOP/s, 0.30 of
 // the measured rate.  A tile of keys takes about 3450 cycles, of which the products are
 // 2048: a stream goes from its scores to its probabilities in 1870 (650 of them the
 // exponentials) and waits 1580 for its two products of 512 and the hand-overs.

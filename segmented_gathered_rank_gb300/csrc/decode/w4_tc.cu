@@ -15,8 +15,8 @@
 // When the rows give too few blocks the columns are split over a cluster, whose
 // blocks each add up a share of the tokens, in rank order.
 //
-// 64 x 4096 -> 16384: 17.5 us (4.5 of them to start and end), 2.2 TB/s, 492 TFLOP/s.  128
-// rows a block make 128 blocks.  What bounds them is the integer pipe, 79 % busy there,
+// 64 x 4096 -> 16384: 17.5 us (4.5 of them to start and end), 2.2 TB/s, 490 TFLOP/s.  128
+// rows a block make 128 blocks.  What bounds them is the integer pipe, 78 % busy there,
 // mostly with the shifts, byte moves and masks of the codes; a fourth warpgroup for
 // those, and a second one that scales, changed nothing (17.0 against 17.0 us with 32
 // tokens, 18.5 against 17.5 with 64).
@@ -571,9 +571,9 @@ int launch_w4_tc(int dtype, const W4Params &p, int group, cudaStream_t st) {
     if (!make_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t *>(p.codes), p.h_in / 2, p.h_out, p.h_in / 2, kCols, kRows))
         return LORA_ERR_CUDA;
     // Few tokens take the narrow tile of x: half the shared memory traffic, products and
-    // scaling.  16 x 4096 -> 16384: 16.9 us with 32 columns for 17.4 with 64, in fp32 30.9 for
-    // 54; 12 x 4096 -> 16384: 16.3 us with 16 columns for 17.0 with 32, groups of 32 34.5 for
-    // 37.5, in fp32 25.5 for 30.9.
+    // scaling.  32 x 4096 -> 16384: 17.2 us with 32 columns for 17.7 with 64, in fp32 33.1 for
+    // 50.0; 12 x 4096 -> 16384: 16.6 us with 16 columns for 17.0 with 32, groups of 32 34.5 for
+    // 37.3, in fp32 27.2 for 31.7.
     if (dtype == LORA_BF16)
         return p.T <= 16 ? launch<__nv_bfloat16, 16>(p, group, map, st) : p.T <= 32 ? launch<__nv_bfloat16, 32>(p, group, map, st) : launch<__nv_bfloat16, 64>(p, group, map, st);
     return p.T <= 16 ? launch<float, 16>(p, group, map, st) : p.T <= 32 ? launch<float, 32>(p, group, map, st) : launch<float, 64>(p, group, map, st);
