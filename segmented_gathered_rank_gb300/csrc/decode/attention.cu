@@ -26,8 +26,9 @@
 // take them (2^-9 relative each, no more than V's own rounding); maximum, sum and
 // output stay in fp32.  The error of a bf16 output, root mean square, is then 0.0018 to
 // 0.0023 of the outputs' size (long contexts most), of which storing them in bf16 makes
-// 0.00165.  A second bf16 part of each probability would take that away for half as many
-// products again, which are what bounds large trees.  fp32 caches are not rounded anywhere.
+// 0.00165.  A second bf16 part of each probability would take that away, but a part that
+// is zero would make NaN of an infinite value (p v is infinite), and large trees, bound by
+// their products, would have half as many again.  fp32 caches are not rounded anywhere.
 #include <cudaTypedefs.h>
 
 #include <type_traits>

@@ -144,3 +144,23 @@ def test_w4_non_finite_activations_of_many_tokens(T, dtype):
     y = host(y)
     others = np.setdiff1d(np.arange(T), [1, 2, T - 1, T - 2])
     assert np.isfinite(y[others]).all() and np.isnan(y[[1, T - 2]]).all() and np.isposinf(y[2]).all() and np.isneginf(y[T - 1]).all()
+
+
+# ----------------------------------------------------------------------------
+# Infinite values that every row sees come out infinite, and stay in their column
+# ----------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [I.BF16, I.F32])
+@pytest.mark.parametrize("requests, n_q, n_kv, d, page", [
+    ([(1, 300), (1, 70)], 4, 2, 128, 16), ([(2, 300), (3, 70)], 8, 2, 80, 4), ([(20, 500), (16, 90)], 8, 2, 64, 16),
+    ([(20, 500), (16, 90)], 8, 2, 128, 2), ([(60, 700), (40, 90)], 16, 2, 128, 64)])
+def test_attention_infinite_values_of_the_prefix(requests, n_q, n_kv, d, page, dtype):
+    c = C.Attention(600, dtype, requests, n_q, n_kv, d, page, mask="tree", scale=0.02)      # no probability underflows
+    clean = run_attention(c)
+    v = c.v.copy()
+    for s, (at, col, value) in enumerate(((37, 5, np.inf), (3, d - 1, -np.inf))):
+        v[c.table[s, at // page], :, at % page, col] = value
+    got = run_attention(c, v=v)
+    first = requests[0][0]
+    expected = clean.reshape(-1, n_q, d).copy()
+    expected[:first, :, 5], expected[first:, :, d - 1] = np.inf, -np.inf
+    assert np.array_equal(got.reshape(-1, n_q, d), expected)
