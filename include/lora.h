@@ -386,6 +386,25 @@ int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, const void 
                    int n_pos, int rot_dim, int interleaved, const void *q_norm, const void *k_norm, float eps,
                    void *q_out, lora_stream stream);
 
+/*
+ * lora_kv_append for tokens whose positions have several axes (time, height and
+ * width of images and video): pair i of a head turns by the row of cos_sin at
+ * positions[t][pair_axis[i]],
+ *   c_i = cos_sin[positions[t][pair_axis[i]]][i], s_i = .. [rot_dim/2 + i].
+ *   positions  T x n_axes device int32.   n_axes  1..LORA_MAX_AXES.
+ *   pair_axis  HOST array of rot_dim/2 axes below n_axes, read during the call: sections
+ *              of the head, axes taken in turn, or any other order.  A text token has
+ *              the same position on every axis.
+ * Everything else, errors included, as lora_kv_append; an axis that no pair names
+ * is not looked at.
+ */
+enum { LORA_MAX_AXES = 4 };
+int lora_kv_append_axes(const lora_kv_pages *kv, const void *q, int ld_q, const void *k, int ld_k, const void *v,
+                        int ld_v, int T, int n_q_heads, const int *positions, int n_axes,
+                        const unsigned char *pair_axis, const long long *slots, const float *cos_sin, int n_pos,
+                        int rot_dim, int interleaved, const void *q_norm, const void *k_norm, float eps, void *q_out,
+                        lora_stream stream);
+
 /* Bytes of device workspace that lora_tree_attention needs at most for up to T
  * drafted tokens of up to S requests (0 on a bad argument): a workspace of the
  * largest batch serves every smaller one. */

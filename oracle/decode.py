@@ -3,6 +3,7 @@ requests and heads), with the sums of magnitudes that rounding bounds need.
 
   w4_matvec        products with 4-bit weights and group scales
   rotate / append  per-head RMS norm, rotation, append to a paged cache
+  append_axes      the same with positions of several axes
   tree_attention   attention of drafted tokens over a paged cache
 """
 from __future__ import annotations
@@ -61,6 +62,16 @@ def append(q, k, v, positions, slots, cos_sin, rot, interleaved, q_norm, k_norm,
         k_pages[p, :, off] = rotate(rms_norm(k[t], k_norm, eps), c, s, interleaved)
         v_pages[p, :, off] = v[t]
     return q_out, k_pages, v_pages
+
+
+def append_axes(q, k, v, positions, pair_axis, slots, cos_sin, rot, interleaved, q_norm, k_norm, eps, k_pages, v_pages):
+    """append() with positions [T, axes]: pair i of token t turns by the table's row positions[t][pair_axis[i]]."""
+    half = rot // 2
+    rows = np.empty((len(slots), 2 * half))
+    for t in range(len(slots)):
+        for i in range(half):
+            rows[t, i], rows[t, half + i] = (cos_sin[positions[t][pair_axis[i]]][x] for x in (i, half + i))
+    return append(q, k, v, np.arange(len(slots)), slots, rows, rot, interleaved, q_norm, k_norm, eps, k_pages, v_pages)
 
 
 def visible(n, kv_len, mask_rows):

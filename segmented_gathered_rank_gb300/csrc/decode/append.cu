@@ -1,4 +1,4 @@
-// Norm, rotation and append of new tokens (lora_kv_append).
+// Norm, rotation and append of new tokens (lora_kv_append, lora_kv_append_axes).
 //
 // Per query and key head h (d elements, fp32 arithmetic, one rounding on store):
 //   h <- h / sqrt(mean(h^2) + eps) * norm,  then (a, b) <- (a c - b s, a s + b c)
@@ -13,6 +13,8 @@
 // when rot is no multiple of 8, in a row of shared memory).  A block takes heads of one
 // token, several a thread for long batches; its lanes keep their pairs' cosines and
 // sines for all of them.
+#include <string.h>
+
 #include "decode.cuh"
 
 namespace lora {
@@ -53,6 +55,8 @@ struct AppendParams {
     void *q_out, *k_pages, *v_pages;
     long long n_slots;
     int *status;
+    int n_axes;                              // positions a token
+    unsigned char axes[kMaxHeadDim / 8];     // axis of each pair, two bits each, four pairs a byte
 };
 
 // The lanes of this thread's head within its warp.
@@ -124,7 +128,34 @@ __device__ __forceinline__ void store_quads(const Quads<E> &h, E *head, int o0, 
 // HEADS: heads a thread.
 enum { kNear, kFar, kAnyNear, kAnyFar };
 
-template <typename E, int LANES, int PAIRS, int HEADS>
+// The table's row for an axis of token t, its position clamped into the table (flagged).
+__device__ __forceinline__ const float *axis_row(const AppendParams &p, long long t, int axis) {
+    int pos = __ldg(p.positions + t * p.n_axes + axis);
+    if (pos < 0 || pos >= p.n_pos) {
+        flag_status(p.status, LORA_DEV_BAD_POSITION);
+        pos = pos < 0 ? 0 : p.n_pos - 1;
+    }
+    return p.cos_sin + (long long)pos * p.rot;
+}
+// Cosines and sines of the pairs 4 * quad .. + 3.  Sections of a head have whole quads of one axis: two vector loads.
+__device__ __forceinline__ void load_axes(const AppendParams &p, long long t, int quad, int half, float *c, float *s) {
+    const uint32_t axes = p.axes[quad], first = axes & 3;
+    if (axes == first * 0x55u) {
+        const float *row = axis_row(p, t, first) + quad * 4;
+        *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(row);
+        *reinterpret_cast<float4 *>(s) = *reinterpret_cast<const float4 *>(row + half);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float *row = axis_row(p, t, (axes >> (2 * e)) & 3) + quad * 4 + e;
+        c[e] = row[0];
+        s[e] = row[half];
+    }
+}
+
+// AXES: a token has n_axes positions, and each pair turns by that of its axis.
+template <typename E, int LANES, int PAIRS, int HEADS, bool AXES>
 __global__ void __launch_bounds__(kThreads, 5) append_kernel(const AppendParams p) {
     constexpr int kGroups = kThreads / LANES;
     constexpr int kTable = PAIRS == kAnyFar ? 8 : 4;
@@ -150,7 +181,21 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const AppendParams 
     }
     const long long slot = p.slots[t];
     float c[kTable], s[kTable];
-    if (half) {
+    if (AXES && half) {
+        if (PAIRS == kNear || PAIRS == kFar) {
+            if (turns) load_axes(p, t, lane, half, c, s);
+        } else {
+#pragma unroll
+            for (int e = 0; e < kTable; ++e) {
+                const int x = PAIRS == kAnyFar ? at + e : at + 2 * e, i = PAIRS == kAnyNear ? x >> 1 : x < half ? x : x - half;
+                if (x < p.rot) {
+                    const float *row = axis_row(p, t, (p.axes[i >> 2] >> (2 * (i & 3))) & 3);
+                    c[e] = row[i];
+                    s[e] = row[half + i];
+                }
+            }
+        }
+    } else if (half) {
         int pos = p.positions[t];
         if (pos < 0 || pos >= p.n_pos) {
             if (threadIdx.x == 0) flag_status(p.status, LORA_DEV_BAD_POSITION);
@@ -249,48 +294,44 @@ __global__ void __launch_bounds__(kThreads, 5) append_kernel(const AppendParams 
     }
 }
 
-template <typename E, int LANES, int PAIRS>
+template <typename E, int LANES, int PAIRS, bool AXES>
 void launch(const AppendParams &p, int T, cudaStream_t st) {
     constexpr int kGroups = kThreads / LANES;
     const int heads = p.n_q + 2 * p.n_kv;
     const dim3 one(T, (heads + kGroups - 1) / kGroups), more(T, (heads + kGroups * kHeads - 1) / (kGroups * kHeads));
     if constexpr (PAIRS == kNear) {
         if (one.y > 1 && (long long)one.x * one.y > kManyBlocks<E>) {
-            append_kernel<E, LANES, PAIRS, kHeads><<<more, kThreads, 0, st>>>(p);
+            append_kernel<E, LANES, PAIRS, kHeads, AXES><<<more, kThreads, 0, st>>>(p);
             return;
         }
     }
-    append_kernel<E, LANES, PAIRS, 1><<<one, kThreads, 0, st>>>(p);
+    append_kernel<E, LANES, PAIRS, 1, AXES><<<one, kThreads, 0, st>>>(p);
 }
 
-template <typename E, int LANES>
+template <typename E, int LANES, bool AXES>
 void launch(const AppendParams &p, int T, bool interleaved, cudaStream_t st) {
     const bool table = aligned16(p.cos_sin);
     if (interleaved) {
-        if (table && p.rot % 8 == 0) launch<E, LANES, kNear>(p, T, st);
-        else launch<E, LANES, kAnyNear>(p, T, st);
+        if (table && p.rot % 8 == 0) launch<E, LANES, kNear, AXES>(p, T, st);
+        else launch<E, LANES, kAnyNear, AXES>(p, T, st);
     } else {
-        if (table && p.rot % 8 == 0) launch<E, LANES, kFar>(p, T, st);
-        else launch<E, LANES, kAnyFar>(p, T, st);
+        if (table && p.rot % 8 == 0) launch<E, LANES, kFar, AXES>(p, T, st);
+        else launch<E, LANES, kAnyFar, AXES>(p, T, st);
     }
 }
 
-template <typename E>
+template <typename E, bool AXES>
 void launch(const AppendParams &p, int T, bool interleaved, cudaStream_t st) {
-    if (p.d <= 64) launch<E, 8>(p, T, interleaved, st);
-    else if (p.d <= 128) launch<E, 16>(p, T, interleaved, st);
-    else launch<E, 32>(p, T, interleaved, st);
+    if (p.d <= 64) launch<E, 8, AXES>(p, T, interleaved, st);
+    else if (p.d <= 128) launch<E, 16, AXES>(p, T, interleaved, st);
+    else launch<E, 32, AXES>(p, T, interleaved, st);
 }
 
-}  // namespace
-}  // namespace lora
-
-using namespace lora;
-
-extern "C" int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, const void *k, int ld_k, const void *v,
-                              int ld_v, int T, int n_q_heads, const int *positions, const long long *slots,
-                              const float *cos_sin, int n_pos, int rot_dim, int interleaved, const void *q_norm,
-                              const void *k_norm, float eps, void *q_out, lora_stream stream) {
+// pair_axis: on the host, NULL for one position a token.
+int append(const lora_kv_pages *kv, const void *q, int ld_q, const void *k, int ld_k, const void *v, int ld_v, int T,
+           int n_q_heads, const int *positions, int n_axes, const unsigned char *pair_axis, const long long *slots,
+           const float *cos_sin, int n_pos, int rot_dim, int interleaved, const void *q_norm, const void *k_norm, float eps,
+           void *q_out, cudaStream_t st) {
     int rc = decode::check_kv(kv, n_q_heads);
     if (rc) return rc;
     if (T < 0 || rot_dim < 0 || !(eps >= 0.f)) return LORA_ERR_ARG;
@@ -299,6 +340,15 @@ extern "C" int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, 
     if ((long long)n_q_heads + 2LL * kv->n_kv_heads > 65535) return LORA_ERR_SHAPE;
     if (ld_k < kv->n_kv_heads * d || ld_v < kv->n_kv_heads * d || ld_k % vec || ld_v % vec) return LORA_ERR_SHAPE;
     if (n_q_heads && (ld_q < n_q_heads * d || ld_q % vec)) return LORA_ERR_SHAPE;
+    AppendParams p;
+    p.n_axes = n_axes;
+    if (pair_axis) {
+        memset(p.axes, 0, sizeof(p.axes));
+        for (int i = 0; i < rot_dim / 2; ++i) {
+            if (pair_axis[i] >= n_axes) return LORA_ERR_ARG;
+            p.axes[i >> 2] |= (unsigned char)(pair_axis[i] << (2 * (i & 3)));
+        }
+    }
     if (T == 0) return LORA_OK;
     if (!k || !v || !slots || !aligned16(k) || !aligned16(v) || ((uintptr_t)slots & 7u)) return LORA_ERR_ARG;
     if (n_q_heads && (!q || !q_out || !aligned16(q) || !aligned16(q_out))) return LORA_ERR_ARG;
@@ -306,7 +356,6 @@ extern "C" int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, 
     if (rot_dim && (!cos_sin || !positions || n_pos < 1 || ((uintptr_t)cos_sin & 3u) || ((uintptr_t)positions & 3u)))
         return LORA_ERR_ARG;
     if (!aligned16(q_norm) || !aligned16(k_norm)) return LORA_ERR_ARG;
-    AppendParams p;
     p.q = q;
     p.k = k;
     p.v = v;
@@ -331,8 +380,37 @@ extern "C" int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, 
     p.v_pages = kv->v;
     p.n_slots = (long long)kv->n_pages * kv->page_size;
     p.status = kv->status;
-    if (kv->dtype == LORA_BF16) launch<__nv_bfloat16>(p, T, interleaved != 0, (cudaStream_t)stream);
-    else launch<float>(p, T, interleaved != 0, (cudaStream_t)stream);
+    const bool near = interleaved != 0;
+    if (pair_axis) {
+        if (kv->dtype == LORA_BF16) launch<__nv_bfloat16, true>(p, T, near, st);
+        else launch<float, true>(p, T, near, st);
+    } else {
+        if (kv->dtype == LORA_BF16) launch<__nv_bfloat16, false>(p, T, near, st);
+        else launch<float, false>(p, T, near, st);
+    }
     count_launch();
     return cuda_status(cudaGetLastError());
+}
+
+}  // namespace
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, const void *k, int ld_k, const void *v,
+                              int ld_v, int T, int n_q_heads, const int *positions, const long long *slots,
+                              const float *cos_sin, int n_pos, int rot_dim, int interleaved, const void *q_norm,
+                              const void *k_norm, float eps, void *q_out, lora_stream stream) {
+    return append(kv, q, ld_q, k, ld_k, v, ld_v, T, n_q_heads, positions, 1, nullptr, slots, cos_sin, n_pos, rot_dim, interleaved,
+                  q_norm, k_norm, eps, q_out, (cudaStream_t)stream);
+}
+
+extern "C" int lora_kv_append_axes(const lora_kv_pages *kv, const void *q, int ld_q, const void *k, int ld_k, const void *v,
+                                   int ld_v, int T, int n_q_heads, const int *positions, int n_axes,
+                                   const unsigned char *pair_axis, const long long *slots, const float *cos_sin, int n_pos,
+                                   int rot_dim, int interleaved, const void *q_norm, const void *k_norm, float eps, void *q_out,
+                                   lora_stream stream) {
+    if (n_axes < 1 || n_axes > LORA_MAX_AXES || !pair_axis) return LORA_ERR_ARG;
+    return append(kv, q, ld_q, k, ld_k, v, ld_v, T, n_q_heads, positions, n_axes, pair_axis, slots, cos_sin, n_pos, rot_dim,
+                  interleaved, q_norm, k_norm, eps, q_out, (cudaStream_t)stream);
 }

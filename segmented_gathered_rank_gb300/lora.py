@@ -37,6 +37,7 @@ LORA_DEV_BAD_LENGTH = 32
 LORA_DEV_BAD_PAGE = 64
 
 LORA_NOALLOC_SCRATCH_BYTES = 16 << 20
+LORA_MAX_AXES = 4
 
 LORA_TIER_GPU = 0
 LORA_TIER_HOST = 1
@@ -49,7 +50,7 @@ EXPORTS = ["lora_pool_create", "lora_pool_destroy", "lora_pool_load", "lora_pool
            "lora_tier_cache_touch", "lora_tier_cache_resident", "lora_tier_sim", "lora_pool_load_async",
            "lora_pool_unload_async", "lora_pool_prefetch", "lora_quantize_e4m3",
            "lora_layer_forward_fp8_workspace_size", "lora_layer_forward_fp8", "lora_w4_matvec", "lora_kv_append",
-           "lora_tree_attention_workspace_size", "lora_tree_attention"]
+           "lora_tree_attention_workspace_size", "lora_tree_attention", "lora_kv_append_axes"]
 
 if not os.path.exists(_build.LIB):
     raise ImportError(f"CUDA library {_build.LIB} is not built: run segmented_gathered_rank_gb300.build.build()")
@@ -122,6 +123,8 @@ class KvPages(ctypes.Structure):
 
 _sig("lora_w4_matvec", _I, _I, _P, _I, _I, _P, _P, _P, _I, _I, _P, _P)
 _sig("lora_kv_append", _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P,
+     ctypes.c_float, _P, _P)
+_sig("lora_kv_append_axes", _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, ctypes.c_char_p, _P, _P, _I, _I, _I, _P, _P,
      ctypes.c_float, _P, _P)
 _sig("lora_tree_attention_workspace_size", ctypes.c_size_t, _P, _I, _I, _I)
 _sig("lora_tree_attention", _I, _P, _P, _I, _P, _I, _I, _P, _P, _I, _P, _I, ctypes.c_float, _P, _P,
@@ -382,6 +385,22 @@ def lora_kv_append(kv, q, k, v, T, n_q_heads, positions, slots, cos_sin, n_pos, 
                              _ptr(q_out), _stream_ptr(stream))
     if rc:
         _check(rc, "lora_kv_append")
+
+
+def lora_kv_append_axes(kv, q, k, v, T, n_q_heads, positions, n_axes, pair_axis, slots, cos_sin, n_pos, rot_dim, interleaved,
+                        q_out, q_norm=None, k_norm=None, eps=1e-6, stream=None) -> None:
+    """lora_kv_append with n_axes positions a token (int32 [T, n_axes]); pair_axis: the axis of each rotated pair, as
+    bytes (quickest) or a sequence of whole numbers."""
+    (pq, ld_q), (pk, ld_k), (pv, ld_v) = _rows(q), _rows(k), _rows(v)
+    if pair_axis is not None:
+        pair_axis = pair_axis if type(pair_axis) is bytes else bytes(list(pair_axis))
+        if len(pair_axis) < rot_dim // 2:
+            raise ValueError("pair_axis names fewer pairs than rot_dim has")
+    rc = _lib.lora_kv_append_axes(kv.address, pq, ld_q, pk, ld_k, pv, ld_v, T, n_q_heads, _ptr(positions), n_axes, pair_axis,
+                                  _ptr(slots), _ptr(cos_sin), n_pos, rot_dim, 1 if interleaved else 0, _ptr(q_norm),
+                                  _ptr(k_norm), eps, _ptr(q_out), _stream_ptr(stream))
+    if rc:
+        _check(rc, "lora_kv_append_axes")
 
 
 def lora_tree_attention_workspace_size(kv, n_q_heads, S, T) -> int:

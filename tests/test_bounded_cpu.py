@@ -1,0 +1,67 @@
+"""Host-side checks of the calls of a bounded cache: refused before any launch, without a GPU (the pointers are host
+memory that nothing reads)."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from segmented_gathered_rank_gb300 import lora as L
+from tests.test_decode_binding_cpu import Cuda
+from tests.test_decode_cpu import BAD_PAGES, P, pages
+
+AXES = bytes(i % 3 for i in range(64))
+
+
+def axes(kv, q=P, ld_q=512, k=P, ld_k=256, v=P, ld_v=256, T=3, n_q=4, positions=P, n_axes=3, pair_axis=AXES, slots=P, cos_sin=P,
+         n_pos=16, rot=128, interleaved=False, q_norm=None, k_norm=None, eps=1e-6, q_out=P):
+    return L._lib.lora_kv_append_axes(ctypes.byref(kv), q, ld_q, k, ld_k, v, ld_v, T, n_q, positions, n_axes, pair_axis, slots, cos_sin,
+                                      n_pos, rot, int(interleaved), q_norm, k_norm, eps, q_out, None)
+
+
+@pytest.mark.parametrize("change, code", BAD_PAGES)
+def test_append_axes_refuses_pages(change, code):
+    assert axes(pages(**change)) == code
+
+
+@pytest.mark.parametrize("change, code", [
+    (dict(n_axes=0), L.LORA_ERR_ARG), (dict(n_axes=L.LORA_MAX_AXES + 1), L.LORA_ERR_ARG), (dict(pair_axis=None), L.LORA_ERR_ARG),
+    (dict(n_axes=2), L.LORA_ERR_ARG), (dict(pair_axis=bytes(63) + bytes([3])), L.LORA_ERR_ARG),        # an axis beyond n_axes
+    (dict(T=0, n_axes=2), L.LORA_ERR_ARG),
+    (dict(T=-1), L.LORA_ERR_ARG), (dict(rot=-2), L.LORA_ERR_ARG), (dict(eps=-1.0), L.LORA_ERR_ARG),
+    (dict(eps=float("nan")), L.LORA_ERR_ARG), (dict(rot=130), L.LORA_ERR_SHAPE), (dict(rot=7), L.LORA_ERR_SHAPE),
+    (dict(n_q=3), L.LORA_ERR_SHAPE), (dict(ld_k=255), L.LORA_ERR_SHAPE), (dict(ld_v=260), L.LORA_ERR_SHAPE),
+    (dict(ld_q=504), L.LORA_ERR_SHAPE), (dict(slots=P + 4), L.LORA_ERR_ARG), (dict(slots=None), L.LORA_ERR_ARG),
+    (dict(q_out=None), L.LORA_ERR_ARG), (dict(positions=None), L.LORA_ERR_ARG), (dict(positions=P + 2), L.LORA_ERR_ARG),
+    (dict(n_pos=0), L.LORA_ERR_ARG), (dict(cos_sin=None), L.LORA_ERR_ARG), (dict(k_norm=P + 4), L.LORA_ERR_ARG),
+    (dict(ld_q=1024), L.LORA_ERR_ARG)])       # in place, rows apart
+def test_append_axes_refuses(change, code):
+    before = L.lora_launch_count()
+    assert axes(pages(), **change) == code
+    assert L.lora_launch_count() == before
+
+
+def test_append_axes_without_tokens():
+    before = L.lora_launch_count()
+    assert axes(pages(), T=0, q=None, k=None, v=None, q_out=None, positions=None, slots=None) == L.LORA_OK
+    assert L.lora_launch_count() == before
+
+
+def test_pair_axis_from_python(monkeypatch):
+    """Whole numbers of any type; what is too short or not a byte is refused."""
+    got = []
+    monkeypatch.setattr(L, "_check", lambda rc, where: got.append(rc))
+    kv = L.KvPages(L.LORA_BF16, Cuda(4, 2, 8, 16), Cuda(4, 2, 8, 16), 4, 8, 2, 16)
+
+    def call(pair_axis, n_axes=3, n_pos=0):
+        got.clear()
+        L.lora_kv_append_axes(kv, Cuda(3, 64), Cuda(3, 32), Cuda(3, 32), 3, 4, Cuda(3, n_axes), n_axes, pair_axis, Cuda(3), Cuda(1, 16), n_pos,
+                              16, False, Cuda(3, 64), stream=0)
+        return got[0] if got else 0
+
+    # n_pos 0 is refused after pair_axis has passed; with n_axes 2 the axis 2 is refused before
+    for a in (bytes([0, 1, 2, 0, 1, 2, 0, 1]), [0, 1, 2, 0, 1, 2, 0, 1], np.array([0, 1, 2, 0, 1, 2, 0, 1])):
+        assert call(a) == L.LORA_ERR_ARG and call(a, n_axes=2) == L.LORA_ERR_ARG
+    with pytest.raises(ValueError):
+        call([0, 1, 2])
+    with pytest.raises(ValueError):
+        call([0, 1, 2, 0, 1, 2, 0, 256])
