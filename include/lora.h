@@ -86,8 +86,9 @@ enum {
     /* decode-step operators (lora_kv_pages.status): */
     LORA_DEV_BAD_SLOT = 8,       /* an append slot beyond the cache (the token is not stored) */
     LORA_DEV_BAD_POSITION = 16,  /* a rotation position outside the table (clamped) */
-    LORA_DEV_BAD_LENGTH = 32,    /* a cached length below the drafted count or beyond the page table (clamped) */
-    LORA_DEV_BAD_PAGE = 64       /* a page id outside the cache (clamped) */
+    LORA_DEV_BAD_LENGTH = 32,    /* a cached length below the drafted count or beyond the page table (clamped;
+                                    eviction: a length or budget beyond its table, the request stays) */
+    LORA_DEV_BAD_PAGE = 64       /* a page id outside the cache (clamped; eviction: the request stays) */
 };
 
 /*
@@ -441,6 +442,35 @@ size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, int n_q_heads
 int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, const int *seg_starts, int S, int T,
                         const int *kv_lens, const int *page_table, int max_pages, const long long *tree_mask,
                         int mask_words, float scale, void *out, void *workspace, size_t ws_bytes, lora_stream stream);
+
+/*
+ * Eviction from the paged cache.  Request s has kv_lens[s] cached tokens, in the
+ * pages of its row of page_table.  If that is more than keep[s], then every kv
+ * head h on its own keeps keep[s] of them: the last `recent`, the `first` first
+ * (less where keep[s] does not hold both: the recent ones go before), and of the
+ * others those with the greatest scores, of equal ones the lower index.  The kept
+ * tokens' keys, values and weights move, in their order, to cached places 0 ..
+ * keep[s] - 1, and new_lens[s] = keep[s]; places from there on are left as they
+ * are.  Other requests (and those with keep[s] < 0) stay as they are, and
+ * new_lens[s] = kv_lens[s].
+ *   scores    n_pages x n_kv_heads x page_size fp32, slots as the cache's; -0 equals
+ *             0, a NaN is below everything.
+ *   weights   the same layout, moved with the tokens; may be scores (else they do not
+ *             overlap), or NULL.
+ *   keep      S device int32.
+ *   kept      S x n_kv_heads x ld_kept device int32: for a request that loses tokens
+ *             entry j < keep[s] of a row gets the index that the token at place j had; the
+ *             rest is not written.  ld_kept is at least every budget that is used.
+ *   new_lens  S device int32, apart from kv_lens and keep.
+ * The pages of a request that loses tokens are its own, each named once: a page shared
+ * with another request, or named twice, ends up with either's tokens.
+ * Errors: LORA_ERR_ARG, LORA_ERR_SHAPE.
+ * Device-detected: LORA_DEV_BAD_LENGTH (a length beyond the table or below 0, a budget
+ * beyond ld_kept), LORA_DEV_BAD_PAGE; the request concerned stays as it is.
+ */
+int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float *weights, int S, const int *kv_lens,
+                  const int *page_table, int max_pages, const int *keep, int first, int recent, int *kept, int ld_kept,
+                  int *new_lens, lora_stream stream);
 
 /*
  * Synchronise the device, read the pool's device status word into

@@ -4,6 +4,7 @@ requests and heads), with the sums of magnitudes that rounding bounds need.
   w4_matvec        products with 4-bit weights and group scales
   rotate / append  per-head RMS norm, rotation, append to a paged cache
   append_axes      the same with positions of several axes
+  evict            eviction from a paged cache by scores
   tree_attention   attention of drafted tokens over a paged cache
 """
 from __future__ import annotations
@@ -111,3 +112,33 @@ def tree_attention(q, k_pages, v_pages, starts, lens, table, masks, scale):
                     mag[b + i, hq] = p @ np.abs(v[on])
                     big[b + i, hq] = (scale * (np.abs(k[on]) @ np.abs(q[b + i, hq]))).max()
     return out, mag, big
+
+
+def evict(planes, scores, lens, table, keep, first, recent):
+    """planes: arrays [n_pages, n_kv, page, ..] that move with the tokens; scores [n_pages, n_kv, page].  Returns (planes
+    moved, per request None or the kept indices [n_kv, keep[s]], new lengths)."""
+    planes = [np.array(p) for p in planes]
+    n_kv, page = scores.shape[1], scores.shape[2]
+    kept, new_lens = [None] * len(lens), np.array(lens)
+    for s, length in enumerate(np.asarray(lens).tolist()):
+        budget = int(keep[s])
+        if budget < 0 or length <= budget:
+            continue
+        last = min(recent, budget)
+        begin = min(first, budget - last)
+        slot = [(int(table[s][c // page]), c % page) for c in range(length)]
+        rows = []
+        for h in range(n_kv):
+            def value(c):
+                f = float(scores[slot[c][0], h, slot[c][1]])
+                return (f == f, f if f == f else 0.0)      # a NaN is below everything
+            middle = sorted(range(begin, length - last), key=lambda c: (*(-x for x in value(c)), c))
+            chosen = sorted([*range(begin), *middle[: budget - begin - last], *range(length - last, length)])
+            for p in planes:
+                old = [np.array(p[slot[c][0], h, slot[c][1]]) for c in chosen]
+                for j, o in enumerate(old):
+                    p[slot[j][0], h, slot[j][1]] = o
+            rows.append(chosen)
+        kept[s] = np.array(rows, np.int64).reshape(n_kv, budget)
+        new_lens[s] = budget
+    return planes, kept, new_lens

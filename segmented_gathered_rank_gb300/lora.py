@@ -50,7 +50,8 @@ EXPORTS = ["lora_pool_create", "lora_pool_destroy", "lora_pool_load", "lora_pool
            "lora_tier_cache_touch", "lora_tier_cache_resident", "lora_tier_sim", "lora_pool_load_async",
            "lora_pool_unload_async", "lora_pool_prefetch", "lora_quantize_e4m3",
            "lora_layer_forward_fp8_workspace_size", "lora_layer_forward_fp8", "lora_w4_matvec", "lora_kv_append",
-           "lora_tree_attention_workspace_size", "lora_tree_attention", "lora_kv_append_axes"]
+           "lora_tree_attention_workspace_size", "lora_tree_attention", "lora_kv_append_axes",
+           "lora_kv_evict"]
 
 if not os.path.exists(_build.LIB):
     raise ImportError(f"CUDA library {_build.LIB} is not built: run segmented_gathered_rank_gb300.build.build()")
@@ -118,6 +119,7 @@ class KvPages(ctypes.Structure):
         super().__init__(dtype, n_pages, page_size, n_kv_heads, head_dim, _dptr(k_pages), _dptr(v_pages),
                          _dptr(status))
         self.tensors = (k_pages, v_pages, status)
+        self.slots = n_pages * n_kv_heads * page_size       # keys, values, weights
         self.address = ctypes.addressof(self)      # what calls pass: no reference, so no cycle, and quick
 
 
@@ -126,6 +128,7 @@ _sig("lora_kv_append", _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _
      ctypes.c_float, _P, _P)
 _sig("lora_kv_append_axes", _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, ctypes.c_char_p, _P, _P, _I, _I, _I, _P, _P,
      ctypes.c_float, _P, _P)
+_sig("lora_kv_evict", _I, _P, _P, _P, _I, _P, _P, _I, _P, _I, _I, _P, _I, _P, _P)
 _sig("lora_tree_attention_workspace_size", ctypes.c_size_t, _P, _I, _I, _I)
 _sig("lora_tree_attention", _I, _P, _P, _I, _P, _I, _I, _P, _P, _I, _P, _I, ctypes.c_float, _P, _P,
      ctypes.c_size_t, _P)
@@ -417,3 +420,20 @@ def lora_tree_attention(kv, q, n_q_heads, seg_starts, S, T, kv_lens, page_table,
                                   _stream_ptr(stream))
     if rc:
         _check(rc, "lora_tree_attention")
+
+
+def _plane(kv, t):
+    """Pointer of one fp32 number a slot and kv head of the cache."""
+    if t is not None and t.numel() < kv.slots:
+        raise ValueError("expected n_pages x n_kv_heads x page_size numbers")
+    return _ptr(t)
+
+
+def lora_kv_evict(kv, scores, weights, S, kv_lens, page_table, max_pages, keep, first, recent, kept, ld_kept, new_lens,
+                  stream=None) -> None:
+    """Every kv head keeps its keep[s] tokens of the greatest scores (float [n_pages, n_kv_heads, page_size]), in order;
+    weights (None, scores itself or another such tensor) move along; kept gets the indices, new_lens the lengths."""
+    rc = _lib.lora_kv_evict(kv.address, _plane(kv, scores), _plane(kv, weights), S, _ptr(kv_lens), _ptr(page_table), max_pages,
+                            _ptr(keep), first, recent, _ptr(kept), ld_kept, _ptr(new_lens), _stream_ptr(stream))
+    if rc:
+        _check(rc, "lora_kv_evict")

@@ -65,3 +65,41 @@ def test_pair_axis_from_python(monkeypatch):
         call([0, 1, 2])
     with pytest.raises(ValueError):
         call([0, 1, 2, 0, 1, 2, 0, 256])
+
+
+def evict(kv, scores=P, weights=P, S=2, lens=P + 64, table=P, max_pages=4, keep=P + 128, first=1, recent=2, kept=P, ld=8, new_lens=P + 256):
+    return L._lib.lora_kv_evict(ctypes.byref(kv), scores, weights, S, lens, table, max_pages, keep, first, recent, kept, ld, new_lens, None)
+
+
+@pytest.mark.parametrize("change, code", BAD_PAGES)
+def test_evict_refuses_pages(change, code):
+    assert evict(pages(**change)) == code
+
+
+@pytest.mark.parametrize("change, code", [
+    (dict(S=-1), L.LORA_ERR_ARG), (dict(max_pages=-1), L.LORA_ERR_ARG), (dict(max_pages=0), L.LORA_ERR_ARG), (dict(first=-1), L.LORA_ERR_ARG),
+    (dict(recent=-1), L.LORA_ERR_ARG), (dict(ld=-1), L.LORA_ERR_ARG), (dict(scores=None), L.LORA_ERR_ARG), (dict(lens=None), L.LORA_ERR_ARG),
+    (dict(table=None), L.LORA_ERR_ARG), (dict(keep=None), L.LORA_ERR_ARG), (dict(kept=None), L.LORA_ERR_ARG), (dict(new_lens=None), L.LORA_ERR_ARG),
+    (dict(scores=P + 2), L.LORA_ERR_ARG), (dict(weights=P + 1), L.LORA_ERR_ARG), (dict(kept=P + 3), L.LORA_ERR_ARG),
+    (dict(weights=P + 4), L.LORA_ERR_ARG), (dict(scores=P + 64 * 16 * 2 * 4 - 4), L.LORA_ERR_ARG),       # half over each other
+    (dict(new_lens=P + 64), L.LORA_ERR_ARG), (dict(new_lens=P + 132), L.LORA_ERR_ARG), (dict(new_lens=P + 124), L.LORA_ERR_ARG),
+    (dict(max_pages=1 << 27), L.LORA_ERR_SHAPE), (dict(S=1 << 28), L.LORA_ERR_SHAPE)])
+def test_evict_refuses(change, code):
+    before = L.lora_launch_count()
+    assert evict(pages(), **change) == code
+    assert L.lora_launch_count() == before
+
+
+def test_evict_without_requests():
+    before = L.lora_launch_count()
+    assert evict(pages(), S=0, scores=None, lens=None, table=None, keep=None, kept=None, new_lens=None) == L.LORA_OK
+    assert L.lora_launch_count() == before
+
+
+def test_planes_that_are_too_small_are_refused_in_python():
+    kv = L.KvPages(L.LORA_BF16, Cuda(4, 2, 8, 16), Cuda(4, 2, 8, 16), 4, 8, 2, 16)
+    args = (2, Cuda(2), Cuda(2, 4), 4, Cuda(2), 0, 0, Cuda(2, 2, 8), 8, Cuda(2))
+    with pytest.raises(ValueError):
+        L.lora_kv_evict(kv, Cuda(4, 2, 7), None, *args, stream=0)
+    with pytest.raises(ValueError):
+        L.lora_kv_evict(kv, Cuda(4, 2, 8), Cuda(63), *args, stream=0)
