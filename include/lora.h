@@ -444,6 +444,29 @@ int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, c
                         int mask_words, float scale, void *out, void *workspace, size_t ws_bytes, lora_stream stream);
 
 /*
+ * lora_tree_attention that also sums up the weight that each cached token gets: for
+ * every request with drafted tokens, kv head and cached token c,
+ *   weights <- decay * weights + sum p_c  for c in the prefix (c < kv_lens[s] - n_s),
+ *   weights <-                   sum p_c  for a drafted token, whose slot may hold anything before,
+ * the sums over the request's drafted tokens that see c and the query heads of the
+ * kv head, p as normalised there.  With decay 0 no weight is read.  Weights of requests
+ * without drafted tokens, and of slots past a request, are left as they were.  out is
+ * lora_tree_attention's, bit for bit.
+ *   weights  n_pages x n_kv_heads x page_size fp32, slots as the cache's, 16-byte
+ *            aligned.   decay  0..1.
+ *   workspace  lora_tree_attention_weights_workspace_size() bytes; it grows with S, T
+ *            and max_pages, and one of the largest call serves every smaller one.
+ * A page that several requests of the call share ends up with either's weights.  A
+ * page outside the cache has none.  Errors, device-detected ones and bad tables as
+ * lora_tree_attention (where nothing is computed, weights stay as well).
+ */
+size_t lora_tree_attention_weights_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T, int max_pages);
+int lora_tree_attention_weights(const lora_kv_pages *kv, float *weights, float decay, const void *q, int n_q_heads,
+                                const int *seg_starts, int S, int T, const int *kv_lens, const int *page_table,
+                                int max_pages, const long long *tree_mask, int mask_words, float scale, void *out,
+                                void *workspace, size_t ws_bytes, lora_stream stream);
+
+/*
  * Eviction from the paged cache.  Request s has kv_lens[s] cached tokens, in the
  * pages of its row of page_table.  If that is more than keep[s], then every kv
  * head h on its own keeps keep[s] of them: the last `recent`, the `first` first

@@ -4,6 +4,7 @@ requests and heads), with the sums of magnitudes that rounding bounds need.
   w4_matvec        products with 4-bit weights and group scales
   rotate / append  per-head RMS norm, rotation, append to a paged cache
   append_axes      the same with positions of several axes
+  attention_weights  the weights that cached tokens get from it
   evict            eviction from a paged cache by scores
   tree_attention   attention of drafted tokens over a paged cache
 """
@@ -112,6 +113,39 @@ def tree_attention(q, k_pages, v_pages, starts, lens, table, masks, scale):
                     mag[b + i, hq] = p @ np.abs(v[on])
                     big[b + i, hq] = (scale * (np.abs(k[on]) @ np.abs(q[b + i, hq]))).max()
     return out, mag, big
+
+
+def attention_weights(q, k_pages, starts, lens, table, masks, scale, weights, decay):
+    """weights [n_pages, n_kv, page] after the attention of q [T, n_q, d]; also, of the same shape, the sum of what was
+    added and that sum with each term times its row's largest scale * sum |q k|."""
+    q = np.asarray(q, np.float64)
+    n_q, n_kv, page = q.shape[1], k_pages.shape[1], k_pages.shape[2]
+    new, gain, loaded = np.array(weights, np.float64), np.zeros(weights.shape), np.zeros(weights.shape)
+    for s in range(len(lens)):
+        b, e, length = int(starts[s]), int(starts[s + 1]), int(lens[s])
+        n = e - b
+        if n == 0:
+            continue
+        ids = np.asarray(table[s][: -(-length // page)])
+        see = visible(n, length, None if masks is None else masks[s])
+        for h in range(n_kv):
+            k = np.asarray(k_pages[ids, h], np.float64).reshape(len(ids) * page, -1)[:length]
+            total, load = np.zeros(length), np.zeros(length)
+            for hq in range(h * (n_q // n_kv), (h + 1) * (n_q // n_kv)):
+                for i in range(n):
+                    on = np.flatnonzero(see[i])
+                    if not len(on):
+                        continue
+                    sc = scale * (k[on] @ q[b + i, hq])
+                    p = np.exp(sc - sc.max())
+                    p /= p.sum()
+                    total[on] += p
+                    load[on] += p * (scale * (np.abs(k[on]) @ np.abs(q[b + i, hq]))).max()
+            for c in range(length):
+                at = (ids[c // page], h, c % page)
+                new[at] = total[c] + (decay * new[at] if c < length - n and decay else 0.0)
+                gain[at], loaded[at] = total[c], load[c]
+    return new, gain, loaded
 
 
 def evict(planes, scores, lens, table, keep, first, recent):

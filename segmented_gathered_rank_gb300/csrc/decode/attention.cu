@@ -346,6 +346,7 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
                     w2.y = pack_bf16(acc.z * r, acc.w * r);
                     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
                                                row_offset(p, cur, cur.row_tile * kRows + row) + col) = w2;
+                    if (p.lse && col == 0) p.lse[row_index(p, cur, cur.row_tile * kRows + row)] = log_sum(top, sum);
                 } else {
                     *reinterpret_cast<float4 *>(dst + partial_at(p, row, col)) = acc;
                     if (col == 0) {
@@ -603,6 +604,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                     dst[p.rt * p.d + ur * 2] = m[a];
                     dst[p.rt * p.d + ur * 2 + 1] = l[a];
                 }
+                if (p.lse && whole && lane == 0) p.lse[row_index(p, cur, cur.row_tile * p.rt + ur)] = log_sum(m[a], l[a]);
             }
             fresh = true;
         }
@@ -787,6 +789,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few
                 const float r = sum == 0.f ? 0.f : 1.f / sum;
                 *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row_offset(p, cur, cur.row_tile * p.rt + row) + c * 4) =
                     make_float4(u.x * r, u.y * r, u.z * r, u.w * r);
+                if (p.lse && c == 0) p.lse[row_index(p, cur, cur.row_tile * p.rt + row)] = log_sum(top, sum);
             } else {
                 *reinterpret_cast<float4 *>(dst + partial_at(p, row, c * 4)) = u;
                 if (c == 0) *reinterpret_cast<float2 *>(dst + p.rt * p.d + row * 2) = make_float2(top, sum);
@@ -831,7 +834,9 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         }
         const float r = l == 0.f ? 0.f : 1.f / l;
         const int unit_row = rec.first_row + row, i = unit_row / p.group;
-        E *out = static_cast<E *>(p.out) + ((long long)(rec.begin + i) * p.n_q + rec.head * p.group + unit_row - i * p.group) * p.d + col;
+        const long long at = (long long)(rec.begin + i) * p.n_q + rec.head * p.group + unit_row - i * p.group;
+        E *out = static_cast<E *>(p.out) + at * p.d + col;
+        if (p.lse && col == 0) p.lse[at] = log_sum(m, l);
         if constexpr (sizeof(E) == 2)
             *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16(o.x * r, o.y * r), pack_bf16(o.z * r, o.w * r));
         else
@@ -948,6 +953,9 @@ int launch_attention(const lora_kv_pages *kv, const AttnParams &p, const Variant
            : p.d <= 128 ? launch_mma<128, false>(maps, p, st) : launch_mma<256, false>(maps, p, st);
 }
 
+// lora_tree_attention_weights: a flag, and the logarithm of each row's sum.
+size_t log_bytes(int n_q_heads, int T) { return (16 + (size_t)T * n_q_heads * sizeof(float) + 15) & ~(size_t)15; }
+
 size_t partial_bytes(const Variant &v, int d) {
     return (size_t)num_sms() * v.per_sm * (2 * v.rt * (d + 2) * sizeof(float) + sizeof(JoinRecord));
 }
@@ -964,10 +972,13 @@ extern "C" size_t lora_tree_attention_workspace_size(const lora_kv_pages *kv, in
     return partial_bytes(variant_of(kv, n_q_heads / kv->n_kv_heads, 1, T), kv->head_dim) + 16;
 }
 
-extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, const int *seg_starts, int S,
-                                   int T, const int *kv_lens, const int *page_table, int max_pages,
-                                   const long long *tree_mask, int mask_words, float scale, void *out, void *workspace,
-                                   size_t ws_bytes, lora_stream stream) {
+namespace lora {
+namespace {
+
+// weights: NULL, or the sums of lora_tree_attention_weights, whose logarithms lie before the attention's workspace.
+int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, int n_q_heads, const int *seg_starts, int S, int T,
+           const int *kv_lens, const int *page_table, int max_pages, const long long *tree_mask, int mask_words, float scale, void *out,
+           void *workspace, size_t ws_bytes, cudaStream_t st) {
     int rc = decode::check_kv(kv, n_q_heads);
     if (rc) return rc;
     if (n_q_heads < 1) return LORA_ERR_SHAPE;
@@ -982,7 +993,8 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
         return LORA_ERR_ARG;
     if (num_sms() < 1) return LORA_ERR_CUDA;
     const Variant variant = variant_of(kv, n_q_heads / kv->n_kv_heads, S, T);
-    if (ws_bytes < partial_bytes(variant, kv->head_dim) + 16) return LORA_ERR_ARG;
+    const size_t logs = weights ? log_bytes(n_q_heads, T) : 0;
+    if (ws_bytes < logs + partial_bytes(variant, kv->head_dim) + 16) return LORA_ERR_ARG;
     decode::AttnParams p;
     p.q = q;
     p.k = kv->k;
@@ -1004,7 +1016,8 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.out = out;
     p.status = kv->status;
-    cudaStream_t st = (cudaStream_t)stream;
+    p.lse = weights ? static_cast<float *>(workspace) + 4 : nullptr;
+    p.computed = weights ? static_cast<int *>(workspace) : nullptr;
     p.rt = variant.rt;
     p.tk = variant.tk;
     p.tk_shift = decode::log2_of(variant.tk);
@@ -1014,8 +1027,10 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     if (tiles * units > 0x7fffffffLL / p.n_kv) return LORA_ERR_SHAPE;
     p.max_places = (uint32_t)(tiles * units * p.n_kv);
     p.grid = num_sms() * variant.per_sm;
-    p.records = static_cast<JoinRecord *>(workspace);
+    p.records = reinterpret_cast<JoinRecord *>(static_cast<char *>(workspace) + logs);
     p.partial = reinterpret_cast<float *>(p.records + p.grid);
+    decode::AttnParams weigh;
+    if (weights && (rc = plan_weigh(kv, p, weigh))) return rc;
     if ((rc = launch_attention(kv, p, variant, st))) return rc;
     // the join starts while the last blocks run; it waits for them before it reads their sums
     cudaLaunchConfig_t cfg = {};
@@ -1030,5 +1045,33 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
     const cudaError_t e = kv->dtype == LORA_BF16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<__nv_bfloat16>, p)
                                                  : cudaLaunchKernelEx(&cfg, attention_join_kernel<float>, p);
     count_launch();
-    return cuda_status(e);
+    if ((rc = cuda_status(e))) return rc;
+    return weights ? launch_weigh(kv, weigh, weights, decay, st) : LORA_OK;
+}
+
+}  // namespace
+}  // namespace lora
+
+extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, const int *seg_starts, int S,
+                                   int T, const int *kv_lens, const int *page_table, int max_pages,
+                                   const long long *tree_mask, int mask_words, float scale, void *out, void *workspace,
+                                   size_t ws_bytes, lora_stream stream) {
+    return attend(kv, nullptr, 0.f, q, n_q_heads, seg_starts, S, T, kv_lens, page_table, max_pages, tree_mask, mask_words, scale, out,
+                  workspace, ws_bytes, (cudaStream_t)stream);
+}
+
+extern "C" size_t lora_tree_attention_weights_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T, int max_pages) {
+    const size_t base = lora_tree_attention_workspace_size(kv, n_q_heads, S, T);
+    if (!base || max_pages < 0) return 0;
+    return base + log_bytes(n_q_heads, T);
+}
+
+extern "C" int lora_tree_attention_weights(const lora_kv_pages *kv, float *weights, float decay, const void *q, int n_q_heads,
+                                           const int *seg_starts, int S, int T, const int *kv_lens, const int *page_table,
+                                           int max_pages, const long long *tree_mask, int mask_words, float scale, void *out,
+                                           void *workspace, size_t ws_bytes, lora_stream stream) {
+    if (!(decay >= 0.f && decay <= 1.f)) return LORA_ERR_ARG;
+    if (T > 0 && (!weights || !aligned16(weights))) return LORA_ERR_ARG;
+    return attend(kv, weights, decay, q, n_q_heads, seg_starts, S, T, kv_lens, page_table, max_pages, tree_mask, mask_words, scale, out,
+                  workspace, ws_bytes, (cudaStream_t)stream);
 }

@@ -36,6 +36,8 @@ struct AttnParams {
     int rt, tk, grid;        // rows a unit, tokens a tile (a power of two), blocks
     int tk_shift, unit_cost;
     uint32_t max_places;     // of the list of any table that keeps the rules; below 2^31
+    float *lse;              // [T][n_q]: log2 of each row's sum, infinity where it saw nothing; or NULL
+    int *computed;           // with lse: whether the list held anything
 };
 
 struct Request {
@@ -137,7 +139,7 @@ __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared 
     if (lane == 31 && warp < kScanThreads / 32) sh.sums[warp] = upto;
     if (tid == 0) {
         sh.request = -1;
-        p.records[blockIdx.x] = JoinRecord{};
+        if (p.records) p.records[blockIdx.x] = JoinRecord{};
     }
     __syncthreads();
     uint32_t total = 0, before = upto - mine;
@@ -147,6 +149,7 @@ __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared 
         total = add_places(total, sh.sums[w]);
     }
     if (total > p.max_places) total = 0;
+    if (flags && p.computed && p.records && tid == 0) *p.computed = total > 0;
     const uint32_t pos = block_begin(total, blockIdx.x, p.grid);
     if (total > 0 && pos >= before && pos < before + mine) {
         uint32_t rest = pos - before;
@@ -229,11 +232,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// Element offset of row `row` of the unit at cursor c in q and out.
-__device__ __forceinline__ long long row_offset(const AttnParams &p, const Cursor &c, int row) {
+// Row `row` of the unit at cursor c among the T x n_q rows of q and out, and its element offset.
+__device__ __forceinline__ long long row_index(const AttnParams &p, const Cursor &c, int row) {
     const int i = row / p.group, g = row - i * p.group;
-    return ((long long)(c.r.begin + i) * p.n_q + c.head * p.group + g) * p.d;
+    return (long long)(c.r.begin + i) * p.n_q + c.head * p.group + g;
 }
+__device__ __forceinline__ long long row_offset(const AttnParams &p, const Cursor &c, int row) { return row_index(p, c, row) * p.d; }
+
+// For p.lse: of a row's maximum and sum.
+__device__ __forceinline__ float log_sum(float top, float sum) { return sum == 0.f ? INFINITY : top + log2f(sum); }
 
 // Place of element (row, col) in a block's sums: neighbouring rows' groups of four columns lie side by side.
 __device__ __forceinline__ int partial_at(const AttnParams &p, int row, int col) { return ((col >> 2) * p.rt + row) * 4 + (col & 3); }
@@ -248,6 +255,11 @@ struct KvMaps;
 // attention_tc.cu: p.rt (128 or 256 rows), p.tk (128), p.grid and p.partial set; p.d is 64
 // or 128.  maps: tensor maps with boxes of min(page, 128) rows, or NULL (pages below 8 tokens).
 int launch_attention_tc(const KvMaps *maps, const AttnParams &p, cudaStream_t st);
+
+// weigh.cu: the weights of the cached tokens from p.lse, after the attention's kernels on the stream.  plan_weigh makes
+// launch_weigh's parameters of the attention's, or refuses.
+int plan_weigh(const lora_kv_pages *kv, const AttnParams &attention, AttnParams &p);
+int launch_weigh(const lora_kv_pages *kv, const AttnParams &p, float *weights, float decay, cudaStream_t st);
 
 }  // namespace decode
 }  // namespace lora

@@ -592,6 +592,7 @@ __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t 
         if (writes && !seg.whole) {
             *reinterpret_cast<float2 *>(dst + p.rt * D + ur * 2) = make_float2(m, l);
         }
+        if (p.lse && writes && seg.whole) p.lse[my_off / D] = log_sum(m, l);
         // stream 1 hands its output over through its queries' space, 64 columns at a time
         float *hand = reinterpret_cast<float *>(queries + Sh::kSlot);
         constexpr int kHandCols = D == 128 ? 64 : 32;

@@ -1,0 +1,173 @@
+// Weights that cached tokens get from an attention (lora_tree_attention_weights):
+//
+//   w_c <- decay w_c (prefix; a drafted token starts from 0) + sum over the request's rows
+//          of 2^(scale log2(e) q . k_c - lse),  lse = log2 sum_c 2^(..) of the row,
+//
+// over the rows that see c.  The attention's kernels leave lse; here the scores are
+// computed once more, keys at rest and rows going by, so that a key's sum stays in one block and its order is fixed.
+#include "attention.cuh"
+
+namespace lora {
+namespace {
+
+using namespace decode;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kTile = 32;              // cached tokens a tile, one a lane
+constexpr int kWarpRows = 4, kRows = kWarps * kWarpRows;
+
+// A block's part of the list whose places are (request, kv head, key tile, row tile): the key tiles that begin in it.
+struct KeyCursor {
+    Request r;
+    int s, head, tile, left;
+    __device__ __forceinline__ void start(const AttnParams &p, const ScanShared &sh, const Cursor &c) {
+        s = c.s;
+        left = 0;
+        if (s < 0) return;
+        r = sh.r;
+        const uint32_t each = (uint32_t)r.tiles * r.row_tiles, h = sh.residual / each, rest = sh.residual - h * each;
+        head = h;
+        tile = rest / (uint32_t)r.row_tiles;
+        left = c.left;
+        const int into = rest - (uint32_t)tile * r.row_tiles;
+        if (into) {                    // the tile began in an earlier block
+            left -= r.row_tiles - into;
+            next(p);
+        }
+    }
+    __device__ __forceinline__ void next(const AttnParams &p) {
+        if (++tile < r.tiles || left <= 0) return;
+        tile = 0;
+        if (++head < p.n_kv) return;
+        head = 0;
+        do {
+            if (++s >= p.S) {
+                left = 0;
+                return;
+            }
+            r = request_of(p, s);
+        } while (r.row_tiles == 0 || r.tiles == 0);
+    }
+    __device__ __forceinline__ void advance(const AttnParams &p) {
+        left -= r.row_tiles;
+        next(p);
+    }
+};
+
+// The weight's place of cached token c, -1 where its page is outside the cache (flagged).
+__device__ __forceinline__ long long weight_at(const AttnParams &p, int s, const Request &r, int head, int c) {
+    const int page = page_of(p, s, r, c);
+    if (page < 0 || page >= p.n_pages) {
+        flag_status(p.status, LORA_DEV_BAD_PAGE);
+        return -1;
+    }
+    return (((long long)page * p.n_kv + head) << p.page_shift) + (c & ((1 << p.page_shift) - 1));
+}
+
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <typename E>
+__global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, float *weights, float decay) {
+    extern __shared__ __align__(16) float smem[];
+    __shared__ ScanShared scan;
+    __shared__ float sums[kWarps][kTile];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pitch = p.d + 4;
+    float *ks = smem, *qs = smem + kTile * pitch;
+    Cursor at;
+    start_block(p, scan, at);
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    KeyCursor cur;
+    cur.start(p, scan, at);
+    if (!*p.computed) return;
+    for (; cur.left > 0; cur.advance(p)) {
+        const int c0 = cur.tile * kTile, rows = cur.r.n * p.group;
+        __syncthreads();
+        for (int x = tid; x < kTile * p.d; x += kThreads) {
+            const int j = x / p.d, e = x - j * p.d;
+            const long long slot = c0 + j < cur.r.len ? weight_at(p, cur.s, cur.r, cur.head, c0 + j) : -1;
+            ks[j * pitch + e] = slot >= 0 ? as_float(static_cast<const E *>(p.k)[slot * p.d + e]) : 0.f;
+        }
+        float acc = 0.f;
+        for (int r0 = 0; r0 < rows; r0 += kRows) {
+            __syncthreads();
+            for (int x = tid; x < kRows * p.d; x += kThreads) {
+                const int j = x / p.d, e = x - j * p.d, row = r0 + j, i = row / p.group;
+                const long long from = ((long long)(cur.r.begin + i) * p.n_q + cur.head * p.group + row - i * p.group) * p.d + e;
+                qs[j * pitch + e] = row < rows ? as_float(static_cast<const E *>(p.q)[from]) : 0.f;
+            }
+            __syncthreads();
+            float dot[kWarpRows] = {};
+            for (int e = 0; e < p.d; e += 4) {
+                const float4 k = *reinterpret_cast<const float4 *>(ks + lane * pitch + e);
+#pragma unroll
+                for (int a = 0; a < kWarpRows; ++a) {
+                    const float4 q = *reinterpret_cast<const float4 *>(qs + (warp * kWarpRows + a) * pitch + e);
+                    dot[a] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, dot[a]))));
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < kWarpRows; ++a) {
+                const int row = r0 + warp * kWarpRows + a;
+                if (row >= rows) continue;
+                const int i = row / p.group;
+                const uint32_t see = seen_word(p, cur.r, i, c0);
+                const float lse = p.lse[(long long)(cur.r.begin + i) * p.n_q + cur.head * p.group + row - i * p.group];
+                if ((see >> lane) & 1) acc += exp2f(dot[a] * p.scale_log2 - lse);
+            }
+        }
+        sums[warp][lane] = acc;
+        __syncthreads();
+        const int c = c0 + tid;
+        if (tid < kTile && c < cur.r.len) {
+            const long long slot = weight_at(p, cur.s, cur.r, cur.head, c);
+            if (slot >= 0) {
+                float w = c < cur.r.len - cur.r.n && decay > 0.f ? weights[slot] * decay : 0.f;
+                for (int x = 0; x < kWarps; ++x) w += sums[x][tid];
+                weights[slot] = w;
+            }
+        }
+    }
+}
+
+}  // namespace
+
+namespace decode {
+
+int plan_weigh(const lora_kv_pages *kv, const AttnParams &attention, AttnParams &p) {
+    p = attention;
+    p.records = nullptr;
+    p.rt = kRows;
+    p.tk = kTile;
+    p.tk_shift = log2_of(kTile);
+    p.unit_cost = 0;
+    const long long tiles = (long long)p.max_pages * kv->page_size / kTile + 1, units = (long long)p.T * p.group / kRows + p.S;
+    if (tiles * units > 0x7fffffffLL / p.n_kv) return LORA_ERR_SHAPE;
+    p.max_places = (uint32_t)(tiles * units * p.n_kv);
+    p.grid = num_sms() * 2;
+    return LORA_OK;
+}
+
+int launch_weigh(const lora_kv_pages *kv, const AttnParams &p, float *weights, float decay, cudaStream_t st) {
+    const size_t smem = (size_t)(kTile + kRows) * (p.d + 4) * sizeof(float);
+    const void *kernel = kv->dtype == LORA_BF16 ? reinterpret_cast<const void *>(weigh_kernel<__nv_bfloat16>)
+                                                : reinterpret_cast<const void *>(weigh_kernel<float>);
+    if (smem_optin(kernel, smem)) return LORA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = kv->dtype == LORA_BF16 ? cudaLaunchKernelEx(&cfg, weigh_kernel<__nv_bfloat16>, p, weights, decay)
+                                                 : cudaLaunchKernelEx(&cfg, weigh_kernel<float>, p, weights, decay);
+    count_launch();
+    return cuda_status(e);
+}
+
+}  // namespace decode
+}  // namespace lora

@@ -51,7 +51,7 @@ EXPORTS = ["lora_pool_create", "lora_pool_destroy", "lora_pool_load", "lora_pool
            "lora_pool_unload_async", "lora_pool_prefetch", "lora_quantize_e4m3",
            "lora_layer_forward_fp8_workspace_size", "lora_layer_forward_fp8", "lora_w4_matvec", "lora_kv_append",
            "lora_tree_attention_workspace_size", "lora_tree_attention", "lora_kv_append_axes",
-           "lora_kv_evict"]
+           "lora_tree_attention_weights_workspace_size", "lora_tree_attention_weights", "lora_kv_evict"]
 
 if not os.path.exists(_build.LIB):
     raise ImportError(f"CUDA library {_build.LIB} is not built: run segmented_gathered_rank_gb300.build.build()")
@@ -128,6 +128,9 @@ _sig("lora_kv_append", _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _
      ctypes.c_float, _P, _P)
 _sig("lora_kv_append_axes", _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, ctypes.c_char_p, _P, _P, _I, _I, _I, _P, _P,
      ctypes.c_float, _P, _P)
+_sig("lora_tree_attention_weights_workspace_size", ctypes.c_size_t, _P, _I, _I, _I, _I)
+_sig("lora_tree_attention_weights", _I, _P, _P, ctypes.c_float, _P, _I, _P, _I, _I, _P, _P, _I, _P, _I, ctypes.c_float, _P, _P,
+     ctypes.c_size_t, _P)
 _sig("lora_kv_evict", _I, _P, _P, _P, _I, _P, _P, _I, _P, _I, _I, _P, _I, _P, _P)
 _sig("lora_tree_attention_workspace_size", ctypes.c_size_t, _P, _I, _I, _I)
 _sig("lora_tree_attention", _I, _P, _P, _I, _P, _I, _I, _P, _P, _I, _P, _I, ctypes.c_float, _P, _P,
@@ -427,6 +430,23 @@ def _plane(kv, t):
     if t is not None and t.numel() < kv.slots:
         raise ValueError("expected n_pages x n_kv_heads x page_size numbers")
     return _ptr(t)
+
+
+def lora_tree_attention_weights_workspace_size(kv, n_q_heads, S, T, max_pages) -> int:
+    return int(_lib.lora_tree_attention_weights_workspace_size(kv.address, n_q_heads, S, T, max_pages))
+
+
+def lora_tree_attention_weights(kv, weights, decay, q, n_q_heads, seg_starts, S, T, kv_lens, page_table, max_pages, tree_mask,
+                                mask_words, scale, out, workspace, ws_bytes=None, stream=None) -> None:
+    """lora_tree_attention that adds the weight of each cached token, times decay what it had, to weights (float
+    [n_pages, n_kv_heads, page_size])."""
+    if ws_bytes is None:
+        ws_bytes = workspace.nbytes
+    rc = _lib.lora_tree_attention_weights(kv.address, _plane(kv, weights), decay, _ptr(q), n_q_heads, _ptr(seg_starts), S, T, _ptr(kv_lens),
+                                          _ptr(page_table), max_pages, _ptr(tree_mask), mask_words, scale, _ptr(out), _ptr(workspace),
+                                          ws_bytes, _stream_ptr(stream))
+    if rc:
+        _check(rc, "lora_tree_attention_weights")
 
 
 def lora_kv_evict(kv, scores, weights, S, kv_lens, page_table, max_pages, keep, first, recent, kept, ld_kept, new_lens,

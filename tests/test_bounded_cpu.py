@@ -103,3 +103,38 @@ def test_planes_that_are_too_small_are_refused_in_python():
         L.lora_kv_evict(kv, Cuda(4, 2, 7), None, *args, stream=0)
     with pytest.raises(ValueError):
         L.lora_kv_evict(kv, Cuda(4, 2, 8), Cuda(63), *args, stream=0)
+
+
+def weigh(kv, weights=P, decay=1.0, q=P, n_q=4, starts=P, S=2, T=2, lens=P, table=P, max_pages=4, mask=None, words=0, scale=0.1, out=P,
+          workspace=P, ws_bytes=1 << 30):
+    return L._lib.lora_tree_attention_weights(ctypes.byref(kv), weights, decay, q, n_q, starts, S, T, lens, table, max_pages, mask, words,
+                                              scale, out, workspace, ws_bytes, None)
+
+
+@pytest.mark.parametrize("change, code", BAD_PAGES)
+def test_attention_weights_refuses_pages(change, code):
+    kv = pages(**change)
+    assert weigh(kv) == code
+    assert L._lib.lora_tree_attention_weights_workspace_size(ctypes.byref(kv), 4, 2, 2, 4) == 0
+
+
+@pytest.mark.parametrize("change, code", [
+    (dict(weights=None), L.LORA_ERR_ARG), (dict(weights=P + 4), L.LORA_ERR_ARG), (dict(decay=-0.1), L.LORA_ERR_ARG),
+    (dict(decay=1.5), L.LORA_ERR_ARG), (dict(decay=float("nan")), L.LORA_ERR_ARG),
+    (dict(n_q=0), L.LORA_ERR_SHAPE), (dict(n_q=5), L.LORA_ERR_SHAPE), (dict(scale=0.0), L.LORA_ERR_ARG),
+    (dict(scale=float("inf")), L.LORA_ERR_ARG), (dict(S=-1), L.LORA_ERR_ARG), (dict(S=0), L.LORA_ERR_ARG), (dict(T=-1), L.LORA_ERR_ARG),
+    (dict(max_pages=-1), L.LORA_ERR_ARG), (dict(max_pages=0), L.LORA_ERR_ARG), (dict(mask=P), L.LORA_ERR_ARG),
+    (dict(mask=P + 4, words=1), L.LORA_ERR_ARG), (dict(q=P + 8), L.LORA_ERR_ARG), (dict(out=None), L.LORA_ERR_ARG),
+    (dict(starts=P + 2), L.LORA_ERR_ARG), (dict(lens=None), L.LORA_ERR_ARG), (dict(table=None), L.LORA_ERR_ARG),
+    (dict(workspace=None), L.LORA_ERR_ARG), (dict(workspace=P + 8), L.LORA_ERR_ARG), (dict(max_pages=1 << 28), L.LORA_ERR_SHAPE)])
+def test_attention_weights_refuses(change, code):
+    before = L.lora_launch_count()
+    assert weigh(pages(), **change) == code
+    assert L.lora_launch_count() == before
+
+
+def test_attention_weights_without_tokens():
+    before = L.lora_launch_count()
+    assert weigh(pages(), T=0, weights=None, q=None, out=None, starts=None, lens=None, table=None, workspace=None) == L.LORA_OK
+    assert L.lora_launch_count() == before
+    assert L._lib.lora_tree_attention_weights_workspace_size(ctypes.byref(pages()), 4, 2, 2, -1) == 0
