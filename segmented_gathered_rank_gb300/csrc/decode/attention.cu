@@ -123,7 +123,8 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, MmaCon
 // Four consumer warps; each takes kWarpKeys of a stage's tokens for all rows of
 // the unit, with a maximum, sum and output of its own (so a tile needs no exchange
 // between warps), joined in shared memory when the block leaves the unit.
-template <int D, bool TMA>
+// KEEP: the scores go to p.scores as well.
+template <int D, bool TMA, bool KEEP>
 __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t *smem, MmaControl &ctl) {
     using Sh = MmaShape<D, TMA>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -205,6 +206,17 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (!((see[e >> 1] >> (j * 8 + t4 * 2 + (e & 1))) & 1)) s[j][e] = -INFINITY;
+            }
+            if constexpr (KEEP) {
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+                    if (hh * 8 + g4 >= rows) continue;
+                    float *dst = p.scores + row_index(p, cur, cur.row_tile * kRows + hh * 8 + g4) * p.ld_scores + c0 + t4 * 2;
+#pragma unroll
+                    for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
+                        if (c0 + j * 8 + t4 * 2 < cur.r.len)
+                            *reinterpret_cast<float2 *>(dst + j * 8) = make_float2(s[j][hh * 2] * p.scale_log2, s[j][hh * 2 + 1] * p.scale_log2);
+                }
             }
             // softmax of the warp's keys
             float a[2];
@@ -370,7 +382,7 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
     }
 }
 
-template <int D, bool TMA>
+template <int D, bool TMA, bool KEEP>
 __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, TMA>::kPerSm))
     attention_mma_kernel(const __grid_constant__ KvMaps maps, const AttnParams p) {
     using Sh = MmaShape<D, TMA>;
@@ -392,7 +404,7 @@ __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, 
     const uint32_t total = start_block(p, scan, cur);
     if (cur.left <= 0) return;
     if (threadIdx.x < kThreads) {
-        consume<D, TMA>(p, cur, total, smem, ctl);
+        consume<D, TMA, KEEP>(p, cur, total, smem, ctl);
     } else {
         const int tid = threadIdx.x - kThreads;
         const uint32_t base = smem_addr(smem);
@@ -427,7 +439,7 @@ __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, 
 constexpr int kSimtTile = 32;
 constexpr int kSimtRows = 16;
 
-template <int D>
+template <int D, bool KEEP>
 __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnParams p) {
     constexpr int kLd = D + 4;            // row pitch: lanes a row apart read different banks
     constexpr int kCols = D / 32;
@@ -523,6 +535,8 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                 if (!sure && row0 + a < rows) see[a] = seen_word(p, cur.r, (cur.row_tile * p.rt + row0 + a) / p.group, cur.tile * kSimtTile);
                 const bool on = (see[a] >> lane) & 1;
                 const float x = on ? (s2[a].x + s2[a].y) * p.scale_log2 : -INFINITY;
+                if (KEEP && row0 + a < rows && cur.tile * kSimtTile + lane < cur.r.len)
+                    p.scores[row_index(p, cur, cur.row_tile * p.rt + row0 + a) * p.ld_scores + cur.tile * kSimtTile + lane] = x;
                 float top = x;
 #pragma unroll
                 for (int b = 16; b > 0; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
@@ -625,7 +639,7 @@ constexpr int kWarpRows = 4;       // query rows a warp
 // leaves the unit; the maximum is raised only when a score passes it by 2^8.  In the
 // steps past the prefix, values that a row does not see are left out, whatever they are.
 // FULL: d is D.
-template <int D, bool FULL>
+template <int D, bool FULL, bool KEEP>
 __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few_kernel(const AttnParams p) {
     constexpr int kLanes = D == 256 ? 16 : 8, kTokens = 32 / kLanes, kVec = D / (4 * kLanes);
     __shared__ ScanShared scan;
@@ -698,6 +712,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few
                     on[a] = (see >> (c & 31)) & 1;
                     if (!on[a]) s[a] = -INFINITY;
                 }
+                if (KEEP && first_chunk == a && row0 + a < rows && c < end)
+                    p.scores[row_index(p, cur, cur.row_tile * p.rt + row0 + a) * p.ld_scores + c] = s[a];
                 raise |= s[a] > m[a] + 8.f;        // from -infinity by any score
             }
             if (__any_sync(0xffffffffu, raise)) {
@@ -909,52 +925,68 @@ bool make_map(CUtensorMap *map, void *pages, const lora_kv_pages *kv, int rows) 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool TMA>
+template <int D, bool TMA, bool KEEP>
 int launch_mma(const KvMaps &maps, const AttnParams &p, cudaStream_t st) {
     using Sh = MmaShape<D, TMA>;
-    if (smem_optin(reinterpret_cast<const void *>(attention_mma_kernel<D, TMA>), Sh::kSmem)) return LORA_ERR_CUDA;
-    attention_mma_kernel<D, TMA><<<p.grid, Sh::kThreadsAll, Sh::kSmem, st>>>(maps, p);
+    if (smem_optin(reinterpret_cast<const void *>(attention_mma_kernel<D, TMA, KEEP>), Sh::kSmem)) return LORA_ERR_CUDA;
+    attention_mma_kernel<D, TMA, KEEP><<<p.grid, Sh::kThreadsAll, Sh::kSmem, st>>>(maps, p);
     count_launch();
     return cuda_status(cudaGetLastError());
 }
 
-template <int D>
+template <int D, bool KEEP>
 int launch_simt(const AttnParams &p, cudaStream_t st) {
     const size_t smem = (size_t)(kSimtRows * D + 4 * kSimtTile * 4 + 4 * kSimtTile * (D + 4)) * 4;
-    if (smem_optin(reinterpret_cast<const void *>(attention_simt_kernel<D>), smem)) return LORA_ERR_CUDA;
-    attention_simt_kernel<D><<<p.grid, kThreads, smem, st>>>(p);
+    if (smem_optin(reinterpret_cast<const void *>(attention_simt_kernel<D, KEEP>), smem)) return LORA_ERR_CUDA;
+    attention_simt_kernel<D, KEEP><<<p.grid, kThreads, smem, st>>>(p);
     count_launch();
     return cuda_status(cudaGetLastError());
 }
 
-template <int D>
+template <int D, bool KEEP>
 int launch_few(const AttnParams &p, cudaStream_t st) {
-    if (p.d == D) attention_few_kernel<D, true><<<p.grid, kFewWarps * 32, 0, st>>>(p);
-    else attention_few_kernel<D, false><<<p.grid, kFewWarps * 32, 0, st>>>(p);
+    if (p.d == D) attention_few_kernel<D, true, KEEP><<<p.grid, kFewWarps * 32, 0, st>>>(p);
+    else attention_few_kernel<D, false, KEEP><<<p.grid, kFewWarps * 32, 0, st>>>(p);
     count_launch();
     return cuda_status(cudaGetLastError());
+}
+
+template <int D, bool KEEP>
+int launch_width(const KvMaps *maps, const AttnParams &p, bool f32, bool few, cudaStream_t st) {
+    if (few) return launch_few<D, KEEP>(p, st);
+    if (f32) return launch_simt<D, KEEP>(p, st);
+    return maps ? launch_mma<D, true, KEEP>(*maps, p, st) : launch_mma<D, false, KEEP>(KvMaps{}, p, st);
+}
+template <bool KEEP>
+int launch_any(const KvMaps *maps, const AttnParams &p, bool f32, bool few, cudaStream_t st) {
+    return p.d <= 64 ? launch_width<64, KEEP>(maps, p, f32, few, st)
+           : p.d <= 128 ? launch_width<128, KEEP>(maps, p, f32, few, st) : launch_width<256, KEEP>(maps, p, f32, few, st);
 }
 
 int launch_attention(const lora_kv_pages *kv, const AttnParams &p, const Variant &v, cudaStream_t st) {
-    if (v.few) return p.d <= 64 ? launch_few<64>(p, st) : p.d <= 128 ? launch_few<128>(p, st) : launch_few<256>(p, st);
-    if (kv->dtype == LORA_F32)
-        return p.d <= 64 ? launch_simt<64>(p, st) : p.d <= 128 ? launch_simt<128>(p, st) : launch_simt<256>(p, st);
     KvMaps maps = {};
-    const bool tma = kv->page_size >= kTmaMinPage;
+    const bool f32 = kv->dtype == LORA_F32, tma = !f32 && kv->page_size >= kTmaMinPage;
     if (tma) {
         const int rows = kv->page_size < v.tk ? kv->page_size : v.tk;
         if (!make_map(&maps.k, kv->k, kv, rows) || !make_map(&maps.v, kv->v, kv, rows)) return LORA_ERR_CUDA;
     }
     if (v.tc) return launch_attention_tc(tma ? &maps : nullptr, p, st);
-    if (tma)
-        return p.d <= 64 ? launch_mma<64, true>(maps, p, st)
-               : p.d <= 128 ? launch_mma<128, true>(maps, p, st) : launch_mma<256, true>(maps, p, st);
-    return p.d <= 64 ? launch_mma<64, false>(maps, p, st)
-           : p.d <= 128 ? launch_mma<128, false>(maps, p, st) : launch_mma<256, false>(maps, p, st);
+    return p.scores ? launch_any<true>(tma ? &maps : nullptr, p, f32, v.few, st)
+                    : launch_any<false>(tma ? &maps : nullptr, p, f32, v.few, st);
 }
 
 // lora_tree_attention_weights: a flag, and the logarithm of each row's sum.
 size_t log_bytes(int n_q_heads, int T) { return (16 + (size_t)T * n_q_heads * sizeof(float) + 15) & ~(size_t)15; }
+
+// Whether the weights are summed up from kept scores: up to 16 rows a kv head and request on average.
+constexpr int kKeepRows = 16;
+bool keeps_scores(int group, int S, int T) { return (long long)T * group <= (long long)kKeepRows * S; }
+long long score_pitch(const lora_kv_pages *kv, int max_pages) { return ((long long)max_pages * kv->page_size + 7) & ~7LL; }
+// At most, for up to T tokens of up to S requests.
+size_t score_bytes(const lora_kv_pages *kv, int n_q_heads, int S, int T, int max_pages) {
+    const long long most = (long long)kKeepRows * S / (n_q_heads / kv->n_kv_heads), tokens = T < most ? T : most;
+    return (size_t)tokens * n_q_heads * score_pitch(kv, max_pages) * sizeof(float);
+}
 
 size_t partial_bytes(const Variant &v, int d) {
     return (size_t)num_sms() * v.per_sm * (2 * v.rt * (d + 2) * sizeof(float) + sizeof(JoinRecord));
@@ -993,8 +1025,10 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
         return LORA_ERR_ARG;
     if (num_sms() < 1) return LORA_ERR_CUDA;
     const Variant variant = variant_of(kv, n_q_heads / kv->n_kv_heads, S, T);
+    const bool keep = weights && keeps_scores(n_q_heads / kv->n_kv_heads, S, T);
     const size_t logs = weights ? log_bytes(n_q_heads, T) : 0;
-    if (ws_bytes < logs + partial_bytes(variant, kv->head_dim) + 16) return LORA_ERR_ARG;
+    const size_t kept = keep ? score_bytes(kv, n_q_heads, S, T, max_pages) : 0, parts = (partial_bytes(variant, kv->head_dim) + 15) & ~(size_t)15;
+    if (ws_bytes < logs + parts + kept + (weights ? 32 : 0) || ws_bytes < partial_bytes(variant, kv->head_dim) + 16) return LORA_ERR_ARG;
     decode::AttnParams p;
     p.q = q;
     p.k = kv->k;
@@ -1018,6 +1052,8 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
     p.status = kv->status;
     p.lse = weights ? static_cast<float *>(workspace) + 4 : nullptr;
     p.computed = weights ? static_cast<int *>(workspace) : nullptr;
+    p.scores = keep ? reinterpret_cast<float *>(((uintptr_t)workspace + logs + parts + 31) & ~(uintptr_t)31) : nullptr;     // whole sectors
+    p.ld_scores = score_pitch(kv, max_pages);
     p.rt = variant.rt;
     p.tk = variant.tk;
     p.tk_shift = decode::log2_of(variant.tk);
@@ -1063,7 +1099,7 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
 extern "C" size_t lora_tree_attention_weights_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T, int max_pages) {
     const size_t base = lora_tree_attention_workspace_size(kv, n_q_heads, S, T);
     if (!base || max_pages < 0) return 0;
-    return base + log_bytes(n_q_heads, T);
+    return base + log_bytes(n_q_heads, T) + score_bytes(kv, n_q_heads, S, T, max_pages) + 48;
 }
 
 extern "C" int lora_tree_attention_weights(const lora_kv_pages *kv, float *weights, float decay, const void *q, int n_q_heads,

@@ -38,6 +38,8 @@ struct AttnParams {
     uint32_t max_places;     // of the list of any table that keeps the rules; below 2^31
     float *lse;              // [T][n_q]: log2 of each row's sum, infinity where it saw nothing; or NULL
     int *computed;           // with lse: whether the list held anything
+    float *scores;           // [T][n_q][ld_scores]: the rows' scores in powers of two (-infinity: not seen); or NULL
+    long long ld_scores;     // a multiple of 8
 };
 
 struct Request {

@@ -3,8 +3,12 @@
 //   w_c <- decay w_c (prefix; a drafted token starts from 0) + sum over the request's rows
 //          of 2^(scale log2(e) q . k_c - lse),  lse = log2 sum_c 2^(..) of the row,
 //
-// over the rows that see c.  The attention's kernels leave lse; here the scores are
-// computed once more, keys at rest and rows going by, so that a key's sum stays in one block and its order is fixed.
+// over the rows that see c.  The attention's kernels leave lse.
+//
+// weigh_scores_kernel: with few rows they leave the scores too (4 bytes a row and token
+//   against 2 d for reading a key again), and a thread sums up four tokens.
+// weigh_kernel: else the scores are computed once more, keys at rest and rows going by,
+//   so that a key's sum stays in one block and its order is fixed.
 #include "attention.cuh"
 
 namespace lora {
@@ -130,6 +134,55 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
     }
 }
 
+constexpr int kScoreTile = 1024;       // cached tokens a tile, four a thread
+
+__global__ void __launch_bounds__(kThreads) weigh_scores_kernel(const AttnParams p, float *weights, float decay) {
+    __shared__ ScanShared scan;
+    Cursor at;
+    start_block(p, scan, at);
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    KeyCursor cur;
+    cur.start(p, scan, at);
+    if (!*p.computed) return;
+    for (; cur.left > 0; cur.advance(p)) {
+        const int c = cur.tile * kScoreTile + threadIdx.x * 4, rows = cur.r.n * p.group;
+        if (c >= cur.r.len) continue;
+        float w[4] = {};
+        // rows of a kv head lie group by group of n_q rows
+        const long long first = (long long)cur.r.begin * p.n_q + cur.head * p.group;
+#pragma unroll 4
+        for (int row = 0; row < rows; ++row) {
+            const int i = row / p.group;
+            const long long line = first + (long long)i * (p.n_q - p.group) + row;
+            const float4 s = *reinterpret_cast<const float4 *>(p.scores + line * p.ld_scores + c);
+            const float lse = p.lse[line];
+            w[0] += exp2f(s.x - lse);
+            w[1] += exp2f(s.y - lse);
+            w[2] += exp2f(s.z - lse);
+            w[3] += exp2f(s.w - lse);
+        }
+        const int prefix = cur.r.len - cur.r.n;
+        if (p.page_shift >= 2 && c + 4 <= cur.r.len) {
+            const long long slot = weight_at(p, cur.s, cur.r, cur.head, c);
+            if (slot < 0) continue;
+            float4 *dst = reinterpret_cast<float4 *>(weights + slot);
+            if (decay > 0.f && c < prefix) {
+                const float4 old = *dst;
+                w[0] += old.x * decay;
+                if (c + 1 < prefix) w[1] += old.y * decay;
+                if (c + 2 < prefix) w[2] += old.z * decay;
+                if (c + 3 < prefix) w[3] += old.w * decay;
+            }
+            *dst = make_float4(w[0], w[1], w[2], w[3]);
+        } else {
+            for (int x = 0; x < 4 && c + x < cur.r.len; ++x) {
+                const long long slot = weight_at(p, cur.s, cur.r, cur.head, c + x);
+                if (slot >= 0) weights[slot] = decay > 0.f && c + x < prefix ? w[x] + weights[slot] * decay : w[x];
+            }
+        }
+    }
+}
+
 }  // namespace
 
 namespace decode {
@@ -137,22 +190,22 @@ namespace decode {
 int plan_weigh(const lora_kv_pages *kv, const AttnParams &attention, AttnParams &p) {
     p = attention;
     p.records = nullptr;
-    p.rt = kRows;
-    p.tk = kTile;
-    p.tk_shift = log2_of(kTile);
+    p.rt = p.scores ? 1 << 30 : kRows;         // kept scores: a tile's rows are one place
+    p.tk = p.scores ? kScoreTile : kTile;
+    p.tk_shift = log2_of(p.tk);
     p.unit_cost = 0;
-    const long long tiles = (long long)p.max_pages * kv->page_size / kTile + 1, units = (long long)p.T * p.group / kRows + p.S;
+    const long long tiles = (long long)p.max_pages * kv->page_size / p.tk + 1, units = (long long)p.T * p.group / p.rt + p.S;
     if (tiles * units > 0x7fffffffLL / p.n_kv) return LORA_ERR_SHAPE;
     p.max_places = (uint32_t)(tiles * units * p.n_kv);
-    p.grid = num_sms() * 2;
+    p.grid = num_sms() * (p.scores ? 8 : 2);
     return LORA_OK;
 }
 
 int launch_weigh(const lora_kv_pages *kv, const AttnParams &p, float *weights, float decay, cudaStream_t st) {
-    const size_t smem = (size_t)(kTile + kRows) * (p.d + 4) * sizeof(float);
-    const void *kernel = kv->dtype == LORA_BF16 ? reinterpret_cast<const void *>(weigh_kernel<__nv_bfloat16>)
-                                                : reinterpret_cast<const void *>(weigh_kernel<float>);
-    if (smem_optin(kernel, smem)) return LORA_ERR_CUDA;
+    void (*const kernel)(AttnParams, float *, float) = p.scores ? weigh_scores_kernel
+                                                       : kv->dtype == LORA_BF16 ? weigh_kernel<__nv_bfloat16> : weigh_kernel<float>;
+    const size_t smem = p.scores ? 0 : (size_t)(kTile + kRows) * (p.d + 4) * sizeof(float);
+    if (smem && smem_optin(reinterpret_cast<const void *>(kernel), smem)) return LORA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid);
     cfg.blockDim = dim3(kThreads);
@@ -163,8 +216,7 @@ int launch_weigh(const lora_kv_pages *kv, const AttnParams &p, float *weights, f
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = kv->dtype == LORA_BF16 ? cudaLaunchKernelEx(&cfg, weigh_kernel<__nv_bfloat16>, p, weights, decay)
-                                                 : cudaLaunchKernelEx(&cfg, weigh_kernel<float>, p, weights, decay);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, weights, decay);
     count_launch();
     return cuda_status(e);
 }
