@@ -34,6 +34,7 @@
 #include <type_traits>
 
 #include "kv_copy.cuh"
+#include "weigh.cuh"
 
 namespace lora {
 namespace {
@@ -963,13 +964,16 @@ int launch_any(const KvMaps *maps, const AttnParams &p, bool f32, bool few, cuda
            : p.d <= 128 ? launch_width<128, KEEP>(maps, p, f32, few, st) : launch_width<256, KEEP>(maps, p, f32, few, st);
 }
 
+// Tensor maps for tiles of up to `tile` cached tokens.
+bool make_maps(KvMaps &maps, const lora_kv_pages *kv, int tile) {
+    const int rows = kv->page_size < tile ? kv->page_size : tile;
+    return make_map(&maps.k, kv->k, kv, rows) && make_map(&maps.v, kv->v, kv, rows);
+}
+
 int launch_attention(const lora_kv_pages *kv, const AttnParams &p, const Variant &v, cudaStream_t st) {
     KvMaps maps = {};
     const bool f32 = kv->dtype == LORA_F32, tma = !f32 && kv->page_size >= kTmaMinPage;
-    if (tma) {
-        const int rows = kv->page_size < v.tk ? kv->page_size : v.tk;
-        if (!make_map(&maps.k, kv->k, kv, rows) || !make_map(&maps.v, kv->v, kv, rows)) return LORA_ERR_CUDA;
-    }
+    if (tma && !make_maps(maps, kv, v.tk)) return LORA_ERR_CUDA;
     if (v.tc) return launch_attention_tc(tma ? &maps : nullptr, p, st);
     return p.scores ? launch_any<true>(tma ? &maps : nullptr, p, f32, v.few, st)
                     : launch_any<false>(tma ? &maps : nullptr, p, f32, v.few, st);
@@ -1066,7 +1070,10 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
     p.records = reinterpret_cast<JoinRecord *>(static_cast<char *>(workspace) + logs);
     p.partial = reinterpret_cast<float *>(p.records + p.grid);
     decode::AttnParams weigh;
+    KvMaps maps = {};
+    const bool tma = weights && !keep && kv->dtype == LORA_BF16 && kv->page_size >= kTmaMinPage;
     if (weights && (rc = plan_weigh(kv, p, weigh))) return rc;
+    if (tma && !make_maps(maps, kv, kWeighTile / 2)) return LORA_ERR_CUDA;
     if ((rc = launch_attention(kv, p, variant, st))) return rc;
     // the join starts while the last blocks run; it waits for them before it reads their sums
     cudaLaunchConfig_t cfg = {};
@@ -1082,7 +1089,7 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
                                                  : cudaLaunchKernelEx(&cfg, attention_join_kernel<float>, p);
     count_launch();
     if ((rc = cuda_status(e))) return rc;
-    return weights ? launch_weigh(kv, weigh, weights, decay, st) : LORA_OK;
+    return weights ? launch_weigh(kv, tma ? &maps : nullptr, weigh, weights, decay, st) : LORA_OK;
 }
 
 }  // namespace

@@ -261,7 +261,7 @@ int launch_attention_tc(const KvMaps *maps, const AttnParams &p, cudaStream_t st
 // weigh.cu: the weights of the cached tokens from p.lse, after the attention's kernels on the stream.  plan_weigh makes
 // launch_weigh's parameters of the attention's, or refuses.
 int plan_weigh(const lora_kv_pages *kv, const AttnParams &attention, AttnParams &p);
-int launch_weigh(const lora_kv_pages *kv, const AttnParams &p, float *weights, float decay, cudaStream_t st);
+int launch_weigh(const lora_kv_pages *kv, const KvMaps *maps, const AttnParams &p, float *weights, float decay, cudaStream_t st);
 
 }  // namespace decode
 }  // namespace lora

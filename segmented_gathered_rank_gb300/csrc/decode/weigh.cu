@@ -7,9 +7,10 @@
 //
 // weigh_scores_kernel: with few rows they leave the scores too (4 bytes a row and token
 //   against 2 d for reading a key again), and a thread sums up four tokens.
-// weigh_kernel: else the scores are computed once more, keys at rest and rows going by,
-//   so that a key's sum stays in one block and its order is fixed.
-#include "attention.cuh"
+// weigh_tc_kernel (weigh_tc.cu; bf16), weigh_kernel (fp32): else the scores are computed
+//   once more, keys at rest and rows going by, so that a key's sum stays in one block and
+//   its order is fixed.
+#include "weigh.cuh"
 
 namespace lora {
 namespace {
@@ -20,58 +21,6 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kTile = 32;              // cached tokens a tile, one a lane
 constexpr int kWarpRows = 4, kRows = kWarps * kWarpRows;
 
-// A block's part of the list whose places are (request, kv head, key tile, row tile): the key tiles that begin in it.
-struct KeyCursor {
-    Request r;
-    int s, head, tile, left;
-    __device__ __forceinline__ void start(const AttnParams &p, const ScanShared &sh, const Cursor &c) {
-        s = c.s;
-        left = 0;
-        if (s < 0) return;
-        r = sh.r;
-        const uint32_t each = (uint32_t)r.tiles * r.row_tiles, h = sh.residual / each, rest = sh.residual - h * each;
-        head = h;
-        tile = rest / (uint32_t)r.row_tiles;
-        left = c.left;
-        const int into = rest - (uint32_t)tile * r.row_tiles;
-        if (into) {                    // the tile began in an earlier block
-            left -= r.row_tiles - into;
-            next(p);
-        }
-    }
-    __device__ __forceinline__ void next(const AttnParams &p) {
-        if (++tile < r.tiles || left <= 0) return;
-        tile = 0;
-        if (++head < p.n_kv) return;
-        head = 0;
-        do {
-            if (++s >= p.S) {
-                left = 0;
-                return;
-            }
-            r = request_of(p, s);
-        } while (r.row_tiles == 0 || r.tiles == 0);
-    }
-    __device__ __forceinline__ void advance(const AttnParams &p) {
-        left -= r.row_tiles;
-        next(p);
-    }
-};
-
-// The weight's place of cached token c, -1 where its page is outside the cache (flagged).
-__device__ __forceinline__ long long weight_at(const AttnParams &p, int s, const Request &r, int head, int c) {
-    const int page = page_of(p, s, r, c);
-    if (page < 0 || page >= p.n_pages) {
-        flag_status(p.status, LORA_DEV_BAD_PAGE);
-        return -1;
-    }
-    return (((long long)page * p.n_kv + head) << p.page_shift) + (c & ((1 << p.page_shift) - 1));
-}
-
-__device__ __forceinline__ float as_float(float v) { return v; }
-__device__ __forceinline__ float as_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-template <typename E>
 __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, float *weights, float decay) {
     extern __shared__ __align__(16) float smem[];
     __shared__ ScanShared scan;
@@ -90,7 +39,7 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
         for (int x = tid; x < kTile * p.d; x += kThreads) {
             const int j = x / p.d, e = x - j * p.d;
             const long long slot = c0 + j < cur.r.len ? weight_at(p, cur.s, cur.r, cur.head, c0 + j) : -1;
-            ks[j * pitch + e] = slot >= 0 ? as_float(static_cast<const E *>(p.k)[slot * p.d + e]) : 0.f;
+            ks[j * pitch + e] = slot >= 0 ? static_cast<const float *>(p.k)[slot * p.d + e] : 0.f;
         }
         float acc = 0.f;
         for (int r0 = 0; r0 < rows; r0 += kRows) {
@@ -98,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
             for (int x = tid; x < kRows * p.d; x += kThreads) {
                 const int j = x / p.d, e = x - j * p.d, row = r0 + j, i = row / p.group;
                 const long long from = ((long long)(cur.r.begin + i) * p.n_q + cur.head * p.group + row - i * p.group) * p.d + e;
-                qs[j * pitch + e] = row < rows ? as_float(static_cast<const E *>(p.q)[from]) : 0.f;
+                qs[j * pitch + e] = row < rows ? static_cast<const float *>(p.q)[from] : 0.f;
             }
             __syncthreads();
             float dot[kWarpRows] = {};
@@ -190,20 +139,21 @@ namespace decode {
 int plan_weigh(const lora_kv_pages *kv, const AttnParams &attention, AttnParams &p) {
     p = attention;
     p.records = nullptr;
-    p.rt = p.scores ? 1 << 30 : kRows;         // kept scores: a tile's rows are one place
-    p.tk = p.scores ? kScoreTile : kTile;
+    const bool tc = !p.scores && kv->dtype == LORA_BF16;
+    p.rt = p.scores ? 1 << 30 : tc ? kWeighRows : kRows;         // kept scores: a tile's rows are one place
+    p.tk = p.scores ? kScoreTile : tc ? kWeighTile : kTile;
     p.tk_shift = log2_of(p.tk);
     p.unit_cost = 0;
     const long long tiles = (long long)p.max_pages * kv->page_size / p.tk + 1, units = (long long)p.T * p.group / p.rt + p.S;
     if (tiles * units > 0x7fffffffLL / p.n_kv) return LORA_ERR_SHAPE;
     p.max_places = (uint32_t)(tiles * units * p.n_kv);
-    p.grid = num_sms() * (p.scores ? 8 : 2);
+    p.grid = num_sms() * (p.scores ? 8 : tc ? 1 : 2);
     return LORA_OK;
 }
 
-int launch_weigh(const lora_kv_pages *kv, const AttnParams &p, float *weights, float decay, cudaStream_t st) {
-    void (*const kernel)(AttnParams, float *, float) = p.scores ? weigh_scores_kernel
-                                                       : kv->dtype == LORA_BF16 ? weigh_kernel<__nv_bfloat16> : weigh_kernel<float>;
+int launch_weigh(const lora_kv_pages *kv, const KvMaps *maps, const AttnParams &p, float *weights, float decay, cudaStream_t st) {
+    if (!p.scores && kv->dtype == LORA_BF16) return launch_weigh_tc(maps, p, weights, decay, st);
+    void (*const kernel)(AttnParams, float *, float) = p.scores ? weigh_scores_kernel : weigh_kernel;
     const size_t smem = p.scores ? 0 : (size_t)(kTile + kRows) * (p.d + 4) * sizeof(float);
     if (smem && smem_optin(reinterpret_cast<const void *>(kernel), smem)) return LORA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
