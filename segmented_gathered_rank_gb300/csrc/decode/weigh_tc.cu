@@ -19,8 +19,8 @@ using namespace decode;
 using namespace tc;
 
 constexpr int kTile = 128;                          // keys a group, rows a query tile
-constexpr int kConsumers = 8, kThreads = 12 * 32;   // warps 8 and 9 copy keys, 10 issues products, 11 copies queries
-constexpr int kKeyWarp = 8, kMmaWarp = 10;
+constexpr int kConsumers = 8, kThreads = 16 * 32;   // warps 8 and 9 copy keys, 10 issues products, 12 to 15 copy queries
+constexpr int kKeyWarp = 8, kMmaWarp = 10, kQueryWarp = 12;
 constexpr uint32_t kTmemCols = 512;
 
 // D: head width padded to 64, 128 or 256.
@@ -113,12 +113,12 @@ __device__ void copy_keys(const AttnParams &p, const KvMaps &maps, KeyCursor cur
     }
 }
 
-// One warp, D / 8 lanes a row; rows past the request become zeros.
+// Four warps of 32 rows, D / 8 lanes a row; rows past the request become zeros.
 template <int D>
 __device__ void copy_queries(const AttnParams &p, KeyCursor cur, uint8_t *ring, Control<D> &ctl) {
     using Sh = Shape<D>;
     constexpr int kLanes = D / 8, kRows = 32 / kLanes;
-    const int lane = threadIdx.x & 31, chunk = lane % kLanes;
+    const int lane = threadIdx.x & 31, chunk = lane % kLanes, row0 = (threadIdx.x >> 5) * 32 - kQueryWarp * 32;
     const bool inside = chunk * 8 < ((p.d + 15) & ~15), real_chunk = chunk * 8 < p.d;
     uint32_t seq = 0;
     while (cur.left > 0) {
@@ -131,20 +131,19 @@ __device__ void copy_queries(const AttnParams &p, KeyCursor cur, uint8_t *ring, 
             const uint32_t slot = seq % Sh::kQueries, use = seq / Sh::kQueries;
             if (!wait_warp<D>(&ctl.q_empty[slot], (use & 1) ^ 1, ctl)) return;
             const uint32_t dst = smem_u32(ring) + slot * Sh::kBytes, sums = smem_u32(ctl.lse[slot]);
-            for (int j = lane; j < kTile; j += 32) {
-                const int row = row_tile * kTile + j, i = row / p.group;
-                const float *src = row < rows ? p.lse + first + (long long)i * (p.n_q - p.group) + row : p.lse;
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(sums + j * 4), "l"(src), "r"(row < rows ? 4 : 0)
-                             : "memory");
-            }
-            if (inside) {
-#pragma unroll 8
-                for (int j = lane / kLanes; j < kTile; j += kRows) {
-                    const int row = row_tile * kTile + j, i = row / p.group;
-                    const bool real = row < rows && real_chunk;
-                    const long long off = real ? (first + (long long)i * (p.n_q - p.group) + row) * p.d + chunk * 8 : 0;
-                    cp_async16(dst + panel_off(kTile, j, chunk), static_cast<const __nv_bfloat16 *>(p.q) + off, real);
-                }
+            const int row = row_tile * kTile + row0 + lane, i = row / p.group;
+            const long long line = row < rows ? first + (long long)i * (p.n_q - p.group) + row : -1;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(sums + (row0 + lane) * 4), "l"(p.lse + max(line, 0ll)),
+                         "r"(line >= 0 ? 4 : 0)
+                         : "memory");
+#pragma unroll
+            for (int j = 0; j < 32; j += kRows) {
+                const int r = j + lane / kLanes;
+                const long long from = __shfl_sync(0xffffffffu, line, r);
+                const bool real = from >= 0 && real_chunk;
+                if (inside)
+                    cp_async16(dst + panel_off(kTile, row0 + r, chunk), static_cast<const __nv_bfloat16 *>(p.q) + (real ? from * p.d + chunk * 8 : 0),
+                               real);
             }
             cp_arrive(&ctl.q_full[slot]);
             if (++row_tile == cur.r.row_tiles) row_tile = 0;
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctl.k_empty[i], 1);
         }
         for (int i = 0; i < Sh::kQueries; ++i) {
-            mbar_init(&ctl.q_full[i], 32);
+            mbar_init(&ctl.q_full[i], 128);
             mbar_init(&ctl.q_empty[i], 1 + kConsumers);
         }
         for (int w = 0; w < 2; ++w)
@@ -327,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait_phase(&ctl.drain, 0, nullptr);
         }
         __syncwarp();
-    } else {
+    } else if (warp >= kQueryWarp) {
         copy_queries<D>(p, cur, queries, ctl);
         cp_wait_all();
     }
