@@ -453,7 +453,7 @@ int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, c
  * without drafted tokens, and of slots past a request, are left as they were.  out is
  * lora_tree_attention's, bit for bit.
  *   weights  n_pages x n_kv_heads x page_size fp32, slots as the cache's, 16-byte
- *            aligned.   decay  0..1.
+ *            aligned.   decay  0..1.   out  apart from q.
  *   workspace  lora_tree_attention_weights_workspace_size() bytes; it grows with S, T
  *            and max_pages, and one of the largest call serves every smaller one.
  * A page that several requests of the call share ends up with either's weights.  A

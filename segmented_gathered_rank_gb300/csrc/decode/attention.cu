@@ -827,6 +827,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few
 template <typename E>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p) {
     const int c = blockIdx.x, lane = threadIdx.x & 31;
+    if (p.lse) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");       // the weights' kernel, which waits as well
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const JoinRecord rec = p.records[c];
     const int across = (p.d + 15) >> 4, pieces = ((rec.rows + 7) >> 3) * across;
@@ -1027,6 +1028,9 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
     if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || ((uintptr_t)tree_mask & 7u) ||
         (((uintptr_t)seg_starts | (uintptr_t)kv_lens | (uintptr_t)page_table) & 3u))
         return LORA_ERR_ARG;
+    // the weights' kernel reads q again
+    const size_t q_bytes = (size_t)T * n_q_heads * kv->head_dim * (kv->dtype == LORA_BF16 ? 2 : 4);
+    if (weights && overlap(q, q_bytes, out, q_bytes)) return LORA_ERR_ARG;
     if (num_sms() < 1) return LORA_ERR_CUDA;
     const Variant variant = variant_of(kv, n_q_heads / kv->n_kv_heads, S, T);
     const bool keep = weights && keeps_scores(n_q_heads / kv->n_kv_heads, S, T);

@@ -22,6 +22,11 @@ inline int check_kv(const lora_kv_pages *kv, int n_q_heads) {
     return LORA_OK;
 }
 
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + nb && y < x + na;
+}
+
 inline int log2_of(int power_of_two) {
     int n = 0;
     while ((1 << n) < power_of_two) ++n;

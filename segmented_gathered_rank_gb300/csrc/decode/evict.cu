@@ -281,11 +281,6 @@ int cluster_of(int S, int n_kv) {
     return n;
 }
 
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + nb && y < x + na;
-}
-
 }  // namespace
 }  // namespace lora
 

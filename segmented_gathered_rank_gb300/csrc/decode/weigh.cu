@@ -28,10 +28,9 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pitch = p.d + 4;
     float *ks = smem, *qs = smem + kTile * pitch;
     Cursor at;
-    start_block(p, scan, at);
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     KeyCursor cur;
-    cur.start(p, scan, at);
+    cur.start(p, scan, start_block(p, scan, at));
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (!*p.computed) return;
     for (; cur.left > 0; cur.advance(p)) {
         const int c0 = cur.tile * kTile, rows = cur.r.n * p.group;
@@ -88,10 +87,9 @@ constexpr int kScoreTile = 1024;       // cached tokens a tile, four a thread
 __global__ void __launch_bounds__(kThreads) weigh_scores_kernel(const AttnParams p, float *weights, float decay) {
     __shared__ ScanShared scan;
     Cursor at;
-    start_block(p, scan, at);
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     KeyCursor cur;
-    cur.start(p, scan, at);
+    cur.start(p, scan, start_block(p, scan, at));
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (!*p.computed) return;
     for (; cur.left > 0; cur.advance(p)) {
         const int c = cur.tile * kScoreTile + threadIdx.x * 4, rows = cur.r.n * p.group;
@@ -143,8 +141,8 @@ int plan_weigh(const lora_kv_pages *kv, const AttnParams &attention, AttnParams 
     p.rt = p.scores ? 1 << 30 : tc ? kWeighRows : kRows;         // kept scores: a tile's rows are one place
     p.tk = p.scores ? kScoreTile : tc ? kWeighTile : kTile;
     p.tk_shift = log2_of(p.tk);
-    p.unit_cost = 0;
-    const long long tiles = (long long)p.max_pages * kv->page_size / p.tk + 1, units = (long long)p.T * p.group / p.rt + p.S;
+    p.unit_cost = tc ? kWeighUnitCost : 0;
+    const long long tiles = (long long)p.max_pages * kv->page_size / p.tk + 1 + p.unit_cost, units = (long long)p.T * p.group / p.rt + p.S;
     if (tiles * units > 0x7fffffffLL / p.n_kv) return LORA_ERR_SHAPE;
     p.max_places = (uint32_t)(tiles * units * p.n_kv);
     p.grid = num_sms() * (p.scores ? 8 : tc ? 1 : 2);

@@ -7,19 +7,22 @@ namespace lora {
 namespace decode {
 
 // A block's part of the list whose places are (request, kv head, key tile, row tile): the key tiles that begin in it.
+// A kv head has unit_cost * row_tiles empty places before its first.
 struct KeyCursor {
     Request r;
     int s, head, tile, left;
-    __device__ __forceinline__ void start(const AttnParams &p, const ScanShared &sh, const Cursor &c) {
-        s = c.s;
+    __device__ __forceinline__ void start(const AttnParams &p, const ScanShared &sh, uint32_t total) {
+        s = sh.request;
         left = 0;
         if (s < 0) return;
         r = sh.r;
-        const uint32_t each = (uint32_t)r.tiles * r.row_tiles, h = sh.residual / each, rest = sh.residual - h * each;
+        left = (int)(block_begin(total, blockIdx.x + 1, p.grid) - block_begin(total, blockIdx.x, p.grid));
+        const uint32_t each = (uint32_t)(r.tiles + p.unit_cost) * r.row_tiles, h = sh.residual / each;
+        const int place = (int)(sh.residual - h * each) - p.unit_cost * r.row_tiles;       // below 0: before the first tile
         head = h;
-        tile = rest / (uint32_t)r.row_tiles;
-        left = c.left;
-        const int into = rest - (uint32_t)tile * r.row_tiles;
+        tile = max(place, 0) / r.row_tiles;
+        left += min(place, 0);
+        const int into = max(place, 0) - tile * r.row_tiles;
         if (into) {                    // the tile began in an earlier block
             left -= r.row_tiles - into;
             next(p);
@@ -28,15 +31,17 @@ struct KeyCursor {
     __device__ __forceinline__ void next(const AttnParams &p) {
         if (++tile < r.tiles || left <= 0) return;
         tile = 0;
-        if (++head < p.n_kv) return;
-        head = 0;
-        do {
-            if (++s >= p.S) {
-                left = 0;
-                return;
-            }
-            r = request_of(p, s);
-        } while (r.row_tiles == 0 || r.tiles == 0);
+        if (++head >= p.n_kv) {
+            head = 0;
+            do {
+                if (++s >= p.S) {
+                    left = 0;
+                    return;
+                }
+                r = request_of(p, s);
+            } while (r.row_tiles == 0 || r.tiles == 0);
+        }
+        left -= p.unit_cost * r.row_tiles;
     }
     __device__ __forceinline__ void advance(const AttnParams &p) { advance(p, 1); }
     // Past `count` key tiles of the kv head.
@@ -60,6 +65,9 @@ __device__ __forceinline__ long long weight_at(const AttnParams &p, int s, const
 }
 
 constexpr int kWeighTile = 256, kWeighRows = 128;      // of weigh_tc_kernel: cached tokens a tile, rows a place of the list
+
+// In places of all rows: what starting a kv head costs.
+constexpr int kWeighUnitCost = 1;
 
 // weigh_tc.cu: a bf16 cache; maps as for launch_attention_tc.
 int launch_weigh_tc(const KvMaps *maps, const AttnParams &p, float *weights, float decay, cudaStream_t st);

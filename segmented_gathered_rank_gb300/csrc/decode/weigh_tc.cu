@@ -6,7 +6,8 @@
 // key tiles of 128, one a group of four warps, against the same tiles of 128 rows; each
 // group has two tiles of scores in tensor memory, so that products run under the
 // exponentials.  Rows that fit in the ring of query tiles stay in it for all key tiles of
-// a kv head.
+// a kv head.  Keys are copied while the attention's last kernel runs; what reads its sums
+// waits for it.
 #include <type_traits>
 
 #include "kv_copy.cuh"
@@ -28,7 +29,7 @@ template <int D>
 struct Shape {
     static constexpr int kBytes = kTile * D * 2;            // a tile of keys or queries
     static constexpr int kKeys = D == 256 ? 1 : 2;          // pairs of key tiles
-    static constexpr int kQueries = D == 64 ? 6 : D == 128 ? 2 : 1;
+    static constexpr int kQueries = D == 64 ? 6 : D == 128 ? 3 : 1;
     static constexpr size_t kSmem = (size_t)(2 * kKeys + kQueries) * kBytes + 1024;
 };
 
@@ -121,6 +122,7 @@ __device__ void copy_queries(const AttnParams &p, KeyCursor cur, uint8_t *ring, 
     const int lane = threadIdx.x & 31, chunk = lane % kLanes, row0 = (threadIdx.x >> 5) * 32 - kQueryWarp * 32;
     const bool inside = chunk * 8 < ((p.d + 15) & ~15), real_chunk = chunk * 8 < p.d;
     uint32_t seq = 0;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");       // lse
     while (cur.left > 0) {
         const Run run(cur, Sh::kQueries);
         const int rows = cur.r.n * p.group;
@@ -211,6 +213,8 @@ __device__ void consume(const AttnParams &p, KeyCursor cur, float *weights, floa
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp >> 2;
     const uint32_t tmem = ctl.tmem + ((uint32_t)((warp & 3) * 32) << 16) + w * 2 * kTile;
     uint32_t q0 = 0, s_seq = 0;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const bool computed = *p.computed != 0;
     while (cur.left > 0) {
         const Run run(cur, Sh::kQueries);
         const int rows = cur.r.n * p.group, prefix = cur.r.len - cur.r.n;
@@ -220,7 +224,7 @@ __device__ void consume(const AttnParams &p, KeyCursor cur, float *weights, floa
             const bool active = g0 < cur.r.len;
             long long slot = -1;
             float old = 0.f;
-            if (c < cur.r.len) slot = weight_at(p, cur.s, cur.r, cur.head, c);
+            if (c < cur.r.len && computed) slot = weight_at(p, cur.s, cur.r, cur.head, c);
             if (slot >= 0 && decay > 0.f && c < prefix) old = weights[slot];
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             for (int row_tile = 0; row_tile < cur.r.row_tiles; ++row_tile) {
@@ -283,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ Control<D> ctl;
     uint8_t *keys = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023), *queries = keys + 2 * Sh::kKeys * Sh::kBytes;
     const int warp = threadIdx.x >> 5;
+    if (TMA && threadIdx.x == kKeyWarp * 32) prefetch_tmap(&maps.k);
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kKeys; ++i) {
             for (int w = 0; w < 2; ++w) mbar_init(&ctl.k_full[i][w], TMA ? 1 : 64);
@@ -302,11 +307,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_fence_init();
     }
     Cursor at;
-    start_block(p, scan, at);
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
     KeyCursor cur;
-    cur.start(p, scan, at);
-    if (cur.left <= 0 || !*p.computed) return;          // the whole block
+    cur.start(p, scan, start_block(p, scan, at));
+    if (cur.left <= 0) return;          // the whole block
     if (warp == kMmaWarp) {
         tmem_alloc(&ctl.tmem, kTmemCols);
         tmem_relinquish();

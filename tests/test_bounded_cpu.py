@@ -107,6 +107,7 @@ def test_planes_that_are_too_small_are_refused_in_python():
 
 def weigh(kv, weights=P, decay=1.0, q=P, n_q=4, starts=P, S=2, T=2, lens=P, table=P, max_pages=4, mask=None, words=0, scale=0.1, out=P,
           workspace=P, ws_bytes=1 << 30):
+    out = P + (1 << 13) if out == P else out
     return L._lib.lora_tree_attention_weights(ctypes.byref(kv), weights, decay, q, n_q, starts, S, T, lens, table, max_pages, mask, words,
                                               scale, out, workspace, ws_bytes, None)
 
@@ -126,6 +127,7 @@ def test_attention_weights_refuses_pages(change, code):
     (dict(max_pages=-1), L.LORA_ERR_ARG), (dict(max_pages=0), L.LORA_ERR_ARG), (dict(mask=P), L.LORA_ERR_ARG),
     (dict(mask=P + 4, words=1), L.LORA_ERR_ARG), (dict(q=P + 8), L.LORA_ERR_ARG), (dict(out=None), L.LORA_ERR_ARG),
     (dict(starts=P + 2), L.LORA_ERR_ARG), (dict(lens=None), L.LORA_ERR_ARG), (dict(table=None), L.LORA_ERR_ARG),
+    (dict(out=P + 16), L.LORA_ERR_ARG), (dict(out=P + 2 * 4 * 128 * 2 - 16), L.LORA_ERR_ARG),       # over q
     (dict(workspace=None), L.LORA_ERR_ARG), (dict(workspace=P + 8), L.LORA_ERR_ARG), (dict(max_pages=1 << 28), L.LORA_ERR_SHAPE)])
 def test_attention_weights_refuses(change, code):
     before = L.lora_launch_count()
