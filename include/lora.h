@@ -476,8 +476,8 @@ int lora_tree_attention_weights(const lora_kv_pages *kv, float *weights, float d
  * keep[s] - 1, and new_lens[s] = keep[s]; places from there on are left as they
  * are.  Other requests (and those with keep[s] < 0) stay as they are, and
  * new_lens[s] = kv_lens[s].
- *   scores    n_pages x n_kv_heads x page_size fp32, slots as the cache's; -0 equals
- *             0, a NaN is below everything.
+ *   scores    n_pages x n_kv_heads x page_size fp32, slots as the cache's, 16-byte
+ *             aligned; -0 equals 0, a NaN is below everything.
  *   weights   the same layout, moved with the tokens; may be scores (else they do not
  *             overlap), or NULL.
  *   keep      S device int32.

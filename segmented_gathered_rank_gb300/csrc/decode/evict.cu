@@ -4,16 +4,19 @@
 // last `recent` stay, and of those between the k = keep - first - recent with the greatest
 // (f_c, -c); the kept ones move, in order, to places 0 .. keep - 1.
 //
-// One cluster of blocks a (request, kv head):
-//   select   scores become whole numbers that order as they do (NaN lowest), 4 bytes a token
-//            in shared memory; the k-th greatest is found 11 bits at a time from the top, by
-//            counts that the cluster's blocks add up; ties are cut by their rank in the row.
-//   list     a warp counts its tokens that stay, the cluster scans the counts, and the
-//            sources of the kept tokens are written in order.
-//   move     a token's source is never before its destination, so a round of destinations
-//            [j, j + n) is read whole, the cluster waits, and it is written: what a round
-//            overwrites, no later round reads.  Tokens before the first evicted one stay.
-#include "decode.cuh"
+// evict_select_kernel, a cluster (or one block) a (request, kv head) that loses tokens:
+//   scores become whole numbers that order as they do (NaN lowest), 4 bytes a token in shared
+//   memory; the k-th greatest is found 11 bits at a time from the top.  Up to kSolo tokens
+//   one block does that, as waiting for one another costs more than it saves; of more, each
+//   block has its share, and counts are added up.  Then a warp counts its tokens that stay,
+//   the counts are scanned, and the sources of the kept tokens are written in order (ties by
+//   their rank in the row).
+// evict_move_kernel, a block a column range of one plane (keys, values, weights) of a pair:
+//   a token's source is never before its destination, so a round of destinations
+//   [j, j + n) is read whole before it is written: what a round overwrites, no later round
+//   reads.  Column ranges move apart from one another, so blocks never wait for one another,
+//   and the next rounds are on their way while one is written.
+#include "kv_copy.cuh"
 
 namespace lora {
 namespace {
@@ -23,7 +26,15 @@ using namespace decode;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBits = 11, kBins = 1 << kBits;
 constexpr int kMaxCluster = 8;
+constexpr int kSolo = 8192;
 constexpr int kMaxHeld = 16384;       // scores a block keeps in shared memory; more are read again
+
+constexpr int kMoveThreads = 256;
+constexpr int kPieces = 8, kStages = 3;               // 16-byte pieces a thread and round; rounds in shared memory
+constexpr int kSlotRounds = 4;
+constexpr int kMovePerSm = 2;
+constexpr int kSliceChunks = 8;       // at most, of 16 bytes
+constexpr size_t kMoveSmem = (size_t)kStages * kPieces * kMoveThreads * 16;
 
 struct EvictParams {
     char *k, *v;
@@ -32,15 +43,16 @@ struct EvictParams {
     int S, n_kv, n_pages, page_shift, max_pages, row_bytes;
     const int *lens, *table, *keep;
     int first, recent, ld_kept, held;
+    int slices;                       // column ranges of a row of keys (and of values)
     int *kept, *new_lens, *status;
 };
 
-struct Shared {
+struct __align__(16) Shared {
     uint32_t bins[kBins];             // this block's counts, read by its cluster
     uint32_t scan[kWarps];
     uint32_t sure[kWarps], equal[kWarps];     // tokens of each warp above the cut, and at it
-    uint32_t block_sure, block_equal, bad, hole;
-    uint32_t cut, wanted;             // key of the last kept token; how many of that key are kept
+    uint32_t block_sure, block_equal, bad;
+    uint32_t cut, wanted, inside;     // a pass's bin: its keys' upper bits, how many are wanted of it, how many it has
 };
 
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -57,11 +69,23 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ uint32_t peer_load(const uint32_t *mine, uint32_t rank) {
-    uint32_t addr, value;
+__device__ __forceinline__ uint32_t peer_addr(const uint32_t *mine, uint32_t rank) {
+    uint32_t addr;
     asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(addr) : "r"((uint32_t)__cvta_generic_to_shared(mine)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(value) : "r"(addr) : "memory");
+    return addr;
+}
+// Each lane's peer has a value (lanes from `blocks` on: 0); volatile, so that loads are on their way together.
+__device__ __forceinline__ uint32_t peer_values(const uint32_t *mine, uint32_t blocks) {
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t value = 0;
+    if (lane < blocks) asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(value) : "r"(peer_addr(mine, lane)));
+    __syncwarp();
     return value;
+}
+__device__ __forceinline__ uint4 peer_load4(const uint32_t *mine, uint32_t rank) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(peer_addr(mine, rank)));
+    return v;
 }
 
 // Orders as the scores do; -0 is 0, a NaN is below everything.
@@ -79,89 +103,115 @@ struct Row {                          // one request and kv head
     }
 };
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
-    extern __shared__ uint32_t keys[];
-    __shared__ Shared sh;
+// Inclusive sum over the warp.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t other = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += other;
+    }
+    return v;
+}
+
+// Whether a request loses tokens; bad: its length or budget is beyond its table.
+__device__ __forceinline__ bool loses(const EvictParams &p, int len, int keep, bool &bad) {
+    const bool shorter = keep >= 0 && len > keep;
+    bad = len < 0 || len > ((long long)p.max_pages << p.page_shift) || (shorter && keep > p.ld_kept);
+    return shorter && !bad;
+}
+
+// The sources of one request and kv head.
+__device__ void select(const EvictParams &p, Shared &sh, uint32_t *keys, int s, int head, uint32_t blocks, uint32_t rank) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t blocks = cluster_size(), rank = cluster_rank();
-    const int unit = blockIdx.x / blocks, s = unit / p.n_kv, head = unit - s * p.n_kv;
-    const long long cap = (long long)p.max_pages << p.page_shift;
     const int len = p.lens[s], keep = p.keep[s];
-    if (len < 0 || len > cap || (keep >= 0 && len > keep && keep > p.ld_kept)) {
-        // a length that the table does not hold, a budget that `kept` does not: the request stays as it is
-        if (head == 0 && rank == 0 && tid == 0) {
-            flag_status(p.status, LORA_DEV_BAD_LENGTH);
-            p.new_lens[s] = len;
-        }
-        return;
-    }
-    if (keep < 0 || len <= keep) {
-        if (head == 0 && rank == 0 && tid == 0) p.new_lens[s] = len;
-        return;
-    }
     const Row row = {p.table + (long long)s * p.max_pages, head};
     const int recent = min(p.recent, keep), first = min(p.first, keep - recent);
     const int last = len - recent;                                  // tokens from here on stay
+    const bool solo = len <= kSolo || blocks == 1;
+    if (solo && rank) return;
     // this block's tokens, and of those this warp's
-    const int each = (((len + blocks - 1) / blocks) + 31) & ~31;
-    const int lo = min(len, (int)rank * each), hi = min(len, lo + each);
-    const int per_warp = ((each / 32 + kWarps - 1) / kWarps) * 32;
+    const int each = solo ? len : (((len + blocks - 1) / blocks) + 31) & ~31;
+    const int lo = solo ? 0 : min(len, (int)rank * each), hi = min(len, lo + each), held = min(hi, lo + p.held);
+    const int per_warp = (((each + 31) / 32 + kWarps - 1) / kWarps) * 32;
     const int w_lo = min(hi, lo + warp * per_warp), w_hi = min(hi, w_lo + per_warp);
 
-    // a page outside the cache: the request stays as it is
-    if (tid == 0) sh.bad = 0;
-    __syncthreads();
-    const int pages = (len + (1 << p.page_shift) - 1) >> p.page_shift;
+    __syncthreads();                  // the unit before has read what is written here
     bool bad = false;
-    for (int x = tid; x < pages; x += kThreads) {
+    for (int x = (lo >> p.page_shift) + tid; x < (hi + (1 << p.page_shift) - 1) >> p.page_shift; x += kThreads) {
         const int page = __ldg(row.table + x);
         bad |= page < 0 || page >= p.n_pages;
     }
-    if (__syncthreads_or(bad)) {            // every block of every head of the request finds the same
+    bad = __syncthreads_or(bad);
+    if (!solo) {                      // a page outside the cache: the request stays as it is, whichever block sees it
+        if (tid == 0) sh.bad = bad;
+        cluster_sync();
+        bad = __any_sync(0xffffffffu, peer_values(&sh.bad, blocks) != 0);
+        cluster_sync();
+    }
+    if (bad) {
         if (head == 0 && rank == 0 && tid == 0) {
             flag_status(p.status, LORA_DEV_BAD_PAGE);
             p.new_lens[s] = len;
         }
         return;
     }
-    for (int c = lo + tid; c < min(hi, lo + p.held); c += kThreads) keys[c - lo] = key_of(p.scores[row.slot(p, c)]);
-    auto key_at = [&](int c) { return c - lo < p.held ? keys[c - lo] : key_of(p.scores[row.slot(p, c)]); };
-
-    // the k-th greatest key of the tokens that compete
-    uint32_t wanted = keep - first - recent, known = 0, mask = 0;
-    if (wanted == 0) {
-        known = mask = ~0u;                 // nobody: no key is above, and of those equal none is wanted
-        __syncthreads();
+    if (p.page_shift >= 2) {
+#pragma unroll 4
+        for (int c = lo + tid * 4; c < held; c += kThreads * 4) {
+            const int at = row.slot(p, c);
+            if (c + 4 <= held) {
+                const float4 f = *reinterpret_cast<const float4 *>(p.scores + at);
+                *reinterpret_cast<uint4 *>(keys + (c - lo)) = make_uint4(key_of(f.x), key_of(f.y), key_of(f.z), key_of(f.w));
+            } else {
+                for (int x = 0; c + x < held; ++x) keys[c + x - lo] = key_of(p.scores[at + x]);
+            }
+        }
+    } else {
+#pragma unroll 4
+        for (int c = lo + tid; c < held; c += kThreads) keys[c - lo] = key_of(p.scores[row.slot(p, c)]);
     }
-    for (int shift = 32 - kBits; wanted && mask != ~0u; shift = max(0, shift - kBits)) {
+    auto key_at = [&](int c) { return c < held ? keys[c - lo] : key_of(p.scores[row.slot(p, c)]); };
+
+    // the k-th greatest key of the tokens that compete: its upper bits as far as they are needed
+    uint32_t wanted = keep - first - recent, cut = 0, mask = 0;
+    if (wanted == 0) cut = mask = ~0u;       // nobody: no key is above, and of those equal none is wanted
+    for (int shift = 32 - kBits; mask != ~0u; shift = max(0, shift - kBits)) {
         const int width = shift == 0 ? 32 - 2 * kBits : kBits, bins = 1 << width;
         for (int x = tid; x < bins; x += kThreads) sh.bins[x] = 0;
         if (tid == 0) {
-            sh.cut = known;
-            sh.wanted = wanted;
+            sh.cut = cut;
+            sh.wanted = sh.inside = wanted;
         }
         __syncthreads();
         for (int c = max(lo, first) + tid; c < min(hi, last); c += kThreads) {
             const uint32_t key = key_at(c);
-            if ((key & mask) == known) atomicAdd(&sh.bins[(key >> shift) & (bins - 1)], 1u);
+            if ((key & mask) == cut) atomicAdd(&sh.bins[(key >> shift) & (bins - 1)], 1u);
         }
-        cluster_sync();
+        if (solo) __syncthreads();
+        else cluster_sync();
         // from the top bin down: the bin in which the count passes `wanted`
-        const int per = bins / kThreads;    // 4 or 2 bins a thread, from the top
-        uint32_t mine[kBins / kThreads], sum = 0;
+        constexpr int kPer = kBins / kThreads;      // 4 bins a thread, side by side (of fewer bins: the lower threads')
+        const int low = bins - kPer * (tid + 1);
+        uint32_t mine[kPer] = {}, sum = 0;          // from the thread's top bin down
+        if (low >= 0) {
+            uint4 part[kMaxCluster];
 #pragma unroll
-        for (int x = 0; x < kBins / kThreads; ++x) {
-            mine[x] = 0;
-            if (x < per)
-                for (uint32_t r = 0; r < blocks; ++r) mine[x] += peer_load(&sh.bins[bins - 1 - (tid * per + x)], r);
-            sum += mine[x];
-        }
-        uint32_t upto = sum;
+            for (uint32_t r = 0; r < kMaxCluster; ++r) {
+                part[r] = make_uint4(0, 0, 0, 0);
+                if (solo ? r == 0 : r < blocks)
+                    part[r] = solo ? *reinterpret_cast<const uint4 *>(sh.bins + low) : peer_load4(sh.bins + low, r);
+            }
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t other = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += other;
+            for (uint32_t r = 0; r < kMaxCluster; ++r) {
+                mine[0] += part[r].w;
+                mine[1] += part[r].z;
+                mine[2] += part[r].y;
+                mine[3] += part[r].x;
+            }
+            sum = mine[0] + mine[1] + mine[2] + mine[3];
         }
+        const uint32_t upto = warp_scan(sum);
         if (lane == 31) sh.scan[warp] = upto;
         __syncthreads();
         uint32_t before = upto - sum;
@@ -169,26 +219,30 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
         for (int w = 0; w < kWarps; ++w)
             if (w < warp) before += sh.scan[w];
 #pragma unroll
-        for (int x = 0; x < kBins / kThreads; ++x) {
-            if (x < per && before < wanted && before + mine[x] >= wanted) {
-                sh.cut = known | (uint32_t)(bins - 1 - (tid * per + x)) << shift;
+        for (int x = 0; x < kPer; ++x) {
+            if (before < wanted && before + mine[x] >= wanted) {
+                sh.cut = cut | (uint32_t)(low + kPer - 1 - x) << shift;
                 sh.wanted = wanted - before;
+                sh.inside = mine[x];
             }
             before += mine[x];
         }
-        cluster_sync();                     // also: the peers have read this block's bins
-        known = sh.cut;
+        if (solo) __syncthreads();
+        else cluster_sync();                // also: the peers have read this block's bins
+        cut = sh.cut;
         wanted = sh.wanted;
         mask |= (uint32_t)(bins - 1) << shift;
+        const bool all = sh.inside == wanted;       // the whole bin stays: its keys need no order
+        __syncthreads();
+        if (all) break;
     }
-    const uint32_t cut = known;
 
     // how many stay before each warp's tokens
     uint32_t sure = 0, equal = 0;
     for (int c0 = w_lo; c0 < w_hi; c0 += 32) {
         const int c = c0 + lane;
         const bool in = c < w_hi, safe = in && (c < first || c >= last);
-        const uint32_t key = in ? key_at(c) : 0u;
+        const uint32_t key = in ? key_at(c) & mask : 0u;
         sure += __popc(__ballot_sync(0xffffffffu, safe || (in && key > cut)));
         equal += __popc(__ballot_sync(0xffffffffu, in && !safe && key == cut));
     }
@@ -196,22 +250,21 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
         sh.sure[warp] = sure;
         sh.equal[warp] = equal;
     }
-    if (tid == 0) sh.hole = 0xffffffffu;
     __syncthreads();
-    if (tid == 0) {
-        uint32_t a = 0, b = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            a += sh.sure[w];
-            b += sh.equal[w];
-        }
-        sh.block_sure = a;
-        sh.block_equal = b;
-    }
-    cluster_sync();
     uint32_t sure_before = 0, equal_before = 0;
-    for (uint32_t r = 0; r < rank; ++r) {
-        sure_before += peer_load(&sh.block_sure, r);
-        equal_before += peer_load(&sh.block_equal, r);
+    if (!solo) {
+        if (tid == 0) {
+            uint32_t a = 0, b = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                a += sh.sure[w];
+                b += sh.equal[w];
+            }
+            sh.block_sure = a;
+            sh.block_equal = b;
+        }
+        cluster_sync();
+        sure_before = __reduce_add_sync(0xffffffffu, peer_values(&sh.block_sure, rank));
+        equal_before = __reduce_add_sync(0xffffffffu, peer_values(&sh.block_equal, rank));
     }
     for (int w = 0; w < warp; ++w) {
         sure_before += sh.sure[w];
@@ -219,66 +272,176 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p) {
     }
     // the sources of the kept tokens, in order
     int *kept = p.kept + ((long long)s * p.n_kv + head) * p.ld_kept;
-    uint32_t hole = 0xffffffffu;
     for (int c0 = w_lo; c0 < w_hi; c0 += 32) {
         const int c = c0 + lane;
         const bool in = c < w_hi, safe = in && (c < first || c >= last);
-        const uint32_t key = in ? key_at(c) : 0u;
+        const uint32_t key = in ? key_at(c) & mask : 0u;
         const uint32_t above = __ballot_sync(0xffffffffu, safe || (in && key > cut));
         const uint32_t at = __ballot_sync(0xffffffffu, in && !safe && key == cut), before = (1u << lane) - 1;
         const uint32_t rank_at = equal_before + __popc(at & before);
         const uint32_t place = sure_before + __popc(above & before) + min(rank_at, wanted);
-        if (((above >> lane) & 1) || (((at >> lane) & 1) && rank_at < wanted)) {
-            if (place < (uint32_t)keep) kept[place] = c;       // always, unless scores change under the call
-        } else if (in) hole = min(hole, (uint32_t)c);
+        const bool stays = ((above >> lane) & 1) || (((at >> lane) & 1) && rank_at < wanted);
+        if (stays && place < (uint32_t)keep) kept[place] = c;       // below keep always, unless scores change under the call
         sure_before += __popc(above);
         equal_before += __popc(at);
     }
-    hole = __reduce_min_sync(0xffffffffu, hole);
-    if (lane == 0 && hole != 0xffffffffu) atomicMin(&sh.hole, hole);
-    cluster_sync();                          // the list is complete, and the scores have been read
-    uint32_t from = 0xffffffffu;
-    for (uint32_t r = 0; r < blocks; ++r) from = min(from, peer_load(&sh.hole, r));
-    cluster_sync();                          // no block leaves while its shared memory is read
     if (rank == 0 && head == 0 && tid == 0) p.new_lens[s] = keep;
+    if (!solo) cluster_sync();               // no block goes on while its shared memory is read
+}
 
-    // the move, up to 32 KB of keys and as much of values a block and round
-    auto source = [&](int j) { return (int)min((uint32_t)kept[j], (uint32_t)len - 1); };
-    constexpr int kPieces = 4;
-    const int chunks = p.row_bytes >> 4, rows = min(kThreads, kThreads * kPieces / chunks);
-    for (long long j0 = from; j0 < keep; j0 += (long long)rows * blocks) {
-        uint4 k[kPieces], v[kPieces];
-        float w = 0.f;
-        const int begin = (int)min((long long)keep, j0 + (long long)rank * rows), count = min(rows, keep - begin);
-#pragma unroll
-        for (int x = 0; x < kPieces; ++x) {
-            const int piece = x * kThreads + tid, j = piece / chunks;
-            if (j < count) {
-                const long long at = (long long)row.slot(p, source(begin + j)) * p.row_bytes + (piece - j * chunks) * 16;
-                k[x] = *reinterpret_cast<const uint4 *>(p.k + at);
-                v[x] = *reinterpret_cast<const uint4 *>(p.v + at);
-            }
+// Calls f(request, unit of n a request) for every gridDim-th (of `workers`) unit of the requests for which active(s) holds.
+template <int THREADS, typename A, typename F>
+__device__ __forceinline__ void in_turn(int S, int n, int worker, int workers, A active, F f) {
+    __shared__ int requests[THREADS], counts[THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long turn = worker;                  // units until this worker's next one
+    for (int s0 = 0; s0 < S; s0 += THREADS) {
+        const int s = s0 + tid;
+        const bool mine = s < S && active(s);
+        const uint32_t on = __ballot_sync(0xffffffffu, mine);
+        __syncthreads();
+        if (lane == 0) counts[warp] = __popc(on);
+        __syncthreads();
+        int at = __popc(on & ((1u << lane) - 1)), count = 0;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) at += counts[w];
+            count += counts[w];
         }
-        if (p.weights && tid < count) w = p.weights[row.slot(p, source(begin + tid))];
-        cluster_sync();
-#pragma unroll
-        for (int x = 0; x < kPieces; ++x) {
-            const int piece = x * kThreads + tid, j = piece / chunks;
-            if (j < count) {
-                const long long at = (long long)row.slot(p, begin + j) * p.row_bytes + (piece - j * chunks) * 16;
-                *reinterpret_cast<uint4 *>(p.k + at) = k[x];
-                *reinterpret_cast<uint4 *>(p.v + at) = v[x];
-            }
-        }
-        if (p.weights && tid < count) p.weights[row.slot(p, begin + tid)] = w;
+        if (mine) requests[at] = s;
+        __syncthreads();
+        for (; turn < (long long)count * n; turn += workers) f(requests[turn / n], (int)(turn % n));
+        turn -= (long long)count * n;
     }
 }
 
-// Blocks of a cluster: as many as let every block have a place on the SMs at once.
-int cluster_of(int S, int n_kv) {
-    int n = kMaxCluster;
-    while (n > 1 && (long long)S * n_kv * n > 2LL * num_sms()) n >>= 1;
-    return n;
+__global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p) {
+    extern __shared__ __align__(16) uint32_t keys[];
+    __shared__ Shared sh;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const uint32_t blocks = cluster_size(), rank = cluster_rank();
+    const int cluster = blockIdx.x / blocks;
+    in_turn<kThreads>(
+        p.S, p.n_kv, cluster, gridDim.x / blocks,
+        [&](int s) {
+            bool bad = false;
+            const int len = p.lens[s];
+            const bool active = loses(p, len, p.keep[s], bad);
+            if (!active && cluster == 0 && rank == 0) {
+                p.new_lens[s] = len;
+                if (bad) flag_status(p.status, LORA_DEV_BAD_LENGTH);
+            }
+            return active;
+        },
+        [&](int s, int head) { select(p, sh, keys, s, head, blocks, rank); });
+}
+
+// Moves a column range of `width` 16-byte chunks of one plane of a request and kv head.  A thread looks up one row of
+// a round: its source's index two rounds before its slots, those a round before the copies, which are two rounds ahead
+// of the stores.
+__device__ void move_range(const EvictParams &p, char *plane, const Row &row, const int *kept, int keep, int len, int first, int width,
+                           uint4 *ring, int2 (*slots)[kMoveThreads]) {
+    const int tid = threadIdx.x, per_pass = kMoveThreads / width, pieces = min(kPieces, kMoveThreads / per_pass), round = per_pass * pieces;
+    const int rounds = (keep + round - 1) / round;
+    const int my_row = tid < per_pass * width ? tid / width : -1;
+    char *column = plane + (first + tid % width) * 16;
+    uint4 *mine = ring + tid;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(mine);
+    auto index = [&](int i) {                            // source of this thread's row of round i, -1: none
+        const int j = i * round + tid;
+        return tid < round && j < keep ? (int)min((uint32_t)kept[j], (uint32_t)len - 1) : -1;
+    };
+    auto places = [&](int i, int src) {                  // slots it moves between; .x -1: it does not
+        const int j = i * round + tid;
+        return src < 0 || src == j ? make_int2(-1, 0) : make_int2(row.slot(p, src), row.slot(p, j));
+    };
+    auto load = [&](int i) {
+        const int2 *at = slots[i % kSlotRounds];
+        const uint32_t dst = base + (i % kStages) * (kPieces * kMoveThreads * 16);
+        if (i < rounds && my_row >= 0)
+#pragma unroll
+            for (int x = 0; x < kPieces; ++x)
+                if (x < pieces) {
+                    const int from = at[x * per_pass + my_row].x;
+                    if (from >= 0) cp_async16(dst + x * (kMoveThreads * 16), column + (long long)from * p.row_bytes, true);
+                }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+    __syncthreads();                                     // the range before has read its slots
+    int2 next = places(0, index(0));
+    const int2 second = places(1, index(1));
+    int src = index(3);
+    slots[0][tid] = next;
+    slots[1][tid] = second;
+    next = places(2, index(2));
+    __syncthreads();
+    load(0);
+    load(1);
+    for (int i = 0; i < rounds; ++i) {
+        slots[(i + 2) % kSlotRounds][tid] = next;
+        next = places(i + 3, src);
+        src = index(i + 4);
+        asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+        __syncthreads();                                 // round i has been read
+        if (my_row >= 0) {
+            const int2 *at = slots[i % kSlotRounds];
+            const uint4 *data = mine + (i % kStages) * (kPieces * kMoveThreads);
+#pragma unroll
+            for (int x = 0; x < kPieces; ++x)
+                if (x < pieces) {
+                    const int2 to = at[x * per_pass + my_row];
+                    if (to.x >= 0) *reinterpret_cast<uint4 *>(column + (long long)to.y * p.row_bytes) = data[x * kMoveThreads];
+                }
+        }
+        load(i + 2);
+    }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+}
+
+__device__ void move_weights(const EvictParams &p, const Row &row, const int *kept, int keep, int len) {
+    const int tid = threadIdx.x;
+    for (int j0 = 0; j0 < keep; j0 += kMoveThreads * kPieces) {
+        float w[kPieces];
+        int src[kPieces];
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x) {
+            const int j = j0 + x * kMoveThreads + tid;
+            src[x] = j < keep ? (int)min((uint32_t)kept[j], (uint32_t)len - 1) : -1;
+        }
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x) w[x] = src[x] >= 0 ? p.weights[row.slot(p, src[x])] : 0.f;
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < kPieces; ++x) {
+            const int j = j0 + x * kMoveThreads + tid;
+            if (src[x] >= 0) p.weights[row.slot(p, j)] = w[x];
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kMoveThreads, kMovePerSm) evict_move_kernel(const EvictParams p) {
+    extern __shared__ __align__(16) uint4 ring[];         // [kStages][kPieces][kMoveThreads]: each thread's own
+    __shared__ int2 slots[kSlotRounds][kMoveThreads];
+    const int chunks = p.row_bytes >> 4, extra = p.weights ? 1 : 0, parts = 2 * p.slices + extra;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    in_turn<kMoveThreads>(
+        p.S, p.n_kv * parts, blockIdx.x, gridDim.x,
+        [&](int s) {
+            const int len = p.lens[s], keep = p.keep[s];
+            bool bad;
+            return loses(p, len, keep, bad) && p.new_lens[s] == keep;
+        },
+        [&](int s, int unit) {
+            const int head = unit / parts, part = unit - head * parts - extra;
+            const int keep = p.keep[s], len = p.lens[s];
+            const Row row = {p.table + (long long)s * p.max_pages, head};
+            const int *kept = p.kept + ((long long)s * p.n_kv + head) * p.ld_kept;
+            if (part < 0) {
+                move_weights(p, row, kept, keep, len);
+                return;
+            }
+            const int slice = part % p.slices, first = chunks * slice / p.slices, width = chunks * (slice + 1) / p.slices - first;
+            move_range(p, part < p.slices ? p.k : p.v, row, kept, keep, len, first, width, ring, slots);
+        });
 }
 
 }  // namespace
@@ -296,7 +459,8 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float
     if ((long long)S * kv->n_kv_heads > 0x7fffffffLL / kMaxCluster) return LORA_ERR_SHAPE;
     if (S == 0) return LORA_OK;
     if (!scores || !kv_lens || !page_table || max_pages < 1 || !keep || !new_lens || (ld_kept && !kept)) return LORA_ERR_ARG;
-    if (((uintptr_t)scores | (uintptr_t)weights | (uintptr_t)kv_lens | (uintptr_t)page_table | (uintptr_t)keep |
+    if (!aligned16(scores) || !aligned16(weights)) return LORA_ERR_ARG;
+    if (((uintptr_t)kv_lens | (uintptr_t)page_table | (uintptr_t)keep |
          (uintptr_t)kept | (uintptr_t)new_lens) & 3u)
         return LORA_ERR_ARG;
     const size_t plane = (size_t)kv->n_pages * kv->n_kv_heads * kv->page_size * sizeof(float), row = (size_t)S * sizeof(int);
@@ -323,12 +487,18 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float
     p.kept = kept;
     p.new_lens = new_lens;
     p.status = kv->status;
-    const int blocks = cluster_of(S, p.n_kv);
-    const long long most = ((((long long)max_pages * kv->page_size + blocks - 1) / blocks) + 31) & ~31LL;     // tokens a block
-    p.held = (int)(most < kMaxHeld ? most : kMaxHeld);
-    if (smem_optin(reinterpret_cast<const void *>(evict_kernel), kMaxHeld * sizeof(uint32_t))) return LORA_ERR_CUDA;
+    const long long cap = (long long)max_pages * kv->page_size, units = (long long)S * p.n_kv;
+    int blocks = 1;
+    while (cap > kSolo && blocks < kMaxCluster && units * blocks <= num_sms()) blocks *= 2;
+    const long long share = ((cap + blocks - 1) / blocks + 31) & ~31LL, solo = ((cap < kSolo ? cap : kSolo) + 3) & ~3LL;
+    p.held = (int)(share < solo ? solo : share < kMaxHeld ? share : kMaxHeld);
+    const long long clusters = units < 4LL * num_sms() / blocks ? units : 4LL * num_sms() / blocks;
+    const int chunks = p.row_bytes >> 4;
+    p.slices = (chunks + kSliceChunks - 1) / kSliceChunks;
+    if (smem_optin(reinterpret_cast<const void *>(evict_move_kernel), kMoveSmem)) return LORA_ERR_CUDA;
+    if (smem_optin(reinterpret_cast<const void *>(evict_select_kernel), kMaxHeld * sizeof(uint32_t))) return LORA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long long)S * p.n_kv * blocks));
+    cfg.gridDim = dim3((unsigned)(clusters * blocks));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = p.held * sizeof(uint32_t);
     cfg.stream = (cudaStream_t)stream;
@@ -338,7 +508,17 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_kernel, p);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+    count_launch();
+    if (e != cudaSuccess) return cuda_status(e);
+    const long long tasks = units * (2 * p.slices + 1), places = (long long)num_sms() * kMovePerSm;
+    cfg.gridDim = dim3((unsigned)(tasks < places ? tasks : places));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = kMoveSmem;
+    attr[0] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    e = cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
     count_launch();
     return cuda_status(e);
 }
