@@ -24,14 +24,14 @@ namespace {
 using namespace decode;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBits = 11, kBins = 1 << kBits;
+constexpr int kBits = 11, kBins = 1 << kBits, kCoarse = 8;      // kCoarse bins side by side are counted together as well
 constexpr int kMaxCluster = 8;
 constexpr int kSolo = 8192;
 constexpr int kMaxHeld = 16384;       // scores a block keeps in shared memory; more are read again
 
 constexpr int kMoveThreads = 256;
 constexpr int kPieces = 8, kStages = 3;               // 16-byte pieces a thread and round; rounds in shared memory
-constexpr int kSlotRounds = 4;
+constexpr int kAhead = kStages - 1, kSlotRounds = kStages + 1;
 constexpr int kMovePerSm = 2;
 constexpr int kSliceChunks = 8;       // at most, of 16 bytes
 constexpr size_t kMoveSmem = (size_t)kStages * kPieces * kMoveThreads * 16;
@@ -48,11 +48,11 @@ struct EvictParams {
 };
 
 struct __align__(16) Shared {
-    uint32_t bins[kBins];             // this block's counts, read by its cluster
+    uint32_t bins[kBins], coarse[kBins / kCoarse];      // this block's counts, read by its cluster
     uint32_t scan[kWarps];
     uint32_t sure[kWarps], equal[kWarps];     // tokens of each warp above the cut, and at it
     uint32_t block_sure, block_equal, bad;
-    uint32_t cut, wanted, inside;     // a pass's bin: its keys' upper bits, how many are wanted of it, how many it has
+    uint32_t cut, wanted, inside, group;      // a pass's bin: its keys' upper bits, how many are wanted of it, how many it has
 };
 
 __device__ __forceinline__ uint32_t cluster_size() {
@@ -82,10 +82,17 @@ __device__ __forceinline__ uint32_t peer_values(const uint32_t *mine, uint32_t b
     __syncwarp();
     return value;
 }
-__device__ __forceinline__ uint4 peer_load4(const uint32_t *mine, uint32_t rank) {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(peer_addr(mine, rank)));
-    return v;
+// Sum over the blocks.
+__device__ __forceinline__ uint32_t peer_sum(const uint32_t *mine, uint32_t blocks) {
+    uint32_t part[kMaxCluster], sum = 0;
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; ++r) {
+        part[r] = 0;
+        if (r < blocks) asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(part[r]) : "r"(peer_addr(mine, r)));
+    }
+#pragma unroll
+    for (uint32_t r = 0; r < kMaxCluster; ++r) sum += part[r];
+    return sum;
 }
 
 // Orders as the scores do; -0 is 0, a NaN is below everything.
@@ -182,50 +189,52 @@ __device__ void select(const EvictParams &p, Shared &sh, uint32_t *keys, int s, 
         if (tid == 0) {
             sh.cut = cut;
             sh.wanted = sh.inside = wanted;
+            sh.group = 0;
         }
         __syncthreads();
         for (int c = max(lo, first) + tid; c < min(hi, last); c += kThreads) {
             const uint32_t key = key_at(c);
             if ((key & mask) == cut) atomicAdd(&sh.bins[(key >> shift) & (bins - 1)], 1u);
         }
-        if (solo) __syncthreads();
-        else cluster_sync();
-        // from the top bin down: the bin in which the count passes `wanted`
-        constexpr int kPer = kBins / kThreads;      // 4 bins a thread, side by side (of fewer bins: the lower threads')
-        const int low = bins - kPer * (tid + 1);
-        uint32_t mine[kPer] = {}, sum = 0;          // from the thread's top bin down
-        if (low >= 0) {
-            uint4 part[kMaxCluster];
-#pragma unroll
-            for (uint32_t r = 0; r < kMaxCluster; ++r) {
-                part[r] = make_uint4(0, 0, 0, 0);
-                if (solo ? r == 0 : r < blocks)
-                    part[r] = solo ? *reinterpret_cast<const uint4 *>(sh.bins + low) : peer_load4(sh.bins + low, r);
-            }
-#pragma unroll
-            for (uint32_t r = 0; r < kMaxCluster; ++r) {
-                mine[0] += part[r].w;
-                mine[1] += part[r].z;
-                mine[2] += part[r].y;
-                mine[3] += part[r].x;
-            }
-            sum = mine[0] + mine[1] + mine[2] + mine[3];
+        __syncthreads();
+        const int groups = bins / kCoarse;
+        uint32_t sum = 0;
+        if (tid < groups) {                 // a group of bins a thread, from the top
+            const uint4 *bin = reinterpret_cast<const uint4 *>(sh.bins + (groups - 1 - tid) * kCoarse);
+            const uint4 u = bin[0], v = bin[1];
+            sum = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
         }
+        if (!solo) {
+            if (tid < groups) sh.coarse[tid] = sum;
+            cluster_sync();
+            if (tid < groups) sum = peer_sum(sh.coarse + tid, blocks);
+        }
+        // from the top down: the group, then its bin, in which the count passes `wanted`
         const uint32_t upto = warp_scan(sum);
         if (lane == 31) sh.scan[warp] = upto;
         __syncthreads();
         uint32_t before = upto - sum;
+        for (int w = 0; w < warp && w < (groups + 31) / 32; ++w) before += sh.scan[w];
+        if (tid < groups && before < wanted && before + sum >= wanted) {
+            sh.group = groups - 1 - tid;
+            sh.wanted = wanted - before;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            const int bin = sh.group * kCoarse + kCoarse - 1 - (lane & (kCoarse - 1));
+            const uint32_t left = sh.wanted, n = solo ? sh.bins[bin] : peer_sum(sh.bins + bin, blocks);
+            uint32_t to = n;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            if (w < warp) before += sh.scan[w];
-#pragma unroll
-        for (int x = 0; x < kPer; ++x) {
-            if (before < wanted && before + mine[x] >= wanted) {
-                sh.cut = cut | (uint32_t)(low + kPer - 1 - x) << shift;
-                sh.wanted = wanted - before;
-                sh.inside = mine[x];
+            for (int o = 1; o < kCoarse; o <<= 1) {
+                const uint32_t other = __shfl_up_sync(0xffffffffu, to, o, kCoarse);
+                if ((lane & (kCoarse - 1)) >= o) to += other;
             }
-            before += mine[x];
+            __syncwarp();
+            if (lane < kCoarse && to - n < left && to >= left) {
+                sh.cut = cut | (uint32_t)bin << shift;
+                sh.wanted = left - (to - n);
+                sh.inside = n;
+            }
         }
         if (solo) __syncthreads();
         else cluster_sync();                // also: the peers have read this block's bins
@@ -289,12 +298,12 @@ __device__ void select(const EvictParams &p, Shared &sh, uint32_t *keys, int s, 
     if (!solo) cluster_sync();               // no block goes on while its shared memory is read
 }
 
-// Calls f(request, unit of n a request) for every gridDim-th (of `workers`) unit of the requests for which active(s) holds.
+// Calls f(request, unit) for the units, n a request, of the requests for which active(s) holds: the one `turn` units
+// from here and every `workers`-th after it.  Returns what is left of `turn`.
 template <int THREADS, typename A, typename F>
-__device__ __forceinline__ void in_turn(int S, int n, int worker, int workers, A active, F f) {
+__device__ __forceinline__ long long in_turn(int S, int n, long long turn, int workers, A active, F f) {
     __shared__ int requests[THREADS], counts[THREADS / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long turn = worker;                  // units until this worker's next one
     for (int s0 = 0; s0 < S; s0 += THREADS) {
         const int s = s0 + tid;
         const bool mine = s < S && active(s);
@@ -312,6 +321,7 @@ __device__ __forceinline__ void in_turn(int S, int n, int worker, int workers, A
         for (; turn < (long long)count * n; turn += workers) f(requests[turn / n], (int)(turn % n));
         turn -= (long long)count * n;
     }
+    return turn;
 }
 
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParams p) {
@@ -367,20 +377,25 @@ __device__ void move_range(const EvictParams &p, char *plane, const Row &row, co
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
     __syncthreads();                                     // the range before has read its slots
-    int2 next = places(0, index(0));
-    const int2 second = places(1, index(1));
-    int src = index(3);
-    slots[0][tid] = next;
-    slots[1][tid] = second;
-    next = places(2, index(2));
+    int2 next;
+    int src;
+    {
+        int at[kAhead + 1];
+#pragma unroll
+        for (int i = 0; i <= kAhead; ++i) at[i] = index(i);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) slots[i][tid] = places(i, at[i]);
+        next = places(kAhead, at[kAhead]);
+        src = index(kAhead + 1);
+    }
     __syncthreads();
-    load(0);
-    load(1);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) load(i);
     for (int i = 0; i < rounds; ++i) {
-        slots[(i + 2) % kSlotRounds][tid] = next;
-        next = places(i + 3, src);
-        src = index(i + 4);
-        asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+        slots[(i + kAhead) % kSlotRounds][tid] = next;
+        next = places(i + kAhead + 1, src);
+        src = index(i + kAhead + 2);
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kAhead - 1) : "memory");
         __syncthreads();                                 // round i has been read
         if (my_row >= 0) {
             const int2 *at = slots[i % kSlotRounds];
@@ -392,7 +407,7 @@ __device__ void move_range(const EvictParams &p, char *plane, const Row &row, co
                     if (to.x >= 0) *reinterpret_cast<uint4 *>(column + (long long)to.y * p.row_bytes) = data[x * kMoveThreads];
                 }
         }
-        load(i + 2);
+        load(i + kAhead);
     }
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 }
@@ -421,26 +436,25 @@ __device__ void move_weights(const EvictParams &p, const Row &row, const int *ke
 __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) evict_move_kernel(const EvictParams p) {
     extern __shared__ __align__(16) uint4 ring[];         // [kStages][kPieces][kMoveThreads]: each thread's own
     __shared__ int2 slots[kSlotRounds][kMoveThreads];
-    const int chunks = p.row_bytes >> 4, extra = p.weights ? 1 : 0, parts = 2 * p.slices + extra;
+    const int chunks = p.row_bytes >> 4, parts = 2 * p.slices, workers = gridDim.x;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    in_turn<kMoveThreads>(
-        p.S, p.n_kv * parts, blockIdx.x, gridDim.x,
-        [&](int s) {
-            const int len = p.lens[s], keep = p.keep[s];
-            bool bad;
-            return loses(p, len, keep, bad) && p.new_lens[s] == keep;
-        },
-        [&](int s, int unit) {
-            const int head = unit / parts, part = unit - head * parts - extra;
-            const int keep = p.keep[s], len = p.lens[s];
+    auto active = [&](int s) {
+        const int len = p.lens[s], keep = p.keep[s];
+        bool bad;
+        return loses(p, len, keep, bad) && p.new_lens[s] == keep;
+    };
+    const long long turn =
+        in_turn<kMoveThreads>(p.S, p.n_kv * parts, blockIdx.x, workers, active, [&](int s, int unit) {
+            const int head = unit / parts, part = unit - head * parts;
             const Row row = {p.table + (long long)s * p.max_pages, head};
-            const int *kept = p.kept + ((long long)s * p.n_kv + head) * p.ld_kept;
-            if (part < 0) {
-                move_weights(p, row, kept, keep, len);
-                return;
-            }
             const int slice = part % p.slices, first = chunks * slice / p.slices, width = chunks * (slice + 1) / p.slices - first;
-            move_range(p, part < p.slices ? p.k : p.v, row, kept, keep, len, first, width, ring, slots);
+            move_range(p, part < p.slices ? p.k : p.v, row, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s], p.lens[s], first,
+                       width, ring, slots);
+        });
+    if (p.weights)
+        in_turn<kMoveThreads>(p.S, p.n_kv, turn, workers, active, [&](int s, int head) {
+            move_weights(p, {p.table + (long long)s * p.max_pages, head}, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s],
+                         p.lens[s]);
         });
 }
 
@@ -489,7 +503,7 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float
     p.status = kv->status;
     const long long cap = (long long)max_pages * kv->page_size, units = (long long)S * p.n_kv;
     int blocks = 1;
-    while (cap > kSolo && blocks < kMaxCluster && units * blocks <= num_sms()) blocks *= 2;
+    while (cap > kSolo && blocks < kMaxCluster && units * blocks * 2 <= num_sms()) blocks *= 2;
     const long long share = ((cap + blocks - 1) / blocks + 31) & ~31LL, solo = ((cap < kSolo ? cap : kSolo) + 3) & ~3LL;
     p.held = (int)(share < solo ? solo : share < kMaxHeld ? share : kMaxHeld);
     const long long clusters = units < 4LL * num_sms() / blocks ? units : 4LL * num_sms() / blocks;
