@@ -48,7 +48,7 @@ struct EvictParams {
 };
 
 struct __align__(16) Shared {
-    uint32_t bins[kBins], coarse[kBins / kCoarse];      // this block's counts, read by its cluster
+    uint32_t bins[2][kBins], coarse[2][kBins / kCoarse];      // this block's counts, of two passes, read by its cluster
     uint32_t scan[kWarps];
     uint32_t sure[kWarps], equal[kWarps];     // tokens of each warp above the cut, and at it
     uint32_t block_sure, block_equal, bad;
@@ -143,30 +143,20 @@ __device__ void select(const EvictParams &p, Shared &sh, uint32_t *keys, int s, 
     const int per_warp = (((each + 31) / 32 + kWarps - 1) / kWarps) * 32;
     const int w_lo = min(hi, lo + warp * per_warp), w_hi = min(hi, w_lo + per_warp);
 
-    __syncthreads();                  // the unit before has read what is written here
+    // a page outside the cache counts as 0 here, and in the end the request stays as it is
     bool bad = false;
-    for (int x = (lo >> p.page_shift) + tid; x < (hi + (1 << p.page_shift) - 1) >> p.page_shift; x += kThreads) {
-        const int page = __ldg(row.table + x);
-        bad |= page < 0 || page >= p.n_pages;
-    }
-    bad = __syncthreads_or(bad);
-    if (!solo) {                      // a page outside the cache: the request stays as it is, whichever block sees it
-        if (tid == 0) sh.bad = bad;
-        cluster_sync();
-        bad = __any_sync(0xffffffffu, peer_values(&sh.bad, blocks) != 0);
-        cluster_sync();
-    }
-    if (bad) {
-        if (head == 0 && rank == 0 && tid == 0) {
-            flag_status(p.status, LORA_DEV_BAD_PAGE);
-            p.new_lens[s] = len;
-        }
-        return;
-    }
+    auto place = [&](int c, bool &outside) {
+        const int page = __ldg(row.table + (c >> p.page_shift));
+        outside = page < 0 || page >= p.n_pages;
+        return (((outside ? 0 : page) * p.n_kv + head) << p.page_shift) + (c & ((1 << p.page_shift) - 1));
+    };
+    __syncthreads();                  // the unit before has read what is written here
     if (p.page_shift >= 2) {
 #pragma unroll 4
         for (int c = lo + tid * 4; c < held; c += kThreads * 4) {
-            const int at = row.slot(p, c);
+            bool outside;
+            const int at = place(c, outside);
+            bad |= outside;
             if (c + 4 <= held) {
                 const float4 f = *reinterpret_cast<const float4 *>(p.scores + at);
                 *reinterpret_cast<uint4 *>(keys + (c - lo)) = make_uint4(key_of(f.x), key_of(f.y), key_of(f.z), key_of(f.w));
@@ -176,16 +166,31 @@ __device__ void select(const EvictParams &p, Shared &sh, uint32_t *keys, int s, 
         }
     } else {
 #pragma unroll 4
-        for (int c = lo + tid; c < held; c += kThreads) keys[c - lo] = key_of(p.scores[row.slot(p, c)]);
+        for (int c = lo + tid; c < held; c += kThreads) {
+            bool outside;
+            keys[c - lo] = key_of(p.scores[place(c, outside)]);
+            bad |= outside;
+        }
     }
-    auto key_at = [&](int c) { return c < held ? keys[c - lo] : key_of(p.scores[row.slot(p, c)]); };
+    for (int x = (held >> p.page_shift) + tid; held < hi && x < (hi + (1 << p.page_shift) - 1) >> p.page_shift; x += kThreads) {
+        bool outside;
+        place(min(x << p.page_shift, hi - 1), outside);
+        bad |= outside;
+    }
+    auto key_at = [&](int c) {
+        bool outside;
+        return c < held ? keys[c - lo] : key_of(p.scores[place(c, outside)]);
+    };
+    bad = __syncthreads_or(bad);
 
     // the k-th greatest key of the tokens that compete: its upper bits as far as they are needed
     uint32_t wanted = keep - first - recent, cut = 0, mask = 0;
     if (wanted == 0) cut = mask = ~0u;       // nobody: no key is above, and of those equal none is wanted
-    for (int shift = 32 - kBits; mask != ~0u; shift = max(0, shift - kBits)) {
+    for (int shift = 32 - kBits, turn = 0; mask != ~0u; shift = max(0, shift - kBits), turn ^= 1) {
+        // the buffer of the pass before the last: a cluster's barrier later, its peers have read it
+        uint32_t *all_bins = sh.bins[turn], *coarse = sh.coarse[turn];
         const int width = shift == 0 ? 32 - 2 * kBits : kBits, bins = 1 << width;
-        for (int x = tid; x < bins; x += kThreads) sh.bins[x] = 0;
+        for (int x = tid; x < bins; x += kThreads) all_bins[x] = 0;
         if (tid == 0) {
             sh.cut = cut;
             sh.wanted = sh.inside = wanted;
@@ -194,20 +199,20 @@ __device__ void select(const EvictParams &p, Shared &sh, uint32_t *keys, int s, 
         __syncthreads();
         for (int c = max(lo, first) + tid; c < min(hi, last); c += kThreads) {
             const uint32_t key = key_at(c);
-            if ((key & mask) == cut) atomicAdd(&sh.bins[(key >> shift) & (bins - 1)], 1u);
+            if ((key & mask) == cut) atomicAdd(&all_bins[(key >> shift) & (bins - 1)], 1u);
         }
         __syncthreads();
         const int groups = bins / kCoarse;
         uint32_t sum = 0;
         if (tid < groups) {                 // a group of bins a thread, from the top
-            const uint4 *bin = reinterpret_cast<const uint4 *>(sh.bins + (groups - 1 - tid) * kCoarse);
+            const uint4 *bin = reinterpret_cast<const uint4 *>(all_bins + (groups - 1 - tid) * kCoarse);
             const uint4 u = bin[0], v = bin[1];
             sum = ((u.x + u.y) + (u.z + u.w)) + ((v.x + v.y) + (v.z + v.w));
         }
         if (!solo) {
-            if (tid < groups) sh.coarse[tid] = sum;
+            if (tid < groups) coarse[tid] = sum;
             cluster_sync();
-            if (tid < groups) sum = peer_sum(sh.coarse + tid, blocks);
+            if (tid < groups) sum = peer_sum(coarse + tid, blocks);
         }
         // from the top down: the group, then its bin, in which the count passes `wanted`
         const uint32_t upto = warp_scan(sum);
@@ -222,7 +227,7 @@ __device__ void select(const EvictParams &p, Shared &sh, uint32_t *keys, int s, 
         __syncthreads();
         if (warp == 0) {
             const int bin = sh.group * kCoarse + kCoarse - 1 - (lane & (kCoarse - 1));
-            const uint32_t left = sh.wanted, n = solo ? sh.bins[bin] : peer_sum(sh.bins + bin, blocks);
+            const uint32_t left = sh.wanted, n = solo ? all_bins[bin] : peer_sum(all_bins + bin, blocks);
             uint32_t to = n;
 #pragma unroll
             for (int o = 1; o < kCoarse; o <<= 1) {
@@ -236,8 +241,7 @@ __device__ void select(const EvictParams &p, Shared &sh, uint32_t *keys, int s, 
                 sh.inside = n;
             }
         }
-        if (solo) __syncthreads();
-        else cluster_sync();                // also: the peers have read this block's bins
+        __syncthreads();
         cut = sh.cut;
         wanted = sh.wanted;
         mask |= (uint32_t)(bins - 1) << shift;
@@ -262,18 +266,27 @@ __device__ void select(const EvictParams &p, Shared &sh, uint32_t *keys, int s, 
     __syncthreads();
     uint32_t sure_before = 0, equal_before = 0;
     if (!solo) {
-        if (tid == 0) {
-            uint32_t a = 0, b = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                a += sh.sure[w];
-                b += sh.equal[w];
+        if (warp == 0) {
+            const uint32_t a = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.sure[lane] : 0u);
+            const uint32_t b = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.equal[lane] : 0u);
+            if (lane == 0) {
+                sh.block_sure = a;
+                sh.block_equal = b;
+                sh.bad = bad;
             }
-            sh.block_sure = a;
-            sh.block_equal = b;
         }
         cluster_sync();
         sure_before = __reduce_add_sync(0xffffffffu, peer_values(&sh.block_sure, rank));
         equal_before = __reduce_add_sync(0xffffffffu, peer_values(&sh.block_equal, rank));
+        bad = __any_sync(0xffffffffu, peer_values(&sh.bad, blocks) != 0);
+        cluster_sync();                      // no block goes on while its shared memory is read
+    }
+    if (bad) {
+        if (head == 0 && rank == 0 && tid == 0) {
+            flag_status(p.status, LORA_DEV_BAD_PAGE);
+            p.new_lens[s] = len;
+        }
+        return;
     }
     for (int w = 0; w < warp; ++w) {
         sure_before += sh.sure[w];
@@ -295,7 +308,6 @@ __device__ void select(const EvictParams &p, Shared &sh, uint32_t *keys, int s, 
         equal_before += __popc(at);
     }
     if (rank == 0 && head == 0 && tid == 0) p.new_lens[s] = keep;
-    if (!solo) cluster_sync();               // no block goes on while its shared memory is read
 }
 
 // Calls f(request, unit) for the units, n a request, of the requests for which active(s) holds: the one `turn` units
