@@ -107,11 +107,49 @@ def test_append_axes(case, n_axes, order, dtype):
     c.check()
 
 
-@pytest.mark.parametrize("interleaved", [False, True])
-def test_table_off_16_bytes(interleaved):
-    c = Axes((40, 8, 2, 64, 64, 16, interleaved, True, True), I.BF16, 3, "sections").to_device(table_offset=1)
+MANY = [   # enough tokens for the ring of whole tokens
+    (1500, 4, 2, 128, 128, 16, False, True, True), (700, 7, 1, 80, 24, 8, False, True, False), (900, 0, 2, 64, 64, 32, True, True, True),
+    (650, 3, 3, 24, 8, 1, True, True, False), (1000, 5, 1, 256, 128, 64, False, False, True), (640, 2, 1, 192, 192, 4, True, True, False),
+    (2100, 1, 1, 8, 8, 16, False, True, True), (800, 6, 2, 112, 0, 16, False, True, True), (1300, 2, 2, 96, 48, 128, False, False, False)]
+
+
+@pytest.mark.parametrize("dtype", [I.BF16, I.F32])
+@pytest.mark.parametrize("n_axes, order", [(3, "sections"), (4, "any"), (2, "last")])
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(map(str, c)))
+def test_append_axes_of_many_tokens(case, n_axes, order, dtype):
+    c = Axes(case, dtype, n_axes, order).to_device()
     c.call()
     c.check()
+    again = Axes(case, dtype, n_axes, order).to_device()
+    if not case[8] and case[1]:                 # queries in place
+        again.out = again.qkv[0]
+    again.call()
+    assert all(np.array_equal(x, y) for x, y in zip(c.results(), again.results()))
+
+
+def test_bad_positions_and_slots_of_many_tokens():
+    c = Axes((1200, 2, 1, 64, 64, 8, False, True, True), I.BF16, 3, "last")
+    n_pos, T = len(c.arrays[5]), 1200
+    c.arrays[6][:, :2] = 1 << 30                # axes that no pair names
+    c.arrays[6][17, 2], c.arrays[6][1100, 2] = -1, n_pos
+    c.arrays[7][5], c.arrays[7][1199] = len(c.arrays[8]) * 8, 1 << 62
+    c.to_device().call()
+    got = c.results()
+    assert int(c.status) == L.LORA_DEV_BAD_SLOT | L.LORA_DEV_BAD_POSITION
+    c.arrays[6] = np.clip(c.arrays[6], 0, n_pos - 1)
+    c.arrays[7][5] = c.arrays[7][1199] = -1
+    ref = c.reference()
+    assert_within(got[0], ref[0], append_bound(ref[0], I.BF16, 64))
+    assert_within(got[1], ref[1], append_bound(ref[1], I.BF16, 64))
+    assert np.array_equal(got[2], ref[2])
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_table_off_16_bytes(interleaved):
+    for T in (40, 1000):
+        c = Axes((T, 8, 2, 64, 64, 16, interleaved, True, True), I.BF16, 3, "sections").to_device(table_offset=1)
+        c.call()
+        c.check()
 
 
 @pytest.mark.parametrize("dtype", [I.BF16, I.F32])
