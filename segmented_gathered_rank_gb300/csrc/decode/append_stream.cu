@@ -18,8 +18,14 @@ using namespace tc;
 constexpr int kConsumers = 8, kWork = kConsumers * 32, kAll = kWork + 64;       // a warp copies, a warp stores
 constexpr int kStages = 4;
 constexpr int kPerSm = 3;
-constexpr int kMaxToken = 16 << 10;       // bytes of a token's heads
-constexpr int kMinTokens = 608;
+constexpr int kThird = 75 << 10;          // of a SM's shared memory
+constexpr int kMaxToken = 26 << 10;       // bytes of a token's heads: two blocks a SM
+// Bytes of all heads from which on this kernel takes a call.  It and append.cu's, bf16, halves, norms, three axes in turn:
+// 48 heads of 128, 512 tokens (6 MB) 6.2 and 6.0 us, 1024 tokens 7.7 and 10.3, 8192 tokens 37.4 and 71.3; neighbours, 1024
+// tokens 7.6 and 7.8, 8192 tokens 36.8 and 54.5; 12 heads of 128, 2048 tokens (6 MB) 7.0 and 7.0, 4096 tokens 11.6 and
+// 12.1, 8192 tokens 20.5 and 24.5; 48 heads of 64, 1024 tokens (6 MB) 6.7 and 6.5, 2048 tokens 9.4 and 11.1; 48 heads of
+// 80, 1024 tokens (8 MB) 7.9 and 9.6.
+constexpr long long kMinBytes = 7 << 20;
 
 struct StreamParams {
     AppendParams a;
@@ -228,7 +234,7 @@ template <typename E, int LANES, int PAIRS>
 int launch(const StreamParams &sp, cudaStream_t st) {
     const size_t smem = (size_t)kStages * sp.stage;
     if (smem_optin(reinterpret_cast<const void *>(append_stream_kernel<E, LANES, PAIRS>), smem)) return LORA_ERR_CUDA;
-    const int places = num_sms() * kPerSm, grid = sp.T < places ? sp.T : places;
+    const int per_sm = smem <= (size_t)kThird ? kPerSm : 2, places = num_sms() * per_sm, grid = sp.T < places ? sp.T : places;
     append_stream_kernel<E, LANES, PAIRS><<<grid, kAll, smem, st>>>(sp);
     count_launch();
     return cuda_status(cudaGetLastError());
@@ -244,7 +250,8 @@ int launch(const StreamParams &sp, cudaStream_t st) {
 namespace decode {
 
 bool streams(const AppendParams &p, int T, int esize) {
-    return T >= kMinTokens && p.rot % 8 == 0 && (p.n_q + 2 * p.n_kv) * (long long)p.d * esize <= kMaxToken;
+    const long long token = (p.n_q + 2LL * p.n_kv) * p.d * esize;
+    return p.rot % 8 == 0 && token <= kMaxToken && token * T >= kMinBytes;
 }
 
 int launch_append_stream(const AppendParams &p, int T, bool bf16, bool near, cudaStream_t st) {

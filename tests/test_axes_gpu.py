@@ -107,10 +107,10 @@ def test_append_axes(case, n_axes, order, dtype):
     c.check()
 
 
-MANY = [   # enough tokens for the ring of whole tokens
-    (1500, 4, 2, 128, 128, 16, False, True, True), (700, 7, 1, 80, 24, 8, False, True, False), (900, 0, 2, 64, 64, 32, True, True, True),
-    (650, 3, 3, 24, 8, 1, True, True, False), (1000, 5, 1, 256, 128, 64, False, False, True), (640, 2, 1, 192, 192, 4, True, True, False),
-    (2100, 1, 1, 8, 8, 16, False, True, True), (800, 6, 2, 112, 0, 16, False, True, True), (1300, 2, 2, 96, 48, 128, False, False, False)]
+MANY = [   # enough bytes for the ring of whole tokens, in one type or both
+    (700, 32, 8, 128, 128, 16, False, True, True), (800, 49, 7, 80, 24, 8, False, True, False), (900, 0, 32, 64, 64, 32, True, True, True),
+    (500, 300, 100, 24, 8, 1, True, True, False), (1000, 20, 5, 256, 128, 64, False, False, True), (600, 30, 10, 192, 192, 4, True, True, False),
+    (500, 900, 30, 8, 8, 16, False, True, True), (650, 48, 16, 112, 0, 16, False, True, True), (1300, 16, 8, 96, 48, 128, False, False, False)]
 
 
 @pytest.mark.parametrize("dtype", [I.BF16, I.F32])
@@ -128,7 +128,7 @@ def test_append_axes_of_many_tokens(case, n_axes, order, dtype):
 
 
 def test_bad_positions_and_slots_of_many_tokens():
-    c = Axes((1200, 2, 1, 64, 64, 8, False, True, True), I.BF16, 3, "last")
+    c = Axes((1200, 32, 8, 64, 64, 8, False, True, True), I.BF16, 3, "last")
     n_pos, T = len(c.arrays[5]), 1200
     c.arrays[6][:, :2] = 1 << 30                # axes that no pair names
     c.arrays[6][17, 2], c.arrays[6][1100, 2] = -1, n_pos
@@ -146,8 +146,8 @@ def test_bad_positions_and_slots_of_many_tokens():
 
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_table_off_16_bytes(interleaved):
-    for T in (40, 1000):
-        c = Axes((T, 8, 2, 64, 64, 16, interleaved, True, True), I.BF16, 3, "sections").to_device(table_offset=1)
+    for T in (40, 1200):
+        c = Axes((T, 32, 8, 64, 64, 16, interleaved, True, True), I.BF16, 3, "sections").to_device(table_offset=1)
         c.call()
         c.check()
 
