@@ -387,7 +387,8 @@ template <int D, bool TMA, bool KEEP>
 __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, TMA>::kPerSm))
     attention_mma_kernel(const __grid_constant__ KvMaps maps, const AttnParams p) {
     using Sh = MmaShape<D, TMA>;
-    using Copy = std::conditional_t<TMA, TmaCopy<D, Sh::kTile>, ChunkCopy<D, Sh::kTile, 128>>;
+    // kept scores stay in L2 until their sums are taken: keys and values make room for them
+    using Copy = std::conditional_t<TMA, TmaCopy<D, Sh::kTile, KEEP>, ChunkCopy<D, Sh::kTile, 128>>;
     extern __shared__ uint8_t raw[];
     __shared__ ScanShared scan;
     __shared__ MmaControl ctl;

@@ -58,7 +58,8 @@ __device__ __forceinline__ bool make_finite(uint4 *at) {
 
 // One warp's tensor copies.  fetch() starts the load of this lane's page id of a
 // tile, copy() uses it: fetched a tile ahead, its latency is hidden.
-template <int D, int TILE>
+// ONCE: what is copied leaves L2 first.
+template <int D, int TILE, bool ONCE = false>
 struct TmaCopy {
     static constexpr int kThreads = 32;
     static constexpr int kArrivals = 1;     // on the tile's barrier
@@ -79,6 +80,17 @@ struct TmaCopy {
         __syncwarp();
         if (offset < 0) return;
         const int row = ((checked_page(p, page) * p.n_kv + head) << p.page_shift) + offset;
+        if constexpr (ONCE) {
+            uint64_t policy;
+            asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(policy));
+            for (int h = 0; h < panels; ++h)
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], [%4], "
+                    "%5;\n" ::"r"(dst + h * (TILE * 128) + lane * per * 128),
+                    "l"(map), "r"(h * 64), "r"(row), "r"(tc::smem_u32(bar)), "l"(policy)
+                    : "memory");
+            return;
+        }
         for (int h = 0; h < panels; ++h)
             asm volatile(
                 "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::

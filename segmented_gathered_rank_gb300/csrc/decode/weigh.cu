@@ -82,9 +82,10 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
     }
 }
 
-constexpr int kScoreTile = 1024;       // cached tokens a tile, four a thread
+constexpr int kScoreThreads = 64, kScorePerSm = 32;
+constexpr int kScoreTile = kScoreThreads * 4;       // cached tokens a tile
 
-__global__ void __launch_bounds__(kThreads) weigh_scores_kernel(const AttnParams p, float *weights, float decay) {
+__global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnParams p, float *weights, float decay) {
     __shared__ ScanShared scan;
     Cursor at;
     KeyCursor cur;
@@ -94,7 +95,21 @@ __global__ void __launch_bounds__(kThreads) weigh_scores_kernel(const AttnParams
     for (; cur.left > 0; cur.advance(p)) {
         const int c = cur.tile * kScoreTile + threadIdx.x * 4, rows = cur.r.n * p.group;
         if (c >= cur.r.len) continue;
-        float w[4] = {};
+        // what the weights were is on its way first
+        const int prefix = cur.r.len - cur.r.n;
+        const bool whole = p.page_shift >= 2 && c + 4 <= cur.r.len;
+        long long slot[4];
+        float w[4] = {}, old[4] = {};
+        slot[0] = weight_at(p, cur.s, cur.r, cur.head, c);
+        if (whole) {
+            if (slot[0] >= 0 && decay > 0.f && c < prefix) *reinterpret_cast<float4 *>(old) = *reinterpret_cast<const float4 *>(weights + slot[0]);
+        } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                slot[x] = c + x < cur.r.len ? weight_at(p, cur.s, cur.r, cur.head, c + x) : -1;
+                if (slot[x] >= 0 && decay > 0.f && c + x < prefix) old[x] = weights[slot[x]];
+            }
+        }
         // rows of a kv head lie group by group of n_q rows
         const long long first = (long long)cur.r.begin * p.n_q + cur.head * p.group;
 #pragma unroll 4
@@ -108,24 +123,15 @@ __global__ void __launch_bounds__(kThreads) weigh_scores_kernel(const AttnParams
             w[2] += exp2f(s.z - lse);
             w[3] += exp2f(s.w - lse);
         }
-        const int prefix = cur.r.len - cur.r.n;
-        if (p.page_shift >= 2 && c + 4 <= cur.r.len) {
-            const long long slot = weight_at(p, cur.s, cur.r, cur.head, c);
-            if (slot < 0) continue;
-            float4 *dst = reinterpret_cast<float4 *>(weights + slot);
-            if (decay > 0.f && c < prefix) {
-                const float4 old = *dst;
-                w[0] += old.x * decay;
-                if (c + 1 < prefix) w[1] += old.y * decay;
-                if (c + 2 < prefix) w[2] += old.z * decay;
-                if (c + 3 < prefix) w[3] += old.w * decay;
-            }
-            *dst = make_float4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (decay > 0.f && c + x < prefix) w[x] += old[x] * decay;
+        if (whole) {
+            if (slot[0] >= 0) *reinterpret_cast<float4 *>(weights + slot[0]) = make_float4(w[0], w[1], w[2], w[3]);
         } else {
-            for (int x = 0; x < 4 && c + x < cur.r.len; ++x) {
-                const long long slot = weight_at(p, cur.s, cur.r, cur.head, c + x);
-                if (slot >= 0) weights[slot] = decay > 0.f && c + x < prefix ? w[x] + weights[slot] * decay : w[x];
-            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (slot[x] >= 0) weights[slot[x]] = w[x];
         }
     }
 }
@@ -145,7 +151,7 @@ int plan_weigh(const lora_kv_pages *kv, const AttnParams &attention, AttnParams 
     const long long tiles = (long long)p.max_pages * kv->page_size / p.tk + 1 + p.unit_cost, units = (long long)p.T * p.group / p.rt + p.S;
     if (tiles * units > 0x7fffffffLL / p.n_kv) return LORA_ERR_SHAPE;
     p.max_places = (uint32_t)(tiles * units * p.n_kv);
-    p.grid = num_sms() * (p.scores ? 8 : tc ? 1 : 2);
+    p.grid = num_sms() * (p.scores ? kScorePerSm : tc ? 1 : 2);
     return LORA_OK;
 }
 
@@ -156,7 +162,7 @@ int launch_weigh(const lora_kv_pages *kv, const KvMaps *maps, const AttnParams &
     if (smem && smem_optin(reinterpret_cast<const void *>(kernel), smem)) return LORA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(p.scores ? kScoreThreads : kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
