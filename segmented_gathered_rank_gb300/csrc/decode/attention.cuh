@@ -114,7 +114,7 @@ __device__ __forceinline__ int block_of(uint32_t total, uint32_t x, uint32_t gri
     return (int)(x < edge ? x / (each + 1) : more + (x - edge) / each);
 }
 
-// Called by every thread of the block: the block's first tile, and the length of
+// Called by every thread of the block (kScanThreads at least): the block's first tile, and the length of
 // the list.  Lets the join launch; block 0 reports bad tables.  A table whose segments
 // overlap until they name more places than the T tokens can have has an empty list.
 __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared &sh, Cursor &c) {

@@ -82,36 +82,50 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
     }
 }
 
-constexpr int kScoreThreads = 64, kScorePerSm = 32;
+constexpr int kScoreThreads = 128, kScorePerSm = 8;
 constexpr int kScoreTile = kScoreThreads * 4;       // cached tokens a tile
 
 __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnParams p, float *weights, float decay) {
+    static_assert(kScoreThreads >= kScanThreads, "start_block");
     __shared__ ScanShared scan;
     Cursor at;
     KeyCursor cur;
     cur.start(p, scan, start_block(p, scan, at));
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    if (!*p.computed) return;
-    for (; cur.left > 0; cur.advance(p)) {
-        const int c = cur.tile * kScoreTile + threadIdx.x * 4, rows = cur.r.n * p.group;
-        if (c >= cur.r.len) continue;
-        // what the weights were is on its way first
-        const int prefix = cur.r.len - cur.r.n;
-        const bool whole = p.page_shift >= 2 && c + 4 <= cur.r.len;
-        long long slot[4];
-        float w[4] = {}, old[4] = {};
-        slot[0] = weight_at(p, cur.s, cur.r, cur.head, c);
-        if (whole) {
-            if (slot[0] >= 0 && decay > 0.f && c < prefix) *reinterpret_cast<float4 *>(old) = *reinterpret_cast<const float4 *>(weights + slot[0]);
-        } else {
+    // A tile's slots (-1: none) and what its weights were, which take two round trips: requested a tile ahead, the first
+    // before the attention's last kernel is done.
+    struct Place {
+        int slot[4];
+        float old[4];
+        __device__ __forceinline__ void fetch(const AttnParams &p, const KeyCursor &c, const float *weights, float decay) {
+            const int c0 = c.tile * kScoreTile + threadIdx.x * 4, prefix = c.r.len - c.r.n;
+            const bool whole = p.page_shift >= 2;        // four tokens of one page
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                slot[x] = c + x < cur.r.len ? weight_at(p, cur.s, cur.r, cur.head, c + x) : -1;
-                if (slot[x] >= 0 && decay > 0.f && c + x < prefix) old[x] = weights[slot[x]];
+                slot[x] = -1;
+                old[x] = 0.f;
+                if (c.left > 0 && c0 + x < c.r.len) slot[x] = whole && x ? (slot[0] < 0 ? -1 : slot[0] + x) : (int)weight_at(p, c.s, c.r, c.head, c0 + x);
             }
+            if (!(decay > 0.f)) return;
+            if (whole && slot[3] >= 0 && c0 + 4 <= prefix) {
+                *reinterpret_cast<float4 *>(old) = *reinterpret_cast<const float4 *>(weights + slot[0]);
+                return;
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (slot[x] >= 0 && c0 + x < prefix) old[x] = weights[slot[x]];
         }
+    } place;
+    place.fetch(p, cur, weights, decay);
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (!*p.computed) return;
+    while (cur.left > 0) {
+        const int c = cur.tile * kScoreTile + threadIdx.x * 4, rows = c < cur.r.len ? cur.r.n * p.group : 0;
         // rows of a kv head lie group by group of n_q rows
         const long long first = (long long)cur.r.begin * p.n_q + cur.head * p.group;
+        const Place now = place;
+        cur.advance(p);
+        place.fetch(p, cur, weights, decay);
+        float w[4] = {};
 #pragma unroll 4
         for (int row = 0; row < rows; ++row) {
             const int i = row / p.group;
@@ -124,14 +138,13 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
             w[3] += exp2f(s.w - lse);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            if (decay > 0.f && c + x < prefix) w[x] += old[x] * decay;
-        if (whole) {
-            if (slot[0] >= 0) *reinterpret_cast<float4 *>(weights + slot[0]) = make_float4(w[0], w[1], w[2], w[3]);
+        for (int x = 0; x < 4; ++x) w[x] += now.old[x] * decay;
+        if (p.page_shift >= 2 && now.slot[3] >= 0) {
+            *reinterpret_cast<float4 *>(weights + now.slot[0]) = make_float4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                if (slot[x] >= 0) weights[slot[x]] = w[x];
+                if (now.slot[x] >= 0) weights[now.slot[x]] = w[x];
         }
     }
 }
