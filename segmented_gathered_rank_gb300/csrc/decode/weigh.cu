@@ -82,8 +82,9 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
     }
 }
 
-constexpr int kScoreThreads = 128, kScorePerSm = 8;
+constexpr int kScoreThreads = 128, kScorePerSm = 6;
 constexpr int kScoreTile = kScoreThreads * 4;       // cached tokens a tile
+constexpr int kScoreRows = 4;                       // rows on their way at once
 
 __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnParams p, float *weights, float decay) {
     static_assert(kScoreThreads >= kScanThreads, "start_block");
@@ -91,60 +92,84 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
     Cursor at;
     KeyCursor cur;
     cur.start(p, scan, start_block(p, scan, at));
-    // A tile's slots (-1: none) and what its weights were, which take two round trips: requested a tile ahead, the first
-    // before the attention's last kernel is done.
-    struct Place {
-        int slot[4];
-        float old[4];
-        __device__ __forceinline__ void fetch(const AttnParams &p, const KeyCursor &c, const float *weights, float decay) {
-            const int c0 = c.tile * kScoreTile + threadIdx.x * 4, prefix = c.r.len - c.r.n;
-            const bool whole = p.page_shift >= 2;        // four tokens of one page
+    // A tile's page ids, then its slots (-1: none) and what its weights were: two round trips, both a tile ahead and the
+    // first before the attention's last kernel is done.
+    int page[4], slot[4];
+    float old[4];
+    const bool whole = p.page_shift >= 2;        // a thread's four tokens are in one page
+    auto fetch_pages = [&](const KeyCursor &c) {
+        const int c0 = c.tile * kScoreTile + threadIdx.x * 4;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                slot[x] = -1;
-                old[x] = 0.f;
-                if (c.left > 0 && c0 + x < c.r.len) slot[x] = whole && x ? (slot[0] < 0 ? -1 : slot[0] + x) : (int)weight_at(p, c.s, c.r, c.head, c0 + x);
-            }
-            if (!(decay > 0.f)) return;
-            if (whole && slot[3] >= 0 && c0 + 4 <= prefix) {
-                *reinterpret_cast<float4 *>(old) = *reinterpret_cast<const float4 *>(weights + slot[0]);
-                return;
-            }
+        for (int x = 0; x < 4; ++x)
+            if ((x == 0 || !whole) && c.left > 0 && c0 + x < c.r.len) page[x] = page_of(p, c.s, c.r, c0 + x);
+    };
+    auto fetch_weights = [&](const KeyCursor &c) {
+        const int c0 = c.tile * kScoreTile + threadIdx.x * 4, prefix = c.r.len - c.r.n;
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                if (slot[x] >= 0 && c0 + x < prefix) old[x] = weights[slot[x]];
+        for (int x = 0; x < 4; ++x) {
+            slot[x] = -1;
+            old[x] = 0.f;
+            const int at = whole ? page[0] : page[x];
+            if (c.left <= 0 || c0 + x >= c.r.len) continue;
+            if (at >= 0 && at < p.n_pages) slot[x] = ((at * p.n_kv + c.head) << p.page_shift) + ((c0 + x) & ((1 << p.page_shift) - 1));
+            else flag_status(p.status, LORA_DEV_BAD_PAGE);
         }
-    } place;
-    place.fetch(p, cur, weights, decay);
+        if (!(decay > 0.f)) return;
+        if (whole && slot[3] >= 0 && c0 + 4 <= prefix) {
+            *reinterpret_cast<float4 *>(old) = *reinterpret_cast<const float4 *>(weights + slot[0]);
+            return;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (slot[x] >= 0 && c0 + x < prefix) old[x] = weights[slot[x]];
+    };
+    fetch_pages(cur);
+    fetch_weights(cur);
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (!*p.computed) return;
     while (cur.left > 0) {
         const int c = cur.tile * kScoreTile + threadIdx.x * 4, rows = c < cur.r.len ? cur.r.n * p.group : 0;
         // rows of a kv head lie group by group of n_q rows
         const long long first = (long long)cur.r.begin * p.n_q + cur.head * p.group;
-        const Place now = place;
-        cur.advance(p);
-        place.fetch(p, cur, weights, decay);
-        float w[4] = {};
-#pragma unroll 4
-        for (int row = 0; row < rows; ++row) {
-            const int i = row / p.group;
-            const long long line = first + (long long)i * (p.n_q - p.group) + row;
-            const float4 s = *reinterpret_cast<const float4 *>(p.scores + line * p.ld_scores + c);
-            const float lse = p.lse[line];
-            w[0] += exp2f(s.x - lse);
-            w[1] += exp2f(s.y - lse);
-            w[2] += exp2f(s.z - lse);
-            w[3] += exp2f(s.w - lse);
-        }
+        auto line_of = [&](int row) { return first + (long long)(row / p.group) * (p.n_q - p.group) + row; };
+        float4 s[kScoreRows];
+        float lse[kScoreRows], w[4] = {};
+        auto load = [&](int row0) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) w[x] += now.old[x] * decay;
-        if (p.page_shift >= 2 && now.slot[3] >= 0) {
-            *reinterpret_cast<float4 *>(weights + now.slot[0]) = make_float4(w[0], w[1], w[2], w[3]);
+            for (int x = 0; x < kScoreRows; ++x)
+                if (row0 + x < rows) {
+                    const long long line = line_of(row0 + x);
+                    s[x] = *reinterpret_cast<const float4 *>(p.scores + line * p.ld_scores + c);
+                    lse[x] = p.lse[line];
+                }
+        };
+        load(0);
+        cur.advance(p);
+        fetch_pages(cur);
+        for (int row0 = 0; row0 < rows; row0 += kScoreRows) {
+#pragma unroll
+            for (int x = 0; x < kScoreRows; ++x)
+                if (row0 + x < rows) {
+                    w[0] += exp2f(s[x].x - lse[x]);
+                    w[1] += exp2f(s[x].y - lse[x]);
+                    w[2] += exp2f(s[x].z - lse[x]);
+                    w[3] += exp2f(s[x].w - lse[x]);
+                }
+            if (row0 + kScoreRows < rows) load(row0 + kScoreRows);
+        }
+        int to[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            w[x] += old[x] * decay;
+            to[x] = slot[x];
+        }
+        fetch_weights(cur);
+        if (whole && to[3] >= 0) {
+            *reinterpret_cast<float4 *>(weights + to[0]) = make_float4(w[0], w[1], w[2], w[3]);
         } else {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                if (now.slot[x] >= 0) weights[now.slot[x]] = w[x];
+                if (to[x] >= 0) weights[to[x]] = w[x];
         }
     }
 }
