@@ -124,6 +124,14 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, MmaCon
 // Four consumer warps; each takes kWarpKeys of a stage's tokens for all rows of
 // the unit, with a maximum, sum and output of its own (so a tile needs no exchange
 // between warps), joined in shared memory when the block leaves the unit.
+// Kept scores leave L2 last.
+__device__ __forceinline__ void store_kept(float *dst, float4 s) {
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;\n" : "=l"(policy));
+    asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;\n" ::"l"(dst), "f"(s.x), "f"(s.y), "f"(s.z), "f"(s.w), "l"(policy)
+                 : "memory");
+}
+
 // KEEP: the scores go to p.scores as well.
 template <int D, bool TMA, bool KEEP>
 __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t *smem, MmaControl &ctl) {
@@ -209,14 +217,21 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
                         if (!((see[e >> 1] >> (j * 8 + t4 * 2 + (e & 1))) & 1)) s[j][e] = -INFINITY;
             }
             if constexpr (KEEP) {
+                // neighbouring lanes swap halves of two groups of eight tokens, so that each has four side by side
+                const bool odd = t4 & 1;
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
-                    if (hh * 8 + g4 >= rows) continue;
-                    float *dst = p.scores + row_index(p, cur, cur.row_tile * kRows + hh * 8 + g4) * p.ld_scores + c0 + t4 * 2;
+                    const bool live = hh * 8 + g4 < rows;
+                    float *dst = p.scores + (live ? row_index(p, cur, cur.row_tile * kRows + hh * 8 + g4) : 0) * p.ld_scores + c0 +
+                                 (odd ? 8 + (t4 - 1) * 2 : t4 * 2);
 #pragma unroll
-                    for (int j = 0; j < Sh::kWarpKeys / 8; ++j)
-                        if (c0 + j * 8 + t4 * 2 < cur.r.len)
-                            *reinterpret_cast<float2 *>(dst + j * 8) = make_float2(s[j][hh * 2] * p.scale_log2, s[j][hh * 2 + 1] * p.scale_log2);
+                    for (int j = 0; j < Sh::kWarpKeys / 8; j += 2) {
+                        const float a = s[j][hh * 2] * p.scale_log2, b = s[j][hh * 2 + 1] * p.scale_log2;
+                        const float c = s[j + 1][hh * 2] * p.scale_log2, d = s[j + 1][hh * 2 + 1] * p.scale_log2;
+                        const float e = __shfl_xor_sync(0xffffffffu, odd ? a : c, 1), f = __shfl_xor_sync(0xffffffffu, odd ? b : d, 1);
+                        if (live && c0 + j * 8 + (odd ? 8 + (t4 - 1) * 2 : t4 * 2) < cur.r.len)
+                            store_kept(dst + j * 8, odd ? make_float4(e, f, c, d) : make_float4(a, b, e, f));
+                    }
                 }
             }
             // softmax of the warp's keys
@@ -984,13 +999,14 @@ int launch_attention(const lora_kv_pages *kv, const AttnParams &p, const Variant
 // lora_tree_attention_weights: a flag, and the logarithm of each row's sum.
 size_t log_bytes(int n_q_heads, int T) { return (16 + (size_t)T * n_q_heads * sizeof(float) + 15) & ~(size_t)15; }
 
-// Whether the weights are summed up from kept scores: up to 16 rows a kv head and request on average.
-constexpr int kKeepRows = 16;
-bool keeps_scores(int group, int S, int T) { return (long long)T * group <= (long long)kKeepRows * S; }
-long long score_pitch(const lora_kv_pages *kv, int max_pages) { return ((long long)max_pages * kv->page_size + 7) & ~7LL; }
+// Whether the weights are summed up from kept scores: up to 16 (fp32: 32) rows a kv head and request on average.
+int keep_rows(const lora_kv_pages *kv) { return kv->dtype == LORA_F32 ? 32 : 16; }
+bool keeps_scores(const lora_kv_pages *kv, int group, int S, int T) { return (long long)T * group <= (long long)keep_rows(kv) * S; }
+// Whole lines of L2 a row: what has been summed up is dropped from it.
+long long score_pitch(const lora_kv_pages *kv, int max_pages) { return ((long long)max_pages * kv->page_size + 31) & ~31LL; }
 // At most, for up to T tokens of up to S requests.
 size_t score_bytes(const lora_kv_pages *kv, int n_q_heads, int S, int T, int max_pages) {
-    const long long most = (long long)kKeepRows * S / (n_q_heads / kv->n_kv_heads), tokens = T < most ? T : most;
+    const long long most = (long long)keep_rows(kv) * S / (n_q_heads / kv->n_kv_heads), tokens = T < most ? T : most;
     return (size_t)tokens * n_q_heads * score_pitch(kv, max_pages) * sizeof(float);
 }
 
@@ -1034,10 +1050,10 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
     if (weights && overlap(q, q_bytes, out, q_bytes)) return LORA_ERR_ARG;
     if (num_sms() < 1) return LORA_ERR_CUDA;
     const Variant variant = variant_of(kv, n_q_heads / kv->n_kv_heads, S, T);
-    const bool keep = weights && keeps_scores(n_q_heads / kv->n_kv_heads, S, T);
+    const bool keep = weights && keeps_scores(kv, n_q_heads / kv->n_kv_heads, S, T);
     const size_t logs = weights ? log_bytes(n_q_heads, T) : 0;
     const size_t kept = keep ? score_bytes(kv, n_q_heads, S, T, max_pages) : 0, parts = (partial_bytes(variant, kv->head_dim) + 15) & ~(size_t)15;
-    if (ws_bytes < logs + parts + kept + (weights ? 32 : 0) || ws_bytes < partial_bytes(variant, kv->head_dim) + 16) return LORA_ERR_ARG;
+    if (ws_bytes < logs + parts + kept + (weights ? 128 : 0) || ws_bytes < partial_bytes(variant, kv->head_dim) + 16) return LORA_ERR_ARG;
     decode::AttnParams p;
     p.q = q;
     p.k = kv->k;
@@ -1061,7 +1077,7 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
     p.status = kv->status;
     p.lse = weights ? static_cast<float *>(workspace) + 4 : nullptr;
     p.computed = weights ? static_cast<int *>(workspace) : nullptr;
-    p.scores = keep ? reinterpret_cast<float *>(((uintptr_t)workspace + logs + parts + 31) & ~(uintptr_t)31) : nullptr;     // whole sectors
+    p.scores = keep ? reinterpret_cast<float *>(((uintptr_t)workspace + logs + parts + 127) & ~(uintptr_t)127) : nullptr;
     p.ld_scores = score_pitch(kv, max_pages);
     p.rt = variant.rt;
     p.tk = variant.tk;
@@ -1111,7 +1127,7 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
 extern "C" size_t lora_tree_attention_weights_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T, int max_pages) {
     const size_t base = lora_tree_attention_workspace_size(kv, n_q_heads, S, T);
     if (!base || max_pages < 0) return 0;
-    return base + log_bytes(n_q_heads, T) + score_bytes(kv, n_q_heads, S, T, max_pages) + 48;
+    return base + log_bytes(n_q_heads, T) + score_bytes(kv, n_q_heads, S, T, max_pages) + 144;
 }
 
 extern "C" int lora_tree_attention_weights(const lora_kv_pages *kv, float *weights, float decay, const void *q, int n_q_heads,

@@ -39,7 +39,7 @@ struct AttnParams {
     float *lse;              // [T][n_q]: log2 of each row's sum, infinity where it saw nothing; or NULL
     int *computed;           // with lse: whether the list held anything
     float *scores;           // [T][n_q][ld_scores]: the rows' scores in powers of two (-infinity: not seen); or NULL
-    long long ld_scores;     // a multiple of 8
+    long long ld_scores;     // a multiple of 32, as scores is of 128 bytes
 };
 
 struct Request {
