@@ -122,7 +122,6 @@ __device__ void copy_queries(const AttnParams &p, KeyCursor cur, uint8_t *ring, 
     const int lane = threadIdx.x & 31, chunk = lane % kLanes, row0 = (threadIdx.x >> 5) * 32 - kQueryWarp * 32;
     const bool inside = chunk * 8 < ((p.d + 15) & ~15), real_chunk = chunk * 8 < p.d;
     uint32_t seq = 0;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");       // lse
     while (cur.left > 0) {
         const Run run(cur, Sh::kQueries);
         const int rows = cur.r.n * p.group;
@@ -135,9 +134,6 @@ __device__ void copy_queries(const AttnParams &p, KeyCursor cur, uint8_t *ring, 
             const uint32_t dst = smem_u32(ring) + slot * Sh::kBytes, sums = smem_u32(ctl.lse[slot]);
             const int row = row_tile * kTile + row0 + lane, i = row / p.group;
             const long long line = row < rows ? first + (long long)i * (p.n_q - p.group) + row : -1;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(sums + (row0 + lane) * 4), "l"(p.lse + max(line, 0ll)),
-                         "r"(line >= 0 ? 4 : 0)
-                         : "memory");
 #pragma unroll
             for (int j = 0; j < 32; j += kRows) {
                 const int r = j + lane / kLanes;
@@ -147,6 +143,10 @@ __device__ void copy_queries(const AttnParams &p, KeyCursor cur, uint8_t *ring, 
                     cp_async16(dst + panel_off(kTile, row0 + r, chunk), static_cast<const __nv_bfloat16 *>(p.q) + (real ? from * p.d + chunk * 8 : 0),
                                real);
             }
+            if (seq == 0) asm volatile("griddepcontrol.wait;\n" ::: "memory");       // the attention's sums
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(sums + (row0 + lane) * 4), "l"(p.lse + max(line, 0ll)),
+                         "r"(line >= 0 ? 4 : 0)
+                         : "memory");
             cp_arrive(&ctl.q_full[slot]);
             if (++row_tile == cur.r.row_tiles) row_tile = 0;
         }
