@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "kv_copy.cuh"
+#include "tmem.cuh"
 #include "weigh.cuh"
 
 namespace lora {
@@ -197,15 +198,6 @@ __device__ void issue(const AttnParams &p, KeyCursor cur, uint8_t *keys, uint8_t
     }
 }
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
-        "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
 // A group of four warps: each thread sums up the weight of one cached token of each of the group's key tiles.
 template <int D>
 __device__ void consume(const AttnParams &p, KeyCursor cur, float *weights, float decay, Control<D> &ctl) {
@@ -237,32 +229,48 @@ __device__ void consume(const AttnParams &p, KeyCursor cur, float *weights, floa
                     ++s_seq;
                     fence_after_sync();
                     const int columns = min(kTile, rows - row_tile * kTile);
-                    for (int x0 = 0; x0 < columns && c0 < cur.r.len; x0 += 32) {
+                    const uint32_t from = tmem + b * kTile;
+                    const float *lse = ctl.lse[at];
+                    const int seen = c0 + 32 > prefix ? 0 : columns & ~31;        // columns that see all of the warp's tokens
+                    auto add = [&](const float (&s)[32], int x0) {
+                        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+#pragma unroll
+                        for (int x = 0; x < 32; x += 4) {
+                            const float4 l = *reinterpret_cast<const float4 *>(lse + x0 + x);
+                            const float2 e0 = fma2(make_float2(s[x], s[x + 1]), scale2, make_float2(-l.x, -l.y));
+                            const float2 e1 = fma2(make_float2(s[x + 2], s[x + 3]), scale2, make_float2(-l.z, -l.w));
+                            sum[0].x += exp2_fast(e0.x);
+                            sum[0].y += exp2_fast(e0.y);
+                            sum[1].x += exp2_fast(e1.x);
+                            sum[1].y += exp2_fast(e1.y);
+                        }
+                    };
+                    // 32 columns are on their way while the 32 before are summed up
+                    int x0 = 0;
+#pragma unroll 1
+                    for (; x0 + 64 <= seen; x0 += 64) {
+                        float s0[32], s1[32];
+                        tmem_ld32_start(from + x0, s0);
+                        tmem_wait_ld();
+                        tmem_arrived(s0);
+                        tmem_ld32_start(from + x0 + 32, s1);
+                        add(s0, x0);
+                        tmem_wait_ld();
+                        tmem_arrived(s1);
+                        add(s1, x0 + 32);
+                    }
+#pragma unroll 1
+                    for (; x0 < columns && c0 < cur.r.len; x0 += 32) {
+                        // drafted tokens, or columns without a row: what is not seen counts nothing, whatever it is
                         float s[32];
-                        tmem_ld32(tmem + b * kTile + x0, s);
-                        const float *lse = ctl.lse[at] + x0;
-                        if (c0 + 32 > prefix || x0 + 32 > columns) {
-                            // drafted tokens, or columns without a row: what is not seen counts nothing, whatever it is
-                            const int row = row_tile * kTile + x0 + lane;
-                            const uint32_t word = row < rows ? seen_word(p, cur.r, row / p.group, c0) : 0u;
+                        tmem_ld32(from + x0, s);
+                        const int row = row_tile * kTile + x0 + lane;
+                        const uint32_t word = row < rows ? seen_word(p, cur.r, row / p.group, c0) : 0u;
 #pragma unroll
-                            for (int x = 0; x < 32; ++x) {
-                                const bool on = (__shfl_sync(0xffffffffu, word, x) >> lane) & 1;
-                                const float e = exp2_fast(fmaf(s[x], p.scale_log2, -lse[x]));
-                                if (on) sum[x & 1].x += e;
-                            }
-                        } else {
-                            const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
-#pragma unroll
-                            for (int x = 0; x < 32; x += 4) {
-                                const float4 l = *reinterpret_cast<const float4 *>(lse + x);
-                                const float2 e0 = fma2(make_float2(s[x], s[x + 1]), scale2, make_float2(-l.x, -l.y));
-                                const float2 e1 = fma2(make_float2(s[x + 2], s[x + 3]), scale2, make_float2(-l.z, -l.w));
-                                sum[0].x += exp2_fast(e0.x);
-                                sum[0].y += exp2_fast(e0.y);
-                                sum[1].x += exp2_fast(e1.x);
-                                sum[1].y += exp2_fast(e1.y);
-                            }
+                        for (int x = 0; x < 32; ++x) {
+                            const bool on = (__shfl_sync(0xffffffffu, word, x) >> lane) & 1;
+                            const float e = exp2_fast(fmaf(s[x], p.scale_log2, -lse[x0 + x]));
+                            if (on) sum[x & 1].x += e;
                         }
                     }
                     fence_before_sync();
