@@ -449,14 +449,18 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) evict_move_kernel(co
     extern __shared__ __align__(16) uint4 ring[];         // [kStages][kPieces][kMoveThreads]: each thread's own
     __shared__ int2 slots[kSlotRounds][kMoveThreads];
     const int chunks = p.row_bytes >> 4, parts = 2 * p.slices, workers = gridDim.x;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    // which requests is known before the sources are; that all pages of one are in the cache, with them
     auto active = [&](int s) {
-        const int len = p.lens[s], keep = p.keep[s];
         bool bad;
-        return loses(p, len, keep, bad) && p.new_lens[s] == keep;
+        return loses(p, p.lens[s], p.keep[s], bad);
+    };
+    auto sound = [&](int s) {
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        return *(volatile int *)(p.new_lens + s) == p.keep[s];
     };
     const long long turn =
         in_turn<kMoveThreads>(p.S, p.n_kv * parts, blockIdx.x, workers, active, [&](int s, int unit) {
+            if (!sound(s)) return;
             const int head = unit / parts, part = unit - head * parts;
             const Row row = {p.table + (long long)s * p.max_pages, head};
             const int slice = part % p.slices, first = chunks * slice / p.slices, width = chunks * (slice + 1) / p.slices - first;
@@ -465,6 +469,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) evict_move_kernel(co
         });
     if (p.weights)
         in_turn<kMoveThreads>(p.S, p.n_kv, turn, workers, active, [&](int s, int head) {
+            if (!sound(s)) return;
             move_weights(p, {p.table + (long long)s * p.max_pages, head}, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s],
                          p.lens[s]);
         });
