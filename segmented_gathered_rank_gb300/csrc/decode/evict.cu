@@ -44,6 +44,7 @@ struct EvictParams {
     const int *lens, *table, *keep;
     int first, recent, ld_kept, held;
     int slices;                       // column ranges of a row of keys (and of values)
+    int places;                       // blocks that move at once
     int *kept, *new_lens, *status;
 };
 
@@ -448,7 +449,7 @@ __device__ void move_weights(const EvictParams &p, const Row &row, const int *ke
 __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) evict_move_kernel(const EvictParams p) {
     extern __shared__ __align__(16) uint4 ring[];         // [kStages][kPieces][kMoveThreads]: each thread's own
     __shared__ int2 slots[kSlotRounds][kMoveThreads];
-    const int chunks = p.row_bytes >> 4, parts = 2 * p.slices, workers = gridDim.x;
+    const int chunks = p.row_bytes >> 4, workers = gridDim.x;
     // which requests is known before the sources are; that all pages of one are in the cache, with them
     auto active = [&](int s) {
         bool bad;
@@ -458,13 +459,19 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) evict_move_kernel(co
         asm volatile("griddepcontrol.wait;\n" ::: "memory");
         return *(volatile int *)(p.new_lens + s) == p.keep[s];
     };
+    // 128 bytes a range; where that leaves three of four blocks without one, 64: one request 1088 -> 1024, 8 heads of
+    // 128, 11.8 us for 12.8, but four 32768 -> 2048 40.5 for 38.2 and 64 over 4352 102 for 93, as memory is read in pieces
+    long long units = 0;
+    for (int s0 = 0; s0 < p.S; s0 += kMoveThreads) units += __syncthreads_count(s0 + (int)threadIdx.x < p.S && active(s0 + threadIdx.x));
+    const int slices = chunks == p.slices * kSliceChunks && units * p.n_kv * p.slices * 8 <= p.places ? 2 * p.slices : p.slices;
+    const int parts = 2 * slices;
     const long long turn =
         in_turn<kMoveThreads>(p.S, p.n_kv * parts, blockIdx.x, workers, active, [&](int s, int unit) {
             if (!sound(s)) return;
             const int head = unit / parts, part = unit - head * parts;
             const Row row = {p.table + (long long)s * p.max_pages, head};
-            const int slice = part % p.slices, first = chunks * slice / p.slices, width = chunks * (slice + 1) / p.slices - first;
-            move_range(p, part < p.slices ? p.k : p.v, row, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s], p.lens[s], first,
+            const int slice = part % slices, first = chunks * slice / slices, width = chunks * (slice + 1) / slices - first;
+            move_range(p, part < slices ? p.k : p.v, row, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s], p.lens[s], first,
                        width, ring, slots);
         });
     if (p.weights)
@@ -526,6 +533,7 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float
     const long long clusters = units < 4LL * num_sms() / blocks ? units : 4LL * num_sms() / blocks;
     const int chunks = p.row_bytes >> 4;
     p.slices = (chunks + kSliceChunks - 1) / kSliceChunks;
+    p.places = num_sms() * kMovePerSm;
     if (smem_optin(reinterpret_cast<const void *>(evict_move_kernel), kMoveSmem)) return LORA_ERR_CUDA;
     if (smem_optin(reinterpret_cast<const void *>(evict_select_kernel), kMaxHeld * sizeof(uint32_t))) return LORA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
@@ -542,8 +550,8 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float
     cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
     count_launch();
     if (e != cudaSuccess) return cuda_status(e);
-    const long long tasks = units * (2 * p.slices + 1), places = (long long)num_sms() * kMovePerSm;
-    cfg.gridDim = dim3((unsigned)(tasks < places ? tasks : places));
+    const long long tasks = units * (4 * p.slices + 1);
+    cfg.gridDim = dim3((unsigned)(tasks < p.places ? tasks : p.places));
     cfg.blockDim = dim3(kMoveThreads);
     cfg.dynamicSmemBytes = kMoveSmem;
     attr[0] = {};
