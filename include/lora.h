@@ -453,7 +453,8 @@ int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, c
  * without drafted tokens, and of slots past a request, are left as they were.  out is
  * lora_tree_attention's, bit for bit.
  *   weights  n_pages x n_kv_heads x page_size fp32, slots as the cache's, 16-byte
- *            aligned.   decay  0..1.   out  apart from q.
+ *            aligned; a prefix token's is what earlier calls left there.
+ *   decay    0..1.   out  apart from q.
  *   workspace  lora_tree_attention_weights_workspace_size() bytes; it grows with S, T
  *            and max_pages, and one of the largest call serves every smaller one.
  * A page that several requests of the call share ends up with either's weights.  A
@@ -484,7 +485,8 @@ int lora_tree_attention_weights(const lora_kv_pages *kv, float *weights, float d
  *   kept      S x n_kv_heads x ld_kept device int32: for a request that loses tokens
  *             entry j < keep[s] of a row gets the index that the token at place j had; the
  *             rest is not written.  ld_kept is at least every budget that is used.
- *   new_lens  S device int32, apart from kv_lens and keep.
+ *   new_lens  S device int32; new_lens and kept are apart from each other and from what
+ *             is read.
  * The pages of a request that loses tokens are its own, each named once: a page shared
  * with another request, or named twice, ends up with either's tokens.
  * Errors: LORA_ERR_ARG, LORA_ERR_SHAPE.

@@ -504,6 +504,11 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float
     const size_t plane = (size_t)kv->n_pages * kv->n_kv_heads * kv->page_size * sizeof(float), row = (size_t)S * sizeof(int);
     if (weights && weights != scores && overlap(weights, plane, scores, plane)) return LORA_ERR_ARG;
     if (overlap(new_lens, row, kv_lens, row) || overlap(new_lens, row, keep, row)) return LORA_ERR_ARG;
+    const size_t list = (size_t)S * kv->n_kv_heads * ld_kept * sizeof(int), table = (size_t)S * max_pages * sizeof(int);
+    if (overlap(kept, list, kv_lens, row) || overlap(kept, list, keep, row) || overlap(kept, list, new_lens, row) ||
+        overlap(kept, list, page_table, table) || overlap(new_lens, row, page_table, table) || overlap(kept, list, scores, plane) ||
+        (weights && overlap(kept, list, weights, plane)))
+        return LORA_ERR_ARG;
     if (num_sms() < 1) return LORA_ERR_CUDA;
     EvictParams p;
     p.k = static_cast<char *>(kv->k);

@@ -130,16 +130,18 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (!*p.computed) return;
     while (cur.left > 0) {
-        const int c = cur.tile * kScoreTile + threadIdx.x * 4, rows = c < cur.r.len ? cur.r.n * p.group : 0;
+        const int c = cur.tile * kScoreTile + threadIdx.x * 4;
+        const int rows = c - (int)(threadIdx.x & 31) * 4 < cur.r.len ? cur.r.n * p.group : 0;       // of the whole warp
+        const bool inside = c < cur.r.len;
         // rows of a kv head lie group by group of n_q rows
         const long long first = (long long)cur.r.begin * p.n_q + cur.head * p.group;
         auto line_of = [&](int row) { return first + (long long)(row / p.group) * (p.n_q - p.group) + row; };
-        float4 s[kScoreRows];
-        float lse[kScoreRows], w[4] = {};
+        float4 s[kScoreRows] = {};
+        float lse[kScoreRows] = {}, w[4] = {};
         auto load = [&](int row0) {
 #pragma unroll
             for (int x = 0; x < kScoreRows; ++x)
-                if (row0 + x < rows) {
+                if (row0 + x < rows && inside) {
                     const long long line = line_of(row0 + x);
                     s[x] = *reinterpret_cast<const float4 *>(p.scores + line * p.ld_scores + c);
                     lse[x] = p.lse[line];
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
             // the scores are not needed again: their lines leave L2 without being written to memory (2 over 131072: 142 ->
             // 135 us; one over 777 would take 15.0 us for 14.2)
             __syncwarp();
-            if (drop && (threadIdx.x & 7) == 0)
+            if (drop && inside && (threadIdx.x & 7) == 0)
 #pragma unroll
                 for (int x = 0; x < kScoreRows; ++x)
                     if (row0 + x < rows)

@@ -67,7 +67,8 @@ def test_pair_axis_from_python(monkeypatch):
         call([0, 1, 2, 0, 1, 2, 0, 256])
 
 
-def evict(kv, scores=P, weights=P, S=2, lens=P + 64, table=P, max_pages=4, keep=P + 128, first=1, recent=2, kept=P, ld=8, new_lens=P + 256):
+def evict(kv, scores=P, weights=P, S=2, lens=P + (1 << 14) + 64, table=P + (1 << 14), max_pages=4, keep=P + (1 << 14) + 128,
+          first=1, recent=2, kept=P + (1 << 14) + 512, ld=8, new_lens=P + (1 << 14) + 256):
     return L._lib.lora_kv_evict(ctypes.byref(kv), scores, weights, S, lens, table, max_pages, keep, first, recent, kept, ld, new_lens, None)
 
 
@@ -82,7 +83,10 @@ def test_evict_refuses_pages(change, code):
     (dict(table=None), L.LORA_ERR_ARG), (dict(keep=None), L.LORA_ERR_ARG), (dict(kept=None), L.LORA_ERR_ARG), (dict(new_lens=None), L.LORA_ERR_ARG),
     (dict(scores=P + 2), L.LORA_ERR_ARG), (dict(weights=P + 1), L.LORA_ERR_ARG), (dict(kept=P + 3), L.LORA_ERR_ARG),
     (dict(weights=P + 4), L.LORA_ERR_ARG), (dict(scores=P + 64 * 16 * 2 * 4 - 4), L.LORA_ERR_ARG),       # half over each other
-    (dict(new_lens=P + 64), L.LORA_ERR_ARG), (dict(new_lens=P + 132), L.LORA_ERR_ARG), (dict(new_lens=P + 124), L.LORA_ERR_ARG),
+    (dict(new_lens=P + (1 << 14) + 64), L.LORA_ERR_ARG), (dict(new_lens=P + (1 << 14) + 132), L.LORA_ERR_ARG),
+    (dict(new_lens=P + (1 << 14) + 124), L.LORA_ERR_ARG), (dict(new_lens=P + (1 << 14) + 28), L.LORA_ERR_ARG),
+    (dict(kept=P + (1 << 14)), L.LORA_ERR_ARG), (dict(kept=P + (1 << 14) + 132), L.LORA_ERR_ARG), (dict(kept=P + 64), L.LORA_ERR_ARG),
+    (dict(kept=P + (1 << 14) + 260), L.LORA_ERR_ARG),
     (dict(max_pages=1 << 27), L.LORA_ERR_SHAPE), (dict(S=1 << 28), L.LORA_ERR_SHAPE)])
 def test_evict_refuses(change, code):
     before = L.lora_launch_count()
