@@ -30,11 +30,20 @@ constexpr int kSolo = 8192;
 constexpr int kMaxHeld = 16384;       // scores a block keeps in shared memory; more are read again
 
 constexpr int kMoveThreads = 256;
-constexpr int kPieces = 8, kStages = 3;               // 16-byte pieces a thread and round; rounds in shared memory
+constexpr int kStages = 3;            // rounds in shared memory
 constexpr int kAhead = kStages - 1, kSlotRounds = kStages + 1;
-constexpr int kMovePerSm = 2;
 constexpr int kSliceChunks = 8;       // at most, of 16 bytes
-constexpr size_t kMoveSmem = (size_t)kStages * kPieces * kMoveThreads * 16;
+// 16-byte pieces a thread and round, and blocks a SM: long rounds where all ranges there can be run at once, else more
+// blocks.  Four 32768 -> 2048 (128 ranges) 40 us with 8 pieces and two blocks, 45 with 5 and three; 64 requests over
+// <= 4352 (368 ranges of 2048 that there could be) 94 and 81.
+struct Few {
+    static constexpr int kPieces = 8, kPerSm = 2;
+};
+struct Many {
+    static constexpr int kPieces = 5, kPerSm = 3;
+};
+template <typename M>
+constexpr size_t kMoveSmem = (size_t)kStages * M::kPieces * kMoveThreads * 16;
 
 struct EvictParams {
     char *k, *v;
@@ -361,6 +370,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
 // Moves a column range of `width` 16-byte chunks of one plane of a request and kv head.  A thread looks up one row of
 // a round: its source's index two rounds before its slots, those a round before the copies, which are two rounds ahead
 // of the stores.
+template <int kPieces>
 __device__ void move_range(const EvictParams &p, char *plane, const Row &row, const int *kept, int keep, int len, int first, int width,
                            uint4 *ring, int2 (*slots)[kMoveThreads]) {
     const int tid = threadIdx.x, per_pass = kMoveThreads / width, pieces = min(kPieces, kMoveThreads / per_pass), round = per_pass * pieces;
@@ -425,6 +435,7 @@ __device__ void move_range(const EvictParams &p, char *plane, const Row &row, co
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 }
 
+template <int kPieces>
 __device__ void move_weights(const EvictParams &p, const Row &row, const int *kept, int keep, int len) {
     const int tid = threadIdx.x;
     for (int j0 = 0; j0 < keep; j0 += kMoveThreads * kPieces) {
@@ -446,8 +457,9 @@ __device__ void move_weights(const EvictParams &p, const Row &row, const int *ke
     }
 }
 
-__global__ void __launch_bounds__(kMoveThreads, kMovePerSm) evict_move_kernel(const EvictParams p) {
-    extern __shared__ __align__(16) uint4 ring[];         // [kStages][kPieces][kMoveThreads]: each thread's own
+template <typename M>
+__global__ void __launch_bounds__(kMoveThreads, M::kPerSm) evict_move_kernel(const EvictParams p) {
+    extern __shared__ __align__(16) uint4 ring[];         // [kStages][M::kPieces][kMoveThreads]: each thread's own
     __shared__ int2 slots[kSlotRounds][kMoveThreads];
     const int chunks = p.row_bytes >> 4, workers = gridDim.x;
     // which requests is known before the sources are; that all pages of one are in the cache, with them
@@ -471,15 +483,34 @@ __global__ void __launch_bounds__(kMoveThreads, kMovePerSm) evict_move_kernel(co
             const int head = unit / parts, part = unit - head * parts;
             const Row row = {p.table + (long long)s * p.max_pages, head};
             const int slice = part % slices, first = chunks * slice / slices, width = chunks * (slice + 1) / slices - first;
-            move_range(p, part < slices ? p.k : p.v, row, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s], p.lens[s], first,
+            move_range<M::kPieces>(p, part < slices ? p.k : p.v, row, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s], p.lens[s], first,
                        width, ring, slots);
         });
     if (p.weights)
         in_turn<kMoveThreads>(p.S, p.n_kv, turn, workers, active, [&](int s, int head) {
             if (!sound(s)) return;
-            move_weights(p, {p.table + (long long)s * p.max_pages, head}, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s],
-                         p.lens[s]);
+            move_weights<8>(p, {p.table + (long long)s * p.max_pages, head}, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s],
+                            p.lens[s]);
         });
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");       // no grid ends before the one it depends on
+}
+
+template <typename M>
+cudaError_t launch_move(EvictParams p, long long units, cudaStream_t st) {
+    if (smem_optin(reinterpret_cast<const void *>(evict_move_kernel<M>), kMoveSmem<M>)) return cudaErrorInvalidValue;
+    p.places = num_sms() * M::kPerSm;
+    const long long tasks = units * (4 * p.slices + 1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tasks < p.places ? tasks : p.places));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = kMoveSmem<M>;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel<M>, p);
 }
 
 }  // namespace
@@ -498,9 +529,7 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float
     if (S == 0) return LORA_OK;
     if (!scores || !kv_lens || !page_table || max_pages < 1 || !keep || !new_lens || (ld_kept && !kept)) return LORA_ERR_ARG;
     if (!aligned16(scores) || !aligned16(weights)) return LORA_ERR_ARG;
-    if (((uintptr_t)kv_lens | (uintptr_t)page_table | (uintptr_t)keep |
-         (uintptr_t)kept | (uintptr_t)new_lens) & 3u)
-        return LORA_ERR_ARG;
+    if (((uintptr_t)kv_lens | (uintptr_t)page_table | (uintptr_t)keep | (uintptr_t)kept | (uintptr_t)new_lens) & 3u) return LORA_ERR_ARG;
     const size_t plane = (size_t)kv->n_pages * kv->n_kv_heads * kv->page_size * sizeof(float), row = (size_t)S * sizeof(int);
     if (weights && weights != scores && overlap(weights, plane, scores, plane)) return LORA_ERR_ARG;
     if (overlap(new_lens, row, kv_lens, row) || overlap(new_lens, row, keep, row)) return LORA_ERR_ARG;
@@ -538,8 +567,7 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float
     const long long clusters = units < 4LL * num_sms() / blocks ? units : 4LL * num_sms() / blocks;
     const int chunks = p.row_bytes >> 4;
     p.slices = (chunks + kSliceChunks - 1) / kSliceChunks;
-    p.places = num_sms() * kMovePerSm;
-    if (smem_optin(reinterpret_cast<const void *>(evict_move_kernel), kMoveSmem)) return LORA_ERR_CUDA;
+    const bool few = units * 2 * p.slices <= num_sms() * Few::kPerSm;
     if (smem_optin(reinterpret_cast<const void *>(evict_select_kernel), kMaxHeld * sizeof(uint32_t))) return LORA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * blocks));
@@ -555,14 +583,7 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float
     cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
     count_launch();
     if (e != cudaSuccess) return cuda_status(e);
-    const long long tasks = units * (4 * p.slices + 1);
-    cfg.gridDim = dim3((unsigned)(tasks < p.places ? tasks : p.places));
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.dynamicSmemBytes = kMoveSmem;
-    attr[0] = {};
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
+    e = few ? launch_move<Few>(p, units, (cudaStream_t)stream) : launch_move<Many>(p, units, (cudaStream_t)stream);
     count_launch();
     return cuda_status(e);
 }

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
     }
 }
 
-constexpr int kScoreThreads = 128, kScorePerSm = 7;
+constexpr int kScoreThreads = 128, kScorePerSm = 9;
 constexpr int kScoreTile = kScoreThreads * 4;       // cached tokens a tile
 constexpr int kScoreRows = 4;                       // rows on their way at once
 
@@ -133,40 +133,50 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
         const int c = cur.tile * kScoreTile + threadIdx.x * 4;
         const int rows = c - (int)(threadIdx.x & 31) * 4 < cur.r.len ? cur.r.n * p.group : 0;       // of the whole warp
         const bool inside = c < cur.r.len;
-        // rows of a kv head lie group by group of n_q rows
-        const long long first = (long long)cur.r.begin * p.n_q + cur.head * p.group;
-        auto line_of = [&](int row) { return first + (long long)(row / p.group) * (p.n_q - p.group) + row; };
+        // rows of a kv head lie group by group of n_q rows: the next one's place, its head in the group
+        const float *scores = p.scores + ((long long)cur.r.begin * p.n_q + cur.head * p.group) * p.ld_scores + c;
+        const float *sums = p.lse + (long long)cur.r.begin * p.n_q + cur.head * p.group;
+        int g = 0;
         float4 s[kScoreRows] = {};
         float lse[kScoreRows] = {}, w[4] = {};
+        const float *loaded[kScoreRows];
         auto load = [&](int row0) {
 #pragma unroll
-            for (int x = 0; x < kScoreRows; ++x)
-                if (row0 + x < rows && inside) {
-                    const long long line = line_of(row0 + x);
-                    s[x] = *reinterpret_cast<const float4 *>(p.scores + line * p.ld_scores + c);
-                    lse[x] = p.lse[line];
+            for (int x = 0; x < kScoreRows; ++x) {
+                if (row0 + x >= rows) break;
+                if (inside) s[x] = *reinterpret_cast<const float4 *>(scores);
+                lse[x] = *sums;
+                loaded[x] = scores;
+                scores += p.ld_scores;
+                ++sums;
+                if (++g == p.group) {
+                    g = 0;
+                    scores += (p.n_q - p.group) * p.ld_scores;
+                    sums += p.n_q - p.group;
                 }
+            }
         };
         load(0);
         cur.advance(p);
         fetch_pages(cur);
         for (int row0 = 0; row0 < rows; row0 += kScoreRows) {
 #pragma unroll
-            for (int x = 0; x < kScoreRows; ++x)
-                if (row0 + x < rows) {
-                    w[0] += exp2f(s[x].x - lse[x]);
-                    w[1] += exp2f(s[x].y - lse[x]);
-                    w[2] += exp2f(s[x].z - lse[x]);
-                    w[3] += exp2f(s[x].w - lse[x]);
-                }
+            for (int x = 0; x < kScoreRows; ++x) {
+                if (row0 + x >= rows) break;
+                w[0] += exp2_fast(s[x].x - lse[x]);
+                w[1] += exp2_fast(s[x].y - lse[x]);
+                w[2] += exp2_fast(s[x].z - lse[x]);
+                w[3] += exp2_fast(s[x].w - lse[x]);
+            }
             // the scores are not needed again: their lines leave L2 without being written to memory (2 over 131072: 142 ->
             // 135 us; one over 777 would take 15.0 us for 14.2)
-            __syncwarp();
-            if (drop && inside && (threadIdx.x & 7) == 0)
+            if (drop) {
+                __syncwarp();
+                if (inside && (threadIdx.x & 7) == 0)
 #pragma unroll
-                for (int x = 0; x < kScoreRows; ++x)
-                    if (row0 + x < rows)
-                        asm volatile("discard.global.L2 [%0], 128;\n" ::"l"(p.scores + line_of(row0 + x) * p.ld_scores + c) : "memory");
+                    for (int x = 0; x < kScoreRows; ++x)
+                        if (row0 + x < rows) asm volatile("discard.global.L2 [%0], 128;\n" ::"l"(loaded[x]) : "memory");
+            }
             if (row0 + kScoreRows < rows) load(row0 + kScoreRows);
         }
         int to[4];

@@ -317,7 +317,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor at;
     KeyCursor cur;
     cur.start(p, scan, start_block(p, scan, at));
-    if (cur.left <= 0) return;          // the whole block
+    if (cur.left <= 0) {                // the whole block; no grid ends before those it depends on
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        return;
+    }
     if (warp == kMmaWarp) {
         tmem_alloc(&ctl.tmem, kTmemCols);
         tmem_relinquish();
