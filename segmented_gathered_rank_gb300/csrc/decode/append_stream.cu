@@ -8,6 +8,7 @@
 // through registers.
 #include "append.cuh"
 #include "tc_common.cuh"
+#include "tmem.cuh"
 
 namespace lora {
 namespace {
@@ -108,13 +109,16 @@ __device__ void turn_tokens(const StreamParams &sp, uint8_t *ring, Control &ctl)
     const int at = lane * 8;
     const bool inside = at < p.d, turns = at < p.rot;
     const int o0 = kApart && turns ? lane * 4 : at, o1 = kApart && turns ? half + lane * 4 : at + 4;
-    float q_norm[8], k_norm[8];
-    auto load_norm = [&](const void *norm, float *w) {
+    float2 q_norm[4] = {}, k_norm[4] = {};
+    auto load_norm = [&](const void *norm, float2 (&to)[4]) {
         if (!norm || !inside) return;
         Quads<E> n;
+        float w[8];
         load_quads<E, kApart>(n, static_cast<const E *>(norm), o0, o1);
         n.a.get(w);
         n.b.get(w + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[e] = make_float2(w[2 * e], w[2 * e + 1]);
     };
     load_norm(p.q_norm, q_norm);
     load_norm(p.k_norm, k_norm);
@@ -123,15 +127,14 @@ __device__ void turn_tokens(const StreamParams &sp, uint8_t *ring, Control &ctl)
         const int stage = it % kStages;
         if (!wait_warp(&ctl.full[stage], (it / kStages) & 1, ctl)) return;
         uint8_t *token = ring + stage * sp.stage;
-        float c[4], s[4];
+        float c[4] = {}, s[4] = {};
         if (turns) {
             const float *table = reinterpret_cast<const float *>(token + sp.table_at) + lane * 4;
             *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(table);
             *reinterpret_cast<float4 *>(s) = *reinterpret_cast<const float4 *>(table + half);
         }
-        for (int head = group; head < heads; head += kGroups) {
-            E *row = reinterpret_cast<E *>(token) + head * p.d;
-            const bool is_q = head < p.n_q;
+        const float2 c2[2] = {make_float2(c[0], c[1]), make_float2(c[2], c[3])}, s2[2] = {make_float2(s[0], s[1]), make_float2(s[2], s[3])};
+        auto turn = [&](E *row, const float2 (&norm)[4], bool normed) {
             Quads<E> held;
             float h[8] = {};
             if (inside) {
@@ -139,39 +142,54 @@ __device__ void turn_tokens(const StreamParams &sp, uint8_t *ring, Control &ctl)
                 held.a.get(h);
                 held.b.get(h + 4);
             }
-            if (is_q ? p.q_norm : p.k_norm) {
+            float2 x[4];
+            float r = 1.f;
+            if (normed) {
                 float sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum += h[e] * h[e];
 #pragma unroll
                 for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(mask, sum, o);
-                const float r = rsqrtf(fmaf(sum, p.inv_d, p.eps));
+                r = rsqrtf(fmaf(sum, p.inv_d, p.eps));
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = h[e] * r * (is_q ? q_norm[e] : k_norm[e]);
+            for (int e = 0; e < 4; ++e) {
+                x[e] = make_float2(h[2 * e], h[2 * e + 1]);
+                if (normed) x[e] = mul2(mul2(x[e], make_float2(r, r)), norm[e]);
             }
             if (turns) {
                 if (PAIRS == kFar) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float a = h[e], b = h[4 + e];
-                        h[e] = a * c[e] - b * s[e];
-                        h[4 + e] = a * s[e] + b * c[e];
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 m = x[e], n = x[2 + e], t = mul2(n, s2[e]);
+                        x[e] = fma2(m, c2[e], make_float2(-t.x, -t.y));
+                        x[2 + e] = fma2(m, s2[e], mul2(n, c2[e]));
                     }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float a = h[2 * e], b = h[2 * e + 1];
-                        h[2 * e] = a * c[e] - b * s[e];
-                        h[2 * e + 1] = a * s[e] + b * c[e];
+                        const float m = x[e].x, n = x[e].y;
+                        x[e].x = m * c[e] - n * s[e];
+                        x[e].y = m * s[e] + n * c[e];
                     }
                 }
             }
             if (inside) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h[2 * e] = x[e].x;
+                    h[2 * e + 1] = x[e].y;
+                }
                 held.a.set(h);
                 held.b.set(h + 4);
                 store_quads<E, kApart>(held, row, o0, o1);
             }
-        }
+        };
+        int head = group;
+        E *row = reinterpret_cast<E *>(token) + head * p.d;
+        const int step = kGroups * p.d;
+        for (; head < p.n_q; head += kGroups, row += step) turn(row, q_norm, p.q_norm != nullptr);
+        for (; head < heads; head += kGroups, row += step) turn(row, k_norm, p.k_norm != nullptr);
         fence_proxy_async();               // the stores read through the async proxy
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(&ctl.done[stage]);
