@@ -999,8 +999,8 @@ int launch_attention(const lora_kv_pages *kv, const AttnParams &p, const Variant
 // lora_tree_attention_weights: a flag, and the logarithm of each row's sum.
 size_t log_bytes(int n_q_heads, int T) { return (16 + (size_t)T * n_q_heads * sizeof(float) + 15) & ~(size_t)15; }
 
-// Whether the weights are summed up from kept scores: up to 16 (fp32: 32) rows a kv head and request on average.
-int keep_rows(const lora_kv_pages *kv) { return kv->dtype == LORA_F32 ? 32 : 16; }
+// Whether the weights are summed up from kept scores: up to 16 (fp32: 128) rows a kv head and request on average.
+int keep_rows(const lora_kv_pages *kv) { return kv->dtype == LORA_F32 ? 128 : 16; }
 bool keeps_scores(const lora_kv_pages *kv, int group, int S, int T) { return (long long)T * group <= (long long)keep_rows(kv) * S; }
 // Whole lines of L2 a row: what has been summed up is dropped from it.
 long long score_pitch(const lora_kv_pages *kv, int max_pages) { return ((long long)max_pages * kv->page_size + 31) & ~31LL; }

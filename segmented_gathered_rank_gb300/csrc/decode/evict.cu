@@ -26,7 +26,7 @@ using namespace decode;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBits = 11, kBins = 1 << kBits, kCoarse = 8;      // kCoarse bins side by side are counted together as well
 constexpr int kMaxCluster = 8;
-constexpr int kSolo = 8192;
+constexpr int kSolo = 4096;
 constexpr int kMaxHeld = 16384;       // scores a block keeps in shared memory; more are read again
 
 constexpr int kMoveThreads = 256;

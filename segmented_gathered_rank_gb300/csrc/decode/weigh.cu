@@ -10,6 +10,7 @@
 // weigh_tc_kernel (weigh_tc.cu; bf16), weigh_kernel (fp32): else the scores are computed
 //   once more, keys at rest and rows going by, so that a key's sum stays in one block and
 //   its order is fixed.
+#include "tmem.cuh"
 #include "weigh.cuh"
 
 namespace lora {
@@ -18,13 +19,15 @@ namespace {
 using namespace decode;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kTile = 32;              // cached tokens a tile, one a lane
-constexpr int kWarpRows = 4, kRows = kWarps * kWarpRows;
+constexpr int kTile = 64;              // cached tokens a tile, two a lane
+constexpr int kWarpRows = 8, kRows = kWarps * kWarpRows;
 
 __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, float *weights, float decay) {
+    static_assert(kThreads >= kScanThreads, "start_block");
     extern __shared__ __align__(16) float smem[];
     __shared__ ScanShared scan;
-    __shared__ float sums[kWarps][kTile];
+    __shared__ float sums[kWarps][kTile], lse[kRows];
+    __shared__ int slots[kTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pitch = p.d + 4;
     float *ks = smem, *qs = smem + kTile * pitch;
     Cursor at;
@@ -34,50 +37,58 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
     if (!*p.computed) return;
     for (; cur.left > 0; cur.advance(p)) {
         const int c0 = cur.tile * kTile, rows = cur.r.n * p.group;
+        const long long first = (long long)cur.r.begin * p.n_q + cur.head * p.group;
         __syncthreads();
-        for (int x = tid; x < kTile * p.d; x += kThreads) {
-            const int j = x / p.d, e = x - j * p.d;
-            const long long slot = c0 + j < cur.r.len ? weight_at(p, cur.s, cur.r, cur.head, c0 + j) : -1;
-            ks[j * pitch + e] = slot >= 0 ? static_cast<const float *>(p.k)[slot * p.d + e] : 0.f;
-        }
-        float acc = 0.f;
+        if (tid < kTile) slots[tid] = c0 + tid < cur.r.len ? (int)weight_at(p, cur.s, cur.r, cur.head, c0 + tid) : -1;
+        __syncthreads();
+        for (int j = tid >> 3; j < kTile; j += kThreads / 8)
+            for (int e = (tid & 7) * 4; e < p.d; e += 32)
+                *reinterpret_cast<float4 *>(ks + j * pitch + e) =
+                    slots[j] >= 0 ? *reinterpret_cast<const float4 *>(static_cast<const float *>(p.k) + (long long)slots[j] * p.d + e)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        float acc[2] = {0.f, 0.f};
         for (int r0 = 0; r0 < rows; r0 += kRows) {
             __syncthreads();
-            for (int x = tid; x < kRows * p.d; x += kThreads) {
-                const int j = x / p.d, e = x - j * p.d, row = r0 + j, i = row / p.group;
-                const long long from = ((long long)(cur.r.begin + i) * p.n_q + cur.head * p.group + row - i * p.group) * p.d + e;
-                qs[j * pitch + e] = row < rows ? static_cast<const float *>(p.q)[from] : 0.f;
+            for (int j = tid >> 3; j < kRows; j += kThreads / 8) {
+                const int row = r0 + j, i = row / p.group;
+                const long long line = first + (long long)i * (p.n_q - p.group) + row;
+                for (int e = (tid & 7) * 4; e < p.d; e += 32)
+                    *reinterpret_cast<float4 *>(qs + j * pitch + e) =
+                        row < rows ? *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + line * p.d + e)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                if ((tid & 7) == 0) lse[j] = row < rows ? p.lse[line] : INFINITY;
             }
             __syncthreads();
-            float dot[kWarpRows] = {};
+            if (r0 + warp * kWarpRows >= rows) continue;
+            float2 dot[2][kWarpRows] = {};
             for (int e = 0; e < p.d; e += 4) {
                 const float4 k = *reinterpret_cast<const float4 *>(ks + lane * pitch + e);
+                const float4 l = *reinterpret_cast<const float4 *>(ks + (lane + 32) * pitch + e);
 #pragma unroll
                 for (int a = 0; a < kWarpRows; ++a) {
                     const float4 q = *reinterpret_cast<const float4 *>(qs + (warp * kWarpRows + a) * pitch + e);
-                    dot[a] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, dot[a]))));
+                    dot[0][a] = fma2(make_float2(k.z, k.w), make_float2(q.z, q.w), fma2(make_float2(k.x, k.y), make_float2(q.x, q.y), dot[0][a]));
+                    dot[1][a] = fma2(make_float2(l.z, l.w), make_float2(q.z, q.w), fma2(make_float2(l.x, l.y), make_float2(q.x, q.y), dot[1][a]));
                 }
             }
 #pragma unroll
             for (int a = 0; a < kWarpRows; ++a) {
                 const int row = r0 + warp * kWarpRows + a;
-                if (row >= rows) continue;
-                const int i = row / p.group;
-                const uint32_t see = seen_word(p, cur.r, i, c0);
-                const float lse = p.lse[(long long)(cur.r.begin + i) * p.n_q + cur.head * p.group + row - i * p.group];
-                if ((see >> lane) & 1) acc += exp2f(dot[a] * p.scale_log2 - lse);
+                if (row >= rows) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t see = seen_word(p, cur.r, row / p.group, c0 + h * 32);
+                    if ((see >> lane) & 1) acc[h] += exp2f((dot[h][a].x + dot[h][a].y) * p.scale_log2 - lse[warp * kWarpRows + a]);
+                }
             }
         }
-        sums[warp][lane] = acc;
+        sums[warp][lane] = acc[0];
+        sums[warp][lane + 32] = acc[1];
         __syncthreads();
-        const int c = c0 + tid;
-        if (tid < kTile && c < cur.r.len) {
-            const long long slot = weight_at(p, cur.s, cur.r, cur.head, c);
-            if (slot >= 0) {
-                float w = c < cur.r.len - cur.r.n && decay > 0.f ? weights[slot] * decay : 0.f;
-                for (int x = 0; x < kWarps; ++x) w += sums[x][tid];
-                weights[slot] = w;
-            }
+        if (tid < kTile && slots[tid] >= 0) {
+            float w = c0 + tid < cur.r.len - cur.r.n && decay > 0.f ? weights[slots[tid]] * decay : 0.f;
+            for (int x = 0; x < kWarps; ++x) w += sums[x][tid];
+            weights[slots[tid]] = w;
         }
     }
 }

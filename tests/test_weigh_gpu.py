@@ -89,7 +89,8 @@ CASES = [   # requests (drafted, cached), n_q, n_kv, d, page, mask, decay
     ([(33, 700), (20, 1500), (0, 10), (64, 64)], 16, 4, 128, 64, "tree", 1.0), ([(64, 3000)], 32, 8, 128, 16, None, 0.0),
     ([(100, 400), (3, 90)], 8, 1, 64, 8, "random", 0.7), ([(129, 200)], 4, 2, 128, 16, None, 1.0), ([(200, 1200), (90, 900)], 2, 1, 64, 128, None, 0.9),
     ([(40, 333)], 6, 3, 80, 16, "tree", 1.0), ([(50, 600), (60, 61)], 4, 1, 256, 1, "tree", 0.5), ([(70, 500)], 4, 4, 192, 32, None, 0.3),
-    ([(30, 260), (11, 400)], 14, 2, 128, 4, "random", 1.0)]
+    ([(30, 260), (11, 400)], 14, 2, 128, 4, "random", 1.0), ([(70, 300)], 12, 3, 80, 16, "tree", 0.8),
+    ([(90, 91), (150, 500)], 6, 2, 112, 2, None, 1.0), ([(65, 129)], 32, 8, 24, 8, "random", 0.0)]
 
 
 @pytest.mark.parametrize("dtype", [I.BF16, I.F32])
