@@ -320,6 +320,12 @@ int lora_layer_forward_fp8(lora_pool *pool, int matrix, const void *x, const voi
  *                         keys and values to a paged cache
  *   lora_tree_attention   attention of the drafted tokens over that cache
  *
+ * and, for long streams of text, images and video whose cache stays bounded,
+ *
+ *   lora_kv_append_axes          append with positions of several axes
+ *   lora_tree_attention_weights  attention that sums up each cached token's weight
+ *   lora_kv_evict                eviction of the tokens with the least
+ *
  * They take no pool: element types are arguments (LORA_F32 or LORA_BF16) and
  * all memory is the caller's.  Arithmetic is fp32 (products of bf16 operands
  * are exact in it); outputs are rounded once on store.
@@ -456,7 +462,8 @@ int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, c
  *            aligned; a prefix token's is what earlier calls left there.
  *   decay    0..1.   out  apart from q.
  *   workspace  lora_tree_attention_weights_workspace_size() bytes; it grows with S, T
- *            and max_pages, and one of the largest call serves every smaller one.
+ *            and max_pages (scores of up to 16 rows a kv head and request, 128 in an fp32
+ *            cache, are kept in it), and one of the largest call serves every smaller one.
  * A page that several requests of the call share ends up with either's weights.  A
  * page outside the cache has none.  Errors, device-detected ones and bad tables as
  * lora_tree_attention (where nothing is computed, weights stay as well).

@@ -6,7 +6,9 @@
 // each head read once and written once: memory is the bound for large T, the
 // chain of dependent loads (position -> table row; slot -> address) for small.
 // Measured, bf16, heads of 128: 1 token 2.0 us, 256 tokens of 48 heads with norms
-// 3.1 us, 8192 tokens 39.8 us (5.2 TB/s).
+// 3.1 us, 8192 tokens 39.8 us (5.2 TB/s).  With axes 1 token 2.6 us: a position and a
+// table entry a pair where a quad's pairs differ in axis, one of each where they do not.
+// Many tokens with axes go to append_stream.cu.
 //
 // Layout: LANES threads (the power of two >= d/8) hold one head, 8 elements each in two
 // quads that are each other's partners in the rotation, so a pair meets in a thread (or,

@@ -6,6 +6,14 @@
 // 4-byte copies, once for all heads), eight warps turn one token in place, and bulk stores
 // take its queries to q_out and each key and value head to its slot.  Values never pass
 // through registers.
+//
+// 8192 tokens of 48 heads of 128 with norms, three axes in turn: 34.7 us, 5.9 TB/s, 0.88
+// of the measured copy (append.cu's kernel, whose halves are read in 8-byte pieces and
+// whose blocks end with their loads: 71 us).  Instructions come next: schedulers issue in
+// two cycles of three.  Four stages and three blocks a SM; 5 stages 35.1 us, 3 stages and
+// four blocks 39.1, 6 stages and two blocks 37.2.  Several small tokens a stage gained
+// little (12 heads 20.5 -> 16.9 us, 48 heads of 64 29.0 -> 27.9) and cost the larger ones
+// (37.4 -> 41.0).
 #include "append.cuh"
 #include "tc_common.cuh"
 #include "tmem.cuh"
@@ -22,10 +30,11 @@ constexpr int kPerSm = 3;
 constexpr int kThird = 75 << 10;          // of a SM's shared memory
 constexpr int kMaxToken = 26 << 10;       // bytes of a token's heads: two blocks a SM
 // Bytes of all heads from which on this kernel takes a call.  It and append.cu's, bf16, halves, norms, three axes in turn:
-// 48 heads of 128, 512 tokens (6 MB) 6.2 and 6.0 us, 1024 tokens 7.7 and 10.3, 8192 tokens 37.4 and 71.3; neighbours, 1024
-// tokens 7.6 and 7.8, 8192 tokens 36.8 and 54.5; 12 heads of 128, 2048 tokens (6 MB) 7.0 and 7.0, 4096 tokens 11.6 and
-// 12.1, 8192 tokens 20.5 and 24.5; 48 heads of 64, 1024 tokens (6 MB) 6.7 and 6.5, 2048 tokens 9.4 and 11.1; 48 heads of
-// 80, 1024 tokens (8 MB) 7.9 and 9.6.
+// 48 heads of 128, 512 tokens (6 MB) 6.2 and 6.0 us, 1024 tokens 7.3 and 10.3, 8192 tokens 34.7 and 71.3; neighbours, 608
+// tokens (7.3 MB) 6.1 and 5.4, 1024 tokens 7.6 and 8.5, 8192 tokens 35.6 and 54.5; 12 heads of 128, 2048 tokens (6 MB)
+// 7.0 and 7.0, 4096 tokens 11.6 and 12.1, 8192 tokens 19.8 and 24.5; 48 heads of 64, 1024 tokens (6 MB) 6.7 and 6.5, 2048
+// tokens 8.8 and 11.1; 48 heads of 80, 1024 tokens (8 MB) 7.2 and 9.6; fp32, 48 heads of 128, 512 tokens (12 MB) 6.2 and
+// 6.4, 8192 tokens 68 and 87.
 constexpr long long kMinBytes = 7 << 20;
 
 struct StreamParams {

@@ -16,6 +16,14 @@
 //   [j, j + n) is read whole before it is written: what a round overwrites, no later round
 //   reads.  Column ranges move apart from one another, so blocks never wait for one another,
 //   and the next rounds are on their way while one is written.
+//
+// Memory is the bound of large calls: 64 requests over <= 4352, 4096 kept, 8 heads of 128,
+// 80 us for 388 MB (4.8 TB/s); the select is 14 of them (its 92 blocks wait for one another's
+// barriers and loads), the rest the ranges' last rounds.  Small calls are chains: one request
+// 1088 -> 1024 11.9 us, of which the select is 6.6: lengths, page ids, scores, two or three
+// passes of 0.7 to 1.4, the list.  Four of 32768 -> 2048: 40 us, 20 of them for passes over
+// scores in clusters of four blocks.  In one kernel, a cluster a unit, the three took 117,
+// 13.7 and 116 us: whole units are too large a piece to spread evenly.
 #include "kv_copy.cuh"
 
 namespace lora {
@@ -26,6 +34,8 @@ using namespace decode;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBits = 11, kBins = 1 << kBits, kCoarse = 8;      // kCoarse bins side by side are counted together as well
 constexpr int kMaxCluster = 8;
+// Alone and in a cluster, four requests, half of them kept: 2100 tokens 26.8 and 27.6 us, 4200 31.9 and 30.2, 8100 38.6
+// and 31.6, 16000 49.4 and 34.5.
 constexpr int kSolo = 4096;
 constexpr int kMaxHeld = 16384;       // scores a block keeps in shared memory; more are read again
 

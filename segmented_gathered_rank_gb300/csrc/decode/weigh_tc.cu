@@ -8,6 +8,13 @@
 // exponentials.  Rows that fit in the ring of query tiles stay in it for all key tiles of
 // a kv head.  Keys are copied while the attention's last kernel runs; what reads its sums
 // waits for it.
+//
+// 8 requests of 64 tokens over <= 16384 (256 rows, 8 kv heads of 128): about 27 us of the
+// call's 85.5, where the products would take 8 and the exponentials, 16 a cycle and SM, 15.
+// A pair of key tiles against 128 rows takes some 2200 cycles, 2048 of them exponentials;
+// the rest is the start (scan, first copies, 4 us) and the cut into whole key tiles.
+// Exponentials on the multiply-add pipe for a quarter of the columns were slower (90 us),
+// as were loads of 32 columns that nothing ran under (89).
 #include <type_traits>
 
 #include "kv_copy.cuh"
