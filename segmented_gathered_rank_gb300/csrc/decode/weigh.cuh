@@ -66,7 +66,7 @@ __device__ __forceinline__ long long weight_at(const AttnParams &p, int s, const
 
 constexpr int kWeighTile = 256, kWeighRows = 128;      // of weigh_tc_kernel: cached tokens a tile, rows a place of the list
 
-// In places of all rows: what starting a kv head costs (1 or 2 is the same, 0 leaves the last blocks 10 us behind).
+// In places of all rows: what starting a kv head costs (8 requests of 64 tokens over <= 16384: 0, 1, 2 places 94.7, 85.9, 86.3 us).
 constexpr int kWeighUnitCost = 1;
 
 // weigh_tc.cu: a bf16 cache; maps as for launch_attention_tc.

@@ -166,7 +166,8 @@ template <int D, bool TMA>
 __device__ void issue(const AttnParams &p, KeyCursor cur, uint8_t *keys, uint8_t *queries, Control<D> &ctl) {
     using Sh = Shape<D>;
     constexpr uint32_t kIdesc = idesc_bf16_f32(kTile, kTile);
-    const uint32_t k_base = smem_u32(keys), q_base = smem_u32(queries);
+    constexpr uint32_t kSwizzled = (1024u >> 4) | (1u << 14) | (2u << 29);      // descriptor bits 32..63
+    const uint32_t k_lo = (uint32_t)desc_kmajor_sw128(smem_u32(keys)), q_lo = (uint32_t)desc_kmajor_sw128(smem_u32(queries));
     const int steps = (p.d + 15) >> 4;
     uint32_t k_seq = 0, q0 = 0, s_seq[2] = {0, 0};
     while (cur.left > 0) {
@@ -179,20 +180,28 @@ __device__ void issue(const AttnParams &p, KeyCursor cur, uint8_t *keys, uint8_t
             if (!TMA) fence_proxy_async();
             for (int row_tile = 0; row_tile < cur.r.row_tiles; ++row_tile) {
                 const uint32_t q = q0 + run.number(cur, t, row_tile), slot = q % Sh::kQueries;
-                if (!wait_bar<D>(&ctl.q_full[slot], (q / Sh::kQueries) & 1, ctl)) return;
-                fence_proxy_async();         // ordinary copies; the products read through the async proxy
+                if (!run.stays || t == 0) {
+                    if (!wait_bar<D>(&ctl.q_full[slot], (q / Sh::kQueries) & 1, ctl)) return;
+                    fence_proxy_async();     // ordinary copies; the products read through the async proxy
+                }
                 fence_after_sync();
                 for (int w = 0; w < groups; ++w) {
                     const uint32_t b = s_seq[w] & 1;
                     if (!wait_bar<D>(&ctl.s_empty[w][b], ((s_seq[w] >> 1) & 1) ^ 1, ctl)) return;
                     ++s_seq[w];
                     fence_after_sync();
-                    const uint64_t kd = desc_kmajor_sw128(k_base + (stage * 2 + w) * Sh::kBytes);
-                    const uint64_t qd = desc_kmajor_sw128(q_base + slot * Sh::kBytes);
+                    // descriptors: 32-bit sums of 16-byte units to a constant upper half
+                    const uint32_t k = k_lo + (stage * 2 + w) * (Sh::kBytes / 16), q_at = q_lo + slot * (Sh::kBytes / 16);
                     const uint32_t d = ctl.tmem + (w * 2 + b) * kTile;
-                    for (int ks = 0; ks < steps; ++ks) {
-                        const uint64_t step = (uint64_t)((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4;
-                        mma_bf16(d, kd + step, qd + step, kIdesc, ks > 0);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks) {
+                        if (ks >= steps) break;
+                        const uint32_t step = ((ks >> 2) * (kTile * 128) + (ks & 3) * 32) >> 4;
+                        asm volatile(
+                            "{\n.reg .pred p;\n.reg .b64 a, b;\nsetp.ne.b32 p, %5, 0;\nmov.b64 a, {%1, %3};\nmov.b64 b, {%2, %3};\n"
+                            "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+                            "r"(k + step), "r"(q_at + step), "n"(kSwizzled), "n"(kIdesc), "r"(ks > 0 ? 1u : 0u)
+                            : "memory");
                     }
                     mma_commit(&ctl.s_full[w][b]);
                 }
