@@ -34,7 +34,7 @@ using namespace decode;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBits = 11, kBins = 1 << kBits, kCoarse = 8;      // kCoarse bins side by side are counted together as well
 constexpr int kMaxCluster = 8;
-// Alone and in a cluster, four requests, half of them kept: 2100 tokens 26.8 and 27.6 us, 4200 31.9 and 30.2, 8100 38.6
+// Alone and in a cluster, four requests, 2048 kept, 8 heads: 2100 tokens 26.8 and 27.6 us, 4200 31.9 and 30.2, 8100 38.6
 // and 31.6, 16000 49.4 and 34.5.
 constexpr int kSolo = 4096;
 constexpr int kMaxHeld = 16384;       // scores a block keeps in shared memory; more are read again
