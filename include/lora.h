@@ -403,7 +403,7 @@ int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, const void 
  *              of the head, axes taken in turn, or any other order.  A text token has
  *              the same position on every axis.
  * Everything else, errors included, as lora_kv_append; an axis that no pair names
- * is not looked at.
+ * is not looked at.  Device-detected also: LORA_DEV_WAIT_TIMEOUT.
  */
 enum { LORA_MAX_AXES = 4 };
 int lora_kv_append_axes(const lora_kv_pages *kv, const void *q, int ld_q, const void *k, int ld_k, const void *v,

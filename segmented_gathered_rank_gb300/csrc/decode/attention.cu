@@ -127,9 +127,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, MmaCon
     return __all_sync(0xffffffffu, wait_bar(bar, parity, ctl));
 }
 
-// Four consumer warps; each takes kWarpKeys of a stage's tokens for all rows of
-// the unit, with a maximum, sum and output of its own (so a tile needs no exchange
-// between warps), joined in shared memory when the block leaves the unit.
 // Kept scores leave L2 last.
 __device__ __forceinline__ void store_kept(float *dst, float4 s) {
     uint64_t policy;
@@ -138,7 +135,10 @@ __device__ __forceinline__ void store_kept(float *dst, float4 s) {
                  : "memory");
 }
 
-// KEEP: the scores go to p.scores as well.
+// Four consumer warps; each takes kWarpKeys of a stage's tokens for all rows of
+// the unit, with a maximum, sum and output of its own (so a tile needs no exchange
+// between warps), joined in shared memory when the block leaves the unit.  KEEP: the
+// scores go to p.scores as well.
 template <int D, bool TMA, bool KEEP>
 __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t *smem, MmaControl &ctl) {
     using Sh = MmaShape<D, TMA>;

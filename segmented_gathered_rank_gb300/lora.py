@@ -453,6 +453,8 @@ def lora_kv_evict(kv, scores, weights, S, kv_lens, page_table, max_pages, keep, 
                   stream=None) -> None:
     """Every kv head keeps its keep[s] tokens of the greatest scores (float [n_pages, n_kv_heads, page_size]), in order;
     weights (None, scores itself or another such tensor) move along; kept gets the indices, new_lens the lengths."""
+    if kept is not None and kept.numel() < S * kv.n_kv_heads * ld_kept:
+        raise ValueError("kept does not hold S x n_kv_heads x ld_kept indices")
     rc = _lib.lora_kv_evict(kv.address, _plane(kv, scores), _plane(kv, weights), S, _ptr(kv_lens), _ptr(page_table), max_pages,
                             _ptr(keep), first, recent, _ptr(kept), ld_kept, _ptr(new_lens), _stream_ptr(stream))
     if rc:

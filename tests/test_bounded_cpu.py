@@ -107,6 +107,8 @@ def test_planes_that_are_too_small_are_refused_in_python():
         L.lora_kv_evict(kv, Cuda(4, 2, 7), None, *args, stream=0)
     with pytest.raises(ValueError):
         L.lora_kv_evict(kv, Cuda(4, 2, 8), Cuda(63), *args, stream=0)
+    with pytest.raises(ValueError):
+        L.lora_kv_evict(kv, Cuda(4, 2, 8), None, *args[:7], Cuda(2, 2, 7), 8, Cuda(2), stream=0)
 
 
 def weigh(kv, weights=P, decay=1.0, q=P, n_q=4, starts=P, S=2, T=2, lens=P, table=P, max_pages=4, mask=None, words=0, scale=0.1, out=P,
