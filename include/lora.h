@@ -399,18 +399,29 @@ int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, const void 
  * positions[t][pair_axis[i]],
  *   c_i = cos_sin[positions[t][pair_axis[i]]][i], s_i = .. [rot_dim/2 + i].
  *   positions  T x n_axes device int32.   n_axes  1..LORA_MAX_AXES.
- *   pair_axis  HOST array of rot_dim/2 axes below n_axes, read during the call: sections
- *              of the head, axes taken in turn, or any other order.  A text token has
- *              the same position on every axis.
+ *   pair_axis  the axes of the rot_dim/2 pairs, below n_axes: sections of the head, axes
+ *              taken in turn, or any other order.  A text token has the same position on
+ *              every axis.
  * Everything else, errors included, as lora_kv_append; an axis that no pair names
  * is not looked at.  Device-detected also: LORA_DEV_WAIT_TIMEOUT.
+ *
+ * This call and the two others of a bounded cache take their arguments as a struct, which
+ * is read during the call only: they have about twenty, which a struct names, and which a
+ * binding can pass as one.
  */
-enum { LORA_MAX_AXES = 4 };
-int lora_kv_append_axes(const lora_kv_pages *kv, const void *q, int ld_q, const void *k, int ld_k, const void *v,
-                        int ld_v, int T, int n_q_heads, const int *positions, int n_axes,
-                        const unsigned char *pair_axis, const long long *slots, const float *cos_sin, int n_pos,
-                        int rot_dim, int interleaved, const void *q_norm, const void *k_norm, float eps, void *q_out,
-                        lora_stream stream);
+enum { LORA_MAX_AXES = 4, LORA_MAX_PAIRS = 128 };
+typedef struct lora_append_axes {
+    const void *q, *k, *v;
+    void *q_out;
+    const int *positions;
+    const long long *slots;
+    const float *cos_sin;
+    const void *q_norm, *k_norm;
+    int ld_q, ld_k, ld_v, T, n_q_heads, n_axes, n_pos, rot_dim, interleaved;
+    float eps;
+    unsigned char pair_axis[LORA_MAX_PAIRS];
+} lora_append_axes;
+int lora_kv_append_axes(const lora_kv_pages *kv, const lora_append_axes *args, lora_stream stream);
 
 /* Bytes of device workspace that lora_tree_attention needs at most for up to T
  * drafted tokens of up to S requests (0 on a bad argument): a workspace of the
@@ -468,11 +479,18 @@ int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, c
  * page outside the cache has none.  Errors, device-detected ones and bad tables as
  * lora_tree_attention (where nothing is computed, weights stay as well).
  */
+typedef struct lora_attention_weights {
+    float *weights;
+    const void *q;
+    const int *seg_starts, *kv_lens, *page_table;
+    const long long *tree_mask;
+    void *out, *workspace;
+    size_t ws_bytes;
+    int n_q_heads, S, T, max_pages, mask_words;
+    float scale, decay;
+} lora_attention_weights;
 size_t lora_tree_attention_weights_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T, int max_pages);
-int lora_tree_attention_weights(const lora_kv_pages *kv, float *weights, float decay, const void *q, int n_q_heads,
-                                const int *seg_starts, int S, int T, const int *kv_lens, const int *page_table,
-                                int max_pages, const long long *tree_mask, int mask_words, float scale, void *out,
-                                void *workspace, size_t ws_bytes, lora_stream stream);
+int lora_tree_attention_weights(const lora_kv_pages *kv, const lora_attention_weights *args, lora_stream stream);
 
 /*
  * Eviction from the paged cache.  Request s has kv_lens[s] cached tokens, in the
@@ -500,9 +518,14 @@ int lora_tree_attention_weights(const lora_kv_pages *kv, float *weights, float d
  * Device-detected: LORA_DEV_BAD_LENGTH (a length beyond the table or below 0, a budget
  * beyond ld_kept), LORA_DEV_BAD_PAGE; the request concerned stays as it is.
  */
-int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float *weights, int S, const int *kv_lens,
-                  const int *page_table, int max_pages, const int *keep, int first, int recent, int *kept, int ld_kept,
-                  int *new_lens, lora_stream stream);
+typedef struct lora_eviction {
+    const float *scores;
+    float *weights;
+    const int *kv_lens, *page_table, *keep;
+    int *kept, *new_lens;
+    int S, max_pages, first, recent, ld_kept;
+} lora_eviction;
+int lora_kv_evict(const lora_kv_pages *kv, const lora_eviction *args, lora_stream stream);
 
 /*
  * Synchronise the device, read the pool's device status word into

@@ -243,7 +243,7 @@ void launch(const AppendParams &p, int T, bool interleaved, cudaStream_t st) {
     else launch<E, 32, AXES>(p, T, interleaved, st);
 }
 
-// pair_axis: on the host, NULL for one position a token.
+// pair_axis: NULL for one position a token.
 int append(const lora_kv_pages *kv, const void *q, int ld_q, const void *k, int ld_k, const void *v, int ld_v, int T,
            int n_q_heads, const int *positions, int n_axes, const unsigned char *pair_axis, const long long *slots,
            const float *cos_sin, int n_pos, int rot_dim, int interleaved, const void *q_norm, const void *k_norm, float eps,
@@ -324,12 +324,8 @@ extern "C" int lora_kv_append(const lora_kv_pages *kv, const void *q, int ld_q, 
                   q_norm, k_norm, eps, q_out, (cudaStream_t)stream);
 }
 
-extern "C" int lora_kv_append_axes(const lora_kv_pages *kv, const void *q, int ld_q, const void *k, int ld_k, const void *v,
-                                   int ld_v, int T, int n_q_heads, const int *positions, int n_axes,
-                                   const unsigned char *pair_axis, const long long *slots, const float *cos_sin, int n_pos,
-                                   int rot_dim, int interleaved, const void *q_norm, const void *k_norm, float eps, void *q_out,
-                                   lora_stream stream) {
-    if (n_axes < 1 || n_axes > LORA_MAX_AXES || !pair_axis) return LORA_ERR_ARG;
-    return append(kv, q, ld_q, k, ld_k, v, ld_v, T, n_q_heads, positions, n_axes, pair_axis, slots, cos_sin, n_pos, rot_dim,
-                  interleaved, q_norm, k_norm, eps, q_out, (cudaStream_t)stream);
+extern "C" int lora_kv_append_axes(const lora_kv_pages *kv, const lora_append_axes *a, lora_stream stream) {
+    if (!a || a->n_axes < 1 || a->n_axes > LORA_MAX_AXES) return LORA_ERR_ARG;
+    return append(kv, a->q, a->ld_q, a->k, a->ld_k, a->v, a->ld_v, a->T, a->n_q_heads, a->positions, a->n_axes, a->pair_axis, a->slots,
+                  a->cos_sin, a->n_pos, a->rot_dim, a->interleaved, a->q_norm, a->k_norm, a->eps, a->q_out, (cudaStream_t)stream);
 }

@@ -1140,12 +1140,9 @@ extern "C" size_t lora_tree_attention_weights_workspace_size(const lora_kv_pages
     return base + log_bytes(n_q_heads, T) + score_bytes(kv, n_q_heads, S, T, max_pages) + 144;
 }
 
-extern "C" int lora_tree_attention_weights(const lora_kv_pages *kv, float *weights, float decay, const void *q, int n_q_heads,
-                                           const int *seg_starts, int S, int T, const int *kv_lens, const int *page_table,
-                                           int max_pages, const long long *tree_mask, int mask_words, float scale, void *out,
-                                           void *workspace, size_t ws_bytes, lora_stream stream) {
-    if (!(decay >= 0.f && decay <= 1.f)) return LORA_ERR_ARG;
-    if (T > 0 && (!weights || !aligned16(weights))) return LORA_ERR_ARG;
-    return attend(kv, weights, decay, q, n_q_heads, seg_starts, S, T, kv_lens, page_table, max_pages, tree_mask, mask_words, scale, out,
-                  workspace, ws_bytes, (cudaStream_t)stream);
+extern "C" int lora_tree_attention_weights(const lora_kv_pages *kv, const lora_attention_weights *a, lora_stream stream) {
+    if (!a || !(a->decay >= 0.f && a->decay <= 1.f)) return LORA_ERR_ARG;
+    if (a->T > 0 && (!a->weights || !aligned16(a->weights))) return LORA_ERR_ARG;
+    return attend(kv, a->weights, a->decay, a->q, a->n_q_heads, a->seg_starts, a->S, a->T, a->kv_lens, a->page_table, a->max_pages,
+                  a->tree_mask, a->mask_words, a->scale, a->out, a->workspace, a->ws_bytes, (cudaStream_t)stream);
 }

@@ -528,9 +528,13 @@ cudaError_t launch_move(EvictParams p, long long units, cudaStream_t st) {
 
 using namespace lora;
 
-extern "C" int lora_kv_evict(const lora_kv_pages *kv, const float *scores, float *weights, int S, const int *kv_lens,
-                             const int *page_table, int max_pages, const int *keep, int first, int recent, int *kept,
-                             int ld_kept, int *new_lens, lora_stream stream) {
+extern "C" int lora_kv_evict(const lora_kv_pages *kv, const lora_eviction *a, lora_stream stream) {
+    if (!a) return LORA_ERR_ARG;
+    const float *const scores = a->scores;
+    float *const weights = a->weights;
+    const int *const kv_lens = a->kv_lens, *const page_table = a->page_table, *const keep = a->keep;
+    int *const kept = a->kept, *const new_lens = a->new_lens;
+    const int S = a->S, max_pages = a->max_pages, first = a->first, recent = a->recent, ld_kept = a->ld_kept;
     const int rc = decode::check_kv(kv, 0);
     if (rc) return rc;
     if (S < 0 || max_pages < 0 || first < 0 || recent < 0 || ld_kept < 0) return LORA_ERR_ARG;

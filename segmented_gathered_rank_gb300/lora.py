@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -126,12 +127,14 @@ class KvPages(ctypes.Structure):
 _sig("lora_w4_matvec", _I, _I, _P, _I, _I, _P, _P, _P, _I, _I, _P, _P)
 _sig("lora_kv_append", _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, _I, _I, _I, _P, _P,
      ctypes.c_float, _P, _P)
-_sig("lora_kv_append_axes", _I, _P, _P, _I, _P, _I, _P, _I, _I, _I, _P, _I, ctypes.c_char_p, _P, _P, _I, _I, _I, _P, _P,
-     ctypes.c_float, _P, _P)
+# The calls of a bounded cache take a struct, packed here: their arguments one by one take ctypes longer than a launch.
+_AXES = struct.Struct("@9P9if128s")             # lora_append_axes
+_WEIGHTS = struct.Struct("@8PN5i2f4x")          # lora_attention_weights
+_EVICTION = struct.Struct("@7P5i4x")            # lora_eviction
+_sig("lora_kv_append_axes", _I, _P, ctypes.c_char_p, _P)
 _sig("lora_tree_attention_weights_workspace_size", ctypes.c_size_t, _P, _I, _I, _I, _I)
-_sig("lora_tree_attention_weights", _I, _P, _P, ctypes.c_float, _P, _I, _P, _I, _I, _P, _P, _I, _P, _I, ctypes.c_float, _P, _P,
-     ctypes.c_size_t, _P)
-_sig("lora_kv_evict", _I, _P, _P, _P, _I, _P, _P, _I, _P, _I, _I, _P, _I, _P, _P)
+_sig("lora_tree_attention_weights", _I, _P, ctypes.c_char_p, _P)
+_sig("lora_kv_evict", _I, _P, ctypes.c_char_p, _P)
 _sig("lora_tree_attention_workspace_size", ctypes.c_size_t, _P, _I, _I, _I)
 _sig("lora_tree_attention", _I, _P, _P, _I, _P, _I, _I, _P, _P, _I, _P, _I, ctypes.c_float, _P, _P,
      ctypes.c_size_t, _P)
@@ -178,6 +181,25 @@ def _rows(t):
         raise ValueError("expected a CUDA matrix with contiguous rows")
     # a single row's stride means nothing, and need not be the width (a transposed column's is 1)
     ld = t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if ld > 0x7fffffff:
+        raise ValueError("rows are further apart than an int says")
+    return t.data_ptr(), ld
+
+
+def _address(t):
+    """_ptr for a packed struct: NULL is 0."""
+    return 0 if t is None else _ptr(t)
+
+
+def _matrix(t):
+    """_rows for a packed struct, with one look at the strides."""
+    if t is None:
+        return 0, 0
+    strides = t.stride()
+    if not (t.is_cuda and len(strides) == 2 and strides[1] == 1):
+        raise ValueError("expected a CUDA matrix with contiguous rows")
+    rows, width = t.shape
+    ld = strides[0] if rows > 1 else width      # a single row's stride means nothing
     if ld > 0x7fffffff:
         raise ValueError("rows are further apart than an int says")
     return t.data_ptr(), ld
@@ -397,14 +419,14 @@ def lora_kv_append_axes(kv, q, k, v, T, n_q_heads, positions, n_axes, pair_axis,
                         q_out, q_norm=None, k_norm=None, eps=1e-6, stream=None) -> None:
     """lora_kv_append with n_axes positions a token (int32 [T, n_axes]); pair_axis: the axis of each rotated pair, as
     bytes (quickest) or a sequence of whole numbers."""
-    (pq, ld_q), (pk, ld_k), (pv, ld_v) = _rows(q), _rows(k), _rows(v)
-    if pair_axis is not None:
-        pair_axis = pair_axis if type(pair_axis) is bytes else bytes(list(pair_axis))
-        if len(pair_axis) < rot_dim // 2:
-            raise ValueError("pair_axis names fewer pairs than rot_dim has")
-    rc = _lib.lora_kv_append_axes(kv.address, pq, ld_q, pk, ld_k, pv, ld_v, T, n_q_heads, _ptr(positions), n_axes, pair_axis,
-                                  _ptr(slots), _ptr(cos_sin), n_pos, rot_dim, 1 if interleaved else 0, _ptr(q_norm),
-                                  _ptr(k_norm), eps, _ptr(q_out), _stream_ptr(stream))
+    (pq, ld_q), (pk, ld_k), (pv, ld_v) = _matrix(q), _matrix(k), _matrix(v)
+    if type(pair_axis) is not bytes:
+        pair_axis = bytes(list(pair_axis))
+    if len(pair_axis) < rot_dim // 2:
+        raise ValueError("pair_axis names fewer pairs than rot_dim has")
+    args = _AXES.pack(pq, pk, pv, _address(q_out), _address(positions), _address(slots), _address(cos_sin), _address(q_norm),
+                      _address(k_norm), ld_q, ld_k, ld_v, T, n_q_heads, n_axes, n_pos, rot_dim, 1 if interleaved else 0, eps, pair_axis)
+    rc = _lib.lora_kv_append_axes(kv.address, args, _stream_ptr(stream))
     if rc:
         _check(rc, "lora_kv_append_axes")
 
@@ -429,7 +451,7 @@ def _plane(kv, t):
     """Pointer of one fp32 number a slot and kv head of the cache."""
     if t is not None and t.numel() < kv.slots:
         raise ValueError("expected n_pages x n_kv_heads x page_size numbers")
-    return _ptr(t)
+    return _address(t)
 
 
 def lora_tree_attention_weights_workspace_size(kv, n_q_heads, S, T, max_pages) -> int:
@@ -442,9 +464,9 @@ def lora_tree_attention_weights(kv, weights, decay, q, n_q_heads, seg_starts, S,
     [n_pages, n_kv_heads, page_size])."""
     if ws_bytes is None:
         ws_bytes = workspace.nbytes
-    rc = _lib.lora_tree_attention_weights(kv.address, _plane(kv, weights), decay, _ptr(q), n_q_heads, _ptr(seg_starts), S, T, _ptr(kv_lens),
-                                          _ptr(page_table), max_pages, _ptr(tree_mask), mask_words, scale, _ptr(out), _ptr(workspace),
-                                          ws_bytes, _stream_ptr(stream))
+    args = _WEIGHTS.pack(_plane(kv, weights), _address(q), _address(seg_starts), _address(kv_lens), _address(page_table), _address(tree_mask),
+                         _address(out), _address(workspace), ws_bytes, n_q_heads, S, T, max_pages, mask_words, scale, decay)
+    rc = _lib.lora_tree_attention_weights(kv.address, args, _stream_ptr(stream))
     if rc:
         _check(rc, "lora_tree_attention_weights")
 
@@ -455,7 +477,8 @@ def lora_kv_evict(kv, scores, weights, S, kv_lens, page_table, max_pages, keep, 
     weights (None, scores itself or another such tensor) move along; kept gets the indices, new_lens the lengths."""
     if kept is not None and kept.numel() < S * kv.n_kv_heads * ld_kept:
         raise ValueError("kept does not hold S x n_kv_heads x ld_kept indices")
-    rc = _lib.lora_kv_evict(kv.address, _plane(kv, scores), _plane(kv, weights), S, _ptr(kv_lens), _ptr(page_table), max_pages,
-                            _ptr(keep), first, recent, _ptr(kept), ld_kept, _ptr(new_lens), _stream_ptr(stream))
+    args = _EVICTION.pack(_plane(kv, scores), _plane(kv, weights), _address(kv_lens), _address(page_table), _address(keep), _address(kept),
+                          _address(new_lens), S, max_pages, first, recent, ld_kept)
+    rc = _lib.lora_kv_evict(kv.address, args, _stream_ptr(stream))
     if rc:
         _check(rc, "lora_kv_evict")

@@ -1,21 +1,31 @@
 """Host-side checks of the calls of a bounded cache: refused before any launch, without a GPU (the pointers are host
 memory that nothing reads)."""
 import ctypes
+import re
 
 import numpy as np
 import pytest
 
 from segmented_gathered_rank_gb300 import lora as L
-from tests.test_decode_binding_cpu import Cuda
+from tests.test_decode_binding_cpu import Cuda as Whole
 from tests.test_decode_cpu import BAD_PAGES, P, pages
 
 AXES = bytes(i % 3 for i in range(64))
 
 
+class Cuda(Whole):
+    def stride(self, i=None):
+        return self._stride if i is None else self._stride[i]
+
+
+def call(name, kv, layout, *values):
+    return getattr(L._lib, name)(ctypes.addressof(kv), layout.pack(*(0 if v is None else v for v in values)), None)
+
+
 def axes(kv, q=P, ld_q=512, k=P, ld_k=256, v=P, ld_v=256, T=3, n_q=4, positions=P, n_axes=3, pair_axis=AXES, slots=P, cos_sin=P,
          n_pos=16, rot=128, interleaved=False, q_norm=None, k_norm=None, eps=1e-6, q_out=P):
-    return L._lib.lora_kv_append_axes(ctypes.byref(kv), q, ld_q, k, ld_k, v, ld_v, T, n_q, positions, n_axes, pair_axis, slots, cos_sin,
-                                      n_pos, rot, int(interleaved), q_norm, k_norm, eps, q_out, None)
+    return call("lora_kv_append_axes", kv, L._AXES, q, k, v, q_out, positions, slots, cos_sin, q_norm, k_norm, ld_q, ld_k, ld_v, T, n_q,
+                n_axes, n_pos, rot, int(interleaved), eps, pair_axis)
 
 
 @pytest.mark.parametrize("change, code", BAD_PAGES)
@@ -24,7 +34,7 @@ def test_append_axes_refuses_pages(change, code):
 
 
 @pytest.mark.parametrize("change, code", [
-    (dict(n_axes=0), L.LORA_ERR_ARG), (dict(n_axes=L.LORA_MAX_AXES + 1), L.LORA_ERR_ARG), (dict(pair_axis=None), L.LORA_ERR_ARG),
+    (dict(n_axes=0), L.LORA_ERR_ARG), (dict(n_axes=L.LORA_MAX_AXES + 1), L.LORA_ERR_ARG),
     (dict(n_axes=2), L.LORA_ERR_ARG), (dict(pair_axis=bytes(63) + bytes([3])), L.LORA_ERR_ARG),        # an axis beyond n_axes
     (dict(T=0, n_axes=2), L.LORA_ERR_ARG),
     (dict(T=-1), L.LORA_ERR_ARG), (dict(rot=-2), L.LORA_ERR_ARG), (dict(eps=-1.0), L.LORA_ERR_ARG),
@@ -44,6 +54,47 @@ def test_append_axes_without_tokens():
     before = L.lora_launch_count()
     assert axes(pages(), T=0, q=None, k=None, v=None, q_out=None, positions=None, slots=None) == L.LORA_OK
     assert L.lora_launch_count() == before
+
+
+def test_no_arguments():
+    kv = pages()
+    for name in ("lora_kv_append_axes", "lora_tree_attention_weights", "lora_kv_evict"):
+        assert getattr(L._lib, name)(ctypes.addressof(kv), None, None) == L.LORA_ERR_ARG
+
+
+def test_packed_structs_are_the_header_s(tmp_path):
+    """Field by field, as the compiler lays them out."""
+    import os
+    import shutil
+    import subprocess
+    if not shutil.which("gcc"):
+        pytest.skip("no C compiler")
+    layouts = {"lora_append_axes": (L._AXES, "q k v q_out positions slots cos_sin q_norm k_norm ld_q ld_k ld_v T n_q_heads n_axes n_pos rot_dim "
+                                             "interleaved eps pair_axis"),
+               "lora_attention_weights": (L._WEIGHTS, "weights q seg_starts kv_lens page_table tree_mask out workspace ws_bytes n_q_heads S T "
+                                                      "max_pages mask_words scale decay"),
+               "lora_eviction": (L._EVICTION, "scores weights kv_lens page_table keep kept new_lens S max_pages first recent ld_kept")}
+    lines = [f'printf("{name} %zu", sizeof({name}));' + "".join(f'printf(" %zu", offsetof({name}, {f}));' for f in fields.split()) + 'puts("");'
+             for name, (_, fields) in layouts.items()]
+    source = tmp_path / "offsets.c"
+    source.write_text('#include <stdio.h>\n#include "lora.h"\nint main(void) {\n' + "\n".join(lines) + "\nreturn 0;\n}\n")
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run(["gcc", "-I", include, "-o", str(tmp_path / "offsets"), str(source)], check=True)
+    got = {line.split()[0]: [int(x) for x in line.split()[1:]]
+           for line in subprocess.run([str(tmp_path / "offsets")], capture_output=True, text=True, check=True).stdout.splitlines()}
+    sizes = {"P": 8, "N": 8, "i": 4, "f": 4}
+    for name, (layout, fields) in layouts.items():
+        at, offsets = 0, []
+        for count, kind in re.findall(r"(\d*)([PNifsx])", layout.format.lstrip("@")):
+            if kind in "sx":
+                offsets += [at] if kind == "s" else []
+                at += int(count)
+                continue
+            for _ in range(int(count or 1)):
+                at = -(-at // sizes[kind]) * sizes[kind]
+                offsets.append(at)
+                at += sizes[kind]
+        assert got[name] == [layout.size, *offsets] and len(offsets) == len(fields.split())
 
 
 def test_pair_axis_from_python(monkeypatch):
@@ -69,7 +120,7 @@ def test_pair_axis_from_python(monkeypatch):
 
 def evict(kv, scores=P, weights=P, S=2, lens=P + (1 << 14) + 64, table=P + (1 << 14), max_pages=4, keep=P + (1 << 14) + 128,
           first=1, recent=2, kept=P + (1 << 14) + 512, ld=8, new_lens=P + (1 << 14) + 256):
-    return L._lib.lora_kv_evict(ctypes.byref(kv), scores, weights, S, lens, table, max_pages, keep, first, recent, kept, ld, new_lens, None)
+    return call("lora_kv_evict", kv, L._EVICTION, scores, weights, lens, table, keep, kept, new_lens, S, max_pages, first, recent, ld)
 
 
 @pytest.mark.parametrize("change, code", BAD_PAGES)
@@ -114,8 +165,8 @@ def test_planes_that_are_too_small_are_refused_in_python():
 def weigh(kv, weights=P, decay=1.0, q=P, n_q=4, starts=P, S=2, T=2, lens=P, table=P, max_pages=4, mask=None, words=0, scale=0.1, out=P,
           workspace=P, ws_bytes=1 << 30):
     out = P + (1 << 13) if out == P else out
-    return L._lib.lora_tree_attention_weights(ctypes.byref(kv), weights, decay, q, n_q, starts, S, T, lens, table, max_pages, mask, words,
-                                              scale, out, workspace, ws_bytes, None)
+    return call("lora_tree_attention_weights", kv, L._WEIGHTS, weights, q, starts, lens, table, mask, out, workspace, ws_bytes, n_q, S, T,
+                max_pages, words, scale, decay)
 
 
 @pytest.mark.parametrize("change, code", BAD_PAGES)
