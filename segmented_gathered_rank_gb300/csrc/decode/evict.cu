@@ -362,6 +362,17 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const uint32_t blocks = cluster_size(), rank = cluster_rank();
     const int cluster = blockIdx.x / blocks;
+    if ((long long)p.S * p.n_kv <= gridDim.x / blocks) {       // a cluster for every unit there can be
+        const int s = cluster / p.n_kv, head = cluster - s * p.n_kv, len = p.lens[s];
+        bool bad = false;
+        if (loses(p, len, p.keep[s], bad)) {
+            select(p, sh, keys, s, head, blocks, rank);
+        } else if (head == 0 && rank == 0 && threadIdx.x == 0) {
+            p.new_lens[s] = len;
+            if (bad) flag_status(p.status, LORA_DEV_BAD_LENGTH);
+        }
+        return;
+    }
     in_turn<kThreads>(
         p.S, p.n_kv, cluster, gridDim.x / blocks,
         [&](int s) {
@@ -377,11 +388,17 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(const EvictParam
         [&](int s, int head) { select(p, sh, keys, s, head, blocks, rank); });
 }
 
+// What evict_select_kernel left, once it is done.
+__device__ __forceinline__ int new_len(const EvictParams &p, int s) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    return *(volatile int *)(p.new_lens + s);
+}
+
 // Moves a column range of `width` 16-byte chunks of one plane of a request and kv head.  A thread looks up one row of
 // a round: its source's index two rounds before its slots, those a round before the copies, which are two rounds ahead
 // of the stores.
 template <int kPieces>
-__device__ void move_range(const EvictParams &p, char *plane, const Row &row, const int *kept, int keep, int len, int first, int width,
+__device__ void move_range(const EvictParams &p, int s, char *plane, const Row &row, const int *kept, int keep, int len, int first, int width,
                            uint4 *ring, int2 (*slots)[kMoveThreads]) {
     const int tid = threadIdx.x, per_pass = kMoveThreads / width, pieces = min(kPieces, kMoveThreads / per_pass), round = per_pass * pieces;
     const int rounds = (keep + round - 1) / round;
@@ -414,8 +431,10 @@ __device__ void move_range(const EvictParams &p, char *plane, const Row &row, co
     int src;
     {
         int at[kAhead + 1];
+        const int now = new_len(p, s);
 #pragma unroll
         for (int i = 0; i <= kAhead; ++i) at[i] = index(i);
+        if (now != keep) return;                         // a page outside the cache: there are no sources
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) slots[i][tid] = places(i, at[i]);
         next = places(kAhead, at[kAhead]);
@@ -446,8 +465,9 @@ __device__ void move_range(const EvictParams &p, char *plane, const Row &row, co
 }
 
 template <int kPieces>
-__device__ void move_weights(const EvictParams &p, const Row &row, const int *kept, int keep, int len) {
+__device__ void move_weights(const EvictParams &p, int s, const Row &row, const int *kept, int keep, int len) {
     const int tid = threadIdx.x;
+    if (new_len(p, s) != keep) return;
     for (int j0 = 0; j0 < keep; j0 += kMoveThreads * kPieces) {
         float w[kPieces];
         int src[kPieces];
@@ -477,31 +497,38 @@ __global__ void __launch_bounds__(kMoveThreads, M::kPerSm) evict_move_kernel(con
         bool bad;
         return loses(p, p.lens[s], p.keep[s], bad);
     };
-    auto sound = [&](int s) {
-        asm volatile("griddepcontrol.wait;\n" ::: "memory");
-        return *(volatile int *)(p.new_lens + s) == p.keep[s];
-    };
     // 128 bytes a range; where that leaves three of four blocks without one, 64: one request 1088 -> 1024, 8 heads of
     // 128, 11.8 us for 12.8, but four 32768 -> 2048 40.5 for 38.2 and 64 over 4352 102 for 93, as memory is read in pieces
-    long long units = 0;
-    for (int s0 = 0; s0 < p.S; s0 += kMoveThreads) units += __syncthreads_count(s0 + (int)threadIdx.x < p.S && active(s0 + threadIdx.x));
-    const int slices = chunks == p.slices * kSliceChunks && units * p.n_kv * p.slices * 8 <= p.places ? 2 * p.slices : p.slices;
+    long long units = (long long)p.S * p.n_kv;
+    const bool direct = units * (2 * p.slices + (p.weights ? 1 : 0)) <= p.places;       // a block for every range there can be
+    if (!direct) {
+        units = 0;
+        for (int s0 = 0; s0 < p.S; s0 += kMoveThreads) units += __syncthreads_count(s0 + (int)threadIdx.x < p.S && active(s0 + threadIdx.x));
+        units *= p.n_kv;
+    }
+    const int slices = chunks == p.slices * kSliceChunks && units * p.slices * 8 <= p.places ? 2 * p.slices : p.slices;
     const int parts = 2 * slices;
-    const long long turn =
-        in_turn<kMoveThreads>(p.S, p.n_kv * parts, blockIdx.x, workers, active, [&](int s, int unit) {
-            if (!sound(s)) return;
-            const int head = unit / parts, part = unit - head * parts;
-            const Row row = {p.table + (long long)s * p.max_pages, head};
-            const int slice = part % slices, first = chunks * slice / slices, width = chunks * (slice + 1) / slices - first;
-            move_range<M::kPieces>(p, part < slices ? p.k : p.v, row, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s], p.lens[s], first,
-                       width, ring, slots);
-        });
-    if (p.weights)
-        in_turn<kMoveThreads>(p.S, p.n_kv, turn, workers, active, [&](int s, int head) {
-            if (!sound(s)) return;
-            move_weights<8>(p, {p.table + (long long)s * p.max_pages, head}, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s],
-                            p.lens[s]);
-        });
+    auto range = [&](int s, int unit) {
+        const int head = unit / parts, part = unit - head * parts;
+        const Row row = {p.table + (long long)s * p.max_pages, head};
+        const int slice = part % slices, first = chunks * slice / slices, width = chunks * (slice + 1) / slices - first;
+        move_range<M::kPieces>(p, s, part < slices ? p.k : p.v, row, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s], p.lens[s],
+                               first, width, ring, slots);
+    };
+    auto weights = [&](int s, int head) {
+        move_weights<8>(p, s, {p.table + (long long)s * p.max_pages, head}, p.kept + ((long long)s * p.n_kv + head) * p.ld_kept, p.keep[s],
+                        p.lens[s]);
+    };
+    if (direct) {
+        const int each = p.n_kv * (parts + (p.weights ? 1 : 0)), s = blockIdx.x / each, unit = blockIdx.x - s * each;
+        if (s < p.S && active(s)) {
+            if (unit < p.n_kv * parts) range(s, unit);
+            else weights(s, unit - p.n_kv * parts);
+        }
+    } else {
+        const long long turn = in_turn<kMoveThreads>(p.S, p.n_kv * parts, blockIdx.x, workers, active, range);
+        if (p.weights) in_turn<kMoveThreads>(p.S, p.n_kv, turn, workers, active, weights);
+    }
     asm volatile("griddepcontrol.wait;\n" ::: "memory");       // no grid ends before the one it depends on
 }
 
