@@ -18,12 +18,12 @@
 //   and the next rounds are on their way while one is written.
 //
 // Memory is the bound of large calls: 64 requests over <= 4352, 4096 kept, 8 heads of 128,
-// 80 us for 388 MB (4.8 TB/s); the select is 14 of them (its 92 blocks wait for one another's
-// barriers and loads), the rest the ranges' last rounds.  Small calls are chains: one request
-// 1088 -> 1024 11.9 us, of which the select is 6.6: lengths, page ids, scores, two or three
-// passes of 0.7 to 1.4, the list.  Four of 32768 -> 2048: 40 us, 20 of them for passes over
-// scores in clusters of four blocks.  In one kernel, a cluster a unit, the three took 117,
-// 13.7 and 116 us: whole units are too large a piece to spread evenly.
+// 81 us for 388 MB (4.8 TB/s); the select is 14 of them (a block goes from barrier to barrier
+// and from load to load), the rest the ranges' last rounds.  Small calls are chains: one
+// request 1088 -> 1024 10.2 us, half of them the select's: lengths, page ids, scores, two or
+// three passes of 0.7 to 1.4, the list.  Four of 32768 -> 2048: 36.7 us, half of them for
+// passes over scores in clusters of four blocks.  In one kernel, a cluster a unit, the three
+// took 117, 13.7 and 116 us: whole units are too large a piece to spread evenly.
 #include "kv_copy.cuh"
 
 namespace lora {
@@ -34,8 +34,8 @@ using namespace decode;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBits = 11, kBins = 1 << kBits, kCoarse = 8;      // kCoarse bins side by side are counted together as well
 constexpr int kMaxCluster = 8;
-// Alone and in a cluster, four requests, 2048 kept, 8 heads: 2100 tokens 26.8 and 27.6 us, 4200 31.9 and 30.2, 8100 38.6
-// and 31.6, 16000 49.4 and 34.5.
+// Alone and in a cluster, four requests, 2048 kept, 8 heads: 2100 tokens 25.8 and 26.7 us, 4200 29.9 and 28.5, 8100 36.1
+// and 30.1, 16000 45.2 and 33.0.
 constexpr int kSolo = 4096;
 constexpr int kMaxHeld = 16384;       // scores a block keeps in shared memory; more are read again
 
@@ -44,8 +44,8 @@ constexpr int kStages = 3;            // rounds in shared memory
 constexpr int kAhead = kStages - 1, kSlotRounds = kStages + 1;
 constexpr int kSliceChunks = 8;       // at most, of 16 bytes
 // 16-byte pieces a thread and round, and blocks a SM: long rounds where all ranges there can be run at once, else more
-// blocks.  Four 32768 -> 2048 (128 ranges) 40 us with 8 pieces and two blocks, 45 with 5 and three; 64 requests over
-// <= 4352 (368 ranges of 2048 that there could be) 94 and 81.
+// blocks.  Four 32768 -> 2048 (128 ranges) 37.6 us with 8 pieces and two blocks, 43.4 with 5 and three; 64 requests over
+// <= 4352 (368 ranges of 2048 that there could be) 99.6 and 81.
 struct Few {
     static constexpr int kPieces = 8, kPerSm = 2;
 };
@@ -497,17 +497,20 @@ __global__ void __launch_bounds__(kMoveThreads, M::kPerSm) evict_move_kernel(con
         bool bad;
         return loses(p, p.lens[s], p.keep[s], bad);
     };
-    // 128 bytes a range; where that leaves three of four blocks without one, 64: one request 1088 -> 1024, 8 heads of
-    // 128, 11.8 us for 12.8, but four 32768 -> 2048 40.5 for 38.2 and 64 over 4352 102 for 93, as memory is read in pieces
+    // 128 bytes a range; where that would leave half of the blocks without one, 64 (if both halves are whole sectors): one
+    // request 1088 -> 1024, 8 heads of 128, 10.2 us for 11.4, four 32768 -> 2048 36.7 for 37.6; but 64 over <= 4352 102 for
+    // 93, as memory is read in smaller pieces
     long long units = (long long)p.S * p.n_kv;
-    const bool direct = units * (2 * p.slices + (p.weights ? 1 : 0)) <= p.places;       // a block for every range there can be
+    const int more = p.weights ? 1 : 0;
+    bool direct = units * (2 * p.slices + more) <= p.places;       // a block for every range there can be
     if (!direct) {
         units = 0;
         for (int s0 = 0; s0 < p.S; s0 += kMoveThreads) units += __syncthreads_count(s0 + (int)threadIdx.x < p.S && active(s0 + threadIdx.x));
         units *= p.n_kv;
     }
-    const int slices = chunks == p.slices * kSliceChunks && units * p.slices * 8 <= p.places ? 2 * p.slices : p.slices;
+    const int slices = chunks == p.slices * kSliceChunks && units * p.slices * 4 <= p.places ? 2 * p.slices : p.slices;
     const int parts = 2 * slices;
+    direct = direct && units * (parts + more) <= workers;
     auto range = [&](int s, int unit) {
         const int head = unit / parts, part = unit - head * parts;
         const Row row = {p.table + (long long)s * p.max_pages, head};
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(kMoveThreads, M::kPerSm) evict_move_kernel(con
                         p.lens[s]);
     };
     if (direct) {
-        const int each = p.n_kv * (parts + (p.weights ? 1 : 0)), s = blockIdx.x / each, unit = blockIdx.x - s * each;
+        const int each = p.n_kv * (parts + more), s = blockIdx.x / each, unit = blockIdx.x - s * each;
         if (s < p.S && active(s)) {
             if (unit < p.n_kv * parts) range(s, unit);
             else weights(s, unit - p.n_kv * parts);

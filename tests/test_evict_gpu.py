@@ -197,3 +197,13 @@ def test_streams_graphs_and_repeats():
     g.keep[2] = 77
     graph.replay()
     g.check()
+
+
+@pytest.mark.parametrize("weights", ["other", None])
+@pytest.mark.parametrize("S", [18, 19, 37, 38, 39, 50, 51, 75, 76, 77, 152, 153, 305, 609])
+def test_as_many_ranges_as_there_are_blocks(S, weights):
+    """Around the sizes at which ranges are halved, dealt out or run by longer rounds (two kv heads of 128 bytes)."""
+    rng = np.random.default_rng(S)
+    e = Eviction(S, I.BF16, rng.integers(0, 90, S), rng.integers(-1, 60, S), 2, 5, 2, 64, 8, weights=weights).to_device()
+    e.call()
+    e.check()
