@@ -7,10 +7,10 @@
 //
 // weigh_scores_kernel: with few rows they leave the scores too (4 bytes a row and token,
 //   written and read, against 2 d for reading a bf16 key again), and a thread sums up four
-//   tokens.  128 requests over <= 8192, 4 rows, 8 kv heads: about 18 us of the call's 270, for
+//   tokens.  128 requests over <= 8192, 4 rows, 8 kv heads: about 17 us of the call's 268, for
 //   50 MB of scores that are still in L2 and 25 MB of weights; the bound is instructions and
 //   the chain page id -> weight -> store, which is why both are requested a tile ahead.  One
-//   request over 777: 14.1 us, of which the attention is 11.2.
+//   request over 777: 13.8 us, of which the attention is 11.2.
 // weigh_tc_kernel (weigh_tc.cu; bf16), weigh_kernel (fp32): else the scores are computed
 //   once more, keys at rest and rows going by, so that a key's sum stays in one block and
 //   its order is fixed.  weigh_kernel has fp32 multiply-adds for its bound, two tokens and
@@ -98,9 +98,11 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
     }
 }
 
-constexpr int kScoreThreads = 128, kScorePerSm = 9;
+constexpr int kScoreThreads = 128, kScorePerSm = 7;
 constexpr int kScoreTile = kScoreThreads * 4;       // cached tokens a tile
-constexpr int kScoreRows = 4;                       // rows on their way at once
+// Rows on their way at once: 8 for 4 gain a microsecond where a small call has more (5 fp32 trees of 7 over <= 300, 21 rows,
+// 19.0 us for 19.7) and lose one in large ones (32 over <= 8192, 8 rows, 88.5 for 87.5).
+constexpr int kScoreRows = 4;
 
 __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnParams p, float *weights, float decay) {
     static_assert(kScoreThreads >= kScanThreads, "start_block");
@@ -149,20 +151,11 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
         const int c = cur.tile * kScoreTile + threadIdx.x * 4;
         const int rows = c - (int)(threadIdx.x & 31) * 4 < cur.r.len ? cur.r.n * p.group : 0;       // of the whole warp
         const bool inside = c < cur.r.len;
-        // rows of a kv head lie group by group of n_q rows: the next one's place, its head in the group
-        const float *scores = p.scores + ((long long)cur.r.begin * p.n_q + cur.head * p.group) * p.ld_scores + c;
-        const float *sums = p.lse + (long long)cur.r.begin * p.n_q + cur.head * p.group;
-        int g = 0;
-        float4 s[kScoreRows] = {};
-        float lse[kScoreRows] = {}, w[4] = {};
-        const float *loaded[kScoreRows];
-        auto load = [&](int row0) {
-#pragma unroll
-            for (int x = 0; x < kScoreRows; ++x) {
-                if (row0 + x >= rows) break;
-                if (inside) s[x] = *reinterpret_cast<const float4 *>(scores);
-                lse[x] = *sums;
-                loaded[x] = scores;
+        // rows of a kv head lie group by group of n_q rows: the place of the next one, and its head in the group
+        struct Place {
+            const float *scores, *sums;
+            int g;
+            __device__ __forceinline__ void next(const AttnParams &p) {
                 scores += p.ld_scores;
                 ++sums;
                 if (++g == p.group) {
@@ -170,6 +163,19 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
                     scores += (p.n_q - p.group) * p.ld_scores;
                     sums += p.n_q - p.group;
                 }
+            }
+        } ahead = {p.scores + ((long long)cur.r.begin * p.n_q + cur.head * p.group) * p.ld_scores + c,
+                   p.lse + (long long)cur.r.begin * p.n_q + cur.head * p.group, 0};
+        Place done = ahead;
+        float4 s[kScoreRows] = {};
+        float lse[kScoreRows] = {}, w[4] = {};
+        auto load = [&](int row0) {
+#pragma unroll
+            for (int x = 0; x < kScoreRows; ++x) {
+                if (row0 + x >= rows) break;
+                if (inside) s[x] = *reinterpret_cast<const float4 *>(ahead.scores);
+                lse[x] = *ahead.sums;
+                ahead.next(p);
             }
         };
         load(0);
@@ -184,16 +190,18 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
                 w[2] += exp2_fast(s[x].z - lse[x]);
                 w[3] += exp2_fast(s[x].w - lse[x]);
             }
+            if (row0 + kScoreRows < rows) load(row0 + kScoreRows);
             // the scores are not needed again: their lines leave L2 without being written to memory (2 over 131072: 142 ->
             // 135 us; one over 777 would take 15.0 us for 14.2)
             if (drop) {
                 __syncwarp();
-                if (inside && (threadIdx.x & 7) == 0)
 #pragma unroll
-                    for (int x = 0; x < kScoreRows; ++x)
-                        if (row0 + x < rows) asm volatile("discard.global.L2 [%0], 128;\n" ::"l"(loaded[x]) : "memory");
+                for (int x = 0; x < kScoreRows; ++x) {
+                    if (row0 + x >= rows) break;
+                    if (inside && (threadIdx.x & 7) == 0) asm volatile("discard.global.L2 [%0], 128;\n" ::"l"(done.scores) : "memory");
+                    done.next(p);
+                }
             }
-            if (row0 + kScoreRows < rows) load(row0 + kScoreRows);
         }
         int to[4];
 #pragma unroll

@@ -121,3 +121,92 @@ def test_example_runs_and_stays_within_its_budget():
         assert (block.held <= 64 + 8).all()
     assert cut >= 2 and int(block.status) == 0 and bool((block.weights >= 0).all())
     block.close()
+
+
+class Step:
+    """One step of all three calls on a cache of n_pages, whose pages `ids` hold the requests."""
+
+    def __init__(self, n_pages, ids, S, seed, n_q=32, n_kv=8, d=128, page=16, length=700, budget=400):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        bf16 = dict(dtype=torch.bfloat16, device="cuda")
+        self.S, self.n_q, self.page, self.length, self.budget, self.max_pages = S, n_q, page, length, budget, -(-length // page)
+        self.ids = ids
+        self.planes = [torch.empty(n_pages, n_kv, page, d, **bf16), torch.empty(n_pages, n_kv, page, d, **bf16),
+                       torch.empty(n_pages, n_kv, page, device="cuda")]
+        for plane in self.planes:
+            plane[ids] = torch.randn(len(ids), *plane.shape[1:], generator=g, device="cuda").to(plane.dtype).abs()
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.kv = L.KvPages(L.LORA_BF16, *self.planes[:2], n_pages, page, n_kv, d, status=self.status)
+        self.table = ids.int().view(S, self.max_pages).contiguous()
+        last = length - 1
+        self.slots = self.table[:, last // page].long() * page + last % page
+        self.positions = torch.randint(0, 64, (S, 3), generator=g, device="cuda", dtype=torch.int32)
+        self.cos_sin = torch.randn(64, d, generator=g, device="cuda")
+        self.q, self.k, self.v = (torch.randn(S, h * d, generator=g, device="cuda").bfloat16() for h in (n_q, n_kv, n_kv))
+        self.lens, self.keep = (torch.full((S,), x, dtype=torch.int32, device="cuda") for x in (length, budget))
+        self.starts = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+        self.q_out, self.out = torch.empty_like(self.q), torch.empty_like(self.q)
+        self.kept = torch.zeros(S, n_kv, budget, dtype=torch.int32, device="cuda")
+        self.new_lens = torch.zeros_like(self.lens)
+        self.ws = torch.empty(L.lora_tree_attention_weights_workspace_size(self.kv, n_q, S, S, self.max_pages), dtype=torch.uint8, device="cuda")
+        self.axis = bytes(i % 3 for i in range(d // 2))
+
+    def run(self, stream=None):
+        L.lora_kv_append_axes(self.kv, self.q, self.k, self.v, self.S, self.n_q, self.positions, 3, self.axis, self.slots, self.cos_sin, 64,
+                              self.k.shape[1] // self.kv.n_kv_heads, False, self.q_out, stream=stream)
+        L.lora_tree_attention_weights(self.kv, self.planes[2], 0.5, self.q_out, self.n_q, self.starts, self.S, self.S, self.lens, self.table,
+                                      self.max_pages, None, 0, 0.088, self.out, self.ws, stream=stream)
+        L.lora_kv_evict(self.kv, self.planes[2], self.planes[2], self.S, self.lens, self.table, self.max_pages, self.keep, 2, 50, self.kept,
+                        self.budget, self.new_lens, stream=stream)
+
+    def results(self):
+        torch.cuda.synchronize()
+        assert int(self.status) == 0
+        return [plane[self.ids] for plane in self.planes] + [self.q_out.clone(), self.out.clone(), self.kept.clone(), self.new_lens.clone()]
+
+
+def test_pages_beyond_32_bits_of_elements():
+    """The last pages of a cache of 2.7e9 elements give what the same pages of a small one do."""
+    n = 165000
+    assert n * 8 * 16 * 128 > 1 << 31
+    ids = torch.randperm(2 * 44, generator=torch.Generator().manual_seed(3)).cuda()
+    small, large = Step(2 * 44, ids, 2, 5), Step(n, n - 1 - ids, 2, 5)
+    small.run()
+    large.run()
+    assert all(torch.equal(a, b) for a, b in zip(small.results(), large.results()))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with caches and workspaces of their own do not meet."""
+    ids = torch.arange(16 * 44, device="cuda")
+    alone = []
+    for seed in (1, 2):
+        step = Step(16 * 44, ids, 16, seed)
+        step.run()
+        alone.append(step.results())
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        steps = [Step(16 * 44, ids, 16, seed) for seed in (1, 2)]
+        torch.cuda.synchronize()
+        for step, stream in zip(steps, streams):
+            step.run(stream)
+        for step, want in zip(steps, alone):
+            assert all(torch.equal(a, b) for a, b in zip(step.results(), want))
+
+
+def test_a_captured_step_replays():
+    ids = torch.arange(8 * 44, device="cuda")
+    want = Step(8 * 44, ids, 8, 4)
+    before = [p.clone() for p in want.planes]
+    want.run()
+    first = want.results()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        want.run()
+    for _ in range(3):
+        for plane, old in zip(want.planes, before):
+            plane.copy_(old)
+        want.kept.zero_()
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(want.results(), first))
