@@ -137,9 +137,8 @@ __device__ __forceinline__ void store_kept(float *dst, float4 s) {
 
 // Four consumer warps; each takes kWarpKeys of a stage's tokens for all rows of
 // the unit, with a maximum, sum and output of its own (so a tile needs no exchange
-// between warps), joined in shared memory when the block leaves the unit.  KEEP: the
-// scores go to p.scores as well.
-template <int D, bool TMA, bool KEEP>
+// between warps), joined in shared memory when the block leaves the unit.
+template <int D, bool TMA, int MODE>
 __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t *smem, MmaControl &ctl) {
     using Sh = MmaShape<D, TMA>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -222,7 +221,7 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
                     for (int e = 0; e < 4; ++e)
                         if (!((see[e >> 1] >> (j * 8 + t4 * 2 + (e & 1))) & 1)) s[j][e] = -INFINITY;
             }
-            if constexpr (KEEP) {
+            if constexpr (MODE == kScores) {
                 // neighbouring lanes swap halves of two groups of eight tokens, so that each has four side by side
                 const bool odd = t4 & 1;
 #pragma unroll
@@ -380,7 +379,7 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
                     w2.y = pack_bf16(acc.z * r, acc.w * r);
                     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) +
                                                row_offset(p, cur, cur.row_tile * kRows + row) + col) = w2;
-                    if (p.lse && col == 0) p.lse[row_index(p, cur, cur.row_tile * kRows + row)] = log_sum(top, sum);
+                    if (MODE != kPlain && col == 0) p.lse[row_index(p, cur, cur.row_tile * kRows + row)] = log_sum(top, sum);
                 } else {
                     *reinterpret_cast<float4 *>(dst + partial_at(p, row, col)) = acc;
                     if (col == 0) {
@@ -404,12 +403,12 @@ __device__ void consume(const AttnParams &p, Cursor cur, uint32_t total, uint8_t
     }
 }
 
-template <int D, bool TMA, bool KEEP>
+template <int D, bool TMA, int MODE>
 __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, TMA>::kPerSm))
     attention_mma_kernel(const __grid_constant__ KvMaps maps, const AttnParams p) {
     using Sh = MmaShape<D, TMA>;
     // kept scores stay in L2 until their sums are taken: keys and values make room for them
-    using Copy = std::conditional_t<TMA, TmaCopy<D, Sh::kTile, KEEP>, ChunkCopy<D, Sh::kTile, 128>>;
+    using Copy = std::conditional_t<TMA, TmaCopy<D, Sh::kTile, MODE == kScores>, ChunkCopy<D, Sh::kTile, 128>>;
     extern __shared__ uint8_t raw[];
     __shared__ ScanShared scan;
     __shared__ MmaControl ctl;
@@ -424,10 +423,10 @@ __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, 
         tc::mbar_fence_init();
     }
     Cursor cur;
-    const uint32_t total = start_block(p, scan, cur);
+    const uint32_t total = start_block<MODE>(p, scan, cur);
     if (cur.left <= 0) return;
     if (threadIdx.x < kThreads) {
-        consume<D, TMA, KEEP>(p, cur, total, smem, ctl);
+        consume<D, TMA, MODE>(p, cur, total, smem, ctl);
     } else {
         const int tid = threadIdx.x - kThreads;
         const uint32_t base = smem_addr(smem);
@@ -462,7 +461,7 @@ __global__ void __launch_bounds__((MmaShape<D, TMA>::kThreadsAll), (MmaShape<D, 
 constexpr int kSimtTile = 32;
 constexpr int kSimtRows = 16;
 
-template <int D, bool KEEP>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnParams p) {
     constexpr int kLd = D + 4;            // row pitch: lanes a row apart read different banks
     constexpr int kCols = D / 32;
@@ -473,7 +472,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
     float *ring = ps + 4 * kSimtTile * 4;                   // [2][K, V][32][kLd]
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Cursor cur;
-    const uint32_t total = start_block(p, scan, cur);
+    const uint32_t total = start_block<MODE>(p, scan, cur);
     if (cur.left <= 0) return;
     Cursor ahead = cur;
     // copies: this thread's 16 bytes of rows copy_row + i * kRowsPerPass, whose pages are fetched a tile ahead
@@ -558,7 +557,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                 if (!sure && row0 + a < rows) see[a] = seen_word(p, cur.r, (cur.row_tile * p.rt + row0 + a) / p.group, cur.tile * kSimtTile);
                 const bool on = (see[a] >> lane) & 1;
                 const float x = on ? (s2[a].x + s2[a].y) * p.scale_log2 : -INFINITY;
-                if (KEEP && row0 + a < rows && cur.tile * kSimtTile + lane < cur.r.len)
+                if (MODE == kScores && row0 + a < rows && cur.tile * kSimtTile + lane < cur.r.len)
                     p.scores[row_index(p, cur, cur.row_tile * p.rt + row0 + a) * p.ld_scores + cur.tile * kSimtTile + lane] = x;
                 float top = x;
 #pragma unroll
@@ -641,7 +640,7 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                     dst[p.rt * p.d + ur * 2] = m[a];
                     dst[p.rt * p.d + ur * 2 + 1] = l[a];
                 }
-                if (p.lse && whole && lane == 0) p.lse[row_index(p, cur, cur.row_tile * p.rt + ur)] = log_sum(m[a], l[a]);
+                if (MODE != kPlain && whole && lane == 0) p.lse[row_index(p, cur, cur.row_tile * p.rt + ur)] = log_sum(m[a], l[a]);
             }
             fresh = true;
         }
@@ -662,7 +661,7 @@ constexpr int kWarpRows = 4;       // query rows a warp
 // leaves the unit; the maximum is raised only when a score passes it by 2^8.  In the
 // steps past the prefix, values that a row does not see are left out, whatever they are.
 // FULL: d is D.
-template <int D, bool FULL, bool KEEP>
+template <int D, bool FULL, int MODE>
 __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few_kernel(const AttnParams p) {
     constexpr int kLanes = D == 256 ? 16 : 8, kTokens = 32 / kLanes, kVec = D / (4 * kLanes);
     __shared__ ScanShared scan;
@@ -671,7 +670,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tok = lane / kLanes, first_chunk = lane % kLanes, chunks = p.d >> 2;
     Cursor cur;
-    const uint32_t total = start_block(p, scan, cur);
+    const uint32_t total = start_block<MODE>(p, scan, cur);
     while (cur.left > 0) {
         const int tiles = min(cur.left, cur.r.tiles - cur.tile), rows = min(p.rt, cur.r.n * p.group - cur.row_tile * p.rt);
         const int begin = cur.tile * kFewTile, end = min(begin + tiles * kFewTile, cur.r.len);
@@ -735,7 +734,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few
                     on[a] = (see >> (c & 31)) & 1;
                     if (!on[a]) s[a] = -INFINITY;
                 }
-                if (KEEP && first_chunk == a && row0 + a < rows && c < end)
+                if (MODE == kScores && first_chunk == a && row0 + a < rows && c < end)
                     p.scores[row_index(p, cur, cur.row_tile * p.rt + row0 + a) * p.ld_scores + c] = s[a];
                 raise |= s[a] > m[a] + 8.f;        // from -infinity by any score
             }
@@ -828,7 +827,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few
                 const float r = sum == 0.f ? 0.f : 1.f / sum;
                 *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row_offset(p, cur, cur.row_tile * p.rt + row) + c * 4) =
                     make_float4(u.x * r, u.y * r, u.z * r, u.w * r);
-                if (p.lse && c == 0) p.lse[row_index(p, cur, cur.row_tile * p.rt + row)] = log_sum(top, sum);
+                if (MODE != kPlain && c == 0) p.lse[row_index(p, cur, cur.row_tile * p.rt + row)] = log_sum(top, sum);
             } else {
                 *reinterpret_cast<float4 *>(dst + partial_at(p, row, c * 4)) = u;
                 if (c == 0) *reinterpret_cast<float2 *>(dst + p.rt * p.d + row * 2) = make_float2(top, sum);
@@ -846,10 +845,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few
 // reads, 32-byte writes.  gridDim.y is a unit's rows / kJoinRows: 16 rows a block made
 // 8 trees of 64 take 58.4 us for 56.6 and the small fp32 case 15.9 for 13.2, 4 rows
 // gained nothing.
-template <typename E>
+template <typename E, bool SUMS>
 __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const AttnParams p) {
     const int c = blockIdx.x, lane = threadIdx.x & 31;
-    if (p.lse) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");       // the weights' kernel, which waits as well
+    if (SUMS) asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");       // the weights' kernel, which waits as well
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     const JoinRecord rec = p.records[c];
     const int across = (p.d + 15) >> 4, pieces = ((rec.rows + 7) >> 3) * across;
@@ -876,7 +875,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_join_kernel(const Attn
         const int unit_row = rec.first_row + row, i = unit_row / p.group;
         const long long at = (long long)(rec.begin + i) * p.n_q + rec.head * p.group + unit_row - i * p.group;
         E *out = static_cast<E *>(p.out) + at * p.d + col;
-        if (p.lse && col == 0) p.lse[at] = log_sum(m, l);
+        if (SUMS && col == 0) p.lse[at] = log_sum(m, l);
         if constexpr (sizeof(E) == 2)
             *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16(o.x * r, o.y * r), pack_bf16(o.z * r, o.w * r));
         else
@@ -949,42 +948,44 @@ bool make_map(CUtensorMap *map, void *pages, const lora_kv_pages *kv, int rows) 
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool TMA, bool KEEP>
+template <int D, bool TMA, int MODE>
 int launch_mma(const KvMaps &maps, const AttnParams &p, cudaStream_t st) {
     using Sh = MmaShape<D, TMA>;
-    if (smem_optin(reinterpret_cast<const void *>(attention_mma_kernel<D, TMA, KEEP>), Sh::kSmem)) return LORA_ERR_CUDA;
-    attention_mma_kernel<D, TMA, KEEP><<<p.grid, Sh::kThreadsAll, Sh::kSmem, st>>>(maps, p);
+    if (smem_optin(reinterpret_cast<const void *>(attention_mma_kernel<D, TMA, MODE>), Sh::kSmem)) return LORA_ERR_CUDA;
+    attention_mma_kernel<D, TMA, MODE><<<p.grid, Sh::kThreadsAll, Sh::kSmem, st>>>(maps, p);
     count_launch();
     return cuda_status(cudaGetLastError());
 }
 
-template <int D, bool KEEP>
+template <int D, int MODE>
 int launch_simt(const AttnParams &p, cudaStream_t st) {
     const size_t smem = (size_t)(kSimtRows * D + 4 * kSimtTile * 4 + 4 * kSimtTile * (D + 4)) * 4;
-    if (smem_optin(reinterpret_cast<const void *>(attention_simt_kernel<D, KEEP>), smem)) return LORA_ERR_CUDA;
-    attention_simt_kernel<D, KEEP><<<p.grid, kThreads, smem, st>>>(p);
+    if (smem_optin(reinterpret_cast<const void *>(attention_simt_kernel<D, MODE>), smem)) return LORA_ERR_CUDA;
+    attention_simt_kernel<D, MODE><<<p.grid, kThreads, smem, st>>>(p);
     count_launch();
     return cuda_status(cudaGetLastError());
 }
 
-template <int D, bool KEEP>
+template <int D, int MODE>
 int launch_few(const AttnParams &p, cudaStream_t st) {
-    if (p.d == D) attention_few_kernel<D, true, KEEP><<<p.grid, kFewWarps * 32, 0, st>>>(p);
-    else attention_few_kernel<D, false, KEEP><<<p.grid, kFewWarps * 32, 0, st>>>(p);
+    if (p.d == D) attention_few_kernel<D, true, MODE><<<p.grid, kFewWarps * 32, 0, st>>>(p);
+    else attention_few_kernel<D, false, MODE><<<p.grid, kFewWarps * 32, 0, st>>>(p);
     count_launch();
     return cuda_status(cudaGetLastError());
 }
 
-template <int D, bool KEEP>
+template <int D, int MODE>
 int launch_width(const KvMaps *maps, const AttnParams &p, bool f32, bool few, cudaStream_t st) {
-    if (few) return launch_few<D, KEEP>(p, st);
-    if (f32) return launch_simt<D, KEEP>(p, st);
-    return maps ? launch_mma<D, true, KEEP>(*maps, p, st) : launch_mma<D, false, KEEP>(KvMaps{}, p, st);
+    if constexpr (MODE != kSums) {         // few rows keep their scores
+        if (few) return launch_few<D, MODE>(p, st);
+    }
+    if (f32) return launch_simt<D, MODE>(p, st);
+    return maps ? launch_mma<D, true, MODE>(*maps, p, st) : launch_mma<D, false, MODE>(KvMaps{}, p, st);
 }
-template <bool KEEP>
+template <int MODE>
 int launch_any(const KvMaps *maps, const AttnParams &p, bool f32, bool few, cudaStream_t st) {
-    return p.d <= 64 ? launch_width<64, KEEP>(maps, p, f32, few, st)
-           : p.d <= 128 ? launch_width<128, KEEP>(maps, p, f32, few, st) : launch_width<256, KEEP>(maps, p, f32, few, st);
+    return p.d <= 64 ? launch_width<64, MODE>(maps, p, f32, few, st)
+           : p.d <= 128 ? launch_width<128, MODE>(maps, p, f32, few, st) : launch_width<256, MODE>(maps, p, f32, few, st);
 }
 
 // Tensor maps for tiles of up to `tile` cached tokens.
@@ -998,8 +999,9 @@ int launch_attention(const lora_kv_pages *kv, const AttnParams &p, const Variant
     const bool f32 = kv->dtype == LORA_F32, tma = !f32 && kv->page_size >= kTmaMinPage;
     if (tma && !make_maps(maps, kv, v.tk)) return LORA_ERR_CUDA;
     if (v.tc) return launch_attention_tc(tma ? &maps : nullptr, p, st);
-    return p.scores ? launch_any<true>(tma ? &maps : nullptr, p, f32, v.few, st)
-                    : launch_any<false>(tma ? &maps : nullptr, p, f32, v.few, st);
+    const KvMaps *const at = tma ? &maps : nullptr;
+    return p.scores ? launch_any<kScores>(at, p, f32, v.few, st)
+           : p.lse ? launch_any<kSums>(at, p, f32, v.few, st) : launch_any<kPlain>(at, p, f32, v.few, st);
 }
 
 // lora_tree_attention_weights: a flag, and the logarithm of each row's sum.
@@ -1116,8 +1118,10 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = kv->dtype == LORA_BF16 ? cudaLaunchKernelEx(&cfg, attention_join_kernel<__nv_bfloat16>, p)
-                                                 : cudaLaunchKernelEx(&cfg, attention_join_kernel<float>, p);
+    void (*const join)(AttnParams) = kv->dtype == LORA_BF16
+                                         ? weights ? attention_join_kernel<__nv_bfloat16, true> : attention_join_kernel<__nv_bfloat16, false>
+                                         : weights ? attention_join_kernel<float, true> : attention_join_kernel<float, false>;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, join, p);
     count_launch();
     if ((rc = cuda_status(e))) return rc;
     return weights ? launch_weigh(kv, tma ? &maps : nullptr, weigh, weights, decay, st) : LORA_OK;

@@ -114,9 +114,14 @@ __device__ __forceinline__ int block_of(uint32_t total, uint32_t x, uint32_t gri
     return (int)(x < edge ? x / (each + 1) : more + (x - edge) / each);
 }
 
+// What a kernel leaves beside its outputs: nothing; p.lse and p.computed; those and p.scores.
+enum { kPlain, kSums, kScores };
+
 // Called by every thread of the block (kScanThreads at least): the block's first tile, and the length of
 // the list.  Lets the join launch; block 0 reports bad tables.  A table whose segments
 // overlap until they name more places than the T tokens can have has an empty list.
+// RECORDS: the block's record is cleared (the weights' kernels have none).
+template <int MODE = kPlain, bool RECORDS = true>
 __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared &sh, Cursor &c) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (p.S + kScanThreads - 1) / kScanThreads;
@@ -141,7 +146,7 @@ __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared 
     if (lane == 31 && warp < kScanThreads / 32) sh.sums[warp] = upto;
     if (tid == 0) {
         sh.request = -1;
-        if (p.records) p.records[blockIdx.x] = JoinRecord{};
+        if (RECORDS) p.records[blockIdx.x] = JoinRecord{};
     }
     __syncthreads();
     uint32_t total = 0, before = upto - mine;
@@ -151,7 +156,7 @@ __device__ __forceinline__ uint32_t start_block(const AttnParams &p, ScanShared 
         total = add_places(total, sh.sums[w]);
     }
     if (total > p.max_places) total = 0;
-    if (flags && p.computed && p.records && tid == 0) *p.computed = total > 0;
+    if (MODE != kPlain && flags && tid == 0) *p.computed = total > 0;
     const uint32_t pos = block_begin(total, blockIdx.x, p.grid);
     if (total > 0 && pos >= before && pos < before + mine) {
         uint32_t rest = pos - before;

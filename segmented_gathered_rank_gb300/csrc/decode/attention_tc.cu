@@ -390,7 +390,7 @@ __device__ __forceinline__ void load_queries(const AttnParams &p, const Cursor &
 }
 
 // The first unit's queries are on their way.
-template <int D, int NQ>
+template <int D, int NQ, bool SUMS>
 __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t *queries, Control *ctl) {
     using Sh = TcShape<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -553,7 +553,7 @@ __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t 
         if (writes && !seg.whole) {
             *reinterpret_cast<float2 *>(dst + p.rt * D + ur * 2) = make_float2(m, l);
         }
-        if (p.lse && writes && seg.whole) p.lse[my_off / D] = log_sum(m, l);
+        if (SUMS && writes && seg.whole) p.lse[my_off / D] = log_sum(m, l);
         // stream 1 hands its output over through its queries' space, 64 columns at a time
         float *hand = reinterpret_cast<float *>(queries + Sh::kSlot);
         constexpr int kHandCols = D == 128 ? 64 : 32;
@@ -614,7 +614,8 @@ __device__ void attend(const AttnParams &p, Cursor cur, uint32_t total, uint8_t 
     }
 }
 
-template <int D, int NQ, bool TMA>
+// SUMS: p.lse and p.computed are left.
+template <int D, int NQ, bool TMA, bool SUMS>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     attention_tc_kernel(const __grid_constant__ KvMaps maps, const AttnParams p) {
     using Sh = TcShape<D>;
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         tmem_relinquish();
     }
     Cursor cur;
-    const uint32_t total = start_block(p, scan, cur);
+    const uint32_t total = start_block<SUMS ? kSums : kPlain>(p, scan, cur);
     // the first queries are requested before the ring's tiles, which would keep them waiting
     if (warp < kProducer0 && cur.left > 0) load_queries<D, NQ>(p, cur, queries);
     fence_before_sync();
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         return;
     }
     if (warp < kProducer0) {
-        attend<D, NQ>(p, cur, total, queries, ctl);
+        attend<D, NQ, SUMS>(p, cur, total, queries, ctl);
         cp_wait_all();             // also where it gave up: no copy outlives the block
     } else if (warp < kMmaWarp) {
         produce<D, TMA>(p, maps, cur, ring, ctl);
@@ -681,20 +682,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     if (warp == kMmaWarp) tmem_dealloc(ctl->tmem, kTmemCols);
 }
 
-template <int D, int NQ, bool TMA>
+template <int D, int NQ, bool TMA, bool SUMS>
 int launch(const KvMaps &maps, const AttnParams &p, cudaStream_t st) {
-    if (smem_optin(reinterpret_cast<const void *>(attention_tc_kernel<D, NQ, TMA>), TcShape<D>::kSmem)) return LORA_ERR_CUDA;
-    attention_tc_kernel<D, NQ, TMA><<<p.grid, kThreadsTc, TcShape<D>::kSmem, st>>>(maps, p);
+    if (smem_optin(reinterpret_cast<const void *>(attention_tc_kernel<D, NQ, TMA, SUMS>), TcShape<D>::kSmem)) return LORA_ERR_CUDA;
+    attention_tc_kernel<D, NQ, TMA, SUMS><<<p.grid, kThreadsTc, TcShape<D>::kSmem, st>>>(maps, p);
     count_launch();
     return cuda_status(cudaGetLastError());
 }
 
-template <int D>
+template <int D, bool SUMS>
 int launch(const KvMaps *maps, const AttnParams &p, cudaStream_t st) {
     const bool two = p.rt == 256;
-    if (maps) return two ? launch<D, 2, true>(*maps, p, st) : launch<D, 1, true>(*maps, p, st);
+    if (maps) return two ? launch<D, 2, true, SUMS>(*maps, p, st) : launch<D, 1, true, SUMS>(*maps, p, st);
     const KvMaps none = {};
-    return two ? launch<D, 2, false>(none, p, st) : launch<D, 1, false>(none, p, st);
+    return two ? launch<D, 2, false, SUMS>(none, p, st) : launch<D, 1, false, SUMS>(none, p, st);
 }
 
 }  // namespace
@@ -702,7 +703,8 @@ int launch(const KvMaps *maps, const AttnParams &p, cudaStream_t st) {
 namespace decode {
 
 int launch_attention_tc(const KvMaps *maps, const AttnParams &p, cudaStream_t st) {
-    return p.d == 128 ? launch<128>(maps, p, st) : launch<64>(maps, p, st);
+    if (p.lse) return p.d == 128 ? launch<128, true>(maps, p, st) : launch<64, true>(maps, p, st);
+    return p.d == 128 ? launch<128, false>(maps, p, st) : launch<64, false>(maps, p, st);
 }
 
 }  // namespace decode

@@ -7,10 +7,10 @@
 //
 // weigh_scores_kernel: with few rows they leave the scores too (4 bytes a row and token,
 //   written and read, against 2 d for reading a bf16 key again), and a thread sums up four
-//   tokens.  128 requests over <= 8192, 4 rows, 8 kv heads: about 17 us of the call's 268, for
+//   tokens.  128 requests over <= 8192, 4 rows, 8 kv heads: about 17 us of the call's 267, for
 //   50 MB of scores that are still in L2 and 25 MB of weights; the bound is instructions and
 //   the chain page id -> weight -> store, which is why both are requested a tile ahead.  One
-//   request over 777: 13.8 us, of which the attention is 11.2.
+//   request over 777: 13.6 us, of which the attention is 10.8.
 // weigh_tc_kernel (weigh_tc.cu; bf16), weigh_kernel (fp32): else the scores are computed
 //   once more, keys at rest and rows going by, so that a key's sum stays in one block and
 //   its order is fixed.  weigh_kernel has fp32 multiply-adds for its bound, two tokens and
@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(kThreads) weigh_kernel(const AttnParams p, flo
     float *ks = smem, *qs = smem + kTile * pitch;
     Cursor at;
     KeyCursor cur;
-    cur.start(p, scan, start_block(p, scan, at));
+    cur.start(p, scan, start_block<kPlain, false>(p, scan, at));
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (!*p.computed) return;
     for (; cur.left > 0; cur.advance(p)) {
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
     __shared__ ScanShared scan;
     Cursor at;
     KeyCursor cur;
-    const uint32_t total = start_block(p, scan, at);
+    const uint32_t total = start_block<kPlain, false>(p, scan, at);
     cur.start(p, scan, total);
     const bool drop = total > (uint32_t)p.grid;
     // A tile's page ids, then its slots (-1: none) and what its weights were: two round trips, both a tile ahead and the
@@ -226,7 +226,6 @@ namespace decode {
 
 int plan_weigh(const lora_kv_pages *kv, const AttnParams &attention, AttnParams &p) {
     p = attention;
-    p.records = nullptr;
     const bool tc = !p.scores && kv->dtype == LORA_BF16;
     p.rt = p.scores ? 1 << 30 : tc ? kWeighRows : kRows;         // kept scores: a tile's rows are one place
     p.tk = p.scores ? kScoreTile : tc ? kWeighTile : kTile;

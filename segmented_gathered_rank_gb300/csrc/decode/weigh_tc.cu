@@ -10,7 +10,7 @@
 // waits for it.
 //
 // 8 requests of 64 tokens over <= 16384 (256 rows, 8 kv heads of 128): about 27 us of the
-// call's 85.5, where the products would take 8 and the exponentials, 16 a cycle and SM, 15.
+// call's 84.5, where the products would take 8 and the exponentials, 16 a cycle and SM, 15.
 // A pair of key tiles against 128 rows takes some 2200 cycles, 2048 of them exponentials;
 // the rest is the start (scan, first copies, 4 us) and the cut into whole key tiles.
 // Exponentials on the multiply-add pipe for a quarter of the columns were slower (90 us),
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     Cursor at;
     KeyCursor cur;
-    cur.start(p, scan, start_block(p, scan, at));
+    cur.start(p, scan, start_block<kPlain, false>(p, scan, at));
     if (cur.left <= 0) {                // the whole block; no grid ends before those it depends on
         asm volatile("griddepcontrol.wait;\n" ::: "memory");
         return;

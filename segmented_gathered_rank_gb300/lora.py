@@ -188,7 +188,11 @@ def _rows(t):
 
 def _address(t):
     """_ptr for a packed struct: NULL is 0."""
-    return 0 if t is None else _ptr(t)
+    if t is None:
+        return 0
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError("expected a contiguous CUDA tensor")
+    return t.data_ptr()
 
 
 def _matrix(t):
