@@ -18,7 +18,7 @@
 //   and the next rounds are on their way while one is written.
 //
 // Memory is the bound of large calls: 64 requests over <= 4352, 4096 kept, 8 heads of 128,
-// 81 us for 388 MB (4.8 TB/s); the select is 14 of them (a block goes from barrier to barrier
+// 81 us for 388 MB (4.8 TB/s); the select is 17 of them (a block goes from barrier to barrier
 // and from load to load), the rest the ranges' last rounds.  Small calls are chains: one
 // request 1088 -> 1024 10.2 us, half of them the select's: lengths, page ids, scores, two or
 // three passes of 0.7 to 1.4, the list.  Four of 32768 -> 2048: 36.7 us, half of them for
