@@ -104,9 +104,34 @@ constexpr int kScoreTile = kScoreThreads * 4;       // cached tokens a tile
 // 19.0 us for 19.7) and lose one in large ones (32 over <= 8192, 8 rows, 88.5 for 87.5).
 constexpr int kScoreRows = 4;
 
-__global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnParams p, float *weights, float decay) {
+struct ScoreTile {
+    int s, head, tile;
+};
+
+// The sums of a thread's four tokens where one of the rows has no number for its sum (a score of it is none, or infinite):
+// what the row sees gets no number either, and what it does not see is left alone.  The sums over all rows cannot tell
+// minus infinity for a token that is not seen from a score.
+__device__ __noinline__ float4 sum_seen(const AttnParams &p, const ScoreTile &at) {
+    const Request r = request_of(p, at.s);
+    const int c = at.tile * kScoreTile + threadIdx.x * 4;
+    float w[4] = {};
+    for (int row = 0; row < r.n * p.group; ++row) {
+        const int i = row / p.group;
+        const long long line = (long long)(r.begin + i) * p.n_q + at.head * p.group + row - i * p.group;
+        const float4 s = *reinterpret_cast<const float4 *>(p.scores + line * p.ld_scores + c);
+        const float lse = p.lse[line], scores[4] = {s.x, s.y, s.z, s.w};
+        const uint32_t see = seen_word(p, r, i, c & ~31) >> (c & 31);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if ((see >> x) & 1) w[x] += exp2_fast(scores[x] - lse);
+    }
+    return make_float4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(kScoreThreads, kScorePerSm) weigh_scores_kernel(const AttnParams p, float *weights, float decay) {
     static_assert(kScoreThreads >= kScanThreads, "start_block");
     __shared__ ScanShared scan;
+    __shared__ ScoreTile tiles[kScoreThreads / 32];       // each warp's, for sum_seen
     Cursor at;
     KeyCursor cur;
     const uint32_t total = start_block<kPlain, false>(p, scan, at);
@@ -179,6 +204,13 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
             }
         };
         load(0);
+        // drafted tokens among the warp's: rows differ in what they see of them
+        const bool drafted = c + 128 - (int)(threadIdx.x & 31) * 4 > cur.r.len - cur.r.n;
+        if (drafted) {
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) tiles[threadIdx.x >> 5] = {cur.s, cur.head, cur.tile};
+            __syncwarp();
+        }
         cur.advance(p);
         fetch_pages(cur);
         for (int row0 = 0; row0 < rows; row0 += kScoreRows) {
@@ -193,7 +225,7 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
             if (row0 + kScoreRows < rows) load(row0 + kScoreRows);
             // the scores are not needed again: their lines leave L2 without being written to memory (2 over 131072: 142 ->
             // 135 us; one over 777 would take 15.0 us for 14.2)
-            if (drop) {
+            if (drop && !drafted) {
                 __syncwarp();
 #pragma unroll
                 for (int x = 0; x < kScoreRows; ++x) {
@@ -202,6 +234,13 @@ __global__ void __launch_bounds__(kScoreThreads) weigh_scores_kernel(const AttnP
                     done.next(p);
                 }
             }
+        }
+        if (drafted && w[0] != w[0] && inside) {         // such a row makes none of any token's sum
+            const float4 seen = sum_seen(p, tiles[threadIdx.x >> 5]);
+            w[0] = seen.x;
+            w[1] = seen.y;
+            w[2] = seen.z;
+            w[3] = seen.w;
         }
         int to[4];
 #pragma unroll
