@@ -472,9 +472,13 @@ int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, c
  *   weights  n_pages x n_kv_heads x page_size fp32, slots as the cache's, 16-byte
  *            aligned; a prefix token's is what earlier calls left there.
  *   decay    0..1.   out  apart from q.
- *   workspace  lora_tree_attention_weights_workspace_size() bytes; it grows with S, T
- *            and max_pages (scores of up to 16 rows a kv head and request, 128 in an fp32
- *            cache, are kept in it), and one of the largest call serves every smaller one.
+ *   workspace  16-byte aligned.  lora_tree_attention_weights_workspace_size() bytes; one of
+ *            the largest call serves every smaller one.  Most of them are for scores of up to
+ *            16 rows a kv head and request (128 in an fp32 cache), which take 4 * T *
+ *            n_q_heads * max_pages * page_size bytes, as wide as the table however short the
+ *            requests are.  A smaller workspace, down to that size for max_pages 0, does as
+ *            well: where it does not hold a call's scores they are computed once more, which
+ *            takes longer (1.1 to 5 times), and weights may differ in their last bits.
  * A page that several requests of the call share ends up with either's weights.  A
  * page outside the cache has none.  Errors, device-detected ones and bad tables as
  * lora_tree_attention (where nothing is computed, weights stay as well).

@@ -976,9 +976,7 @@ int launch_few(const AttnParams &p, cudaStream_t st) {
 
 template <int D, int MODE>
 int launch_width(const KvMaps *maps, const AttnParams &p, bool f32, bool few, cudaStream_t st) {
-    if constexpr (MODE != kSums) {         // few rows keep their scores
-        if (few) return launch_few<D, MODE>(p, st);
-    }
+    if (few) return launch_few<D, MODE>(p, st);
     if (f32) return launch_simt<D, MODE>(p, st);
     return maps ? launch_mma<D, true, MODE>(*maps, p, st) : launch_mma<D, false, MODE>(KvMaps{}, p, st);
 }
@@ -1011,15 +1009,14 @@ size_t log_bytes(int n_q_heads, int T) { return (16 + (size_t)T * n_q_heads * si
 // and computed once more, 32 requests over <= 8192, 8 kv heads of 128: 4 rows 84.8 and 121.5 us, 8 rows 80.1 and 113.3, 16
 // rows 93.1 and 122.6; of 80, 16 rows 82.3 and 105.1; 4 requests over <= 600, 4 rows 13.6 and 14.1, 16 rows 15.7 and 14.8.
 // More rows of 64 or 128 go to tcgen05, whose kernel keeps none.  fp32, 16 requests over <= 4096: 8 rows 140 and 726 us,
-// 32 rows 260 and 343, 64 rows 465 and 583; kept, more would take more memory than the cache.
+// 32 rows 260 and 343, 64 rows 465 and 583.  A row's scores are as wide as the table, so in a wide one those of short
+// requests can take more memory than their keys and values: where the workspace does not hold them they are not kept.
 int keep_rows(const lora_kv_pages *kv) { return kv->dtype == LORA_F32 ? 128 : 16; }
 bool keeps_scores(const lora_kv_pages *kv, int group, int S, int T) { return (long long)T * group <= (long long)keep_rows(kv) * S; }
 // Whole lines of L2 a row: what has been summed up is dropped from it.
 long long score_pitch(const lora_kv_pages *kv, int max_pages) { return ((long long)max_pages * kv->page_size + 31) & ~31LL; }
-// At most, for up to T tokens of up to S requests.
-size_t score_bytes(const lora_kv_pages *kv, int n_q_heads, int S, int T, int max_pages) {
-    const long long most = (long long)keep_rows(kv) * S / (n_q_heads / kv->n_kv_heads), tokens = T < most ? T : most;
-    return (size_t)tokens * n_q_heads * score_pitch(kv, max_pages) * sizeof(float);
+size_t score_bytes(const lora_kv_pages *kv, int n_q_heads, int T, int max_pages) {
+    return (size_t)T * n_q_heads * score_pitch(kv, max_pages) * sizeof(float);
 }
 
 size_t partial_bytes(const Variant &v, int d) {
@@ -1062,10 +1059,10 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
     if (weights && overlap(q, q_bytes, out, q_bytes)) return LORA_ERR_ARG;
     if (num_sms() < 1) return LORA_ERR_CUDA;
     const Variant variant = variant_of(kv, n_q_heads / kv->n_kv_heads, S, T);
-    const bool keep = weights && keeps_scores(kv, n_q_heads / kv->n_kv_heads, S, T);
-    const size_t logs = weights ? log_bytes(n_q_heads, T) : 0;
-    const size_t kept = keep ? score_bytes(kv, n_q_heads, S, T, max_pages) : 0, parts = (partial_bytes(variant, kv->head_dim) + 15) & ~(size_t)15;
-    if (ws_bytes < logs + parts + kept + (weights ? 128 : 0) || ws_bytes < partial_bytes(variant, kv->head_dim) + 16) return LORA_ERR_ARG;
+    const size_t logs = weights ? log_bytes(n_q_heads, T) : 0, parts = (partial_bytes(variant, kv->head_dim) + 15) & ~(size_t)15;
+    const size_t least = logs + parts + (weights ? 128 : 0), scores = score_bytes(kv, n_q_heads, T, max_pages);
+    if (ws_bytes < least || ws_bytes < partial_bytes(variant, kv->head_dim) + 16) return LORA_ERR_ARG;
+    const bool keep = weights && keeps_scores(kv, n_q_heads / kv->n_kv_heads, S, T) && scores <= ws_bytes - least;
     decode::AttnParams p;
     p.q = q;
     p.k = kv->k;
@@ -1140,8 +1137,10 @@ extern "C" int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n
 
 extern "C" size_t lora_tree_attention_weights_workspace_size(const lora_kv_pages *kv, int n_q_heads, int S, int T, int max_pages) {
     const size_t base = lora_tree_attention_workspace_size(kv, n_q_heads, S, T);
-    if (!base || max_pages < 0) return 0;
-    return base + log_bytes(n_q_heads, T) + score_bytes(kv, n_q_heads, S, T, max_pages) + 144;
+    if (!base || max_pages < 0 || (long long)max_pages * kv->page_size > 0x7fffffffLL - 1024 || (long long)T * n_q_heads > 0x7fffffffLL) return 0;
+    // the most tokens whose scores are kept, here or in a smaller call
+    const long long most = (long long)keep_rows(kv) * S / (n_q_heads / kv->n_kv_heads);
+    return base + log_bytes(n_q_heads, T) + score_bytes(kv, n_q_heads, T < most ? T : (int)most, max_pages) + 144;
 }
 
 extern "C" int lora_tree_attention_weights(const lora_kv_pages *kv, const lora_attention_weights *a, lora_stream stream) {

@@ -197,3 +197,14 @@ def test_attention_weights_without_tokens():
     assert weigh(pages(), T=0, weights=None, q=None, out=None, starts=None, lens=None, table=None, workspace=None) == L.LORA_OK
     assert L.lora_launch_count() == before
     assert L._lib.lora_tree_attention_weights_workspace_size(ctypes.byref(pages()), 4, 2, 2, -1) == 0
+
+
+def test_attention_weights_workspace_sizes():
+    """They grow with the table up to the widest that a call takes, and sizes that no call takes have none."""
+    size = lambda *args: L._lib.lora_tree_attention_weights_workspace_size(ctypes.byref(pages()), *args)  # noqa: E731
+    for S, T in ((1, 1), (128, 128), (1000, 4000)):
+        sizes = [size(4, S, T, n) for n in (0, 1, 2, 4, 64, 8192, (1 << 27) - 65)]
+        assert 0 < sizes[0] and sizes == sorted(sizes)
+        kept = min(T, 16 * S // 2)                      # two query heads a kv head
+        assert sizes[4] - sizes[0] == kept * 4 * 64 * 16 * 4
+    assert size(4, 2, 2, (1 << 27) - 64) == 0 and size(4, 2, 1 << 29, 4) == 0
