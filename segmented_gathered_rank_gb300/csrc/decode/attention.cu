@@ -1011,8 +1011,10 @@ size_t log_bytes(int n_q_heads, int T) { return (16 + (size_t)T * n_q_heads * si
 // More rows of 64 or 128 go to tcgen05, whose kernel keeps none.  fp32, 16 requests over <= 4096: 8 rows 140 and 726 us,
 // 32 rows 260 and 343, 64 rows 465 and 583.  A row's scores are as wide as the table, so in a wide one those of short
 // requests can take more memory than their keys and values: where the workspace does not hold them they are not kept.
-int keep_rows(const lora_kv_pages *kv) { return kv->dtype == LORA_F32 ? 128 : 16; }
-bool keeps_scores(const lora_kv_pages *kv, int group, int S, int T) { return (long long)T * group <= (long long)keep_rows(kv) * S; }
+int keep_rows(const lora_kv_pages *kv) { return kv->dtype == LORA_F32 ? 128 : kRows; }
+bool keeps_scores(const lora_kv_pages *kv, const Variant &v, int group, int S, int T) {
+    return !v.tc && (long long)T * group <= (long long)keep_rows(kv) * S;
+}
 // Whole lines of L2 a row: what has been summed up is dropped from it.
 long long score_pitch(const lora_kv_pages *kv, int max_pages) { return ((long long)max_pages * kv->page_size + 31) & ~31LL; }
 size_t score_bytes(const lora_kv_pages *kv, int n_q_heads, int T, int max_pages) {
@@ -1062,7 +1064,7 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
     const size_t logs = weights ? log_bytes(n_q_heads, T) : 0, parts = (partial_bytes(variant, kv->head_dim) + 15) & ~(size_t)15;
     const size_t least = logs + parts + (weights ? 128 : 0), scores = score_bytes(kv, n_q_heads, T, max_pages);
     if (ws_bytes < least || ws_bytes < partial_bytes(variant, kv->head_dim) + 16) return LORA_ERR_ARG;
-    const bool keep = weights && keeps_scores(kv, n_q_heads / kv->n_kv_heads, S, T) && scores <= ws_bytes - least;
+    const bool keep = weights && keeps_scores(kv, variant, n_q_heads / kv->n_kv_heads, S, T) && scores <= ws_bytes - least;
     decode::AttnParams p;
     p.q = q;
     p.k = kv->k;
