@@ -105,3 +105,15 @@ def test_many_ranges_of_several_rounds(dtype, d, page, S, n_kv):
         e = Eviction(S, dtype, lens, keep, 4, 33, n_kv, d, page, scores=scores, weights=weights).to_device()
         e.call()
         e.check()
+
+
+# kept scores with many rows in one request and one in the others: places of the list by rows, tiles that begin in a block
+@pytest.mark.parametrize("dtype", [I.BF16, I.F32])
+@pytest.mark.parametrize("requests, n_q, n_kv, d, page", [
+    ([(1, 1500)] * 10 + [(37, 1600)] + [(1, 700)] * 5, 8, 2, 64, 16), ([(190, 2600)] + [(1, 2048), (1, 300)] * 32, 8, 2, 128, 16),
+    ([(0, 90), (17, 17), (1, 513), (33, 1025), (1, 5), (0, 3)] + [(1, 129)] * 12, 6, 2, 80, 8)])
+def test_one_long_request_among_short_ones(dtype, requests, n_q, n_kv, d, page):
+    w = Weigh(43, dtype, requests, n_q, n_kv, d, page, decay=0.9).to_device()
+    assert w.T * (n_q // n_kv) <= 16 * w.S            # on average few rows, so that scores are kept
+    w.call()
+    check(w)
