@@ -1122,7 +1122,7 @@ int attend(const lora_kv_pages *kv, float *weights, float decay, const void *q, 
                                          : weights ? attention_join_kernel<float, true> : attention_join_kernel<float, false>;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, join, p);
     count_launch();
-    if ((rc = cuda_status(e))) return rc;
+    if ((rc = launch_status(e))) return rc;
     return weights ? launch_weigh(kv, tma ? &maps : nullptr, weigh, weights, decay, st) : LORA_OK;
 }
 

@@ -27,6 +27,13 @@ inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// Of a launch by cudaLaunchKernelEx, which returns its error and also leaves it as the runtime's last one, for the next
+// call that asks for that: it is reported once.
+inline int launch_status(cudaError_t e) {
+    if (e != cudaSuccess) cudaGetLastError();
+    return cuda_status(e);
+}
+
 inline int log2_of(int power_of_two) {
     int n = 0;
     while ((1 << n) < power_of_two) ++n;

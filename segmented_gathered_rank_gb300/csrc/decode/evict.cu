@@ -630,8 +630,8 @@ extern "C" int lora_kv_evict(const lora_kv_pages *kv, const lora_eviction *a, lo
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
     count_launch();
-    if (e != cudaSuccess) return cuda_status(e);
+    if (e != cudaSuccess) return launch_status(e);
     e = few ? launch_move<Few>(p, units, (cudaStream_t)stream) : launch_move<Many>(p, units, (cudaStream_t)stream);
     count_launch();
-    return cuda_status(e);
+    return launch_status(e);
 }

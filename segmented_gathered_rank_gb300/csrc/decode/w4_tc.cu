@@ -548,7 +548,7 @@ int launch(const W4Params &p, const CUtensorMap &map, const CUtensorMap &x_map, 
     cfg.numAttrs = splits > 1 ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, w4_tc_kernel<E, GROUP, NTOK>, map, x_map, p, splits);
     count_launch();
-    return cuda_status(e);
+    return launch_status(e);
 }
 
 template <typename E, int NTOK>

@@ -298,7 +298,7 @@ int launch_weigh(const lora_kv_pages *kv, const KvMaps *maps, const AttnParams &
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, weights, decay);
     count_launch();
-    return cuda_status(e);
+    return launch_status(e);
 }
 
 }  // namespace decode

@@ -382,7 +382,7 @@ int launch(const KvMaps &maps, const AttnParams &p, float *weights, float decay,
     cfg.numAttrs = 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, weigh_tc_kernel<D, TMA>, maps, p, weights, decay);
     count_launch();
-    return cuda_status(e);
+    return launch_status(e);
 }
 
 template <int D>

@@ -124,12 +124,7 @@ inline int matrix_dims(const lora_pool *pool, int matrix, int *h_in, int *h_out)
     return LORA_OK;
 }
 
-// An error is reported once: the runtime would keep it for the next call that asks for the last one.
-inline int cuda_status(cudaError_t e) {
-    if (e == cudaSuccess) return LORA_OK;
-    cudaGetLastError();
-    return LORA_ERR_CUDA;
-}
+inline int cuda_status(cudaError_t e) { return e == cudaSuccess ? LORA_OK : LORA_ERR_CUDA; }
 
 // ---------------------------------------------------------------------------
 // Device helpers
