@@ -15,8 +15,8 @@
 // little (12 heads 20.5 -> 16.9 us, 48 heads of 64 29.0 -> 27.9) and cost the larger ones
 // (37.4 -> 41.0).
 #include "append.cuh"
+#include "packed.cuh"
 #include "tc_common.cuh"
-#include "tmem.cuh"
 
 namespace lora {
 namespace {
@@ -114,7 +114,7 @@ __device__ void turn_tokens(const StreamParams &sp, uint8_t *ring, Control &ctl)
     constexpr bool kApart = PAIRS == kFar;
     const AppendParams &p = sp.a;
     const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES, half = p.rot >> 1, heads = p.n_q + p.n_kv;
-    const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << ((threadIdx.x & 31) / LANES * LANES);
+    const unsigned mask = group_mask<LANES>();
     const int at = lane * 8;
     const bool inside = at < p.d, turns = at < p.rot;
     const int o0 = kApart && turns ? lane * 4 : at, o1 = kApart && turns ? half + lane * 4 : at + 4;

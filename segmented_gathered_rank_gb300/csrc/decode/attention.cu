@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include "kv_copy.cuh"
+#include "packed.cuh"
 #include "weigh.cuh"
 
 namespace lora {
@@ -77,16 +78,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-// Two fp32 operations an instruction.
-__device__ __forceinline__ float2 mul_add2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
-        "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
 }
 
 constexpr int kThreads = 128;      // the join kernel's, the fp32 kernel's, the consumers of the MMA kernel
@@ -545,8 +536,8 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
 #pragma unroll
                 for (int a = 0; a < 4; ++a) {
                     const float4 qq = *reinterpret_cast<const float4 *>(qs + (row0 + a) * D + k);
-                    s2[a] = mul_add2(make_float2(kk.x, kk.y), make_float2(qq.x, qq.y), s2[a]);
-                    s2[a] = mul_add2(make_float2(kk.z, kk.w), make_float2(qq.z, qq.w), s2[a]);
+                    s2[a] = fma2(make_float2(kk.x, kk.y), make_float2(qq.x, qq.y), s2[a]);
+                    s2[a] = fma2(make_float2(kk.z, kk.w), make_float2(qq.z, qq.w), s2[a]);
                 }
             }
             uint32_t see[4];
@@ -582,8 +573,8 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
 #pragma unroll
                     for (int j = 0; j < kCols; ++j) {
                         const float v = vs[x * kLd + j * 32 + lane];
-                        o2[0][j] = mul_add2(make_float2(pp.x, pp.y), make_float2(v, v), o2[0][j]);
-                        o2[1][j] = mul_add2(make_float2(pp.z, pp.w), make_float2(v, v), o2[1][j]);
+                        o2[0][j] = fma2(make_float2(pp.x, pp.y), make_float2(v, v), o2[0][j]);
+                        o2[1][j] = fma2(make_float2(pp.z, pp.w), make_float2(v, v), o2[1][j]);
                     }
                 }
             } else {
@@ -597,8 +588,8 @@ __global__ void __launch_bounds__(kThreads) attention_simt_kernel(const AttnPara
                             bad |= j * 32 + lane < p.d;
                             v = 0.f;
                         }
-                        o2[0][j] = mul_add2(make_float2(pp.x, pp.y), make_float2(v, v), o2[0][j]);
-                        o2[1][j] = mul_add2(make_float2(pp.z, pp.w), make_float2(v, v), o2[1][j]);
+                        o2[0][j] = fma2(make_float2(pp.x, pp.y), make_float2(v, v), o2[0][j]);
+                        o2[1][j] = fma2(make_float2(pp.z, pp.w), make_float2(v, v), o2[1][j]);
                     }
                 }
             }
@@ -714,8 +705,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few
                 float2 t = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int x = 0; x < kVec; ++x) {
-                    t = mul_add2(make_float2(k[x].x, k[x].y), q[a][2 * x], t);
-                    t = mul_add2(make_float2(k[x].z, k[x].w), q[a][2 * x + 1], t);
+                    t = fma2(make_float2(k[x].x, k[x].y), q[a][2 * x], t);
+                    t = fma2(make_float2(k[x].z, k[x].w), q[a][2 * x + 1], t);
                 }
                 s[a] = t.x + t.y;
                 on[a] = true;
@@ -756,8 +747,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, D == 64 ? 2 : 1) attention_few
                 if (masked && !on[a]) continue;
 #pragma unroll
                 for (int x = 0; x < kVec; ++x) {
-                    o[a][2 * x] = mul_add2(w2, make_float2(v[x].x, v[x].y), o[a][2 * x]);
-                    o[a][2 * x + 1] = mul_add2(w2, make_float2(v[x].z, v[x].w), o[a][2 * x + 1]);
+                    o[a][2 * x] = fma2(w2, make_float2(v[x].x, v[x].y), o[a][2 * x]);
+                    o[a][2 * x + 1] = fma2(w2, make_float2(v[x].z, v[x].w), o[a][2 * x + 1]);
                 }
             }
         };

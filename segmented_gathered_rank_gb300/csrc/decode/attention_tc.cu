@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "kv_copy.cuh"
+#include "packed.cuh"
 #include "tmem.cuh"
 
 namespace lora {

@@ -15,7 +15,7 @@
 //   once more, keys at rest and rows going by, so that a key's sum stays in one block and
 //   its order is fixed.  weigh_kernel has fp32 multiply-adds for its bound, two tokens and
 //   eight rows a thread.
-#include "tmem.cuh"
+#include "packed.cuh"
 #include "weigh.cuh"
 
 namespace lora {

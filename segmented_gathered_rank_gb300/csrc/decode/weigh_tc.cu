@@ -18,6 +18,7 @@
 #include <type_traits>
 
 #include "kv_copy.cuh"
+#include "packed.cuh"
 #include "tmem.cuh"
 #include "weigh.cuh"
 
