@@ -479,6 +479,7 @@ int lora_tree_attention(const lora_kv_pages *kv, const void *q, int n_q_heads, c
  *            requests are.  A smaller workspace, down to that size for max_pages 0, does as
  *            well: where it does not hold a call's scores they are computed once more, which
  *            takes longer (1.1 to 5 times), and weights may differ in their last bits.
+ * Every drafted token counts: rows of tokens that are rejected afterwards stay in the sums.
  * A page that several requests of the call share ends up with either's weights.  A
  * page outside the cache has none.  Errors, device-detected ones and bad tables as
  * lora_tree_attention (where nothing is computed, weights stay as well).

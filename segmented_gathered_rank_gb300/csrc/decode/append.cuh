@@ -93,7 +93,7 @@ __device__ __forceinline__ void store_quads(const Quads<E> &h, E *head, int o0, 
 // HEADS: heads a thread.
 enum { kNear, kFar, kAnyNear, kAnyFar };
 
-// append_stream.cu: tokens with axes, pairs near or far; or LORA_ERR_SHAPE (nothing launched) where it does not serve.
+// append_stream.cu: tokens with axes, pairs near or far.  launch_append_stream checks nothing: only where streams() holds.
 bool streams(const AppendParams &p, int T, int esize);
 int launch_append_stream(const AppendParams &p, int T, bool bf16, bool near, cudaStream_t st);
 

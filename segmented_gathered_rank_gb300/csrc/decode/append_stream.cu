@@ -34,7 +34,8 @@ constexpr int kMaxToken = 26 << 10;       // bytes of a token's heads: two block
 // tokens (7.3 MB) 6.1 and 5.4, 1024 tokens 7.6 and 8.5, 8192 tokens 35.6 and 54.5; 12 heads of 128, 2048 tokens (6 MB)
 // 7.0 and 7.0, 4096 tokens 11.6 and 12.1, 8192 tokens 19.8 and 24.5; 48 heads of 64, 1024 tokens (6 MB) 6.7 and 6.5, 2048
 // tokens 8.8 and 11.1; 48 heads of 80, 1024 tokens (8 MB) 7.2 and 9.6; fp32, 48 heads of 128, 512 tokens (12 MB) 6.2 and
-// 6.4, 8192 tokens 68 and 87.
+// 6.4, 8192 tokens 68 and 87.  One limit for all of them: neighbours, which append.cu reads in 16-byte pieces, break even
+// between 8 and 12 MB, and lose up to 0.7 us below that.
 constexpr long long kMinBytes = 7 << 20;
 
 struct StreamParams {

@@ -34,8 +34,9 @@ using namespace decode;
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBits = 11, kBins = 1 << kBits, kCoarse = 8;      // kCoarse bins side by side are counted together as well
 constexpr int kMaxCluster = 8;
-// Alone and in a cluster, four requests, 2048 kept, 8 heads: 2100 tokens 25.8 and 26.7 us, 4200 29.9 and 28.5, 8100 36.1
-// and 30.1, 16000 45.2 and 33.0.
+// Alone and in clusters of four, four requests, 8 heads of 128, 2048 kept: 2100 tokens 28.7 and 29.7 us, 4200 31.7 and
+// 30.7, 8100 36.9 and 32.0, 16000 47.1 and 34.8; half of the tokens kept: 2100 22.5 and 24.4, 4200 32.8 and 30.7, 8100 51.2
+// and 45.1, 16000 86.0 and 73.7 (events around a call, L2 flushed before it).
 constexpr int kSolo = 4096;
 constexpr int kMaxHeld = 16384;       // scores a block keeps in shared memory; more are read again
 

@@ -7,10 +7,11 @@
 //
 // weigh_scores_kernel: with few rows they leave the scores too (4 bytes a row and token,
 //   written and read, against 2 d for reading a bf16 key again), and a thread sums up four
-//   tokens.  128 requests over <= 8192, 4 rows, 8 kv heads: about 17 us of the call's 267, for
+//   tokens.  128 requests over <= 8192, 4 rows, 8 kv heads: about 18 us of the call's 269, for
 //   50 MB of scores that are still in L2 and 25 MB of weights; the bound is instructions and
 //   the chain page id -> weight -> store, which is why both are requested a tile ahead.  One
-//   request over 777: 13.6 us, of which the attention is 10.8.
+//   request over 777: 13.6 us, of which the attention is 10.8.  Its exponentials are the fast
+//   ones for an fp32 cache as well (2^-22 relative, as exp2f's; a weight below 2^-126 is 0).
 // weigh_tc_kernel (weigh_tc.cu; bf16), weigh_kernel (fp32): else the scores are computed
 //   once more, keys at rest and rows going by, so that a key's sum stays in one block and
 //   its order is fixed.  weigh_kernel has fp32 multiply-adds for its bound, two tokens and
@@ -112,9 +113,9 @@ struct ScoreTile {
     int s, head, tile;
 };
 
-// The sums of a thread's four tokens where one of the rows has no number for its sum (a score of it is none, or infinite):
-// what the row sees gets no number either, and what it does not see is left alone.  The sums over all rows cannot tell
-// minus infinity for a token that is not seen from a score.
+// The sums of a thread's four tokens where the sum of one of the rows is NaN (a score of it is, or is infinite): what the
+// row sees gets NaN, and what it does not see is left alone.  Sums that do not look at the mask cannot tell minus infinity
+// for a token that is not seen from a score.
 __device__ __noinline__ float4 sum_seen(const AttnParams &p, const ScoreTile &at) {
     const Request r = request_of(p, at.s);
     const int c = at.tile * kScoreTile + threadIdx.x * 4;
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kScoreThreads, kScorePerSm) weigh_scores_kerne
                 }
             }
         }
-        if (drafted && w[0] != w[0] && inside) {         // such a row makes none of any token's sum
+        if (drafted && w[0] != w[0] && inside) {         // such a row makes NaN of any token's sum
             const float4 seen = sum_seen(p, tiles[threadIdx.x >> 5]);
             w[0] = seen.x;
             w[1] = seen.y;

@@ -10,11 +10,14 @@
 // waits for it.
 //
 // 8 requests of 64 tokens over <= 16384 (256 rows, 8 kv heads of 128): about 27 us of the
-// call's 84.5, where the products would take 8 and the exponentials, 16 a cycle and SM, 15.
-// A pair of key tiles against 128 rows takes some 2200 cycles, 2048 of them exponentials;
-// the rest is the start (scan, first copies, 4 us) and the cut into whole key tiles.
-// Exponentials on the multiply-add pipe for a quarter of the columns were slower (90 us),
-// as were loads of 32 columns that nothing ran under (89).
+// call's 85, where the products would take 8 and the exponentials, at the 25 a cycle and SM
+// that attention_tc.cu measures, 10.  Neither is the bound: the tensor pipe is active for 32 %
+// of the time and the exponentials' for 27 %.  A pair of key tiles against 128 rows takes some
+// 2200 cycles, for 1024 of products and 1300 of exponentials that run beside them; what the
+// summing warps wait for in the other 900 is not known.  To that come the start (scan, first
+// copies, 4 us) and the cut into whole key tiles: 16.4 such pairs a block.  Exponentials on
+// the multiply-add pipe for a quarter of the columns were slower (90 us), as were twice the
+// summing warps (89) and loads of 32 columns that nothing ran under (89).
 #include <type_traits>
 
 #include "kv_copy.cuh"

@@ -465,7 +465,7 @@ def lora_tree_attention_weights_workspace_size(kv, n_q_heads, S, T, max_pages) -
 def lora_tree_attention_weights(kv, weights, decay, q, n_q_heads, seg_starts, S, T, kv_lens, page_table, max_pages, tree_mask,
                                 mask_words, scale, out, workspace, ws_bytes=None, stream=None) -> None:
     """lora_tree_attention that adds the weight of each cached token, times decay what it had, to weights (float
-    [n_pages, n_kv_heads, page_size])."""
+    [n_pages, n_kv_heads, page_size]).  A workspace below its size, down to that for max_pages 0, takes longer."""
     if ws_bytes is None:
         ws_bytes = workspace.nbytes
     args = _WEIGHTS.pack(_plane(kv, weights), _address(q), _address(seg_starts), _address(kv_lens), _address(page_table), _address(tree_mask),
