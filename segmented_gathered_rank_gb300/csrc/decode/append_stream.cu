@@ -35,7 +35,7 @@ constexpr int kMaxToken = 26 << 10;       // bytes of a token's heads: two block
 // 7.0 and 7.0, 4096 tokens 11.6 and 12.1, 8192 tokens 19.8 and 24.5; 48 heads of 64, 1024 tokens (6 MB) 6.7 and 6.5, 2048
 // tokens 8.8 and 11.1; 48 heads of 80, 1024 tokens (8 MB) 7.2 and 9.6; fp32, 48 heads of 128, 512 tokens (12 MB) 6.2 and
 // 6.4, 8192 tokens 68 and 87.  One limit for all of them: neighbours, which append.cu reads in 16-byte pieces, break even
-// between 8 and 12 MB, and lose up to 0.7 us below that.
+// between 700 and 800 tokens of 48 heads of 128 (9 MB), and lose about a microsecond between the limit and that.
 constexpr long long kMinBytes = 7 << 20;
 
 struct StreamParams {
